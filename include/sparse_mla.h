@@ -237,6 +237,173 @@ int sparse_mla_kv_append(const smla_append_dims* dims, const void* latent, const
                          const int32_t* block_table, const int32_t* requests, const int32_t* positions,
                          void* kv_cache, uint32_t* err_word, smla_stream_t stream);
 
+/* Element types of the operators that take more than one. */
+typedef enum smla_dtype {
+  SMLA_BF16 = 0,
+  SMLA_FP16 = 1,
+  SMLA_FP32 = 2
+} smla_dtype;
+
+/* Shapes of one fused norm + rotation + append call. */
+typedef struct smla_norm_append_dims {
+  int32_t tokens;             /* new tokens to write, >= 0                               */
+  int32_t num_requests;       /* rows of block_table, >= 1                               */
+  int32_t page_size;          /* tokens per page; must be 64                             */
+  int32_t max_pages_per_seq;  /* row length of block_table, >= 1                         */
+  int32_t d_latent;           /* must be 512                                             */
+  int32_t d_rope;             /* must be 64                                              */
+  int64_t num_pages;          /* pages in kv_cache, >= 1                                 */
+  int64_t latent_stride;      /* elements between rows of latent, >= 512                 */
+  int64_t rope_stride;        /* elements between rows of rope, >= 64                    */
+  int32_t dtype;              /* smla_dtype of latent and rope                           */
+  int32_t weight_dtype;       /* smla_dtype of norm_weight: dtype or SMLA_FP32           */
+  int32_t max_positions;      /* rows of cos_sin, >= 1                                   */
+  int32_t interleaved;        /* 1: rotation pairs (2i, 2i+1); 0: pairs (i, i+32)        */
+} smla_norm_append_dims;
+
+/* sparse_mla_kv_append for the key projection's raw output: RMS norm of the
+ * latent, rotation of the rope part, FP8 quantisation and the record write in
+ * one pass.  For token i at position t = positions[i] of request r:
+ *   n_d    = latent_d / sqrt(mean_d latent_d^2 + eps) * norm_weight_d     (fp32)
+ *   scale, code: of n as sparse_mla_kv_append has them (n is not rounded to
+ *            16 bits before it is quantised);
+ *   rope   = bf16 of the pairs (a, b) rotated to (a c - b s, a s + b c) with
+ *            c = cos_sin[t][j], s = cos_sin[t][32 + j] for pair j (fp32).
+ *   latent  dtype [tokens][512], rope dtype [tokens][64]: unit stride in a
+ *           row, rows latent_stride / rope_stride elements apart (slices of
+ *           one projection output); any element alignment, 16-byte aligned
+ *           rows take wide loads
+ *   norm_weight weight_dtype [512] (element aligned)
+ *   cos_sin float32 [max_positions][64] (16-byte aligned), the others as in
+ *           sparse_mla_kv_append
+ * A token whose request, position or page is out of range, or whose position
+ * is not below max_positions, is skipped and sets SMLA_DEVERR_PAGE_RANGE.  A
+ * row holding a NaN or an infinity is written with NaN codes where n is NaN.
+ * Statuses as sparse_mla_kv_append; SMLA_ERR_INVALID_ARG also for a stride
+ * below the row, an unknown dtype, a weight_dtype that is neither dtype nor
+ * SMLA_FP32, or an eps that is negative or not finite. */
+int sparse_mla_kv_norm_append(const smla_norm_append_dims* dims, const void* latent, const void* rope,
+                              const void* norm_weight, float eps, const float* cos_sin,
+                              const int32_t* block_table, const int32_t* requests, const int32_t* positions,
+                              void* kv_cache, uint32_t* err_word, smla_stream_t stream);
+
+/* Shapes of one per-head norm + rotation call. */
+typedef struct smla_norm_rope_dims {
+  int32_t tokens;             /* T >= 0                                                  */
+  int32_t num_heads;          /* H >= 1                                                  */
+  int32_t head_dim;           /* D, 1 .. 1024                                            */
+  int32_t rope_dim;           /* rotated dims, even, 0 .. D (0: no rotation)             */
+  int32_t rope_offset;        /* first rotated dim, rope_offset + rope_dim <= D          */
+  int32_t dtype;              /* smla_dtype of x and out                                 */
+  int32_t weight_dtype;       /* smla_dtype of weight: dtype or SMLA_FP32                */
+  int32_t norm;               /* 1: RMS norm over the D dims of each head; 0: none       */
+  int32_t interleaved;        /* 1: pairs (2i, 2i+1); 0: pairs (i, i + rope_dim / 2)     */
+  int32_t max_positions;      /* rows of cos_sin, >= 1 (ignored when rope_dim = 0)       */
+  int64_t x_token_stride, x_head_stride;      /* elements; unit stride along D          */
+  int64_t out_token_stride, out_head_stride;  /* elements; unit stride along D          */
+} smla_norm_rope_dims;
+
+/* Norm of each head's vector and rotation of a part of it, in one pass: what a
+ * step does to its query (or key) heads before the attention.  For token t,
+ * head h, x = x[t][h][0..D):
+ *   n_d = x_d / sqrt(mean_d x_d^2 + eps) * weight_d  (norm = 1; weight may be
+ *         NULL: no weight), n = x (norm = 0);
+ *   out = n with the dims [rope_offset, rope_offset + rope_dim) rotated in
+ *         pairs (a, b) -> (a c - b s, a s + b c), c = cos_sin[p][j],
+ *         s = cos_sin[p][rope_dim / 2 + j] for pair j and p = positions[t].
+ * All in fp32, rounded once to dtype.
+ *   x, out   dtype, element aligned, strides in elements (non-negative); out
+ *            may be x with equal strides (in place), else must not overlap it,
+ *            and the rows of out must not overlap one another
+ *   weight   weight_dtype [D] or NULL
+ *   cos_sin  float32 [max_positions][rope_dim] (4-byte aligned), positions
+ *            int32 [T]; both may be NULL when rope_dim = 0
+ *   err_word device uint32 (may be NULL): a token whose position is outside
+ *            [0, max_positions) has its rows written as zeros and sets
+ *            SMLA_DEVERR_LEN_RANGE.
+ * Returns SMLA_ERR_INVALID_ARG for null or misaligned pointers, bad shapes or
+ * strides, an unknown dtype or eps that is negative or not finite,
+ * SMLA_ERR_UNSUPPORTED for D > 1024, SMLA_ERR_CUDA if the launch fails.
+ * Asynchronous on `stream`. */
+int sparse_mla_norm_rope(const smla_norm_rope_dims* dims, const void* x, const void* weight, float eps,
+                         const float* cos_sin, const int32_t* positions, void* out, uint32_t* err_word,
+                         smla_stream_t stream);
+
+/* Reads records back: for every token i (request and position as in
+ * sparse_mla_kv_append),
+ *   out[i] = [e4m3(code_d) * scale_{d / 128}, d < 512 | rope, 64 values],
+ * the product in fp32, rounded once to out_dtype: the key rows a chunked
+ * prompt needs of its earlier context.
+ *   out      out_dtype [tokens][576] (16-byte aligned, written)
+ *   err_word a token whose request, position or page is out of range gets a
+ *            row of zeros and sets SMLA_DEVERR_PAGE_RANGE.
+ * Shapes in smla_append_dims; statuses as sparse_mla_kv_append, and
+ * SMLA_ERR_INVALID_ARG for an unknown out_dtype. */
+int sparse_mla_kv_read(const smla_append_dims* dims, const void* kv_cache, const int32_t* block_table,
+                       const int32_t* requests, const int32_t* positions, void* out, int32_t out_dtype,
+                       uint32_t* err_word, smla_stream_t stream);
+
+/* Shapes of one dense decode call. */
+typedef struct smla_dense_dims {
+  int32_t batch;              /* B decode queries, 1 .. 65535                            */
+  int32_t num_heads;          /* H, 1 .. 128                                             */
+  int32_t page_size;          /* tokens per page; must be 64                             */
+  int32_t max_pages_per_seq;  /* row length of block_table, >= 1                         */
+  int32_t d_latent;           /* must be 512                                             */
+  int32_t d_rope;             /* must be 64                                              */
+  int64_t num_pages;          /* pages in kv_cache, 1 .. 2^31 - 1                        */
+  int32_t queries_per_request;/* s_q >= 1 (0 means 1): query b reads block_table row     */
+                              /* b / s_q; batch must be a multiple                       */
+  int32_t ctas;               /* CTAs of the decode kernel, 1 .. 1024; 0 = one per SM    */
+} smla_dense_dims;
+
+typedef struct smla_dense_plan {
+  int32_t rows_per_cta;       /* (query, head) rows a CTA handles at once: 16, 32 or 64  */
+  int32_t row_groups;         /* groups of rows_per_cta rows per request                 */
+  int32_t ctas;               /* CTAs the batch's tiles are shared out over              */
+  int32_t reserved;
+  size_t workspace_bytes;     /* bytes sparse_mla_dense_decode needs                     */
+} smla_dense_plan;
+
+/* Launch shape and workspace of sparse_mla_dense_decode on a device with
+ * sm_count SMs (host only, no CUDA call).  SMLA_ERR_INVALID_ARG for null
+ * pointers, sm_count < 1 or bad shapes, SMLA_ERR_UNSUPPORTED for shapes
+ * outside smla_dense_dims' stated ranges. */
+int sparse_mla_dense_plan_for(const smla_dense_dims* dims, int32_t sm_count, smla_dense_plan* plan);
+
+/* As sparse_mla_dense_plan_for, with sm_count read from CUDA device `device`. */
+int sparse_mla_dense_plan(const smla_dense_dims* dims, int32_t device, smla_dense_plan* plan);
+
+/* Decode attention over every cached position instead of a top-k list: query
+ * b, head h attends over the positions 0 <= t < seq_lens[b] of its request,
+ *   s_t = sm_scale * q[b][h].k_t, lse = ln sum_t exp(s_t),
+ *   out = sum_t exp(s_t - lse) v_t (k, v of the cache record above).
+ * The s_q queries of a request (verification of several new tokens) have a
+ * seq_lens entry each, so the causal limit of query j is seq_lens[b].
+ * The batch's 128-position tiles are shared out evenly over the CTAs on the
+ * device, from seq_lens as they are when the kernel runs: a captured call may
+ * be replayed with other lengths.  The result does not depend on timing.
+ *   q           bf16 [B][H][576], kv_cache, block_table, seq_lens, sm_scale,
+ *               out and lse as in sparse_mla_decode
+ *   workspace   >= plan.workspace_bytes, 256-byte aligned; its first 4 bytes
+ *               are the device error word.  Concurrent calls must not share a
+ *               workspace.
+ * Positions below seq_lens[b] whose logical page is >= max_pages_per_seq or
+ * whose physical page is outside the cache are skipped and set
+ * SMLA_DEVERR_PAGE_RANGE.  A negative length counts as 0; a query without a
+ * position gets out = 0 and lse = -inf.  Positions at or past seq_lens[b] are
+ * never used, whatever their records hold.
+ * Numerics: the latent scores are sums of E4M3 codes times q as two E4M3
+ * terms, the rope scores bf16 products, all accumulated in fp32 (q is exact but
+ * for elements below about 2^-9 of the largest of their row's 128-dim block,
+ * whose absolute error stays below 2^-17 of that largest); softmax weights and
+ * dequantised latents are fp16 on chip, |dequantised latent| must stay below
+ * 65504 (larger values saturate and set SMLA_DEVERR_RANGE).
+ * Statuses as sparse_mla_decode. */
+int sparse_mla_dense_decode(const smla_dense_dims* dims, const void* q, const void* kv_cache,
+                            const int32_t* block_table, const int32_t* seq_lens, float sm_scale, void* out,
+                            float* lse, void* workspace, size_t workspace_bytes, smla_stream_t stream);
+
 /* Shapes of one top-k selection call. */
 typedef struct smla_topk_dims {
   int32_t batch;          /* queries (rows of scores), >= 0                               */

@@ -1,0 +1,98 @@
+"""Oracle for the dense decode (every cached position attends) and for reading records back.
+
+TEST INFRASTRUCTURE ONLY.  Nothing in the product path imports this module:
+only the tests may call it.  It shares no code with the CUDA library.
+
+What it computes, in float64: query b, head h of request b // s_q attends over
+the positions 0 <= t < seq_lens[b] whose logical page lies in the block-table
+row and whose physical page lies in the cache,
+    s_t = sm_scale * q.k_t,  lse = ln sum exp(s_t),  out = sum exp(s_t - lse) v_t
+(out = 0 and lse = -inf without a position), with k and v of the cache record.
+
+Beside the result it gives two sizes that rounding-error bounds need:
+    weighted   sum_t exp(s_t - lse) |v_t|
+    score_err  a bound on the error of a score whose latent part multiplies the
+               codes with q as two E4M3 terms and accumulates in float32, see
+               score_error_bound.
+"""
+from __future__ import annotations
+
+import numpy as np
+
+from .sparse_mla_oracle import D_LATENT, PAGE_SIZE, RECORD_BYTES, as_f64_q, dequantize_record
+
+
+def positions_rows(bt_row, n: int, num_pages: int) -> np.ndarray:
+    """Physical rows of positions 0 .. n - 1 (skipping those without a page)."""
+    rows = []
+    for t in range(max(0, n)):
+        lp = t // PAGE_SIZE
+        if lp >= len(bt_row):
+            break
+        page = int(bt_row[lp])
+        if 0 <= page < num_pages:
+            rows.append(page * PAGE_SIZE + t % PAGE_SIZE)
+    return np.array(rows, dtype=np.int64)
+
+
+def score_error_bound(q: np.ndarray, k: np.ndarray, sm_scale: float) -> np.ndarray:
+    """[H, n] bound on |score error|.
+
+    Accumulating 576 products in float32 is off by at most 2^-20 of the sum of
+    their magnitudes (the accumulator adds groups of 16 or 32 products, so about
+    40 roundings of 2^-24 each).  q as hi + lo in E4M3, scaled so that the
+    largest of a 128-dim block lies in [2^7, 2^8): hi keeps 4 bits, so an element
+    of 8 bits leaves a remainder of 4 bits, which lo holds exactly unless it
+    falls below E4M3's step of 2^-9; that needs an element below 2^-8 of the
+    largest, and the error is then at most 2^-10 / 2^7 of the largest.
+    """
+    err = 2.0 ** -20 * (np.abs(q) @ np.abs(k).T)
+    for b in range(4):
+        qb, kb = np.abs(q[:, 128 * b:128 * b + 128]), np.abs(k[:, 128 * b:128 * b + 128])
+        top = qb.max(axis=1, keepdims=True)
+        small = (qb < 2.0 ** -8 * top) & (qb > 0)
+        err = err + 2.0 ** -17 * (top * small) @ kb.T
+    return sm_scale * err
+
+
+def dense_decode(q, kv_cache, block_table, seq_lens, sm_scale: float):
+    """(out [B, H, 512], lse [B, H], weighted [B, H, 512], score_err [B, H]) in float64."""
+    qf = as_f64_q(q)
+    cache = np.asarray(kv_cache, dtype=np.uint8)
+    flat = cache.reshape(-1, RECORD_BYTES)
+    bt = np.asarray(block_table, dtype=np.int64)
+    B, H, _ = qf.shape
+    s_q = B // bt.shape[0]
+    out = np.zeros((B, H, D_LATENT))
+    weighted = np.zeros((B, H, D_LATENT))
+    lse = np.full((B, H), -np.inf)
+    score_err = np.zeros((B, H))
+    for b in range(B):
+        rows = positions_rows(bt[b // s_q], int(seq_lens[b]), cache.shape[0])
+        if rows.size == 0:
+            continue
+        k = dequantize_record(flat[rows])
+        s = sm_scale * (qf[b] @ k.T)
+        m = s.max(axis=1, keepdims=True)
+        e = np.exp(s - m)
+        z = e.sum(axis=1, keepdims=True)
+        lse[b] = (m + np.log(z))[:, 0]
+        out[b] = (e / z) @ k[:, :D_LATENT]
+        weighted[b] = (e / z) @ np.abs(k[:, :D_LATENT])
+        score_err[b] = score_error_bound(qf[b], k, sm_scale).max(axis=1)
+    return out, lse, weighted, score_err
+
+
+def read_records(kv_cache, block_table, positions, requests=None) -> np.ndarray:
+    """float64 [T, 576]: the dequantised records; zeros for a token out of range."""
+    cache = np.asarray(kv_cache, dtype=np.uint8)
+    bt = np.asarray(block_table, dtype=np.int64)
+    out = np.zeros((len(positions), D_LATENT + 64))
+    for i, t in enumerate(np.asarray(positions, dtype=np.int64)):
+        r = int(requests[i]) if requests is not None else i
+        if r < 0 or r >= bt.shape[0] or t < 0 or t // PAGE_SIZE >= bt.shape[1]:
+            continue
+        page = bt[r, t // PAGE_SIZE]
+        if 0 <= page < cache.shape[0]:
+            out[i] = dequantize_record(cache[page, t % PAGE_SIZE])
+    return out

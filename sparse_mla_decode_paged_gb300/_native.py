@@ -22,6 +22,32 @@ class SmlaAppendDims(C.Structure):
                 ("num_pages", C.c_int64)]
 
 
+class SmlaNormAppendDims(C.Structure):
+    _fields_ = [("tokens", C.c_int32), ("num_requests", C.c_int32), ("page_size", C.c_int32),
+                ("max_pages_per_seq", C.c_int32), ("d_latent", C.c_int32), ("d_rope", C.c_int32),
+                ("num_pages", C.c_int64), ("latent_stride", C.c_int64), ("rope_stride", C.c_int64),
+                ("dtype", C.c_int32), ("weight_dtype", C.c_int32), ("max_positions", C.c_int32),
+                ("interleaved", C.c_int32)]
+
+
+class SmlaNormRopeDims(C.Structure):
+    _fields_ = [("tokens", C.c_int32), ("num_heads", C.c_int32), ("head_dim", C.c_int32), ("rope_dim", C.c_int32),
+                ("rope_offset", C.c_int32), ("dtype", C.c_int32), ("weight_dtype", C.c_int32), ("norm", C.c_int32),
+                ("interleaved", C.c_int32), ("max_positions", C.c_int32), ("x_token_stride", C.c_int64),
+                ("x_head_stride", C.c_int64), ("out_token_stride", C.c_int64), ("out_head_stride", C.c_int64)]
+
+
+class SmlaDenseDims(C.Structure):
+    _fields_ = [("batch", C.c_int32), ("num_heads", C.c_int32), ("page_size", C.c_int32),
+                ("max_pages_per_seq", C.c_int32), ("d_latent", C.c_int32), ("d_rope", C.c_int32),
+                ("num_pages", C.c_int64), ("queries_per_request", C.c_int32), ("ctas", C.c_int32)]
+
+
+class SmlaDensePlan(C.Structure):
+    _fields_ = [("rows_per_cta", C.c_int32), ("row_groups", C.c_int32), ("ctas", C.c_int32),
+                ("reserved", C.c_int32), ("workspace_bytes", C.c_size_t)]
+
+
 class SmlaTopkDims(C.Structure):
     _fields_ = [("batch", C.c_int32), ("num_cols", C.c_int32), ("row_stride", C.c_int64), ("k", C.c_int32),
                 ("cluster_ctas", C.c_int32)]
@@ -40,6 +66,14 @@ _SIGS = {
     "sparse_mla_plan": (C.c_int, [C.POINTER(SmlaDims), C.c_int32, C.POINTER(SmlaPlan)]),
     "sparse_mla_workspace_size": (C.c_size_t, [C.POINTER(SmlaDims), C.c_int32]),
     "sparse_mla_kv_append": (C.c_int, [C.POINTER(SmlaAppendDims), _P, _P, _P, _P, _P, _P, _P, _P]),
+    "sparse_mla_kv_norm_append": (C.c_int, [C.POINTER(SmlaNormAppendDims), _P, _P, _P, C.c_float, _P, _P, _P, _P, _P,
+                                            _P, _P]),
+    "sparse_mla_norm_rope": (C.c_int, [C.POINTER(SmlaNormRopeDims), _P, _P, C.c_float, _P, _P, _P, _P, _P]),
+    "sparse_mla_kv_read": (C.c_int, [C.POINTER(SmlaAppendDims), _P, _P, _P, _P, _P, C.c_int32, _P, _P]),
+    "sparse_mla_dense_plan_for": (C.c_int, [C.POINTER(SmlaDenseDims), C.c_int32, C.POINTER(SmlaDensePlan)]),
+    "sparse_mla_dense_plan": (C.c_int, [C.POINTER(SmlaDenseDims), C.c_int32, C.POINTER(SmlaDensePlan)]),
+    "sparse_mla_dense_decode": (C.c_int, [C.POINTER(SmlaDenseDims), _P, _P, _P, _P, C.c_float, _P, _P, _P,
+                                          C.c_size_t, _P]),
     "sparse_mla_topk_select": (C.c_int, [C.POINTER(SmlaTopkDims), _P, _P, _P, _P, _P]),
     "sparse_mla_topk_plan_for": (C.c_int, [C.POINTER(SmlaTopkDims), C.c_int32, C.POINTER(C.c_int32),
                                          C.POINTER(C.c_int32)]),
@@ -61,7 +95,8 @@ _SIGS = {
 
 STATUS = {0: "SMLA_OK", 1: "SMLA_ERR_INVALID_ARG", 2: "SMLA_ERR_UNSUPPORTED", 3: "SMLA_ERR_WORKSPACE",
           4: "SMLA_ERR_CUDA"}
-DEVERR_PAGE_RANGE, DEVERR_TIMEOUT, DEVERR_RANGE = 0x1, 0x2, 0x4
+DEVERR_PAGE_RANGE, DEVERR_TIMEOUT, DEVERR_RANGE, DEVERR_LEN_RANGE = 0x1, 0x2, 0x4, 0x8
+BF16, FP16, FP32 = 0, 1, 2      # smla_dtype
 
 
 def lib_path() -> str:

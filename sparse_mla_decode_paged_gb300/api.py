@@ -11,7 +11,8 @@ from typing import Optional, Tuple
 import torch
 
 from . import _native
-from ._native import SmlaAppendDims, SmlaDims, SmlaPlan, SmlaTopkDims, check
+from ._native import (SmlaAppendDims, SmlaDenseDims, SmlaDensePlan, SmlaDims, SmlaNormAppendDims, SmlaNormRopeDims,
+                      SmlaPlan, SmlaTopkDims, check)
 
 PAGE_SIZE, D_LATENT, D_ROPE, D_QK = 64, 512, 64, 576
 
@@ -208,6 +209,301 @@ def sparse_mla_kv_append(latent: torch.Tensor, rope: torch.Tensor, block_table: 
     check("sparse_mla_kv_append", _lib().sparse_mla_kv_append(
         C.byref(dims), _ptr(latent), _ptr(rope), _ptr(block_table), _ptr(requests), _ptr(positions),
         _ptr(kv_cache), _ptr(err_word), _stream(stream)))
+
+
+# ----------------------------------------------------------------------------- around the paged cache
+
+_DTYPE = {torch.bfloat16: _native.BF16, torch.float16: _native.FP16, torch.float32: _native.FP32}
+
+
+def _same_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+
+
+def _err_word(t, dev):
+    if t is not None:
+        _need(t, "err_word", torch.int32, 1)
+        if t.numel() < 1 or t.device != dev:
+            raise ValueError(f"err_word must hold one int32 on {dev}")
+    return _ptr(t)
+
+
+class _on:
+    """The stream a call launches on (the caller's, or its device's current one), with the tensors' device
+    current and, for a stream of the caller's, allocations made on it."""
+
+    def __init__(self, dev, stream=None):
+        self.raw = (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
+        self.ctx = None
+        if stream is not None:
+            if stream.device != dev:
+                raise ValueError(f"stream must belong to {dev}, got {stream.device}")
+            self.ctx = torch.cuda.stream(stream)
+        elif dev.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.raw
+
+    def __exit__(self, *a):
+        if self.ctx is not None:
+            self.ctx.__exit__(*a)
+
+
+def rope_table(max_positions: int, rope_dim: int = D_ROPE, base: float = 10000.0, device=None) -> torch.Tensor:
+    """float32 [max_positions, rope_dim]: cos of the rotation angles of each position in the first half of a row,
+    sin in the second (angle of pair j at position t: t * base ** (-2 j / rope_dim), formed in 64 bits)."""
+    if rope_dim < 2 or rope_dim % 2 != 0 or max_positions < 1:
+        raise ValueError("rope_dim must be even and positive, max_positions positive")
+    dev = device or "cuda"
+    freq = base ** (-torch.arange(0, rope_dim, 2, dtype=torch.float64, device=dev) / rope_dim)
+    angle = torch.arange(max_positions, dtype=torch.float64, device=dev)[:, None] * freq
+    return torch.cat([angle.cos(), angle.sin()], dim=-1).float().contiguous()
+
+
+def _need_rows(t, name: str, cols: int):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or t.dtype not in _DTYPE:
+        raise TypeError(f"{name} must be a bfloat16, float16 or float32 CUDA tensor")
+    if t.dim() != 2 or t.shape[1] != cols or t.stride(1) != 1 or (t.shape[0] > 1 and t.stride(0) < cols):
+        raise ValueError(f"{name} must be [T,{cols}] with unit stride in a row and rows that do not overlap")
+
+
+def _need_paged(kv_cache, block_table, positions, requests, T: int):
+    _need(block_table, "block_table", torch.int32, 2)
+    _need(positions, "positions", torch.int32, 1)
+    _need(kv_cache, "kv_cache", torch.uint8, 3)
+    if kv_cache.shape[1] != PAGE_SIZE or kv_cache.shape[2] != 656:
+        raise ValueError("kv_cache must be [pages,64,656]")
+    if positions.shape[0] != T:
+        raise ValueError("positions must be [T]")
+    if requests is not None:
+        _need(requests, "requests", torch.int32, 1)
+        if requests.shape[0] != T:
+            raise ValueError("requests must be [T]")
+    _same_device(kv_cache.device, block_table=block_table, positions=positions, requests=requests)
+
+
+def sparse_mla_kv_norm_append(latent: torch.Tensor, rope: torch.Tensor, norm_weight: torch.Tensor, eps: float,
+                              cos_sin: torch.Tensor, block_table: torch.Tensor, positions: torch.Tensor,
+                              kv_cache: torch.Tensor, requests: Optional[torch.Tensor] = None,
+                              interleaved: bool = True, err_word: Optional[torch.Tensor] = None,
+                              stream=None) -> None:
+    """RMS norm of the latent [T,512] (weight [512]), rotation of the rope [T,64] at its position, FP8
+    quantisation and the record write of sparse_mla_kv_append in one pass; kv_cache is written in place.
+
+    latent and rope: bf16, fp16 or fp32, rows may be strided (slices of one projection output); norm_weight of
+    their type or fp32; cos_sin fp32 [positions,64] (rope_table)."""
+    _need_rows(latent, "latent", D_LATENT)
+    _need_rows(rope, "rope", D_ROPE)
+    T = latent.shape[0]
+    if rope.shape[0] != T or rope.dtype != latent.dtype:
+        raise ValueError("latent and rope need the same number of rows and one type")
+    _need(norm_weight, "norm_weight", norm_weight.dtype if norm_weight.dtype == torch.float32 else latent.dtype, 1)
+    if norm_weight.shape[0] != D_LATENT:
+        raise ValueError("norm_weight must be [512]")
+    _need(cos_sin, "cos_sin", torch.float32, 2)
+    if cos_sin.shape[1] != D_ROPE:
+        raise ValueError("cos_sin must be [positions,64]")
+    _need_paged(kv_cache, block_table, positions, requests, T)
+    dev = kv_cache.device
+    _same_device(dev, latent=latent, rope=rope, norm_weight=norm_weight, cos_sin=cos_sin)
+    dims = SmlaNormAppendDims(T, block_table.shape[0], PAGE_SIZE, block_table.shape[1], D_LATENT, D_ROPE,
+                              kv_cache.shape[0], latent.stride(0) if T > 1 else D_LATENT,
+                              rope.stride(0) if T > 1 else D_ROPE, _DTYPE[latent.dtype], _DTYPE[norm_weight.dtype],
+                              cos_sin.shape[0], 1 if interleaved else 0)
+    err = _err_word(err_word, dev)
+    with _on(dev, stream) as st:
+        check("sparse_mla_kv_norm_append", _lib().sparse_mla_kv_norm_append(
+            C.byref(dims), _ptr(latent), _ptr(rope), _ptr(norm_weight), eps, _ptr(cos_sin), _ptr(block_table),
+            _ptr(requests), _ptr(positions), _ptr(kv_cache), err, st))
+
+
+def _apart(x: torch.Tensor, out: torch.Tensor) -> bool:
+    """Whether out may be written while x is read: x itself, memory of its own, or other columns of x's rows."""
+    if x.data_ptr() == out.data_ptr() and x.stride() == out.stride():
+        return True
+    size = x.element_size()
+    span = [(t.data_ptr(), t.data_ptr() + size * (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))))
+            for t in (x, out)]
+    if x.numel() == 0 or span[0][1] <= span[1][0] or span[1][1] <= span[0][0]:
+        return True
+    if x.stride() != out.stride() or min(x.stride()[:2]) < 1 or max(x.stride()[:2]) % min(x.stride()[:2]) != 0:
+        return False
+    step, d = min(x.stride()[:2]), (out.data_ptr() - x.data_ptr()) % (size * min(x.stride()[:2]))
+    return size * x.shape[2] <= d <= size * (step - x.shape[2])
+
+
+def sparse_mla_norm_rope(x: torch.Tensor, positions: Optional[torch.Tensor] = None,
+                         cos_sin: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+                         eps: float = 1e-6, norm: bool = True, rope_offset: int = 0, interleaved: bool = True,
+                         out: Optional[torch.Tensor] = None, err_word: Optional[torch.Tensor] = None,
+                         stream=None) -> torch.Tensor:
+    """x [T,H,D] (bf16, fp16 or fp32, unit stride along D): RMS norm of each head's vector (norm, with an optional
+    weight [D] of x's type or fp32), then rotation of the dims [rope_offset, rope_offset + cos_sin.shape[1]) at
+    positions [T] (cos_sin fp32, rope_table; None: no rotation).  out: as x, or x itself."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    if not x.is_cuda or x.dtype not in _DTYPE:
+        raise TypeError("x must be a bfloat16, float16 or float32 CUDA tensor")
+    if x.dim() != 3 or x.shape[1] < 1 or x.shape[2] < 1 or (x.shape[2] > 1 and x.stride(2) != 1):
+        raise ValueError("x must be [T,H,D] with unit stride along D")
+    T, H, D = x.shape
+    dev = x.device
+    if weight is not None:
+        if not norm:
+            raise ValueError("weight without norm")
+        _need(weight, "weight", weight.dtype if weight.dtype == torch.float32 else x.dtype, 1)
+        if weight.shape[0] != D:
+            raise ValueError("weight must be [D]")
+    rope_dim = max_pos = 0
+    if cos_sin is not None:
+        _need(cos_sin, "cos_sin", torch.float32, 2)
+        if positions is None:
+            raise ValueError("cos_sin without positions")
+        _need(positions, "positions", torch.int32, 1)
+        if positions.shape[0] != T:
+            raise ValueError("positions must be [T]")
+        max_pos, rope_dim = cos_sin.shape
+    _same_device(dev, weight=weight, cos_sin=cos_sin, positions=positions, out=out)
+    err = _err_word(err_word, dev)
+    with _on(dev, stream) as st:
+        if out is None:
+            out = torch.empty((T, H, D), dtype=x.dtype, device=dev)
+        elif out.shape != x.shape or out.dtype != x.dtype or (D > 1 and out.stride(2) != 1):
+            raise ValueError("out must have x's shape and type and unit stride along D")
+        elif not _apart(x, out):
+            raise ValueError("out must be x itself or not overlap it")
+        dims = SmlaNormRopeDims(T, H, D, rope_dim, rope_offset, _DTYPE[x.dtype],
+                                _DTYPE[weight.dtype if weight is not None else x.dtype], 1 if norm else 0,
+                                1 if interleaved else 0, max_pos, x.stride(0), x.stride(1), out.stride(0),
+                                out.stride(1))
+        check("sparse_mla_norm_rope", _lib().sparse_mla_norm_rope(
+            C.byref(dims), _ptr(x), _ptr(weight), eps, _ptr(cos_sin), _ptr(positions) if rope_dim else None,
+            _ptr(out), err, st))
+    return out
+
+
+def sparse_mla_kv_read(kv_cache: torch.Tensor, block_table: torch.Tensor, positions: torch.Tensor,
+                       requests: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                       dtype: torch.dtype = torch.bfloat16, err_word: Optional[torch.Tensor] = None,
+                       stream=None) -> torch.Tensor:
+    """[T,576]: the records at (requests[i] or i, positions[i]) as [latent * scale | rope] rows of dtype (out's type
+    when out is given); zeros for a token out of range."""
+    T = positions.shape[0] if isinstance(positions, torch.Tensor) and positions.dim() == 1 else -1
+    _need_paged(kv_cache, block_table, positions, requests, T)
+    dev = kv_cache.device
+    if out is not None:
+        dtype = out.dtype
+        _need(out, "out", dtype, 2)
+        if out.shape != (T, D_QK) or out.device != dev:
+            raise ValueError(f"out must be [T,576] on {dev}")
+    if dtype not in _DTYPE:
+        raise TypeError("out must be bfloat16, float16 or float32")
+    err = _err_word(err_word, dev)
+    dims = SmlaAppendDims(T, block_table.shape[0], PAGE_SIZE, block_table.shape[1], D_LATENT, D_ROPE,
+                          kv_cache.shape[0])
+    with _on(dev, stream) as st:
+        if out is None:
+            out = torch.empty((T, D_QK), dtype=dtype, device=dev)
+        check("sparse_mla_kv_read", _lib().sparse_mla_kv_read(
+            C.byref(dims), _ptr(kv_cache), _ptr(block_table), _ptr(requests), _ptr(positions), _ptr(out),
+            _DTYPE[dtype], err, st))
+    return out
+
+
+def make_dense_dims(B: int, H: int, max_pages_per_seq: int, num_pages: int, queries_per_request: int = 1,
+                    ctas: int = 0) -> SmlaDenseDims:
+    return SmlaDenseDims(B, H, PAGE_SIZE, max_pages_per_seq, D_LATENT, D_ROPE, num_pages, queries_per_request, ctas)
+
+
+def dense_dims_of(q, kv_cache, block_table, ctas: int = 0) -> SmlaDenseDims:
+    """Shapes of a dense decode; several queries per request when q has a multiple of block_table's rows."""
+    return make_dense_dims(q.shape[0], q.shape[1], block_table.shape[1], kv_cache.shape[0],
+                           q.shape[0] // block_table.shape[0], ctas)
+
+
+def dense_plan_for(dims: SmlaDenseDims, sm_count: int) -> SmlaDensePlan:
+    p = SmlaDensePlan()
+    check("sparse_mla_dense_plan_for", _lib().sparse_mla_dense_plan_for(C.byref(dims), sm_count, C.byref(p)))
+    return p
+
+
+def dense_plan(dims: SmlaDenseDims, device: Optional[int] = None) -> SmlaDensePlan:
+    p = SmlaDensePlan()
+    dev = torch.cuda.current_device() if device is None else device
+    check("sparse_mla_dense_plan", _lib().sparse_mla_dense_plan(C.byref(dims), dev, C.byref(p)))
+    return p
+
+
+def alloc_dense_workspace(dims: SmlaDenseDims, device=None) -> torch.Tensor:
+    """Caller-owned workspace of sparse_mla_dense_decode with a clear error word."""
+    dev = torch.device(device or "cuda")
+    ws = torch.empty(dense_plan(dims, dev.index).workspace_bytes, dtype=torch.uint8, device=dev)
+    ws[:256].zero_()
+    return ws
+
+
+# Dense decode dims by call shape (the library reads dims, never writes them).
+_DENSE_DIMS = {}
+
+
+def sparse_mla_dense_decode(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.Tensor,
+                            seq_lens: torch.Tensor, sm_scale: float, out: Optional[torch.Tensor] = None,
+                            lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                            stream=None, ctas: int = 0) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of q bf16 [B,H,576] over every position below seq_lens[b] of its request's cache: out bf16
+    [B,H,512], lse fp32 [B,H].  H is 1 .. 128; block_table has one row per request, seq_lens one entry per query
+    (B a multiple of the requests).  ctas = 0: one CTA per SM.  Calls in flight at once need a workspace each
+    (alloc_dense_workspace); without one a call allocates its own, and its error word is lost."""
+    _need(q, "q", torch.bfloat16, 3)
+    _need(kv_cache, "kv_cache", torch.uint8, 3)
+    _need(block_table, "block_table", torch.int32, 2)
+    _need(seq_lens, "seq_lens", torch.int32, 1)
+    dev = q.device
+    key = (q.shape, kv_cache.shape, block_table.shape, seq_lens.shape, ctas)
+    dims = _DENSE_DIMS.get(key)
+    if dims is None:
+        B, R = q.shape[0], block_table.shape[0]
+        if q.shape[2] != D_QK or kv_cache.shape[1] != PAGE_SIZE or kv_cache.shape[2] != 656:
+            raise ValueError("q must be [B,H,576] and kv_cache [pages,64,656]")
+        if R < 1 or B % R != 0 or seq_lens.shape[0] != B:
+            raise ValueError("q and seq_lens need one row per query, block_table one row per request (a divisor of "
+                             "the query count)")
+        dims = dense_dims_of(q, kv_cache, block_table, ctas)
+        if len(_DENSE_DIMS) > 256:
+            _DENSE_DIMS.clear()
+        _DENSE_DIMS[key] = dims
+    _same_device(dev, kv_cache=kv_cache, block_table=block_table, seq_lens=seq_lens, out=out, lse=lse,
+                 workspace=workspace)
+    with _on(dev, stream) as st:
+        if out is None:
+            out = torch.empty((q.shape[0], q.shape[1], D_LATENT), dtype=torch.bfloat16, device=dev)
+        else:
+            _need(out, "out", torch.bfloat16, 3)
+            if out.shape[:2] != q.shape[:2] or out.shape[2] != D_LATENT:
+                raise ValueError("out must be [B,H,512]")
+        if lse is None:
+            lse = torch.empty((q.shape[0], q.shape[1]), dtype=torch.float32, device=dev)
+        else:
+            _need(lse, "lse", torch.float32, 2)
+            if lse.shape != q.shape[:2]:
+                raise ValueError("lse must be [B,H]")
+        if workspace is None:
+            workspace = alloc_dense_workspace(dims, dev)
+        else:
+            _need(workspace, "workspace", torch.uint8, 1)
+        r = _lib().sparse_mla_dense_decode(
+            dims, q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), sm_scale,
+            out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(), st)
+    if r != 0:
+        check("sparse_mla_dense_decode", r)
+    return out, lse
 
 
 def sparse_mla_topk_select(scores: torch.Tensor, seq_lens: torch.Tensor, k: int, cluster_ctas: int = 0,

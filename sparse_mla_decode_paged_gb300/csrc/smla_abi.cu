@@ -2,6 +2,7 @@
 // the caller's stream.  No allocation, no synchronisation (except
 // sparse_mla_read_errors).
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include <atomic>
@@ -48,6 +49,11 @@ int check_inputs(const void* q, const void* kv, const int32_t* bt, const int32_t
     return SMLA_ERR_INVALID_ARG;
   return SMLA_OK;
 }
+
+bool dtype_known(int32_t t) { return t == SMLA_BF16 || t == SMLA_FP16 || t == SMLA_FP32; }
+uintptr_t dtype_size(int32_t t) { return t == SMLA_FP32 ? 4 : 2; }
+bool weight_dtype_ok(int32_t w, int32_t x) { return w == x || w == SMLA_FP32; }
+bool eps_ok(float eps) { return eps >= 0.f && eps < INFINITY; }     // false for a NaN
 
 constexpr int kMaxDevices = 64;
 
@@ -247,6 +253,183 @@ extern "C" int sparse_mla_kv_append(const smla_append_dims* d, const void* laten
   p.num_pages = d->num_pages;
   p.err = err_word;
   return launch_kv_append(p, (cudaStream_t)stream) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+}
+
+extern "C" int sparse_mla_kv_norm_append(const smla_norm_append_dims* d, const void* latent, const void* rope,
+                                         const void* norm_weight, float eps, const float* cos_sin,
+                                         const int32_t* block_table, const int32_t* requests,
+                                         const int32_t* positions, void* kv_cache, uint32_t* err_word,
+                                         smla_stream_t stream) {
+  if (!d) return SMLA_ERR_INVALID_ARG;
+  if (d->tokens < 0 || d->num_requests < 1 || d->max_pages_per_seq < 1 || d->num_pages < 1 || d->max_positions < 1)
+    return SMLA_ERR_INVALID_ARG;
+  if (!dtype_known(d->dtype) || !weight_dtype_ok(d->weight_dtype, d->dtype) || !eps_ok(eps) ||
+      (d->interleaved != 0 && d->interleaved != 1))
+    return SMLA_ERR_INVALID_ARG;
+  if (d->page_size != kPageSize || d->d_latent != kDLatent || d->d_rope != kDRope) return SMLA_ERR_UNSUPPORTED;
+  if (d->latent_stride < kDLatent || d->rope_stride < kDRope) return SMLA_ERR_INVALID_ARG;
+  if (d->tokens > 0) {
+    if (!latent || !rope || !norm_weight || !cos_sin || !block_table || !positions || !kv_cache)
+      return SMLA_ERR_INVALID_ARG;
+    const uintptr_t e = dtype_size(d->dtype);
+    if (!aligned(latent, e) || !aligned(rope, e) || !aligned(norm_weight, dtype_size(d->weight_dtype)) ||
+        !aligned(cos_sin, 16) || !aligned(kv_cache, 16) || !aligned(block_table, 4) || !aligned(positions, 4) ||
+        (requests && !aligned(requests, 4)))
+      return SMLA_ERR_INVALID_ARG;
+  }
+  if (err_word && !aligned(err_word, 4)) return SMLA_ERR_INVALID_ARG;
+  NormAppendParams p{};
+  p.latent = latent;
+  p.rope = rope;
+  p.weight = norm_weight;
+  p.cos_sin = cos_sin;
+  p.block_table = block_table;
+  p.requests = requests;
+  p.positions = positions;
+  p.kv = static_cast<uint8_t*>(kv_cache);
+  p.num_pages = d->num_pages;
+  p.latent_stride = d->latent_stride;
+  p.rope_stride = d->rope_stride;
+  p.tokens = d->tokens;
+  p.num_requests = d->num_requests;
+  p.max_pages = d->max_pages_per_seq;
+  p.max_positions = d->max_positions;
+  p.dtype = d->dtype;
+  p.weight_dtype = d->weight_dtype;
+  p.interleaved = d->interleaved;
+  p.eps = eps;
+  p.err = err_word;
+  return launch_kv_norm_append(p, (cudaStream_t)stream) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+}
+
+extern "C" int sparse_mla_norm_rope(const smla_norm_rope_dims* d, const void* x, const void* weight, float eps,
+                                    const float* cos_sin, const int32_t* positions, void* out, uint32_t* err_word,
+                                    smla_stream_t stream) {
+  if (!d) return SMLA_ERR_INVALID_ARG;
+  if (d->tokens < 0 || d->num_heads < 1 || d->head_dim < 1 || d->rope_dim < 0 || d->rope_dim % 2 != 0 ||
+      d->rope_offset < 0 || (int64_t)d->rope_offset + d->rope_dim > d->head_dim)
+    return SMLA_ERR_INVALID_ARG;
+  if (!dtype_known(d->dtype) || !weight_dtype_ok(d->weight_dtype, d->dtype) || (d->norm != 0 && d->norm != 1) ||
+      (d->interleaved != 0 && d->interleaved != 1) || !eps_ok(eps))
+    return SMLA_ERR_INVALID_ARG;
+  if (d->rope_dim > 0 && d->max_positions < 1) return SMLA_ERR_INVALID_ARG;
+  if (d->head_dim > kMaxNormRopeDim) return SMLA_ERR_UNSUPPORTED;
+  if (d->x_token_stride < 0 || d->x_head_stride < 0 || d->out_token_stride < 0 || d->out_head_stride < 0)
+    return SMLA_ERR_INVALID_ARG;
+  // rows of out must not overlap: the smaller stride covers a row, the larger one every row of the smaller
+  if (d->tokens > 0) {
+    const bool token_outer = d->out_token_stride >= d->out_head_stride;
+    const int64_t inner = token_outer ? d->out_head_stride : d->out_token_stride;
+    const int64_t outer = token_outer ? d->out_token_stride : d->out_head_stride;
+    const int64_t n_inner = token_outer ? d->num_heads : d->tokens, n_outer = token_outer ? d->tokens : d->num_heads;
+    if (n_inner > 1 && inner < d->head_dim) return SMLA_ERR_INVALID_ARG;
+    const int64_t span = (n_inner > 1 ? (n_inner - 1) * inner : 0) + d->head_dim;
+    if (n_outer > 1 && outer < (n_inner > 1 ? span : d->head_dim)) return SMLA_ERR_INVALID_ARG;
+    if (!x || !out || (d->rope_dim > 0 && (!cos_sin || !positions))) return SMLA_ERR_INVALID_ARG;
+    const uintptr_t e = dtype_size(d->dtype);
+    if (!aligned(x, e) || !aligned(out, e) || (weight && !aligned(weight, dtype_size(d->weight_dtype))) ||
+        (cos_sin && !aligned(cos_sin, 4)) || (positions && !aligned(positions, 4)))
+      return SMLA_ERR_INVALID_ARG;
+  }
+  if (err_word && !aligned(err_word, 4)) return SMLA_ERR_INVALID_ARG;
+  NormRopeParams p{};
+  p.x = x;
+  p.weight = weight;
+  p.cos_sin = cos_sin;
+  p.positions = positions;
+  p.out = out;
+  p.x_token = d->x_token_stride;
+  p.x_head = d->x_head_stride;
+  p.out_token = d->out_token_stride;
+  p.out_head = d->out_head_stride;
+  p.tokens = d->tokens;
+  p.heads = d->num_heads;
+  p.dim = d->head_dim;
+  p.rope_dim = d->rope_dim;
+  p.rope_offset = d->rope_offset;
+  p.max_positions = d->max_positions;
+  p.dtype = d->dtype;
+  p.weight_dtype = d->weight_dtype;
+  p.norm = d->norm;
+  p.interleaved = d->interleaved;
+  p.eps = eps;
+  p.err = err_word;
+  return launch_norm_rope(p, (cudaStream_t)stream) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+}
+
+extern "C" int sparse_mla_kv_read(const smla_append_dims* d, const void* kv_cache, const int32_t* block_table,
+                                  const int32_t* requests, const int32_t* positions, void* out, int32_t out_dtype,
+                                  uint32_t* err_word, smla_stream_t stream) {
+  if (!d) return SMLA_ERR_INVALID_ARG;
+  if (d->tokens < 0 || d->num_requests < 1 || d->max_pages_per_seq < 1 || d->num_pages < 1 || !dtype_known(out_dtype))
+    return SMLA_ERR_INVALID_ARG;
+  if (d->page_size != kPageSize || d->d_latent != kDLatent || d->d_rope != kDRope) return SMLA_ERR_UNSUPPORTED;
+  if (d->tokens > 0) {
+    if (!kv_cache || !block_table || !positions || !out) return SMLA_ERR_INVALID_ARG;
+    if (!aligned(kv_cache, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(positions, 4) ||
+        (requests && !aligned(requests, 4)))
+      return SMLA_ERR_INVALID_ARG;
+  }
+  if (err_word && !aligned(err_word, 4)) return SMLA_ERR_INVALID_ARG;
+  ReadParams p{};
+  p.kv = static_cast<const uint8_t*>(kv_cache);
+  p.block_table = block_table;
+  p.requests = requests;
+  p.positions = positions;
+  p.out = out;
+  p.num_pages = d->num_pages;
+  p.tokens = d->tokens;
+  p.num_requests = d->num_requests;
+  p.max_pages = d->max_pages_per_seq;
+  p.out_dtype = out_dtype;
+  p.err = err_word;
+  return launch_kv_read(p, (cudaStream_t)stream) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+}
+
+extern "C" int sparse_mla_dense_plan(const smla_dense_dims* dims, int32_t device, smla_dense_plan* plan) {
+  if (!dims || !plan || device < 0) return SMLA_ERR_INVALID_ARG;
+  int sms = 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return SMLA_ERR_CUDA;
+  return sparse_mla_dense_plan_for(dims, sms, plan);
+}
+
+extern "C" int sparse_mla_dense_decode(const smla_dense_dims* d, const void* q, const void* kv_cache,
+                                       const int32_t* block_table, const int32_t* seq_lens, float sm_scale, void* out,
+                                       float* lse, void* workspace, size_t workspace_bytes, smla_stream_t stream) {
+  // the checks that need no device come first, with a nominal SM count
+  smla_dense_plan plan;
+  int st = sparse_mla_dense_plan_for(d, 1, &plan);
+  if (st != SMLA_OK) return st;
+  st = check_inputs(q, kv_cache, block_table, seq_lens, seq_lens);
+  if (st != SMLA_OK) return st;
+  if (!out || !lse || !aligned(out, 16) || !aligned(lse, 4)) return SMLA_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < plan.workspace_bytes || !aligned(workspace, 256)) return SMLA_ERR_WORKSPACE;
+  int sms = 0;
+  st = sm_count_of_current_device(&sms);
+  if (st != SMLA_OK) return st;
+  st = sparse_mla_dense_plan_for(d, sms, &plan);
+  if (st != SMLA_OK) return st;
+  if (workspace_bytes < plan.workspace_bytes) return SMLA_ERR_WORKSPACE;
+  DenseParams p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.kv = static_cast<const uint8_t*>(kv_cache);
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.sm_scale = sm_scale;
+  p.B = d->batch;
+  p.H = d->num_heads;
+  p.q_per_req = d->queries_per_request > 1 ? d->queries_per_request : 1;
+  p.max_pages = d->max_pages_per_seq;
+  p.num_pages = d->num_pages;
+  p.requests = p.B / p.q_per_req;
+  p.nr = plan.rows_per_cta;
+  p.groups = plan.row_groups;
+  p.ctas = plan.ctas;
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.err = static_cast<uint32_t*>(workspace);
+  p.wait_ns = split_wait_limit_ns();
+  return launch_dense(p, (cudaStream_t)stream) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
 }
 
 extern "C" int sparse_mla_topk_select(const smla_topk_dims* d, const float* scores, const int32_t* seq_lens,

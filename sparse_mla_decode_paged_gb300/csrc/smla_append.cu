@@ -17,13 +17,6 @@ namespace {
 
 constexpr int kAppendThreads = 128;
 
-// fp32 pair -> two E4M3 codes (round to nearest even, saturating to +-448), low byte = a.
-__device__ __forceinline__ uint16_t f32x2_to_e4m3x2(float a, float b) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
-  return r;
-}
-
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendParams p) {
   const int tok = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

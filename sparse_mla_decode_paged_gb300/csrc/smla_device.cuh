@@ -51,6 +51,13 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t two) {
   return r;
 }
 
+// fp32 pair -> two E4M3 codes (round to nearest even, saturating to +-448), low byte = a.
+__device__ __forceinline__ uint16_t f32x2_to_e4m3x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+
 __device__ __forceinline__ float2 f16x2_to_f32x2(uint32_t h) {
   __half2 v = *reinterpret_cast<__half2*>(&h);
   return __half22float2(v);

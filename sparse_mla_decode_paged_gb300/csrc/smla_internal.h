@@ -89,12 +89,84 @@ bool topk_plan(int batch, int num_cols, int sm_count, int forced_csize, int* csi
 size_t topk_smem_bytes(int chunk);
 cudaError_t launch_topk(const TopkParams& p, int batch, cudaStream_t stream);
 
+// Everything the fused norm + rotation + append kernel needs for one launch.
+struct NormAppendParams {
+  const void* latent;         // dtype, rows latent_stride elements apart
+  const void* rope;           // dtype, rows rope_stride elements apart
+  const void* weight;         // weight type [512]
+  const float* cos_sin;       // [max_positions][64]
+  const int32_t* block_table; // [num_requests][max_pages]
+  const int32_t* requests;    // [tokens] or null: token i belongs to request i
+  const int32_t* positions;   // [tokens]
+  uint8_t* kv;                // [num_pages][64][656]
+  int64_t num_pages, latent_stride, rope_stride;
+  int tokens, num_requests, max_pages, max_positions;
+  int dtype, weight_dtype;
+  int interleaved;
+  float eps;
+  uint32_t* err;              // device error word (may be null)
+};
+
+constexpr int kMaxNormRopeDim = 1024;  // largest head of the per-head norm + rotation
+
+// Everything the per-head norm + rotation kernel needs for one launch.
+struct NormRopeParams {
+  const void* x;
+  const void* weight;         // [D] or null
+  const float* cos_sin;       // [max_positions][rope_dim]
+  const int32_t* positions;   // [tokens]
+  void* out;
+  int64_t x_token, x_head, out_token, out_head;   // strides in elements
+  int tokens, heads, dim, rope_dim, rope_offset, max_positions;
+  int dtype, weight_dtype, norm, interleaved;
+  float eps;
+  uint32_t* err;              // device error word (may be null)
+};
+
+// Everything the record reader needs for one launch.
+struct ReadParams {
+  const uint8_t* kv;          // [num_pages][64][656]
+  const int32_t* block_table; // [num_requests][max_pages]
+  const int32_t* requests;    // [tokens] or null: token i belongs to request i
+  const int32_t* positions;   // [tokens]
+  void* out;                  // [tokens][576]
+  int64_t num_pages;
+  int tokens, num_requests, max_pages, out_dtype;
+  uint32_t* err;              // device error word (may be null)
+};
+
+// Dense decode (every cached position): see smla_dense.cu for the work split.
+constexpr int kDenseTile = 128;        // positions per tile (two pages)
+constexpr int kDenseMaxCtas = 1024;
+constexpr int kDenseMaxHeads = 128;
+struct DenseParams {
+  const uint16_t* q;          // bf16 [B][H][576]
+  const uint8_t* kv;          // [num_pages][64][656]
+  const int32_t* block_table; // [B / q_per_req][max_pages]
+  const int32_t* seq_lens;    // [B]
+  float sm_scale;
+  int B, H, q_per_req, max_pages;
+  int64_t num_pages;
+  int requests;               // B / q_per_req
+  int nr;                     // rows per CTA (16, 32 or 64)
+  int groups;                 // row groups per request
+  int ctas;
+  uint16_t* out;              // bf16 [B][H][512]
+  float* lse;                 // [B][H]
+  uint32_t* err;              // device error word
+  uint64_t wait_ns;           // time limit of each pipeline wait inside the kernel
+};
+
 // Kernel launchers (return the launch error).
 cudaError_t launch_split(const SplitParams& p, cudaStream_t stream);
 size_t workspace_bytes_for(int B, int H, int nsplit);
 cudaError_t launch_combine(int B, int H, int nsplit, const float* o_part, const float* lse_part,
                            uint16_t* out, float* lse, cudaStream_t stream);
 cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream);
+cudaError_t launch_kv_norm_append(const NormAppendParams& p, cudaStream_t stream);
+cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t stream);
+cudaError_t launch_kv_read(const ReadParams& p, cudaStream_t stream);
+cudaError_t launch_dense(const DenseParams& p, cudaStream_t stream);
 cudaError_t launch_gather_rows(const int32_t* bt, const int32_t* topk, const int32_t* seq_lens,
                                int B, int topk_n, int max_pages, int64_t num_pages, int q_per_req,
                                int64_t* rows, cudaStream_t stream);
