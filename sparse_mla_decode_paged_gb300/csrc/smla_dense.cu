@@ -1,97 +1,1082 @@
 // Dense decode attention over the paged FP8 latent cache: every cached position of a request attends
-// (no top-k list).  s_t = sm_scale q.k_t, out = softmax(s).v, lse = ln sum exp(s); each record is
-// k = [e4m3(code) * scale | rope], v = k[0..511].
+// (no top-k list).
 //
-// One CTA per (query, head): its 8 warps walk the positions in turn, each with a running maximum and
-// sum, and merge at the end.
+//   s_t = sm_scale q.k_t,  out = sum_t softmax_t(s) v_t,  lse = ln sum_t exp(s_t),
+//   k = [e4m3(code_d) scale_{d/128}, d < 512 | rope, 64], v = k[0..511].
+//
+// A request's rows (its queries' heads) form groups of NR = 16, 32 or 64 rows; an item is one (request, row
+// group), a tile 128 positions (two pages) of an item.  The tiles of all items, laid end to end, are shared
+// out over the CTAs in equal runs (from seq_lens, on the device), so a ragged batch or a single long request
+// keeps every SM busy; an item that crosses a CTA boundary leaves partial results that the merge kernel joins.
+//
+// Scores.  The codes go to the tensor core as they are (kind::f8f6f4), with no conversion: q is split into
+// two E4M3 terms, q 2^-x = hi + lo with x chosen per (row, 128-dim block) so that the block's largest element
+// lies in [2^7, 2^8).  hi keeps 4 significant bits and lo the other 4 of a bf16 value, so the split is exact but
+// for elements below about 2^-9 of the largest (their error is below 2^-17 of it).  S^T of a tile: M = 128
+// positions, N = 2 NR columns (hi rows, then lo rows), one accumulator per 128-dim scale block; the softmax
+// threads form s = sum_b (S_hi + S_lo) scale_b 2^x_b in fp32.  The rope part is a bf16 product.
+// Weights and values.  P = 2^(s - ref) in fp16 with ref = (a running maximum) - 7, moved only when a score
+// exceeds ref by more than 15: P stays below 2^15, and weights down to 2^-31 of the largest keep an absolute
+// error below 2^-32 of it, so that a long tail beside one dominating position is not lost.  V = fp16(code *
+// scale): O^T[512 x NR] += V^T P, M = 128 dims, fp32 in TMEM.
+//
+// What bounds it: HBM bytes (656 per position) for up to 64 rows, where one SM's share of the HBM rate is a
+// tile per 1.9 us; inside an SM the shared-memory path, which a tile of 64 rows takes about 640 KB through
+// (84 in, 152 QK operands, 64 + 128 conversion, 192 PV operands, 16 P).
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
+
+#include <atomic>
 
 #include "smla_device.cuh"
 #include "smla_internal.h"
 #include "smla_ptx.cuh"
+#include "smla_split_layout.cuh"
 
 namespace smla {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNoRef = -1e30f;          // reference of a row that has met no position yet
+constexpr float kRefBelowMax = 7.f;       // a new reference lies this far below the maximum it was taken from
+constexpr float kRefSlack = 15.f;         // a score this far above the reference moves it (2^15 is an fp16 value)
 
-__global__ void __launch_bounds__(32 * kWarps) dense_kernel(const DenseParams p) {
-  const int row = blockIdx.x, b = row / p.H;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t table_len = (int64_t)p.max_pages * kPageSize;
-  int len = max(__ldg(p.seq_lens + b), 0);
-  if (len > table_len) {
-    if (threadIdx.x == 0) atomicOr(p.err, SMLA_DEVERR_PAGE_RANGE);
-    len = (int)table_len;
+// Warps: 0-7 softmax (warp w: TMEM lanes of quadrant w % 4, row half w / 4), 8-15 conversion (two groups of
+// four), then one warp each for the copies, the QK and the PV.
+constexpr int kSoftWarps = 8, kConvWarps = 8;
+constexpr int kCopyWarp = 16, kQkWarp = 17, kPvWarp = 18;
+constexpr int kDenseThreads = 19 * 32;
+
+constexpr uint32_t kSlot = 16384;         // 128 positions x 128 bytes: one code block or the rope of a tile
+constexpr int kChunks = 5;                // rope, then the four code blocks
+constexpr int kSliceTokens = 16;          // positions of one V slice (one MMA K step)
+constexpr int kSlices = kDenseTile / kSliceTokens;
+constexpr int kScaleSlots = 3;
+
+template <int NR>
+struct DC {
+  static constexpr int kRing = 5;         // K slots
+  static constexpr int kVRing = 3;        // V slices
+  static constexpr int kSBufs = 2;        // score accumulators
+  static constexpr int HC = NR / 2;       // rows of one softmax thread
+  static constexpr uint32_t kQ8Chunk = 2 * NR * 128;
+  static constexpr uint32_t kQ8 = 0;
+  static constexpr uint32_t kQr = kQ8 + 4 * kQ8Chunk;
+  static constexpr uint32_t kK = (kQr + NR * 128 + 1023) / 1024 * 1024;
+  static constexpr uint32_t kV = kK + kRing * kSlot;
+  static constexpr uint32_t kP = kV + kVRing * kSlot;
+  static constexpr uint32_t kScale = kP + 128 * 2 * NR;
+  static constexpr uint32_t kF = kScale + kScaleSlots * 2048;     // [2][4][NR] float
+  static constexpr uint32_t kLen = kF + 2 * 4 * NR * 4;           // [2][NR] int
+  static constexpr uint32_t kRef = kLen + 2 * NR * 4;             // [NR] float
+  static constexpr uint32_t kRed = kRef + NR * 4;                 // [4][NR] float
+  static constexpr uint32_t kBar = kRed + 4 * NR * 4;
+  static constexpr uint32_t kBytes = kBar + 512;
+  static constexpr uint32_t kTmemCols = 8 * NR;
+  static constexpr uint32_t kSCol = 4 * NR;                       // score buffer i at 4 NR + 2 NR i
+  static constexpr int kPRow = 2 * NR;
+  static_assert(kBytes <= 232448, "shared memory");
+};
+
+struct Bars {
+  uint64_t kfull[8], kempty[8], vfull[4], vempty[4], sfull[2], sempty[2], scfull[4], scempty[4];
+  uint64_t pfull, pdone, qfull, drain[2];
+  uint32_t tmem;
+  int abort;
+  int armed_k[8], armed_sc[4];            // copies armed so far per slot
+  int pages_ok[4];                        // of the tile in each scale slot: bit h: page h is loaded
+  int first_item, first_tile, my_tiles;   // this CTA's run
+  long long total;
+};
+static_assert(sizeof(Bars) <= 512, "barrier area");
+
+// One (request, row group).
+struct Item {
+  int req, row0, nrows;                   // rows row0 .. row0 + nrows - 1 of the request's s_q H rows
+  int max_len, min_len;                   // over the group's queries, clamped to [0, table]
+  int tiles;                              // at least 1: a group without positions has one empty tile
+};
+
+__device__ __forceinline__ int clamped_len(const DenseParams& p, int b) {
+  const long long table = (long long)p.max_pages * kPageSize;
+  const long long n = max(__ldg(p.seq_lens + b), 0);
+  return (int)min(n, table);
+}
+
+__device__ __forceinline__ Item item_at(const DenseParams& p, int i) {
+  Item it;
+  it.req = i / p.groups;
+  const int rows = p.q_per_req * p.H;
+  it.row0 = (i - it.req * p.groups) * p.nr;
+  it.nrows = min(p.nr, rows - it.row0);
+  const int j0 = it.row0 / p.H, j1 = (it.row0 + it.nrows - 1) / p.H;
+  it.max_len = 0;
+  it.min_len = 0x7fffffff;
+  for (int j = j0; j <= j1; ++j) {
+    const int n = clamped_len(p, it.req * p.q_per_req + j);
+    it.max_len = max(it.max_len, n);
+    it.min_len = min(it.min_len, n);
   }
-  const int32_t* bt = p.block_table + (size_t)(b / p.q_per_req) * p.max_pages;
-  const uint16_t* q = p.q + (size_t)row * kDQK;
-  float ql[16], qr[2];
-  for (int i = 0; i < 16; ++i) ql[i] = bf16_to_f32(q[16 * lane + i]);
-  for (int i = 0; i < 2; ++i) qr[i] = bf16_to_f32(q[kDLatent + 2 * lane + i]);
-  float m = -CUDART_INF_F, l = 0.f, acc[16] = {};
-  for (int t = warp; t < len; t += kWarps) {
-    const int64_t r = row_of(bt, t, len, p.max_pages, p.num_pages, p.err);
-    if (r < 0) continue;
-    const unsigned char* rec = p.kv + r * kRecordBytes;
-    const uint4 codes = __ldg(reinterpret_cast<const uint4*>(rec) + lane);
-    const float scale = __ldg(reinterpret_cast<const float*>(rec + kDLatent) + (lane >> 3));
-    const uint32_t rope = __ldg(reinterpret_cast<const uint32_t*>(rec + kDLatent + 16) + lane);
-    const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-    float v[16], s = 0.f;
+  it.tiles = max(1, (int)(((long long)it.max_len + kDenseTile - 1) / kDenseTile));
+  return it;
+}
+
+// First tile of CTA c's run when T tiles are shared out over n CTAs.
+__device__ __forceinline__ long long run_start(long long T, int n, int c) { return T * c / n; }
+
+// The run as the kernel leaves it for the merge: where the last item of the run begins and ends.
+struct RunDesc {
+  long long total;                        // tiles of the batch
+  long long item_begin, item_end;         // global tile range of the run's last item
+  int item;
+  int pad;
+};
+
+// Walks the (item, tile) pairs of a run; every role has its own.
+struct Walk {
+  int i, t, left;
+  Item it;
+  __device__ __forceinline__ Walk(const DenseParams& p, const Bars* bars)
+      : i(bars->first_item), t(bars->first_tile), left(bars->my_tiles) {
+    if (left > 0) it = item_at(p, i);
+  }
+  __device__ __forceinline__ bool last_of_segment() const { return left == 1 || t == it.tiles - 1; }
+  __device__ __forceinline__ void next(const DenseParams& p) {
+    --left;
+    if (++t == it.tiles && left > 0) {
+      t = 0;
+      it = item_at(p, ++i);
+    }
+  }
+};
+
+// A ring position: slot and the parity of its current use.
+template <int N>
+struct Ring {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      parity ^= 1;
+    }
+  }
+};
+
+// Wait for a slot to be freed: passes at once on the ring's first round (an mbarrier that has completed no
+// phase yet reports the phase before its first as complete).
+// Once a wait has given up (ok false) a role runs its loop to the end without waiting, arriving or issuing, so
+// that the named barriers of the softmax warps stay matched.
+#define SMLA_WAIT(bar, par) \
+  if (ok) ok = ptx::mbar_wait_warp((bar), (par), &bars->abort, lane, p.wait_ns)
+
+// ----------------------------------------------------------------------------- copies
+
+__device__ __forceinline__ int page_entry(const DenseParams& p, const Item& it, int lp) {
+  return lp < p.max_pages && (long long)lp * kPageSize < it.max_len
+             ? __ldg(p.block_table + (size_t)it.req * p.max_pages + lp)
+             : -1;
+}
+
+template <int NR>
+__device__ void copy_role(const DenseParams& p, const CUtensorMap* map, const CUtensorMap* smap, uint32_t base,
+                          Bars* bars, int lane) {
+  using C = DC<NR>;
+  Walk w(p, bars);
+  Ring<C::kRing> k;
+  Ring<kScaleSlots> sc;
+  bool ok = true;
+  // block-table entries of 16 tiles per load, one lane each, the next 16 tiles' already in flight
+  int cur = 0, nxt = 0, base_lp = -1;
+  while (w.left > 0) {
+    const int lp = 2 * w.t;
+    if (base_lp < 0) {                                 // a new item
+      base_lp = lp;
+      cur = page_entry(p, w.it, base_lp + lane);
+      nxt = page_entry(p, w.it, base_lp + 32 + lane);
+      if (lane == 0) {
+        const int j0 = w.it.row0 / p.H, j1 = (w.it.row0 + w.it.nrows - 1) / p.H;
+        for (int j = j0; j <= j1; ++j)
+          if (__ldg(p.seq_lens + w.it.req * p.q_per_req + j) > (long long)p.max_pages * kPageSize)
+            atomicOr(p.err, SMLA_DEVERR_PAGE_RANGE);
+      }
+    } else if (lp == base_lp + 32) {
+      base_lp = lp;
+      cur = nxt;
+      nxt = page_entry(p, w.it, base_lp + 32 + lane);
+    }
+    const int pg[2] = {__shfl_sync(0xffffffffu, cur, lp - base_lp), __shfl_sync(0xffffffffu, cur, lp - base_lp + 1)};
+    int good = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool used = (long long)(lp + h) * kPageSize < w.it.max_len;
+      const bool in_cache = pg[h] >= 0 && (int64_t)pg[h] < p.num_pages;
+      if (used && in_cache) good |= 1 << h;
+      if (used && !in_cache && lane == 0) atomicOr(p.err, SMLA_DEVERR_PAGE_RANGE);
+    }
+    const uint32_t n_good = (good & 1) + (good >> 1);
+    SMLA_WAIT(&bars->scempty[sc.slot], sc.parity ^ 1);
+    if (ok && ptx::elect_one()) {
+      bars->pages_ok[sc.slot] = good;
+      ++bars->armed_sc[sc.slot];
+      ptx::mbar_arrive_expect_tx(&bars->scfull[sc.slot], n_good * 1024);
+      for (int h = 0; h < 2; ++h)
+        if (good >> h & 1)
+          ptx::tma_load_3d(base + C::kScale + sc.slot * 2048 + h * 1024, smap, kDLatent, 0, pg[h],
+                           &bars->scfull[sc.slot]);
+    }
+    __syncwarp();
+    sc.next();
+    for (int c = 0; c < kChunks; ++c) {
+      SMLA_WAIT(&bars->kempty[k.slot], k.parity ^ 1);
+      if (ok && ptx::elect_one()) {
+        ++bars->armed_k[k.slot];
+        ptx::mbar_arrive_expect_tx(&bars->kfull[k.slot], n_good * (kSlot / 2));
+        for (int h = 0; h < 2; ++h)
+          if (good >> h & 1)
+            ptx::tma_load_3d(base + C::kK + k.slot * kSlot + h * (kSlot / 2), map, c == 0 ? kDLatent + 16 : 128 * (c - 1),
+                             0, pg[h], &bars->kfull[k.slot]);
+      }
+      __syncwarp();
+      k.next();
+    }
+    const int was = w.i;
+    w.next(p);
+    if (w.i != was) base_lp = -1;
+  }
+}
+
+// After a wait that gave up: every copy that was armed has to land before the CTA leaves.  Nothing arms a slot
+// again by then, so the slot's last phase is waited for.
+__device__ void drain_copies(uint64_t* bar, const int* armed, int n, int lane) {
+  int never = 0;
+  for (int s = 0; s < n; ++s)
+    if (armed[s] > 0) ptx::mbar_wait_warp(&bar[s], (uint32_t)(armed[s] - 1) & 1u, &never, lane, 100000000ull);
+}
+
+// ----------------------------------------------------------------------------- MMA issue
+
+template <int NR>
+__device__ void qk_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars* bars, int lane) {
+  using C = DC<NR>;
+  constexpr uint32_t kIdescCodes = ptx::idesc_e4m3(128, 2 * NR), kIdescRope = ptx::idesc_bf16(128, NR);
+  Walk w(p, bars);
+  Ring<C::kRing> k;
+  Ring<C::kSBufs> s;
+  uint32_t qpar = 0;
+  bool ok = true, new_item = true;
+  const uint64_t dq = ptx::sw128_desc(base + C::kQ8, 16, 1024), dr = ptx::sw128_desc(base + C::kQr, 16, 1024);
+  while (w.left > 0) {
+    if (new_item) {
+      SMLA_WAIT(&bars->qfull, qpar);
+      qpar ^= 1;
+    }
+    for (int c = 0; c < kChunks; ++c) {
+      SMLA_WAIT(&bars->sempty[s.slot], s.parity ^ 1);
+      SMLA_WAIT(&bars->kfull[k.slot], k.parity);
+      ptx::tc_fence_after();
+      if (ok && ptx::elect_one()) {
+        const uint64_t dk = ptx::sw128_desc(base + C::kK + k.slot * kSlot, 16, 1024);
+        const uint32_t d = tmem + C::kSCol + 2 * NR * s.slot;
+        if (c == 0) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) ptx::mma_f16_ss(d, dk + 2 * kk, dr + 2 * kk, kIdescRope, kk > 0);
+        } else {
+          const uint64_t dqb = dq + (uint64_t)(((c - 1) * C::kQ8Chunk) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) ptx::mma_f8_ss(d, dk + 2 * kk, dqb + 2 * kk, kIdescCodes, kk > 0);
+        }
+        ptx::mma_commit(&bars->kempty[k.slot]);
+        ptx::mma_commit(&bars->sfull[s.slot]);
+      }
+      __syncwarp();
+      k.next();
+      s.next();
+    }
+    const int was = w.i;
+    w.next(p);
+    new_item = w.i != was;
+  }
+  if (ptx::elect_one()) ptx::mma_commit(&bars->drain[0]);
+  __syncwarp();
+}
+
+template <int NR>
+__device__ void pv_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars* bars, int lane) {
+  using C = DC<NR>;
+  constexpr uint32_t kIdesc = ptx::idesc_f16(128, NR, 1, 1);
+  Walk w(p, bars);
+  Ring<C::kVRing> v;
+  uint32_t ppar = 0;
+  bool ok = true, first = true;
+  const uint64_t dp = ptx::swz_desc(base + C::kP, 8 * C::kPRow, 8 * C::kPRow, C::kPRow);
+  while (w.left > 0) {
+    SMLA_WAIT(&bars->pfull, ppar);
+    ppar ^= 1;
+    for (int s = 0; s < kSlices; ++s) {
+      SMLA_WAIT(&bars->vfull[v.slot], v.parity);
+      ptx::tc_fence_after();
+      if (ok && ptx::elect_one()) {
+        const uint64_t dv = ptx::sw128_desc(base + C::kV + v.slot * kSlot, 2048, 1024);
+        const uint64_t dps = dp + (uint64_t)(s * C::kPRow);
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          ptx::mma_f16_ss(tmem + NR * b, dv + (uint64_t)(256 * b), dps, kIdesc, !(first && s == 0));
+        ptx::mma_commit(&bars->vempty[v.slot]);
+        if (s == kSlices - 1) ptx::mma_commit(&bars->pdone);
+      }
+      __syncwarp();
+      v.next();
+    }
+    first = w.last_of_segment();
+    w.next(p);
+  }
+  if (ptx::elect_one()) ptx::mma_commit(&bars->drain[1]);
+  __syncwarp();
+}
+
+// ----------------------------------------------------------------------------- conversion
+
+// 16 codes times a scale given as (mantissa, power of two) fp16 pairs -> 16 fp16 values.  The first product has
+// 4 + 11 bits and is rounded once; the second is exact above fp16's subnormals.
+__device__ __forceinline__ void convert16(uint4 codes, __half2 mant, __half2 pow2, uint4& lo, uint4& hi) {
+  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t h = e4m3x2_to_f16x2((uint16_t)(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xffffu));
+    const __half2 v = __hmul2(__hmul2(*reinterpret_cast<const __half2*>(&h), mant), pow2);
+    o[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  lo = make_uint4(o[0], o[1], o[2], o[3]);
+  hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// Whether one of 16 codes times the scale leaves fp16's range.
+__device__ __noinline__ bool beyond_fp16(uint4 codes, float scale) {
+  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+  bool over = false;
+  for (int i = 0; i < 8; ++i) {
+    const float2 c = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xffffu)));
+    over |= fabsf(c.x * scale) > 65504.f || fabsf(c.y * scale) > 65504.f;
+  }
+  return over;
+}
+
+// Values brought into fp16's range; a NaN becomes a number: the position's score is NaN already, so the rows
+// that see the position are NaN whatever its value, and the rows that do not (weight 0) stay clean.
+__device__ __forceinline__ uint4 into_range(uint4 v) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const __half2 top = __float2half2_rn(65504.f), bottom = __float2half2_rn(-65504.f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 c = __hmax2(__hmin2(*reinterpret_cast<const __half2*>(&w[i]), top), bottom);
+    w[i] = *reinterpret_cast<const uint32_t*>(&c);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Group g converts slices g, g + 2, g + 4, g + 6 of a tile: lane -> position (lane & 15) of the slice, 16-dim
+// unit 2 (warp % 4) + lane / 16 of every 128-dim block.  A warp reads its part of each code block into
+// registers as it lands (which frees the slot for the next tile's copy), then writes slice by slice.
+template <int NR>
+__device__ void convert_role(const DenseParams& p, unsigned char* sm, uint32_t base, Bars* bars, int warp, int lane) {
+  using C = DC<NR>;
+  const int group = (warp - kSoftWarps) >> 2;
+  const int tok = lane & 15, unit = 2 * (warp & 3) + (lane >> 4);
+  Walk w(p, bars);
+  Ring<C::kRing> k;
+  Ring<kScaleSlots> sc;
+  Ring<C::kVRing> v;
+  if (group) v.next();
+  bool ok = true, over = false;
+  while (w.left > 0) {
+    uint4 codes[4][4];
+    SMLA_WAIT(&bars->kfull[k.slot], k.parity);                     // the rope: nothing to read
+    if (ok && lane == 0) ptx::mbar_arrive(&bars->kempty[k.slot]);
+    k.next();
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      SMLA_WAIT(&bars->kfull[k.slot], k.parity);
+      const uint32_t slot = base + C::kK + k.slot * kSlot;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        codes[b][j] = ptx::lds128(slot + swz128((2 * j + group) * kSliceTokens + tok, unit));
+      __syncwarp();
+      if (ok && lane == 0) ptx::mbar_arrive(&bars->kempty[k.slot]);
+      k.next();
+    }
+    SMLA_WAIT(&bars->scfull[sc.slot], sc.parity);
+    const int pages = bars->pages_ok[sc.slot];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = (2 * j + group) * kSliceTokens + tok;
+      const long long t = (long long)w.t * kDenseTile + row;
+      const bool valid = t < w.it.max_len && (pages >> (row >> 6) & 1);
+      const float4 s4 = ptx::lds128f(base + C::kScale + sc.slot * 2048 + row * 16);
+      const float scale[4] = {s4.x, s4.y, s4.z, s4.w};
+      const float top = fmaxf(fmaxf(fabsf(s4.x), fabsf(s4.y)), fmaxf(fabsf(s4.z), fabsf(s4.w)));
+      const bool wide = valid && !(top <= 146.f && !isnan(s4.x + s4.y + s4.z + s4.w));   // 448 * 146 < 65504
+      const bool careful = wide || (valid && t >= w.it.min_len);
+      SMLA_WAIT(&bars->vempty[v.slot], v.parity ^ 1);
+      const uint32_t dst = base + C::kV + v.slot * kSlot;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+        if (valid) {
+          const int e = min(max((int)(__float_as_uint(scale[b]) >> 23 & 255u) - 127, -24), 15);
+          const __half2 mant = __float2half2_rn(scale[b] * __uint_as_float((uint32_t)(127 - e) << 23));
+          const __half2 pow2 = __float2half2_rn(__uint_as_float((uint32_t)(127 + e) << 23));
+          convert16(codes[b][j], mant, pow2, lo, hi);
+          if (careful) {
+            lo = into_range(lo);
+            hi = into_range(hi);
+            if (wide) over |= beyond_fp16(codes[b][j], scale[b]);
+          }
+        }
+        const uint32_t chunk = dst + (2 * b + (unit >> 2)) * 2048;
+        ptx::sts128_async_only(chunk + swz128(tok, (unit & 3) * 2), lo);
+        ptx::sts128_async_only(chunk + swz128(tok, (unit & 3) * 2 + 1), hi);
+      }
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (ok && lane == 0) ptx::mbar_arrive(&bars->vfull[v.slot]);
+      v.next();
+      v.next();
+    }
+    if (ok && lane == 0) ptx::mbar_arrive(&bars->scempty[sc.slot]);
+    sc.next();
+    w.next(p);
+  }
+  if (__any_sync(0xffffffffu, over) && lane == 0) atomicOr(p.err, SMLA_DEVERR_RANGE);
+}
+
+// ----------------------------------------------------------------------------- softmax
+
+// Reduce v[N] over the warp's lanes with op; lane i ends with the result of element i % N.
+template <int N, typename Op>
+__device__ __forceinline__ float reduce_scatter(float (&v)[N], int lane, Op op) {
+#pragma unroll
+  for (int h = N / 2; h >= 1; h >>= 1) {
+    const bool up = lane & h;
+#pragma unroll
+    for (int i = 0; i < h; ++i) {
+      const float send = up ? v[i] : v[i + h];
+      const float got = __shfl_xor_sync(0xffffffffu, send, h);
+      v[i] = op(up ? v[i + h] : v[i], got);
+    }
+  }
+  float r = v[0];
+#pragma unroll
+  for (int h = N; h < 32; h <<= 1) r = op(r, __shfl_xor_sync(0xffffffffu, r, h));
+  return r;
+}
+
+// Rows of one item into the Q operands: hi and lo E4M3 codes of each 128-dim block scaled by 2^-x, the rope as
+// it is; the factor 2^x sm_scale log2 e per (block, row) and each row's length go to buffer `buf`.
+template <int NR>
+__device__ void load_q(const DenseParams& p, const Item& it, unsigned char* sm, uint32_t base, int buf, int warp, int lane) {
+  using C = DC<NR>;
+  float* f = reinterpret_cast<float*>(sm + C::kF) + buf * 4 * NR;
+  int* lens = reinterpret_cast<int*>(sm + C::kLen) + buf * NR;
+  const float kf = p.sm_scale * kLog2e;
+  const uint16_t* q0 = p.q + ((size_t)it.req * p.q_per_req * p.H + it.row0) * kDQK;
+  const int b = lane >> 3, u = lane & 7;
+#pragma unroll 2
+  for (int r = warp; r < NR; r += kSoftWarps) {
+    uint4 raw[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)}, rope = raw[0];
+    if (r < it.nrows) {
+      const uint4* src = reinterpret_cast<const uint4*>(q0 + (size_t)r * kDQK);
+      raw[0] = __ldg(src + 2 * lane);
+      raw[1] = __ldg(src + 2 * lane + 1);
+      if (lane < 8) rope = __ldg(src + 64 + lane);
+    }
+    const uint32_t wds[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(wds[i] << 16)), fabsf(__uint_as_float(wds[i] & 0xffff0000u))));
+#pragma unroll
+    for (int o = 4; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    // x = floor(log2 amax) - 7, kept where 2^x and 2^-x are normal floats
+    const int x = amax > 0.f ? min(max((int)(__float_as_uint(amax) >> 23) - 127 - 7, -120), 120) : 0;
+    const float down = __uint_as_float((uint32_t)(127 - x) << 23);
+    uint32_t hi[4], lo[4];
+#pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 a = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)(w[i] & 0xffffu)));
-      const float2 c = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)(w[i] >> 16)));
-      v[4 * i] = a.x * scale;
-      v[4 * i + 1] = a.y * scale;
-      v[4 * i + 2] = c.x * scale;
-      v[4 * i + 3] = c.y * scale;
+      uint16_t h2[2], l2[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float a = __uint_as_float(wds[2 * i + j] << 16) * down, c = __uint_as_float(wds[2 * i + j] & 0xffff0000u) * down;
+        a = isinf(a) ? CUDART_NAN_F : a;                 // an infinite q makes the row NaN
+        c = isinf(c) ? CUDART_NAN_F : c;
+        h2[j] = f32x2_to_e4m3x2(a, c);
+        const float2 back = f16x2_to_f32x2(e4m3x2_to_f16x2(h2[j]));
+        l2[j] = f32x2_to_e4m3x2(a - back.x, c - back.y);
+      }
+      hi[i] = (uint32_t)h2[0] | ((uint32_t)h2[1] << 16);
+      lo[i] = (uint32_t)l2[0] | ((uint32_t)l2[1] << 16);
     }
-    bool over = false;
-    for (int i = 0; i < 16; ++i) {
-      over |= fabsf(v[i]) > 65504.f;
-      s = fmaf(ql[i], v[i], s);
+    const uint32_t q8 = base + C::kQ8 + b * C::kQ8Chunk;
+    ptx::sts128(q8 + swz128(r, u), make_uint4(hi[0], hi[1], hi[2], hi[3]));
+    ptx::sts128(q8 + swz128(NR + r, u), make_uint4(lo[0], lo[1], lo[2], lo[3]));
+    if (lane < 8) ptx::sts128(base + C::kQr + swz128(r, lane), rope);
+    if (u == 0) f[b * NR + r] = __uint_as_float((uint32_t)(127 + x) << 23) * kf;
+    if (lane == 0)
+      lens[r] = r < it.nrows ? clamped_len(p, it.req * p.q_per_req + (it.row0 + r) / p.H) : it.max_len;
+  }
+}
+
+template <int NR>
+__device__ __forceinline__ void tmem_ld(uint32_t a, uint32_t (&r)[NR]) {
+  if constexpr (NR == 32) ptx::tmem_ld32(a, r);
+  else if constexpr (NR == 16) ptx::tmem_ld16(a, r);
+  else ptx::tmem_ld8(a, r);
+}
+template <int NR>
+__device__ __forceinline__ void tmem_st(uint32_t a, const uint32_t (&r)[NR]) {
+  if constexpr (NR == 32) ptx::tmem_st32(a, r);
+  else if constexpr (NR == 16) ptx::tmem_st16(a, r);
+  else ptx::tmem_st8(a, r);
+}
+
+template <int NR>
+__device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t base, uint32_t tmem, Bars* bars, int warp,
+                             int lane, float* o_part, float* lse_part) {
+  using C = DC<NR>;
+  constexpr int HC = C::HC, LC = HC < 16 ? HC : 16;     // rows per thread, columns per TMEM load
+  const int half = warp >> 2, quad = warp & 3, col0 = half * HC;
+  const int tok = 32 * quad + lane;
+  const uint32_t lane_base = tmem + ((uint32_t)(32 * quad) << 16);
+  const float kf = p.sm_scale * kLog2e;
+  float* ref = reinterpret_cast<float*>(sm + C::kRef) + col0;
+  float* red = reinterpret_cast<float*>(sm + C::kRed) + col0;   // [4][NR]
+  Walk w(p, bars);
+  Ring<C::kSBufs> s;
+  Ring<kScaleSlots> sc;
+  uint32_t dpar = 0;
+  bool ok = true, first = true, begins = w.t == 0;
+  int buf = 0;
+  float l[HC];
+  if (w.left > 0) {
+    load_q<NR>(p, w.it, sm, base, 0, warp, lane);
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&bars->qfull);
+    ptx::named_bar_sync(3, kSoftWarps * 32);            // every row's factors and lengths are written
+  }
+  while (w.left > 0) {
+    if (first) {
+#pragma unroll
+      for (int i = 0; i < HC; ++i) l[i] = 0.f;
     }
-    if (over) atomicOr(p.err, SMLA_DEVERR_RANGE);
-    s = fmaf(qr[0], __uint_as_float(rope << 16), s);
-    s = fmaf(qr[1], __uint_as_float(rope & 0xFFFF0000u), s);
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    s *= p.sm_scale;
-    if (isnan(s)) m = s;                             // the row's result is NaN
-    const float mn = fmaxf(m, s), c = m == -CUDART_INF_F ? 0.f : expf(m - mn), e = expf(s - mn);
-    l = l * c + e;
-    for (int i = 0; i < 16; ++i) acc[i] = acc[i] * c + e * v[i];
-    if (!isnan(m)) m = mn;
+    // scores of this thread's position for its HC rows, in units of log2
+    SMLA_WAIT(&bars->scfull[sc.slot], sc.parity);
+    const float4 s4 = ptx::lds128f(base + C::kScale + sc.slot * 2048 + tok * 16);
+    const int pages = bars->pages_ok[sc.slot];
+    __syncwarp();
+    if (ok && lane == 0) ptx::mbar_arrive(&bars->scempty[sc.slot]);
+    sc.next();
+    float acc[HC];
+    const uint32_t fb = base + C::kF + (buf * 4 * NR + col0) * 4;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      SMLA_WAIT(&bars->sfull[s.slot], s.parity);
+      ptx::tc_fence_after();
+      const uint32_t a = lane_base + C::kSCol + 2 * NR * s.slot + col0;
+      const float scale = c == 1 ? s4.x : c == 2 ? s4.y : c == 3 ? s4.z : s4.w;
+#pragma unroll
+      for (int i0 = 0; i0 < HC; i0 += LC) {
+        uint32_t hi[LC];
+        tmem_ld<LC>(a + i0, hi);
+        if (c == 0) {
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < LC; ++i) acc[i0 + i] = __uint_as_float(hi[i]) * kf;
+        } else {
+          uint32_t lo[LC];
+          tmem_ld<LC>(a + NR + i0, lo);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < LC; i += 4) {
+            const float4 f = ptx::lds128f(fb + ((c - 1) * NR + i0 + i) * 4);
+            const float ff[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              acc[i0 + i + j] = fmaf(__uint_as_float(hi[i + j]) + __uint_as_float(lo[i + j]), scale * ff[j], acc[i0 + i + j]);
+          }
+        }
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (ok && lane == 0) ptx::mbar_arrive(&bars->sempty[s.slot]);
+      s.next();
+    }
+    // positions that a row may not see
+    const long long t = (long long)w.t * kDenseTile + tok;
+    if ((long long)(w.t + 1) * kDenseTile > w.it.min_len || pages != 3) {
+      const int* lens = reinterpret_cast<const int*>(sm + C::kLen) + buf * NR + col0;
+      const bool here = pages >> (tok >> 6) & 1;
+#pragma unroll
+      for (int i = 0; i < HC; ++i)
+        if (!here || t >= lens[i]) acc[i] = -CUDART_INF_F;
+    }
+    // the reference moves when a score lies more than kRefSlack above it
+    bool move = first;
+    if (!first) {
+#pragma unroll
+      for (int i = 0; i < HC; i += 4) {
+        const float4 r = ptx::lds128f(base + C::kRef + (col0 + i) * 4);
+        move |= acc[i] > r.x + kRefSlack || acc[i + 1] > r.y + kRefSlack || acc[i + 2] > r.z + kRefSlack ||
+                acc[i + 3] > r.w + kRefSlack;
+      }
+    }
+    move = ptx::named_bar_or(1 + half, 128, move);
+    if (!first) {                                       // P and O are free once the tile before is done
+      SMLA_WAIT(&bars->pdone, dpar);
+      dpar ^= 1;
+    }
+    if (move) {
+      float v[HC];
+#pragma unroll
+      for (int i = 0; i < HC; ++i) v[i] = acc[i];
+      const float m = reduce_scatter<HC>(v, lane, [](float a, float b) { return fmaxf(a, b); });
+      if (lane < HC) red[quad * NR + lane] = m;
+      ptx::named_bar_sync(1 + half, 128);
+      float factor = 1.f, now = kNoRef;
+      if (lane < HC) {
+        const float top = fmaxf(fmaxf(red[lane], red[NR + lane]), fmaxf(red[2 * NR + lane], red[3 * NR + lane]));
+        const float old = first ? kNoRef : ref[lane];
+        now = top > old + kRefSlack ? top - kRefBelowMax : old;
+        factor = ptx::ex2_approx(old - now);
+      }
+      ptx::named_bar_sync(1 + half, 128);
+      if (quad == 0 && lane < HC) ref[lane] = now;
+      ptx::named_bar_sync(1 + half, 128);
+      if (!first) {
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < HC; ++i) l[i] *= __shfl_sync(0xffffffffu, factor, i);
+#pragma unroll 1
+        for (int b = 0; b < 4; ++b) {
+#pragma unroll
+          for (int i0 = 0; i0 < HC; i0 += LC) {
+            uint32_t o[LC];
+            tmem_ld<LC>(lane_base + NR * b + col0 + i0, o);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < LC; ++i)
+              o[i] = __float_as_uint(__uint_as_float(o[i]) * __shfl_sync(0xffffffffu, factor, i0 + i));
+            tmem_st<LC>(lane_base + NR * b + col0 + i0, o);
+          }
+        }
+        ptx::tmem_wait_st();
+      }
+    }
+    // weights
+#pragma unroll
+    for (int i = 0; i < HC; i += 8) {
+      const float4 r0 = ptx::lds128f(base + C::kRef + (col0 + i) * 4), r1 = ptx::lds128f(base + C::kRef + (col0 + i + 4) * 4);
+      const float r[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+      uint32_t h[4];
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        const float a = ptx::ex2_approx(acc[i + j] - r[j]), c = ptx::ex2_approx(acc[i + j + 1] - r[j + 1]);
+        l[i + j] += a;
+        l[i + j + 1] += c;
+        const __half2 hh = __floats2half2_rn(a, c);
+        h[j >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
+      }
+      ptx::sts128_async_only(base + C::kP + swz_row<C::kPRow>(tok, (col0 + i) >> 3), make_uint4(h[0], h[1], h[2], h[3]));
+    }
+    ptx::fence_proxy_async_smem();
+    ptx::tc_fence_before();
+    __syncwarp();
+    if (ok && lane == 0) ptx::mbar_arrive(&bars->pfull);
+
+    const bool last = w.last_of_segment(), ends = w.t == w.it.tiles - 1;
+    const Item it = w.it;
+    w.next(p);
+    first = last;
+    if (!last) continue;
+
+    // the next item's rows, so that its scores can start beside this one's last PV
+    if (w.left > 0) {
+      load_q<NR>(p, w.it, sm, base, buf ^ 1, warp, lane);
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (ok && lane == 0) ptx::mbar_arrive(&bars->qfull);
+    }
+    // row sums over the tile's 128 positions
+    const float sum = reduce_scatter<HC>(l, lane, [](float a, float b) { return a + b; });
+    if (lane < HC) red[quad * NR + lane] = sum;
+    SMLA_WAIT(&bars->pdone, dpar);
+    dpar ^= 1;
+    ptx::tc_fence_after();
+    ptx::named_bar_sync(3, kSoftWarps * 32);
+    const bool whole = begins && ends;
+    // a run's first segment that continues an item goes to slot 0 of the CTA, its last segment to slot 1
+    const size_t slot = 2 * (size_t)blockIdx.x + (begins ? 1 : 0);
+    float inv = 0.f;
+    if (lane < HC) {
+      const float z = red[lane] + red[NR + lane] + red[2 * NR + lane] + red[3 * NR + lane];
+      inv = z > 0.f ? 1.f / z : (z == 0.f ? 0.f : CUDART_NAN_F);
+      const float lse = z == 0.f ? -CUDART_INF_F : (ref[lane] + log2f(z)) * kLn2;
+      if (quad == 0 && ok && col0 + lane < it.nrows) {
+        if (whole) p.lse[(size_t)it.req * p.q_per_req * p.H + it.row0 + col0 + lane] = lse;
+        else lse_part[slot * NR + col0 + lane] = lse;
+      }
+    }
+#pragma unroll 1
+    for (int b = 0; b < 4; ++b) {
+      const int dim = 128 * b + tok;
+#pragma unroll
+      for (int i0 = 0; i0 < HC; i0 += LC) {
+        uint32_t o[LC];
+        tmem_ld<LC>(lane_base + NR * b + col0 + i0, o);
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < LC; i += 2) {
+          // lanes 2j, 2j + 1 hold dims d, d + 1: the even one ends with both dims of the first row, the odd
+          // one with both of the second
+          const float va = __uint_as_float(o[i]) * __shfl_sync(0xffffffffu, inv, i0 + i);
+          const float vb = __uint_as_float(o[i + 1]) * __shfl_sync(0xffffffffu, inv, i0 + i + 1);
+          const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? va : vb, 1);
+          const int c = col0 + i0 + i + (lane & 1);
+          const float d0 = lane & 1 ? got : va, d1 = lane & 1 ? vb : got;
+          if (ok && c < it.nrows) {
+            if (whole) {
+              uint16_t* o16 = p.out + ((size_t)it.req * p.q_per_req * p.H + it.row0 + c) * kDLatent;
+              *reinterpret_cast<uint32_t*>(o16 + (dim & ~1)) = f32x2_to_bf16x2(d0, d1);
+            } else {
+              *reinterpret_cast<float2*>(o_part + (slot * NR + c) * kDLatent + (dim & ~1)) = make_float2(d0, d1);
+            }
+          }
+        }
+      }
+    }
+    ptx::tc_fence_before();
+    ptx::named_bar_sync(3, kSoftWarps * 32);             // red, ref and TMEM are free; the next factors are written
+    begins = true;
+    buf ^= 1;
   }
-  __shared__ float sm[kWarps], sl[kWarps], so[kWarps][kDLatent];
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
-  for (int i = 0; i < 16; ++i) so[warp][16 * lane + i] = acc[i];
+}
+
+// ----------------------------------------------------------------------------- kernel
+
+// This CTA's run of tiles: every CTA adds up the tiles of all items (a run of items per thread, then a scan of
+// the threads' sums).
+__device__ void find_run(const DenseParams& p, unsigned char* scratch, Bars* bars, RunDesc* desc) {
+  long long* sums = reinterpret_cast<long long*>(scratch);
+  const int n = p.requests * p.groups, per = (n + kDenseThreads - 1) / kDenseThreads;
+  const int i0 = min(n, (int)threadIdx.x * per), i1 = min(n, i0 + per);
+  long long mine = 0;
+  for (int i = i0; i < i1; ++i) mine += item_at(p, i).tiles;
+  sums[threadIdx.x] = mine;
   __syncthreads();
-  float mx = -CUDART_INF_F, z = 0.f;
-  for (int w = 0; w < kWarps; ++w) mx = isnan(sm[w]) || isnan(mx) ? CUDART_NAN_F : fmaxf(mx, sm[w]);
-  for (int w = 0; w < kWarps; ++w) z += sm[w] == -CUDART_INF_F ? 0.f : sl[w] * expf(sm[w] - mx);
-  const float inv = z > 0.f ? 1.f / z : (z == 0.f ? 0.f : CUDART_NAN_F);
-  for (int d = 2 * threadIdx.x; d < kDLatent; d += 2 * 32 * kWarps) {
-    float o0 = 0.f, o1 = 0.f;
-    for (int w = 0; w < kWarps; ++w) {
-      const float c = sm[w] == -CUDART_INF_F ? 0.f : expf(sm[w] - mx);
-      o0 += c * so[w][d];
-      o1 += c * so[w][d + 1];
+  if (threadIdx.x < 32) {                                // exclusive prefix over 19 sums per lane
+    long long v[19], part = 0;
+#pragma unroll
+    for (int j = 0; j < 19; ++j) {
+      v[j] = part;
+      part += sums[19 * threadIdx.x + j];
     }
-    reinterpret_cast<uint32_t*>(p.out + (size_t)row * kDLatent)[d / 2] = f32x2_to_bf16x2(o0 * inv, o1 * inv);
+    long long before = part;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long up = __shfl_up_sync(0xffffffffu, before, o);
+      if ((int)threadIdx.x >= o) before += up;
+    }
+    if (threadIdx.x == 31) bars->total = before;
+    before -= part;
+#pragma unroll
+    for (int j = 0; j < 19; ++j) sums[19 * threadIdx.x + j] = before + v[j];
   }
-  if (threadIdx.x == 0) p.lse[row] = z == 0.f ? -CUDART_INF_F : mx + logf(z);
+  __syncthreads();
+  const long long T = bars->total;
+  const int active = (int)min((long long)p.ctas, T);     // CTAs with at least one tile
+  const int c = blockIdx.x;
+  const long long a = c < active ? run_start(T, active, c) : T, e = c < active ? run_start(T, active, c + 1) : T;
+  if (threadIdx.x == 0) bars->my_tiles = (int)(e - a);
+  if (threadIdx.x == 0 && a == e) *desc = RunDesc{T, 0, 0, -1, 0};
+  const long long at = sums[threadIdx.x];
+  if (a < e && mine > 0) {
+    if (a >= at && a < at + mine) {                      // the run begins in this thread's items
+      long long x = at;
+      for (int i = i0; i < i1; ++i) {
+        const int tiles = item_at(p, i).tiles;
+        if (a < x + tiles) {
+          bars->first_item = i;
+          bars->first_tile = (int)(a - x);
+          break;
+        }
+        x += tiles;
+      }
+    }
+    if (e - 1 >= at && e - 1 < at + mine) {              // and ends in these
+      long long x = at;
+      for (int i = i0; i < i1; ++i) {
+        const int tiles = item_at(p, i).tiles;
+        if (e - 1 < x + tiles) {
+          *desc = RunDesc{T, x, x + tiles, i, 0};
+          break;
+        }
+        x += tiles;
+      }
+    }
+  }
+  __syncthreads();
+}
+
+template <int NR>
+__global__ void __launch_bounds__(kDenseThreads, 1)
+    dense_kernel(const DenseParams p, const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap smap,
+                 RunDesc* descs, float* lse_part, float* o_part) {
+  using C = DC<NR>;
+  extern __shared__ __align__(1024) unsigned char sm[];
+  const uint32_t base = ptx::smem_u32(sm);
+  Bars* bars = reinterpret_cast<Bars*>(sm + C::kBar);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  ptx::griddep_wait();                                   // the call before may still be merging from the workspace
+  if (threadIdx.x == 0) ptx::griddep_launch_dependents();
+  if (threadIdx.x == 0) {
+    ptx::prefetch_tensormap(&map);
+    ptx::prefetch_tensormap(&smap);
+    for (int i = 0; i < 8; ++i) {
+      ptx::mbar_init(&bars->kfull[i], 1);
+      ptx::mbar_init(&bars->kempty[i], 1 + kConvWarps);
+    }
+    for (int i = 0; i < 4; ++i) {
+      ptx::mbar_init(&bars->vfull[i], 4);
+      ptx::mbar_init(&bars->vempty[i], 1);
+      ptx::mbar_init(&bars->scfull[i], 1);
+      ptx::mbar_init(&bars->scempty[i], kSoftWarps + kConvWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&bars->sfull[i], 1);
+      ptx::mbar_init(&bars->sempty[i], kSoftWarps);
+      ptx::mbar_init(&bars->drain[i], 1);
+    }
+    ptx::mbar_init(&bars->pfull, kSoftWarps);
+    ptx::mbar_init(&bars->pdone, 1);
+    ptx::mbar_init(&bars->qfull, kSoftWarps);
+    bars->abort = 0;
+    for (int i = 0; i < 8; ++i) bars->armed_k[i] = 0;
+    for (int i = 0; i < 4; ++i) bars->armed_sc[i] = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == kQkWarp) {
+    ptx::tmem_alloc(&bars->tmem, C::kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  find_run(p, sm, bars, descs + blockIdx.x);             // the scratch is overwritten by the pipeline afterwards
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = bars->tmem;
+
+  if (warp < kSoftWarps) softmax_role<NR>(p, sm, base, tmem, bars, warp, lane, o_part, lse_part);
+  else if (warp < kSoftWarps + kConvWarps) convert_role<NR>(p, sm, base, bars, warp, lane);
+  else if (warp == kCopyWarp) copy_role<NR>(p, &map, &smap, base, bars, lane);
+  else if (warp == kQkWarp) qk_role<NR>(p, base, tmem, bars, lane);
+  else if (warp == kPvWarp) pv_role<NR>(p, base, tmem, bars, lane);
+
+  // nothing of this CTA's may be in flight when it leaves: the MMAs (their last commits) and, after a wait
+  // that gave up, the copies
+  __syncthreads();
+  int never = 0;
+  if (warp == kCopyWarp && bars->abort) {
+    drain_copies(bars->kfull, bars->armed_k, C::kRing, lane);
+    drain_copies(bars->scfull, bars->armed_sc, kScaleSlots, lane);
+  }
+  if (warp == kQkWarp) {
+    ptx::mbar_wait_warp(&bars->drain[0], 0, &never, lane, 100000000ull);
+    ptx::mbar_wait_warp(&bars->drain[1], 0, &never, lane, 100000000ull);
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, C::kTmemCols);
+  }
+  if (threadIdx.x == 0 && bars->abort) atomicOr(p.err, SMLA_DEVERR_TIMEOUT);
+}
+
+// ----------------------------------------------------------------------------- merge
+
+constexpr int kMergeThreads = 128;        // 4 output dims per thread
+constexpr int kMergeBatch = 8;            // partial rows in flight per thread
+
+// Joins the partials of the items that cross CTA runs: lse = ln sum_s exp(lse_s), out = sum_s exp(lse_s - lse)
+// o_s.  An item that begins in CTA c and ends in CTA c1 left its partials in slot 1 of c and slot 0 of
+// c + 1 .. c1.  Every CTA lists those items from the run descriptors and takes rows of them in turn.
+__global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const DenseParams p, const RunDesc* descs,
+                                                                    const float* lse_part, const float* o_part) {
+  __shared__ int list_s[kDenseMaxCtas];
+  __shared__ float w_s[kDenseMaxCtas];
+  __shared__ int n_s;
+  __shared__ float lse_s;
+  const int tid = threadIdx.x, lane = tid & 31;
+  ptx::griddep_wait();
+  const long long T = descs[0].total;
+  const int active = (int)min((long long)p.ctas, T);
+  for (int c = tid; c < active; c += kMergeThreads) {
+    const long long begin = descs[c].item_begin, end = descs[c].item_end;
+    list_s[c] = begin >= run_start(T, active, c) && end > run_start(T, active, c + 1);
+  }
+  __syncthreads();
+  if (tid < 32) {                                        // the flagged CTAs in order, the same list in every CTA
+    int n = 0;
+    for (int c0 = 0; c0 < active; c0 += 32) {
+      const bool mine = c0 + lane < active && list_s[c0 + lane];
+      const uint32_t votes = __ballot_sync(0xffffffffu, mine);
+      __syncwarp();
+      if (mine) list_s[n + __popc(votes & ((1u << lane) - 1))] = c0 + lane;   // at most c0 + lane: already read
+      n += __popc(votes);
+      __syncwarp();
+    }
+    if (lane == 0) n_s = n;
+  }
+  __syncthreads();
+  const int nr = p.nr, work = n_s * nr;
+  for (int idx = blockIdx.x; idx < work; idx += gridDim.x) {
+    const int c = list_s[idx / nr], row = idx % nr;
+    const RunDesc d = descs[c];
+    const Item it = item_at(p, d.item);
+    if (row >= it.nrows) continue;                       // uniform over the CTA
+    int c1 = (int)((d.item_end * active + T - 1) / T);   // first CTA past the item, give or take one
+    while (c1 > c && run_start(T, active, c1) >= d.item_end) --c1;
+    while (c1 + 1 < active && run_start(T, active, c1 + 1) < d.item_end) ++c1;
+    const int parts = c1 - c + 1;
+    auto slot = [&](int s) { return s == 0 ? 2 * (size_t)c + 1 : 2 * (size_t)(c + s); };
+    const float4* rows = reinterpret_cast<const float4*>(o_part) + tid;
+    auto at = [&](int s) { return (slot(s) * nr + row) * (kDLatent / 4); };
+    float4 v[kMergeBatch];
+#pragma unroll
+    for (int s = 0; s < kMergeBatch; ++s) v[s] = s < parts ? __ldg(rows + at(s)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    __syncthreads();                                     // w_s of the row before has been read
+    if (tid < 32) {
+      float m = -CUDART_INF_F;
+      bool bad = false;
+      for (int s = lane; s < parts; s += 32) {
+        const float x = __ldg(lse_part + slot(s) * nr + row);
+        bad |= isnan(x);
+        m = fmaxf(m, x);
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (__any_sync(0xffffffffu, bad)) m = CUDART_NAN_F;
+      float z = 0.f;
+      for (int s = lane; s < parts; s += 32) {
+        const float e = m == -CUDART_INF_F ? 0.f : expf(__ldg(lse_part + slot(s) * nr + row) - m);
+        w_s[s] = e;
+        z += e;
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+      const float inv = z == 0.f ? 0.f : 1.f / z;
+      __syncwarp();
+      for (int s = lane; s < parts; s += 32) w_s[s] *= inv;
+      if (lane == 0) lse_s = z == 0.f ? -CUDART_INF_F : m + logf(z);
+    }
+    __syncthreads();
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < parts; s0 += kMergeBatch) {
+      if (s0 > 0) {
+#pragma unroll
+        for (int s = 0; s < kMergeBatch; ++s)
+          v[s] = s0 + s < parts ? __ldg(rows + at(s0 + s)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int s = 0; s < kMergeBatch; ++s) {
+        if (s0 + s >= parts) break;
+        const float w = w_s[s0 + s];
+        acc.x = fmaf(w, v[s].x, acc.x);
+        acc.y = fmaf(w, v[s].y, acc.y);
+        acc.z = fmaf(w, v[s].z, acc.z);
+        acc.w = fmaf(w, v[s].w, acc.w);
+      }
+    }
+    const size_t out_row = (size_t)it.req * p.q_per_req * p.H + it.row0 + row;
+    reinterpret_cast<uint2*>(p.out + out_row * kDLatent)[tid] =
+        make_uint2(f32x2_to_bf16x2(acc.x, acc.y), f32x2_to_bf16x2(acc.z, acc.w));
+    if (tid == 0) p.lse[out_row] = lse_s;
+  }
+}
+
+// ----------------------------------------------------------------------------- host
+
+// Workspace: header (error word), run descriptors, lse partials [2 ctas][NR], row partials [2 ctas][NR][512].
+constexpr size_t kDescBytes = (kDenseMaxCtas * sizeof(RunDesc) + 255) / 256 * 256;
+size_t lse_part_bytes(int ctas, int nr) { return ((size_t)2 * ctas * nr * sizeof(float) + 255) / 256 * 256; }
+
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encoder() {
+  static const EncodeTiled fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeTiled>(f);
+  }();
+  return fn;
+}
+
+// The cache as [page][record][byte], in boxes of 64 records of one page, `bytes` wide.
+bool encode_map(CUtensorMap* map, const DenseParams& p, uint32_t bytes, CUtensorMapSwizzle swizzle) {
+  const cuuint64_t dims[3] = {kRecordBytes, kPageSize, (cuuint64_t)p.num_pages};
+  const cuuint64_t strides[2] = {kRecordBytes, (cuuint64_t)kRecordBytes * kPageSize};
+  const cuuint32_t box[3] = {bytes, kPageSize, 1}, step[3] = {1, 1, 1};
+  return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(p.kv), dims, strides, box, step,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NR>
+cudaError_t launch_nr(const DenseParams& p, unsigned char* ws, cudaStream_t stream) {
+  CUtensorMap map, smap;
+  if (!encoder() || !encode_map(&map, p, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_map(&smap, p, 16, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return cudaErrorNotSupported;
+  // the shared-memory attribute belongs to the device's copy of the kernel: set once per device
+  static std::atomic<bool> set[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !set[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(dense_kernel<NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, DC<NR>::kBytes);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) set[dev].store(true, std::memory_order_relaxed);
+  }
+  RunDesc* descs = reinterpret_cast<RunDesc*>(ws + kWorkspaceHeader);
+  float* lse_part = reinterpret_cast<float*>(ws + kWorkspaceHeader + kDescBytes);
+  float* o_part = reinterpret_cast<float*>(ws + kWorkspaceHeader + kDescBytes + lse_part_bytes(p.ctas, NR));
+  dense_kernel<NR><<<p.ctas, kDenseThreads, DC<NR>::kBytes, stream>>>(p, map, smap, descs, lse_part, o_part);
+  e = cudaGetLastError();
+  // a table of at most two pages gives every item one tile: nothing to merge
+  if (e != cudaSuccess || p.max_pages <= 2) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(8 * p.ctas);
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, dense_merge_kernel, p, (const RunDesc*)descs, (const float*)lse_part,
+                            (const float*)o_part);
 }
 
 }  // namespace
 
 cudaError_t launch_dense(const DenseParams& p, cudaStream_t stream) {
-  dense_kernel<<<p.B * p.H, 32 * kWarps, 0, stream>>>(p);
-  return cudaGetLastError();
+  unsigned char* ws = reinterpret_cast<unsigned char*>(p.err);    // the workspace begins with the error word
+  if (p.nr == 16) return launch_nr<16>(p, ws, stream);
+  if (p.nr == 32) return launch_nr<32>(p, ws, stream);
+  return launch_nr<64>(p, ws, stream);
 }
 
 }  // namespace smla
@@ -113,6 +1098,10 @@ extern "C" int sparse_mla_dense_plan_for(const smla_dense_dims* d, int32_t sm_co
   plan->row_groups = (int32_t)((rows + plan->rows_per_cta - 1) / plan->rows_per_cta);
   plan->ctas = d->ctas > 0 ? d->ctas : (sm_count < kDenseMaxCtas ? sm_count : kDenseMaxCtas);
   plan->reserved = 0;
-  plan->workspace_bytes = kWorkspaceHeader;
+  // a CTA counts its tiles in 32 bits
+  const int64_t most = d->batch / sq * (int64_t)plan->row_groups * ((d->max_pages_per_seq + (int64_t)1) / 2);
+  if (most / plan->ctas >= 0x7fffffff) return SMLA_ERR_UNSUPPORTED;
+  plan->workspace_bytes = kWorkspaceHeader + kDescBytes + lse_part_bytes(plan->ctas, plan->rows_per_cta) +
+                          (size_t)2 * plan->ctas * plan->rows_per_cta * kDLatent * sizeof(float);
   return SMLA_OK;
 }
