@@ -47,7 +47,8 @@ constexpr float kRefSlack = 15.f;         // a score this far above the referenc
 // four), then one warp each for the copies, the QK and the PV.
 constexpr int kSoftWarps = 8, kConvWarps = 8;
 constexpr int kCopyWarp = 16, kQkWarp = 17, kPvWarp = 18;
-constexpr int kDenseThreads = 19 * 32;
+constexpr int kDenseThreads = 20 * 32;     // five warpgroups; the last warp is idle
+constexpr int kSoftRegs = 128, kMiscRegs = 32;   // of 96 at launch: 2 x 128 + 2 x 96 + 32 = 5 x 96
 
 constexpr uint32_t kSlot = 16384;         // 128 positions x 128 bytes: one code block or the rope of a tile
 constexpr int kChunks = 5;                // rope, then the four code blocks
@@ -170,7 +171,7 @@ struct Ring {
 // Once a wait has given up (ok false) a role runs its loop to the end without waiting, arriving or issuing, so
 // that the named barriers of the softmax warps stay matched.
 #define SMLA_WAIT(bar, par) \
-  if (ok) ok = ptx::mbar_wait_warp((bar), (par), &bars->abort, lane, p.wait_ns)
+  if (ok) ok = ptx::mbar_wait_warp_small((bar), (par), &bars->abort, p.wait_ns)
 
 // ----------------------------------------------------------------------------- copies
 
@@ -229,6 +230,7 @@ __device__ void copy_role(const DenseParams& p, const CUtensorMap* map, const CU
     }
     __syncwarp();
     sc.next();
+#pragma unroll 1
     for (int c = 0; c < kChunks; ++c) {
       SMLA_WAIT(&bars->kempty[k.slot], k.parity ^ 1);
       if (ok && ptx::elect_one()) {
@@ -273,6 +275,7 @@ __device__ void qk_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars
       SMLA_WAIT(&bars->qfull, qpar);
       qpar ^= 1;
     }
+#pragma unroll 1
     for (int c = 0; c < kChunks; ++c) {
       SMLA_WAIT(&bars->sempty[s.slot], s.parity ^ 1);
       SMLA_WAIT(&bars->kfull[k.slot], k.parity);
@@ -315,6 +318,7 @@ __device__ void pv_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars
   while (w.left > 0) {
     SMLA_WAIT(&bars->pfull, ppar);
     ppar ^= 1;
+#pragma unroll 1
     for (int s = 0; s < kSlices; ++s) {
       SMLA_WAIT(&bars->vfull[v.slot], v.parity);
       ptx::tc_fence_after();
@@ -339,50 +343,49 @@ __device__ void pv_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars
 
 // ----------------------------------------------------------------------------- conversion
 
-// 16 codes times a scale given as (mantissa, power of two) fp16 pairs -> 16 fp16 values.  The first product has
-// 4 + 11 bits and is rounded once; the second is exact above fp16's subnormals.
-__device__ __forceinline__ void convert16(uint4 codes, __half2 mant, __half2 pow2, uint4& lo, uint4& hi) {
-  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-  uint32_t o[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t h = e4m3x2_to_f16x2((uint16_t)(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xffffu));
-    const __half2 v = __hmul2(__hmul2(*reinterpret_cast<const __half2*>(&h), mant), pow2);
-    o[i] = *reinterpret_cast<const uint32_t*>(&v);
-  }
-  lo = make_uint4(o[0], o[1], o[2], o[3]);
-  hi = make_uint4(o[4], o[5], o[6], o[7]);
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, __half2 b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), b);
+  return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// Whether one of 16 codes times the scale leaves fp16's range.
-__device__ __noinline__ bool beyond_fp16(uint4 codes, float scale) {
+// 16 codes of one 128-dim block as fp16 values: code 2^-8 times scale 2^8, rounded once.
+//
+// A code's bits, shifted to where fp16 has its sign, the low four exponent bits and the top of the fraction, read
+// as 2^-8 of its value, subnormals included; a NaN code reads as 480 (the position's score is NaN already, so
+// the rows that see it are NaN whatever its value, and the rows that do not stay clean).  One word of four codes
+// gives the pairs of dims 0, 2 and 1, 3.  scale 2^8 has fp16's full precision for scales from 2^-22 (latents up
+// to 1e-4) to 255; below, the absolute error stays that of fp16's subnormals.
+__device__ __forceinline__ void convert16(uint4 codes, float scale, uint32_t (&o)[8]) {
   const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-  bool over = false;
-  for (int i = 0; i < 8; ++i) {
-    const float2 c = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xffffu)));
-    over |= fabsf(c.x * scale) > 65504.f || fabsf(c.y * scale) > 65504.f;
-  }
-  return over;
-}
-
-// Values brought into fp16's range; a NaN becomes a number: the position's score is NaN already, so the rows
-// that see the position are NaN whatever its value, and the rows that do not (weight 0) stay clean.
-__device__ __forceinline__ uint4 into_range(uint4 v) {
-  uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  const __half2 top = __float2half2_rn(65504.f), bottom = __float2half2_rn(-65504.f);
+  const __half2 s = __float2half2_rn(scale * 256.f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __half2 c = __hmax2(__hmin2(*reinterpret_cast<const __half2*>(&w[i]), top), bottom);
-    w[i] = *reinterpret_cast<const uint32_t*>(&c);
+    o[2 * i] = hmul2(((w[i] << 8) & 0x80008000u) | ((w[i] << 7) & 0x3f803f80u), s);
+    o[2 * i + 1] = hmul2((w[i] & 0x80008000u) | ((w[i] >> 1) & 0x3f803f80u), s);
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The rest of a scale above 146 (a block that may leave fp16's range): times a power of two, saturating; true
+// if a value left the range.
+__device__ __forceinline__ bool scale_up(uint32_t (&o)[8], int e) {
+  const __half2 up = __float2half2_rn(__uint_as_float((uint32_t)(127 + e) << 23));
+  const __half2 top = __float2half2_rn(65504.f), bottom = __float2half2_rn(-65504.f);
+  bool over = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t v = hmul2(o[i], up);
+    const __half2 c = __hmax2(__hmin2(*reinterpret_cast<const __half2*>(&v), top), bottom);
+    o[i] = *reinterpret_cast<const uint32_t*>(&c);
+    over |= o[i] != v;
+  }
+  return over;
 }
 
 // Group g converts slices g, g + 2, g + 4, g + 6 of a tile: lane -> position (lane & 15) of the slice, 16-dim
 // unit 2 (warp % 4) + lane / 16 of every 128-dim block.  A warp reads its part of each code block into
 // registers as it lands (which frees the slot for the next tile's copy), then writes slice by slice.
 template <int NR>
-__device__ void convert_role(const DenseParams& p, unsigned char* sm, uint32_t base, Bars* bars, int warp, int lane) {
+__device__ void convert_role(const DenseParams& p, uint32_t base, Bars* bars, int warp, int lane) {
   using C = DC<NR>;
   const int group = (warp - kSoftWarps) >> 2;
   const int tok = lane & 15, unit = 2 * (warp & 3) + (lane >> 4);
@@ -416,29 +419,26 @@ __device__ void convert_role(const DenseParams& p, unsigned char* sm, uint32_t b
       const long long t = (long long)w.t * kDenseTile + row;
       const bool valid = t < w.it.max_len && (pages >> (row >> 6) & 1);
       const float4 s4 = ptx::lds128f(base + C::kScale + sc.slot * 2048 + row * 16);
-      const float scale[4] = {s4.x, s4.y, s4.z, s4.w};
+      float scale[4] = {s4.x, s4.y, s4.z, s4.w};
       const float top = fmaxf(fmaxf(fabsf(s4.x), fabsf(s4.y)), fmaxf(fabsf(s4.z), fabsf(s4.w)));
       const bool wide = valid && !(top <= 146.f && !isnan(s4.x + s4.y + s4.z + s4.w));   // 448 * 146 < 65504
-      const bool careful = wide || (valid && t >= w.it.min_len);
+      int e = 0;
+      if (__builtin_expect(wide, 0)) {                 // the largest scale's exponent comes off before fp16
+        e = min(max((int)(__float_as_uint(top) >> 23) - 127, 0), 15);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) scale[b] *= __uint_as_float((uint32_t)(127 - e) << 23);
+      }
+      if (!valid) scale[0] = scale[1] = scale[2] = scale[3] = 0.f;
       SMLA_WAIT(&bars->vempty[v.slot], v.parity ^ 1);
       const uint32_t dst = base + C::kV + v.slot * kSlot;
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-        if (valid) {
-          const int e = min(max((int)(__float_as_uint(scale[b]) >> 23 & 255u) - 127, -24), 15);
-          const __half2 mant = __float2half2_rn(scale[b] * __uint_as_float((uint32_t)(127 - e) << 23));
-          const __half2 pow2 = __float2half2_rn(__uint_as_float((uint32_t)(127 + e) << 23));
-          convert16(codes[b][j], mant, pow2, lo, hi);
-          if (careful) {
-            lo = into_range(lo);
-            hi = into_range(hi);
-            if (wide) over |= beyond_fp16(codes[b][j], scale[b]);
-          }
-        }
+        uint32_t o[8];
+        convert16(codes[b][j], scale[b], o);
+        if (__builtin_expect(wide, 0)) over |= scale_up(o, e);
         const uint32_t chunk = dst + (2 * b + (unit >> 2)) * 2048;
-        ptx::sts128_async_only(chunk + swz128(tok, (unit & 3) * 2), lo);
-        ptx::sts128_async_only(chunk + swz128(tok, (unit & 3) * 2 + 1), hi);
+        ptx::sts128_async_only(chunk + swz128(tok, (unit & 3) * 2), make_uint4(o[0], o[1], o[2], o[3]));
+        ptx::sts128_async_only(chunk + swz128(tok, (unit & 3) * 2 + 1), make_uint4(o[4], o[5], o[6], o[7]));
       }
       ptx::fence_proxy_async_smem();
       __syncwarp();
@@ -484,7 +484,7 @@ __device__ void load_q(const DenseParams& p, const Item& it, unsigned char* sm, 
   const float kf = p.sm_scale * kLog2e;
   const uint16_t* q0 = p.q + ((size_t)it.req * p.q_per_req * p.H + it.row0) * kDQK;
   const int b = lane >> 3, u = lane & 7;
-#pragma unroll 2
+#pragma unroll 1
   for (int r = warp; r < NR; r += kSoftWarps) {
     uint4 raw[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)}, rope = raw[0];
     if (r < it.nrows) {
@@ -574,41 +574,50 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
     }
     // scores of this thread's position for its HC rows, in units of log2
     SMLA_WAIT(&bars->scfull[sc.slot], sc.parity);
-    const float4 s4 = ptx::lds128f(base + C::kScale + sc.slot * 2048 + tok * 16);
+    float4 s4 = ptx::lds128f(base + C::kScale + sc.slot * 2048 + tok * 16);
     const int pages = bars->pages_ok[sc.slot];
     __syncwarp();
     if (ok && lane == 0) ptx::mbar_arrive(&bars->scempty[sc.slot]);
     sc.next();
     float acc[HC];
-    const uint32_t fb = base + C::kF + (buf * 4 * NR + col0) * 4;
+    uint32_t fb = base + C::kF + (buf * 4 * NR + col0) * 4;
+    SMLA_WAIT(&bars->sfull[s.slot], s.parity);
+    ptx::tc_fence_after();
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
+    for (int i0 = 0; i0 < HC; i0 += LC) {
+      uint32_t r[LC];
+      tmem_ld<LC>(lane_base + C::kSCol + 2 * NR * s.slot + col0 + i0, r);
+      ptx::tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < LC; ++i) acc[i0 + i] = __uint_as_float(r[i]) * kf;
+    }
+    ptx::tc_fence_before();
+    __syncwarp();
+    if (ok && lane == 0) ptx::mbar_arrive(&bars->sempty[s.slot]);
+    s.next();
+#pragma unroll 1
+    for (int b = 0; b < 4; ++b) {
       SMLA_WAIT(&bars->sfull[s.slot], s.parity);
       ptx::tc_fence_after();
       const uint32_t a = lane_base + C::kSCol + 2 * NR * s.slot + col0;
-      const float scale = c == 1 ? s4.x : c == 2 ? s4.y : c == 3 ? s4.z : s4.w;
+      const float scale = s4.x;
+      s4 = make_float4(s4.y, s4.z, s4.w, s4.x);
 #pragma unroll
       for (int i0 = 0; i0 < HC; i0 += LC) {
-        uint32_t hi[LC];
+        uint32_t hi[LC], lo[LC];
         tmem_ld<LC>(a + i0, hi);
-        if (c == 0) {
-          ptx::tmem_wait_ld();
+        tmem_ld<LC>(a + NR + i0, lo);
+        ptx::tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < LC; ++i) acc[i0 + i] = __uint_as_float(hi[i]) * kf;
-        } else {
-          uint32_t lo[LC];
-          tmem_ld<LC>(a + NR + i0, lo);
-          ptx::tmem_wait_ld();
+        for (int i = 0; i < LC; i += 4) {
+          const float4 f = ptx::lds128f(fb + (i0 + i) * 4);
+          const float ff[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-          for (int i = 0; i < LC; i += 4) {
-            const float4 f = ptx::lds128f(fb + ((c - 1) * NR + i0 + i) * 4);
-            const float ff[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              acc[i0 + i + j] = fmaf(__uint_as_float(hi[i + j]) + __uint_as_float(lo[i + j]), scale * ff[j], acc[i0 + i + j]);
-          }
+          for (int j = 0; j < 4; ++j)
+            acc[i0 + i + j] = fmaf(__uint_as_float(hi[i + j]) + __uint_as_float(lo[i + j]), scale * ff[j], acc[i0 + i + j]);
         }
       }
+      fb += NR * 4;
       ptx::tc_fence_before();
       __syncwarp();
       if (ok && lane == 0) ptx::mbar_arrive(&bars->sempty[s.slot]);
@@ -638,7 +647,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
       SMLA_WAIT(&bars->pdone, dpar);
       dpar ^= 1;
     }
-    if (move) {
+    if (__builtin_expect(move, 0)) {
       float v[HC];
 #pragma unroll
       for (int i = 0; i < HC; ++i) v[i] = acc[i];
@@ -731,7 +740,8 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
     }
 #pragma unroll 1
     for (int b = 0; b < 4; ++b) {
-      const int dim = 128 * b + tok;
+      // lane -> dim within a group of four: 0, 2, 1, 3 (codes_to_f16's order)
+    const int dim = 128 * b + (tok & ~3) + 2 * (tok & 1);
 #pragma unroll
       for (int i0 = 0; i0 < HC; i0 += LC) {
         uint32_t o[LC];
@@ -739,19 +749,20 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
         ptx::tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < LC; i += 2) {
-          // lanes 2j, 2j + 1 hold dims d, d + 1: the even one ends with both dims of the first row, the odd
-          // one with both of the second
+          // lanes i, i + 2 hold dims d, d + 1: the first ends with both dims of the first row, the other with
+          // both of the second
+          const bool second = lane & 2;
           const float va = __uint_as_float(o[i]) * __shfl_sync(0xffffffffu, inv, i0 + i);
           const float vb = __uint_as_float(o[i + 1]) * __shfl_sync(0xffffffffu, inv, i0 + i + 1);
-          const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? va : vb, 1);
-          const int c = col0 + i0 + i + (lane & 1);
-          const float d0 = lane & 1 ? got : va, d1 = lane & 1 ? vb : got;
+          const float got = __shfl_xor_sync(0xffffffffu, second ? va : vb, 2);
+          const int c = col0 + i0 + i + (second ? 1 : 0);
+          const float d0 = second ? got : va, d1 = second ? vb : got;
           if (ok && c < it.nrows) {
             if (whole) {
               uint16_t* o16 = p.out + ((size_t)it.req * p.q_per_req * p.H + it.row0 + c) * kDLatent;
-              *reinterpret_cast<uint32_t*>(o16 + (dim & ~1)) = f32x2_to_bf16x2(d0, d1);
+              *reinterpret_cast<uint32_t*>(o16 + dim) = f32x2_to_bf16x2(d0, d1);
             } else {
-              *reinterpret_cast<float2*>(o_part + (slot * NR + c) * kDLatent + (dim & ~1)) = make_float2(d0, d1);
+              *reinterpret_cast<float2*>(o_part + (slot * NR + c) * kDLatent + dim) = make_float2(d0, d1);
             }
           }
         }
@@ -776,12 +787,12 @@ __device__ void find_run(const DenseParams& p, unsigned char* scratch, Bars* bar
   for (int i = i0; i < i1; ++i) mine += item_at(p, i).tiles;
   sums[threadIdx.x] = mine;
   __syncthreads();
-  if (threadIdx.x < 32) {                                // exclusive prefix over 19 sums per lane
-    long long v[19], part = 0;
+  if (threadIdx.x < 32) {                                // exclusive prefix over 20 sums per lane
+    long long v[20], part = 0;
 #pragma unroll
-    for (int j = 0; j < 19; ++j) {
+    for (int j = 0; j < 20; ++j) {
       v[j] = part;
-      part += sums[19 * threadIdx.x + j];
+      part += sums[20 * threadIdx.x + j];
     }
     long long before = part;
 #pragma unroll
@@ -792,7 +803,7 @@ __device__ void find_run(const DenseParams& p, unsigned char* scratch, Bars* bar
     if (threadIdx.x == 31) bars->total = before;
     before -= part;
 #pragma unroll
-    for (int j = 0; j < 19; ++j) sums[19 * threadIdx.x + j] = before + v[j];
+    for (int j = 0; j < 20; ++j) sums[20 * threadIdx.x + j] = before + v[j];
   }
   __syncthreads();
   const long long T = bars->total;
@@ -877,11 +888,17 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = bars->tmem;
 
-  if (warp < kSoftWarps) softmax_role<NR>(p, sm, base, tmem, bars, warp, lane, o_part, lse_part);
-  else if (warp < kSoftWarps + kConvWarps) convert_role<NR>(p, sm, base, bars, warp, lane);
-  else if (warp == kCopyWarp) copy_role<NR>(p, &map, &smap, base, bars, lane);
-  else if (warp == kQkWarp) qk_role<NR>(p, base, tmem, bars, lane);
-  else if (warp == kPvWarp) pv_role<NR>(p, base, tmem, bars, lane);
+  if (warp < kSoftWarps) {
+    ptx::setmaxnreg_inc<kSoftRegs>();
+    softmax_role<NR>(p, sm, base, tmem, bars, warp, lane, o_part, lse_part);
+  } else if (warp < kSoftWarps + kConvWarps) {
+    convert_role<NR>(p, base, bars, warp, lane);
+  } else {
+    ptx::setmaxnreg_dec<kMiscRegs>();
+    if (warp == kCopyWarp) copy_role<NR>(p, &map, &smap, base, bars, lane);
+    else if (warp == kQkWarp) qk_role<NR>(p, base, tmem, bars, lane);
+    else if (warp == kPvWarp) pv_role<NR>(p, base, tmem, bars, lane);
+  }
 
   // nothing of this CTA's may be in flight when it leaves: the MMAs (their last commits) and, after a wait
   // that gave up, the copies

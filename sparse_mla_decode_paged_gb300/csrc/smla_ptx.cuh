@@ -87,6 +87,36 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
   }
 }
 
+// try_wait that suspends the thread for about `hint_ns` at most.
+__device__ __forceinline__ bool mbar_try_wait_for(uint64_t* bar, uint32_t parity, uint32_t hint_ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(hint_ns)
+      : "memory");
+  return ok != 0;
+}
+
+// mbar_wait_bounded in few instructions, for a kernel whose many waits compete for the instruction cache: each
+// try suspends for at most the limit (or 1 ms), so a limit of nanoseconds runs out as such.  A whole warp calls
+// it; the verdict is the AND over its lanes.
+__device__ __forceinline__ bool mbar_wait_warp_small(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                                     uint64_t limit_ns) {
+  const uint32_t hint = limit_ns < 1000000ull ? (uint32_t)limit_ns : 1000000u;
+  bool ok = mbar_try_wait_for(bar, parity, hint);
+  if (!ok) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!(ok = mbar_try_wait_for(bar, parity, hint))) {
+      if (*abort || globaltimer_ns() - t0 > limit_ns) {
+        *abort = 1;
+        break;
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
 // Arrive on an mbarrier and add `bytes` to the transaction count its current phase waits for.
 __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
@@ -167,6 +197,17 @@ __device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t threads, bool
       : "r"(id), "r"(threads), "r"((uint32_t)pred)
       : "memory");
   return r != 0;
+}
+
+// Registers per thread of the calling warpgroup from here on (every warp of it executes the call).  An increase
+// waits until the block's other warpgroups have released enough of the registers it was launched with.
+template <int kRegs>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
 // ----------------------------------------------------------------------------- tcgen05
