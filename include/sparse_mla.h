@@ -395,10 +395,10 @@ int sparse_mla_dense_plan(const smla_dense_dims* dims, int32_t device, smla_dens
  * never used, whatever their records hold.
  * Numerics: the latent scores are sums of E4M3 codes times q as two E4M3
  * terms, the rope scores bf16 products, all accumulated in fp32 (q is exact but
- * for elements below about 2^-9 of the largest of their row's 128-dim block,
- * whose absolute error stays below 2^-17 of that largest); softmax weights and
- * dequantised latents are fp16 on chip, |dequantised latent| must stay below
- * 65504 (larger values saturate and set SMLA_DEVERR_RANGE).
+ * for latent elements below about 2^-9 of their row's largest, whose absolute
+ * error stays below 2^-17 of that largest); softmax weights and values are
+ * fp16 on chip with a power of two per position and a running reference, so
+ * neither has to stay in fp16's range.
  * Statuses as sparse_mla_decode. */
 int sparse_mla_dense_decode(const smla_dense_dims* dims, const void* q, const void* kv_cache,
                             const int32_t* block_table, const int32_t* seq_lens, float sm_scale, void* out,

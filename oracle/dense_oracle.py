@@ -41,17 +41,16 @@ def score_error_bound(q: np.ndarray, k: np.ndarray, sm_scale: float) -> np.ndarr
     Accumulating 576 products in float32 is off by at most 2^-20 of the sum of
     their magnitudes (the accumulator adds groups of 16 or 32 products, so about
     40 roundings of 2^-24 each).  q as hi + lo in E4M3, scaled so that the
-    largest of a 128-dim block lies in [2^7, 2^8): hi keeps 4 bits, so an element
-    of 8 bits leaves a remainder of 4 bits, which lo holds exactly unless it
-    falls below E4M3's step of 2^-9; that needs an element below 2^-8 of the
+    largest latent element of a row lies in [2^7, 2^8): hi keeps 4 bits, so an
+    element of 8 bits leaves a remainder of 4 bits, which lo holds exactly unless
+    it falls below E4M3's step of 2^-9; that needs an element below 2^-8 of the
     largest, and the error is then at most 2^-10 / 2^7 of the largest.
     """
     err = 2.0 ** -20 * (np.abs(q) @ np.abs(k).T)
-    for b in range(4):
-        qb, kb = np.abs(q[:, 128 * b:128 * b + 128]), np.abs(k[:, 128 * b:128 * b + 128])
-        top = qb.max(axis=1, keepdims=True)
-        small = (qb < 2.0 ** -8 * top) & (qb > 0)
-        err = err + 2.0 ** -17 * (top * small) @ kb.T
+    ql, kl = np.abs(q[:, :D_LATENT]), np.abs(k[:, :D_LATENT])
+    top = ql.max(axis=1, keepdims=True)
+    small = (ql < 2.0 ** -8 * top) & (ql > 0)
+    err = err + 2.0 ** -17 * (top * small) @ kl.T
     return sm_scale * err
 
 

@@ -10,15 +10,18 @@
 // keeps every SM busy; an item that crosses a CTA boundary leaves partial results that the merge kernel joins.
 //
 // Scores.  The codes go to the tensor core as they are (kind::f8f6f4), with no conversion: q is split into
-// two E4M3 terms, q 2^-x = hi + lo with x chosen per (row, 128-dim block) so that the block's largest element
-// lies in [2^7, 2^8).  hi keeps 4 significant bits and lo the other 4 of a bf16 value, so the split is exact but
-// for elements below about 2^-9 of the largest (their error is below 2^-17 of it).  S^T of a tile: M = 128
-// positions, N = 2 NR columns (hi rows, then lo rows), one accumulator per 128-dim scale block; the softmax
-// threads form s = sum_b (S_hi + S_lo) scale_b 2^x_b in fp32.  The rope part is a bf16 product.
-// Weights and values.  P = 2^(s - ref) in fp16 with ref = (a running maximum) - 7, moved only when a score
-// exceeds ref by more than 15: P stays below 2^15, and weights down to 2^-31 of the largest keep an absolute
-// error below 2^-32 of it, so that a long tail beside one dominating position is not lost.  V = fp16(code *
-// scale): O^T[512 x NR] += V^T P, M = 128 dims, fp32 in TMEM.
+// two E4M3 terms, q 2^-x = hi + lo with x chosen per row so that its largest latent element lies in [2^7, 2^8).  hi
+// keeps 4 significant bits and lo the other 4 of a bf16 value, so the split is exact but for elements below
+// about 2^-9 of the largest (their error is below 2^-17 of it, 2^-8 of that element's own bf16 rounding).  S^T of
+// a tile: M = 128 positions, N = 2 NR columns (hi rows, then lo rows), one accumulator per 128-dim scale block; the
+// softmax threads form s = 2^x sum_b (S_hi + S_lo) scale_b in fp32.  The rope part is a bf16 product.
+// Weights and values.  A position's scales are split as scale_b = m_b 2^e, e the exponent of the largest of the four;
+// V = fp16(code * m_b) (at most 896, one rounding) and the weight takes the power of two,
+//   P = 2^(s + e - ref) in fp16, l = sum P 2^-e in fp32, out = O / l, lse = ln 2 (ref + log2 l),
+// with ref = (a running maximum of s + e) - 7, moved only when s + e exceeds ref by more than 15: P stays below 2^15, and
+// contributions down to 2^-31 of the largest keep an absolute error below 2^-32 of it, so that a long tail
+// beside one dominating position is not lost and latents of any size fit.  O^T[512 x NR] += V^T P, M = 128 dims,
+// fp32 in TMEM.
 //
 // What bounds it: HBM bytes (656 per position) for up to 64 rows, where one SM's share of the HBM rate is a
 // tile per 1.9 us; inside an SM the shared-memory path, which a tile of 64 rows takes about 640 KB through
@@ -39,7 +42,6 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNoRef = -1e30f;          // reference of a row that has met no position yet
 constexpr float kRefBelowMax = 7.f;       // a new reference lies this far below the maximum it was taken from
 constexpr float kRefSlack = 15.f;         // a score this far above the reference moves it (2^15 is an fp16 value)
 
@@ -48,10 +50,10 @@ constexpr float kRefSlack = 15.f;         // a score this far above the referenc
 constexpr int kSoftWarps = 8, kConvWarps = 8;
 constexpr int kCopyWarp = 16, kQkWarp = 17, kPvWarp = 18;
 constexpr int kDenseThreads = 20 * 32;     // five warpgroups; the last warp is idle
-constexpr int kSoftRegs = 128, kMiscRegs = 32;   // of 96 at launch: 2 x 128 + 2 x 96 + 32 = 5 x 96
+constexpr int kSoftRegs = 128, kConvRegs = 88, kMiscRegs = 48;   // of 96 at launch: 2 x 128 + 2 x 88 + 48 = 5 x 96
 
 constexpr uint32_t kSlot = 16384;         // 128 positions x 128 bytes: one code block or the rope of a tile
-constexpr int kChunks = 5;                // rope, then the four code blocks
+constexpr int kChunks = 5;                // the four code blocks, then the rope
 constexpr int kSliceTokens = 16;          // positions of one V slice (one MMA K step)
 constexpr int kSlices = kDenseTile / kSliceTokens;
 constexpr int kScaleSlots = 3;
@@ -69,11 +71,11 @@ struct DC {
   static constexpr uint32_t kV = kK + kRing * kSlot;
   static constexpr uint32_t kP = kV + kVRing * kSlot;
   static constexpr uint32_t kScale = kP + 128 * 2 * NR;
-  static constexpr uint32_t kF = kScale + kScaleSlots * 2048;     // [2][4][NR] float
-  static constexpr uint32_t kLen = kF + 2 * 4 * NR * 4;           // [2][NR] int
-  static constexpr uint32_t kRef = kLen + 2 * NR * 4;             // [NR] float
-  static constexpr uint32_t kRed = kRef + NR * 4;                 // [4][NR] float
-  static constexpr uint32_t kBar = kRed + 4 * NR * 4;
+  static constexpr uint32_t kF = kScale + kScaleSlots * 2048;     // [2][NR] float
+  static constexpr uint32_t kLen = kF + 2 * NR * 4;           // [2][NR] int
+  static constexpr uint32_t kRef = kLen + 2 * NR * 4;             // [NR] float: minus the reference
+  static constexpr uint32_t kRed = kRef + NR * 4;                 // [5][NR] float
+  static constexpr uint32_t kBar = kRed + 5 * NR * 4;
   static constexpr uint32_t kBytes = kBar + 512;
   static constexpr uint32_t kTmemCols = 8 * NR;
   static constexpr uint32_t kSCol = 4 * NR;                       // score buffer i at 4 NR + 2 NR i
@@ -238,7 +240,7 @@ __device__ void copy_role(const DenseParams& p, const CUtensorMap* map, const CU
         ptx::mbar_arrive_expect_tx(&bars->kfull[k.slot], n_good * (kSlot / 2));
         for (int h = 0; h < 2; ++h)
           if (good >> h & 1)
-            ptx::tma_load_3d(base + C::kK + k.slot * kSlot + h * (kSlot / 2), map, c == 0 ? kDLatent + 16 : 128 * (c - 1),
+            ptx::tma_load_3d(base + C::kK + k.slot * kSlot + h * (kSlot / 2), map, c == 4 ? kDLatent + 16 : 128 * c,
                              0, pg[h], &bars->kfull[k.slot]);
       }
       __syncwarp();
@@ -283,11 +285,11 @@ __device__ void qk_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars
       if (ok && ptx::elect_one()) {
         const uint64_t dk = ptx::sw128_desc(base + C::kK + k.slot * kSlot, 16, 1024);
         const uint32_t d = tmem + C::kSCol + 2 * NR * s.slot;
-        if (c == 0) {
+        if (c == 4) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) ptx::mma_f16_ss(d, dk + 2 * kk, dr + 2 * kk, kIdescRope, kk > 0);
         } else {
-          const uint64_t dqb = dq + (uint64_t)(((c - 1) * C::kQ8Chunk) >> 4);
+          const uint64_t dqb = dq + (uint64_t)((c * C::kQ8Chunk) >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) ptx::mma_f8_ss(d, dk + 2 * kk, dqb + 2 * kk, kIdescCodes, kk > 0);
         }
@@ -348,38 +350,33 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, __half2 b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// 16 codes of one 128-dim block as fp16 values: code 2^-8 times scale 2^8, rounded once.
-//
-// A code's bits, shifted to where fp16 has its sign, the low four exponent bits and the top of the fraction, read
-// as 2^-8 of its value, subnormals included; a NaN code reads as 480 (the position's score is NaN already, so
-// the rows that see it are NaN whatever its value, and the rows that do not stay clean).  One word of four codes
-// gives the pairs of dims 0, 2 and 1, 3.  scale 2^8 has fp16's full precision for scales from 2^-22 (latents up
-// to 1e-4) to 255; below, the absolute error stays that of fp16's subnormals.
-__device__ __forceinline__ void convert16(uint4 codes, float scale, uint32_t (&o)[8]) {
+// 16 codes of one 128-dim block times its factor, as fp16.
+__device__ __forceinline__ void convert16(uint4 codes, __half2 m, uint32_t (&o)[8]) {
   const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-  const __half2 s = __float2half2_rn(scale * 256.f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    o[2 * i] = hmul2(((w[i] << 8) & 0x80008000u) | ((w[i] << 7) & 0x3f803f80u), s);
-    o[2 * i + 1] = hmul2((w[i] & 0x80008000u) | ((w[i] >> 1) & 0x3f803f80u), s);
+    o[2 * i] = hmul2(e4m3x2_to_f16x2((uint16_t)(w[i] & 0xffffu)), m);
+    o[2 * i + 1] = hmul2(e4m3x2_to_f16x2((uint16_t)(w[i] >> 16)), m);
   }
 }
 
-// The rest of a scale above 146 (a block that may leave fp16's range): times a power of two, saturating; true
-// if a value left the range.
-__device__ __forceinline__ bool scale_up(uint32_t (&o)[8], int e) {
-  const __half2 up = __float2half2_rn(__uint_as_float((uint32_t)(127 + e) << 23));
-  const __half2 top = __float2half2_rn(65504.f), bottom = __float2half2_rn(-65504.f);
-  bool over = false;
+// NaNs to numbers, for positions that some row does not see: their weight 0 must give 0.  (A row that does
+// see a NaN code or scale has a NaN score, so it is NaN whatever the value.)
+__device__ __forceinline__ void no_nan(uint32_t (&o)[8]) {
+  const __half2 top = __float2half2_rn(65504.f);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const uint32_t v = hmul2(o[i], up);
-    const __half2 c = __hmax2(__hmin2(*reinterpret_cast<const __half2*>(&v), top), bottom);
+    const __half2 c = __hmin2(*reinterpret_cast<const __half2*>(&o[i]), top);
     o[i] = *reinterpret_cast<const uint32_t*>(&c);
-    over |= o[i] != v;
   }
-  return over;
 }
+
+// The exponent e that a position's weight takes from its scales.
+__device__ __forceinline__ int scale_exponent(const float4& s) {
+  const float top = fmaxf(fmaxf(fabsf(s.x), fabsf(s.y)), fmaxf(fabsf(s.z), fabsf(s.w)));
+  return min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 100);
+}
+__device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
 // Group g converts slices g, g + 2, g + 4, g + 6 of a tile: lane -> position (lane & 15) of the slice, 16-dim
 // unit 2 (warp % 4) + lane / 16 of every 128-dim block.  A warp reads its part of each code block into
@@ -394,12 +391,9 @@ __device__ void convert_role(const DenseParams& p, uint32_t base, Bars* bars, in
   Ring<kScaleSlots> sc;
   Ring<C::kVRing> v;
   if (group) v.next();
-  bool ok = true, over = false;
+  bool ok = true;
   while (w.left > 0) {
     uint4 codes[4][4];
-    SMLA_WAIT(&bars->kfull[k.slot], k.parity);                     // the rope: nothing to read
-    if (ok && lane == 0) ptx::mbar_arrive(&bars->kempty[k.slot]);
-    k.next();
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       SMLA_WAIT(&bars->kfull[k.slot], k.parity);
@@ -411,6 +405,9 @@ __device__ void convert_role(const DenseParams& p, uint32_t base, Bars* bars, in
       if (ok && lane == 0) ptx::mbar_arrive(&bars->kempty[k.slot]);
       k.next();
     }
+    SMLA_WAIT(&bars->kfull[k.slot], k.parity);         // the rope: nothing to read
+    if (ok && lane == 0) ptx::mbar_arrive(&bars->kempty[k.slot]);
+    k.next();
     SMLA_WAIT(&bars->scfull[sc.slot], sc.parity);
     const int pages = bars->pages_ok[sc.slot];
 #pragma unroll
@@ -419,23 +416,19 @@ __device__ void convert_role(const DenseParams& p, uint32_t base, Bars* bars, in
       const long long t = (long long)w.t * kDenseTile + row;
       const bool valid = t < w.it.max_len && (pages >> (row >> 6) & 1);
       const float4 s4 = ptx::lds128f(base + C::kScale + sc.slot * 2048 + row * 16);
-      float scale[4] = {s4.x, s4.y, s4.z, s4.w};
-      const float top = fmaxf(fmaxf(fabsf(s4.x), fabsf(s4.y)), fmaxf(fabsf(s4.z), fabsf(s4.w)));
-      const bool wide = valid && !(top <= 146.f && !isnan(s4.x + s4.y + s4.z + s4.w));   // 448 * 146 < 65504
-      int e = 0;
-      if (__builtin_expect(wide, 0)) {                 // the largest scale's exponent comes off before fp16
-        e = min(max((int)(__float_as_uint(top) >> 23) - 127, 0), 15);
+      const float down = valid ? exp2_int(-scale_exponent(s4)) : 0.f;
+      const float scale[4] = {s4.x, s4.y, s4.z, s4.w};
+      __half2 m[4];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) scale[b] *= __uint_as_float((uint32_t)(127 - e) << 23);
-      }
-      if (!valid) scale[0] = scale[1] = scale[2] = scale[3] = 0.f;
+      for (int b = 0; b < 4; ++b) m[b] = __float2half2_rn(fminf(fmaxf(scale[b] * down, -2.f), 2.f));
+      const bool partly = !valid || t >= w.it.min_len;
       SMLA_WAIT(&bars->vempty[v.slot], v.parity ^ 1);
       const uint32_t dst = base + C::kV + v.slot * kSlot;
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         uint32_t o[8];
-        convert16(codes[b][j], scale[b], o);
-        if (__builtin_expect(wide, 0)) over |= scale_up(o, e);
+        convert16(codes[b][j], m[b], o);
+        if (__builtin_expect(partly, 0)) no_nan(o);
         const uint32_t chunk = dst + (2 * b + (unit >> 2)) * 2048;
         ptx::sts128_async_only(chunk + swz128(tok, (unit & 3) * 2), make_uint4(o[0], o[1], o[2], o[3]));
         ptx::sts128_async_only(chunk + swz128(tok, (unit & 3) * 2 + 1), make_uint4(o[4], o[5], o[6], o[7]));
@@ -450,7 +443,6 @@ __device__ void convert_role(const DenseParams& p, uint32_t base, Bars* bars, in
     sc.next();
     w.next(p);
   }
-  if (__any_sync(0xffffffffu, over) && lane == 0) atomicOr(p.err, SMLA_DEVERR_RANGE);
 }
 
 // ----------------------------------------------------------------------------- softmax
@@ -474,12 +466,12 @@ __device__ __forceinline__ float reduce_scatter(float (&v)[N], int lane, Op op) 
   return r;
 }
 
-// Rows of one item into the Q operands: hi and lo E4M3 codes of each 128-dim block scaled by 2^-x, the rope as
-// it is; the factor 2^x sm_scale log2 e per (block, row) and each row's length go to buffer `buf`.
+// Rows of one item into the Q operands: hi and lo E4M3 codes of the latent part scaled by 2^-x, the rope as it is;
+// each row's factor 2^x sm_scale log2 e and length go to buffer `buf`.
 template <int NR>
 __device__ void load_q(const DenseParams& p, const Item& it, unsigned char* sm, uint32_t base, int buf, int warp, int lane) {
   using C = DC<NR>;
-  float* f = reinterpret_cast<float*>(sm + C::kF) + buf * 4 * NR;
+  float* f = reinterpret_cast<float*>(sm + C::kF) + buf * NR;
   int* lens = reinterpret_cast<int*>(sm + C::kLen) + buf * NR;
   const float kf = p.sm_scale * kLog2e;
   const uint16_t* q0 = p.q + ((size_t)it.req * p.q_per_req * p.H + it.row0) * kDQK;
@@ -499,10 +491,10 @@ __device__ void load_q(const DenseParams& p, const Item& it, unsigned char* sm, 
     for (int i = 0; i < 8; ++i)
       amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(wds[i] << 16)), fabsf(__uint_as_float(wds[i] & 0xffff0000u))));
 #pragma unroll
-    for (int o = 4; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     // x = floor(log2 amax) - 7, kept where 2^x and 2^-x are normal floats
     const int x = amax > 0.f ? min(max((int)(__float_as_uint(amax) >> 23) - 127 - 7, -120), 120) : 0;
-    const float down = __uint_as_float((uint32_t)(127 - x) << 23);
+    const float down = exp2_int(-x);
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -523,9 +515,10 @@ __device__ void load_q(const DenseParams& p, const Item& it, unsigned char* sm, 
     ptx::sts128(q8 + swz128(r, u), make_uint4(hi[0], hi[1], hi[2], hi[3]));
     ptx::sts128(q8 + swz128(NR + r, u), make_uint4(lo[0], lo[1], lo[2], lo[3]));
     if (lane < 8) ptx::sts128(base + C::kQr + swz128(r, lane), rope);
-    if (u == 0) f[b * NR + r] = __uint_as_float((uint32_t)(127 + x) << 23) * kf;
-    if (lane == 0)
+    if (lane == 0) {
+      f[r] = exp2_int(x) * kf;
       lens[r] = r < it.nrows ? clamped_len(p, it.req * p.q_per_req + (it.row0 + r) / p.H) : it.max_len;
+    }
   }
 }
 
@@ -551,15 +544,15 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
   const int tok = 32 * quad + lane;
   const uint32_t lane_base = tmem + ((uint32_t)(32 * quad) << 16);
   const float kf = p.sm_scale * kLog2e;
-  float* ref = reinterpret_cast<float*>(sm + C::kRef) + col0;
-  float* red = reinterpret_cast<float*>(sm + C::kRed) + col0;   // [4][NR]
+  float* nref = reinterpret_cast<float*>(sm + C::kRef) + col0;  // minus the reference
+  float* red = reinterpret_cast<float*>(sm + C::kRed) + col0;   // [5][NR]
   Walk w(p, bars);
   Ring<C::kSBufs> s;
   Ring<kScaleSlots> sc;
   uint32_t dpar = 0;
-  bool ok = true, first = true, begins = w.t == 0;
+  bool ok = true, first = true, fresh = true, begins = w.t == 0;
   int buf = 0;
-  float l[HC];
+  uint64_t l[HC / 2];                                   // row sums over this thread's positions, pairs of rows
   if (w.left > 0) {
     load_q<NR>(p, w.it, sm, base, 0, warp, lane);
     ptx::fence_proxy_async_smem();
@@ -570,7 +563,8 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
   while (w.left > 0) {
     if (first) {
 #pragma unroll
-      for (int i = 0; i < HC; ++i) l[i] = 0.f;
+      for (int i = 0; i < HC / 2; ++i) l[i] = 0;
+      fresh = true;
     }
     // scores of this thread's position for its HC rows, in units of log2
     SMLA_WAIT(&bars->scfull[sc.slot], sc.parity);
@@ -579,28 +573,16 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
     __syncwarp();
     if (ok && lane == 0) ptx::mbar_arrive(&bars->scempty[sc.slot]);
     sc.next();
-    float acc[HC];
-    uint32_t fb = base + C::kF + (buf * 4 * NR + col0) * 4;
-    SMLA_WAIT(&bars->sfull[s.slot], s.parity);
-    ptx::tc_fence_after();
+    const int e = scale_exponent(s4);
+    uint64_t acc[HC / 2];                               // pairs of rows
 #pragma unroll
-    for (int i0 = 0; i0 < HC; i0 += LC) {
-      uint32_t r[LC];
-      tmem_ld<LC>(lane_base + C::kSCol + 2 * NR * s.slot + col0 + i0, r);
-      ptx::tmem_wait_ld();
-#pragma unroll
-      for (int i = 0; i < LC; ++i) acc[i0 + i] = __uint_as_float(r[i]) * kf;
-    }
-    ptx::tc_fence_before();
-    __syncwarp();
-    if (ok && lane == 0) ptx::mbar_arrive(&bars->sempty[s.slot]);
-    s.next();
+    for (int i = 0; i < HC / 2; ++i) acc[i] = 0;
 #pragma unroll 1
     for (int b = 0; b < 4; ++b) {
       SMLA_WAIT(&bars->sfull[s.slot], s.parity);
       ptx::tc_fence_after();
       const uint32_t a = lane_base + C::kSCol + 2 * NR * s.slot + col0;
-      const float scale = s4.x;
+      const uint64_t scale = ptx::pack2(s4.x, s4.x);
       s4 = make_float4(s4.y, s4.z, s4.w, s4.x);
 #pragma unroll
       for (int i0 = 0; i0 < HC; i0 += LC) {
@@ -609,40 +591,63 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
         tmem_ld<LC>(a + NR + i0, lo);
         ptx::tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < LC; i += 4) {
-          const float4 f = ptx::lds128f(fb + (i0 + i) * 4);
-          const float ff[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            acc[i0 + i + j] = fmaf(__uint_as_float(hi[i + j]) + __uint_as_float(lo[i + j]), scale * ff[j], acc[i0 + i + j]);
-        }
+        for (int i = 0; i < LC; i += 2)
+          acc[(i0 + i) / 2] = ptx::fma2(ptx::add2(ptx::pack2(hi[i], hi[i + 1]), ptx::pack2(lo[i], lo[i + 1])), scale,
+                                        acc[(i0 + i) / 2]);
       }
-      fb += NR * 4;
       ptx::tc_fence_before();
       __syncwarp();
       if (ok && lane == 0) ptx::mbar_arrive(&bars->sempty[s.slot]);
       s.next();
     }
+    // s + e - ref, as 2^x (latent part) + (rope part sm_scale log2 e) + (e - ref)
+    SMLA_WAIT(&bars->sfull[s.slot], s.parity);
+    ptx::tc_fence_after();
+    {
+      const uint32_t a = lane_base + C::kSCol + 2 * NR * s.slot + col0;
+      const uint64_t kf2 = ptx::pack2(kf, kf), e2 = ptx::pack2((float)e, (float)e);
+      const uint32_t fa = base + C::kF + (buf * NR + col0) * 4, ra = base + C::kRef + col0 * 4;
+#pragma unroll
+      for (int i0 = 0; i0 < HC; i0 += LC) {
+        uint32_t r[LC];
+        tmem_ld<LC>(a + i0, r);
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < LC; i += 4) {
+          const ulonglong2 f = ptx::lds128_pairs(fa + (i0 + i) * 4);
+          ulonglong2 off = ptx::lds128_pairs(ra + (i0 + i) * 4);
+          if (fresh) off.x = off.y = 0;
+          uint64_t* d = &acc[(i0 + i) / 2];
+          d[0] = ptx::fma2(d[0], f.x, ptx::fma2(ptx::pack2(r[i], r[i + 1]), kf2, ptx::add2(off.x, e2)));
+          d[1] = ptx::fma2(d[1], f.y, ptx::fma2(ptx::pack2(r[i + 2], r[i + 3]), kf2, ptx::add2(off.y, e2)));
+        }
+      }
+    }
+    ptx::tc_fence_before();
+    __syncwarp();
+    if (ok && lane == 0) ptx::mbar_arrive(&bars->sempty[s.slot]);
+    s.next();
     // positions that a row may not see
     const long long t = (long long)w.t * kDenseTile + tok;
-    if ((long long)(w.t + 1) * kDenseTile > w.it.min_len || pages != 3) {
+    if (__builtin_expect((long long)(w.t + 1) * kDenseTile > w.it.min_len || pages != 3, 0)) {
       const int* lens = reinterpret_cast<const int*>(sm + C::kLen) + buf * NR + col0;
       const bool here = pages >> (tok >> 6) & 1;
 #pragma unroll
-      for (int i = 0; i < HC; ++i)
-        if (!here || t >= lens[i]) acc[i] = -CUDART_INF_F;
-    }
-    // the reference moves when a score lies more than kRefSlack above it
-    bool move = first;
-    if (!first) {
-#pragma unroll
-      for (int i = 0; i < HC; i += 4) {
-        const float4 r = ptx::lds128f(base + C::kRef + (col0 + i) * 4);
-        move |= acc[i] > r.x + kRefSlack || acc[i + 1] > r.y + kRefSlack || acc[i + 2] > r.z + kRefSlack ||
-                acc[i + 3] > r.w + kRefSlack;
+      for (int i = 0; i < HC; i += 2) {
+        float2 d = ptx::unpack2(acc[i / 2]);
+        if (!here || t >= lens[i]) d.x = -CUDART_INF_F;
+        if (!here || t >= lens[i + 1]) d.y = -CUDART_INF_F;
+        acc[i / 2] = ptx::pack2(d.x, d.y);
       }
     }
-    move = ptx::named_bar_or(1 + half, 128, move);
+    // the reference moves when a contribution lies more than kRefSlack above it
+    float top = -CUDART_INF_F;
+#pragma unroll
+    for (int i = 0; i < HC / 2; ++i) {
+      const float2 d = ptx::unpack2(acc[i]);
+      top = fmaxf(top, fmaxf(d.x, d.y));
+    }
+    const bool move = ptx::named_bar_or(1 + half, 128, fresh || top > kRefSlack);
     if (!first) {                                       // P and O are free once the tile before is done
       SMLA_WAIT(&bars->pdone, dpar);
       dpar ^= 1;
@@ -650,53 +655,64 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
     if (__builtin_expect(move, 0)) {
       float v[HC];
 #pragma unroll
-      for (int i = 0; i < HC; ++i) v[i] = acc[i];
+      for (int i = 0; i < HC / 2; ++i) {
+        const float2 d = ptx::unpack2(acc[i]);
+        v[2 * i] = d.x;
+        v[2 * i + 1] = d.y;
+      }
       const float m = reduce_scatter<HC>(v, lane, [](float a, float b) { return fmaxf(a, b); });
       if (lane < HC) red[quad * NR + lane] = m;
       ptx::named_bar_sync(1 + half, 128);
-      float factor = 1.f, now = kNoRef;
+      // by how much row `lane`'s reference rises (or, for the first positions it meets, is set)
+      float up = 0.f;
       if (lane < HC) {
-        const float top = fmaxf(fmaxf(red[lane], red[NR + lane]), fmaxf(red[2 * NR + lane], red[3 * NR + lane]));
-        const float old = first ? kNoRef : ref[lane];
-        now = top > old + kRefSlack ? top - kRefBelowMax : old;
-        factor = ptx::ex2_approx(old - now);
+        const float most = fmaxf(fmaxf(red[lane], red[NR + lane]), fmaxf(red[2 * NR + lane], red[3 * NR + lane]));
+        if (most > (fresh ? -CUDART_INF_F : kRefSlack)) up = most - kRefBelowMax;
+        if (quad == 0) red[4 * NR + lane] = (fresh ? 0.f : nref[lane]) - up;
       }
       ptx::named_bar_sync(1 + half, 128);
-      if (quad == 0 && lane < HC) ref[lane] = now;
-      ptx::named_bar_sync(1 + half, 128);
+      if (quad == 0 && lane < HC) nref[lane] = red[4 * NR + lane];
+      const float factor = ptx::ex2_approx(-up);
+#pragma unroll
+      for (int i = 0; i < HC / 2; ++i) {
+        const float2 d = ptx::unpack2(acc[i]);
+        acc[i] = ptx::pack2(d.x - __shfl_sync(0xffffffffu, up, 2 * i), d.y - __shfl_sync(0xffffffffu, up, 2 * i + 1));
+      }
       if (!first) {
         ptx::tc_fence_after();
 #pragma unroll
-        for (int i = 0; i < HC; ++i) l[i] *= __shfl_sync(0xffffffffu, factor, i);
+        for (int i = 0; i < HC / 2; ++i)
+          l[i] = ptx::mul2(l[i], ptx::pack2(__shfl_sync(0xffffffffu, factor, 2 * i), __shfl_sync(0xffffffffu, factor, 2 * i + 1)));
 #pragma unroll 1
         for (int b = 0; b < 4; ++b) {
-#pragma unroll
-          for (int i0 = 0; i0 < HC; i0 += LC) {
-            uint32_t o[LC];
-            tmem_ld<LC>(lane_base + NR * b + col0 + i0, o);
+#pragma unroll 1
+          for (int i0 = 0; i0 < HC; i0 += 8) {
+            uint32_t o[8];
+            tmem_ld<8>(lane_base + NR * b + col0 + i0, o);
             ptx::tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < LC; ++i)
+            for (int i = 0; i < 8; ++i)
               o[i] = __float_as_uint(__uint_as_float(o[i]) * __shfl_sync(0xffffffffu, factor, i0 + i));
-            tmem_st<LC>(lane_base + NR * b + col0 + i0, o);
+            tmem_st<8>(lane_base + NR * b + col0 + i0, o);
           }
         }
         ptx::tmem_wait_st();
       }
+      ptx::named_bar_sync(1 + half, 128);               // the new reference is written
     }
+    fresh = fresh && pages == 0;                        // a tile of skipped pages sets no reference
     // weights
+    const uint64_t down = ptx::pack2(exp2_int(-e), exp2_int(-e));
 #pragma unroll
     for (int i = 0; i < HC; i += 8) {
-      const float4 r0 = ptx::lds128f(base + C::kRef + (col0 + i) * 4), r1 = ptx::lds128f(base + C::kRef + (col0 + i + 4) * 4);
-      const float r[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
       uint32_t h[4];
 #pragma unroll
-      for (int j = 0; j < 8; j += 2) {
-        const float a = ptx::ex2_approx(acc[i + j] - r[j]), c = ptx::ex2_approx(acc[i + j + 1] - r[j + 1]);
-        l[i + j] += a;
-        l[i + j + 1] += c;
+      for (int j = 0; j < 4; ++j) {
+        const float2 d = ptx::unpack2(acc[i / 2 + j]);
+        const float a = ptx::ex2_approx(d.x), c = ptx::ex2_approx(d.y);
+        l[i / 2 + j] = ptx::fma2(ptx::pack2(a, c), down, l[i / 2 + j]);
         const __half2 hh = __floats2half2_rn(a, c);
-        h[j >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
+        h[j] = *reinterpret_cast<const uint32_t*>(&hh);
       }
       ptx::sts128_async_only(base + C::kP + swz_row<C::kPRow>(tok, (col0 + i) >> 3), make_uint4(h[0], h[1], h[2], h[3]));
     }
@@ -719,7 +735,14 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
       if (ok && lane == 0) ptx::mbar_arrive(&bars->qfull);
     }
     // row sums over the tile's 128 positions
-    const float sum = reduce_scatter<HC>(l, lane, [](float a, float b) { return a + b; });
+    float ls[HC];
+#pragma unroll
+    for (int i = 0; i < HC / 2; ++i) {
+      const float2 x = ptx::unpack2(l[i]);
+      ls[2 * i] = x.x;
+      ls[2 * i + 1] = x.y;
+    }
+    const float sum = reduce_scatter<HC>(ls, lane, [](float a, float b) { return a + b; });
     if (lane < HC) red[quad * NR + lane] = sum;
     SMLA_WAIT(&bars->pdone, dpar);
     dpar ^= 1;
@@ -732,7 +755,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
     if (lane < HC) {
       const float z = red[lane] + red[NR + lane] + red[2 * NR + lane] + red[3 * NR + lane];
       inv = z > 0.f ? 1.f / z : (z == 0.f ? 0.f : CUDART_NAN_F);
-      const float lse = z == 0.f ? -CUDART_INF_F : (ref[lane] + log2f(z)) * kLn2;
+      const float lse = z == 0.f ? -CUDART_INF_F : (log2f(z) - nref[lane]) * kLn2;
       if (quad == 0 && ok && col0 + lane < it.nrows) {
         if (whole) p.lse[(size_t)it.req * p.q_per_req * p.H + it.row0 + col0 + lane] = lse;
         else lse_part[slot * NR + col0 + lane] = lse;
@@ -740,8 +763,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
     }
 #pragma unroll 1
     for (int b = 0; b < 4; ++b) {
-      // lane -> dim within a group of four: 0, 2, 1, 3 (codes_to_f16's order)
-    const int dim = 128 * b + (tok & ~3) + 2 * (tok & 1);
+      const int dim = 128 * b + (tok & ~1);
 #pragma unroll
       for (int i0 = 0; i0 < HC; i0 += LC) {
         uint32_t o[LC];
@@ -749,12 +771,12 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
         ptx::tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < LC; i += 2) {
-          // lanes i, i + 2 hold dims d, d + 1: the first ends with both dims of the first row, the other with
+          // lanes 2j, 2j + 1 hold dims d, d + 1: the first ends with both dims of the first row, the other with
           // both of the second
-          const bool second = lane & 2;
+          const bool second = lane & 1;
           const float va = __uint_as_float(o[i]) * __shfl_sync(0xffffffffu, inv, i0 + i);
           const float vb = __uint_as_float(o[i + 1]) * __shfl_sync(0xffffffffu, inv, i0 + i + 1);
-          const float got = __shfl_xor_sync(0xffffffffu, second ? va : vb, 2);
+          const float got = __shfl_xor_sync(0xffffffffu, second ? va : vb, 1);
           const int c = col0 + i0 + i + (second ? 1 : 0);
           const float d0 = second ? got : va, d1 = second ? vb : got;
           if (ok && c < it.nrows) {
@@ -892,6 +914,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     ptx::setmaxnreg_inc<kSoftRegs>();
     softmax_role<NR>(p, sm, base, tmem, bars, warp, lane, o_part, lse_part);
   } else if (warp < kSoftWarps + kConvWarps) {
+    ptx::setmaxnreg_dec<kConvRegs>();
     convert_role<NR>(p, base, bars, warp, lane);
   } else {
     ptx::setmaxnreg_dec<kMiscRegs>();

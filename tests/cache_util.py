@@ -45,9 +45,9 @@ def make_dense(lens, H, s_q=1, seed=0, spare_pages=3, q_scale=1.0, poison=True):
 def check_dense(out, lse, q, cache, bt, lens, sm_scale):
     """Element by element against the float64 oracle.
 
-    out: one bf16 rounding (2^-8 of the value); the softmax weight and the two fp16 factors of a dequantised
-    latent, 2^-11 each of the weighted magnitudes, with 2^-11 more for the float32 exponential, sums and merge and
-    for fp16 subnormals (steps of 2^-24 on latents); a score error e changes a weight by at most 2 e.
+    out: one bf16 rounding (2^-8 of the value); the softmax weight, the scale's factor and the value in fp16, 2^-11 each of
+    the weighted magnitudes, with 2^-11 more for the float32 exponential, sums and merge and for fp16 subnormals; a
+    score error e changes a weight by at most 2 e.
     lse: the score error, and 2^-20 for exponential, sum and logarithm with 2^-22 of its size."""
     ref, rl, weighted, e = dense_oracle.dense_decode(bits(q).reshape(q.shape), cache.cpu().numpy(), bt.cpu().numpy(),
                                                      lens.cpu().numpy(), sm_scale)

@@ -168,11 +168,15 @@ def test_lengths_outside_the_table():
     _check(q, cache, bt, lens, flags=_native.DEVERR_PAGE_RANGE)
 
 
-def test_latents_beyond_fp16_are_flagged():
+def test_latents_beyond_fp16():
+    # one position far beyond fp16's range beside ordinary ones, and scales that differ by 2^40 within one
     q, cache, bt, lens = make_dense([100], 16, seed=19, poison=False)
-    cache[int(bt[0, 0]), 3, 512:516] = torch.tensor([1000.0]).view(torch.uint8)   # 448 * 1000
-    out, lse, err = _run(torch.zeros_like(q), cache, bt, lens)
-    assert err == _native.DEVERR_RANGE and torch.isfinite(out.float()).all()
+    cache[int(bt[0, 0]), 3, 512:516] = torch.tensor([1000.0]).view(torch.uint8)        # up to 448 * 1000
+    cache[int(bt[0, 0]), 5, 512:528] = torch.tensor([1e-9, 1e3, 1e-3, 0.0]).view(torch.uint8)
+    _check(torch.zeros_like(q), cache, bt, lens)
+    q[:] = 0
+    q[:, :, 560] = 2.0
+    _check(q, cache, bt, lens)
 
 
 def test_cache_beyond_4_gib():
