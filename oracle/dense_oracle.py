@@ -9,8 +9,11 @@ row and whose physical page lies in the cache,
     s_t = sm_scale * q.k_t,  lse = ln sum exp(s_t),  out = sum exp(s_t - lse) v_t
 (out = 0 and lse = -inf without a position), with k and v of the cache record.
 
-Beside the result it gives two sizes that rounding-error bounds need:
+Beside the result it gives sizes that rounding-error bounds need:
     weighted   sum_t exp(s_t - lse) |v_t|
+    floor      the sum over tiles of 128 positions of (the tile's largest
+               exp(s_t - lse) 2^e_t) times sum_t |code_t|, with e_t the exponent of
+               the largest of a position's four scales
     score_err  a bound on the error of a score whose latent part multiplies the
                codes with q as two E4M3 terms and accumulates in float32, see
                score_error_bound.
@@ -19,12 +22,14 @@ from __future__ import annotations
 
 import numpy as np
 
-from .sparse_mla_oracle import D_LATENT, PAGE_SIZE, RECORD_BYTES, as_f64_q, dequantize_record
+from .sparse_mla_oracle import D_LATENT, PAGE_SIZE, RECORD_BYTES, as_f64_q, decode_record, dequantize_record
+
+TILE = 128
 
 
-def positions_rows(bt_row, n: int, num_pages: int) -> np.ndarray:
-    """Physical rows of positions 0 .. n - 1 (skipping those without a page)."""
-    rows = []
+def positions_rows(bt_row, n: int, num_pages: int):
+    """Physical rows of positions 0 .. n - 1 (skipping those without a page), and the positions."""
+    rows, pos = [], []
     for t in range(max(0, n)):
         lp = t // PAGE_SIZE
         if lp >= len(bt_row):
@@ -32,7 +37,8 @@ def positions_rows(bt_row, n: int, num_pages: int) -> np.ndarray:
         page = int(bt_row[lp])
         if 0 <= page < num_pages:
             rows.append(page * PAGE_SIZE + t % PAGE_SIZE)
-    return np.array(rows, dtype=np.int64)
+            pos.append(t)
+    return np.array(rows, dtype=np.int64), np.array(pos, dtype=np.int64)
 
 
 def score_error_bound(q: np.ndarray, k: np.ndarray, sm_scale: float) -> np.ndarray:
@@ -55,7 +61,7 @@ def score_error_bound(q: np.ndarray, k: np.ndarray, sm_scale: float) -> np.ndarr
 
 
 def dense_decode(q, kv_cache, block_table, seq_lens, sm_scale: float):
-    """(out [B, H, 512], lse [B, H], weighted [B, H, 512], score_err [B, H]) in float64."""
+    """(out [B, H, 512], lse [B, H], weighted [B, H, 512], floor [B, H, 512], score_err [B, H]) in float64."""
     qf = as_f64_q(q)
     cache = np.asarray(kv_cache, dtype=np.uint8)
     flat = cache.reshape(-1, RECORD_BYTES)
@@ -64,10 +70,11 @@ def dense_decode(q, kv_cache, block_table, seq_lens, sm_scale: float):
     s_q = B // bt.shape[0]
     out = np.zeros((B, H, D_LATENT))
     weighted = np.zeros((B, H, D_LATENT))
+    floor = np.zeros((B, H, D_LATENT))
     lse = np.full((B, H), -np.inf)
     score_err = np.zeros((B, H))
     for b in range(B):
-        rows = positions_rows(bt[b // s_q], int(seq_lens[b]), cache.shape[0])
+        rows, pos = positions_rows(bt[b // s_q], int(seq_lens[b]), cache.shape[0])
         if rows.size == 0:
             continue
         k = dequantize_record(flat[rows])
@@ -79,7 +86,13 @@ def dense_decode(q, kv_cache, block_table, seq_lens, sm_scale: float):
         out[b] = (e / z) @ k[:, :D_LATENT]
         weighted[b] = (e / z) @ np.abs(k[:, :D_LATENT])
         score_err[b] = score_error_bound(qf[b], k, sm_scale).max(axis=1)
-    return out, lse, weighted, score_err
+        codes, scales, _ = decode_record(flat[rows])
+        top = np.abs(scales).max(axis=1)
+        size = e / z * np.exp2(np.floor(np.log2(np.where(top > 0, top, 1.0))))
+        for tile in np.unique(pos // TILE):
+            at = pos // TILE == tile
+            floor[b] += size[:, at].max(axis=1)[:, None] * np.abs(codes[at]).sum(axis=0)
+    return out, lse, weighted, floor, score_err
 
 
 def read_records(kv_cache, block_table, positions, requests=None) -> np.ndarray:

@@ -15,17 +15,19 @@
 // about 2^-9 of the largest (their error is below 2^-17 of it, 2^-8 of that element's own bf16 rounding).  S^T of
 // a tile: M = 128 positions, N = 2 NR columns (hi rows, then lo rows), one accumulator per 128-dim scale block; the
 // softmax threads form s = 2^x sum_b (S_hi + S_lo) scale_b in fp32.  The rope part is a bf16 product.
-// Weights and values.  A position's scales are split as scale_b = m_b 2^e, e the exponent of the largest of the four;
-// V = fp16(code * m_b) (at most 896, one rounding) and the weight takes the power of two,
-//   P = 2^(s + e - ref) in fp16, l = sum P 2^-e in fp32, out = O / l, lse = ln 2 (ref + log2 l),
-// with ref = (a running maximum of s + e) - 7, moved only when s + e exceeds ref by more than 15: P stays below 2^15, and
-// contributions down to 2^-31 of the largest keep an absolute error below 2^-32 of it, so that a long tail
-// beside one dominating position is not lost and latents of any size fit.  O^T[512 x NR] += V^T P, M = 128 dims,
-// fp32 in TMEM.
+// Weights and values.  The codes are the values, too: O^T[512 x NR] += codes^T (P scale), with the same tile read
+// MN-major.  A position's scales are split as scale_b = m_b 2^e, e the exponent of the largest of the four, and the
+// weight takes the power of two: w = 2^(s + e - R), with R a row's maximum of s + e over the tile's 128
+// positions (rounded up) less 7, so that w m_b stays below 2^8.  Block b's operand is w m_b as two E4M3 terms, hi + lo:
+// 8 significant bits (off by 2^-9 at most) down to 2^-6 of that range and steps of 2^-9 below, so every
+// weight keeps an error below 2^-16 of the tile's largest and 2^-9 of itself.  A tile's O^T is added to fp32
+// accumulators in registers with the row's factor 2^(R - ref) (ref: R of the row's first tile), so tiles of
+// very different weight (a long tail beside one dominating position) lose nothing to one another.
+//   l = sum w 2^(R - ref - e) in fp32, out = O / l, lse = ln 2 (ref + log2 l).
 //
-// What bounds it: HBM bytes (656 per position) for up to 64 rows, where one SM's share of the HBM rate is a
-// tile per 1.9 us; inside an SM the shared-memory path, which a tile of 64 rows takes about 640 KB through
-// (84 in, 152 QK operands, 64 + 128 conversion, 192 PV operands, 16 P).
+// What bounds it: HBM bytes (656 per position) for up to 64 rows, where one SM's share of the HBM rate is a tile
+// per 1.9 us; inside an SM the shared-memory path, which a tile of 64 rows takes about 490 KB through (84 in, 152
+// QK operands, 64 P, 192 PV operands).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -42,65 +44,78 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRefBelowMax = 7.f;       // a new reference lies this far below the maximum it was taken from
-constexpr float kRefSlack = 15.f;         // a score this far above the reference moves it (2^15 is an fp16 value)
+constexpr float kTopWeight = 7.f;         // a tile's largest weight of a row lies in (2^6, 2^7]
+constexpr float kMaxFactor = 20.f;        // a tile's factor 2^(R - ref) above 2^20 moves ref
 
-// Warps: 0-7 softmax (warp w: TMEM lanes of quadrant w % 4, row half w / 4), 8-15 conversion (two groups of
-// four), then one warp each for the copies, the QK and the PV.
-constexpr int kSoftWarps = 8, kConvWarps = 8;
-constexpr int kCopyWarp = 16, kQkWarp = 17, kPvWarp = 18;
-constexpr int kDenseThreads = 20 * 32;     // five warpgroups; the last warp is idle
-constexpr int kSoftRegs = 128, kConvRegs = 88, kMiscRegs = 48;   // of 96 at launch: 2 x 128 + 2 x 88 + 48 = 5 x 96
+// Warps: 0-7 softmax (warp w: TMEM lanes of quadrant w % 4, row half w / 4), then one warp each for the copies,
+// the QK and the PV; the last one is idle.
+constexpr int kSoftWarps = 8;
+constexpr int kCopyWarp = 8, kQkWarp = 9, kPvWarp = 10;
+constexpr int kDenseThreads = 12 * 32;
+constexpr int kSoftRegs = 232, kMiscRegs = 40;   // of 168 at launch: 2 x 232 + 40 = 3 x 168
 
 constexpr uint32_t kSlot = 16384;         // 128 positions x 128 bytes: one code block or the rope of a tile
 constexpr int kChunks = 5;                // the four code blocks, then the rope
-constexpr int kSliceTokens = 16;          // positions of one V slice (one MMA K step)
-constexpr int kSlices = kDenseTile / kSliceTokens;
 constexpr int kScaleSlots = 3;
 
 template <int NR>
 struct DC {
-  static constexpr int kRing = 5;         // K slots
-  static constexpr int kVRing = 3;        // V slices
-  static constexpr int kSBufs = 2;        // score accumulators
+  static constexpr int kRing = NR == 64 ? 7 : NR == 32 ? 9 : 11;    // K slots
+  static constexpr int kPBufs = NR == 64 ? 2 : 4;                   // weights of so many blocks
+  static constexpr int kSBufs = NR == 64 ? 2 : 4;                   // score accumulators
+  // hi and lo weights meet in one accumulator for 64 rows (TMEM is full); for fewer rows they are one MMA of twice
+  // the columns and meet in the registers
+  static constexpr int kPasses = NR == 64 ? 2 : 1;
+  static constexpr int kOCols = NR == 64 ? NR : 2 * NR;             // columns of a block's O^T of one tile
+  // TMEM: O^T of one tile (kPBufs blocks at a time), score buffers, and for 64 rows, whose accumulators do not all fit
+  // the registers, those of blocks 0 and 1
+  static constexpr int kHeldBlocks = NR == 64 ? 2 : 0;
   static constexpr int HC = NR / 2;       // rows of one softmax thread
   static constexpr uint32_t kQ8Chunk = 2 * NR * 128;
   static constexpr uint32_t kQ8 = 0;
   static constexpr uint32_t kQr = kQ8 + 4 * kQ8Chunk;
   static constexpr uint32_t kK = (kQr + NR * 128 + 1023) / 1024 * 1024;
-  static constexpr uint32_t kV = kK + kRing * kSlot;
-  static constexpr uint32_t kP = kV + kVRing * kSlot;
-  static constexpr uint32_t kScale = kP + 128 * 2 * NR;
+  static constexpr int kPRow = 2 * NR;                            // bytes of a position's weights: hi, then lo
+  static constexpr uint32_t kPBuf = 128 * kPRow;
+  static constexpr uint32_t kP = kK + kRing * kSlot;
+  static constexpr uint32_t kScale = kP + kPBufs * kPBuf;
   static constexpr uint32_t kF = kScale + kScaleSlots * 2048;     // [2][NR] float
-  static constexpr uint32_t kLen = kF + 2 * NR * 4;           // [2][NR] int
-  static constexpr uint32_t kRef = kLen + 2 * NR * 4;             // [NR] float: minus the reference
-  static constexpr uint32_t kRed = kRef + NR * 4;                 // [5][NR] float
-  static constexpr uint32_t kBar = kRed + 5 * NR * 4;
+  static constexpr uint32_t kLen = kF + 2 * NR * 4;               // [2][NR] int
+  static constexpr uint32_t kRed = kLen + 2 * NR * 4;             // [4][NR] float
+  static constexpr uint32_t kRow = kRed + 4 * NR * 4;             // per softmax warp [HC] minus R, [HC] factor
+  static constexpr uint32_t kBar = kRow + kSoftWarps * 2 * HC * 4;
   static constexpr uint32_t kBytes = kBar + 512;
-  static constexpr uint32_t kTmemCols = 8 * NR;
-  static constexpr uint32_t kSCol = 4 * NR;                       // score buffer i at 4 NR + 2 NR i
-  static constexpr int kPRow = 2 * NR;
+  static constexpr uint32_t kSCol = kPBufs * kOCols;              // score buffer i at kSCol + 2 NR i
+  static constexpr uint32_t kHeld = kSCol + kSBufs * 2 * NR;      // accumulators of block b at kHeld + NR b
+  static constexpr uint32_t kTmemCols = kHeld + kHeldBlocks * NR;
   static_assert(kBytes <= 232448, "shared memory");
+  static_assert(kTmemCols == 512 || kTmemCols == 256, "TMEM allocations are powers of two");
 };
 
 struct Bars {
-  uint64_t kfull[8], kempty[8], vfull[4], vempty[4], sfull[2], sempty[2], scfull[4], scempty[4];
-  uint64_t pfull, pdone, qfull, drain[2];
+  uint64_t kfull[12], kempty[12], sfull[4], sempty[4], scfull[3], scempty[3];
+  uint64_t pfull[4], pempty[4], qfull, drain[2];
   uint32_t tmem;
   int abort;
-  int armed_k[8], armed_sc[4];            // copies armed so far per slot
-  int pages_ok[4];                        // of the tile in each scale slot: bit h: page h is loaded
+  int armed_k[12], armed_sc[3];            // copies armed so far per slot
+  int pages_ok[3];                        // of the tile in each scale slot: bit h: page h is loaded
   int first_item, first_tile, my_tiles;   // this CTA's run
   long long total;
 };
 static_assert(sizeof(Bars) <= 512, "barrier area");
 
-// One (request, row group).
-struct Item {
-  int req, row0, nrows;                   // rows row0 .. row0 + nrows - 1 of the request's s_q H rows
-  int max_len, min_len;                   // over the group's queries, clamped to [0, table]
-  int tiles;                              // at least 1: a group without positions has one empty tile
+// One (request, row group): rows row0 .. row0 + nrows - 1 of the request's s_q H rows.
+struct Rows {
+  int req, row0, nrows;
 };
+
+__device__ __forceinline__ Rows rows_of(const DenseParams& p, int i) {
+  Rows r;
+  r.req = i / p.groups;
+  r.row0 = (i - r.req * p.groups) * p.nr;
+  r.nrows = min(p.nr, p.q_per_req * p.H - r.row0);
+  return r;
+}
 
 __device__ __forceinline__ int clamped_len(const DenseParams& p, int b) {
   const long long table = (long long)p.max_pages * kPageSize;
@@ -108,22 +123,24 @@ __device__ __forceinline__ int clamped_len(const DenseParams& p, int b) {
   return (int)min(n, table);
 }
 
-__device__ __forceinline__ Item item_at(const DenseParams& p, int i) {
-  Item it;
-  it.req = i / p.groups;
-  const int rows = p.q_per_req * p.H;
-  it.row0 = (i - it.req * p.groups) * p.nr;
-  it.nrows = min(p.nr, rows - it.row0);
-  const int j0 = it.row0 / p.H, j1 = (it.row0 + it.nrows - 1) / p.H;
-  it.max_len = 0;
-  it.min_len = 0x7fffffff;
-  for (int j = j0; j <= j1; ++j) {
-    const int n = clamped_len(p, it.req * p.q_per_req + j);
-    it.max_len = max(it.max_len, n);
-    it.min_len = min(it.min_len, n);
+// Lengths of an item's queries (clamped to [0, table]) and its tiles: at least 1, so that a group without
+// positions has one empty tile.
+struct Lens {
+  int max_len, min_len, tiles;
+};
+
+__device__ __forceinline__ Lens lens_of(const DenseParams& p, const Rows& r) {
+  Lens n{0, 0x7fffffff, 0};
+  int b = r.req * p.q_per_req + r.row0 / p.H;
+  const int last = r.req * p.q_per_req + (r.row0 + r.nrows - 1) / p.H;
+#pragma unroll 1
+  for (; b <= last; ++b) {
+    const int len = clamped_len(p, b);
+    n.max_len = max(n.max_len, len);
+    n.min_len = min(n.min_len, len);
   }
-  it.tiles = max(1, (int)(((long long)it.max_len + kDenseTile - 1) / kDenseTile));
-  return it;
+  n.tiles = max(1, (int)(((long long)n.max_len + kDenseTile - 1) / kDenseTile));
+  return n;
 }
 
 // First tile of CTA c's run when T tiles are shared out over n CTAs.
@@ -137,20 +154,27 @@ struct RunDesc {
   int pad;
 };
 
-// Walks the (item, tile) pairs of a run; every role has its own.
+// Walks the (item, tile) pairs of a run; every role has its own:  while (w.here(p)) { ...; w.next(); }
 struct Walk {
   int i, t, left;
-  Item it;
-  __device__ __forceinline__ Walk(const DenseParams& p, const Bars* bars)
-      : i(bars->first_item), t(bars->first_tile), left(bars->my_tiles) {
-    if (left > 0) it = item_at(p, i);
+  bool entered = false;
+  Lens n;
+  __device__ __forceinline__ explicit Walk(const Bars* bars)
+      : i(bars->first_item), t(bars->first_tile), left(bars->my_tiles) {}
+  __device__ __forceinline__ bool here(const DenseParams& p) {
+    if (left > 0 && !entered) {
+      n = lens_of(p, rows_of(p, i));
+      entered = true;
+    }
+    return left > 0;
   }
-  __device__ __forceinline__ bool last_of_segment() const { return left == 1 || t == it.tiles - 1; }
-  __device__ __forceinline__ void next(const DenseParams& p) {
+  __device__ __forceinline__ bool last_of_segment() const { return left == 1 || t == n.tiles - 1; }
+  __device__ __forceinline__ void next() {
     --left;
-    if (++t == it.tiles && left > 0) {
+    if (++t == n.tiles) {
       t = 0;
-      it = item_at(p, ++i);
+      ++i;
+      entered = false;
     }
   }
 };
@@ -172,14 +196,19 @@ struct Ring {
 // phase yet reports the phase before its first as complete).
 // Once a wait has given up (ok false) a role runs its loop to the end without waiting, arriving or issuing, so
 // that the named barriers of the softmax warps stay matched.
-#define SMLA_WAIT(bar, par) \
-  if (ok) ok = ptx::mbar_wait_warp_small((bar), (par), &bars->abort, p.wait_ns)
+// (`ok` is passed through an empty asm: otherwise the compiler makes a copy of the rest of the role for each wait
+// that may give up, five hundred KB of code in all, and the instruction cache becomes the bound.)
+#define SMLA_WAIT(bar, par)                                                                        \
+  do {                                                                                             \
+    if (ok) ok = ptx::mbar_wait_warp_small((bar), (par), &bars->abort, p.wait_ns);                 \
+    asm volatile("" : "+r"(ok));                                                                   \
+  } while (0)
 
 // ----------------------------------------------------------------------------- copies
 
-__device__ __forceinline__ int page_entry(const DenseParams& p, const Item& it, int lp) {
-  return lp < p.max_pages && (long long)lp * kPageSize < it.max_len
-             ? __ldg(p.block_table + (size_t)it.req * p.max_pages + lp)
+__device__ __forceinline__ int page_entry(const DenseParams& p, int req, int max_len, int lp) {
+  return lp < p.max_pages && (long long)lp * kPageSize < max_len
+             ? __ldg(p.block_table + (size_t)req * p.max_pages + lp)
              : -1;
 }
 
@@ -187,34 +216,40 @@ template <int NR>
 __device__ void copy_role(const DenseParams& p, const CUtensorMap* map, const CUtensorMap* smap, uint32_t base,
                           Bars* bars, int lane) {
   using C = DC<NR>;
-  Walk w(p, bars);
+  Walk w(bars);
+  int req = 0;
   Ring<C::kRing> k;
   Ring<kScaleSlots> sc;
-  bool ok = true;
+  uint32_t ok = 1;
   // block-table entries of 16 tiles per load, one lane each, the next 16 tiles' already in flight
-  int cur = 0, nxt = 0, base_lp = -1;
-  while (w.left > 0) {
+  int cur = 0, nxt = 0, base_lp = 0, item = -1;
+#pragma unroll 1
+  while (w.here(p)) {
     const int lp = 2 * w.t;
-    if (base_lp < 0) {                                 // a new item
+    const bool enters = item != w.i;
+    if (enters) {
+      item = w.i;
+      const Rows r = rows_of(p, item);
+      req = r.req;
       base_lp = lp;
-      cur = page_entry(p, w.it, base_lp + lane);
-      nxt = page_entry(p, w.it, base_lp + 32 + lane);
+      nxt = page_entry(p, req, w.n.max_len, lp + lane);
       if (lane == 0) {
-        const int j0 = w.it.row0 / p.H, j1 = (w.it.row0 + w.it.nrows - 1) / p.H;
-        for (int j = j0; j <= j1; ++j)
-          if (__ldg(p.seq_lens + w.it.req * p.q_per_req + j) > (long long)p.max_pages * kPageSize)
-            atomicOr(p.err, SMLA_DEVERR_PAGE_RANGE);
+        const int last = req * p.q_per_req + (r.row0 + r.nrows - 1) / p.H;
+#pragma unroll 1
+        for (int b = req * p.q_per_req + r.row0 / p.H; b <= last; ++b)
+          if (__ldg(p.seq_lens + b) > (long long)p.max_pages * kPageSize) atomicOr(p.err, SMLA_DEVERR_PAGE_RANGE);
       }
-    } else if (lp == base_lp + 32) {
+    }
+    if (enters || lp == base_lp + 32) {
       base_lp = lp;
       cur = nxt;
-      nxt = page_entry(p, w.it, base_lp + 32 + lane);
+      nxt = page_entry(p, req, w.n.max_len, lp + 32 + lane);
     }
     const int pg[2] = {__shfl_sync(0xffffffffu, cur, lp - base_lp), __shfl_sync(0xffffffffu, cur, lp - base_lp + 1)};
     int good = 0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const bool used = (long long)(lp + h) * kPageSize < w.it.max_len;
+      const bool used = (long long)(lp + h) * kPageSize < w.n.max_len;
       const bool in_cache = pg[h] >= 0 && (int64_t)pg[h] < p.num_pages;
       if (used && in_cache) good |= 1 << h;
       if (used && !in_cache && lane == 0) atomicOr(p.err, SMLA_DEVERR_PAGE_RANGE);
@@ -246,9 +281,7 @@ __device__ void copy_role(const DenseParams& p, const CUtensorMap* map, const CU
       __syncwarp();
       k.next();
     }
-    const int was = w.i;
-    w.next(p);
-    if (w.i != was) base_lp = -1;
+    w.next();
   }
 }
 
@@ -266,14 +299,17 @@ template <int NR>
 __device__ void qk_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars* bars, int lane) {
   using C = DC<NR>;
   constexpr uint32_t kIdescCodes = ptx::idesc_e4m3(128, 2 * NR), kIdescRope = ptx::idesc_bf16(128, NR);
-  Walk w(p, bars);
+  Walk w(bars);
   Ring<C::kRing> k;
   Ring<C::kSBufs> s;
   uint32_t qpar = 0;
-  bool ok = true, new_item = true;
+  uint32_t ok = 1;
+  int item = -1;
   const uint64_t dq = ptx::sw128_desc(base + C::kQ8, 16, 1024), dr = ptx::sw128_desc(base + C::kQr, 16, 1024);
-  while (w.left > 0) {
-    if (new_item) {
+#pragma unroll 1
+  while (w.here(p)) {
+    if (item != w.i) {
+      item = w.i;
       SMLA_WAIT(&bars->qfull, qpar);
       qpar ^= 1;
     }
@@ -282,27 +318,25 @@ __device__ void qk_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars
       SMLA_WAIT(&bars->sempty[s.slot], s.parity ^ 1);
       SMLA_WAIT(&bars->kfull[k.slot], k.parity);
       ptx::tc_fence_after();
+      const uint32_t ks = k.slot, d = tmem + C::kSCol + 2 * NR * s.slot, cu = c;
       if (ok && ptx::elect_one()) {
-        const uint64_t dk = ptx::sw128_desc(base + C::kK + k.slot * kSlot, 16, 1024);
-        const uint32_t d = tmem + C::kSCol + 2 * NR * s.slot;
+        const uint64_t dk = ptx::sw128_desc(base + C::kK + ks * kSlot, 16, 1024);
         if (c == 4) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) ptx::mma_f16_ss(d, dk + 2 * kk, dr + 2 * kk, kIdescRope, kk > 0);
         } else {
-          const uint64_t dqb = dq + (uint64_t)((c * C::kQ8Chunk) >> 4);
+          const uint64_t dqb = dq + (uint64_t)((cu * C::kQ8Chunk) >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) ptx::mma_f8_ss(d, dk + 2 * kk, dqb + 2 * kk, kIdescCodes, kk > 0);
         }
-        ptx::mma_commit(&bars->kempty[k.slot]);
+        if (c == 4) ptx::mma_commit(&bars->kempty[k.slot]);   // the codes stay for the PV
         ptx::mma_commit(&bars->sfull[s.slot]);
       }
       __syncwarp();
       k.next();
       s.next();
     }
-    const int was = w.i;
-    w.next(p);
-    new_item = w.i != was;
+    w.next();
   }
   if (ptx::elect_one()) ptx::mma_commit(&bars->drain[0]);
   __syncwarp();
@@ -311,138 +345,41 @@ __device__ void qk_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars
 template <int NR>
 __device__ void pv_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars* bars, int lane) {
   using C = DC<NR>;
-  constexpr uint32_t kIdesc = ptx::idesc_f16(128, NR, 1, 1);
-  Walk w(p, bars);
-  Ring<C::kVRing> v;
-  uint32_t ppar = 0;
-  bool ok = true, first = true;
-  const uint64_t dp = ptx::swz_desc(base + C::kP, 8 * C::kPRow, 8 * C::kPRow, C::kPRow);
-  while (w.left > 0) {
-    SMLA_WAIT(&bars->pfull, ppar);
-    ppar ^= 1;
+  constexpr int N = C::kOCols;
+  constexpr uint32_t kIdesc = ptx::idesc_e4m3(128, N) | (1u << 15) | (1u << 16);     // A and B MN-major
+  Walk w(bars);
+  Ring<C::kRing> k;
+  Ring<C::kPBufs> pb;
+  uint32_t ok = 1;
 #pragma unroll 1
-    for (int s = 0; s < kSlices; ++s) {
-      SMLA_WAIT(&bars->vfull[v.slot], v.parity);
+  while (w.here(p)) {
+#pragma unroll 1
+    for (int b = 0; b < 4; ++b) {
+      SMLA_WAIT(&bars->pfull[pb.slot], pb.parity);
       ptx::tc_fence_after();
+      const uint32_t ks = k.slot, ps = pb.slot, d = tmem + N * pb.slot;
       if (ok && ptx::elect_one()) {
-        const uint64_t dv = ptx::sw128_desc(base + C::kV + v.slot * kSlot, 2048, 1024);
-        const uint64_t dps = dp + (uint64_t)(s * C::kPRow);
+        // codes^T: 128-byte rows of one position, 8-position groups 1024 bytes apart; 32 positions per MMA
+        const uint64_t dv = ptx::sw128_desc(base + C::kK + ks * kSlot, 1024, 1024);
+        const uint64_t dp = ptx::swz_desc(base + C::kP + ps * C::kPBuf, 8 * C::kPRow, 8 * C::kPRow, C::kPRow);
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
-          ptx::mma_f16_ss(tmem + NR * b, dv + (uint64_t)(256 * b), dps, kIdesc, !(first && s == 0));
-        ptx::mma_commit(&bars->vempty[v.slot]);
-        if (s == kSlices - 1) ptx::mma_commit(&bars->pdone);
+        for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+          for (int pass = 0; pass < C::kPasses; ++pass)
+            ptx::mma_f8_ss(d, dv + (uint64_t)(256 * kk),
+                           dp + (uint64_t)((32 * C::kPRow * kk + NR * pass) >> 4), kIdesc, kk > 0 || pass > 0);
+        ptx::mma_commit(&bars->kempty[k.slot]);
+        ptx::mma_commit(&bars->pempty[pb.slot]);
       }
       __syncwarp();
-      v.next();
+      k.next();
+      pb.next();
     }
-    first = w.last_of_segment();
-    w.next(p);
+    k.next();                                             // the rope
+    w.next();
   }
   if (ptx::elect_one()) ptx::mma_commit(&bars->drain[1]);
   __syncwarp();
-}
-
-// ----------------------------------------------------------------------------- conversion
-
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, __half2 b) {
-  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), b);
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-// 16 codes of one 128-dim block times its factor, as fp16.
-__device__ __forceinline__ void convert16(uint4 codes, __half2 m, uint32_t (&o)[8]) {
-  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    o[2 * i] = hmul2(e4m3x2_to_f16x2((uint16_t)(w[i] & 0xffffu)), m);
-    o[2 * i + 1] = hmul2(e4m3x2_to_f16x2((uint16_t)(w[i] >> 16)), m);
-  }
-}
-
-// NaNs to numbers, for positions that some row does not see: their weight 0 must give 0.  (A row that does
-// see a NaN code or scale has a NaN score, so it is NaN whatever the value.)
-__device__ __forceinline__ void no_nan(uint32_t (&o)[8]) {
-  const __half2 top = __float2half2_rn(65504.f);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const __half2 c = __hmin2(*reinterpret_cast<const __half2*>(&o[i]), top);
-    o[i] = *reinterpret_cast<const uint32_t*>(&c);
-  }
-}
-
-// The exponent e that a position's weight takes from its scales.
-__device__ __forceinline__ int scale_exponent(const float4& s) {
-  const float top = fmaxf(fmaxf(fabsf(s.x), fabsf(s.y)), fmaxf(fabsf(s.z), fabsf(s.w)));
-  return min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 100);
-}
-__device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
-
-// Group g converts slices g, g + 2, g + 4, g + 6 of a tile: lane -> position (lane & 15) of the slice, 16-dim
-// unit 2 (warp % 4) + lane / 16 of every 128-dim block.  A warp reads its part of each code block into
-// registers as it lands (which frees the slot for the next tile's copy), then writes slice by slice.
-template <int NR>
-__device__ void convert_role(const DenseParams& p, uint32_t base, Bars* bars, int warp, int lane) {
-  using C = DC<NR>;
-  const int group = (warp - kSoftWarps) >> 2;
-  const int tok = lane & 15, unit = 2 * (warp & 3) + (lane >> 4);
-  Walk w(p, bars);
-  Ring<C::kRing> k;
-  Ring<kScaleSlots> sc;
-  Ring<C::kVRing> v;
-  if (group) v.next();
-  bool ok = true;
-  while (w.left > 0) {
-    uint4 codes[4][4];
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      SMLA_WAIT(&bars->kfull[k.slot], k.parity);
-      const uint32_t slot = base + C::kK + k.slot * kSlot;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        codes[b][j] = ptx::lds128(slot + swz128((2 * j + group) * kSliceTokens + tok, unit));
-      __syncwarp();
-      if (ok && lane == 0) ptx::mbar_arrive(&bars->kempty[k.slot]);
-      k.next();
-    }
-    SMLA_WAIT(&bars->kfull[k.slot], k.parity);         // the rope: nothing to read
-    if (ok && lane == 0) ptx::mbar_arrive(&bars->kempty[k.slot]);
-    k.next();
-    SMLA_WAIT(&bars->scfull[sc.slot], sc.parity);
-    const int pages = bars->pages_ok[sc.slot];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int row = (2 * j + group) * kSliceTokens + tok;
-      const long long t = (long long)w.t * kDenseTile + row;
-      const bool valid = t < w.it.max_len && (pages >> (row >> 6) & 1);
-      const float4 s4 = ptx::lds128f(base + C::kScale + sc.slot * 2048 + row * 16);
-      const float down = valid ? exp2_int(-scale_exponent(s4)) : 0.f;
-      const float scale[4] = {s4.x, s4.y, s4.z, s4.w};
-      __half2 m[4];
-#pragma unroll
-      for (int b = 0; b < 4; ++b) m[b] = __float2half2_rn(fminf(fmaxf(scale[b] * down, -2.f), 2.f));
-      const bool partly = !valid || t >= w.it.min_len;
-      SMLA_WAIT(&bars->vempty[v.slot], v.parity ^ 1);
-      const uint32_t dst = base + C::kV + v.slot * kSlot;
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        uint32_t o[8];
-        convert16(codes[b][j], m[b], o);
-        if (__builtin_expect(partly, 0)) no_nan(o);
-        const uint32_t chunk = dst + (2 * b + (unit >> 2)) * 2048;
-        ptx::sts128_async_only(chunk + swz128(tok, (unit & 3) * 2), make_uint4(o[0], o[1], o[2], o[3]));
-        ptx::sts128_async_only(chunk + swz128(tok, (unit & 3) * 2 + 1), make_uint4(o[4], o[5], o[6], o[7]));
-      }
-      ptx::fence_proxy_async_smem();
-      __syncwarp();
-      if (ok && lane == 0) ptx::mbar_arrive(&bars->vfull[v.slot]);
-      v.next();
-      v.next();
-    }
-    if (ok && lane == 0) ptx::mbar_arrive(&bars->scempty[sc.slot]);
-    sc.next();
-    w.next(p);
-  }
 }
 
 // ----------------------------------------------------------------------------- softmax
@@ -466,11 +403,14 @@ __device__ __forceinline__ float reduce_scatter(float (&v)[N], int lane, Op op) 
   return r;
 }
 
+__device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
 // Rows of one item into the Q operands: hi and lo E4M3 codes of the latent part scaled by 2^-x, the rope as it is;
 // each row's factor 2^x sm_scale log2 e and length go to buffer `buf`.
 template <int NR>
-__device__ void load_q(const DenseParams& p, const Item& it, unsigned char* sm, uint32_t base, int buf, int warp, int lane) {
+__device__ __forceinline__ void load_q(const DenseParams& p, int item, unsigned char* sm, uint32_t base, int buf, int warp, int lane) {
   using C = DC<NR>;
+  const Rows it = rows_of(p, item);
   float* f = reinterpret_cast<float*>(sm + C::kF) + buf * NR;
   int* lens = reinterpret_cast<int*>(sm + C::kLen) + buf * NR;
   const float kf = p.sm_scale * kLog2e;
@@ -517,96 +457,271 @@ __device__ void load_q(const DenseParams& p, const Item& it, unsigned char* sm, 
     if (lane < 8) ptx::sts128(base + C::kQr + swz128(r, lane), rope);
     if (lane == 0) {
       f[r] = exp2_int(x) * kf;
-      lens[r] = r < it.nrows ? clamped_len(p, it.req * p.q_per_req + (it.row0 + r) / p.H) : it.max_len;
+      lens[r] = r < it.nrows ? clamped_len(p, it.req * p.q_per_req + (it.row0 + r) / p.H) : 0x7fffffff;
     }
   }
 }
 
-template <int NR>
-__device__ __forceinline__ void tmem_ld(uint32_t a, uint32_t (&r)[NR]) {
-  if constexpr (NR == 32) ptx::tmem_ld32(a, r);
-  else if constexpr (NR == 16) ptx::tmem_ld16(a, r);
-  else ptx::tmem_ld8(a, r);
-}
 template <int NR>
 __device__ __forceinline__ void tmem_st(uint32_t a, const uint32_t (&r)[NR]) {
   if constexpr (NR == 32) ptx::tmem_st32(a, r);
   else if constexpr (NR == 16) ptx::tmem_st16(a, r);
   else ptx::tmem_st8(a, r);
 }
+template <int NR>
+__device__ __forceinline__ void tmem_ld(uint32_t a, uint32_t (&r)[NR]) {
+  if constexpr (NR == 32) ptx::tmem_ld32(a, r);
+  else if constexpr (NR == 16) ptx::tmem_ld16(a, r);
+  else ptx::tmem_ld8(a, r);
+}
+// The exponent e that a position's weights take from its scales.
+__device__ __forceinline__ int scale_exponent(const float4& s) {
+  const float top = fmaxf(fmaxf(fabsf(s.x), fabsf(s.y)), fmaxf(fabsf(s.z), fabsf(s.w)));
+  return min(max((int)(__float_as_uint(top) >> 23) - 127, -60), 100);
+}
+
+// Two fp16 values -> two E4M3 codes (round to nearest even, saturating).
+__device__ __forceinline__ uint16_t f16x2_to_e4m3x2(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+
+// Makes the codes of positions that some row does not see harmless for the PV (a weight of 0 must give 0):
+// NaN codes become 0, and every code of a position that no row sees.  (A row that does see a NaN code has a NaN
+// score, so it is NaN whatever the value.)  Threads of half h take blocks 2 h, 2 h + 1.
+template <int NR>
+__device__ __noinline__ void clean_codes(uint32_t base, int slot, int tok, int half, bool seen) {
+  using C = DC<NR>;
+#pragma unroll 1
+  for (int b = 0; b < 4; ++b) {
+    if (b >> 1 == half) {
+      const uint32_t at = base + C::kK + slot * kSlot;
+#pragma unroll 1
+      for (int u = 0; u < 8; ++u) {
+        uint4 v = ptx::lds128(at + swz128(tok, u));
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = seen ? w[i] & ~__vcmpeq4(w[i] & 0x7f7f7f7fu, 0x7f7f7f7fu) : 0u;
+        ptx::sts128(at + swz128(tok, u), make_uint4(w[0], w[1], w[2], w[3]));
+      }
+    }
+    if (++slot == C::kRing) slot = 0;
+  }
+}
 
 template <int NR>
 __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t base, uint32_t tmem, Bars* bars, int warp,
                              int lane, float* o_part, float* lse_part) {
   using C = DC<NR>;
-  constexpr int HC = C::HC, LC = HC < 16 ? HC : 16;     // rows per thread, columns per TMEM load
+  constexpr int HC = C::HC, LC = HC;// rows per thread, columns per TMEM load
   const int half = warp >> 2, quad = warp & 3, col0 = half * HC;
   const int tok = 32 * quad + lane;
   const uint32_t lane_base = tmem + ((uint32_t)(32 * quad) << 16);
   const float kf = p.sm_scale * kLog2e;
-  float* nref = reinterpret_cast<float*>(sm + C::kRef) + col0;  // minus the reference
-  float* red = reinterpret_cast<float*>(sm + C::kRed) + col0;   // [5][NR]
-  Walk w(p, bars);
+  float* red = reinterpret_cast<float*>(sm + C::kRed) + col0;   // [4][NR]
+  const uint32_t row_nr = base + C::kRow + warp * 2 * HC * 4, row_c = row_nr + HC * 4;
+  Walk w(bars);
   Ring<C::kSBufs> s;
   Ring<kScaleSlots> sc;
+  int kslot = 0, pslot = 0;
   uint32_t dpar = 0;
-  bool ok = true, first = true, fresh = true, begins = w.t == 0;
+  uint32_t ok = 1;
+  bool first = true, begins = w.t == 0;
   int buf = 0;
-  uint64_t l[HC / 2];                                   // row sums over this thread's positions, pairs of rows
-  if (w.left > 0) {
-    load_q<NR>(p, w.it, sm, base, 0, warp, lane);
-    ptx::fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(&bars->qfull);
-    ptx::named_bar_sync(3, kSoftWarps * 32);            // every row's factors and lengths are written
-  }
-  while (w.left > 0) {
-    if (first) {
+  // O of dim 128 b + tok, pairs of rows: blocks from kHeldBlocks on (the others are held in TMEM)
+  uint64_t o[4 - C::kHeldBlocks][HC / 2];
+  uint64_t l[HC / 2];                                   // row sums over this thread's positions
+  float ref = CUDART_NAN_F;                             // of row col0 + lane; NaN: the row has met no position
+
+  // Block b's O^T of one tile (pairs of rows); with `held`, its accumulators from TMEM in the same wait.
+  auto tile_part = [&](int b, uint64_t (&x)[HC / 2], uint32_t (&held)[HC], bool load_held) {
+    uint32_t hi[HC], lo[HC];
+    const uint32_t a = lane_base + C::kOCols * (b % C::kPBufs) + col0;
+    tmem_ld<HC>(a, hi);
+    if constexpr (C::kPasses == 1) tmem_ld<HC>(a + NR, lo);
+    if (load_held) tmem_ld<HC>(lane_base + C::kHeld + NR * b + col0, held);
+    ptx::tmem_wait_ld();
 #pragma unroll
-      for (int i = 0; i < HC / 2; ++i) l[i] = 0;
-      fresh = true;
+    for (int i = 0; i < HC / 2; ++i) {
+      x[i] = ptx::pack2(hi[2 * i], hi[2 * i + 1]);
+      if constexpr (C::kPasses == 1) x[i] = ptx::add2(x[i], ptx::pack2(lo[2 * i], lo[2 * i + 1]));
+    }
+  };
+  auto wait_pv = [&](int b, uint32_t parity) {
+    SMLA_WAIT(&bars->pempty[b % C::kPBufs], parity);
+    ptx::tc_fence_after();
+  };
+  // adds a tile's blocks that are kept in registers (the PV of the tile before, see below)
+  auto flush_registers = [&]() {
+#pragma unroll
+    for (int b = C::kHeldBlocks; b < 4; ++b) {
+      wait_pv(b, C::kHeldBlocks ? 1u : dpar);
+      uint64_t x[HC / 2];
+      uint32_t none[HC];
+      tile_part(b, x, none, false);
+#pragma unroll
+      for (int i = 0; i < HC / 2; i += 2) {
+        const ulonglong2 c = ptx::lds128_pairs(row_c + i * 8);
+        uint64_t* d = &o[b - C::kHeldBlocks][i];
+        d[0] = ptx::fma2(x[i], c.x, d[0]);
+        d[1] = ptx::fma2(x[i + 1], c.y, d[1]);
+      }
+    }
+    dpar ^= 1;
+    ptx::tc_fence_before();
+  };
+  // adds block b (held in TMEM); `start`: the segment's first tile
+  auto flush_held = [&](int b, bool start) {
+    wait_pv(b, 0u);
+    uint64_t x[HC / 2];
+    uint32_t h[HC];
+    tile_part(b, x, h, true);                           // (before the segment's first tile: whatever was there)
+#pragma unroll
+    for (int i = 0; i < HC / 2; i += 2) {
+      const ulonglong2 c = ptx::lds128_pairs(row_c + i * 8);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint64_t before = start ? 0 : ptx::pack2(h[2 * (i + j)], h[2 * (i + j) + 1]);
+        const float2 d = ptx::unpack2(ptx::fma2(x[i + j], j ? c.y : c.x, before));
+        h[2 * (i + j)] = __float_as_uint(d.x);
+        h[2 * (i + j) + 1] = __float_as_uint(d.y);
+      }
+    }
+    tmem_st<HC>(lane_base + C::kHeld + NR * b + col0, h);
+    ptx::tmem_wait_st();
+    ptx::tc_fence_before();
+  };
+
+  int item = -1, done = -1;                             // items whose rows are loaded, whose segment has ended
+  bool whole = false;                                   // the segment is its whole item
+#pragma unroll 1
+  for (;;) {
+    const bool more = w.here(p);
+    if (more && item != w.i) {
+      // the next item's rows, so that its scores can start beside the last one's PV
+      done = item;
+      item = w.i;
+      buf ^= 1;
+      load_q<NR>(p, item, sm, base, buf, warp, lane);
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (ok && lane == 0) ptx::mbar_arrive(&bars->qfull);
+    }
+    if (!more) done = item;
+    if (first && done >= 0) {
+      const Rows it = rows_of(p, done);
+      flush_registers();
+      // row sums over the tile's 128 positions
+      float ls[HC];
+#pragma unroll
+      for (int i = 0; i < HC / 2; ++i) {
+        const float2 x = ptx::unpack2(l[i]);
+        ls[2 * i] = x.x;
+        ls[2 * i + 1] = x.y;
+      }
+      const float sum = reduce_scatter<HC>(ls, lane, [](float a, float b) { return a + b; });
+      ptx::named_bar_sync(1 + half, 128);                 // the maxima have been read
+      if (lane < HC) red[quad * NR + lane] = sum;
+      ptx::named_bar_sync(1 + half, 128);
+      // a run's first segment that continues an item goes to slot 0 of the CTA, its last segment to slot 1
+      const size_t slot = 2 * (size_t)blockIdx.x + (begins ? 1 : 0);
+      float inv = 0.f;
+      if (lane < HC) {
+        const float z = red[lane] + red[NR + lane] + red[2 * NR + lane] + red[3 * NR + lane];
+        inv = z > 0.f ? 1.f / z : (z == 0.f ? 0.f : CUDART_NAN_F);
+        const float lse = z == 0.f ? -CUDART_INF_F : (log2f(z) + ref) * kLn2;
+        if (quad == 0 && ok && col0 + lane < it.nrows) {
+          if (whole) p.lse[(size_t)it.req * p.q_per_req * p.H + it.row0 + col0 + lane] = lse;
+          else lse_part[slot * NR + col0 + lane] = lse;
+        }
+      }
+      // lanes 2j, 2j + 1 hold dims d, d + 1 of two rows: the first ends with both dims of the first row, the other
+      // with both of the second
+      const bool second = lane & 1;
+      const size_t row0 = whole ? (size_t)it.req * p.q_per_req * p.H + it.row0 : slot * NR;
+      auto write_pair = [&](int b, int i, float2 x) {
+        const float va = x.x * __shfl_sync(0xffffffffu, inv, i), vb = x.y * __shfl_sync(0xffffffffu, inv, i + 1);
+        const float got = __shfl_xor_sync(0xffffffffu, second ? va : vb, 1);
+        const float d0 = second ? got : va, d1 = second ? vb : got;
+        const int c = col0 + i + (second ? 1 : 0);
+        if (ok && c < it.nrows) {
+          const size_t at = (row0 + c) * kDLatent + 128 * b + (tok & ~1);
+          if (whole) *reinterpret_cast<uint32_t*>(p.out + at) = f32x2_to_bf16x2(d0, d1);
+          else *reinterpret_cast<float2*>(o_part + at) = make_float2(d0, d1);
+        }
+      };
+#pragma unroll
+      for (int b = C::kHeldBlocks; b < 4; ++b)
+#pragma unroll
+        for (int i = 0; i < HC; i += 2) write_pair(b, i, ptx::unpack2(o[b - C::kHeldBlocks][i / 2]));
+#pragma unroll 1
+      for (int b = 0; b < C::kHeldBlocks; ++b)
+#pragma unroll 1
+        for (int i0 = 0; i0 < HC; i0 += 8) {
+          uint32_t h[8];
+          ptx::tmem_ld8(lane_base + C::kHeld + NR * b + col0 + i0, h);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) write_pair(b, i0 + i, make_float2(__uint_as_float(h[i]), __uint_as_float(h[i + 1])));
+        }
+      begins = true;
+    }
+    if (!more) break;
+    if (first) {
+      ptx::named_bar_sync(3, kSoftWarps * 32);          // red is free, the rows' factors and lengths are written
+#pragma unroll
+      for (int i = 0; i < HC / 2; ++i) {
+        l[i] = 0;
+#pragma unroll
+        for (int b = 0; b < 4 - C::kHeldBlocks; ++b) o[b][i] = 0;
+      }
+      ref = CUDART_NAN_F;
     }
     // scores of this thread's position for its HC rows, in units of log2
     SMLA_WAIT(&bars->scfull[sc.slot], sc.parity);
-    float4 s4 = ptx::lds128f(base + C::kScale + sc.slot * 2048 + tok * 16);
+    const float4 s4 = ptx::lds128f(base + C::kScale + sc.slot * 2048 + tok * 16);
     const int pages = bars->pages_ok[sc.slot];
     __syncwarp();
     if (ok && lane == 0) ptx::mbar_arrive(&bars->scempty[sc.slot]);
     sc.next();
     const int e = scale_exponent(s4);
     uint64_t acc[HC / 2];                               // pairs of rows
+    {
+      float4 rot = s4;
 #pragma unroll
-    for (int i = 0; i < HC / 2; ++i) acc[i] = 0;
+      for (int i = 0; i < HC / 2; ++i) acc[i] = 0;
 #pragma unroll 1
-    for (int b = 0; b < 4; ++b) {
-      SMLA_WAIT(&bars->sfull[s.slot], s.parity);
-      ptx::tc_fence_after();
-      const uint32_t a = lane_base + C::kSCol + 2 * NR * s.slot + col0;
-      const uint64_t scale = ptx::pack2(s4.x, s4.x);
-      s4 = make_float4(s4.y, s4.z, s4.w, s4.x);
+      for (int b = 0; b < 4; ++b) {
+        SMLA_WAIT(&bars->sfull[s.slot], s.parity);
+        ptx::tc_fence_after();
+        const uint32_t a = lane_base + C::kSCol + 2 * NR * s.slot + col0;
+        const uint64_t scale = ptx::pack2(rot.x, rot.x);
+        rot = make_float4(rot.y, rot.z, rot.w, rot.x);
 #pragma unroll
-      for (int i0 = 0; i0 < HC; i0 += LC) {
-        uint32_t hi[LC], lo[LC];
-        tmem_ld<LC>(a + i0, hi);
-        tmem_ld<LC>(a + NR + i0, lo);
-        ptx::tmem_wait_ld();
+        for (int i0 = 0; i0 < HC; i0 += LC) {
+          uint32_t hi[LC], lo[LC];
+          tmem_ld<LC>(a + i0, hi);
+          tmem_ld<LC>(a + NR + i0, lo);
+          ptx::tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < LC; i += 2)
-          acc[(i0 + i) / 2] = ptx::fma2(ptx::add2(ptx::pack2(hi[i], hi[i + 1]), ptx::pack2(lo[i], lo[i + 1])), scale,
-                                        acc[(i0 + i) / 2]);
+          for (int i = 0; i < LC; i += 2)
+            acc[(i0 + i) / 2] = ptx::fma2(ptx::add2(ptx::pack2(hi[i], hi[i + 1]), ptx::pack2(lo[i], lo[i + 1])), scale,
+                                          acc[(i0 + i) / 2]);
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (ok && lane == 0) ptx::mbar_arrive(&bars->sempty[s.slot]);
+        s.next();
       }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (ok && lane == 0) ptx::mbar_arrive(&bars->sempty[s.slot]);
-      s.next();
     }
-    // s + e - ref, as 2^x (latent part) + (rope part sm_scale log2 e) + (e - ref)
+    // s + e, as 2^x (latent part) + (rope part sm_scale log2 e + e)
     SMLA_WAIT(&bars->sfull[s.slot], s.parity);
     ptx::tc_fence_after();
     {
       const uint32_t a = lane_base + C::kSCol + 2 * NR * s.slot + col0;
       const uint64_t kf2 = ptx::pack2(kf, kf), e2 = ptx::pack2((float)e, (float)e);
-      const uint32_t fa = base + C::kF + (buf * NR + col0) * 4, ra = base + C::kRef + col0 * 4;
+      const uint32_t fa = base + C::kF + (buf * NR + col0) * 4;
 #pragma unroll
       for (int i0 = 0; i0 < HC; i0 += LC) {
         uint32_t r[LC];
@@ -615,11 +730,9 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
 #pragma unroll
         for (int i = 0; i < LC; i += 4) {
           const ulonglong2 f = ptx::lds128_pairs(fa + (i0 + i) * 4);
-          ulonglong2 off = ptx::lds128_pairs(ra + (i0 + i) * 4);
-          if (fresh) off.x = off.y = 0;
           uint64_t* d = &acc[(i0 + i) / 2];
-          d[0] = ptx::fma2(d[0], f.x, ptx::fma2(ptx::pack2(r[i], r[i + 1]), kf2, ptx::add2(off.x, e2)));
-          d[1] = ptx::fma2(d[1], f.y, ptx::fma2(ptx::pack2(r[i + 2], r[i + 3]), kf2, ptx::add2(off.y, e2)));
+          d[0] = ptx::fma2(d[0], f.x, ptx::fma2(ptx::pack2(r[i], r[i + 1]), kf2, e2));
+          d[1] = ptx::fma2(d[1], f.y, ptx::fma2(ptx::pack2(r[i + 2], r[i + 3]), kf2, e2));
         }
       }
     }
@@ -628,8 +741,8 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
     if (ok && lane == 0) ptx::mbar_arrive(&bars->sempty[s.slot]);
     s.next();
     // positions that a row may not see
-    const long long t = (long long)w.t * kDenseTile + tok;
-    if (__builtin_expect((long long)(w.t + 1) * kDenseTile > w.it.min_len || pages != 3, 0)) {
+    if (__builtin_expect((long long)(w.t + 1) * kDenseTile > w.n.min_len || pages != 3, 0)) {
+      const long long t = (long long)w.t * kDenseTile + tok;
       const int* lens = reinterpret_cast<const int*>(sm + C::kLen) + buf * NR + col0;
       const bool here = pages >> (tok >> 6) & 1;
 #pragma unroll
@@ -639,20 +752,12 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
         if (!here || t >= lens[i + 1]) d.y = -CUDART_INF_F;
         acc[i / 2] = ptx::pack2(d.x, d.y);
       }
+      if (!here || t >= w.n.min_len) clean_codes<NR>(base, kslot, tok, half, here && t < w.n.max_len);
     }
-    // the reference moves when a contribution lies more than kRefSlack above it
-    float top = -CUDART_INF_F;
-#pragma unroll
-    for (int i = 0; i < HC / 2; ++i) {
-      const float2 d = ptx::unpack2(acc[i]);
-      top = fmaxf(top, fmaxf(d.x, d.y));
-    }
-    const bool move = ptx::named_bar_or(1 + half, 128, fresh || top > kRefSlack);
-    if (!first) {                                       // P and O are free once the tile before is done
-      SMLA_WAIT(&bars->pdone, dpar);
-      dpar ^= 1;
-    }
-    if (__builtin_expect(move, 0)) {
+    kslot = kslot + kChunks >= C::kRing ? kslot + kChunks - C::kRing : kslot + kChunks;
+    if (!first) flush_registers();
+    // R of each row: every warp ends with its rows' maxima over the 128 positions, lane -> row
+    {
       float v[HC];
 #pragma unroll
       for (int i = 0; i < HC / 2; ++i) {
@@ -662,138 +767,117 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
       }
       const float m = reduce_scatter<HC>(v, lane, [](float a, float b) { return fmaxf(a, b); });
       if (lane < HC) red[quad * NR + lane] = m;
-      ptx::named_bar_sync(1 + half, 128);
-      // by how much row `lane`'s reference rises (or, for the first positions it meets, is set)
-      float up = 0.f;
-      if (lane < HC) {
-        const float most = fmaxf(fmaxf(red[lane], red[NR + lane]), fmaxf(red[2 * NR + lane], red[3 * NR + lane]));
-        if (most > (fresh ? -CUDART_INF_F : kRefSlack)) up = most - kRefBelowMax;
-        if (quad == 0) red[4 * NR + lane] = (fresh ? 0.f : nref[lane]) - up;
+    }
+    ptx::named_bar_sync(1 + half, 128);
+    float back = 1.f;                                   // what a reference that moves takes from the sums so far
+    if (lane < HC) {
+      const float m = fmaxf(fmaxf(red[lane], red[NR + lane]), fmaxf(red[2 * NR + lane], red[3 * NR + lane]));
+      float r = 0.f, c = 1.f;
+      if (m > -CUDART_INF_F) {                          // not a row without positions here, or of NaNs alone
+        r = ceilf(m) - kTopWeight;
+        if (!(ref == ref)) ref = r;
+        if (r - ref > kMaxFactor) {
+          back = ptx::ex2_approx(ref - r);
+          ref = r;
+        }
+        c = ptx::ex2_approx(r - ref);
       }
-      ptx::named_bar_sync(1 + half, 128);
-      if (quad == 0 && lane < HC) nref[lane] = red[4 * NR + lane];
-      const float factor = ptx::ex2_approx(-up);
+      ptx::sts32f(row_nr + lane * 4, -r);
+      ptx::sts32f(row_c + lane * 4, c);
+    }
+    if (__builtin_expect(__any_sync(0xffffffffu, back != 1.f), 0)) {
 #pragma unroll
       for (int i = 0; i < HC / 2; ++i) {
-        const float2 d = ptx::unpack2(acc[i]);
-        acc[i] = ptx::pack2(d.x - __shfl_sync(0xffffffffu, up, 2 * i), d.y - __shfl_sync(0xffffffffu, up, 2 * i + 1));
+        const uint64_t f = ptx::pack2(__shfl_sync(0xffffffffu, back, 2 * i), __shfl_sync(0xffffffffu, back, 2 * i + 1));
+        l[i] = ptx::mul2(l[i], f);
+#pragma unroll
+        for (int b = 0; b < 4 - C::kHeldBlocks; ++b) o[b][i] = ptx::mul2(o[b][i], f);
       }
       if (!first) {
-        ptx::tc_fence_after();
-#pragma unroll
-        for (int i = 0; i < HC / 2; ++i)
-          l[i] = ptx::mul2(l[i], ptx::pack2(__shfl_sync(0xffffffffu, factor, 2 * i), __shfl_sync(0xffffffffu, factor, 2 * i + 1)));
 #pragma unroll 1
-        for (int b = 0; b < 4; ++b) {
-#pragma unroll 1
-          for (int i0 = 0; i0 < HC; i0 += 8) {
-            uint32_t o[8];
-            tmem_ld<8>(lane_base + NR * b + col0 + i0, o);
-            ptx::tmem_wait_ld();
+        for (int j = 0; j < C::kHeldBlocks * HC; j += 8) {
+          const uint32_t a = lane_base + C::kHeld + NR * (j / HC) + col0 + j % HC;
+          uint32_t h[8];
+          ptx::tmem_ld8(a, h);
+          ptx::tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              o[i] = __float_as_uint(__uint_as_float(o[i]) * __shfl_sync(0xffffffffu, factor, i0 + i));
-            tmem_st<8>(lane_base + NR * b + col0 + i0, o);
-          }
+          for (int i = 0; i < 8; ++i)
+            h[i] = __float_as_uint(__uint_as_float(h[i]) * __shfl_sync(0xffffffffu, back, j % HC + i));
+          ptx::tmem_st8(a, h);
         }
         ptx::tmem_wait_st();
       }
-      ptx::named_bar_sync(1 + half, 128);               // the new reference is written
     }
-    fresh = fresh && pages == 0;                        // a tile of skipped pages sets no reference
-    // weights
-    const uint64_t down = ptx::pack2(exp2_int(-e), exp2_int(-e));
-#pragma unroll
-    for (int i = 0; i < HC; i += 8) {
-      uint32_t h[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 d = ptx::unpack2(acc[i / 2 + j]);
-        const float a = ptx::ex2_approx(d.x), c = ptx::ex2_approx(d.y);
-        l[i / 2 + j] = ptx::fma2(ptx::pack2(a, c), down, l[i / 2 + j]);
-        const __half2 hh = __floats2half2_rn(a, c);
-        h[j] = *reinterpret_cast<const uint32_t*>(&hh);
-      }
-      ptx::sts128_async_only(base + C::kP + swz_row<C::kPRow>(tok, (col0 + i) >> 3), make_uint4(h[0], h[1], h[2], h[3]));
-    }
-    ptx::fence_proxy_async_smem();
-    ptx::tc_fence_before();
     __syncwarp();
-    if (ok && lane == 0) ptx::mbar_arrive(&bars->pfull);
-
-    const bool last = w.last_of_segment(), ends = w.t == w.it.tiles - 1;
-    const Item it = w.it;
-    w.next(p);
-    first = last;
-    if (!last) continue;
-
-    // the next item's rows, so that its scores can start beside this one's last PV
-    if (w.left > 0) {
-      load_q<NR>(p, w.it, sm, base, buf ^ 1, warp, lane);
-      ptx::fence_proxy_async_smem();
-      __syncwarp();
-      if (ok && lane == 0) ptx::mbar_arrive(&bars->qfull);
-    }
-    // row sums over the tile's 128 positions
-    float ls[HC];
+    // weights
+    uint32_t w16[HC / 2];
+    {
+      const float d = exp2_int(-e);
+      const uint64_t down = ptx::pack2(d, d);
 #pragma unroll
-    for (int i = 0; i < HC / 2; ++i) {
-      const float2 x = ptx::unpack2(l[i]);
-      ls[2 * i] = x.x;
-      ls[2 * i + 1] = x.y;
-    }
-    const float sum = reduce_scatter<HC>(ls, lane, [](float a, float b) { return a + b; });
-    if (lane < HC) red[quad * NR + lane] = sum;
-    SMLA_WAIT(&bars->pdone, dpar);
-    dpar ^= 1;
-    ptx::tc_fence_after();
-    ptx::named_bar_sync(3, kSoftWarps * 32);
-    const bool whole = begins && ends;
-    // a run's first segment that continues an item goes to slot 0 of the CTA, its last segment to slot 1
-    const size_t slot = 2 * (size_t)blockIdx.x + (begins ? 1 : 0);
-    float inv = 0.f;
-    if (lane < HC) {
-      const float z = red[lane] + red[NR + lane] + red[2 * NR + lane] + red[3 * NR + lane];
-      inv = z > 0.f ? 1.f / z : (z == 0.f ? 0.f : CUDART_NAN_F);
-      const float lse = z == 0.f ? -CUDART_INF_F : (log2f(z) - nref[lane]) * kLn2;
-      if (quad == 0 && ok && col0 + lane < it.nrows) {
-        if (whole) p.lse[(size_t)it.req * p.q_per_req * p.H + it.row0 + col0 + lane] = lse;
-        else lse_part[slot * NR + col0 + lane] = lse;
-      }
-    }
-#pragma unroll 1
-    for (int b = 0; b < 4; ++b) {
-      const int dim = 128 * b + (tok & ~1);
+      for (int i = 0; i < HC / 2; i += 2) {
+        const ulonglong2 nr = ptx::lds128_pairs(row_nr + i * 8), c = ptx::lds128_pairs(row_c + i * 8);
 #pragma unroll
-      for (int i0 = 0; i0 < HC; i0 += LC) {
-        uint32_t o[LC];
-        tmem_ld<LC>(lane_base + NR * b + col0 + i0, o);
-        ptx::tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < LC; i += 2) {
-          // lanes 2j, 2j + 1 hold dims d, d + 1: the first ends with both dims of the first row, the other with
-          // both of the second
-          const bool second = lane & 1;
-          const float va = __uint_as_float(o[i]) * __shfl_sync(0xffffffffu, inv, i0 + i);
-          const float vb = __uint_as_float(o[i + 1]) * __shfl_sync(0xffffffffu, inv, i0 + i + 1);
-          const float got = __shfl_xor_sync(0xffffffffu, second ? va : vb, 1);
-          const int c = col0 + i0 + i + (second ? 1 : 0);
-          const float d0 = second ? got : va, d1 = second ? vb : got;
-          if (ok && c < it.nrows) {
-            if (whole) {
-              uint16_t* o16 = p.out + ((size_t)it.req * p.q_per_req * p.H + it.row0 + c) * kDLatent;
-              *reinterpret_cast<uint32_t*>(o16 + dim) = f32x2_to_bf16x2(d0, d1);
-            } else {
-              *reinterpret_cast<float2*>(o_part + (slot * NR + c) * kDLatent + dim) = make_float2(d0, d1);
-            }
-          }
+        for (int j = 0; j < 2; ++j) {
+          const float2 x = ptx::unpack2(ptx::add2(acc[i + j], j ? nr.y : nr.x));
+          const float a = ptx::ex2_approx(x.x), b = ptx::ex2_approx(x.y);
+          l[i + j] = ptx::fma2(ptx::mul2(ptx::pack2(a, b), down), j ? c.y : c.x, l[i + j]);
+          const __half2 h = __floats2half2_rn(a, b);
+          w16[i + j] = *reinterpret_cast<const uint32_t*>(&h);
         }
       }
     }
-    ptx::tc_fence_before();
-    ptx::named_bar_sync(3, kSoftWarps * 32);             // red, ref and TMEM are free; the next factors are written
-    begins = true;
-    buf ^= 1;
+    // block b's operand: w m_b as hi + lo
+    {
+      const float d = exp2_int(-e);
+      float4 rot = s4;
+#pragma unroll 1
+      for (int b = 0; b < 4; ++b) {
+        // (a NaN or infinite scale: its rows are NaN by their scores)
+        const __half2 m = __float2half2_rn(fminf(fmaxf(rot.x * d, -2.f), 2.f));
+        rot = make_float4(rot.y, rot.z, rot.w, rot.x);
+        uint32_t hi[HC / 4], lo[HC / 4];
+#pragma unroll
+        for (int i = 0; i < HC / 4; ++i) {
+          uint32_t h2[2], l2[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&w16[2 * i + j]), m);
+            h2[j] = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&x));
+            const uint32_t back2 = e4m3x2_to_f16x2((uint16_t)h2[j]);
+            const __half2 r = __hsub2(x, *reinterpret_cast<const __half2*>(&back2));
+            l2[j] = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&r));
+          }
+          hi[i] = __byte_perm(h2[0], h2[1], 0x5410);
+          lo[i] = __byte_perm(l2[0], l2[1], 0x5410);
+        }
+        // a tile's blocks beyond the buffers wait for the block before in theirs, and take its O^T; the others find
+        // their buffers free, since the tile before has been added up
+        if (C::kHeldBlocks > 0 && b >= C::kPBufs) flush_held(b - C::kPBufs, first);
+        const uint32_t dst = base + C::kP + pslot * C::kPBuf;
+        if constexpr (HC >= 16) {
+#pragma unroll
+          for (int u = 0; u < HC / 16; ++u) {
+            ptx::sts128_async_only(dst + swz_row<C::kPRow>(tok, col0 / 16 + u),
+                                   make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]));
+            ptx::sts128_async_only(dst + swz_row<C::kPRow>(tok, (NR + col0) / 16 + u),
+                                   make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]));
+          }
+        } else {
+          ptx::sts64_async_only(dst + swz_row<C::kPRow>(tok, 0) + col0, hi[0], hi[1]);
+          ptx::sts64_async_only(dst + swz_row<C::kPRow>(tok, 1) + col0, lo[0], lo[1]);
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (ok && lane == 0) ptx::mbar_arrive(&bars->pfull[pslot]);
+        pslot = pslot + 1 == C::kPBufs ? 0 : pslot + 1;
+      }
+    }
+
+    const bool last = w.last_of_segment(), ends = w.t == w.n.tiles - 1;
+    whole = begins && ends;
+    w.next();
+    first = last;
   }
 }
 
@@ -806,15 +890,16 @@ __device__ void find_run(const DenseParams& p, unsigned char* scratch, Bars* bar
   const int n = p.requests * p.groups, per = (n + kDenseThreads - 1) / kDenseThreads;
   const int i0 = min(n, (int)threadIdx.x * per), i1 = min(n, i0 + per);
   long long mine = 0;
-  for (int i = i0; i < i1; ++i) mine += item_at(p, i).tiles;
+#pragma unroll 1
+  for (int i = i0; i < i1; ++i) mine += lens_of(p, rows_of(p, i)).tiles;
   sums[threadIdx.x] = mine;
   __syncthreads();
-  if (threadIdx.x < 32) {                                // exclusive prefix over 20 sums per lane
-    long long v[20], part = 0;
+  if (threadIdx.x < 32) {                                // exclusive prefix over 12 sums per lane
+    long long v[12], part = 0;
 #pragma unroll
-    for (int j = 0; j < 20; ++j) {
+    for (int j = 0; j < 12; ++j) {
       v[j] = part;
-      part += sums[20 * threadIdx.x + j];
+      part += sums[12 * threadIdx.x + j];
     }
     long long before = part;
 #pragma unroll
@@ -825,7 +910,7 @@ __device__ void find_run(const DenseParams& p, unsigned char* scratch, Bars* bar
     if (threadIdx.x == 31) bars->total = before;
     before -= part;
 #pragma unroll
-    for (int j = 0; j < 20; ++j) sums[20 * threadIdx.x + j] = before + v[j];
+    for (int j = 0; j < 12; ++j) sums[12 * threadIdx.x + j] = before + v[j];
   }
   __syncthreads();
   const long long T = bars->total;
@@ -838,8 +923,9 @@ __device__ void find_run(const DenseParams& p, unsigned char* scratch, Bars* bar
   if (a < e && mine > 0) {
     if (a >= at && a < at + mine) {                      // the run begins in this thread's items
       long long x = at;
+#pragma unroll 1
       for (int i = i0; i < i1; ++i) {
-        const int tiles = item_at(p, i).tiles;
+        const int tiles = lens_of(p, rows_of(p, i)).tiles;
         if (a < x + tiles) {
           bars->first_item = i;
           bars->first_tile = (int)(a - x);
@@ -850,8 +936,9 @@ __device__ void find_run(const DenseParams& p, unsigned char* scratch, Bars* bar
     }
     if (e - 1 >= at && e - 1 < at + mine) {              // and ends in these
       long long x = at;
+#pragma unroll 1
       for (int i = i0; i < i1; ++i) {
-        const int tiles = item_at(p, i).tiles;
+        const int tiles = lens_of(p, rows_of(p, i)).tiles;
         if (e - 1 < x + tiles) {
           *desc = RunDesc{T, x, x + tiles, i, 0};
           break;
@@ -877,27 +964,25 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
   if (threadIdx.x == 0) {
     ptx::prefetch_tensormap(&map);
     ptx::prefetch_tensormap(&smap);
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 12; ++i) {
       ptx::mbar_init(&bars->kfull[i], 1);
-      ptx::mbar_init(&bars->kempty[i], 1 + kConvWarps);
+      ptx::mbar_init(&bars->kempty[i], 1);
+      bars->armed_k[i] = 0;
     }
     for (int i = 0; i < 4; ++i) {
-      ptx::mbar_init(&bars->vfull[i], 4);
-      ptx::mbar_init(&bars->vempty[i], 1);
-      ptx::mbar_init(&bars->scfull[i], 1);
-      ptx::mbar_init(&bars->scempty[i], kSoftWarps + kConvWarps);
-    }
-    for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&bars->sfull[i], 1);
       ptx::mbar_init(&bars->sempty[i], kSoftWarps);
-      ptx::mbar_init(&bars->drain[i], 1);
+      ptx::mbar_init(&bars->pfull[i], kSoftWarps);
+      ptx::mbar_init(&bars->pempty[i], 1);
     }
-    ptx::mbar_init(&bars->pfull, kSoftWarps);
-    ptx::mbar_init(&bars->pdone, 1);
+    for (int i = 0; i < kScaleSlots; ++i) {
+      ptx::mbar_init(&bars->scfull[i], 1);
+      ptx::mbar_init(&bars->scempty[i], kSoftWarps);
+      bars->armed_sc[i] = 0;
+    }
+    for (int i = 0; i < 2; ++i) ptx::mbar_init(&bars->drain[i], 1);
     ptx::mbar_init(&bars->qfull, kSoftWarps);
     bars->abort = 0;
-    for (int i = 0; i < 8; ++i) bars->armed_k[i] = 0;
-    for (int i = 0; i < 4; ++i) bars->armed_sc[i] = 0;
     ptx::fence_mbar_init();
   }
   if (warp == kQkWarp) {
@@ -913,9 +998,6 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
   if (warp < kSoftWarps) {
     ptx::setmaxnreg_inc<kSoftRegs>();
     softmax_role<NR>(p, sm, base, tmem, bars, warp, lane, o_part, lse_part);
-  } else if (warp < kSoftWarps + kConvWarps) {
-    ptx::setmaxnreg_dec<kConvRegs>();
-    convert_role<NR>(p, base, bars, warp, lane);
   } else {
     ptx::setmaxnreg_dec<kMiscRegs>();
     if (warp == kCopyWarp) copy_role<NR>(p, &map, &smap, base, bars, lane);
@@ -980,7 +1062,7 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const DenseP
   for (int idx = blockIdx.x; idx < work; idx += gridDim.x) {
     const int c = list_s[idx / nr], row = idx % nr;
     const RunDesc d = descs[c];
-    const Item it = item_at(p, d.item);
+    const Rows it = rows_of(p, d.item);
     if (row >= it.nrows) continue;                       // uniform over the CTA
     int c1 = (int)((d.item_end * active + T - 1) / T);   // first CTA past the item, give or take one
     while (c1 > c && run_start(T, active, c1) >= d.item_end) --c1;

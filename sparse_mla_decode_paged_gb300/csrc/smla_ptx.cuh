@@ -87,32 +87,25 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
   }
 }
 
-// try_wait that suspends the thread for about `hint_ns` at most.
-__device__ __forceinline__ bool mbar_try_wait_for(uint64_t* bar, uint32_t parity, uint32_t hint_ns) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(hint_ns)
-      : "memory");
-  return ok != 0;
-}
-
-// mbar_wait_bounded in few instructions, for a kernel whose many waits compete for the instruction cache: each
-// try suspends for at most the limit (or 1 ms), so a limit of nanoseconds runs out as such.  A whole warp calls
-// it; the verdict is the AND over its lanes.
+// mbar_wait_bounded for a whole warp in little code, for a kernel whose many waits compete for issue slots and the
+// instruction cache: between tries the warp sleeps briefly (one that polls without a pause takes issue slots from
+// the warps it waits for), and the clock and the abort flag are looked at once in 64 tries.  With a limit of 0 a
+// wait is one test, so that it gives up unless its phase is complete.  The verdict is the AND over the lanes.
 __device__ __forceinline__ bool mbar_wait_warp_small(uint64_t* bar, uint32_t parity, volatile int* abort,
                                                      uint64_t limit_ns) {
-  const uint32_t hint = limit_ns < 1000000ull ? (uint32_t)limit_ns : 1000000u;
-  bool ok = mbar_try_wait_for(bar, parity, hint);
+  bool ok = mbar_test_wait(bar, parity);
   if (!ok) {
     const uint64_t t0 = globaltimer_ns();
-    while (!(ok = mbar_try_wait_for(bar, parity, hint))) {
-      if (*abort || globaltimer_ns() - t0 > limit_ns) {
+    uint32_t n = 0;
+#pragma unroll 1
+    do {
+      if ((n++ & 63) == 0 && (limit_ns == 0 || *abort || globaltimer_ns() - t0 > limit_ns)) {
         *abort = 1;
         break;
       }
-    }
+      ok = mbar_try_wait(bar, parity);
+      if (!ok) __nanosleep(20);
+    } while (!ok);
   }
   return __all_sync(0xffffffffu, ok);
 }
@@ -482,6 +475,10 @@ __device__ __forceinline__ uint4 lds128(uint32_t saddr) {
 // copy) reads after a proxy fence and a thread barrier, so no C++ access needs ordering against it.
 __device__ __forceinline__ void sts128_async_only(uint32_t saddr, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(saddr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w));
+}
+
+__device__ __forceinline__ void sts64_async_only(uint32_t saddr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(saddr), "r"(a), "r"(b));
 }
 
 __device__ __forceinline__ void sts128(uint32_t saddr, uint4 v) {

@@ -115,7 +115,7 @@ def test_dense_oracle_equals_the_sparse_oracle_over_every_position():
     a = dense_oracle.dense_decode(bits(q), cache.numpy(), bt.numpy(), lens.numpy(), 0.05)
     b = oracle.sparse_mla_decode(bits(q), cache.numpy(), bt.numpy(), tk, lens.numpy(), 0.05)
     assert np.allclose(a[0], b[0], rtol=1e-12, atol=1e-14) and np.allclose(a[1], b[1], rtol=1e-12)
-    assert np.all(a[2] >= np.abs(a[0]) - 1e-12) and np.all(a[3] >= 0)
+    assert np.all(a[2] >= np.abs(a[0]) - 1e-12) and np.all(a[3] >= 0) and np.all(a[4] >= 0)
 
 
 def test_rotation_oracle_turns_by_the_angle():
