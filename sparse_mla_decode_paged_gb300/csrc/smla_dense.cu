@@ -47,12 +47,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kTopWeight = 7.f;         // a tile's largest weight of a row lies in (2^6, 2^7]
 constexpr float kMaxFactor = 20.f;        // a tile's factor 2^(R - ref) above 2^20 moves ref
 
-// Warps: 0-7 softmax (warp w: TMEM lanes of quadrant w % 4, row half w / 4), then one warp each for the copies,
-// the QK and the PV; the last one is idle.
-constexpr int kSoftWarps = 8;
-constexpr int kCopyWarp = 8, kQkWarp = 9, kPvWarp = 10;
-constexpr int kDenseThreads = 12 * 32;
-constexpr int kSoftRegs = 232, kMiscRegs = 40;   // of 168 at launch: 2 x 232 + 40 = 3 x 168
+// Warps: the softmax warps (warp w: TMEM lanes of quadrant w % 4, row part w / 4), then one for the copies, and two
+// each for the QK and the PV, which take chunks and blocks in turn: one warp alone needs longer for the waits,
+// descriptors and commits around a chunk's MMAs than the MMAs take (NR = 64: xxx us with one each, xxx with two).
+constexpr int kCopyRole = 0, kQkRole = 1, kPvRole = 3, kIssuers = 2, kMiscWarps = 8;
 
 constexpr uint32_t kSlot = 16384;         // 128 positions x 128 bytes: one code block or the rope of a tile
 constexpr int kChunks = 5;                // the four code blocks, then the rope
@@ -60,17 +58,22 @@ constexpr int kScaleSlots = 3;
 
 template <int NR>
 struct DC {
-  static constexpr int kRing = NR == 64 ? 7 : NR == 32 ? 9 : 11;    // K slots
-  static constexpr int kPBufs = NR == 64 ? 2 : 4;                   // weights of so many blocks
-  static constexpr int kSBufs = NR == 64 ? 2 : 4;                   // score accumulators
-  // hi and lo weights meet in one accumulator for 64 rows (TMEM is full); for fewer rows they are one MMA of twice
-  // the columns and meet in the registers
+  static constexpr int kRing = NR == 64 ? 6 : NR == 32 ? 9 : 11;    // K slots
+  static constexpr int kPBufs = NR == 64 ? 3 : 4;                   // weights of so many blocks, and their O^T
+  static constexpr int kSBufs = NR == 64 ? 3 : 4;                   // score accumulators
+  // hi and lo terms (of q, and of the weights) meet in one accumulator for 64 rows, where TMEM is full; for fewer rows
+  // they are one MMA of twice the columns and meet in the registers
   static constexpr int kPasses = NR == 64 ? 2 : 1;
-  static constexpr int kOCols = NR == 64 ? NR : 2 * NR;             // columns of a block's O^T of one tile
+  static constexpr int kOCols = NR == 64 ? NR : 2 * NR;             // columns of a block's O^T of one tile, or scores
   // TMEM: O^T of one tile (kPBufs blocks at a time), score buffers, and for 64 rows, whose accumulators do not all fit
   // the registers, those of blocks 0 and 1
   static constexpr int kHeldBlocks = NR == 64 ? 2 : 0;
-  static constexpr int HC = NR / 2;       // rows of one softmax thread
+  static constexpr int kParts = 2;
+  static constexpr int kSoftWarps = 4 * kParts;
+  static constexpr int kThreads = 32 * (kSoftWarps + kMiscWarps);
+  // registers after setmaxnreg, of 128 at launch: 2 x 216 + 2 x 40 = 4 x 128
+  static constexpr int kSoftRegs = 216, kMiscRegs = 40;
+  static constexpr int HC = NR / kParts;       // rows of one softmax thread
   static constexpr uint32_t kQ8Chunk = 2 * NR * 128;
   static constexpr uint32_t kQ8 = 0;
   static constexpr uint32_t kQr = kQ8 + 4 * kQ8Chunk;
@@ -85,16 +88,25 @@ struct DC {
   static constexpr uint32_t kRow = kRed + 4 * NR * 4;             // per softmax warp [HC] minus R, [HC] factor
   static constexpr uint32_t kBar = kRow + kSoftWarps * 2 * HC * 4;
   static constexpr uint32_t kBytes = kBar + 512;
-  static constexpr uint32_t kSCol = kPBufs * kOCols;              // score buffer i at kSCol + 2 NR i
-  static constexpr uint32_t kHeld = kSCol + kSBufs * 2 * NR;      // accumulators of block b at kHeld + NR b
+  static constexpr uint32_t kSCol = kPBufs * kOCols;              // score buffer i at kSCol + kOCols i
+  static constexpr uint32_t kHeld = kSCol + kSBufs * kOCols;      // accumulators of block b at kHeld + NR b
   static constexpr uint32_t kTmemCols = kHeld + kHeldBlocks * NR;
   static_assert(kBytes <= 232448, "shared memory");
   static_assert(kTmemCols == 512 || kTmemCols == 256, "TMEM allocations are powers of two");
 };
 
+// Weights buffer (and O^T slot) of block b, and the parity of its use in a tile whose number has parity `tile`: with
+// three buffers block 3 takes block 0's a second time.
+template <int NR>
+__device__ __forceinline__ int pbuf(int b) { return b < DC<NR>::kPBufs ? b : b - DC<NR>::kPBufs; }
+template <int NR>
+__device__ __forceinline__ uint32_t pparity(int b, uint32_t tile) {
+  return DC<NR>::kPBufs == 3 && (b == 0 || b == 3) ? (b == 3 ? 1u : 0u) : tile;
+}
+
 struct Bars {
   uint64_t kfull[12], kempty[12], sfull[4], sempty[4], scfull[3], scempty[3];
-  uint64_t pfull[4], pempty[4], qfull, drain[2];
+  uint64_t pfull[4], pempty[4], qfull, drain;
   uint32_t tmem;
   int abort;
   int armed_k[12], armed_sc[3];            // copies armed so far per slot
@@ -179,6 +191,9 @@ struct Walk {
   }
 };
 
+// Limits below this are meant to run out: nothing is issued and the call reports a timeout.
+constexpr uint64_t kLeastWaitNs = 1000;
+
 // A ring position: slot and the parity of its current use.
 template <int N>
 struct Ring {
@@ -194,14 +209,16 @@ struct Ring {
 
 // Wait for a slot to be freed: passes at once on the ring's first round (an mbarrier that has completed no
 // phase yet reports the phase before its first as complete).
-// Once a wait has given up (ok false) a role runs its loop to the end without waiting, arriving or issuing, so
-// that the named barriers of the softmax warps stay matched.
-// (`ok` is passed through an empty asm: otherwise the compiler makes a copy of the rest of the role for each wait
-// that may give up, five hundred KB of code in all, and the instruction cache becomes the bound.)
-#define SMLA_WAIT(bar, par)                                                                        \
-  do {                                                                                             \
-    if (ok) ok = ptx::mbar_wait_warp_small((bar), (par), &bars->abort, p.wait_ns);                 \
-    asm volatile("" : "+r"(ok));                                                                   \
+// A wait of a whole warp, bounded by p.wait_ns.  The common case is one try; once a wait has given up (ok 0) a
+// role runs its loop to the end without arriving or issuing, so that the named barriers of the softmax warps stay
+// matched.  (`ok` passes through an empty asm: otherwise the compiler makes a copy of the rest of the role for
+// each wait that may give up.)
+#define SMLA_WAIT(bar, par)                                                                               \
+  do {                                                                                                    \
+    if (__builtin_expect(__any_sync(0xffffffffu, !ptx::mbar_try_wait((bar), (par))), 0)) {                \
+      if (ok) ok = ptx::mbar_wait_rest((bar), (par), &bars->abort, p.wait_ns);                            \
+      asm volatile("" : "+r"(ok));                                                                        \
+    }                                                                                                     \
   } while (0)
 
 // ----------------------------------------------------------------------------- copies
@@ -220,7 +237,7 @@ __device__ void copy_role(const DenseParams& p, const CUtensorMap* map, const CU
   int req = 0;
   Ring<C::kRing> k;
   Ring<kScaleSlots> sc;
-  uint32_t ok = 1;
+  uint32_t ok = p.wait_ns >= kLeastWaitNs;
   // block-table entries of 16 tiles per load, one lane each, the next 16 tiles' already in flight
   int cur = 0, nxt = 0, base_lp = 0, item = -1;
 #pragma unroll 1
@@ -296,15 +313,15 @@ __device__ void drain_copies(uint64_t* bar, const int* armed, int n, int lane) {
 // ----------------------------------------------------------------------------- MMA issue
 
 template <int NR>
-__device__ void qk_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars* bars, int lane) {
+__device__ void qk_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars* bars, int which, int lane) {
   using C = DC<NR>;
-  constexpr uint32_t kIdescCodes = ptx::idesc_e4m3(128, 2 * NR), kIdescRope = ptx::idesc_bf16(128, NR);
+  constexpr uint32_t kIdescCodes = ptx::idesc_e4m3(128, C::kOCols), kIdescRope = ptx::idesc_bf16(128, NR);
   Walk w(bars);
   Ring<C::kRing> k;
   Ring<C::kSBufs> s;
   uint32_t qpar = 0;
-  uint32_t ok = 1;
-  int item = -1;
+  uint32_t ok = p.wait_ns >= kLeastWaitNs;
+  int item = -1, turn = which;                          // 0: the next chunk is this warp's
   const uint64_t dq = ptx::sw128_desc(base + C::kQ8, 16, 1024), dr = ptx::sw128_desc(base + C::kQr, 16, 1024);
 #pragma unroll 1
   while (w.here(p)) {
@@ -315,70 +332,79 @@ __device__ void qk_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars
     }
 #pragma unroll 1
     for (int c = 0; c < kChunks; ++c) {
-      SMLA_WAIT(&bars->sempty[s.slot], s.parity ^ 1);
-      SMLA_WAIT(&bars->kfull[k.slot], k.parity);
-      ptx::tc_fence_after();
-      const uint32_t ks = k.slot, d = tmem + C::kSCol + 2 * NR * s.slot, cu = c;
-      if (ok && ptx::elect_one()) {
-        const uint64_t dk = ptx::sw128_desc(base + C::kK + ks * kSlot, 16, 1024);
-        if (c == 4) {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) ptx::mma_f16_ss(d, dk + 2 * kk, dr + 2 * kk, kIdescRope, kk > 0);
-        } else {
-          const uint64_t dqb = dq + (uint64_t)((cu * C::kQ8Chunk) >> 4);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) ptx::mma_f8_ss(d, dk + 2 * kk, dqb + 2 * kk, kIdescCodes, kk > 0);
+      if (turn == 0) {
+        SMLA_WAIT(&bars->sempty[s.slot], s.parity ^ 1);
+        SMLA_WAIT(&bars->kfull[k.slot], k.parity);
+        ptx::tc_fence_after();
+        const uint32_t ks = k.slot, d = tmem + C::kSCol + C::kOCols * s.slot, cu = c;
+        if (ok && ptx::elect_one()) {
+          const uint64_t dk = ptx::sw128_desc(base + C::kK + ks * kSlot, 16, 1024);
+          if (c == 4) {
+  #pragma unroll
+            for (int kk = 0; kk < 4; ++kk) ptx::mma_f16_ss(d, dk + 2 * kk, dr + 2 * kk, kIdescRope, kk > 0);
+          } else {
+            const uint64_t dqb = dq + (uint64_t)((cu * C::kQ8Chunk) >> 4);
+  #pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+  #pragma unroll
+              for (int pass = 0; pass < C::kPasses; ++pass)
+                ptx::mma_f8_ss(d, dk + 2 * kk, dqb + 2 * kk + (uint64_t)((pass * NR * 128) >> 4), kIdescCodes, kk > 0 || pass > 0);
+          }
+          if (c == 4) ptx::mma_commit(&bars->kempty[k.slot]);   // the codes stay for the PV
+          ptx::mma_commit(&bars->sfull[s.slot]);
         }
-        if (c == 4) ptx::mma_commit(&bars->kempty[k.slot]);   // the codes stay for the PV
-        ptx::mma_commit(&bars->sfull[s.slot]);
+        __syncwarp();
       }
-      __syncwarp();
+      turn = turn == 0 ? kIssuers - 1 : turn - 1;
       k.next();
       s.next();
     }
     w.next();
   }
-  if (ptx::elect_one()) ptx::mma_commit(&bars->drain[0]);
+  if (ptx::elect_one()) ptx::mma_commit(&bars->drain);
   __syncwarp();
 }
 
 template <int NR>
-__device__ void pv_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars* bars, int lane) {
+__device__ void pv_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars* bars, int which, int lane) {
   using C = DC<NR>;
   constexpr int N = C::kOCols;
   constexpr uint32_t kIdesc = ptx::idesc_e4m3(128, N) | (1u << 15) | (1u << 16);     // A and B MN-major
   Walk w(bars);
   Ring<C::kRing> k;
-  Ring<C::kPBufs> pb;
-  uint32_t ok = 1;
+  uint32_t tile = 0;
+  uint32_t ok = p.wait_ns >= kLeastWaitNs;
 #pragma unroll 1
   while (w.here(p)) {
 #pragma unroll 1
     for (int b = 0; b < 4; ++b) {
-      SMLA_WAIT(&bars->pfull[pb.slot], pb.parity);
-      ptx::tc_fence_after();
-      const uint32_t ks = k.slot, ps = pb.slot, d = tmem + N * pb.slot;
-      if (ok && ptx::elect_one()) {
-        // codes^T: 128-byte rows of one position, 8-position groups 1024 bytes apart; 32 positions per MMA
-        const uint64_t dv = ptx::sw128_desc(base + C::kK + ks * kSlot, 1024, 1024);
-        const uint64_t dp = ptx::swz_desc(base + C::kP + ps * C::kPBuf, 8 * C::kPRow, 8 * C::kPRow, C::kPRow);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-          for (int pass = 0; pass < C::kPasses; ++pass)
-            ptx::mma_f8_ss(d, dv + (uint64_t)(256 * kk),
-                           dp + (uint64_t)((32 * C::kPRow * kk + NR * pass) >> 4), kIdesc, kk > 0 || pass > 0);
-        ptx::mma_commit(&bars->kempty[k.slot]);
-        ptx::mma_commit(&bars->pempty[pb.slot]);
+      // blocks 0 and 3 share a buffer, so one warp takes both (the waits on it alternate in parity)
+      if ((b == 1 || b == 2) == (which == 1)) {
+        const uint32_t ks = k.slot, ps = pbuf<NR>(b), d = tmem + N * ps;
+        SMLA_WAIT(&bars->pfull[ps], pparity<NR>(b, tile));
+        ptx::tc_fence_after();
+        if (ok && ptx::elect_one()) {
+          // codes^T: 128-byte rows of one position, 8-position groups 1024 bytes apart; 32 positions per MMA
+          const uint64_t dv = ptx::sw128_desc(base + C::kK + ks * kSlot, 1024, 1024);
+          const uint64_t dp = ptx::swz_desc(base + C::kP + ps * C::kPBuf, 8 * C::kPRow, 8 * C::kPRow, C::kPRow);
+  #pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+  #pragma unroll
+            for (int pass = 0; pass < C::kPasses; ++pass)
+              ptx::mma_f8_ss(d, dv + (uint64_t)(256 * kk),
+                             dp + (uint64_t)((32 * C::kPRow * kk + NR * pass) >> 4), kIdesc, kk > 0 || pass > 0);
+          ptx::mma_commit(&bars->kempty[k.slot]);
+          ptx::mma_commit(&bars->pempty[ps]);
+        }
+        __syncwarp();
       }
-      __syncwarp();
       k.next();
-      pb.next();
     }
+    tile ^= 1;
     k.next();                                             // the rope
     w.next();
   }
-  if (ptx::elect_one()) ptx::mma_commit(&bars->drain[1]);
+  if (ptx::elect_one()) ptx::mma_commit(&bars->drain);
   __syncwarp();
 }
 
@@ -417,7 +443,7 @@ __device__ __forceinline__ void load_q(const DenseParams& p, int item, unsigned 
   const uint16_t* q0 = p.q + ((size_t)it.req * p.q_per_req * p.H + it.row0) * kDQK;
   const int b = lane >> 3, u = lane & 7;
 #pragma unroll 1
-  for (int r = warp; r < NR; r += kSoftWarps) {
+  for (int r = warp; r < NR; r += C::kSoftWarps) {
     uint4 raw[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)}, rope = raw[0];
     if (r < it.nrows) {
       const uint4* src = reinterpret_cast<const uint4*>(q0 + (size_t)r * kDQK);
@@ -480,22 +506,32 @@ __device__ __forceinline__ int scale_exponent(const float4& s) {
   return min(max((int)(__float_as_uint(top) >> 23) - 127, -60), 100);
 }
 
-// Two fp16 values -> two E4M3 codes (round to nearest even, saturating).
-__device__ __forceinline__ uint16_t f16x2_to_e4m3x2(uint32_t h) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+// Two fp16 pairs -> four E4M3 codes in one word (round to nearest even, saturating), and back.
+__device__ __forceinline__ uint32_t f16x4_to_e4m3x4(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("{\n .reg .b16 x, y;\n cvt.rn.satfinite.e4m3x2.f16x2 x, %1;\n cvt.rn.satfinite.e4m3x2.f16x2 y, %2;\n"
+      " mov.b32 %0, {x, y};\n}\n"
+      : "=r"(r)
+      : "r"(a), "r"(b));
   return r;
 }
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& a, uint32_t& b) {
+  asm("{\n .reg .b16 x, y;\n mov.b32 {x, y}, %2;\n cvt.rn.f16x2.e4m3x2 %0, x;\n cvt.rn.f16x2.e4m3x2 %1, y;\n}\n"
+      : "=r"(a), "=r"(b)
+      : "r"(w));
+}
+__device__ __forceinline__ __half2 as_half2(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
+__device__ __forceinline__ uint32_t as_u32(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
 
 // Makes the codes of positions that some row does not see harmless for the PV (a weight of 0 must give 0):
 // NaN codes become 0, and every code of a position that no row sees.  (A row that does see a NaN code has a NaN
-// score, so it is NaN whatever the value.)  Threads of half h take blocks 2 h, 2 h + 1.
+// score, so it is NaN whatever the value.)  The threads of a row part take every kParts-th block.
 template <int NR>
-__device__ __noinline__ void clean_codes(uint32_t base, int slot, int tok, int half, bool seen) {
+__device__ __noinline__ void clean_codes(uint32_t base, int slot, int tok, int part, bool seen) {
   using C = DC<NR>;
 #pragma unroll 1
   for (int b = 0; b < 4; ++b) {
-    if (b >> 1 == half) {
+    if (b % C::kParts == part) {
       const uint32_t at = base + C::kK + slot * kSlot;
 #pragma unroll 1
       for (int u = 0; u < 8; ++u) {
@@ -515,7 +551,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
                              int lane, float* o_part, float* lse_part) {
   using C = DC<NR>;
   constexpr int HC = C::HC, LC = HC;// rows per thread, columns per TMEM load
-  const int half = warp >> 2, quad = warp & 3, col0 = half * HC;
+  const int part = warp >> 2, quad = warp & 3, col0 = part * HC;
   const int tok = 32 * quad + lane;
   const uint32_t lane_base = tmem + ((uint32_t)(32 * quad) << 16);
   const float kf = p.sm_scale * kLog2e;
@@ -524,9 +560,9 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
   Walk w(bars);
   Ring<C::kSBufs> s;
   Ring<kScaleSlots> sc;
-  int kslot = 0, pslot = 0;
+  int kslot = 0;
   uint32_t dpar = 0;
-  uint32_t ok = 1;
+  uint32_t ok = p.wait_ns >= kLeastWaitNs;
   bool first = true, begins = w.t == 0;
   int buf = 0;
   // O of dim 128 b + tok, pairs of rows: blocks from kHeldBlocks on (the others are held in TMEM)
@@ -537,7 +573,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
   // Block b's O^T of one tile (pairs of rows); with `held`, its accumulators from TMEM in the same wait.
   auto tile_part = [&](int b, uint64_t (&x)[HC / 2], uint32_t (&held)[HC], bool load_held) {
     uint32_t hi[HC], lo[HC];
-    const uint32_t a = lane_base + C::kOCols * (b % C::kPBufs) + col0;
+    const uint32_t a = lane_base + C::kOCols * pbuf<NR>(b) + col0;
     tmem_ld<HC>(a, hi);
     if constexpr (C::kPasses == 1) tmem_ld<HC>(a + NR, lo);
     if (load_held) tmem_ld<HC>(lane_base + C::kHeld + NR * b + col0, held);
@@ -548,15 +584,15 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
       if constexpr (C::kPasses == 1) x[i] = ptx::add2(x[i], ptx::pack2(lo[2 * i], lo[2 * i + 1]));
     }
   };
-  auto wait_pv = [&](int b, uint32_t parity) {
-    SMLA_WAIT(&bars->pempty[b % C::kPBufs], parity);
+  auto wait_pv = [&](int b) {
+    SMLA_WAIT(&bars->pempty[pbuf<NR>(b)], pparity<NR>(b, dpar));
     ptx::tc_fence_after();
   };
   // adds a tile's blocks that are kept in registers (the PV of the tile before, see below)
   auto flush_registers = [&]() {
 #pragma unroll
     for (int b = C::kHeldBlocks; b < 4; ++b) {
-      wait_pv(b, C::kHeldBlocks ? 1u : dpar);
+      wait_pv(b);
       uint64_t x[HC / 2];
       uint32_t none[HC];
       tile_part(b, x, none, false);
@@ -568,12 +604,11 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
         d[1] = ptx::fma2(x[i + 1], c.y, d[1]);
       }
     }
-    dpar ^= 1;
     ptx::tc_fence_before();
   };
   // adds block b (held in TMEM); `start`: the segment's first tile
   auto flush_held = [&](int b, bool start) {
-    wait_pv(b, 0u);
+    wait_pv(b);
     uint64_t x[HC / 2];
     uint32_t h[HC];
     tile_part(b, x, h, true);                           // (before the segment's first tile: whatever was there)
@@ -591,6 +626,14 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
     tmem_st<HC>(lane_base + C::kHeld + NR * b + col0, h);
     ptx::tmem_wait_st();
     ptx::tc_fence_before();
+  };
+
+  // what is left of a tile once its weights are written: every block but the first (see there) of 64 rows
+  bool start = true;                                    // that tile was its segment's first
+  auto finish_tile = [&]() {
+    if constexpr (C::kHeldBlocks > 0) flush_held(1, start);
+    flush_registers();
+    dpar ^= 1;
   };
 
   int item = -1, done = -1;                             // items whose rows are loaded, whose segment has ended
@@ -611,7 +654,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
     if (!more) done = item;
     if (first && done >= 0) {
       const Rows it = rows_of(p, done);
-      flush_registers();
+      finish_tile();
       // row sums over the tile's 128 positions
       float ls[HC];
 #pragma unroll
@@ -621,9 +664,9 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
         ls[2 * i + 1] = x.y;
       }
       const float sum = reduce_scatter<HC>(ls, lane, [](float a, float b) { return a + b; });
-      ptx::named_bar_sync(1 + half, 128);                 // the maxima have been read
+      ptx::named_bar_sync(1 + part, 128);                 // the maxima have been read
       if (lane < HC) red[quad * NR + lane] = sum;
-      ptx::named_bar_sync(1 + half, 128);
+      ptx::named_bar_sync(1 + part, 128);
       // a run's first segment that continues an item goes to slot 0 of the CTA, its last segment to slot 1
       const size_t slot = 2 * (size_t)blockIdx.x + (begins ? 1 : 0);
       float inv = 0.f;
@@ -669,7 +712,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
     }
     if (!more) break;
     if (first) {
-      ptx::named_bar_sync(3, kSoftWarps * 32);          // red is free, the rows' factors and lengths are written
+      ptx::named_bar_sync(1 + C::kParts, C::kSoftWarps * 32);          // red is free, the rows' factors and lengths are written
 #pragma unroll
       for (int i = 0; i < HC / 2; ++i) {
         l[i] = 0;
@@ -695,19 +738,21 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
       for (int b = 0; b < 4; ++b) {
         SMLA_WAIT(&bars->sfull[s.slot], s.parity);
         ptx::tc_fence_after();
-        const uint32_t a = lane_base + C::kSCol + 2 * NR * s.slot + col0;
+        const uint32_t a = lane_base + C::kSCol + C::kOCols * s.slot + col0;
         const uint64_t scale = ptx::pack2(rot.x, rot.x);
         rot = make_float4(rot.y, rot.z, rot.w, rot.x);
 #pragma unroll
         for (int i0 = 0; i0 < HC; i0 += LC) {
           uint32_t hi[LC], lo[LC];
           tmem_ld<LC>(a + i0, hi);
-          tmem_ld<LC>(a + NR + i0, lo);
+          if constexpr (C::kPasses == 1) tmem_ld<LC>(a + NR + i0, lo);
           ptx::tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < LC; i += 2)
-            acc[(i0 + i) / 2] = ptx::fma2(ptx::add2(ptx::pack2(hi[i], hi[i + 1]), ptx::pack2(lo[i], lo[i + 1])), scale,
-                                          acc[(i0 + i) / 2]);
+          for (int i = 0; i < LC; i += 2) {
+            uint64_t x = ptx::pack2(hi[i], hi[i + 1]);
+            if constexpr (C::kPasses == 1) x = ptx::add2(x, ptx::pack2(lo[i], lo[i + 1]));
+            acc[(i0 + i) / 2] = ptx::fma2(x, scale, acc[(i0 + i) / 2]);
+          }
         }
         ptx::tc_fence_before();
         __syncwarp();
@@ -719,7 +764,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
     SMLA_WAIT(&bars->sfull[s.slot], s.parity);
     ptx::tc_fence_after();
     {
-      const uint32_t a = lane_base + C::kSCol + 2 * NR * s.slot + col0;
+      const uint32_t a = lane_base + C::kSCol + C::kOCols * s.slot + col0;
       const uint64_t kf2 = ptx::pack2(kf, kf), e2 = ptx::pack2((float)e, (float)e);
       const uint32_t fa = base + C::kF + (buf * NR + col0) * 4;
 #pragma unroll
@@ -752,10 +797,10 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
         if (!here || t >= lens[i + 1]) d.y = -CUDART_INF_F;
         acc[i / 2] = ptx::pack2(d.x, d.y);
       }
-      if (!here || t >= w.n.min_len) clean_codes<NR>(base, kslot, tok, half, here && t < w.n.max_len);
+      if (!here || t >= w.n.min_len) clean_codes<NR>(base, kslot, tok, part, here && t < w.n.max_len);
     }
     kslot = kslot + kChunks >= C::kRing ? kslot + kChunks - C::kRing : kslot + kChunks;
-    if (!first) flush_registers();
+    if (!first) finish_tile();
     // R of each row: every warp ends with its rows' maxima over the 128 positions, lane -> row
     {
       float v[HC];
@@ -768,7 +813,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
       const float m = reduce_scatter<HC>(v, lane, [](float a, float b) { return fmaxf(a, b); });
       if (lane < HC) red[quad * NR + lane] = m;
     }
-    ptx::named_bar_sync(1 + half, 128);
+    ptx::named_bar_sync(1 + part, 128);
     float back = 1.f;                                   // what a reference that moves takes from the sums so far
     if (lane < HC) {
       const float m = fmaxf(fmaxf(red[lane], red[NR + lane]), fmaxf(red[2 * NR + lane], red[3 * NR + lane]));
@@ -839,22 +884,16 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
         uint32_t hi[HC / 4], lo[HC / 4];
 #pragma unroll
         for (int i = 0; i < HC / 4; ++i) {
-          uint32_t h2[2], l2[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&w16[2 * i + j]), m);
-            h2[j] = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&x));
-            const uint32_t back2 = e4m3x2_to_f16x2((uint16_t)h2[j]);
-            const __half2 r = __hsub2(x, *reinterpret_cast<const __half2*>(&back2));
-            l2[j] = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&r));
-          }
-          hi[i] = __byte_perm(h2[0], h2[1], 0x5410);
-          lo[i] = __byte_perm(l2[0], l2[1], 0x5410);
+          const __half2 x = __hmul2(as_half2(w16[2 * i]), m), y = __hmul2(as_half2(w16[2 * i + 1]), m);
+          hi[i] = f16x4_to_e4m3x4(as_u32(x), as_u32(y));
+          uint32_t bx, by;
+          e4m3x4_to_f16x4(hi[i], bx, by);
+          lo[i] = f16x4_to_e4m3x4(as_u32(__hsub2(x, as_half2(bx))), as_u32(__hsub2(y, as_half2(by))));
         }
-        // a tile's blocks beyond the buffers wait for the block before in theirs, and take its O^T; the others find
-        // their buffers free, since the tile before has been added up
-        if (C::kHeldBlocks > 0 && b >= C::kPBufs) flush_held(b - C::kPBufs, first);
-        const uint32_t dst = base + C::kP + pslot * C::kPBuf;
+        // three buffers: the last block takes the first one's, after adding up its O^T; the other buffers are free,
+        // since the tile before has been added up
+        if (C::kHeldBlocks > 0 && b >= C::kPBufs) flush_held(0, first);
+        const uint32_t dst = base + C::kP + pbuf<NR>(b) * C::kPBuf;
         if constexpr (HC >= 16) {
 #pragma unroll
           for (int u = 0; u < HC / 16; ++u) {
@@ -869,13 +908,13 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (ok && lane == 0) ptx::mbar_arrive(&bars->pfull[pslot]);
-        pslot = pslot + 1 == C::kPBufs ? 0 : pslot + 1;
+        if (ok && lane == 0) ptx::mbar_arrive(&bars->pfull[pbuf<NR>(b)]);
       }
     }
 
     const bool last = w.last_of_segment(), ends = w.t == w.n.tiles - 1;
     whole = begins && ends;
+    start = first;
     w.next();
     first = last;
   }
@@ -885,21 +924,23 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
 
 // This CTA's run of tiles: every CTA adds up the tiles of all items (a run of items per thread, then a scan of
 // the threads' sums).
-__device__ void find_run(const DenseParams& p, unsigned char* scratch, Bars* bars, RunDesc* desc) {
+template <int kThreads>
+__device__ __forceinline__ void find_run(const DenseParams& p, unsigned char* scratch, Bars* bars, RunDesc* desc) {
+  constexpr int kPer = kThreads / 32;
   long long* sums = reinterpret_cast<long long*>(scratch);
-  const int n = p.requests * p.groups, per = (n + kDenseThreads - 1) / kDenseThreads;
+  const int n = p.requests * p.groups, per = (n + kThreads - 1) / kThreads;
   const int i0 = min(n, (int)threadIdx.x * per), i1 = min(n, i0 + per);
   long long mine = 0;
 #pragma unroll 1
   for (int i = i0; i < i1; ++i) mine += lens_of(p, rows_of(p, i)).tiles;
   sums[threadIdx.x] = mine;
   __syncthreads();
-  if (threadIdx.x < 32) {                                // exclusive prefix over 12 sums per lane
-    long long v[12], part = 0;
+  if (threadIdx.x < 32) {                                // exclusive prefix over kPer sums per lane
+    long long v[kPer], part = 0;
 #pragma unroll
-    for (int j = 0; j < 12; ++j) {
+    for (int j = 0; j < kPer; ++j) {
       v[j] = part;
-      part += sums[12 * threadIdx.x + j];
+      part += sums[kPer * threadIdx.x + j];
     }
     long long before = part;
 #pragma unroll
@@ -910,7 +951,7 @@ __device__ void find_run(const DenseParams& p, unsigned char* scratch, Bars* bar
     if (threadIdx.x == 31) bars->total = before;
     before -= part;
 #pragma unroll
-    for (int j = 0; j < 12; ++j) sums[12 * threadIdx.x + j] = before + v[j];
+    for (int j = 0; j < kPer; ++j) sums[kPer * threadIdx.x + j] = before + v[j];
   }
   __syncthreads();
   const long long T = bars->total;
@@ -951,7 +992,7 @@ __device__ void find_run(const DenseParams& p, unsigned char* scratch, Bars* bar
 }
 
 template <int NR>
-__global__ void __launch_bounds__(kDenseThreads, 1)
+__global__ void __launch_bounds__(DC<NR>::kThreads, 1)
     dense_kernel(const DenseParams p, const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap smap,
                  RunDesc* descs, float* lse_part, float* o_part) {
   using C = DC<NR>;
@@ -971,51 +1012,51 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     }
     for (int i = 0; i < 4; ++i) {
       ptx::mbar_init(&bars->sfull[i], 1);
-      ptx::mbar_init(&bars->sempty[i], kSoftWarps);
-      ptx::mbar_init(&bars->pfull[i], kSoftWarps);
+      ptx::mbar_init(&bars->sempty[i], C::kSoftWarps);
+      ptx::mbar_init(&bars->pfull[i], C::kSoftWarps);
       ptx::mbar_init(&bars->pempty[i], 1);
     }
     for (int i = 0; i < kScaleSlots; ++i) {
       ptx::mbar_init(&bars->scfull[i], 1);
-      ptx::mbar_init(&bars->scempty[i], kSoftWarps);
+      ptx::mbar_init(&bars->scempty[i], C::kSoftWarps);
       bars->armed_sc[i] = 0;
     }
-    for (int i = 0; i < 2; ++i) ptx::mbar_init(&bars->drain[i], 1);
-    ptx::mbar_init(&bars->qfull, kSoftWarps);
-    bars->abort = 0;
+    ptx::mbar_init(&bars->drain, 2 * kIssuers);
+    ptx::mbar_init(&bars->qfull, C::kSoftWarps);
+    bars->abort = p.wait_ns < kLeastWaitNs;
     ptx::fence_mbar_init();
   }
-  if (warp == kQkWarp) {
+  const int role = warp - C::kSoftWarps;                 // of the warps behind the softmax warps
+  if (role == kQkRole) {
     ptx::tmem_alloc(&bars->tmem, C::kTmemCols);
     ptx::tmem_relinquish();
   }
-  find_run(p, sm, bars, descs + blockIdx.x);             // the scratch is overwritten by the pipeline afterwards
+  find_run<C::kThreads>(p, sm, bars, descs + blockIdx.x);            // the scratch is overwritten by the pipeline afterwards
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = bars->tmem;
 
-  if (warp < kSoftWarps) {
-    ptx::setmaxnreg_inc<kSoftRegs>();
+  if (role < 0) {
+    ptx::setmaxnreg_inc<C::kSoftRegs>();
     softmax_role<NR>(p, sm, base, tmem, bars, warp, lane, o_part, lse_part);
   } else {
-    ptx::setmaxnreg_dec<kMiscRegs>();
-    if (warp == kCopyWarp) copy_role<NR>(p, &map, &smap, base, bars, lane);
-    else if (warp == kQkWarp) qk_role<NR>(p, base, tmem, bars, lane);
-    else if (warp == kPvWarp) pv_role<NR>(p, base, tmem, bars, lane);
+    ptx::setmaxnreg_dec<C::kMiscRegs>();
+    if (role == kCopyRole) copy_role<NR>(p, &map, &smap, base, bars, lane);
+    else if (role < kPvRole) qk_role<NR>(p, base, tmem, bars, role - kQkRole, lane);
+    else if (role < kPvRole + kIssuers) pv_role<NR>(p, base, tmem, bars, role - kPvRole, lane);
   }
 
   // nothing of this CTA's may be in flight when it leaves: the MMAs (their last commits) and, after a wait
   // that gave up, the copies
   __syncthreads();
   int never = 0;
-  if (warp == kCopyWarp && bars->abort) {
+  if (role == kCopyRole && bars->abort) {
     drain_copies(bars->kfull, bars->armed_k, C::kRing, lane);
     drain_copies(bars->scfull, bars->armed_sc, kScaleSlots, lane);
   }
-  if (warp == kQkWarp) {
-    ptx::mbar_wait_warp(&bars->drain[0], 0, &never, lane, 100000000ull);
-    ptx::mbar_wait_warp(&bars->drain[1], 0, &never, lane, 100000000ull);
+  if (role == kQkRole) {
+    ptx::mbar_wait_warp(&bars->drain, 0, &never, lane, 100000000ull);
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, C::kTmemCols);
   }
@@ -1175,7 +1216,7 @@ cudaError_t launch_nr(const DenseParams& p, unsigned char* ws, cudaStream_t stre
   RunDesc* descs = reinterpret_cast<RunDesc*>(ws + kWorkspaceHeader);
   float* lse_part = reinterpret_cast<float*>(ws + kWorkspaceHeader + kDescBytes);
   float* o_part = reinterpret_cast<float*>(ws + kWorkspaceHeader + kDescBytes + lse_part_bytes(p.ctas, NR));
-  dense_kernel<NR><<<p.ctas, kDenseThreads, DC<NR>::kBytes, stream>>>(p, map, smap, descs, lse_part, o_part);
+  dense_kernel<NR><<<p.ctas, DC<NR>::kThreads, DC<NR>::kBytes, stream>>>(p, map, smap, descs, lse_part, o_part);
   e = cudaGetLastError();
   // a table of at most two pages gives every item one tile: nothing to merge
   if (e != cudaSuccess || p.max_pages <= 2) return e;

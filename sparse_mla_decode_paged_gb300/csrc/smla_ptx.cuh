@@ -87,26 +87,22 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
   }
 }
 
-// mbar_wait_bounded for a whole warp in little code, for a kernel whose many waits compete for issue slots and the
-// instruction cache: between tries the warp sleeps briefly (one that polls without a pause takes issue slots from
-// the warps it waits for), and the clock and the abort flag are looked at once in 64 tries.  With a limit of 0 a
-// wait is one test, so that it gives up unless its phase is complete.  The verdict is the AND over the lanes.
-__device__ __forceinline__ bool mbar_wait_warp_small(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                                     uint64_t limit_ns) {
-  bool ok = mbar_test_wait(bar, parity);
-  if (!ok) {
-    const uint64_t t0 = globaltimer_ns();
-    uint32_t n = 0;
+// The rest of a wait whose first try_wait did not succeed: tries with short sleeps between them (a warp that polls
+// without a pause takes issue slots from the warps it waits for), with a look at the clock and the abort flag once
+// in 64 tries.  The verdict is the AND over the warp's lanes.
+__device__ __forceinline__ bool mbar_wait_rest(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+  const uint64_t t0 = globaltimer_ns();
+  uint32_t n = 0;
+  bool ok = false;
 #pragma unroll 1
-    do {
-      if ((n++ & 63) == 0 && (limit_ns == 0 || *abort || globaltimer_ns() - t0 > limit_ns)) {
-        *abort = 1;
-        break;
-      }
-      ok = mbar_try_wait(bar, parity);
-      if (!ok) __nanosleep(20);
-    } while (!ok);
-  }
+  do {
+    if ((n++ & 63) == 0 && (*abort || globaltimer_ns() - t0 > limit_ns)) {
+      *abort = 1;
+      break;
+    }
+    ok = mbar_try_wait(bar, parity);
+    if (!ok) __nanosleep(20);
+  } while (!ok);
   return __all_sync(0xffffffffu, ok);
 }
 
