@@ -47,10 +47,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kTopWeight = 7.f;         // a tile's largest weight of a row lies in (2^6, 2^7]
 constexpr float kMaxFactor = 20.f;        // a tile's factor 2^(R - ref) above 2^20 moves ref
 
-// Warps: the softmax warps (warp w: TMEM lanes of quadrant w % 4, row part w / 4), then one for the copies, and two
-// each for the QK and the PV, which take chunks and blocks in turn: one warp alone needs longer for the waits,
-// descriptors and commits around a chunk's MMAs than the MMAs take (NR = 64: xxx us with one each, xxx with two).
-constexpr int kCopyRole = 0, kQkRole = 1, kPvRole = 3, kIssuers = 2, kMiscWarps = 8;
+// Warps: the softmax warps (warp w: TMEM lanes of quadrant w % 4, row part w / 4), then one warp each for the
+// copies, the QK and the PV, and an idle one.
+enum { kCopyRole, kQkRole, kPvRole };
 
 constexpr uint32_t kSlot = 16384;         // 128 positions x 128 bytes: one code block or the rope of a tile
 constexpr int kChunks = 5;                // the four code blocks, then the rope
@@ -58,21 +57,22 @@ constexpr int kScaleSlots = 3;
 
 template <int NR>
 struct DC {
-  static constexpr int kRing = NR == 64 ? 6 : NR == 32 ? 9 : 11;    // K slots
-  static constexpr int kPBufs = NR == 64 ? 3 : 4;                   // weights of so many blocks, and their O^T
-  static constexpr int kSBufs = NR == 64 ? 3 : 4;                   // score accumulators
-  // hi and lo terms (of q, and of the weights) meet in one accumulator for 64 rows, where TMEM is full; for fewer rows
-  // they are one MMA of twice the columns and meet in the registers
+  static constexpr int kRing = NR == 64 ? 7 : NR == 32 ? 9 : 11;    // K slots
+  static constexpr int kPBufs = NR == 64 ? 2 : 4;                   // weights of so many blocks
+  static constexpr int kSBufs = NR == 64 ? 2 : 4;                   // score accumulators
+  // hi and lo weights meet in one accumulator for 64 rows (TMEM is full); for fewer rows they are one MMA of twice
+  // the columns and meet in the registers
   static constexpr int kPasses = NR == 64 ? 2 : 1;
-  static constexpr int kOCols = NR == 64 ? NR : 2 * NR;             // columns of a block's O^T of one tile, or scores
+  static constexpr int kOCols = NR == 64 ? NR : 2 * NR;             // columns of a block's O^T of one tile
   // TMEM: O^T of one tile (kPBufs blocks at a time), score buffers, and for 64 rows, whose accumulators do not all fit
   // the registers, those of blocks 0 and 1
   static constexpr int kHeldBlocks = NR == 64 ? 2 : 0;
+  // Row parts: 8 softmax warps, 16 for 64 rows (the weights' work of 64 rows needs the warps to hide its latencies).
   static constexpr int kParts = 2;
   static constexpr int kSoftWarps = 4 * kParts;
-  static constexpr int kThreads = 32 * (kSoftWarps + kMiscWarps);
-  // registers after setmaxnreg, of 128 at launch: 2 x 216 + 2 x 40 = 4 x 128
-  static constexpr int kSoftRegs = 216, kMiscRegs = 40;
+  static constexpr int kThreads = 32 * (kSoftWarps + 4);
+  // registers after setmaxnreg, of 96 (640 threads) or 168 (384) at launch: 4 x 112 + 32 = 5 x 96, 2 x 232 + 40 = 3 x 168
+  static constexpr int kSoftRegs = 232, kMiscRegs = 40;
   static constexpr int HC = NR / kParts;       // rows of one softmax thread
   static constexpr uint32_t kQ8Chunk = 2 * NR * 128;
   static constexpr uint32_t kQ8 = 0;
@@ -88,25 +88,16 @@ struct DC {
   static constexpr uint32_t kRow = kRed + 4 * NR * 4;             // per softmax warp [HC] minus R, [HC] factor
   static constexpr uint32_t kBar = kRow + kSoftWarps * 2 * HC * 4;
   static constexpr uint32_t kBytes = kBar + 512;
-  static constexpr uint32_t kSCol = kPBufs * kOCols;              // score buffer i at kSCol + kOCols i
-  static constexpr uint32_t kHeld = kSCol + kSBufs * kOCols;      // accumulators of block b at kHeld + NR b
+  static constexpr uint32_t kSCol = kPBufs * kOCols;              // score buffer i at kSCol + 2 NR i
+  static constexpr uint32_t kHeld = kSCol + kSBufs * 2 * NR;      // accumulators of block b at kHeld + NR b
   static constexpr uint32_t kTmemCols = kHeld + kHeldBlocks * NR;
   static_assert(kBytes <= 232448, "shared memory");
   static_assert(kTmemCols == 512 || kTmemCols == 256, "TMEM allocations are powers of two");
 };
 
-// Weights buffer (and O^T slot) of block b, and the parity of its use in a tile whose number has parity `tile`: with
-// three buffers block 3 takes block 0's a second time.
-template <int NR>
-__device__ __forceinline__ int pbuf(int b) { return b < DC<NR>::kPBufs ? b : b - DC<NR>::kPBufs; }
-template <int NR>
-__device__ __forceinline__ uint32_t pparity(int b, uint32_t tile) {
-  return DC<NR>::kPBufs == 3 && (b == 0 || b == 3) ? (b == 3 ? 1u : 0u) : tile;
-}
-
 struct Bars {
   uint64_t kfull[12], kempty[12], sfull[4], sempty[4], scfull[3], scempty[3];
-  uint64_t pfull[4], pempty[4], qfull, drain;
+  uint64_t pfull[4], pempty[4], qfull, drain[2];
   uint32_t tmem;
   int abort;
   int armed_k[12], armed_sc[3];            // copies armed so far per slot
@@ -313,15 +304,15 @@ __device__ void drain_copies(uint64_t* bar, const int* armed, int n, int lane) {
 // ----------------------------------------------------------------------------- MMA issue
 
 template <int NR>
-__device__ void qk_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars* bars, int which, int lane) {
+__device__ void qk_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars* bars, int lane) {
   using C = DC<NR>;
-  constexpr uint32_t kIdescCodes = ptx::idesc_e4m3(128, C::kOCols), kIdescRope = ptx::idesc_bf16(128, NR);
+  constexpr uint32_t kIdescCodes = ptx::idesc_e4m3(128, 2 * NR), kIdescRope = ptx::idesc_bf16(128, NR);
   Walk w(bars);
   Ring<C::kRing> k;
   Ring<C::kSBufs> s;
   uint32_t qpar = 0;
   uint32_t ok = p.wait_ns >= kLeastWaitNs;
-  int item = -1, turn = which;                          // 0: the next chunk is this warp's
+  int item = -1;
   const uint64_t dq = ptx::sw128_desc(base + C::kQ8, 16, 1024), dr = ptx::sw128_desc(base + C::kQr, 16, 1024);
 #pragma unroll 1
   while (w.here(p)) {
@@ -332,79 +323,70 @@ __device__ void qk_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars
     }
 #pragma unroll 1
     for (int c = 0; c < kChunks; ++c) {
-      if (turn == 0) {
-        SMLA_WAIT(&bars->sempty[s.slot], s.parity ^ 1);
-        SMLA_WAIT(&bars->kfull[k.slot], k.parity);
-        ptx::tc_fence_after();
-        const uint32_t ks = k.slot, d = tmem + C::kSCol + C::kOCols * s.slot, cu = c;
-        if (ok && ptx::elect_one()) {
-          const uint64_t dk = ptx::sw128_desc(base + C::kK + ks * kSlot, 16, 1024);
-          if (c == 4) {
-  #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) ptx::mma_f16_ss(d, dk + 2 * kk, dr + 2 * kk, kIdescRope, kk > 0);
-          } else {
-            const uint64_t dqb = dq + (uint64_t)((cu * C::kQ8Chunk) >> 4);
-  #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-  #pragma unroll
-              for (int pass = 0; pass < C::kPasses; ++pass)
-                ptx::mma_f8_ss(d, dk + 2 * kk, dqb + 2 * kk + (uint64_t)((pass * NR * 128) >> 4), kIdescCodes, kk > 0 || pass > 0);
-          }
-          if (c == 4) ptx::mma_commit(&bars->kempty[k.slot]);   // the codes stay for the PV
-          ptx::mma_commit(&bars->sfull[s.slot]);
+      SMLA_WAIT(&bars->sempty[s.slot], s.parity ^ 1);
+      SMLA_WAIT(&bars->kfull[k.slot], k.parity);
+      ptx::tc_fence_after();
+      const uint32_t ks = k.slot, d = tmem + C::kSCol + 2 * NR * s.slot, cu = c;
+      if (ok && ptx::elect_one()) {
+        const uint64_t dk = ptx::sw128_desc(base + C::kK + ks * kSlot, 16, 1024);
+        if (c == 4) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) ptx::mma_f16_ss(d, dk + 2 * kk, dr + 2 * kk, kIdescRope, kk > 0);
+        } else {
+          const uint64_t dqb = dq + (uint64_t)((cu * C::kQ8Chunk) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) ptx::mma_f8_ss(d, dk + 2 * kk, dqb + 2 * kk, kIdescCodes, kk > 0);
         }
-        __syncwarp();
+        if (c == 4) ptx::mma_commit(&bars->kempty[k.slot]);   // the codes stay for the PV
+        ptx::mma_commit(&bars->sfull[s.slot]);
       }
-      turn = turn == 0 ? kIssuers - 1 : turn - 1;
+      __syncwarp();
       k.next();
       s.next();
     }
     w.next();
   }
-  if (ptx::elect_one()) ptx::mma_commit(&bars->drain);
+  if (ptx::elect_one()) ptx::mma_commit(&bars->drain[0]);
   __syncwarp();
 }
 
 template <int NR>
-__device__ void pv_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars* bars, int which, int lane) {
+__device__ void pv_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars* bars, int lane) {
   using C = DC<NR>;
   constexpr int N = C::kOCols;
   constexpr uint32_t kIdesc = ptx::idesc_e4m3(128, N) | (1u << 15) | (1u << 16);     // A and B MN-major
   Walk w(bars);
   Ring<C::kRing> k;
-  uint32_t tile = 0;
+  Ring<C::kPBufs> pb;
   uint32_t ok = p.wait_ns >= kLeastWaitNs;
 #pragma unroll 1
   while (w.here(p)) {
 #pragma unroll 1
     for (int b = 0; b < 4; ++b) {
-      // blocks 0 and 3 share a buffer, so one warp takes both (the waits on it alternate in parity)
-      if ((b == 1 || b == 2) == (which == 1)) {
-        const uint32_t ks = k.slot, ps = pbuf<NR>(b), d = tmem + N * ps;
-        SMLA_WAIT(&bars->pfull[ps], pparity<NR>(b, tile));
-        ptx::tc_fence_after();
-        if (ok && ptx::elect_one()) {
-          // codes^T: 128-byte rows of one position, 8-position groups 1024 bytes apart; 32 positions per MMA
-          const uint64_t dv = ptx::sw128_desc(base + C::kK + ks * kSlot, 1024, 1024);
-          const uint64_t dp = ptx::swz_desc(base + C::kP + ps * C::kPBuf, 8 * C::kPRow, 8 * C::kPRow, C::kPRow);
-  #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-  #pragma unroll
-            for (int pass = 0; pass < C::kPasses; ++pass)
-              ptx::mma_f8_ss(d, dv + (uint64_t)(256 * kk),
-                             dp + (uint64_t)((32 * C::kPRow * kk + NR * pass) >> 4), kIdesc, kk > 0 || pass > 0);
-          ptx::mma_commit(&bars->kempty[k.slot]);
-          ptx::mma_commit(&bars->pempty[ps]);
-        }
-        __syncwarp();
+      SMLA_WAIT(&bars->pfull[pb.slot], pb.parity);
+      ptx::tc_fence_after();
+      const uint32_t ks = k.slot, ps = pb.slot, d = tmem + N * pb.slot;
+      if (ok && ptx::elect_one()) {
+        // codes^T: 128-byte rows of one position, 8-position groups 1024 bytes apart; 32 positions per MMA
+        const uint64_t dv = ptx::sw128_desc(base + C::kK + ks * kSlot, 1024, 1024);
+        const uint64_t dp = ptx::swz_desc(base + C::kP + ps * C::kPBuf, 8 * C::kPRow, 8 * C::kPRow, C::kPRow);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+          for (int pass = 0; pass < C::kPasses; ++pass)
+            ptx::mma_f8_ss(d, dv + (uint64_t)(256 * kk),
+                           dp + (uint64_t)((32 * C::kPRow * kk + NR * pass) >> 4), kIdesc, kk > 0 || pass > 0);
+        ptx::mma_commit(&bars->kempty[k.slot]);
+        ptx::mma_commit(&bars->pempty[pb.slot]);
       }
+      __syncwarp();
       k.next();
+      pb.next();
     }
-    tile ^= 1;
     k.next();                                             // the rope
     w.next();
   }
-  if (ptx::elect_one()) ptx::mma_commit(&bars->drain);
+  if (ptx::elect_one()) ptx::mma_commit(&bars->drain[1]);
   __syncwarp();
 }
 
@@ -560,7 +542,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
   Walk w(bars);
   Ring<C::kSBufs> s;
   Ring<kScaleSlots> sc;
-  int kslot = 0;
+  int kslot = 0, pslot = 0;
   uint32_t dpar = 0;
   uint32_t ok = p.wait_ns >= kLeastWaitNs;
   bool first = true, begins = w.t == 0;
@@ -573,7 +555,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
   // Block b's O^T of one tile (pairs of rows); with `held`, its accumulators from TMEM in the same wait.
   auto tile_part = [&](int b, uint64_t (&x)[HC / 2], uint32_t (&held)[HC], bool load_held) {
     uint32_t hi[HC], lo[HC];
-    const uint32_t a = lane_base + C::kOCols * pbuf<NR>(b) + col0;
+    const uint32_t a = lane_base + C::kOCols * (b % C::kPBufs) + col0;
     tmem_ld<HC>(a, hi);
     if constexpr (C::kPasses == 1) tmem_ld<HC>(a + NR, lo);
     if (load_held) tmem_ld<HC>(lane_base + C::kHeld + NR * b + col0, held);
@@ -584,15 +566,15 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
       if constexpr (C::kPasses == 1) x[i] = ptx::add2(x[i], ptx::pack2(lo[2 * i], lo[2 * i + 1]));
     }
   };
-  auto wait_pv = [&](int b) {
-    SMLA_WAIT(&bars->pempty[pbuf<NR>(b)], pparity<NR>(b, dpar));
+  auto wait_pv = [&](int b, uint32_t parity) {
+    SMLA_WAIT(&bars->pempty[b % C::kPBufs], parity);
     ptx::tc_fence_after();
   };
   // adds a tile's blocks that are kept in registers (the PV of the tile before, see below)
   auto flush_registers = [&]() {
 #pragma unroll
     for (int b = C::kHeldBlocks; b < 4; ++b) {
-      wait_pv(b);
+      wait_pv(b, C::kHeldBlocks ? 1u : dpar);
       uint64_t x[HC / 2];
       uint32_t none[HC];
       tile_part(b, x, none, false);
@@ -604,11 +586,12 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
         d[1] = ptx::fma2(x[i + 1], c.y, d[1]);
       }
     }
+    dpar ^= 1;
     ptx::tc_fence_before();
   };
   // adds block b (held in TMEM); `start`: the segment's first tile
   auto flush_held = [&](int b, bool start) {
-    wait_pv(b);
+    wait_pv(b, 0u);
     uint64_t x[HC / 2];
     uint32_t h[HC];
     tile_part(b, x, h, true);                           // (before the segment's first tile: whatever was there)
@@ -626,14 +609,6 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
     tmem_st<HC>(lane_base + C::kHeld + NR * b + col0, h);
     ptx::tmem_wait_st();
     ptx::tc_fence_before();
-  };
-
-  // what is left of a tile once its weights are written: every block but the first (see there) of 64 rows
-  bool start = true;                                    // that tile was its segment's first
-  auto finish_tile = [&]() {
-    if constexpr (C::kHeldBlocks > 0) flush_held(1, start);
-    flush_registers();
-    dpar ^= 1;
   };
 
   int item = -1, done = -1;                             // items whose rows are loaded, whose segment has ended
@@ -654,7 +629,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
     if (!more) done = item;
     if (first && done >= 0) {
       const Rows it = rows_of(p, done);
-      finish_tile();
+      flush_registers();
       // row sums over the tile's 128 positions
       float ls[HC];
 #pragma unroll
@@ -738,21 +713,19 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
       for (int b = 0; b < 4; ++b) {
         SMLA_WAIT(&bars->sfull[s.slot], s.parity);
         ptx::tc_fence_after();
-        const uint32_t a = lane_base + C::kSCol + C::kOCols * s.slot + col0;
+        const uint32_t a = lane_base + C::kSCol + 2 * NR * s.slot + col0;
         const uint64_t scale = ptx::pack2(rot.x, rot.x);
         rot = make_float4(rot.y, rot.z, rot.w, rot.x);
 #pragma unroll
         for (int i0 = 0; i0 < HC; i0 += LC) {
           uint32_t hi[LC], lo[LC];
           tmem_ld<LC>(a + i0, hi);
-          if constexpr (C::kPasses == 1) tmem_ld<LC>(a + NR + i0, lo);
+          tmem_ld<LC>(a + NR + i0, lo);
           ptx::tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < LC; i += 2) {
-            uint64_t x = ptx::pack2(hi[i], hi[i + 1]);
-            if constexpr (C::kPasses == 1) x = ptx::add2(x, ptx::pack2(lo[i], lo[i + 1]));
-            acc[(i0 + i) / 2] = ptx::fma2(x, scale, acc[(i0 + i) / 2]);
-          }
+          for (int i = 0; i < LC; i += 2)
+            acc[(i0 + i) / 2] = ptx::fma2(ptx::add2(ptx::pack2(hi[i], hi[i + 1]), ptx::pack2(lo[i], lo[i + 1])), scale,
+                                          acc[(i0 + i) / 2]);
         }
         ptx::tc_fence_before();
         __syncwarp();
@@ -764,7 +737,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
     SMLA_WAIT(&bars->sfull[s.slot], s.parity);
     ptx::tc_fence_after();
     {
-      const uint32_t a = lane_base + C::kSCol + C::kOCols * s.slot + col0;
+      const uint32_t a = lane_base + C::kSCol + 2 * NR * s.slot + col0;
       const uint64_t kf2 = ptx::pack2(kf, kf), e2 = ptx::pack2((float)e, (float)e);
       const uint32_t fa = base + C::kF + (buf * NR + col0) * 4;
 #pragma unroll
@@ -800,7 +773,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
       if (!here || t >= w.n.min_len) clean_codes<NR>(base, kslot, tok, part, here && t < w.n.max_len);
     }
     kslot = kslot + kChunks >= C::kRing ? kslot + kChunks - C::kRing : kslot + kChunks;
-    if (!first) finish_tile();
+    if (!first) flush_registers();
     // R of each row: every warp ends with its rows' maxima over the 128 positions, lane -> row
     {
       float v[HC];
@@ -890,10 +863,10 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
           e4m3x4_to_f16x4(hi[i], bx, by);
           lo[i] = f16x4_to_e4m3x4(as_u32(__hsub2(x, as_half2(bx))), as_u32(__hsub2(y, as_half2(by))));
         }
-        // three buffers: the last block takes the first one's, after adding up its O^T; the other buffers are free,
-        // since the tile before has been added up
-        if (C::kHeldBlocks > 0 && b >= C::kPBufs) flush_held(0, first);
-        const uint32_t dst = base + C::kP + pbuf<NR>(b) * C::kPBuf;
+        // a tile's blocks beyond the buffers wait for the block before in theirs, and take its O^T; the others find
+        // their buffers free, since the tile before has been added up
+        if (C::kHeldBlocks > 0 && b >= C::kPBufs) flush_held(b - C::kPBufs, first);
+        const uint32_t dst = base + C::kP + pslot * C::kPBuf;
         if constexpr (HC >= 16) {
 #pragma unroll
           for (int u = 0; u < HC / 16; ++u) {
@@ -908,13 +881,13 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (ok && lane == 0) ptx::mbar_arrive(&bars->pfull[pbuf<NR>(b)]);
+        if (ok && lane == 0) ptx::mbar_arrive(&bars->pfull[pslot]);
+        pslot = pslot + 1 == C::kPBufs ? 0 : pslot + 1;
       }
     }
 
     const bool last = w.last_of_segment(), ends = w.t == w.n.tiles - 1;
     whole = begins && ends;
-    start = first;
     w.next();
     first = last;
   }
@@ -1021,7 +994,7 @@ __global__ void __launch_bounds__(DC<NR>::kThreads, 1)
       ptx::mbar_init(&bars->scempty[i], C::kSoftWarps);
       bars->armed_sc[i] = 0;
     }
-    ptx::mbar_init(&bars->drain, 2 * kIssuers);
+    for (int i = 0; i < 2; ++i) ptx::mbar_init(&bars->drain[i], 1);
     ptx::mbar_init(&bars->qfull, C::kSoftWarps);
     bars->abort = p.wait_ns < kLeastWaitNs;
     ptx::fence_mbar_init();
@@ -1043,8 +1016,8 @@ __global__ void __launch_bounds__(DC<NR>::kThreads, 1)
   } else {
     ptx::setmaxnreg_dec<C::kMiscRegs>();
     if (role == kCopyRole) copy_role<NR>(p, &map, &smap, base, bars, lane);
-    else if (role < kPvRole) qk_role<NR>(p, base, tmem, bars, role - kQkRole, lane);
-    else if (role < kPvRole + kIssuers) pv_role<NR>(p, base, tmem, bars, role - kPvRole, lane);
+    else if (role == kQkRole) qk_role<NR>(p, base, tmem, bars, lane);
+    else if (role == kPvRole) pv_role<NR>(p, base, tmem, bars, lane);
   }
 
   // nothing of this CTA's may be in flight when it leaves: the MMAs (their last commits) and, after a wait
@@ -1056,7 +1029,8 @@ __global__ void __launch_bounds__(DC<NR>::kThreads, 1)
     drain_copies(bars->scfull, bars->armed_sc, kScaleSlots, lane);
   }
   if (role == kQkRole) {
-    ptx::mbar_wait_warp(&bars->drain, 0, &never, lane, 100000000ull);
+    ptx::mbar_wait_warp(&bars->drain[0], 0, &never, lane, 100000000ull);
+    ptx::mbar_wait_warp(&bars->drain[1], 0, &never, lane, 100000000ull);
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, C::kTmemCols);
   }
