@@ -299,6 +299,9 @@ extern "C" int sparse_mla_kv_norm_append(const smla_norm_append_dims* d, const v
   p.interleaved = d->interleaved;
   p.eps = eps;
   p.err = err_word;
+  if (d->tokens == 0) return SMLA_OK;
+  const int st = sm_count_of_current_device(&p.sms);
+  if (st != SMLA_OK) return st;
   return launch_kv_norm_append(p, (cudaStream_t)stream) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
 }
 
@@ -354,6 +357,9 @@ extern "C" int sparse_mla_norm_rope(const smla_norm_rope_dims* d, const void* x,
   p.interleaved = d->interleaved;
   p.eps = eps;
   p.err = err_word;
+  if (d->tokens == 0) return SMLA_OK;
+  const int st = sm_count_of_current_device(&p.sms);
+  if (st != SMLA_OK) return st;
   return launch_norm_rope(p, (cudaStream_t)stream) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
 }
 

@@ -103,6 +103,7 @@ struct NormAppendParams {
   int tokens, num_requests, max_pages, max_positions;
   int dtype, weight_dtype;
   int interleaved;
+  int sms;                    // SMs of the device
   float eps;
   uint32_t* err;              // device error word (may be null)
 };
@@ -119,6 +120,7 @@ struct NormRopeParams {
   int64_t x_token, x_head, out_token, out_head;   // strides in elements
   int tokens, heads, dim, rope_dim, rope_offset, max_positions;
   int dtype, weight_dtype, norm, interleaved;
+  int sms;                    // SMs of the device
   float eps;
   uint32_t* err;              // device error word (may be null)
 };

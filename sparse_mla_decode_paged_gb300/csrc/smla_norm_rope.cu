@@ -76,72 +76,99 @@ __device__ __forceinline__ void load_weight(const void* w, int at, int weight_dt
 // ---------------------------------------------------------------------------- norm + rotation + append
 
 constexpr int kNormAppendWarps = 4;
+constexpr int kNormAppendBlocksPerSm = 16;
 
-// One warp per token.  Lane l holds latent dims 16 l .. 16 l + 15 (block l / 8 of 128 dims, so a block's
-// amax is a reduction over 8 lanes) and rope dims 2 l, 2 l + 1; the codes go out as one 16-byte store per
-// lane.  The weights stay in registers over the warp's tokens.
+// One token of a warp, as loaded: latent dims 8 l .. 8 l + 7 and 256 + 8 l .. (blocks l / 16 and 2 + l / 16, so a
+// block's amax is a reduction over 16 lanes, and every access of the warp is contiguous), rope dims 2 l, 2 l + 1, and
+// the block-table entry.
+struct AppendToken {
+  float x[16], r0, r1;
+  int pos, page;
+};
+
+template <typename T, bool kWide>
+__device__ __forceinline__ AppendToken append_load(const NormAppendParams& p, int tok, int lane) {
+  AppendToken a;
+  const T* row = static_cast<const T*>(p.latent) + (int64_t)tok * p.latent_stride + 8 * lane;
+  float (&lo)[8] = reinterpret_cast<float (&)[8]>(a.x[0]);
+  float (&hi)[8] = reinterpret_cast<float (&)[8]>(a.x[8]);
+  if constexpr (kWide) {
+    load_vec<8, T>(row, lo);
+    load_vec<8, T>(row + 256, hi);
+  } else {
+    load_each<8, T>(row, lo);
+    load_each<8, T>(row + 256, hi);
+  }
+  const T* rr = static_cast<const T*>(p.rope) + (int64_t)tok * p.rope_stride + 2 * lane;
+  a.r0 = to_f32<T>(rr[0]);
+  a.r1 = to_f32<T>(rr[1]);
+  const int req = p.requests ? __ldg(p.requests + tok) : tok;
+  a.pos = __ldg(p.positions + tok);
+  a.page = -1;
+  if (req >= 0 && req < p.num_requests && a.pos >= 0 && (a.pos >> 6) < p.max_pages && a.pos < p.max_positions)
+    a.page = __ldg(p.block_table + (size_t)req * p.max_pages + (a.pos >> 6));
+  return a;
+}
+
+// One warp per token, the weights in registers over the warp's tokens.  What bounds it: HBM bytes (1152 read, 256 of
+// cos and sin mostly from L2, 656 written per token of a 16-bit type).  Codes are n times the scale's reciprocal (one
+// reciprocal per block; sixteen divisions per lane took half the kernel's issue slots).
 template <typename T, bool kWide>
 __global__ void __launch_bounds__(32 * kNormAppendWarps) kv_norm_append_kernel(const NormAppendParams p) {
   const int lane = threadIdx.x & 31;
   const int warps = gridDim.x * kNormAppendWarps;
   float w[16];
-  load_weight<16, T>(p.weight, 16 * lane, p.weight_dtype, w);
-  for (int tok = blockIdx.x * kNormAppendWarps + (threadIdx.x >> 5); tok < p.tokens; tok += warps) {
-    const int req = p.requests ? __ldg(p.requests + tok) : tok;
-    const int pos = __ldg(p.positions + tok);
-    float x[16];
-    const T* row = static_cast<const T*>(p.latent) + (int64_t)tok * p.latent_stride + 16 * lane;
-    if constexpr (kWide) load_vec<16, T>(row, x); else load_each<16, T>(row, x);
-    const T* rr = static_cast<const T*>(p.rope) + (int64_t)tok * p.rope_stride + 2 * lane;
-    float r0 = to_f32<T>(rr[0]), r1 = to_f32<T>(rr[1]);
-    int page = -1;
-    if (req >= 0 && req < p.num_requests && pos >= 0 && (pos >> 6) < p.max_pages && pos < p.max_positions)
-      page = __ldg(p.block_table + (size_t)req * p.max_pages + (pos >> 6));
-    if (page < 0 || (int64_t)page >= p.num_pages) {
+  load_weight<8, T>(p.weight, 8 * lane, p.weight_dtype, reinterpret_cast<float (&)[8]>(w[0]));
+  load_weight<8, T>(p.weight, 256 + 8 * lane, p.weight_dtype, reinterpret_cast<float (&)[8]>(w[8]));
+  for (int64_t tok = blockIdx.x * kNormAppendWarps + (threadIdx.x >> 5); tok < p.tokens; tok += warps) {
+    AppendToken a = append_load<T, kWide>(p, (int)tok, lane);
+    if (a.page < 0 || (int64_t)a.page >= p.num_pages) {
       if (lane == 0 && p.err) atomicOr(p.err, SMLA_DEVERR_PAGE_RANGE);
       continue;                                      // warp-uniform
     }
-    unsigned char* rec = p.kv + ((int64_t)page * kPageSize + (pos & (kPageSize - 1))) * kRecordBytes;
-    const float* cs = p.cos_sin + (size_t)pos * kDRope;
+    unsigned char* rec = p.kv + ((int64_t)a.page * kPageSize + (a.pos & (kPageSize - 1))) * kRecordBytes;
+    const float* cs = p.cos_sin + (size_t)a.pos * kDRope;
 
     float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
+    for (int i = 0; i < 16; ++i) ss = fmaf(a.x[i], a.x[i], ss);
 #pragma unroll
     for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     const float inv = rsqrtf(ss * (1.f / kDLatent) + p.eps);
-    float amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      x[i] = x[i] * inv * w[i];
-      amax = fmaxf(amax, fabsf(x[i]));
+    for (int h = 0; h < 2; ++h) {
+      float* x = a.x + 8 * h;
+      float amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[i] = x[i] * inv * w[8 * h + i];
+        amax = fmaxf(amax, fabsf(x[i]));
+      }
+#pragma unroll
+      for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      const float scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+      const float up = __frcp_rn(scale);
+      uint32_t c[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        c[i] = (uint32_t)f32x2_to_e4m3x2(x[4 * i] * up, x[4 * i + 1] * up) |
+               ((uint32_t)f32x2_to_e4m3x2(x[4 * i + 2] * up, x[4 * i + 3] * up) << 16);
+      reinterpret_cast<uint2*>(rec)[32 * h + lane] = make_uint2(c[0], c[1]);
+      if ((lane & 15) == 0) reinterpret_cast<float*>(rec + kDLatent)[2 * h + (lane >> 4)] = scale;
     }
-#pragma unroll
-    for (int o = 4; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    // the quantisation of sparse_mla_kv_append: two correctly rounded fp32 divisions, then E4M3
-    const float scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
-    uint32_t c[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint16_t lo = f32x2_to_e4m3x2(__fdiv_rn(x[4 * i], scale), __fdiv_rn(x[4 * i + 1], scale));
-      const uint16_t hi = f32x2_to_e4m3x2(__fdiv_rn(x[4 * i + 2], scale), __fdiv_rn(x[4 * i + 3], scale));
-      c[i] = (uint32_t)lo | ((uint32_t)hi << 16);
-    }
-    reinterpret_cast<uint4*>(rec)[lane] = make_uint4(c[0], c[1], c[2], c[3]);
-    if ((lane & 7) == 0) reinterpret_cast<float*>(rec + kDLatent)[lane >> 3] = scale;
 
     float y0, y1;
     if (p.interleaved) {                             // this lane's two dims are pair `lane`
       const float co = __ldg(cs + lane), si = __ldg(cs + 32 + lane);
-      y0 = r0 * co - r1 * si;
-      y1 = r0 * si + r1 * co;
+      y0 = a.r0 * co - a.r1 * si;
+      y1 = a.r0 * si + a.r1 * co;
     } else {                                         // partners of dims 2 l, 2 l + 1 sit 16 lanes away
-      const float q0 = __shfl_xor_sync(0xffffffffu, r0, 16), q1 = __shfl_xor_sync(0xffffffffu, r1, 16);
+      const float q0 = __shfl_xor_sync(0xffffffffu, a.r0, 16), q1 = __shfl_xor_sync(0xffffffffu, a.r1, 16);
       const int j = (2 * lane) & 31;
       const float2 co = __ldg(reinterpret_cast<const float2*>(cs + j));
       const float2 si = __ldg(reinterpret_cast<const float2*>(cs + 32 + j));
-      y0 = lane < 16 ? r0 * co.x - q0 * si.x : q0 * si.x + r0 * co.x;
-      y1 = lane < 16 ? r1 * co.y - q1 * si.y : q1 * si.y + r1 * co.y;
+      y0 = lane < 16 ? a.r0 * co.x - q0 * si.x : q0 * si.x + a.r0 * co.x;
+      y1 = lane < 16 ? a.r1 * co.y - q1 * si.y : q1 * si.y + a.r1 * co.y;
     }
     reinterpret_cast<uint32_t*>(rec + kDLatent + 16)[lane] = f32x2_to_bf16x2(y0, y1);
   }
@@ -218,13 +245,136 @@ __global__ void __launch_bounds__(kNormRopeThreads) norm_rope_any_kernel(const N
   }
 }
 
+// Whole 16-byte units (E elements): kLanes lanes per row, kUnits units per lane (unit u = lane + kLanes i), 32 / kLanes
+// rows per warp at once; a lane keeps its units' weights over its rows.  What bounds it: HBM bytes (each element read
+// once and written once; the rows of cos and sin stay in L1 over a token's heads).
+template <typename T, int kLanes, int kUnits>
+__global__ void __launch_bounds__(kNormRopeThreads) norm_rope_kernel(const NormRopeParams p) {
+  constexpr int E = 16 / sizeof(T), kRows = 32 / kLanes;
+  const int lane = threadIdx.x & (kLanes - 1);
+  const int units = p.dim / E, half = p.rope_dim >> 1;
+  const uint32_t rows = (uint32_t)p.tokens * (uint32_t)p.heads;
+  const uint32_t step = gridDim.x * (kNormRopeThreads / kLanes);
+  const bool weighted = p.norm && p.weight;
+  float w[kUnits][E];
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const int u = lane + kLanes * i;
+    if (weighted && u < units) load_weight<E, T>(p.weight, u * E, p.weight_dtype, w[i]);
+    else
+#pragma unroll
+      for (int e = 0; e < E; ++e) w[i][e] = 1.f;
+  }
+  // the warps' trip counts are uniform: a warp whose last rows run out works on a row of nothing
+  for (uint32_t r0 = blockIdx.x * (kNormRopeThreads / kLanes) + (threadIdx.x >> 5) * kRows; r0 < rows; r0 += step) {
+    const uint32_t r = r0 + ((threadIdx.x & 31) / kLanes);
+    const bool here = r < rows;
+    const uint32_t t = here ? r / (uint32_t)p.heads : 0, h = here ? r - t * (uint32_t)p.heads : 0;
+    const T* x = static_cast<const T*>(p.x) + (int64_t)t * p.x_token + (int64_t)h * p.x_head;
+    T* out = static_cast<T*>(p.out) + (int64_t)t * p.out_token + (int64_t)h * p.out_head;
+    float v[kUnits][E], q[kUnits][E];
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int u = lane + kLanes * i;
+      if (here && u < units) load_vec<E, T>(x + u * E, v[i]);
+      else
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[i][e] = 0.f;
+    }
+    const int pos = p.rope_dim ? __ldg(p.positions + t) : 0;
+    const bool inside = p.rope_dim == 0 || (pos >= 0 && pos < p.max_positions);
+    if (p.rope_dim && !p.interleaved) {               // the partners, half the rotated dims away
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int o = (lane + kLanes * i) * E - p.rope_offset;
+        if (here && o >= 0 && o < p.rope_dim) load_vec<E, T>(x + (o < half ? o + half : o - half) + p.rope_offset, q[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i)
+#pragma unroll
+      for (int e = 0; e < E; ++e) ss = fmaf(v[i][e], v[i][e], ss);
+    float inv = 1.f;
+    if (p.norm) {
+#pragma unroll
+      for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      inv = rsqrtf(ss / (float)p.dim + p.eps);
+    }
+    __syncwarp();                                     // in place: every lane has read its units and partners
+    if (here && !inside && lane == 0 && p.err) atomicOr(p.err, SMLA_DEVERR_LEN_RANGE);
+    const float* cs = p.cos_sin + (size_t)(inside ? pos : 0) * p.rope_dim;
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int u = lane + kLanes * i, o = u * E - p.rope_offset;
+      if (!here || u >= units) continue;
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[i][e] = v[i][e] * inv * w[i][e];
+      if (o >= 0 && o < p.rope_dim) {
+        if (p.interleaved) {
+#pragma unroll
+          for (int e = 0; e < E; e += 2) {
+            const float c = __ldg(cs + (o + e) / 2), s = __ldg(cs + half + (o + e) / 2), a = v[i][e], b = v[i][e + 1];
+            v[i][e] = a * c - b * s;
+            v[i][e + 1] = a * s + b * c;
+          }
+        } else {
+          float wq[E];
+          const bool first = o < half;
+          if (weighted) load_weight<E, T>(p.weight, (first ? o + half : o - half) + p.rope_offset, p.weight_dtype, wq);
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const int j = (first ? o : o - half) + e;
+            const float c = __ldg(cs + j), s = __ldg(cs + half + j), b = q[i][e] * inv * (weighted ? wq[e] : 1.f);
+            v[i][e] = first ? v[i][e] * c - b * s : b * s + v[i][e] * c;
+          }
+        }
+      }
+      if (!inside)
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[i][e] = 0.f;
+      store_vec<E, T>(out + u * E, v[i]);
+    }
+  }
+}
+
+template <typename T>
+bool launch_norm_rope_wide(const NormRopeParams& p, cudaStream_t stream) {
+  constexpr int E = 16 / sizeof(T);
+  auto whole = [&](const void* q, int64_t a, int64_t b) {
+    return reinterpret_cast<uintptr_t>(q) % 16 == 0 && a % E == 0 && b % E == 0;
+  };
+  const int unit = p.interleaved ? E : 2 * E;           // a rotated half, or pairs, in whole units
+  if (p.dim % E || p.rope_offset % E || p.rope_dim % unit || !whole(p.x, p.x_token, p.x_head) ||
+      !whole(p.out, p.out_token, p.out_head) || (int64_t)p.tokens * p.heads > 0x7fffffff)
+    return false;
+  const int units = p.dim / E;
+  auto go = [&](auto kernel, int lanes) {
+    const int64_t per = kNormRopeThreads / lanes, want = ((int64_t)p.tokens * p.heads + per - 1) / per;
+    const int64_t most = (int64_t)p.sms * 8;            // blocks of 256 threads resident at once, at most
+    kernel<<<(int)(want < most ? want : most), kNormRopeThreads, 0, stream>>>(p);
+    return true;
+  };
+  // up to 32 units (256 elements of 16 bits) a row is eight lanes', so that short rows fill the warp
+  if (units <= 8) return go(norm_rope_kernel<T, 8, 1>, 8);
+  if (units <= 16) return go(norm_rope_kernel<T, 8, 2>, 8);
+  if (units <= 24) return go(norm_rope_kernel<T, 8, 3>, 8);
+  if (units <= 32) return go(norm_rope_kernel<T, 8, 4>, 8);
+  if (units <= 64) return go(norm_rope_kernel<T, 32, 2>, 32);
+  if (units <= 96) return go(norm_rope_kernel<T, 32, 3>, 32);
+  if (units <= 128) return go(norm_rope_kernel<T, 32, 4>, 32);
+  if (units <= 160) return go(norm_rope_kernel<T, 32, 5>, 32);
+  return go(norm_rope_kernel<T, 32, 8>, 32);
+}
+
 }  // namespace
 
 cudaError_t launch_kv_norm_append(const NormAppendParams& p, cudaStream_t stream) {
   if (p.tokens == 0) return cudaSuccess;
   const int esz = p.dtype == SMLA_FP32 ? 4 : 2;
   const bool wide = reinterpret_cast<uintptr_t>(p.latent) % 16 == 0 && (p.latent_stride * esz) % 16 == 0;
-  const int blocks = (p.tokens + kNormAppendWarps - 1) / kNormAppendWarps;
+  const int want = (int)(((int64_t)p.tokens + kNormAppendWarps - 1) / kNormAppendWarps);
+  const int blocks = want < p.sms * kNormAppendBlocksPerSm ? want : p.sms * kNormAppendBlocksPerSm;
   auto go = [&](auto kernel) { kernel<<<blocks, 32 * kNormAppendWarps, 0, stream>>>(p); };
   if (p.dtype == SMLA_BF16)
     wide ? go(kv_norm_append_kernel<__nv_bfloat16, true>) : go(kv_norm_append_kernel<__nv_bfloat16, false>);
@@ -238,6 +388,10 @@ cudaError_t launch_kv_norm_append(const NormAppendParams& p, cudaStream_t stream
 cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t stream) {
   const int64_t rows = (int64_t)p.tokens * p.heads;
   if (rows == 0) return cudaSuccess;
+  const bool wide = p.dtype == SMLA_BF16   ? launch_norm_rope_wide<__nv_bfloat16>(p, stream)
+                    : p.dtype == SMLA_FP16 ? launch_norm_rope_wide<__half>(p, stream)
+                                           : launch_norm_rope_wide<float>(p, stream);
+  if (wide) return cudaGetLastError();
   const int64_t want = (rows + kNormRopeThreads / 32 - 1) / (kNormRopeThreads / 32);
   const int blocks = (int)(want < (1 << 20) ? want : (1 << 20));
   auto go = [&](auto kernel) { kernel<<<blocks, kNormRopeThreads, 0, stream>>>(p); };
