@@ -233,16 +233,19 @@ def _err_word(t, dev):
 class _on:
     """The stream a call launches on (the caller's, or its device's current one), with the tensors' device
     current and, for a stream of the caller's, allocations made on it."""
+    __slots__ = ("raw", "ctx")
 
     def __init__(self, dev, stream=None):
-        self.raw = (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
         self.ctx = None
-        if stream is not None:
+        if stream is None:
+            self.raw = torch._C._cuda_getCurrentRawStream(dev.index)      # current_stream(dev) without its object
+            if dev.index != torch.cuda.current_device():
+                self.ctx = torch.cuda.device(dev)
+        else:
             if stream.device != dev:
                 raise ValueError(f"stream must belong to {dev}, got {stream.device}")
+            self.raw = stream.cuda_stream
             self.ctx = torch.cuda.stream(stream)
-        elif dev.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(dev)
 
     def __enter__(self):
         if self.ctx is not None:
