@@ -418,22 +418,45 @@ __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint3
 template <int NR>
 __device__ __forceinline__ void load_q(const DenseParams& p, int item, unsigned char* sm, uint32_t base, int buf, int warp, int lane) {
   using C = DC<NR>;
+  constexpr int kRows = NR / C::kSoftWarps;             // rows warp, warp + kSoftWarps, ... of this warp
   const Rows it = rows_of(p, item);
   float* f = reinterpret_cast<float*>(sm + C::kF) + buf * NR;
   int* lens = reinterpret_cast<int*>(sm + C::kLen) + buf * NR;
   const float kf = p.sm_scale * kLog2e;
   const uint16_t* q0 = p.q + ((size_t)it.req * p.q_per_req * p.H + it.row0) * kDQK;
   const int b = lane >> 3, u = lane & 7;
-#pragma unroll 1
-  for (int r = warp; r < NR; r += C::kSoftWarps) {
-    uint4 raw[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)}, rope = raw[0];
+  uint4 raw[kRows][2], rope[(kRows + 3) / 4];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int r = warp + C::kSoftWarps * i;
+    const uint4* src = reinterpret_cast<const uint4*>(q0 + (size_t)r * kDQK);
+    raw[i][0] = raw[i][1] = make_uint4(0u, 0u, 0u, 0u);
     if (r < it.nrows) {
-      const uint4* src = reinterpret_cast<const uint4*>(q0 + (size_t)r * kDQK);
-      raw[0] = __ldg(src + 2 * lane);
-      raw[1] = __ldg(src + 2 * lane + 1);
-      if (lane < 8) rope = __ldg(src + 64 + lane);
+      raw[i][0] = __ldg(src + 2 * lane);
+      raw[i][1] = __ldg(src + 2 * lane + 1);
     }
-    const uint32_t wds[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
+  }
+  // the rope, 16 bytes per lane: four rows at a time
+#pragma unroll
+  for (int i = 0; i < (kRows + 3) / 4; ++i) {
+    const int k = 4 * i + b, r = warp + C::kSoftWarps * k;
+    rope[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (k < kRows && r < it.nrows) rope[i] = __ldg(reinterpret_cast<const uint4*>(q0 + (size_t)r * kDQK) + 64 + u);
+  }
+  if (lane < kRows) {
+    const int r = warp + C::kSoftWarps * lane;
+    lens[r] = r < it.nrows ? clamped_len(p, it.req * p.q_per_req + (it.row0 + r) / p.H) : 0x7fffffff;
+  }
+#pragma unroll
+  for (int i = 0; i < (kRows + 3) / 4; ++i) {
+    const int k = 4 * i + b;
+    if (k < kRows) ptx::sts128(base + C::kQr + swz128(warp + C::kSoftWarps * k, u), rope[i]);
+  }
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    const int r = warp + C::kSoftWarps * k;
+    const uint32_t wds[8] = {raw[k][0].x, raw[k][0].y, raw[k][0].z, raw[k][0].w,
+                             raw[k][1].x, raw[k][1].y, raw[k][1].z, raw[k][1].w};
     float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -462,11 +485,7 @@ __device__ __forceinline__ void load_q(const DenseParams& p, int item, unsigned 
     const uint32_t q8 = base + C::kQ8 + b * C::kQ8Chunk;
     ptx::sts128(q8 + swz128(r, u), make_uint4(hi[0], hi[1], hi[2], hi[3]));
     ptx::sts128(q8 + swz128(NR + r, u), make_uint4(lo[0], lo[1], lo[2], lo[3]));
-    if (lane < 8) ptx::sts128(base + C::kQr + swz128(r, lane), rope);
-    if (lane == 0) {
-      f[r] = exp2_int(x) * kf;
-      lens[r] = r < it.nrows ? clamped_len(p, it.req * p.q_per_req + (it.row0 + r) / p.H) : 0x7fffffff;
-    }
+    if (lane == 0) f[r] = exp2_int(x) * kf;
   }
 }
 
@@ -525,6 +544,27 @@ __device__ __noinline__ void clean_codes(uint32_t base, int slot, int tok, int p
       }
     }
     if (++slot == C::kRing) slot = 0;
+  }
+}
+
+// One dim of a block for HC rows (pairs), times the rows' factors, out to global memory: lanes 2j, 2j + 1 hold dims
+// d, d + 1 of two rows; the first ends with both dims of the first row, the other (`second`) with both of the second,
+// and stores them at `to` (rows 2 apart; `left` of them from this thread's first on), as bf16 or fp32.
+template <int HC, bool kBf16>
+__device__ __forceinline__ void write_block(const uint64_t (&x)[HC / 2], uint32_t row_c, int left, bool second, void* to) {
+#pragma unroll
+  for (int i = 0; i < HC / 2; i += 2) {
+    const ulonglong2 f = ptx::lds128_pairs(row_c + i * 8);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float2 v = ptx::unpack2(ptx::mul2(x[i + j], j ? f.y : f.x));
+      const float got = __shfl_xor_sync(0xffffffffu, second ? v.x : v.y, 1);
+      const float d0 = second ? got : v.x, d1 = second ? v.y : got;
+      if (2 * (i + j) < left) {
+        if constexpr (kBf16) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(to) + 2 * (i + j) * kDLatent) = f32x2_to_bf16x2(d0, d1);
+        else *reinterpret_cast<float2*>(static_cast<float*>(to) + 2 * (i + j) * kDLatent) = make_float2(d0, d1);
+      }
+    }
   }
 }
 
@@ -654,35 +694,33 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
           else lse_part[slot * NR + col0 + lane] = lse;
         }
       }
+      // the rows' factors 1 / l, read back as pairs
+      if (lane < HC) ptx::sts32f(row_c + lane * 4, inv);
+      __syncwarp();
       // lanes 2j, 2j + 1 hold dims d, d + 1 of two rows: the first ends with both dims of the first row, the other
-      // with both of the second
+      // with both of the second, and writes them there
       const bool second = lane & 1;
+      const int c0 = col0 + (second ? 1 : 0);             // this thread's rows: c0, c0 + 2, ...
+      const bool all = ok && it.nrows == NR;
       const size_t row0 = whole ? (size_t)it.req * p.q_per_req * p.H + it.row0 : slot * NR;
-      auto write_pair = [&](int b, int i, float2 x) {
-        const float va = x.x * __shfl_sync(0xffffffffu, inv, i), vb = x.y * __shfl_sync(0xffffffffu, inv, i + 1);
-        const float got = __shfl_xor_sync(0xffffffffu, second ? va : vb, 1);
-        const float d0 = second ? got : va, d1 = second ? vb : got;
-        const int c = col0 + i + (second ? 1 : 0);
-        if (ok && c < it.nrows) {
-          const size_t at = (row0 + c) * kDLatent + 128 * b + (tok & ~1);
-          if (whole) *reinterpret_cast<uint32_t*>(p.out + at) = f32x2_to_bf16x2(d0, d1);
-          else *reinterpret_cast<float2*>(o_part + at) = make_float2(d0, d1);
-        }
-      };
+      const size_t at = (row0 + c0) * kDLatent + (tok & ~1);
+      const int rows_left = ok ? (all ? NR : it.nrows - c0) : 0;
 #pragma unroll
-      for (int b = C::kHeldBlocks; b < 4; ++b)
-#pragma unroll
-        for (int i = 0; i < HC; i += 2) write_pair(b, i, ptx::unpack2(o[b - C::kHeldBlocks][i / 2]));
+      for (int b = C::kHeldBlocks; b < 4; ++b) {
+        if (whole) write_block<HC, true>(o[b - C::kHeldBlocks], row_c, rows_left, second, p.out + at + 128 * b);
+        else write_block<HC, false>(o[b - C::kHeldBlocks], row_c, rows_left, second, o_part + at + 128 * b);
+      }
 #pragma unroll 1
-      for (int b = 0; b < C::kHeldBlocks; ++b)
-#pragma unroll 1
-        for (int i0 = 0; i0 < HC; i0 += 8) {
-          uint32_t h[8];
-          ptx::tmem_ld8(lane_base + C::kHeld + NR * b + col0 + i0, h);
-          ptx::tmem_wait_ld();
+      for (int b = 0; b < C::kHeldBlocks; ++b) {
+        uint32_t h[HC];
+        uint64_t x[HC / 2];
+        tmem_ld<HC>(lane_base + C::kHeld + NR * b + col0, h);
+        ptx::tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 8; i += 2) write_pair(b, i0 + i, make_float2(__uint_as_float(h[i]), __uint_as_float(h[i + 1])));
-        }
+        for (int i = 0; i < HC / 2; ++i) x[i] = ptx::pack2(h[2 * i], h[2 * i + 1]);
+        if (whole) write_block<HC, true>(x, row_c, rows_left, second, p.out + at + 128 * b);
+        else write_block<HC, false>(x, row_c, rows_left, second, o_part + at + 128 * b);
+      }
       begins = true;
     }
     if (!more) break;
@@ -1039,18 +1077,21 @@ __global__ void __launch_bounds__(DC<NR>::kThreads, 1)
 
 // ----------------------------------------------------------------------------- merge
 
-constexpr int kMergeThreads = 128;        // 4 output dims per thread
+constexpr int kMergeThreads = 128;        // four warps share a row's partials, each lane 4 of 128 dims
 constexpr int kMergeBatch = 8;            // partial rows in flight per thread
 
 // Joins the partials of the items that cross CTA runs: lse = ln sum_s exp(lse_s), out = sum_s exp(lse_s - lse)
 // o_s.  An item that begins in CTA c and ends in CTA c1 left its partials in slot 1 of c and slot 0 of
-// c + 1 .. c1.  Every CTA lists those items from the run descriptors and takes rows of them in turn.
+// c + 1 .. c1.  Every CTA lists those items from the run descriptors and takes (row, 128 dims)
+// of them in turn.  Bound by the latency of the partials (in L2) for a single long item of many parts, so a row's
+// partials are spread over four warps and its dims over four CTAs.
 __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const DenseParams p, const RunDesc* descs,
                                                                     const float* lse_part, const float* o_part) {
   __shared__ int list_s[kDenseMaxCtas];
   __shared__ float w_s[kDenseMaxCtas];
   __shared__ int n_s;
   __shared__ float lse_s;
+  __shared__ float4 sum_s[4][32];
   const int tid = threadIdx.x, lane = tid & 31;
   ptx::griddep_wait();
   const long long T = descs[0].total;
@@ -1073,9 +1114,9 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const DenseP
     if (lane == 0) n_s = n;
   }
   __syncthreads();
-  const int nr = p.nr, work = n_s * nr;
+  const int nr = p.nr, work = n_s * nr * 4, warp = tid >> 5;
   for (int idx = blockIdx.x; idx < work; idx += gridDim.x) {
-    const int c = list_s[idx / nr], row = idx % nr;
+    const int c = list_s[idx / (4 * nr)], row = (idx >> 2) % nr, block = idx & 3;
     const RunDesc d = descs[c];
     const Rows it = rows_of(p, d.item);
     if (row >= it.nrows) continue;                       // uniform over the CTA
@@ -1084,58 +1125,72 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const DenseP
     while (c1 + 1 < active && run_start(T, active, c1 + 1) < d.item_end) ++c1;
     const int parts = c1 - c + 1;
     auto slot = [&](int s) { return s == 0 ? 2 * (size_t)c + 1 : 2 * (size_t)(c + s); };
-    const float4* rows = reinterpret_cast<const float4*>(o_part) + tid;
+    // warp w takes parts w, w + 4, ...: their rows in flight before the weights are known
+    const float4* rows = reinterpret_cast<const float4*>(o_part) + 32 * block + lane;
     auto at = [&](int s) { return (slot(s) * nr + row) * (kDLatent / 4); };
     float4 v[kMergeBatch];
 #pragma unroll
-    for (int s = 0; s < kMergeBatch; ++s) v[s] = s < parts ? __ldg(rows + at(s)) : make_float4(0.f, 0.f, 0.f, 0.f);
-    __syncthreads();                                     // w_s of the row before has been read
-    if (tid < 32) {
+    for (int s = 0; s < kMergeBatch; ++s)
+      v[s] = warp + 4 * s < parts ? __ldg(rows + at(warp + 4 * s)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    __syncthreads();                                     // w_s and sum_s of the row before have been read
+    if (warp == 0) {
       float m = -CUDART_INF_F;
       bool bad = false;
       for (int s = lane; s < parts; s += 32) {
         const float x = __ldg(lse_part + slot(s) * nr + row);
         bad |= isnan(x);
         m = fmaxf(m, x);
+        w_s[s] = x;
       }
 #pragma unroll
       for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       if (__any_sync(0xffffffffu, bad)) m = CUDART_NAN_F;
       float z = 0.f;
       for (int s = lane; s < parts; s += 32) {
-        const float e = m == -CUDART_INF_F ? 0.f : expf(__ldg(lse_part + slot(s) * nr + row) - m);
+        const float e = m == -CUDART_INF_F ? 0.f : expf(w_s[s] - m);
         w_s[s] = e;
         z += e;
       }
 #pragma unroll
       for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
       const float inv = z == 0.f ? 0.f : 1.f / z;
-      __syncwarp();
       for (int s = lane; s < parts; s += 32) w_s[s] *= inv;
       if (lane == 0) lse_s = z == 0.f ? -CUDART_INF_F : m + logf(z);
     }
     __syncthreads();
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < parts; s0 += kMergeBatch) {
+    for (int s0 = 0; warp + 4 * s0 < parts; s0 += kMergeBatch) {
       if (s0 > 0) {
 #pragma unroll
         for (int s = 0; s < kMergeBatch; ++s)
-          v[s] = s0 + s < parts ? __ldg(rows + at(s0 + s)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          v[s] = warp + 4 * (s0 + s) < parts ? __ldg(rows + at(warp + 4 * (s0 + s))) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
       for (int s = 0; s < kMergeBatch; ++s) {
-        if (s0 + s >= parts) break;
-        const float w = w_s[s0 + s];
+        if (warp + 4 * (s0 + s) >= parts) break;
+        const float w = w_s[warp + 4 * (s0 + s)];
         acc.x = fmaf(w, v[s].x, acc.x);
         acc.y = fmaf(w, v[s].y, acc.y);
         acc.z = fmaf(w, v[s].z, acc.z);
         acc.w = fmaf(w, v[s].w, acc.w);
       }
     }
+    sum_s[warp][lane] = acc;
+    __syncthreads();
     const size_t out_row = (size_t)it.req * p.q_per_req * p.H + it.row0 + row;
-    reinterpret_cast<uint2*>(p.out + out_row * kDLatent)[tid] =
-        make_uint2(f32x2_to_bf16x2(acc.x, acc.y), f32x2_to_bf16x2(acc.z, acc.w));
-    if (tid == 0) p.lse[out_row] = lse_s;
+    if (warp == 0) {
+#pragma unroll
+      for (int s = 1; s < 4; ++s) {
+        const float4 o = sum_s[s][lane];
+        acc.x += o.x;
+        acc.y += o.y;
+        acc.z += o.z;
+        acc.w += o.w;
+      }
+      reinterpret_cast<uint2*>(p.out + out_row * kDLatent + 128 * block)[lane] =
+          make_uint2(f32x2_to_bf16x2(acc.x, acc.y), f32x2_to_bf16x2(acc.z, acc.w));
+      if (lane == 0 && block == 0) p.lse[out_row] = lse_s;
+    }
   }
 }
 
