@@ -59,11 +59,11 @@ template <int NR>
 struct DC {
   static constexpr int kRing = NR == 64 ? 7 : NR == 32 ? 9 : 11;    // K slots
   static constexpr int kPBufs = NR == 64 ? 2 : 4;                   // weights of so many blocks
-  static constexpr int kSBufs = NR == 64 ? 2 : 4;                   // score accumulators
-  // hi and lo weights meet in one accumulator for 64 rows (TMEM is full); for fewer rows they are one MMA of twice
-  // the columns and meet in the registers
+  static constexpr int kSBufs = 4;                                  // score accumulators
+  // hi and lo terms (of q, and of the weights) meet in one accumulator for 64 rows, where TMEM is full; for fewer rows
+  // they are one MMA of twice the columns and meet in the registers
   static constexpr int kPasses = NR == 64 ? 2 : 1;
-  static constexpr int kOCols = NR == 64 ? NR : 2 * NR;             // columns of a block's O^T of one tile
+  static constexpr int kOCols = NR == 64 ? NR : 2 * NR;             // columns of a block's O^T of one tile, or scores
   // TMEM: O^T of one tile (kPBufs blocks at a time), score buffers, and for 64 rows, whose accumulators do not all fit
   // the registers, those of blocks 0 and 1
   static constexpr int kHeldBlocks = NR == 64 ? 2 : 0;
@@ -88,8 +88,8 @@ struct DC {
   static constexpr uint32_t kRow = kRed + 4 * NR * 4;             // per softmax warp [HC] minus R, [HC] factor
   static constexpr uint32_t kBar = kRow + kSoftWarps * 2 * HC * 4;
   static constexpr uint32_t kBytes = kBar + 512;
-  static constexpr uint32_t kSCol = kPBufs * kOCols;              // score buffer i at kSCol + 2 NR i
-  static constexpr uint32_t kHeld = kSCol + kSBufs * 2 * NR;      // accumulators of block b at kHeld + NR b
+  static constexpr uint32_t kSCol = kPBufs * kOCols;              // score buffer i at kSCol + kOCols i
+  static constexpr uint32_t kHeld = kSCol + kSBufs * kOCols;      // accumulators of block b at kHeld + NR b
   static constexpr uint32_t kTmemCols = kHeld + kHeldBlocks * NR;
   static_assert(kBytes <= 232448, "shared memory");
   static_assert(kTmemCols == 512 || kTmemCols == 256, "TMEM allocations are powers of two");
@@ -306,7 +306,7 @@ __device__ void drain_copies(uint64_t* bar, const int* armed, int n, int lane) {
 template <int NR>
 __device__ void qk_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars* bars, int lane) {
   using C = DC<NR>;
-  constexpr uint32_t kIdescCodes = ptx::idesc_e4m3(128, 2 * NR), kIdescRope = ptx::idesc_bf16(128, NR);
+  constexpr uint32_t kIdescCodes = ptx::idesc_e4m3(128, C::kOCols), kIdescRope = ptx::idesc_bf16(128, NR);
   Walk w(bars);
   Ring<C::kRing> k;
   Ring<C::kSBufs> s;
@@ -326,7 +326,7 @@ __device__ void qk_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars
       SMLA_WAIT(&bars->sempty[s.slot], s.parity ^ 1);
       SMLA_WAIT(&bars->kfull[k.slot], k.parity);
       ptx::tc_fence_after();
-      const uint32_t ks = k.slot, d = tmem + C::kSCol + 2 * NR * s.slot, cu = c;
+      const uint32_t ks = k.slot, d = tmem + C::kSCol + C::kOCols * s.slot, cu = c;
       if (ok && ptx::elect_one()) {
         const uint64_t dk = ptx::sw128_desc(base + C::kK + ks * kSlot, 16, 1024);
         if (c == 4) {
@@ -335,7 +335,10 @@ __device__ void qk_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars
         } else {
           const uint64_t dqb = dq + (uint64_t)((cu * C::kQ8Chunk) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) ptx::mma_f8_ss(d, dk + 2 * kk, dqb + 2 * kk, kIdescCodes, kk > 0);
+          for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+            for (int pass = 0; pass < C::kPasses; ++pass)
+              ptx::mma_f8_ss(d, dk + 2 * kk, dqb + 2 * kk + (uint64_t)((pass * NR * 128) >> 4), kIdescCodes, kk > 0 || pass > 0);
         }
         if (c == 4) ptx::mma_commit(&bars->kempty[k.slot]);   // the codes stay for the PV
         ptx::mma_commit(&bars->sfull[s.slot]);
@@ -751,19 +754,21 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
       for (int b = 0; b < 4; ++b) {
         SMLA_WAIT(&bars->sfull[s.slot], s.parity);
         ptx::tc_fence_after();
-        const uint32_t a = lane_base + C::kSCol + 2 * NR * s.slot + col0;
+        const uint32_t a = lane_base + C::kSCol + C::kOCols * s.slot + col0;
         const uint64_t scale = ptx::pack2(rot.x, rot.x);
         rot = make_float4(rot.y, rot.z, rot.w, rot.x);
 #pragma unroll
         for (int i0 = 0; i0 < HC; i0 += LC) {
           uint32_t hi[LC], lo[LC];
           tmem_ld<LC>(a + i0, hi);
-          tmem_ld<LC>(a + NR + i0, lo);
+          if constexpr (C::kPasses == 1) tmem_ld<LC>(a + NR + i0, lo);
           ptx::tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < LC; i += 2)
-            acc[(i0 + i) / 2] = ptx::fma2(ptx::add2(ptx::pack2(hi[i], hi[i + 1]), ptx::pack2(lo[i], lo[i + 1])), scale,
-                                          acc[(i0 + i) / 2]);
+          for (int i = 0; i < LC; i += 2) {
+            uint64_t x = ptx::pack2(hi[i], hi[i + 1]);
+            if constexpr (C::kPasses == 1) x = ptx::add2(x, ptx::pack2(lo[i], lo[i + 1]));
+            acc[(i0 + i) / 2] = ptx::fma2(x, scale, acc[(i0 + i) / 2]);
+          }
         }
         ptx::tc_fence_before();
         __syncwarp();
@@ -775,7 +780,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
     SMLA_WAIT(&bars->sfull[s.slot], s.parity);
     ptx::tc_fence_after();
     {
-      const uint32_t a = lane_base + C::kSCol + 2 * NR * s.slot + col0;
+      const uint32_t a = lane_base + C::kSCol + C::kOCols * s.slot + col0;
       const uint64_t kf2 = ptx::pack2(kf, kf), e2 = ptx::pack2((float)e, (float)e);
       const uint32_t fa = base + C::kF + (buf * NR + col0) * 4;
 #pragma unroll
