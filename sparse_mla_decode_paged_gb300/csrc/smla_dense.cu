@@ -637,6 +637,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
     wait_pv(b, 0u);
     uint64_t x[HC / 2];
     uint32_t h[HC];
+    ptx::tmem_wait_st();                                // the last tile's
     tile_part(b, x, h, true);                           // (before the segment's first tile: whatever was there)
 #pragma unroll
     for (int i = 0; i < HC / 2; i += 2) {
@@ -650,7 +651,6 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
       }
     }
     tmem_st<HC>(lane_base + C::kHeld + NR * b + col0, h);
-    ptx::tmem_wait_st();
     ptx::tc_fence_before();
   };
 
@@ -717,6 +717,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
       for (int b = 0; b < C::kHeldBlocks; ++b) {
         uint32_t h[HC];
         uint64_t x[HC / 2];
+        ptx::tmem_wait_st();
         tmem_ld<HC>(lane_base + C::kHeld + NR * b + col0, h);
         ptx::tmem_wait_ld();
 #pragma unroll
@@ -750,30 +751,41 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
       float4 rot = s4;
 #pragma unroll
       for (int i = 0; i < HC / 2; ++i) acc[i] = 0;
+      // two blocks at a time: their TMEM loads wait once
 #pragma unroll 1
-      for (int b = 0; b < 4; ++b) {
+      for (int b = 0; b < 4; b += 2) {
+        const uint32_t a0 = lane_base + C::kSCol + C::kOCols * s.slot + col0;
+        const int s0 = s.slot;
         SMLA_WAIT(&bars->sfull[s.slot], s.parity);
+        s.next();
+        const uint32_t a1 = lane_base + C::kSCol + C::kOCols * s.slot + col0;
+        const int s1 = s.slot;
+        SMLA_WAIT(&bars->sfull[s.slot], s.parity);
+        s.next();
         ptx::tc_fence_after();
-        const uint32_t a = lane_base + C::kSCol + C::kOCols * s.slot + col0;
-        const uint64_t scale = ptx::pack2(rot.x, rot.x);
-        rot = make_float4(rot.y, rot.z, rot.w, rot.x);
+        const uint64_t scale0 = ptx::pack2(rot.x, rot.x), scale1 = ptx::pack2(rot.y, rot.y);
+        rot = make_float4(rot.z, rot.w, rot.x, rot.y);
+        uint32_t x0[HC], y0[HC], x1[HC], y1[HC];
+        tmem_ld<HC>(a0, x0);
+        if constexpr (C::kPasses == 1) tmem_ld<HC>(a0 + NR, y0);
+        tmem_ld<HC>(a1, x1);
+        if constexpr (C::kPasses == 1) tmem_ld<HC>(a1 + NR, y1);
+        ptx::tmem_wait_ld();
 #pragma unroll
-        for (int i0 = 0; i0 < HC; i0 += LC) {
-          uint32_t hi[LC], lo[LC];
-          tmem_ld<LC>(a + i0, hi);
-          if constexpr (C::kPasses == 1) tmem_ld<LC>(a + NR + i0, lo);
-          ptx::tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < LC; i += 2) {
-            uint64_t x = ptx::pack2(hi[i], hi[i + 1]);
-            if constexpr (C::kPasses == 1) x = ptx::add2(x, ptx::pack2(lo[i], lo[i + 1]));
-            acc[(i0 + i) / 2] = ptx::fma2(x, scale, acc[(i0 + i) / 2]);
+        for (int i = 0; i < HC; i += 2) {
+          uint64_t x = ptx::pack2(x0[i], x0[i + 1]), y = ptx::pack2(x1[i], x1[i + 1]);
+          if constexpr (C::kPasses == 1) {
+            x = ptx::add2(x, ptx::pack2(y0[i], y0[i + 1]));
+            y = ptx::add2(y, ptx::pack2(y1[i], y1[i + 1]));
           }
+          acc[i / 2] = ptx::fma2(y, scale1, ptx::fma2(x, scale0, acc[i / 2]));
         }
         ptx::tc_fence_before();
         __syncwarp();
-        if (ok && lane == 0) ptx::mbar_arrive(&bars->sempty[s.slot]);
-        s.next();
+        if (ok && lane == 0) {
+          ptx::mbar_arrive(&bars->sempty[s0]);
+          ptx::mbar_arrive(&bars->sempty[s1]);
+        }
       }
     }
     // s + e, as 2^x (latent part) + (rope part sm_scale log2 e + e)
@@ -818,16 +830,11 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
     kslot = kslot + kChunks >= C::kRing ? kslot + kChunks - C::kRing : kslot + kChunks;
     if (!first) flush_registers();
     // R of each row: every warp ends with its rows' maxima over the 128 positions, lane -> row
-    {
-      float v[HC];
 #pragma unroll
-      for (int i = 0; i < HC / 2; ++i) {
-        const float2 d = ptx::unpack2(acc[i]);
-        v[2 * i] = d.x;
-        v[2 * i + 1] = d.y;
-      }
-      const float m = reduce_scatter<HC>(v, lane, [](float a, float b) { return fmaxf(a, b); });
-      if (lane < HC) red[quad * NR + lane] = m;
+    for (int i = 0; i < HC / 2; i += 2) {
+      const float2 a = ptx::unpack2(acc[i]), b = ptx::unpack2(acc[i + 1]);
+      const float m0 = ptx::warp_max(a.x), m1 = ptx::warp_max(a.y), m2 = ptx::warp_max(b.x), m3 = ptx::warp_max(b.y);
+      if (lane == 0) ptx::sts128f(base + C::kRed + (quad * NR + col0 + 2 * i) * 4, m0, m1, m2, m3);
     }
     ptx::named_bar_sync(1 + part, 128);
     float back = 1.f;                                   // what a reference that moves takes from the sums so far
@@ -855,6 +862,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
         for (int b = 0; b < 4 - C::kHeldBlocks; ++b) o[b][i] = ptx::mul2(o[b][i], f);
       }
       if (!first) {
+        ptx::tmem_wait_st();
 #pragma unroll 1
         for (int j = 0; j < C::kHeldBlocks * HC; j += 8) {
           const uint32_t a = lane_base + C::kHeld + NR * (j / HC) + col0 + j % HC;

@@ -430,6 +430,13 @@ __device__ __forceinline__ void prefetch_l2_bulk(const void* p, uint32_t bytes) 
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
+// Maximum over the warp's lanes (NaNs ignored unless every lane has one).
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // 2^x, hardware approximation (relative error about 2^-22), flushing subnormal results to zero.
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
@@ -439,6 +446,10 @@ __device__ __forceinline__ float ex2_approx(float x) {
 
 __device__ __forceinline__ void sts32f(uint32_t saddr, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(saddr), "f"(v) : "memory");
+}
+
+__device__ __forceinline__ void sts128f(uint32_t saddr, float a, float b, float c, float d) {
+  asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(saddr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
 }
 
 __device__ __forceinline__ float4 lds128f(uint32_t saddr) {
