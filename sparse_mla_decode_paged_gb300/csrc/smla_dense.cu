@@ -1090,73 +1090,135 @@ __global__ void __launch_bounds__(DC<NR>::kThreads, 1)
 
 // ----------------------------------------------------------------------------- merge
 
-constexpr int kMergeThreads = 128;        // four warps share a row's partials, each lane 4 of 128 dims
+constexpr int kMergeThreads = 128;
 constexpr int kMergeBatch = 8;            // partial rows in flight per thread
+constexpr int kFewParts = 16;             // items of at most so many parts: one warp per (row, 128 dims)
+
+// The partials of one row: part 0 in slot 1 of CTA c, part s in slot 0 of CTA c + s.
+struct PartRows {
+  int c, row, nr;
+  __device__ __forceinline__ size_t at(int s) const { return (s == 0 ? 2 * (size_t)c + 1 : 2 * (size_t)(c + s)) * nr + row; }
+};
+
+__device__ __forceinline__ void add_part(float4& acc, float w, const float4& v) {
+  acc.x = fmaf(w, v.x, acc.x);
+  acc.y = fmaf(w, v.y, acc.y);
+  acc.z = fmaf(w, v.z, acc.z);
+  acc.w = fmaf(w, v.w, acc.w);
+}
+
+__device__ __forceinline__ void store_joined(const DenseParams& p, size_t row, int block, int lane, const float4& v, float lse) {
+  reinterpret_cast<uint2*>(p.out + row * kDLatent + 128 * block)[lane] =
+      make_uint2(f32x2_to_bf16x2(v.x, v.y), f32x2_to_bf16x2(v.z, v.w));
+  if (lane == 0 && block == 0) p.lse[row] = lse;
+}
 
 // Joins the partials of the items that cross CTA runs: lse = ln sum_s exp(lse_s), out = sum_s exp(lse_s - lse)
 // o_s.  An item that begins in CTA c and ends in CTA c1 left its partials in slot 1 of c and slot 0 of
-// c + 1 .. c1.  Every CTA lists those items from the run descriptors and takes (row, 128 dims)
-// of them in turn.  Bound by the latency of the partials (in L2) for a single long item of many parts, so a row's
-// partials are spread over four warps and its dims over four CTAs.
+// c + 1 .. c1.  Every CTA lists those items from the run descriptors, in the same order, and takes its share of their
+// (row, 128 dims).  Bound by the latency of the partials (in L2): an item of few parts, of which a batch has many,
+// takes one warp, all its loads in flight at once and no barrier; in one of many parts (a single long request) four
+// warps share the parts.
 __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const DenseParams p, const RunDesc* descs,
                                                                     const float* lse_part, const float* o_part) {
-  __shared__ int list_s[kDenseMaxCtas];
+  __shared__ int parts_s[kDenseMaxCtas], item_s[kDenseMaxCtas];     // of the item that begins in CTA c, 0: none to join
+  __shared__ uint16_t order_s[kDenseMaxCtas];                       // few parts from the front, many from the back
   __shared__ float w_s[kDenseMaxCtas];
-  __shared__ int n_s;
+  __shared__ int few_s, many_s;
   __shared__ float lse_s;
   __shared__ float4 sum_s[4][32];
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   ptx::griddep_wait();
-  const long long T = descs[0].total;
-  const int active = (int)min((long long)p.ctas, T);
-  for (int c = tid; c < active; c += kMergeThreads) {
-    const long long begin = descs[c].item_begin, end = descs[c].item_end;
-    list_s[c] = begin >= run_start(T, active, c) && end > run_start(T, active, c + 1);
-  }
-  __syncthreads();
-  if (tid < 32) {                                        // the flagged CTAs in order, the same list in every CTA
-    int n = 0;
-    for (int c0 = 0; c0 < active; c0 += 32) {
-      const bool mine = c0 + lane < active && list_s[c0 + lane];
-      const uint32_t votes = __ballot_sync(0xffffffffu, mine);
-      __syncwarp();
-      if (mine) list_s[n + __popc(votes & ((1u << lane) - 1))] = c0 + lane;   // at most c0 + lane: already read
-      n += __popc(votes);
-      __syncwarp();
-    }
-    if (lane == 0) n_s = n;
-  }
-  __syncthreads();
-  const int nr = p.nr, work = n_s * nr * 4, warp = tid >> 5;
-  for (int idx = blockIdx.x; idx < work; idx += gridDim.x) {
-    const int c = list_s[idx / (4 * nr)], row = (idx >> 2) % nr, block = idx & 3;
+  for (int c = tid; c < p.ctas; c += kMergeThreads) {
     const RunDesc d = descs[c];
-    const Rows it = rows_of(p, d.item);
-    if (row >= it.nrows) continue;                       // uniform over the CTA
-    int c1 = (int)((d.item_end * active + T - 1) / T);   // first CTA past the item, give or take one
-    while (c1 > c && run_start(T, active, c1) >= d.item_end) --c1;
-    while (c1 + 1 < active && run_start(T, active, c1 + 1) < d.item_end) ++c1;
-    const int parts = c1 - c + 1;
-    auto slot = [&](int s) { return s == 0 ? 2 * (size_t)c + 1 : 2 * (size_t)(c + s); };
-    // warp w takes parts w, w + 4, ...: their rows in flight before the weights are known
-    const float4* rows = reinterpret_cast<const float4*>(o_part) + 32 * block + lane;
-    auto at = [&](int s) { return (slot(s) * nr + row) * (kDLatent / 4); };
+    const long long T = d.total;
+    const int active = (int)min((long long)p.ctas, T);
+    int parts = 0;
+    if (c < active && d.item_begin >= run_start(T, active, c) && d.item_end > run_start(T, active, c + 1)) {
+      int c1 = (int)((d.item_end * active + T - 1) / T);   // first CTA past the item, give or take one
+      while (c1 > c && run_start(T, active, c1) >= d.item_end) --c1;
+      while (c1 + 1 < active && run_start(T, active, c1 + 1) < d.item_end) ++c1;
+      parts = c1 - c + 1;
+    }
+    parts_s[c] = parts;
+    item_s[c] = d.item;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int few = 0, many = 0;
+    const uint32_t below = (1u << lane) - 1;
+    for (int c0 = 0; c0 < p.ctas; c0 += 32) {
+      const int parts = c0 + lane < p.ctas ? parts_s[c0 + lane] : 0;
+      const uint32_t f = __ballot_sync(0xffffffffu, parts > 0 && parts <= kFewParts);
+      const uint32_t m = __ballot_sync(0xffffffffu, parts > kFewParts);
+      if (f >> lane & 1) order_s[few + __popc(f & below)] = (uint16_t)(c0 + lane);
+      if (m >> lane & 1) order_s[kDenseMaxCtas - 1 - many - __popc(m & below)] = (uint16_t)(c0 + lane);
+      few += __popc(f);
+      many += __popc(m);
+    }
+    if (lane == 0) {
+      few_s = few;
+      many_s = many;
+    }
+  }
+  __syncthreads();
+  const int nr = p.nr;
+  for (int idx = blockIdx.x * (kMergeThreads / 32) + warp; idx < few_s * nr * 4; idx += gridDim.x * (kMergeThreads / 32)) {
+    const int c = order_s[idx / (4 * nr)], row = (idx >> 2) % nr, block = idx & 3, parts = parts_s[c];
+    const Rows it = rows_of(p, item_s[c]);
+    if (row >= it.nrows) continue;
+    const PartRows rows{c, row, nr};
+    const float4* o = reinterpret_cast<const float4*>(o_part) + 32 * block + lane;
+    const float x = lane < parts ? __ldg(lse_part + rows.at(lane)) : -CUDART_INF_F;
     float4 v[kMergeBatch];
 #pragma unroll
     for (int s = 0; s < kMergeBatch; ++s)
-      v[s] = warp + 4 * s < parts ? __ldg(rows + at(warp + 4 * s)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s < parts) v[s] = __ldg(o + rows.at(s) * (kDLatent / 4));
+    float m = x;
+#pragma unroll
+    for (int h = 16; h; h >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, h));
+    if (__any_sync(0xffffffffu, isnan(x))) m = CUDART_NAN_F;
+    const float e = m == -CUDART_INF_F ? 0.f : expf(x - m);
+    float z = e;
+#pragma unroll
+    for (int h = 16; h; h >>= 1) z += __shfl_xor_sync(0xffffffffu, z, h);
+    const float w = z == 0.f ? 0.f : e / z;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int s = 0; s < kMergeBatch; ++s)
+      if (s < parts) add_part(acc, __shfl_sync(0xffffffffu, w, s), v[s]);
+#pragma unroll
+    for (int s = kMergeBatch; s < kFewParts; ++s)
+      if (s < parts) v[s - kMergeBatch] = __ldg(o + rows.at(s) * (kDLatent / 4));
+#pragma unroll
+    for (int s = kMergeBatch; s < kFewParts; ++s)
+      if (s < parts) add_part(acc, __shfl_sync(0xffffffffu, w, s), v[s - kMergeBatch]);
+    store_joined(p, (size_t)it.req * p.q_per_req * p.H + it.row0 + row, block, lane, acc,
+                 z == 0.f ? -CUDART_INF_F : m + logf(z));
+  }
+  for (int idx = blockIdx.x; idx < many_s * nr * 4; idx += gridDim.x) {
+    const int c = order_s[kDenseMaxCtas - 1 - idx / (4 * nr)], row = (idx >> 2) % nr, block = idx & 3, parts = parts_s[c];
+    const Rows it = rows_of(p, item_s[c]);
+    if (row >= it.nrows) continue;                       // uniform over the CTA
+    // warp w takes parts w, w + 4, ...: their rows in flight before the weights are known
+    const PartRows rows{c, row, nr};
+    const float4* o = reinterpret_cast<const float4*>(o_part) + 32 * block + lane;
+    float4 v[kMergeBatch];
+#pragma unroll
+    for (int s = 0; s < kMergeBatch; ++s)
+      if (warp + 4 * s < parts) v[s] = __ldg(o + rows.at(warp + 4 * s) * (kDLatent / 4));
     __syncthreads();                                     // w_s and sum_s of the row before have been read
     if (warp == 0) {
       float m = -CUDART_INF_F;
       bool bad = false;
       for (int s = lane; s < parts; s += 32) {
-        const float x = __ldg(lse_part + slot(s) * nr + row);
+        const float x = __ldg(lse_part + rows.at(s));
         bad |= isnan(x);
         m = fmaxf(m, x);
         w_s[s] = x;
       }
 #pragma unroll
-      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      for (int h = 16; h; h >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, h));
       if (__any_sync(0xffffffffu, bad)) m = CUDART_NAN_F;
       float z = 0.f;
       for (int s = lane; s < parts; s += 32) {
@@ -1165,7 +1227,7 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const DenseP
         z += e;
       }
 #pragma unroll
-      for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+      for (int h = 16; h; h >>= 1) z += __shfl_xor_sync(0xffffffffu, z, h);
       const float inv = z == 0.f ? 0.f : 1.f / z;
       for (int s = lane; s < parts; s += 32) w_s[s] *= inv;
       if (lane == 0) lse_s = z == 0.f ? -CUDART_INF_F : m + logf(z);
@@ -1176,33 +1238,18 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const DenseP
       if (s0 > 0) {
 #pragma unroll
         for (int s = 0; s < kMergeBatch; ++s)
-          v[s] = warp + 4 * (s0 + s) < parts ? __ldg(rows + at(warp + 4 * (s0 + s))) : make_float4(0.f, 0.f, 0.f, 0.f);
+          if (warp + 4 * (s0 + s) < parts) v[s] = __ldg(o + rows.at(warp + 4 * (s0 + s)) * (kDLatent / 4));
       }
 #pragma unroll
-      for (int s = 0; s < kMergeBatch; ++s) {
-        if (warp + 4 * (s0 + s) >= parts) break;
-        const float w = w_s[warp + 4 * (s0 + s)];
-        acc.x = fmaf(w, v[s].x, acc.x);
-        acc.y = fmaf(w, v[s].y, acc.y);
-        acc.z = fmaf(w, v[s].z, acc.z);
-        acc.w = fmaf(w, v[s].w, acc.w);
-      }
+      for (int s = 0; s < kMergeBatch; ++s)
+        if (warp + 4 * (s0 + s) < parts) add_part(acc, w_s[warp + 4 * (s0 + s)], v[s]);
     }
     sum_s[warp][lane] = acc;
     __syncthreads();
-    const size_t out_row = (size_t)it.req * p.q_per_req * p.H + it.row0 + row;
     if (warp == 0) {
 #pragma unroll
-      for (int s = 1; s < 4; ++s) {
-        const float4 o = sum_s[s][lane];
-        acc.x += o.x;
-        acc.y += o.y;
-        acc.z += o.z;
-        acc.w += o.w;
-      }
-      reinterpret_cast<uint2*>(p.out + out_row * kDLatent + 128 * block)[lane] =
-          make_uint2(f32x2_to_bf16x2(acc.x, acc.y), f32x2_to_bf16x2(acc.z, acc.w));
-      if (lane == 0 && block == 0) p.lse[out_row] = lse_s;
+      for (int s = 1; s < 4; ++s) add_part(acc, 1.f, sum_s[s][lane]);
+      store_joined(p, (size_t)it.req * p.q_per_req * p.H + it.row0 + row, block, lane, acc, lse_s);
     }
   }
 }
