@@ -359,7 +359,8 @@ typedef struct smla_dense_dims {
 } smla_dense_dims;
 
 typedef struct smla_dense_plan {
-  int32_t rows_per_cta;       /* (query, head) rows a CTA handles at once: 16, 32 or 64  */
+  int32_t rows_per_cta;       /* (query, head) rows a CTA handles at once: 16, 32 or 64, */
+                              /* fewer for short tables (work for every CTA)             */
   int32_t row_groups;         /* groups of rows_per_cta rows per request                 */
   int32_t ctas;               /* CTAs the batch's tiles are shared out over              */
   int32_t reserved;

@@ -45,10 +45,11 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kTopWeight = 7.f;         // a tile's largest weight of a row lies in (2^6, 2^7]
+constexpr int kMostTiles16 = 4, kMostTiles32 = 24;   // tiles of a CTA up to which row groups are of 16 and of 32
 constexpr float kMaxFactor = 20.f;        // a tile's factor 2^(R - ref) above 2^20 moves ref
 
 // Warps: the softmax warps (warp w: TMEM lanes of quadrant w % 4, row part w / 4), then one warp each for the
-// copies, the QK and the PV, and an idle one.
+// copies, the QK and the PV, and one that describes the run for the merge.
 enum { kCopyRole, kQkRole, kPvRole };
 
 constexpr uint32_t kSlot = 16384;         // 128 positions x 128 bytes: one code block or the rope of a tile
@@ -87,7 +88,7 @@ struct DC {
   static constexpr uint32_t kRed = kLen + 2 * NR * 4;             // [4][NR] float
   static constexpr uint32_t kRow = kRed + 4 * NR * 4;             // per softmax warp [HC] minus R, [HC] factor
   static constexpr uint32_t kBar = kRow + kSoftWarps * 2 * HC * 4;
-  static constexpr uint32_t kBytes = kBar + 512;
+  static constexpr uint32_t kBytes = kBar + 640;
   static constexpr uint32_t kSCol = kPBufs * kOCols;              // score buffer i at kSCol + kOCols i
   static constexpr uint32_t kHeld = kSCol + kSBufs * kOCols;      // accumulators of block b at kHeld + NR b
   static constexpr uint32_t kTmemCols = kHeld + kHeldBlocks * NR;
@@ -103,9 +104,10 @@ struct Bars {
   int armed_k[12], armed_sc[3];            // copies armed so far per slot
   int pages_ok[3];                        // of the tile in each scale slot: bit h: page h is loaded
   int first_item, first_tile, my_tiles;   // this CTA's run
-  long long total;
+  int last_item, active;                  // its last item, the number of CTAs that have a run
+  long long total, last_begin, last_end;  // tiles of the batch, global tile range of the last item
 };
-static_assert(sizeof(Bars) <= 512, "barrier area");
+static_assert(sizeof(Bars) <= 640, "barrier area");
 
 // One (request, row group): rows row0 .. row0 + nrows - 1 of the request's s_q H rows.
 struct Rows {
@@ -149,12 +151,10 @@ __device__ __forceinline__ Lens lens_of(const DenseParams& p, const Rows& r) {
 // First tile of CTA c's run when T tiles are shared out over n CTAs.
 __device__ __forceinline__ long long run_start(long long T, int n, int c) { return T * c / n; }
 
-// The run as the kernel leaves it for the merge: where the last item of the run begins and ends.
+// What the kernel leaves for the merge: the item that begins in a CTA's run and ends in a later one's, if any, and
+// the number of runs that it crosses (0: nothing to join).
 struct RunDesc {
-  long long total;                        // tiles of the batch
-  long long item_begin, item_end;         // global tile range of the run's last item
-  int item;
-  int pad;
+  int item, parts;
 };
 
 // Walks the (item, tile) pairs of a run; every role has its own:  while (w.here(p)) { ...; w.next(); }
@@ -949,7 +949,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
 // This CTA's run of tiles: every CTA adds up the tiles of all items (a run of items per thread, then a scan of
 // the threads' sums).
 template <int kThreads>
-__device__ __forceinline__ void find_run(const DenseParams& p, unsigned char* scratch, Bars* bars, RunDesc* desc) {
+__device__ __forceinline__ void find_run(const DenseParams& p, unsigned char* scratch, Bars* bars) {
   constexpr int kPer = kThreads / 32;
   long long* sums = reinterpret_cast<long long*>(scratch);
   const int n = p.requests * p.groups, per = (n + kThreads - 1) / kThreads;
@@ -982,8 +982,10 @@ __device__ __forceinline__ void find_run(const DenseParams& p, unsigned char* sc
   const int active = (int)min((long long)p.ctas, T);     // CTAs with at least one tile
   const int c = blockIdx.x;
   const long long a = c < active ? run_start(T, active, c) : T, e = c < active ? run_start(T, active, c + 1) : T;
-  if (threadIdx.x == 0) bars->my_tiles = (int)(e - a);
-  if (threadIdx.x == 0 && a == e) *desc = RunDesc{T, 0, 0, -1, 0};
+  if (threadIdx.x == 0) {
+    bars->my_tiles = (int)(e - a);
+    bars->active = active;
+  }
   const long long at = sums[threadIdx.x];
   if (a < e && mine > 0) {
     if (a >= at && a < at + mine) {                      // the run begins in this thread's items
@@ -1005,7 +1007,9 @@ __device__ __forceinline__ void find_run(const DenseParams& p, unsigned char* sc
       for (int i = i0; i < i1; ++i) {
         const int tiles = lens_of(p, rows_of(p, i)).tiles;
         if (e - 1 < x + tiles) {
-          *desc = RunDesc{T, x, x + tiles, i, 0};
+          bars->last_item = i;
+          bars->last_begin = x;
+          bars->last_end = x + tiles;
           break;
         }
         x += tiles;
@@ -1013,6 +1017,16 @@ __device__ __forceinline__ void find_run(const DenseParams& p, unsigned char* sc
     }
   }
   __syncthreads();
+}
+
+__device__ __forceinline__ RunDesc describe_run(const Bars* bars) {
+  const int c = blockIdx.x, active = bars->active;
+  const long long T = bars->total, end = bars->last_end;
+  if (bars->my_tiles == 0 || bars->last_begin < run_start(T, active, c) || end <= run_start(T, active, c + 1)) return RunDesc{0, 0};
+  int c1 = (int)((end * active + T - 1) / T);            // first CTA past the item, give or take one
+  while (c1 > c && run_start(T, active, c1) >= end) --c1;
+  while (c1 + 1 < active && run_start(T, active, c1 + 1) < end) ++c1;
+  return RunDesc{bars->last_item, c1 - c + 1};
 }
 
 template <int NR>
@@ -1055,7 +1069,7 @@ __global__ void __launch_bounds__(DC<NR>::kThreads, 1)
     ptx::tmem_alloc(&bars->tmem, C::kTmemCols);
     ptx::tmem_relinquish();
   }
-  find_run<C::kThreads>(p, sm, bars, descs + blockIdx.x);            // the scratch is overwritten by the pipeline afterwards
+  find_run<C::kThreads>(p, sm, bars);            // the scratch is overwritten by the pipeline afterwards
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -1069,6 +1083,7 @@ __global__ void __launch_bounds__(DC<NR>::kThreads, 1)
     if (role == kCopyRole) copy_role<NR>(p, &map, &smap, base, bars, lane);
     else if (role == kQkRole) qk_role<NR>(p, base, tmem, bars, lane);
     else if (role == kPvRole) pv_role<NR>(p, base, tmem, bars, lane);
+    else if (lane == 0) descs[blockIdx.x] = describe_run(bars);
   }
 
   // nothing of this CTA's may be in flight when it leaves: the MMAs (their last commits) and, after a wait
@@ -1131,16 +1146,7 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const DenseP
   ptx::griddep_wait();
   for (int c = tid; c < p.ctas; c += kMergeThreads) {
     const RunDesc d = descs[c];
-    const long long T = d.total;
-    const int active = (int)min((long long)p.ctas, T);
-    int parts = 0;
-    if (c < active && d.item_begin >= run_start(T, active, c) && d.item_end > run_start(T, active, c + 1)) {
-      int c1 = (int)((d.item_end * active + T - 1) / T);   // first CTA past the item, give or take one
-      while (c1 > c && run_start(T, active, c1) >= d.item_end) --c1;
-      while (c1 + 1 < active && run_start(T, active, c1 + 1) < d.item_end) ++c1;
-      parts = c1 - c + 1;
-    }
-    parts_s[c] = parts;
+    parts_s[c] = d.parts;
     item_s[c] = d.item;
   }
   __syncthreads();
@@ -1346,12 +1352,21 @@ extern "C" int sparse_mla_dense_plan_for(const smla_dense_dims* d, int32_t sm_co
   if (d->batch > kMaxBatch || d->num_heads > kDenseMaxHeads || d->num_pages > 0x7fffffff || d->ctas > kDenseMaxCtas)
     return SMLA_ERR_UNSUPPORTED;
   const int64_t rows = (int64_t)sq * d->num_heads;
-  plan->rows_per_cta = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-  plan->row_groups = (int32_t)((rows + plan->rows_per_cta - 1) / plan->rows_per_cta);
   plan->ctas = d->ctas > 0 ? d->ctas : (sm_count < kDenseMaxCtas ? sm_count : kDenseMaxCtas);
   plan->reserved = 0;
+  // Rows that a CTA takes through a tile together.  Few rows: a tile is done sooner (1.9, 2.5 and 3.9 us for 16, 32
+  // and 64 rows), and so are the steps around the tiles (a CTA's rows read and its results written), but each row
+  // group reads the tile again.  Measured at 64 heads, 16 / 32 / 64 rows: 1 request x 8192 positions 19.0 / 20.1 / 25.0
+  // us, 4 x 8192 30.1 / 27.9 / 32.1, 32 x 4096 69 / 58 / 67, 32 x 8192 130 / 99 / 101, 32 x 16384 237 / 166 / 154.  So:
+  // the fewest rows with which a CTA has at most a few tiles if every request is as long as its table.
+  const int64_t tiles = d->batch / sq * ((d->max_pages_per_seq + (int64_t)1) / 2);
+  auto groups = [&](int nr) { return (rows + nr - 1) / nr; };
+  if (rows <= 16 || tiles * groups(16) <= kMostTiles16 * (int64_t)plan->ctas) plan->rows_per_cta = 16;
+  else if (rows <= 32 || tiles * groups(32) <= kMostTiles32 * (int64_t)plan->ctas) plan->rows_per_cta = 32;
+  else plan->rows_per_cta = 64;
+  plan->row_groups = (int32_t)groups(plan->rows_per_cta);
   // a CTA counts its tiles in 32 bits
-  const int64_t most = d->batch / sq * (int64_t)plan->row_groups * ((d->max_pages_per_seq + (int64_t)1) / 2);
+  const int64_t most = tiles * plan->row_groups;
   if (most / plan->ctas >= 0x7fffffff) return SMLA_ERR_UNSUPPORTED;
   plan->workspace_bytes = kWorkspaceHeader + kDescBytes + lse_part_bytes(plan->ctas, plan->rows_per_cta) +
                           (size_t)2 * plan->ctas * plan->rows_per_cta * kDLatent * sizeof(float);

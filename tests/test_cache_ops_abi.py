@@ -43,9 +43,14 @@ def test_dense_refusals(lib):
 def test_dense_plan(lib):
     for H, sq, rows, groups in ((1, 1, 16, 1), (16, 1, 16, 1), (17, 1, 32, 1), (16, 2, 32, 1), (64, 1, 64, 1),
                                 (128, 1, 64, 2), (128, 3, 64, 6), (5, 13, 64, 2)):
-        p = api.dense_plan_for(api.make_dense_dims(sq * 3, H, 8, 100, sq), 152)
+        p = api.dense_plan_for(api.make_dense_dims(sq * 3, H, 65536, 100, sq), 152)
         assert (p.rows_per_cta, p.row_groups) == (rows, groups)
         assert p.ctas == 152 and p.workspace_bytes >= 256
+    # short tables: smaller row groups while a CTA has at most 4 (16 rows) or 24 (32 rows) tiles
+    for pages, sq, rows, groups in ((128, 1, 16, 4), (304, 1, 16, 4), (306, 1, 32, 2), (3648, 1, 32, 2), (3650, 1, 64, 1),
+                                    (304, 2, 32, 4), (1, 9, 16, 36)):
+        p = api.dense_plan_for(api.make_dense_dims(sq, 64, pages, 100, sq), 152)
+        assert (p.rows_per_cta, p.row_groups) == (rows, groups)
     p = api.dense_plan_for(api.make_dense_dims(3, 64, 8, 100, ctas=40), 152)
     assert p.ctas == 40
     assert lib.sparse_mla_dense_plan_for(None, 152, C.byref(p)) == INVALID

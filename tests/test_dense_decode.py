@@ -23,11 +23,33 @@ def _run(q, cache, bt, lens, scale=SCALE, ctas=0, ws=None):
     return out, lse, api.read_errors(ws)
 
 
+def _every_row_group(q, cache, bt, ctas=0):
+    """The block table as it is and widened, so that a CTA handles 16, 32 and 64 rows at once as far as the query has
+    them (long tables make for large groups)."""
+    seen = {}
+    pages = bt.shape[1]
+    while pages < 1 << 20:
+        wide = torch.full((bt.shape[0], pages), -1, dtype=torch.int32)
+        wide[:, :bt.shape[1]] = bt
+        rows = api.dense_plan(api.dense_dims_of(q, cache, wide, ctas), 0).rows_per_cta
+        seen.setdefault(rows, wide)
+        if rows >= min(64, q.shape[0] // bt.shape[0] * q.shape[1]):
+            break
+        pages *= 2
+    return seen
+
+
 def _check(q, cache, bt, lens, scale=SCALE, ctas=0, flags=0):
-    out, lse, err = _run(q, cache, bt, lens, scale, ctas)
-    assert err == flags
-    check_dense(out, lse, q, cache, bt, lens, scale)
-    return out, lse
+    for rows, wide in _every_row_group(q, cache, bt, ctas).items():
+        out, lse, err = _run(q, cache, wide, lens, scale, ctas)
+        assert err == flags
+        check_dense(out, lse, q, cache, bt, lens, scale)
+
+
+@pytest.mark.parametrize("H,groups", [(16, [16]), (32, [16, 32]), (64, [16, 32, 64]), (128, [16, 32, 64])])
+def test_the_checks_below_reach_every_row_group(H, groups):
+    q, cache, bt, _ = make_dense([300], H, seed=1)
+    assert sorted(_every_row_group(q, cache, bt)) == groups
 
 
 @pytest.mark.parametrize("n", [0, 1, 2, 63, 64, 65, 127, 128, 129, 191, 193, 256, 1000, 4097])
