@@ -55,6 +55,7 @@ enum { kCopyRole, kQkRole, kPvRole };
 constexpr uint32_t kSlot = 16384;         // 128 positions x 128 bytes: one code block or the rope of a tile
 constexpr int kChunks = 5;                // the four code blocks, then the rope
 constexpr int kScaleSlots = 3;
+constexpr int kAhead = 1;                 // tiles between a tile's prefetch into L2 and its copy
 
 template <int NR>
 struct DC {
@@ -263,6 +264,13 @@ __device__ void copy_role(const DenseParams& p, const CUtensorMap* map, const CU
       if (used && !in_cache && lane == 0) atomicOr(p.err, SMLA_DEVERR_PAGE_RANGE);
     }
     const uint32_t n_good = (good & 1) + (good >> 1);
+    // a later tile of the item into L2: K slots come free one by one behind the PV, and their loads would bring the
+    // latency of HBM into every tile
+    const int ahead = lp - base_lp + 2 * kAhead + (lane & 1);
+    const int page_cur = __shfl_sync(0xffffffffu, cur, ahead & 31), page_nxt = __shfl_sync(0xffffffffu, nxt, ahead & 31);
+    const int page = ahead < 32 ? page_cur : page_nxt;
+    if (w.left > kAhead && lane < 2 && page >= 0 && (int64_t)page < p.num_pages)
+      ptx::prefetch_l2_bulk(p.kv + (size_t)page * kPageSize * kRecordBytes, kPageSize * kRecordBytes);
     SMLA_WAIT(&bars->scempty[sc.slot], sc.parity ^ 1);
     if (ok && ptx::elect_one()) {
       bars->pages_ok[sc.slot] = good;
