@@ -146,8 +146,14 @@ __global__ void __launch_bounds__(32 * kNormAppendWarps) kv_norm_append_kernel(c
       }
 #pragma unroll
       for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      const float scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
-      const float up = __frcp_rn(scale);
+      float scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+      if (scale == 0.f) scale = 1.f;                 // amax below the smallest float's 224 fold: codes of 0
+      const bool tiny = scale < 0x1p-100f;           // its reciprocal may not be a float: both sides times 2^64
+      const float up = __frcp_rn(tiny ? scale * 0x1p64f : scale);
+      if (__builtin_expect(tiny, 0)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] *= 0x1p64f;
+      }
       uint32_t c[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i)

@@ -267,6 +267,29 @@ def test_norm_append_nan_latent_writes_nan_codes():
     assert torch.all((rec & 0x7F) == 0x7F)
 
 
+def test_norm_append_blocks_of_tiny_values():
+    # block maxima down to where amax / 448, or its reciprocal, is no normal float: no code may become NaN
+    g = torch.Generator().manual_seed(36)
+    lat, rope = torch.randn((6, 512), generator=g), torch.zeros((6, 64))
+    lat *= torch.tensor([1e-30, 1e-35, 1e-36, 1e-38, 1e-41, 1e-44])[:, None]
+    lat[:, ::7] = 0
+    bt, pos = torch.arange(6, dtype=torch.int32)[:, None], torch.zeros(6, dtype=torch.int32)
+    cache = torch.full((6, 64, 656), 0x7F, dtype=torch.uint8, device=DEV)
+    api.sparse_mla_kv_norm_append(lat.to(DEV), rope.to(DEV), torch.ones(512, device=DEV), 1.0, _table(1).to(DEV),
+                                  bt.to(DEV), pos.to(DEV), cache)
+    rec = cache.cpu().numpy()
+    for i in range(6):
+        codes, scales, _ = oracle.decode_record(rec[i, 0])
+        n = lat[i].double().numpy().reshape(4, 128)            # (the mean square is 0 beside eps)
+        got = codes.reshape(4, 128) * np.asarray(scales, dtype=np.float64)[:, None]
+        # half a step of a code (2^-4 of it, 2^-10 scales at least), and the scale's own rounding in steps of 2^-149
+        tol = 2.0 ** -4 * np.abs(n) * 1.001 + 2.0 ** -10 * scales[:, None] + 448 * 2.0 ** -150
+        if i == 5:
+            tol = np.abs(n)                                    # a scale of 1: codes of 0
+        assert np.all(np.abs(got - n) <= tol)
+        assert np.all(got[n == 0] == 0)
+
+
 def test_norm_append_refused():
     lat, rope, w, cache, bt, req, pos = [t.to(DEV) for t in _append_case(4, "bf16", seed=35)]
     tab = _table(640).to(DEV)
