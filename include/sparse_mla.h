@@ -188,11 +188,11 @@ int sparse_mla_decode_rows(const smla_dims* dims, const void* q, const void* kv_
                            void* workspace, size_t workspace_bytes, int64_t* rows_out,
                            smla_stream_t stream);
 
-/* Test hook for the split kernel's failure path: every wait of the kernel's
+/* Test hook for the split kernel's and the dense decode's failure path: every wait of the kernel's
  * internal pipeline (one thread group waiting for another's shared-memory
  * tile, an MMA or a bulk copy) gives up after `ns` nanoseconds of the GPU's
  * global timer, sets SMLA_DEVERR_TIMEOUT and leaves that call's outputs
- * unwritten; the waits that drain in-flight MMAs and copies before the kernel
+ * unwritten (those that a merge joins hold nothing of use); the waits that drain in-flight MMAs and copies before the kernel
  * exits keep their own limit.  Applies to launches made after the call, from
  * every host thread.  ns = 0 restores the default (one second).  A limit far
  * below a tile's latency makes every launch fail: it exists to test that such
@@ -278,8 +278,9 @@ typedef struct smla_norm_append_dims {
  *   cos_sin float32 [max_positions][64] (16-byte aligned), the others as in
  *           sparse_mla_kv_append
  * A token whose request, position or page is out of range, or whose position
- * is not below max_positions, is skipped and sets SMLA_DEVERR_PAGE_RANGE.  A
- * row holding a NaN or an infinity is written with NaN codes where n is NaN.
+ * is not below max_positions, is skipped and sets SMLA_DEVERR_PAGE_RANGE.  Two
+ * tokens of a call must not name the same position of a page (which one's bytes
+ * the record then holds, or which of each, is not defined).  A row holding a NaN or an infinity is written with NaN codes where n is NaN.
  * Statuses as sparse_mla_kv_append; SMLA_ERR_INVALID_ARG also for a stride
  * below the row, an unknown dtype, a weight_dtype that is neither dtype nor
  * SMLA_FP32, or an eps that is negative or not finite. */
@@ -398,9 +399,13 @@ int sparse_mla_dense_plan(const smla_dense_dims* dims, int32_t device, smla_dens
  * Numerics: the latent scores are sums of E4M3 codes times q as two E4M3
  * terms, the rope scores bf16 products, all accumulated in fp32 (q is exact but
  * for latent elements below about 2^-9 of their row's largest, whose absolute
- * error stays below 2^-17 of that largest); softmax weights and values are
- * fp16 on chip with a power of two per position and a running reference, so
- * neither has to stay in fp16's range.
+ * error stays below 2^-17 of that largest).  The values are the codes as they
+ * are; a softmax weight times a position's scale is two E4M3 terms on chip,
+ * scaled by a power of two per row and 128-position tile: off by 2^-8 of itself
+ * or 2^-16 of the tile's largest, whichever is more.  Tiles are added in fp32
+ * with their own powers of two, so that a long tail of small weights is kept
+ * beside one dominating position.  A row that sees a NaN (in q, a code, a scale
+ * or the rope) is NaN.
  * Statuses as sparse_mla_decode. */
 int sparse_mla_dense_decode(const smla_dense_dims* dims, const void* q, const void* kv_cache,
                             const int32_t* block_table, const int32_t* seq_lens, float sm_scale, void* out,

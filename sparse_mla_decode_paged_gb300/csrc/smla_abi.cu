@@ -402,14 +402,14 @@ extern "C" int sparse_mla_dense_plan(const smla_dense_dims* dims, int32_t device
 extern "C" int sparse_mla_dense_decode(const smla_dense_dims* d, const void* q, const void* kv_cache,
                                        const int32_t* block_table, const int32_t* seq_lens, float sm_scale, void* out,
                                        float* lse, void* workspace, size_t workspace_bytes, smla_stream_t stream) {
-  // the checks that need no device come first, with a nominal SM count
+  // the checks that need no device come first; the workspace's size and what a CTA can count depend on its SMs
   smla_dense_plan plan;
-  int st = sparse_mla_dense_plan_for(d, 1, &plan);
+  int st = sparse_mla_dense_plan_for(d, kDenseMaxCtas, &plan);
   if (st != SMLA_OK) return st;
   st = check_inputs(q, kv_cache, block_table, seq_lens, seq_lens);
   if (st != SMLA_OK) return st;
   if (!out || !lse || !aligned(out, 16) || !aligned(lse, 4)) return SMLA_ERR_INVALID_ARG;
-  if (!workspace || workspace_bytes < plan.workspace_bytes || !aligned(workspace, 256)) return SMLA_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < kWorkspaceHeader || !aligned(workspace, 256)) return SMLA_ERR_WORKSPACE;
   int sms = 0;
   st = sm_count_of_current_device(&sms);
   if (st != SMLA_OK) return st;

@@ -13,21 +13,26 @@
 // two E4M3 terms, q 2^-x = hi + lo with x chosen per row so that its largest latent element lies in [2^7, 2^8).  hi
 // keeps 4 significant bits and lo the other 4 of a bf16 value, so the split is exact but for elements below
 // about 2^-9 of the largest (their error is below 2^-17 of it, 2^-8 of that element's own bf16 rounding).  S^T of
-// a tile: M = 128 positions, N = 2 NR columns (hi rows, then lo rows), one accumulator per 128-dim scale block; the
-// softmax threads form s = 2^x sum_b (S_hi + S_lo) scale_b in fp32.  The rope part is a bf16 product.
+// a tile: M = 128 positions, one accumulator per 128-dim scale block; for up to 32 rows hi and lo are one MMA of N = 2 NR
+// columns and meet in the softmax threads, for 64, where TMEM is full, two MMAs into NR columns.  The softmax threads
+// form s = 2^x sum_b (S_hi + S_lo) scale_b in fp32.  The rope part is a bf16 product.
 // Weights and values.  The codes are the values, too: O^T[512 x NR] += codes^T (P scale), with the same tile read
 // MN-major.  A position's scales are split as scale_b = m_b 2^e, e the exponent of the largest of the four, and the
 // weight takes the power of two: w = 2^(s + e - R), with R a row's maximum of s + e over the tile's 128
 // positions (rounded up) less 7, so that w m_b stays below 2^8.  Block b's operand is w m_b as two E4M3 terms, hi + lo:
-// 8 significant bits (off by 2^-9 at most) down to 2^-6 of that range and steps of 2^-9 below, so every
-// weight keeps an error below 2^-16 of the tile's largest and 2^-9 of itself.  A tile's O^T is added to fp32
-// accumulators in registers with the row's factor 2^(R - ref) (ref: R of the row's first tile), so tiles of
+// 8 significant bits (off by 2^-9 at most) down to 2^-6 of that range and steps of 2^-9 below.  w and m_b are fp16
+// before (their product once more: 3 roundings of 2^-11), so every weight is off by at most 2^-8 of itself or 2^-16 of
+// the tile's largest.  A tile's O^T is added to fp32
+// accumulators (in registers; for 64 rows those of blocks 0 and 1 in TMEM) with the row's factor 2^(R - ref) (ref: R of the row's first tile), so tiles of
 // very different weight (a long tail beside one dominating position) lose nothing to one another.
 //   l = sum w 2^(R - ref - e) in fp32, out = O / l, lse = ln 2 (ref + log2 l).
 //
-// What bounds it: HBM bytes (656 per position) for up to 64 rows, where one SM's share of the HBM rate is a tile
-// per 1.9 us; inside an SM the shared-memory path, which a tile of 64 rows takes about 490 KB through (84 in, 152
-// QK operands, 64 P, 192 PV operands).
+// What bounds it: HBM bytes (656 per position) for 16 rows and all but that for 32; for 64 rows the steps of a tile
+// inside an SM.  Of the 8000 cycles that a tile of 64 rows takes (3.9 us; an SM's share of the HBM rate is a tile per
+// 1.9 us) the tensor core is busy for about 3300, which is the rate at which shared memory feeds it (M = 128 positions,
+// N = 64: 6 KB of operands per MMA of 32 dims or positions); the rest is the chain from scores to weights to O^T, whose
+// K slots come free behind the PV.  Measured, 32 requests x 32768 positions: 64 heads 249 us (2.8 TB/s), 32 heads 157 us
+// (4.4 TB/s), 16 heads 123 us (5.6 TB/s); 1 x 8192 positions of 64 heads 18.6 us, 1 x 77 of 16 heads 11 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -69,11 +74,12 @@ struct DC {
   // TMEM: O^T of one tile (kPBufs blocks at a time), score buffers, and for 64 rows, whose accumulators do not all fit
   // the registers, those of blocks 0 and 1
   static constexpr int kHeldBlocks = NR == 64 ? 2 : 0;
-  // Row parts: 8 softmax warps, 16 for 64 rows (the weights' work of 64 rows needs the warps to hide its latencies).
+  // Row parts: 8 softmax warps.  (16, with half the rows per thread, were slower, and so were 8 with 8 more for the
+  // accumulators: 32 x 32768 positions of 64 heads took 292 us instead of 249.)
   static constexpr int kParts = 2;
   static constexpr int kSoftWarps = 4 * kParts;
   static constexpr int kThreads = 32 * (kSoftWarps + 4);
-  // registers after setmaxnreg, of 96 (640 threads) or 168 (384) at launch: 4 x 112 + 32 = 5 x 96, 2 x 232 + 40 = 3 x 168
+  // registers after setmaxnreg, of the 168 at launch: two warpgroups of 232 and one of 40 are 3 x 168
   static constexpr int kSoftRegs = 232, kMiscRegs = 40;
   static constexpr int HC = NR / kParts;       // rows of one softmax thread
   static constexpr uint32_t kQ8Chunk = 2 * NR * 128;
@@ -199,8 +205,8 @@ struct Ring {
   }
 };
 
-// Wait for a slot to be freed: passes at once on the ring's first round (an mbarrier that has completed no
-// phase yet reports the phase before its first as complete).
+// A wait for a slot to be freed (the other parity) passes at once on the ring's first round: an mbarrier that has
+// completed no phase yet reports the phase before its first as complete.
 // A wait of a whole warp, bounded by p.wait_ns.  The common case is one try; once a wait has given up (ok 0) a
 // role runs its loop to the end without arriving or issuing, so that the named barriers of the softmax warps stay
 // matched.  (`ok` passes through an empty asm: otherwise the compiler makes a copy of the rest of the role for
@@ -583,7 +589,7 @@ template <int NR>
 __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t base, uint32_t tmem, Bars* bars, int warp,
                              int lane, float* o_part, float* lse_part) {
   using C = DC<NR>;
-  constexpr int HC = C::HC, LC = HC;// rows per thread, columns per TMEM load
+  constexpr int HC = C::HC;                             // rows per thread
   const int part = warp >> 2, quad = warp & 3, col0 = part * HC;
   const int tok = 32 * quad + lane;
   const uint32_t lane_base = tmem + ((uint32_t)(32 * quad) << 16);
@@ -803,18 +809,15 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
       const uint32_t a = lane_base + C::kSCol + C::kOCols * s.slot + col0;
       const uint64_t kf2 = ptx::pack2(kf, kf), e2 = ptx::pack2((float)e, (float)e);
       const uint32_t fa = base + C::kF + (buf * NR + col0) * 4;
+      uint32_t r[HC];
+      tmem_ld<HC>(a, r);
+      ptx::tmem_wait_ld();
 #pragma unroll
-      for (int i0 = 0; i0 < HC; i0 += LC) {
-        uint32_t r[LC];
-        tmem_ld<LC>(a + i0, r);
-        ptx::tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < LC; i += 4) {
-          const ulonglong2 f = ptx::lds128_pairs(fa + (i0 + i) * 4);
-          uint64_t* d = &acc[(i0 + i) / 2];
-          d[0] = ptx::fma2(d[0], f.x, ptx::fma2(ptx::pack2(r[i], r[i + 1]), kf2, e2));
-          d[1] = ptx::fma2(d[1], f.y, ptx::fma2(ptx::pack2(r[i + 2], r[i + 3]), kf2, e2));
-        }
+      for (int i = 0; i < HC; i += 4) {
+        const ulonglong2 f = ptx::lds128_pairs(fa + i * 4);
+        uint64_t* d = &acc[i / 2];
+        d[0] = ptx::fma2(d[0], f.x, ptx::fma2(ptx::pack2(r[i], r[i + 1]), kf2, e2));
+        d[1] = ptx::fma2(d[1], f.y, ptx::fma2(ptx::pack2(r[i + 2], r[i + 3]), kf2, e2));
       }
     }
     ptx::tc_fence_before();
@@ -1046,8 +1049,7 @@ __global__ void __launch_bounds__(DC<NR>::kThreads, 1)
   const uint32_t base = ptx::smem_u32(sm);
   Bars* bars = reinterpret_cast<Bars*>(sm + C::kBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  ptx::griddep_wait();                                   // the call before may still be merging from the workspace
-  if (threadIdx.x == 0) ptx::griddep_launch_dependents();
+  if (threadIdx.x == 0) ptx::griddep_launch_dependents();   // the merge, which waits for this grid's results
   if (threadIdx.x == 0) {
     ptx::prefetch_tensormap(&map);
     ptx::prefetch_tensormap(&smap);

@@ -365,6 +365,62 @@ def test_read_refused():
 
 # --------------------------------------------------------------------------- together
 
+def test_a_captured_step_replayed_over_new_tokens():
+    """Append, query rotation and dense decode captured on a stream of their own and replayed with the positions moved
+    on: each step attends over what the steps before it wrote."""
+    g = torch.Generator().manual_seed(51)
+    R, H, start = 2, 16, torch.tensor([62, 0], dtype=torch.int32)
+    tab, w = _table(128).to(DEV), torch.ones(512, device=DEV)
+    bt = torch.tensor([[3, 0], [1, 2]], dtype=torch.int32)
+    from sparse_mla_decode_paged_gb300 import workloads as wl
+    cache = wl.fill_kv_cache(4, torch.Generator().manual_seed(52), "cpu").to(DEV)
+    kv, raw = torch.zeros((R, 576), device=DEV), torch.zeros((R, H, 576), dtype=torch.bfloat16, device=DEV)
+    pos, dbt, q, seq = start.to(DEV), bt.to(DEV), torch.empty_like(raw), torch.zeros(R, dtype=torch.int32, device=DEV)
+    ws = api.alloc_dense_workspace(api.dense_dims_of(raw, cache, dbt), DEV)
+    out, lse = torch.empty((R, H, 512), dtype=torch.bfloat16, device=DEV), torch.empty((R, H), device=DEV)
+    stream = torch.cuda.Stream()
+
+    def step():
+        api.sparse_mla_kv_norm_append(kv[:, :512], kv[:, 512:], w, 1e-6, tab, dbt, pos, cache)
+        api.sparse_mla_norm_rope(raw, pos, tab, rope_offset=512, out=q)
+        torch.add(pos, 1, out=seq)
+        api.sparse_mla_dense_decode(q, cache, dbt, seq, 576 ** -0.5, out=out, lse=lse, workspace=ws)
+
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        step()
+    for i in range(4):
+        kv.copy_(torch.randn((R, 576), generator=g))
+        raw.copy_(torch.randn((R, H, 576), generator=g))
+        pos.copy_(start + i)
+        before = cache.cpu()
+        graph.replay()
+        torch.cuda.synchronize()
+        _check_append(cache, before, kv[:, :512].cpu(), kv[:, 512:].cpu(), w.cpu(), tab.cpu(), bt, torch.arange(R),
+                      start + i, True, 1e-6)
+        check_dense(out, lse, q.cpu(), cache.cpu(), bt, start + i + 1, 576 ** -0.5)
+    assert api.read_errors(ws) == 0
+
+
+def test_calls_on_a_stream_of_their_own():
+    lat, rope, w, cache, bt, req, pos = _append_case(40, "bf16", seed=53)
+    tab, dc = _table(640).to(DEV), cache.to(DEV)
+    d = [t.to(DEV) for t in (lat, rope, w, bt, req, pos)]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    api.sparse_mla_kv_norm_append(d[0], d[1], d[2], 1e-5, tab, d[3], d[5], dc, requests=d[4], stream=s)
+    rows = api.sparse_mla_kv_read(dc, d[3], d[5], requests=d[4], dtype=torch.float32, stream=s)
+    x = api.sparse_mla_norm_rope(rows.view(40, 1, 576), d[5], tab, norm=False, rope_offset=512, stream=s)
+    s.synchronize()
+    _check_append(dc, cache, lat, rope, w, tab.cpu(), bt, req, pos, True, 1e-5)
+    ref = dense_oracle.read_records(dc.cpu().numpy(), bt.numpy(), pos.numpy(), req.numpy()).astype(np.float32)
+    assert np.array_equal(rows.cpu().numpy(), ref)
+    _check_norm_rope(x, rows.view(40, 1, 576).cpu(), None, tab.cpu(), pos, "fp32", False, 512, True)
+    with pytest.raises((TypeError, AttributeError)):
+        api.sparse_mla_kv_read(dc, d[3], d[5], requests=d[4], stream=0)
+
+
 def test_a_decode_step_from_projections_to_output():
     """Prompt and new token written by the fused append, queries normed and rotated in place, the dense decode over
     the cache, and the context read back: each stage against the float64 oracle on what the stage before it wrote."""

@@ -51,6 +51,10 @@ def test_dense_plan(lib):
                                     (304, 2, 32, 4), (1, 9, 16, 36)):
         p = api.dense_plan_for(api.make_dense_dims(sq, 64, pages, 100, sq), 152)
         assert (p.rows_per_cta, p.row_groups) == (rows, groups)
+    # very wide tables: a CTA counts its tiles in 32 bits
+    assert api.dense_plan_for(api.make_dense_dims(65535, 128, 1 << 17, 100), 152).row_groups == 2
+    assert lib.sparse_mla_dense_plan_for(C.byref(api.make_dense_dims(65535, 128, 1 << 24, 100)), 152,
+                                         C.byref(p)) == UNSUPPORTED
     p = api.dense_plan_for(api.make_dense_dims(3, 64, 8, 100, ctas=40), 152)
     assert p.ctas == 40
     assert lib.sparse_mla_dense_plan_for(None, 152, C.byref(p)) == INVALID

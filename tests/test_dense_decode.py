@@ -122,6 +122,22 @@ def test_rising_scores_move_the_reference():
     _check(q, cache, bt, lens, 1.0)
 
 
+@pytest.mark.parametrize("steps", ["rise", "fall", "both"])
+def test_scores_that_jump_from_page_to_page(steps):
+    # whole pages 50 (in units of e) above or below the one before, in rows of every magnitude: accumulators in
+    # registers and in TMEM are scaled back by far more than a tile's own range, or keep what a later tile adds to
+    q, cache, bt, lens = make_dense([1300, 257], 64, seed=30)
+    q[:] = 0
+    q[:, :, 512] = torch.linspace(0.02, 1.0, 64).to(torch.bfloat16)[None]
+    for r in range(bt.shape[0]):
+        for i in range(bt.shape[1]):
+            if bt[r, i] < 0:
+                continue
+            h = 50.0 * {"rise": i, "fall": -i, "both": (i * 7) % 5 - 2}[steps]
+            cache[int(bt[r, i]), :, 528:530] = torch.tensor([h], dtype=torch.bfloat16).view(torch.uint8)
+    _check(q, cache, bt, lens, 1.0)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.05, 0.3])
 def test_score_scales(scale):
     _check(*make_dense([321, 50], 16, seed=12), scale=scale)
@@ -173,6 +189,41 @@ def test_a_later_query_sees_a_nan_that_an_earlier_one_does_not():
     assert torch.isnan(lse[1]).all()
 
 
+def test_nan_positions_in_every_row_group():
+    q, cache, bt, lens = make_dense([260, 259, 130, 127], 64, 2, seed=31)
+    cache[int(bt[0, 4]), 3, 300] = 0x7F                         # position 259: query 0 alone reads it
+    cache[int(bt[1, 1]), 64 - 1, 512 + 4:512 + 8] = torch.tensor([float("nan")]).view(torch.uint8)   # 127: query 2 alone
+    for wide in _every_row_group(q, cache, bt).values():
+        out, lse, err = _run(q, cache, wide, lens)
+        assert err == 0
+        bad = torch.tensor([True, False, True, False])
+        assert torch.equal(torch.isnan(lse).all(1).cpu(), bad) and torch.equal(torch.isnan(lse).any(1).cpu(), bad)
+        assert torch.equal(torch.isnan(out.float()).all(2).all(1).cpu(), bad)
+        assert torch.equal(torch.isnan(out.float()).any(2).any(1).cpu(), bad)
+
+
+def test_a_wait_that_runs_out_is_reported_and_recoverable():
+    q, cache, bt, lens = make_dense([1300, 257, 5], 64, seed=32)
+    for wide in _every_row_group(q, cache, bt).values():
+        d = [t.to(DEV) for t in (q, cache, wide, lens)]
+        ws = api.alloc_dense_workspace(api.dense_dims_of(d[0], d[1], d[2]), DEV)
+        out = torch.full((3, 64, 512), 3.0, dtype=torch.bfloat16, device=DEV)
+        lse = torch.full((3, 64), 3.0, device=DEV)
+        try:
+            api.debug_set_wait_limit(1)                        # no wait of this call is issued anything to wait for
+            api.sparse_mla_dense_decode(*d, SCALE, out=out, lse=lse, workspace=ws)
+            torch.cuda.synchronize()
+        finally:
+            api.debug_set_wait_limit(0)
+        assert api.read_errors(ws) & _native.DEVERR_TIMEOUT
+        assert torch.all(out[2] == 3.0) and torch.all(lse[2] == 3.0)      # a request of one tile: unwritten
+        api.clear_errors(ws)
+        api.sparse_mla_dense_decode(*d, SCALE, out=out, lse=lse, workspace=ws)
+        torch.cuda.synchronize()
+        assert api.read_errors(ws) == 0
+        check_dense(out, lse, q, cache, bt, lens, SCALE)
+
+
 def test_bad_pages_are_skipped_and_flagged():
     q, cache, bt, lens = make_dense([500, 300], 16, seed=17)
     bt[0, 2] = cache.shape[0] + 5
@@ -209,14 +260,16 @@ def test_cache_beyond_4_gib():
     where = torch.randperm(40000, generator=torch.Generator().manual_seed(1))[:cache.shape[0]] + total - 40000
     big[where.to(DEV)] = cache.to(DEV)
     btb = torch.where(bt >= 0, where[bt.clamp_min(0).long()].to(torch.int32), bt)
-    out, lse = api.sparse_mla_dense_decode(q.to(DEV), big, btb.to(DEV), lens.to(DEV), SCALE)
-    torch.cuda.synchronize()
-    check_dense(out, lse, q, cache, bt, lens, SCALE)
+    for wide in _every_row_group(q, cache, btb).values():
+        out, lse = api.sparse_mla_dense_decode(q.to(DEV), big, wide.to(DEV), lens.to(DEV), SCALE)
+        torch.cuda.synchronize()
+        check_dense(out, lse, q, cache, bt, lens, SCALE)
 
 
-def test_captured_call_follows_new_lengths():
-    q, cache, bt, lens = make_dense([900, 500, 64], 32, seed=21, poison=False)
-    d = [t.to(DEV) for t in (q, cache, bt, lens)]
+@pytest.mark.parametrize("H,rows", [(32, 16), (32, 32), (64, 32), (64, 64)])
+def test_captured_call_follows_new_lengths(H, rows):
+    q, cache, bt, lens = make_dense([900, 500, 64], H, seed=21, poison=False)
+    d = [t.to(DEV) for t in (q, cache, _every_row_group(q, cache, bt)[rows], lens)]
     ws = api.alloc_dense_workspace(api.dense_dims_of(d[0], d[1], d[2]), DEV)
     out, lse = api.sparse_mla_dense_decode(*d, SCALE, workspace=ws)
     torch.cuda.synchronize()
