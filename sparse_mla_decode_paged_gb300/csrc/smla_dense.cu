@@ -58,13 +58,14 @@ constexpr float kMaxFactor = 20.f;        // a tile's factor 2^(R - ref) above 2
 enum { kCopyRole, kQkRole, kPvRole };
 
 constexpr uint32_t kSlot = 16384;         // 128 positions x 128 bytes: one code block or the rope of a tile
-constexpr int kChunks = 5;                // the four code blocks, then the rope
+constexpr int kChunks = 5;                // of a tile's scores: the four code blocks, then the rope
 constexpr int kScaleSlots = 3;
 constexpr int kAhead = 1;                 // tiles between a tile's prefetch into L2 and its copy
 
 template <int NR>
 struct DC {
-  static constexpr int kRing = NR == 64 ? 7 : NR == 32 ? 9 : 11;    // K slots
+  static constexpr int kRing = NR == 64 ? 6 : NR == 32 ? 8 : 9;     // slots of code blocks
+  static constexpr int kRopeSlots = NR == 16 ? 2 : 1;
   static constexpr int kPBufs = NR == 64 ? 2 : 4;                   // weights of so many blocks
   static constexpr int kSBufs = 4;                                  // score accumulators
   // hi and lo terms (of q, and of the weights) meet in one accumulator for 64 rows, where TMEM is full; for fewer rows
@@ -88,7 +89,8 @@ struct DC {
   static constexpr uint32_t kK = (kQr + NR * 128 + 1023) / 1024 * 1024;
   static constexpr int kPRow = 2 * NR;                            // bytes of a position's weights: hi, then lo
   static constexpr uint32_t kPBuf = 128 * kPRow;
-  static constexpr uint32_t kP = kK + kRing * kSlot;
+  static constexpr uint32_t kRope = kK + kRing * kSlot;
+  static constexpr uint32_t kP = kRope + kRopeSlots * kSlot;
   static constexpr uint32_t kScale = kP + kPBufs * kPBuf;
   static constexpr uint32_t kF = kScale + kScaleSlots * 2048;     // [2][NR] float
   static constexpr uint32_t kLen = kF + 2 * NR * 4;               // [2][NR] int
@@ -104,11 +106,11 @@ struct DC {
 };
 
 struct Bars {
-  uint64_t kfull[12], kempty[12], sfull[4], sempty[4], scfull[3], scempty[3];
+  uint64_t kfull[9], kempty[9], rfull[2], rempty[2], sfull[4], sempty[4], scfull[3], scempty[3];
   uint64_t pfull[4], pempty[4], qfull, drain[2];
   uint32_t tmem;
   int abort;
-  int armed_k[12], armed_sc[3];            // copies armed so far per slot
+  int armed_k[9], armed_r[2], armed_sc[3];            // copies armed so far per slot
   int pages_ok[3];                        // of the tile in each scale slot: bit h: page h is loaded
   int first_item, first_tile, my_tiles;   // this CTA's run
   int last_item, active;                  // its last item, the number of CTAs that have a run
@@ -235,6 +237,7 @@ __device__ void copy_role(const DenseParams& p, const CUtensorMap* map, const CU
   int req = 0;
   Ring<C::kRing> k;
   Ring<kScaleSlots> sc;
+  Ring<C::kRopeSlots> rope;
   uint32_t ok = p.wait_ns >= kLeastWaitNs;
   // block-table entries of 16 tiles per load, one lane each, the next 16 tiles' already in flight
   int cur = 0, nxt = 0, base_lp = 0, item = -1;
@@ -289,16 +292,30 @@ __device__ void copy_role(const DenseParams& p, const CUtensorMap* map, const CU
     }
     __syncwarp();
     sc.next();
+    // the rope between the blocks that are loaded ahead and those that wait for the PV of the tile before
 #pragma unroll 1
-    for (int c = 0; c < kChunks; ++c) {
+    for (int c = 0; c < 4; ++c) {
+      if (c == 2) {
+        SMLA_WAIT(&bars->rempty[rope.slot], rope.parity ^ 1);
+        if (ok && ptx::elect_one()) {
+          ++bars->armed_r[rope.slot];
+          ptx::mbar_arrive_expect_tx(&bars->rfull[rope.slot], n_good * (kSlot / 2));
+          for (int h = 0; h < 2; ++h)
+            if (good >> h & 1)
+              ptx::tma_load_3d(base + C::kRope + rope.slot * kSlot + h * (kSlot / 2), map, kDLatent + 16, 0, pg[h],
+                               &bars->rfull[rope.slot]);
+        }
+        __syncwarp();
+        rope.next();
+      }
       SMLA_WAIT(&bars->kempty[k.slot], k.parity ^ 1);
       if (ok && ptx::elect_one()) {
         ++bars->armed_k[k.slot];
         ptx::mbar_arrive_expect_tx(&bars->kfull[k.slot], n_good * (kSlot / 2));
         for (int h = 0; h < 2; ++h)
           if (good >> h & 1)
-            ptx::tma_load_3d(base + C::kK + k.slot * kSlot + h * (kSlot / 2), map, c == 4 ? kDLatent + 16 : 128 * c,
-                             0, pg[h], &bars->kfull[k.slot]);
+            ptx::tma_load_3d(base + C::kK + k.slot * kSlot + h * (kSlot / 2), map, 128 * c, 0, pg[h],
+                             &bars->kfull[k.slot]);
       }
       __syncwarp();
       k.next();
@@ -324,6 +341,7 @@ __device__ void qk_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars
   Walk w(bars);
   Ring<C::kRing> k;
   Ring<C::kSBufs> s;
+  Ring<C::kRopeSlots> rope;
   uint32_t qpar = 0;
   uint32_t ok = p.wait_ns >= kLeastWaitNs;
   int item = -1;
@@ -338,15 +356,17 @@ __device__ void qk_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars
 #pragma unroll 1
     for (int c = 0; c < kChunks; ++c) {
       SMLA_WAIT(&bars->sempty[s.slot], s.parity ^ 1);
-      SMLA_WAIT(&bars->kfull[k.slot], k.parity);
+      SMLA_WAIT(c < 4 ? &bars->kfull[k.slot] : &bars->rfull[rope.slot], c < 4 ? k.parity : rope.parity);
       ptx::tc_fence_after();
       const uint32_t ks = k.slot, d = tmem + C::kSCol + C::kOCols * s.slot, cu = c;
       if (ok && ptx::elect_one()) {
-        const uint64_t dk = ptx::sw128_desc(base + C::kK + ks * kSlot, 16, 1024);
         if (c == 4) {
+          const uint64_t dk = ptx::sw128_desc(base + C::kRope + rope.slot * kSlot, 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) ptx::mma_f16_ss(d, dk + 2 * kk, dr + 2 * kk, kIdescRope, kk > 0);
+          ptx::mma_commit(&bars->rempty[rope.slot]);                // the codes stay for the PV
         } else {
+          const uint64_t dk = ptx::sw128_desc(base + C::kK + ks * kSlot, 16, 1024);
           const uint64_t dqb = dq + (uint64_t)((cu * C::kQ8Chunk) >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
@@ -354,13 +374,13 @@ __device__ void qk_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars
             for (int pass = 0; pass < C::kPasses; ++pass)
               ptx::mma_f8_ss(d, dk + 2 * kk, dqb + 2 * kk + (uint64_t)((pass * NR * 128) >> 4), kIdescCodes, kk > 0 || pass > 0);
         }
-        if (c == 4) ptx::mma_commit(&bars->kempty[k.slot]);   // the codes stay for the PV
         ptx::mma_commit(&bars->sfull[s.slot]);
       }
       __syncwarp();
-      k.next();
+      if (c < 4) k.next();
       s.next();
     }
+    rope.next();
     w.next();
   }
   if (ptx::elect_one()) ptx::mma_commit(&bars->drain[0]);
@@ -400,7 +420,6 @@ __device__ void pv_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars
       k.next();
       pb.next();
     }
-    k.next();                                             // the rope
     w.next();
   }
   if (ptx::elect_one()) ptx::mma_commit(&bars->drain[1]);
@@ -629,18 +648,33 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
   };
   // adds a tile's blocks that are kept in registers (the PV of the tile before, see below)
   auto flush_registers = [&]() {
+    constexpr int kPair = C::kPasses == 2 ? 2 : 1;      // blocks whose loads wait together
 #pragma unroll
-    for (int b = C::kHeldBlocks; b < 4; ++b) {
-      wait_pv(b, C::kHeldBlocks ? 1u : dpar);
-      uint64_t x[HC / 2];
-      uint32_t none[HC];
-      tile_part(b, x, none, false);
+    for (int b0 = C::kHeldBlocks; b0 < 4; b0 += kPair) {
+      uint32_t hi[kPair][HC], lo[kPair][HC];
 #pragma unroll
-      for (int i = 0; i < HC / 2; i += 2) {
-        const ulonglong2 c = ptx::lds128_pairs(row_c + i * 8);
-        uint64_t* d = &o[b - C::kHeldBlocks][i];
-        d[0] = ptx::fma2(x[i], c.x, d[0]);
-        d[1] = ptx::fma2(x[i + 1], c.y, d[1]);
+      for (int j = 0; j < kPair; ++j) {
+        const int b = b0 + j;
+        wait_pv(b, C::kHeldBlocks ? 1u : dpar);
+        const uint32_t a = lane_base + C::kOCols * (b % C::kPBufs) + col0;
+        tmem_ld<HC>(a, hi[j]);
+        if constexpr (C::kPasses == 1) tmem_ld<HC>(a + NR, lo[j]);
+      }
+      ptx::tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < HC; i += 4) {
+        const ulonglong2 c = ptx::lds128_pairs(row_c + i * 4);
+#pragma unroll
+        for (int j = 0; j < kPair; ++j) {
+          uint64_t x0 = ptx::pack2(hi[j][i], hi[j][i + 1]), x1 = ptx::pack2(hi[j][i + 2], hi[j][i + 3]);
+          if constexpr (C::kPasses == 1) {
+            x0 = ptx::add2(x0, ptx::pack2(lo[j][i], lo[j][i + 1]));
+            x1 = ptx::add2(x1, ptx::pack2(lo[j][i + 2], lo[j][i + 3]));
+          }
+          uint64_t* d = &o[b0 + j - C::kHeldBlocks][i / 2];
+          d[0] = ptx::fma2(x0, c.x, d[0]);
+          d[1] = ptx::fma2(x1, c.y, d[1]);
+        }
       }
     }
     dpar ^= 1;
@@ -838,7 +872,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
       }
       if (!here || t >= w.n.min_len) clean_codes<NR>(base, kslot, tok, part, here && t < w.n.max_len);
     }
-    kslot = kslot + kChunks >= C::kRing ? kslot + kChunks - C::kRing : kslot + kChunks;
+    kslot = kslot + 4 >= C::kRing ? kslot + 4 - C::kRing : kslot + 4;
     if (!first) flush_registers();
     // R of each row: every warp ends with its rows' maxima over the 128 positions, lane -> row
 #pragma unroll
@@ -850,19 +884,18 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
     ptx::named_bar_sync(1 + part, 128);
     float back = 1.f;                                   // what a reference that moves takes from the sums so far
     if (lane < HC) {
-      const float m = fmaxf(fmaxf(red[lane], red[NR + lane]), fmaxf(red[2 * NR + lane], red[3 * NR + lane]));
-      float r = 0.f, c = 1.f;
-      if (m > -CUDART_INF_F) {                          // not a row without positions here, or of NaNs alone
-        r = ceilf(m) - kTopWeight;
-        if (!(ref == ref)) ref = r;
-        if (r - ref > kMaxFactor) {
-          back = ptx::ex2_approx(ref - r);
-          ref = r;
-        }
-        c = ptx::ex2_approx(r - ref);
-      }
+      const uint32_t ra = base + C::kRed + (col0 + lane) * 4;
+      const float m = fmaxf(fmaxf(ptx::lds32f(ra), ptx::lds32f(ra + NR * 4)), fmaxf(ptx::lds32f(ra + 2 * NR * 4), ptx::lds32f(ra + 3 * NR * 4)));
+      // a row without positions here, or of NaNs alone: a tile of no weight
+      const bool some = m > -CUDART_INF_F;
+      const float r = some ? ceilf(m) - kTopWeight : 0.f;
+      const float d = some && ref == ref ? r - ref : 0.f;   // (its first tile sets the reference)
+      const bool up = d > kMaxFactor;
       ptx::sts32f(row_nr + lane * 4, -r);
-      ptx::sts32f(row_c + lane * 4, c);
+      const float f = ptx::ex2_approx(up ? -d : d);
+      ptx::sts32f(row_c + lane * 4, up ? 1.f : f);
+      if (up) back = f;
+      if (some && (up || !(ref == ref))) ref = r;
     }
     if (__builtin_expect(__any_sync(0xffffffffu, back != 1.f), 0)) {
 #pragma unroll
@@ -1053,7 +1086,7 @@ __global__ void __launch_bounds__(DC<NR>::kThreads, 1)
   if (threadIdx.x == 0) {
     ptx::prefetch_tensormap(&map);
     ptx::prefetch_tensormap(&smap);
-    for (int i = 0; i < 12; ++i) {
+    for (int i = 0; i < C::kRing; ++i) {
       ptx::mbar_init(&bars->kfull[i], 1);
       ptx::mbar_init(&bars->kempty[i], 1);
       bars->armed_k[i] = 0;
@@ -1070,6 +1103,11 @@ __global__ void __launch_bounds__(DC<NR>::kThreads, 1)
       bars->armed_sc[i] = 0;
     }
     for (int i = 0; i < 2; ++i) ptx::mbar_init(&bars->drain[i], 1);
+    for (int i = 0; i < C::kRopeSlots; ++i) {
+      ptx::mbar_init(&bars->rfull[i], 1);
+      ptx::mbar_init(&bars->rempty[i], 1);
+      bars->armed_r[i] = 0;
+    }
     ptx::mbar_init(&bars->qfull, C::kSoftWarps);
     bars->abort = p.wait_ns < kLeastWaitNs;
     ptx::fence_mbar_init();
@@ -1102,6 +1140,7 @@ __global__ void __launch_bounds__(DC<NR>::kThreads, 1)
   int never = 0;
   if (role == kCopyRole && bars->abort) {
     drain_copies(bars->kfull, bars->armed_k, C::kRing, lane);
+    drain_copies(bars->rfull, bars->armed_r, C::kRopeSlots, lane);
     drain_copies(bars->scfull, bars->armed_sc, kScaleSlots, lane);
   }
   if (role == kQkRole) {
