@@ -49,9 +49,10 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kTopWeight = 7.f;         // a tile's largest weight of a row lies in (2^6, 2^7]
+constexpr float kTopWeight = 7.75f;       // a row's largest weight is at most 2^7.75: times m_b < 2 within E4M3's 448
+constexpr float kWindow = 2.f;            // a tile's largest weight may lie so many powers of two lower
+constexpr float kLowest = 30.f;           // how far below its highest value a reference may go
 constexpr int kMostTiles16 = 4, kMostTiles32 = 24;   // tiles of a CTA up to which row groups are of 16 and of 32
-constexpr float kMaxFactor = 20.f;        // a tile's factor 2^(R - ref) above 2^20 moves ref
 
 // Warps: the softmax warps (warp w: TMEM lanes of quadrant w % 4, row part w / 4), then one warp each for the
 // copies, the QK and the PV, and one that describes the run for the merge.
@@ -59,22 +60,19 @@ enum { kCopyRole, kQkRole, kPvRole };
 
 constexpr uint32_t kSlot = 16384;         // 128 positions x 128 bytes: one code block or the rope of a tile
 constexpr int kChunks = 5;                // of a tile's scores: the four code blocks, then the rope
-constexpr int kScaleSlots = 3;
 constexpr int kAhead = 1;                 // tiles between a tile's prefetch into L2 and its copy
 
 template <int NR>
 struct DC {
   static constexpr int kRing = NR == 64 ? 6 : NR == 32 ? 8 : 9;     // slots of code blocks
   static constexpr int kRopeSlots = NR == 16 ? 2 : 1;
+  static constexpr int kScaleSlots = NR == 64 ? 2 : 3;
   static constexpr int kPBufs = NR == 64 ? 2 : 4;                   // weights of so many blocks
   static constexpr int kSBufs = 4;                                  // score accumulators
   // hi and lo terms (of q, and of the weights) meet in one accumulator for 64 rows, where TMEM is full; for fewer rows
   // they are one MMA of twice the columns and meet in the registers
   static constexpr int kPasses = NR == 64 ? 2 : 1;
   static constexpr int kOCols = NR == 64 ? NR : 2 * NR;             // columns of a block's O^T of one tile, or scores
-  // TMEM: O^T of one tile (kPBufs blocks at a time), score buffers, and for 64 rows, whose accumulators do not all fit
-  // the registers, those of blocks 0 and 1
-  static constexpr int kHeldBlocks = NR == 64 ? 2 : 0;
   // Row parts: 8 softmax warps.  (16, with half the rows per thread, were slower, and so were 8 with 8 more for the
   // accumulators: 32 x 32768 positions of 64 heads took 292 us instead of 249.)
   static constexpr int kParts = 2;
@@ -94,13 +92,13 @@ struct DC {
   static constexpr uint32_t kScale = kP + kPBufs * kPBuf;
   static constexpr uint32_t kF = kScale + kScaleSlots * 2048;     // [2][NR] float
   static constexpr uint32_t kLen = kF + 2 * NR * 4;               // [2][NR] int
-  static constexpr uint32_t kRed = kLen + 2 * NR * 4;             // [4][NR] float
-  static constexpr uint32_t kRow = kRed + 4 * NR * 4;             // per softmax warp [HC] minus R, [HC] factor
+  static constexpr uint32_t kRed = kLen + 2 * NR * 4;             // [2][4][NR] float
+  static constexpr uint32_t kRow = kRed + 8 * NR * 4;             // per softmax warp [HC] minus R, [HC] factor
   static constexpr uint32_t kBar = kRow + kSoftWarps * 2 * HC * 4;
   static constexpr uint32_t kBytes = kBar + 640;
-  static constexpr uint32_t kSCol = kPBufs * kOCols;              // score buffer i at kSCol + kOCols i
-  static constexpr uint32_t kHeld = kSCol + kSBufs * kOCols;      // accumulators of block b at kHeld + NR b
-  static constexpr uint32_t kTmemCols = kHeld + kHeldBlocks * NR;
+  // TMEM: O^T of block b at kOCols b, score buffer i at kSCol + kOCols i
+  static constexpr uint32_t kSCol = 4 * kOCols;
+  static constexpr uint32_t kTmemCols = kSCol + kSBufs * kOCols;
   static_assert(kBytes <= 232448, "shared memory");
   static_assert(kTmemCols == 512 || kTmemCols == 256, "TMEM allocations are powers of two");
 };
@@ -236,7 +234,7 @@ __device__ void copy_role(const DenseParams& p, const CUtensorMap* map, const CU
   Walk w(bars);
   int req = 0;
   Ring<C::kRing> k;
-  Ring<kScaleSlots> sc;
+  Ring<C::kScaleSlots> sc;
   Ring<C::kRopeSlots> rope;
   uint32_t ok = p.wait_ns >= kLeastWaitNs;
   // block-table entries of 16 tiles per load, one lane each, the next 16 tiles' already in flight
@@ -396,13 +394,16 @@ __device__ void pv_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars
   Ring<C::kRing> k;
   Ring<C::kPBufs> pb;
   uint32_t ok = p.wait_ns >= kLeastWaitNs;
+  int item = -1;
 #pragma unroll 1
   while (w.here(p)) {
+    const uint32_t more = item == w.i;                    // not the segment's first tile
+    item = w.i;
 #pragma unroll 1
     for (int b = 0; b < 4; ++b) {
       SMLA_WAIT(&bars->pfull[pb.slot], pb.parity);
       ptx::tc_fence_after();
-      const uint32_t ks = k.slot, ps = pb.slot, d = tmem + N * pb.slot;
+      const uint32_t ks = k.slot, ps = pb.slot, d = tmem + N * b;
       if (ok && ptx::elect_one()) {
         // codes^T: 128-byte rows of one position, 8-position groups 1024 bytes apart; 32 positions per MMA
         const uint64_t dv = ptx::sw128_desc(base + C::kK + ks * kSlot, 1024, 1024);
@@ -412,7 +413,8 @@ __device__ void pv_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars
 #pragma unroll
           for (int pass = 0; pass < C::kPasses; ++pass)
             ptx::mma_f8_ss(d, dv + (uint64_t)(256 * kk),
-                           dp + (uint64_t)((32 * C::kPRow * kk + NR * pass) >> 4), kIdesc, kk > 0 || pass > 0);
+                           dp + (uint64_t)((32 * C::kPRow * kk + NR * pass) >> 4), kIdesc,
+                           kk > 0 || pass > 0 ? 1 : more);
         ptx::mma_commit(&bars->kempty[k.slot]);
         ptx::mma_commit(&bars->pempty[pb.slot]);
       }
@@ -609,97 +611,35 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
                              int lane, float* o_part, float* lse_part) {
   using C = DC<NR>;
   constexpr int HC = C::HC;                             // rows per thread
+  constexpr int kChunk = 8;                             // rows that are scaled back or written at once
   const int part = warp >> 2, quad = warp & 3, col0 = part * HC;
   const int tok = 32 * quad + lane;
   const uint32_t lane_base = tmem + ((uint32_t)(32 * quad) << 16);
   const float kf = p.sm_scale * kLog2e;
-  float* red = reinterpret_cast<float*>(sm + C::kRed) + col0;   // [4][NR]
-  const uint32_t row_nr = base + C::kRow + warp * 2 * HC * 4, row_c = row_nr + HC * 4;
+  const uint32_t row_nr = base + C::kRow + warp * 2 * HC * 4, row_f = row_nr + HC * 4;
   Walk w(bars);
   Ring<C::kSBufs> s;
-  Ring<kScaleSlots> sc;
-  int kslot = 0, pslot = 0;
-  uint32_t dpar = 0;
+  Ring<C::kScaleSlots> sc;
+  Ring<C::kPBufs> pb;
+  int kslot = 0;
+  uint32_t red = base + C::kRed + col0 * 4, red_other = red + 4 * NR * 4;   // values of a part's rows meet here: [quad][row]
+  uint32_t last_par = 0;                                // of the last tile's last PV
   uint32_t ok = p.wait_ns >= kLeastWaitNs;
   bool first = true, begins = w.t == 0;
   int buf = 0;
-  // O of dim 128 b + tok, pairs of rows: blocks from kHeldBlocks on (the others are held in TMEM)
-  uint64_t o[4 - C::kHeldBlocks][HC / 2];
-  uint64_t l[HC / 2];                                   // row sums over this thread's positions
-  float ref = CUDART_NAN_F;                             // of row col0 + lane; NaN: the row has met no position
+  uint64_t l[HC / 2];                                   // row sums over this thread's positions, pairs of rows
+  float ref = CUDART_NAN_F;                             // R of row col0 + lane; NaN: the row has met no position
+  float top = 0.f;                                      // its highest value
 
-  // Block b's O^T of one tile (pairs of rows); with `held`, its accumulators from TMEM in the same wait.
-  auto tile_part = [&](int b, uint64_t (&x)[HC / 2], uint32_t (&held)[HC], bool load_held) {
-    uint32_t hi[HC], lo[HC];
-    const uint32_t a = lane_base + C::kOCols * (b % C::kPBufs) + col0;
-    tmem_ld<HC>(a, hi);
-    if constexpr (C::kPasses == 1) tmem_ld<HC>(a + NR, lo);
-    if (load_held) tmem_ld<HC>(lane_base + C::kHeld + NR * b + col0, held);
-    ptx::tmem_wait_ld();
-#pragma unroll
-    for (int i = 0; i < HC / 2; ++i) {
-      x[i] = ptx::pack2(hi[2 * i], hi[2 * i + 1]);
-      if constexpr (C::kPasses == 1) x[i] = ptx::add2(x[i], ptx::pack2(lo[2 * i], lo[2 * i + 1]));
-    }
-  };
-  auto wait_pv = [&](int b, uint32_t parity) {
-    SMLA_WAIT(&bars->pempty[b % C::kPBufs], parity);
+  // every PV of the tiles before is done: their accumulators (dims 128 b + tok) can be read and scaled
+  auto wait_pv = [&]() {
+    SMLA_WAIT(&bars->pempty[3 % C::kPBufs], last_par);
     ptx::tc_fence_after();
   };
-  // adds a tile's blocks that are kept in registers (the PV of the tile before, see below)
-  auto flush_registers = [&]() {
-    constexpr int kPair = C::kPasses == 2 ? 2 : 1;      // blocks whose loads wait together
-#pragma unroll
-    for (int b0 = C::kHeldBlocks; b0 < 4; b0 += kPair) {
-      uint32_t hi[kPair][HC], lo[kPair][HC];
-#pragma unroll
-      for (int j = 0; j < kPair; ++j) {
-        const int b = b0 + j;
-        wait_pv(b, C::kHeldBlocks ? 1u : dpar);
-        const uint32_t a = lane_base + C::kOCols * (b % C::kPBufs) + col0;
-        tmem_ld<HC>(a, hi[j]);
-        if constexpr (C::kPasses == 1) tmem_ld<HC>(a + NR, lo[j]);
-      }
-      ptx::tmem_wait_ld();
-#pragma unroll
-      for (int i = 0; i < HC; i += 4) {
-        const ulonglong2 c = ptx::lds128_pairs(row_c + i * 4);
-#pragma unroll
-        for (int j = 0; j < kPair; ++j) {
-          uint64_t x0 = ptx::pack2(hi[j][i], hi[j][i + 1]), x1 = ptx::pack2(hi[j][i + 2], hi[j][i + 3]);
-          if constexpr (C::kPasses == 1) {
-            x0 = ptx::add2(x0, ptx::pack2(lo[j][i], lo[j][i + 1]));
-            x1 = ptx::add2(x1, ptx::pack2(lo[j][i + 2], lo[j][i + 3]));
-          }
-          uint64_t* d = &o[b0 + j - C::kHeldBlocks][i / 2];
-          d[0] = ptx::fma2(x0, c.x, d[0]);
-          d[1] = ptx::fma2(x1, c.y, d[1]);
-        }
-      }
-    }
-    dpar ^= 1;
-    ptx::tc_fence_before();
-  };
-  // adds block b (held in TMEM); `start`: the segment's first tile
-  auto flush_held = [&](int b, bool start) {
-    wait_pv(b, 0u);
-    uint64_t x[HC / 2];
-    uint32_t h[HC];
-    ptx::tmem_wait_st();                                // the last tile's
-    tile_part(b, x, h, true);                           // (before the segment's first tile: whatever was there)
-#pragma unroll
-    for (int i = 0; i < HC / 2; i += 2) {
-      const ulonglong2 c = ptx::lds128_pairs(row_c + i * 8);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint64_t before = start ? 0 : ptx::pack2(h[2 * (i + j)], h[2 * (i + j) + 1]);
-        const float2 d = ptx::unpack2(ptx::fma2(x[i + j], j ? c.y : c.x, before));
-        h[2 * (i + j)] = __float_as_uint(d.x);
-        h[2 * (i + j) + 1] = __float_as_uint(d.y);
-      }
-    }
-    tmem_st<HC>(lane_base + C::kHeld + NR * b + col0, h);
-    ptx::tc_fence_before();
+  auto swap_red = [&]() {
+    const uint32_t r = red;
+    red = red_other;
+    red_other = r;
   };
 
   int item = -1, done = -1;                             // items whose rows are loaded, whose segment has ended
@@ -720,7 +660,6 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
     if (!more) done = item;
     if (first && done >= 0) {
       const Rows it = rows_of(p, done);
-      flush_registers();
       // row sums over the tile's 128 positions
       float ls[HC];
 #pragma unroll
@@ -730,60 +669,61 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
         ls[2 * i + 1] = x.y;
       }
       const float sum = reduce_scatter<HC>(ls, lane, [](float a, float b) { return a + b; });
-      ptx::named_bar_sync(1 + part, 128);                 // the maxima have been read
-      if (lane < HC) red[quad * NR + lane] = sum;
+      if (lane < HC) ptx::sts32f(red + (quad * NR + lane) * 4, sum);
       ptx::named_bar_sync(1 + part, 128);
       // a run's first segment that continues an item goes to slot 0 of the CTA, its last segment to slot 1
       const size_t slot = 2 * (size_t)blockIdx.x + (begins ? 1 : 0);
-      float inv = 0.f;
       if (lane < HC) {
-        const float z = red[lane] + red[NR + lane] + red[2 * NR + lane] + red[3 * NR + lane];
-        inv = z > 0.f ? 1.f / z : (z == 0.f ? 0.f : CUDART_NAN_F);
+        const uint32_t at = red + lane * 4;
+        const float z = ptx::lds32f(at) + ptx::lds32f(at + NR * 4) + ptx::lds32f(at + 2 * NR * 4) + ptx::lds32f(at + 3 * NR * 4);
+        const float inv = z > 0.f ? 1.f / z : (z == 0.f ? 0.f : CUDART_NAN_F);
         const float lse = z == 0.f ? -CUDART_INF_F : (log2f(z) + ref) * kLn2;
         if (quad == 0 && ok && col0 + lane < it.nrows) {
           if (whole) p.lse[(size_t)it.req * p.q_per_req * p.H + it.row0 + col0 + lane] = lse;
           else lse_part[slot * NR + col0 + lane] = lse;
         }
+        ptx::sts32f(row_f + lane * 4, inv);               // the rows' factors 1 / l, read back as pairs
       }
-      // the rows' factors 1 / l, read back as pairs
-      if (lane < HC) ptx::sts32f(row_c + lane * 4, inv);
+      swap_red();
       __syncwarp();
       // lanes 2j, 2j + 1 hold dims d, d + 1 of two rows: the first ends with both dims of the first row, the other
       // with both of the second, and writes them there
       const bool second = lane & 1;
       const int c0 = col0 + (second ? 1 : 0);             // this thread's rows: c0, c0 + 2, ...
-      const bool all = ok && it.nrows == NR;
       const size_t row0 = whole ? (size_t)it.req * p.q_per_req * p.H + it.row0 : slot * NR;
       const size_t at = (row0 + c0) * kDLatent + (tok & ~1);
-      const int rows_left = ok ? (all ? NR : it.nrows - c0) : 0;
-#pragma unroll
-      for (int b = C::kHeldBlocks; b < 4; ++b) {
-        if (whole) write_block<HC, true>(o[b - C::kHeldBlocks], row_c, rows_left, second, p.out + at + 128 * b);
-        else write_block<HC, false>(o[b - C::kHeldBlocks], row_c, rows_left, second, o_part + at + 128 * b);
-      }
+      const int rows_left = ok ? it.nrows - c0 : 0;
+      wait_pv();
 #pragma unroll 1
-      for (int b = 0; b < C::kHeldBlocks; ++b) {
-        uint32_t h[HC];
-        uint64_t x[HC / 2];
-        ptx::tmem_wait_st();
-        tmem_ld<HC>(lane_base + C::kHeld + NR * b + col0, h);
+      for (int i0 = 0; i0 < HC; i0 += kChunk) {
+        uint32_t hi[4][kChunk], lo[4][kChunk];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          tmem_ld<kChunk>(lane_base + C::kOCols * b + col0 + i0, hi[b]);
+          if constexpr (C::kPasses == 1) tmem_ld<kChunk>(lane_base + C::kOCols * b + NR + col0 + i0, lo[b]);
+        }
         ptx::tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < HC / 2; ++i) x[i] = ptx::pack2(h[2 * i], h[2 * i + 1]);
-        if (whole) write_block<HC, true>(x, row_c, rows_left, second, p.out + at + 128 * b);
-        else write_block<HC, false>(x, row_c, rows_left, second, o_part + at + 128 * b);
+        for (int b = 0; b < 4; ++b) {
+          uint64_t x[kChunk / 2];
+#pragma unroll
+          for (int i = 0; i < kChunk / 2; ++i) {
+            x[i] = ptx::pack2(hi[b][2 * i], hi[b][2 * i + 1]);
+            if constexpr (C::kPasses == 1) x[i] = ptx::add2(x[i], ptx::pack2(lo[b][2 * i], lo[b][2 * i + 1]));
+          }
+          const size_t to = at + 128 * b + (size_t)i0 * kDLatent;
+          if (whole) write_block<kChunk, true>(x, row_f + i0 * 4, rows_left - i0, second, p.out + to);
+          else write_block<kChunk, false>(x, row_f + i0 * 4, rows_left - i0, second, o_part + to);
+        }
       }
+      ptx::tc_fence_before();
       begins = true;
     }
     if (!more) break;
     if (first) {
       ptx::named_bar_sync(1 + C::kParts, C::kSoftWarps * 32);          // red is free, the rows' factors and lengths are written
 #pragma unroll
-      for (int i = 0; i < HC / 2; ++i) {
-        l[i] = 0;
-#pragma unroll
-        for (int b = 0; b < 4 - C::kHeldBlocks; ++b) o[b][i] = 0;
-      }
+      for (int i = 0; i < HC / 2; ++i) l[i] = 0;
       ref = CUDART_NAN_F;
     }
     // scores of this thread's position for its HC rows, in units of log2
@@ -873,53 +813,62 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
       if (!here || t >= w.n.min_len) clean_codes<NR>(base, kslot, tok, part, here && t < w.n.max_len);
     }
     kslot = kslot + 4 >= C::kRing ? kslot + 4 - C::kRing : kslot + 4;
-    if (!first) flush_registers();
     // R of each row: every warp ends with its rows' maxima over the 128 positions, lane -> row
 #pragma unroll
     for (int i = 0; i < HC / 2; i += 2) {
       const float2 a = ptx::unpack2(acc[i]), b = ptx::unpack2(acc[i + 1]);
       const float m0 = ptx::warp_max(a.x), m1 = ptx::warp_max(a.y), m2 = ptx::warp_max(b.x), m3 = ptx::warp_max(b.y);
-      if (lane == 0) ptx::sts128f(base + C::kRed + (quad * NR + col0 + 2 * i) * 4, m0, m1, m2, m3);
+      if (lane == 0) ptx::sts128f(red + (quad * NR + 2 * i) * 4, m0, m1, m2, m3);
     }
     ptx::named_bar_sync(1 + part, 128);
-    float back = 1.f;                                   // what a reference that moves takes from the sums so far
+    float f = 1.f;                                      // what a reference that moves takes from the sums so far
     if (lane < HC) {
-      const uint32_t ra = base + C::kRed + (col0 + lane) * 4;
-      const float m = fmaxf(fmaxf(ptx::lds32f(ra), ptx::lds32f(ra + NR * 4)), fmaxf(ptx::lds32f(ra + 2 * NR * 4), ptx::lds32f(ra + 3 * NR * 4)));
-      // a row without positions here, or of NaNs alone: a tile of no weight
-      const bool some = m > -CUDART_INF_F;
-      const float r = some ? ceilf(m) - kTopWeight : 0.f;
-      const float d = some && ref == ref ? r - ref : 0.f;   // (its first tile sets the reference)
-      const bool up = d > kMaxFactor;
-      ptx::sts32f(row_nr + lane * 4, -r);
-      const float f = ptx::ex2_approx(up ? -d : d);
-      ptx::sts32f(row_c + lane * 4, up ? 1.f : f);
-      if (up) back = f;
-      if (some && (up || !(ref == ref))) ref = r;
-    }
-    if (__builtin_expect(__any_sync(0xffffffffu, back != 1.f), 0)) {
-#pragma unroll
-      for (int i = 0; i < HC / 2; ++i) {
-        const uint64_t f = ptx::pack2(__shfl_sync(0xffffffffu, back, 2 * i), __shfl_sync(0xffffffffu, back, 2 * i + 1));
-        l[i] = ptx::mul2(l[i], f);
-#pragma unroll
-        for (int b = 0; b < 4 - C::kHeldBlocks; ++b) o[b][i] = ptx::mul2(o[b][i], f);
+      const uint32_t at = red + lane * 4;
+      const float m = fmaxf(fmaxf(ptx::lds32f(at), ptx::lds32f(at + NR * 4)),
+                            fmaxf(ptx::lds32f(at + 2 * NR * 4), ptx::lds32f(at + 3 * NR * 4)));
+      // (a row without positions here, or of NaNs alone, keeps its reference)
+      const float r = ceilf(m - kTopWeight);
+      if (m > -CUDART_INF_F && !(r <= ref && r >= ref - kWindow)) {
+        const bool set = ref == ref;
+        const float to = set ? fmaxf(r + 1.f, top - kLowest) : r + 1.f;
+        if (set) f = exp2_int((int)fminf(fmaxf(ref - to, -126.f), 126.f));
+        top = set ? fmaxf(top, to) : to;
+        ref = to;
       }
-      if (!first) {
-        ptx::tmem_wait_st();
+      ptx::sts32f(row_nr + lane * 4, ref == ref ? -ref : 0.f);
+      ptx::sts32f(row_f + lane * 4, f);
+    }
+    swap_red();
+    const uint32_t moved = __ballot_sync(0xffffffffu, f != 1.f);
+    if (moved) {                                        // (the ballot orders the factors' stores before the loads)
+#pragma unroll
+      for (int i = 0; i < HC / 2; i += 2) {
+        const ulonglong2 c = ptx::lds128_pairs(row_f + i * 8);
+        l[i] = ptx::mul2(l[i], c.x);
+        l[i + 1] = ptx::mul2(l[i + 1], c.y);
+      }
+      wait_pv();
 #pragma unroll 1
-        for (int j = 0; j < C::kHeldBlocks * HC; j += 8) {
-          const uint32_t a = lane_base + C::kHeld + NR * (j / HC) + col0 + j % HC;
-          uint32_t h[8];
-          ptx::tmem_ld8(a, h);
+      for (int i0 = 0; i0 < HC; i0 += kChunk) {
+        if (!(moved >> i0 & 0xffu)) continue;
+        const float4 f0 = ptx::lds128f(row_f + i0 * 4), f1 = ptx::lds128f(row_f + i0 * 4 + 16);
+        const float c[kChunk] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+#pragma unroll
+        for (int j = 0; j < (C::kPasses == 1 ? 2 : 1); ++j) {
+          uint32_t x[4][kChunk];
+#pragma unroll
+          for (int b = 0; b < 4; ++b) tmem_ld<kChunk>(lane_base + C::kOCols * b + NR * j + col0 + i0, x[b]);
           ptx::tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            h[i] = __float_as_uint(__uint_as_float(h[i]) * __shfl_sync(0xffffffffu, back, j % HC + i));
-          ptx::tmem_st8(a, h);
+          for (int b = 0; b < 4; ++b) {
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) x[b][i] = __float_as_uint(__uint_as_float(x[b][i]) * c[i]);
+            tmem_st<kChunk>(lane_base + C::kOCols * b + NR * j + col0 + i0, x[b]);
+          }
         }
-        ptx::tmem_wait_st();
       }
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
     }
     __syncwarp();
     // weights
@@ -929,12 +878,12 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
       const uint64_t down = ptx::pack2(d, d);
 #pragma unroll
       for (int i = 0; i < HC / 2; i += 2) {
-        const ulonglong2 nr = ptx::lds128_pairs(row_nr + i * 8), c = ptx::lds128_pairs(row_c + i * 8);
+        const ulonglong2 nr = ptx::lds128_pairs(row_nr + i * 8);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const float2 x = ptx::unpack2(ptx::add2(acc[i + j], j ? nr.y : nr.x));
           const float a = ptx::ex2_approx(x.x), b = ptx::ex2_approx(x.y);
-          l[i + j] = ptx::fma2(ptx::mul2(ptx::pack2(a, b), down), j ? c.y : c.x, l[i + j]);
+          l[i + j] = ptx::fma2(ptx::pack2(a, b), down, l[i + j]);
           const __half2 h = __floats2half2_rn(a, b);
           w16[i + j] = *reinterpret_cast<const uint32_t*>(&h);
         }
@@ -958,10 +907,8 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
           e4m3x4_to_f16x4(hi[i], bx, by);
           lo[i] = f16x4_to_e4m3x4(as_u32(__hsub2(x, as_half2(bx))), as_u32(__hsub2(y, as_half2(by))));
         }
-        // a tile's blocks beyond the buffers wait for the block before in theirs, and take its O^T; the others find
-        // their buffers free, since the tile before has been added up
-        if (C::kHeldBlocks > 0 && b >= C::kPBufs) flush_held(b - C::kPBufs, first);
-        const uint32_t dst = base + C::kP + pslot * C::kPBuf;
+        SMLA_WAIT(&bars->pempty[pb.slot], pb.parity ^ 1);
+        const uint32_t dst = base + C::kP + pb.slot * C::kPBuf;
         if constexpr (HC >= 16) {
 #pragma unroll
           for (int u = 0; u < HC / 16; ++u) {
@@ -976,8 +923,9 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (ok && lane == 0) ptx::mbar_arrive(&bars->pfull[pslot]);
-        pslot = pslot + 1 == C::kPBufs ? 0 : pslot + 1;
+        if (ok && lane == 0) ptx::mbar_arrive(&bars->pfull[pb.slot]);
+        if (b == 3) last_par = pb.parity;
+        pb.next();
       }
     }
 
@@ -1097,7 +1045,7 @@ __global__ void __launch_bounds__(DC<NR>::kThreads, 1)
       ptx::mbar_init(&bars->pfull[i], C::kSoftWarps);
       ptx::mbar_init(&bars->pempty[i], 1);
     }
-    for (int i = 0; i < kScaleSlots; ++i) {
+    for (int i = 0; i < C::kScaleSlots; ++i) {
       ptx::mbar_init(&bars->scfull[i], 1);
       ptx::mbar_init(&bars->scempty[i], C::kSoftWarps);
       bars->armed_sc[i] = 0;
@@ -1141,7 +1089,7 @@ __global__ void __launch_bounds__(DC<NR>::kThreads, 1)
   if (role == kCopyRole && bars->abort) {
     drain_copies(bars->kfull, bars->armed_k, C::kRing, lane);
     drain_copies(bars->rfull, bars->armed_r, C::kRopeSlots, lane);
-    drain_copies(bars->scfull, bars->armed_sc, kScaleSlots, lane);
+    drain_copies(bars->scfull, bars->armed_sc, C::kScaleSlots, lane);
   }
   if (role == kQkRole) {
     ptx::mbar_wait_warp(&bars->drain[0], 0, &never, lane, 100000000ull);
