@@ -401,10 +401,9 @@ int sparse_mla_dense_plan(const smla_dense_dims* dims, int32_t device, smla_dens
  * for latent elements below about 2^-9 of their row's largest, whose absolute
  * error stays below 2^-17 of that largest).  The values are the codes as they
  * are; a softmax weight times a position's scale is two E4M3 terms on chip,
- * scaled by a power of two per row and 128-position tile: off by 2^-8 of itself
- * or 2^-16 of the tile's largest, whichever is more.  Tiles are added in fp32
- * with their own powers of two, so that a long tail of small weights is kept
- * beside one dominating position.  A row that sees a NaN (in q, a code, a scale
+ * scaled by a power of two per row that follows its 128-position tiles: off by
+ * 2^-8 of itself or 2^-13 of its tile's largest, whichever is more, so that a
+ * long tail of small weights is kept beside one dominating position.  A row that sees a NaN (in q, a code, a scale
  * or the rope) is NaN.
  * Statuses as sparse_mla_decode. */
 int sparse_mla_dense_decode(const smla_dense_dims* dims, const void* q, const void* kv_cache,

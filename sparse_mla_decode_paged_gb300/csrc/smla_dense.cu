@@ -17,22 +17,25 @@
 // columns and meet in the softmax threads, for 64, where TMEM is full, two MMAs into NR columns.  The softmax threads
 // form s = 2^x sum_b (S_hi + S_lo) scale_b in fp32.  The rope part is a bf16 product.
 // Weights and values.  The codes are the values, too: O^T[512 x NR] += codes^T (P scale), with the same tile read
-// MN-major.  A position's scales are split as scale_b = m_b 2^e, e the exponent of the largest of the four, and the
-// weight takes the power of two: w = 2^(s + e - R), with R a row's maximum of s + e over the tile's 128
-// positions (rounded up) less 7, so that w m_b stays below 2^8.  Block b's operand is w m_b as two E4M3 terms, hi + lo:
-// 8 significant bits (off by 2^-9 at most) down to 2^-6 of that range and steps of 2^-9 below.  w and m_b are fp16
-// before (their product once more: 3 roundings of 2^-11), so every weight is off by at most 2^-8 of itself or 2^-16 of
-// the tile's largest.  A tile's O^T is added to fp32
-// accumulators (in registers; for 64 rows those of blocks 0 and 1 in TMEM) with the row's factor 2^(R - ref) (ref: R of the row's first tile), so tiles of
-// very different weight (a long tail beside one dominating position) lose nothing to one another.
-//   l = sum w 2^(R - ref - e) in fp32, out = O / l, lse = ln 2 (ref + log2 l).
+// MN-major, accumulated in TMEM over the run's tiles of an item.  A position's scales are split as scale_b = m_b 2^e, e
+// the exponent of the largest of the four, and the weight takes the power of two: w = 2^(s + e - R), with R an integer
+// per row.  Block b's operand is w m_b as two E4M3 terms, hi + lo: 8 significant bits (off by 2^-9 at most) down to
+// 2^-6 and steps of 2^-9 below.  w and m_b are fp16 before (their product once more: 3 roundings of 2^-11).
+//   R follows the tiles' maxima: it moves when a tile's largest weight of the row would lie above 2^7.75 (w m_b < 448)
+// or at or below 2^3.75, and the row's accumulators and sum are then scaled by a power of two, which is exact.  So every
+// weight is off by at most 2^-8 of itself or 2^-13.75 of its tile's largest, and a long tail beside one dominating
+// position keeps its bits.  Moves cost: with a range of 3 powers of two 32 x 32768 positions of 64 heads (random
+// queries and records) take 224 us, with 2 228 us, with 4 218 us, without moves 214 us.  (R does not go further than 30
+// below its highest: what lies there is below 2^-30 of the row's largest weight, and the sums stay finite.)
+//   l = sum w 2^-e in fp32, out = O / l, lse = ln 2 (R + log2 l).
 //
-// What bounds it: HBM bytes (656 per position) for 16 rows and all but that for 32; for 64 rows the steps of a tile
-// inside an SM.  Of the 8000 cycles that a tile of 64 rows takes (3.9 us; an SM's share of the HBM rate is a tile per
-// 1.9 us) the tensor core is busy for about 3300, which is the rate at which shared memory feeds it (M = 128 positions,
-// N = 64: 6 KB of operands per MMA of 32 dims or positions); the rest is the chain from scores to weights to O^T, whose
-// K slots come free behind the PV.  Measured, 32 requests x 32768 positions: 64 heads 249 us (2.8 TB/s), 32 heads 157 us
-// (4.4 TB/s), 16 heads 123 us (5.6 TB/s); 1 x 8192 positions of 64 heads 18.6 us, 1 x 77 of 16 heads 11 us.
+// What bounds it: HBM bytes (656 per position) for 16 rows and nearly so for 32; for 64 rows the steps of a tile inside
+// an SM.  Of the 6700 cycles that a tile of 64 rows takes (3.2 us; an SM's share of the HBM rate is a tile per 1.9 us)
+// shared memory feeds the tensor core for 3300 (M = 128 positions or dims, N = 64: 6 KB of operands per MMA of 32 dims or
+// positions) and takes in and gives out another 100 KB; the rest is the latency from scores to weights to the PV, whose
+// K slots come free one by one for the next tile's blocks.  Measured, 32 requests x 32768 positions: 64 heads 224 us
+// (3.1 TB/s), 32 heads 140 us (4.9 TB/s), 16 heads 122 us (5.7 TB/s); 1 x 8192 positions of 64 heads 18.5 us, 1 x 77 of
+// 16 heads 11 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -50,7 +53,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kTopWeight = 7.75f;       // a row's largest weight is at most 2^7.75: times m_b < 2 within E4M3's 448
-constexpr float kWindow = 2.f;            // a tile's largest weight may lie so many powers of two lower
+constexpr float kWindow = 3.f;            // a row's reference moves when a tile's largest weight would lie further below that
 constexpr float kLowest = 30.f;           // how far below its highest value a reference may go
 constexpr int kMostTiles16 = 4, kMostTiles32 = 24;   // tiles of a CTA up to which row groups are of 16 and of 32
 
@@ -60,12 +63,14 @@ enum { kCopyRole, kQkRole, kPvRole };
 
 constexpr uint32_t kSlot = 16384;         // 128 positions x 128 bytes: one code block or the rope of a tile
 constexpr int kChunks = 5;                // of a tile's scores: the four code blocks, then the rope
-constexpr int kAhead = 1;                 // tiles between a tile's prefetch into L2 and its copy
+// Tiles between a tile's prefetch into L2 and its copy (32 x 32768 positions of 64 heads when a tile took 3.9 us: 249 us, 2
+// tiles 253, 3 tiles 261, no prefetch 255).
+constexpr int kAhead = 1;
 
 template <int NR>
 struct DC {
   static constexpr int kRing = NR == 64 ? 6 : NR == 32 ? 8 : 9;     // slots of code blocks
-  static constexpr int kRopeSlots = NR == 16 ? 2 : 1;
+  static constexpr int kRopeSlots = NR == 16 ? 2 : 1;              // the rope's slot is free once its scores are done
   static constexpr int kScaleSlots = NR == 64 ? 2 : 3;
   static constexpr int kPBufs = NR == 64 ? 2 : 4;                   // weights of so many blocks
   static constexpr int kSBufs = 4;                                  // score accumulators
@@ -73,8 +78,8 @@ struct DC {
   // they are one MMA of twice the columns and meet in the registers
   static constexpr int kPasses = NR == 64 ? 2 : 1;
   static constexpr int kOCols = NR == 64 ? NR : 2 * NR;             // columns of a block's O^T of one tile, or scores
-  // Row parts: 8 softmax warps.  (16, with half the rows per thread, were slower, and so were 8 with 8 more for the
-  // accumulators: 32 x 32768 positions of 64 heads took 292 us instead of 249.)
+  // Row parts: 8 softmax warps.  (16, with half the rows per thread, take as long for 64 rows and longer for 32: 32 x
+  // 32768 positions of 64 heads 231 us instead of 228.)
   static constexpr int kParts = 2;
   static constexpr int kSoftWarps = 4 * kParts;
   static constexpr int kThreads = 32 * (kSoftWarps + 4);

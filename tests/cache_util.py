@@ -48,8 +48,8 @@ def check_dense(out, lse, q, cache, bt, lens, sm_scale):
     out: one bf16 rounding (2^-8 of the value).  A weight is rounded to fp16, times a scale factor rounded to fp16, the
     product rounded to fp16, then to two E4M3 terms of 8 bits in all: 3 * 2^-11 + 2^-9 of itself, with 2^-11 more for
     the float32 exponential, sums and merge, so 2^-8 of the weighted magnitudes; below the range of those 8
-    bits the second term has steps of 2^-9 where the tile's largest weight is at least 2^4.75 (of a row whose reference
-    has not gone as far below its highest as it may): 2^-14 of the tile's largest.  A score error e changes a weight by at most 2 e.
+    bits the second term has steps of 2^-9 where the tile's largest weight is at least 2^3.75 (of a row whose reference
+    has not gone as far below its highest as it may): 2^-13.75 of the tile's largest.  A score error e changes a weight by at most 2 e.
     lse: the score error, and 2^-20 for exponential, sum and logarithm with 2^-22 of its size."""
     ref, rl, weighted, floor, e = dense_oracle.dense_decode(bits(q).reshape(q.shape), cache.cpu().numpy(), bt.cpu().numpy(),
                                                             lens.cpu().numpy(), sm_scale)
@@ -60,7 +60,7 @@ def check_dense(out, lse, q, cache, bt, lens, sm_scale):
     full = ~empty
     if not full.any():
         return
-    tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2 * e[..., None]) * weighted + 2.0 ** -14 * floor
+    tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2 * e[..., None]) * weighted + 2.0 ** -13.75 * floor
     worst = (np.abs(got - ref) / np.maximum(tol, 1e-300))[full].max()
     ltol = e + 2.0 ** -20 + 2.0 ** -22 * np.abs(np.where(full, rl, 0.0))
     lworst = (np.abs(gl - np.where(full, rl, 0.0)) / ltol)[full].max()
