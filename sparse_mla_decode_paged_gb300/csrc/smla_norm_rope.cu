@@ -33,24 +33,13 @@ __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2hal
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// N consecutive elements as floats: 16-byte accesses (N * sizeof(T) a multiple of 16, p aligned), or
-// element by element.
-template <int N, typename T>
-__device__ __forceinline__ void load_vec(const T* p, float (&v)[N]) {
-  constexpr int kPer = 16 / sizeof(T);
-#pragma unroll
-  for (int i = 0; i < N / kPer; ++i) {
-    const uint4 raw = *reinterpret_cast<const uint4*>(p + i * kPer);
-    const T* e = reinterpret_cast<const T*>(&raw);
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) v[i * kPer + j] = to_f32<T>(e[j]);
-  }
-}
+// N consecutive elements as floats.
 template <int N, typename T>
 __device__ __forceinline__ void load_each(const T* p, float (&v)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = to_f32<T>(p[i]);
 }
+// And back, rounded, in 16-byte stores.
 template <int N, typename T>
 __device__ __forceinline__ void store_vec(T* p, const float (&v)[N]) {
   constexpr int kPer = 16 / sizeof(T);
@@ -64,119 +53,159 @@ __device__ __forceinline__ void store_vec(T* p, const float (&v)[N]) {
   }
 }
 
-// N weights at `at` (fp32, or the type of x).
-template <int N, typename T>
-__device__ __forceinline__ void load_weight(const void* w, int at, int weight_dtype, float (&v)[N]) {
-  if (weight_dtype == SMLA_FP32)
-    load_each<N, float>(static_cast<const float*>(w) + at, v);
-  else
-    load_each<N, T>(static_cast<const T*>(w) + at, v);
-}
-
 // ---------------------------------------------------------------------------- norm + rotation + append
 
-constexpr int kNormAppendWarps = 4;
-constexpr int kNormAppendBlocksPerSm = 16;
-
-// One token of a warp, as loaded: latent dims 8 l .. 8 l + 7 and 256 + 8 l .. (blocks l / 16 and 2 + l / 16, so a
-// block's amax is a reduction over 16 lanes, and every access of the warp is contiguous), rope dims 2 l, 2 l + 1, and
-// the block-table entry.
-struct AppendToken {
-  float x[16], r0, r1;
-  int pos, page;
-};
-
+// 8 weights at `at` (fp32, or the type of x), which stay in L1.
 template <typename T, bool kWide>
-__device__ __forceinline__ AppendToken append_load(const NormAppendParams& p, int tok, int lane) {
-  AppendToken a;
-  const T* row = static_cast<const T*>(p.latent) + (int64_t)tok * p.latent_stride + 8 * lane;
-  float (&lo)[8] = reinterpret_cast<float (&)[8]>(a.x[0]);
-  float (&hi)[8] = reinterpret_cast<float (&)[8]>(a.x[8]);
-  if constexpr (kWide) {
-    load_vec<8, T>(row, lo);
-    load_vec<8, T>(row + 256, hi);
-  } else {
-    load_each<8, T>(row, lo);
-    load_each<8, T>(row + 256, hi);
+__device__ __forceinline__ void load_weights(const void* w, int at, int weight_dtype, float (&v)[8]) {
+  if (weight_dtype == SMLA_FP32) {
+    const float* p = static_cast<const float*>(w) + at;
+    if constexpr (kWide) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+      const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = f[i];
+    } else {
+      load_each<8, float>(p, v);
+    }
+  } else if constexpr (sizeof(T) == 2) {
+    const T* p = static_cast<const T*>(w) + at;
+    if constexpr (kWide) {
+      const uint4 raw = __ldg(reinterpret_cast<const uint4*>(p));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = to_f32<T>(reinterpret_cast<const T*>(&raw)[i]);
+    } else {
+      load_each<8, T>(p, v);
+    }
   }
-  const T* rr = static_cast<const T*>(p.rope) + (int64_t)tok * p.rope_stride + 2 * lane;
-  a.r0 = to_f32<T>(rr[0]);
-  a.r1 = to_f32<T>(rr[1]);
-  const int req = p.requests ? __ldg(p.requests + tok) : tok;
-  a.pos = __ldg(p.positions + tok);
-  a.page = -1;
-  if (req >= 0 && req < p.num_requests && a.pos >= 0 && (a.pos >> 6) < p.max_pages && a.pos < p.max_positions)
-    a.page = __ldg(p.block_table + (size_t)req * p.max_pages + (a.pos >> 6));
-  return a;
 }
 
-// One warp per token, the weights in registers over the warp's tokens.  What bounds it: HBM bytes (1152 read, 256 of
-// cos and sin mostly from L2, 656 written per token of a 16-bit type).  Codes are n times the scale's reciprocal (one
-// reciprocal per block; sixteen divisions per lane took half the kernel's issue slots).
+constexpr int kNormAppendWarps = 4;
+constexpr int kNormAppendBlocksPerSm = 6;   // resident at once (80 registers; 5: 27.7 us, 7: 26.6)
+
+// Half a warp per token (two tokens per warp).  Lane l of a half takes
+// dims 8 l .. 8 l + 7 of each 128-dim block, so every access of the warp is contiguous and a block's amax is a
+// reduction over the 16 lanes; the four reductions share their exchanges (each lane ends with one block's amax and
+// forms that block's scale and reciprocal).  What bounds it: HBM bytes (1152 read, 256 of cos and sin mostly from L2, 656
+// written per token of a 16-bit type) and, behind them, issue.  Measured, 65521 bf16 tokens: 26.5 us (4.5 TB/s of these
+// bytes without the table); a warp per token, which repeats the addresses, divisions and reductions, 30.4 us; with the
+// next token's loads in flight as well (half the warps) 34 us.
 template <typename T, bool kWide>
-__global__ void __launch_bounds__(32 * kNormAppendWarps) kv_norm_append_kernel(const NormAppendParams p) {
-  const int lane = threadIdx.x & 31;
-  const int warps = gridDim.x * kNormAppendWarps;
-  float w[16];
-  load_weight<8, T>(p.weight, 8 * lane, p.weight_dtype, reinterpret_cast<float (&)[8]>(w[0]));
-  load_weight<8, T>(p.weight, 256 + 8 * lane, p.weight_dtype, reinterpret_cast<float (&)[8]>(w[8]));
-  for (int64_t tok = blockIdx.x * kNormAppendWarps + (threadIdx.x >> 5); tok < p.tokens; tok += warps) {
-    AppendToken a = append_load<T, kWide>(p, (int)tok, lane);
-    if (a.page < 0 || (int64_t)a.page >= p.num_pages) {
-      if (lane == 0 && p.err) atomicOr(p.err, SMLA_DEVERR_PAGE_RANGE);
-      continue;                                      // warp-uniform
+__global__ void __launch_bounds__(32 * kNormAppendWarps, kNormAppendBlocksPerSm)
+    kv_norm_append_kernel(const NormAppendParams p) {
+  constexpr int kPer = 16 / sizeof(T);
+  const int lane = threadIdx.x & 31, l = lane & 15, half = lane >> 4;
+  const int64_t step = 2 * (int64_t)gridDim.x * kNormAppendWarps;
+  for (int64_t t0 = 2 * ((int64_t)blockIdx.x * kNormAppendWarps + (threadIdx.x >> 5)); t0 < p.tokens; t0 += step) {
+    const int64_t tok = t0 + half;
+    const bool in = tok < p.tokens;
+    alignas(16) T x[32], r[4];
+    int pos = -1, page = -1;
+    if (in) {
+      const int req = p.requests ? __ldg(p.requests + tok) : (int)tok;
+      pos = __ldg(p.positions + tok);
+      const T* row = static_cast<const T*>(p.latent) + tok * p.latent_stride + 8 * l;
+      const T* rr = static_cast<const T*>(p.rope) + tok * p.rope_stride + 4 * l;
+      if constexpr (kWide) {
+#pragma unroll
+        for (int i = 0; i < 32; i += kPer)
+          *reinterpret_cast<uint4*>(x + i) = *reinterpret_cast<const uint4*>(row + 128 * (i / 8) + i % 8);
+        if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4*>(r) = *reinterpret_cast<const uint4*>(rr);
+        else *reinterpret_cast<uint2*>(r) = *reinterpret_cast<const uint2*>(rr);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = row[128 * (i / 8) + i % 8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = rr[i];
+      }
+      if (req >= 0 && req < p.num_requests && pos >= 0 && (pos >> 6) < p.max_pages && pos < p.max_positions)
+        page = __ldg(p.block_table + (size_t)req * p.max_pages + (pos >> 6));
+      if (page < 0 || (int64_t)page >= p.num_pages) {
+        if (l == 0 && p.err) atomicOr(p.err, SMLA_DEVERR_PAGE_RANGE);
+        page = -1;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = from_f32<T>(0.f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[i] = from_f32<T>(0.f);
     }
-    unsigned char* rec = p.kv + ((int64_t)a.page * kPageSize + (a.pos & (kPageSize - 1))) * kRecordBytes;
-    const float* cs = p.cos_sin + (size_t)a.pos * kDRope;
+    const bool write = page >= 0;
+    unsigned char* rec = p.kv + (write ? ((int64_t)page * kPageSize + (pos & (kPageSize - 1))) * kRecordBytes : 0);
+    const float* cs = p.cos_sin + (write ? (size_t)pos * kDRope : 0);
 
     float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) ss = fmaf(a.x[i], a.x[i], ss);
+    for (int i = 0; i < 32; ++i) ss = fmaf(to_f32<T>(x[i]), to_f32<T>(x[i]), ss);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    for (int o = 8; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     const float inv = rsqrtf(ss * (1.f / kDLatent) + p.eps);
+    float n[32], amax[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float* x = a.x + 8 * h;
-      float amax = 0.f;
+    for (int b = 0; b < 4; ++b) {
+      float f[8];
+      load_weights<T, kWide>(p.weight, 128 * b + 8 * l, p.weight_dtype, f);
+      amax[b] = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        x[i] = x[i] * inv * w[8 * h + i];
-        amax = fmaxf(amax, fabsf(x[i]));
+        n[8 * b + i] = to_f32<T>(x[8 * b + i]) * inv * f[i];
+        amax[b] = fmaxf(amax[b], fabsf(n[8 * b + i]));
       }
+    }
+    // lane l ends with block 2 (l / 8) + (l / 4) % 2
+    const bool hi8 = l & 8, hi4 = l & 4;
+    float m0 = fmaxf(hi8 ? amax[2] : amax[0], __shfl_xor_sync(0xffffffffu, hi8 ? amax[0] : amax[2], 8));
+    float m1 = fmaxf(hi8 ? amax[3] : amax[1], __shfl_xor_sync(0xffffffffu, hi8 ? amax[1] : amax[3], 8));
+    float m = fmaxf(hi4 ? m1 : m0, __shfl_xor_sync(0xffffffffu, hi4 ? m0 : m1, 4));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    float scale = m > 0.f ? __fdiv_rn(m, 448.f) : 1.f;
+    if (scale == 0.f) scale = 1.f;                   // amax below the smallest float's 224 fold: codes of 0
+    const bool tiny = scale < 0x1p-100f;             // its reciprocal may not be a float: both sides times 2^64
+    const float up = __frcp_rn(tiny ? scale * 0x1p64f : scale);
+    const bool any_tiny = __any_sync(0xffffffffu, tiny);
+    if (write && (l & 3) == 0) reinterpret_cast<float*>(rec + kDLatent)[l >> 2] = scale;
 #pragma unroll
-      for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      float scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
-      if (scale == 0.f) scale = 1.f;                 // amax below the smallest float's 224 fold: codes of 0
-      const bool tiny = scale < 0x1p-100f;           // its reciprocal may not be a float: both sides times 2^64
-      const float up = __frcp_rn(tiny ? scale * 0x1p64f : scale);
-      if (__builtin_expect(tiny, 0)) {
+    for (int b = 0; b < 4; ++b) {
+      const int from = 16 * half + 4 * b;
+      const float u = __shfl_sync(0xffffffffu, up, from);
+      float* v = n + 8 * b;
+      if (__builtin_expect(any_tiny, 0)) {
+        const float lift = __shfl_sync(0xffffffffu, tiny ? 0x1p64f : 1.f, from);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= 0x1p64f;
+        for (int i = 0; i < 8; ++i) v[i] *= lift;
       }
       uint32_t c[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        c[i] = (uint32_t)f32x2_to_e4m3x2(x[4 * i] * up, x[4 * i + 1] * up) |
-               ((uint32_t)f32x2_to_e4m3x2(x[4 * i + 2] * up, x[4 * i + 3] * up) << 16);
-      reinterpret_cast<uint2*>(rec)[32 * h + lane] = make_uint2(c[0], c[1]);
-      if ((lane & 15) == 0) reinterpret_cast<float*>(rec + kDLatent)[2 * h + (lane >> 4)] = scale;
+        c[i] = (uint32_t)f32x2_to_e4m3x2(v[4 * i] * u, v[4 * i + 1] * u) |
+               ((uint32_t)f32x2_to_e4m3x2(v[4 * i + 2] * u, v[4 * i + 3] * u) << 16);
+      if (write) reinterpret_cast<uint2*>(rec)[16 * b + l] = make_uint2(c[0], c[1]);
     }
 
-    float y0, y1;
-    if (p.interleaved) {                             // this lane's two dims are pair `lane`
-      const float co = __ldg(cs + lane), si = __ldg(cs + 32 + lane);
-      y0 = a.r0 * co - a.r1 * si;
-      y1 = a.r0 * si + a.r1 * co;
-    } else {                                         // partners of dims 2 l, 2 l + 1 sit 16 lanes away
-      const float q0 = __shfl_xor_sync(0xffffffffu, a.r0, 16), q1 = __shfl_xor_sync(0xffffffffu, a.r1, 16);
-      const int j = (2 * lane) & 31;
-      const float2 co = __ldg(reinterpret_cast<const float2*>(cs + j));
-      const float2 si = __ldg(reinterpret_cast<const float2*>(cs + 32 + j));
-      y0 = lane < 16 ? a.r0 * co.x - q0 * si.x : q0 * si.x + a.r0 * co.x;
-      y1 = lane < 16 ? a.r1 * co.y - q1 * si.y : q1 * si.y + a.r1 * co.y;
+    // rope dims 4 l .. 4 l + 3
+    float v[4], y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = to_f32<T>(r[i]);
+    if (p.interleaved) {                             // pairs 2 l and 2 l + 1
+      const float2 co = __ldg(reinterpret_cast<const float2*>(cs) + l);
+      const float2 si = __ldg(reinterpret_cast<const float2*>(cs + 32) + l);
+      y[0] = v[0] * co.x - v[1] * si.x;
+      y[1] = v[0] * si.x + v[1] * co.x;
+      y[2] = v[2] * co.y - v[3] * si.y;
+      y[3] = v[2] * si.y + v[3] * co.y;
+    } else {                                         // partners 32 dims, or 8 lanes, away
+      const float4 co = __ldg(reinterpret_cast<const float4*>(cs) + (l & 7));
+      const float4 si = __ldg(reinterpret_cast<const float4*>(cs + 32) + (l & 7));
+      const float c4[4] = {co.x, co.y, co.z, co.w}, s4[4] = {si.x, si.y, si.z, si.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float q = __shfl_xor_sync(0xffffffffu, v[i], 8);
+        y[i] = l < 8 ? v[i] * c4[i] - q * s4[i] : q * s4[i] + v[i] * c4[i];
+      }
     }
-    reinterpret_cast<uint32_t*>(rec + kDLatent + 16)[lane] = f32x2_to_bf16x2(y0, y1);
+    if (write)
+      reinterpret_cast<uint2*>(rec + kDLatent + 16)[l] = make_uint2(f32x2_to_bf16x2(y[0], y[1]), f32x2_to_bf16x2(y[2], y[3]));
   }
 }
 
@@ -419,8 +448,10 @@ bool launch_norm_rope_wide(const NormRopeParams& p, cudaStream_t stream) {
 cudaError_t launch_kv_norm_append(const NormAppendParams& p, cudaStream_t stream) {
   if (p.tokens == 0) return cudaSuccess;
   const int esz = p.dtype == SMLA_FP32 ? 4 : 2;
-  const bool wide = reinterpret_cast<uintptr_t>(p.latent) % 16 == 0 && (p.latent_stride * esz) % 16 == 0;
-  const int want = (int)(((int64_t)p.tokens + kNormAppendWarps - 1) / kNormAppendWarps);
+  const bool wide = reinterpret_cast<uintptr_t>(p.latent) % 16 == 0 && (p.latent_stride * esz) % 16 == 0 &&
+                    reinterpret_cast<uintptr_t>(p.rope) % (4 * esz) == 0 && p.rope_stride % 4 == 0 &&
+                    reinterpret_cast<uintptr_t>(p.weight) % 16 == 0;
+  const int want = (int)(((int64_t)p.tokens + 2 * kNormAppendWarps - 1) / (2 * kNormAppendWarps));
   const int blocks = want < p.sms * kNormAppendBlocksPerSm ? want : p.sms * kNormAppendBlocksPerSm;
   auto go = [&](auto kernel) { kernel<<<blocks, 32 * kNormAppendWarps, 0, stream>>>(p); };
   if (p.dtype == SMLA_BF16)
