@@ -266,8 +266,8 @@ typedef struct smla_norm_append_dims {
  * one pass.  For token i at position t = positions[i] of request r:
  *   n_d    = latent_d / sqrt(mean_d latent_d^2 + eps) * norm_weight_d     (fp32)
  *   scale_j = fp32(amax_j / 448) of n as in sparse_mla_kv_append,
- *   code_d  = E4M3(n_d * fp32(1 / scale_{d / 128})), round to nearest even,
- *            saturating (n is not rounded to 16 bits before it is quantised);
+ *   code_d  = E4M3(n_d / scale_{d / 128}), round to nearest even, saturating
+ *            (n is not rounded to 16 bits before it is quantised);
  *   rope   = bf16 of the pairs (a, b) rotated to (a c - b s, a s + b c) with
  *            c = cos_sin[t][j], s = cos_sin[t][32 + j] for pair j (fp32).
  *   latent  dtype [tokens][512], rope dtype [tokens][64]: unit stride in a

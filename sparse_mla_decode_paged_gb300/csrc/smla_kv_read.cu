@@ -1,5 +1,6 @@
 // Reading records of the paged FP8 cache back: out[i] = [e4m3(code) * scale | rope].
-// Bound by HBM bytes (656 read, 576 elements written per token).
+// Bound by HBM bytes (656 read, 576 elements written per token).  Measured, 131071 records to bf16: 38.3 us (6.2 TB/s);
+// 16 dims of one block per lane, whose accesses leave gaps, took 44 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

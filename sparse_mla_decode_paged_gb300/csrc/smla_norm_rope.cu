@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(32 * kNormAppendWarps, kNormAppendBlocksPerSm)
     for (int i = 0; i < 32; ++i) ss = fmaf(to_f32<T>(x[i]), to_f32<T>(x[i]), ss);
 #pragma unroll
     for (int o = 8; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float inv = rsqrtf(ss * (1.f / kDLatent) + p.eps);
+    const float inv = __frsqrt_rn(ss * (1.f / kDLatent) + p.eps);
     float n[32], amax[4];
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
@@ -162,24 +162,32 @@ __global__ void __launch_bounds__(32 * kNormAppendWarps, kNormAppendBlocksPerSm)
     float scale = m > 0.f ? __fdiv_rn(m, 448.f) : 1.f;
     if (scale == 0.f) scale = 1.f;                   // amax below the smallest float's 224 fold: codes of 0
     const bool tiny = scale < 0x1p-100f;             // its reciprocal may not be a float: both sides times 2^64
-    const float up = __frcp_rn(tiny ? scale * 0x1p64f : scale);
+    const float div = tiny ? scale * 0x1p64f : scale;
+    const float up = __frcp_rn(div);
     const bool any_tiny = __any_sync(0xffffffffu, tiny);
     if (write && (l & 3) == 0) reinterpret_cast<float*>(rec + kDLatent)[l >> 2] = scale;
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       const int from = 16 * half + 4 * b;
-      const float u = __shfl_sync(0xffffffffu, up, from);
+      const float u = __shfl_sync(0xffffffffu, up, from), d = -__shfl_sync(0xffffffffu, div, from);
       float* v = n + 8 * b;
       if (__builtin_expect(any_tiny, 0)) {
         const float lift = __shfl_sync(0xffffffffu, tiny ? 0x1p64f : 1.f, from);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= lift;
       }
+      // n / scale: the product with the reciprocal, corrected once by its remainder (Markstein's division step), so that
+      // the codes are those of the quotient rounded to fp32
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float q = v[i] * u;
+        v[i] = fmaf(fmaf(q, d, v[i]), u, q);
+      }
       uint32_t c[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        c[i] = (uint32_t)f32x2_to_e4m3x2(v[4 * i] * u, v[4 * i + 1] * u) |
-               ((uint32_t)f32x2_to_e4m3x2(v[4 * i + 2] * u, v[4 * i + 3] * u) << 16);
+        c[i] = (uint32_t)f32x2_to_e4m3x2(v[4 * i], v[4 * i + 1]) |
+               ((uint32_t)f32x2_to_e4m3x2(v[4 * i + 2], v[4 * i + 3]) << 16);
       if (write) reinterpret_cast<uint2*>(rec)[16 * b + l] = make_uint2(c[0], c[1]);
     }
 
