@@ -257,6 +257,27 @@ class _on:
             self.ctx.__exit__(*a)
 
 
+# Dims of calls whose arguments have been checked, by the shapes, strides, types and devices of the tensors and the
+# values that the checks look at (the library reads dims, never writes them).
+_CHECKED = {}
+
+
+def _call_key(tensors, *values):
+    """None when one of the tensors is something else: the checks name it."""
+    try:
+        return (tuple([t if t is None else (t.shape, t.stride(), t.dtype, t.device) for t in tensors]), values)
+    except (AttributeError, TypeError):
+        return None
+
+
+def _remember(key, checked):
+    if key is not None:
+        if len(_CHECKED) > 256:
+            _CHECKED.clear()
+        _CHECKED[key] = checked
+    return checked
+
+
 def rope_table(max_positions: int, rope_dim: int = D_ROPE, base: float = 10000.0, device=None) -> torch.Tensor:
     """float32 [max_positions, rope_dim]: cos of the rotation angles of each position in the first half of a row,
     sin in the second (angle of pair j at position t: t * base ** (-2 j / rope_dim), formed in 64 bits)."""
@@ -302,6 +323,20 @@ def sparse_mla_kv_norm_append(latent: torch.Tensor, rope: torch.Tensor, norm_wei
 
     latent and rope: bf16, fp16 or fp32, rows may be strided (slices of one projection output); norm_weight of
     their type or fp32; cos_sin fp32 [positions,64] (rope_table)."""
+    key = _call_key((latent, rope, norm_weight, cos_sin, block_table, positions, kv_cache, requests, err_word),
+                    "kv_norm_append", bool(interleaved))
+    dims = _CHECKED.get(key) or _remember(key, _norm_append_dims(latent, rope, norm_weight, cos_sin, block_table,
+                                                                 positions, kv_cache, requests, interleaved, err_word))
+    with _on(kv_cache.device, stream) as st:
+        r = _lib().sparse_mla_kv_norm_append(
+            dims, latent.data_ptr(), rope.data_ptr(), norm_weight.data_ptr(), eps, cos_sin.data_ptr(),
+            block_table.data_ptr(), _ptr(requests), positions.data_ptr(), kv_cache.data_ptr(), _ptr(err_word), st)
+    if r != 0:
+        check("sparse_mla_kv_norm_append", r)
+
+
+def _norm_append_dims(latent, rope, norm_weight, cos_sin, block_table, positions, kv_cache, requests, interleaved,
+                      err_word) -> SmlaNormAppendDims:
     _need_rows(latent, "latent", D_LATENT)
     _need_rows(rope, "rope", D_ROPE)
     T = latent.shape[0]
@@ -316,30 +351,28 @@ def sparse_mla_kv_norm_append(latent: torch.Tensor, rope: torch.Tensor, norm_wei
     _need_paged(kv_cache, block_table, positions, requests, T)
     dev = kv_cache.device
     _same_device(dev, latent=latent, rope=rope, norm_weight=norm_weight, cos_sin=cos_sin)
-    dims = SmlaNormAppendDims(T, block_table.shape[0], PAGE_SIZE, block_table.shape[1], D_LATENT, D_ROPE,
+    _err_word(err_word, dev)
+    return SmlaNormAppendDims(T, block_table.shape[0], PAGE_SIZE, block_table.shape[1], D_LATENT, D_ROPE,
                               kv_cache.shape[0], latent.stride(0) if T > 1 else D_LATENT,
                               rope.stride(0) if T > 1 else D_ROPE, _DTYPE[latent.dtype], _DTYPE[norm_weight.dtype],
                               cos_sin.shape[0], 1 if interleaved else 0)
-    err = _err_word(err_word, dev)
-    with _on(dev, stream) as st:
-        check("sparse_mla_kv_norm_append", _lib().sparse_mla_kv_norm_append(
-            C.byref(dims), _ptr(latent), _ptr(rope), _ptr(norm_weight), eps, _ptr(cos_sin), _ptr(block_table),
-            _ptr(requests), _ptr(positions), _ptr(kv_cache), err, st))
 
 
-def _apart(x: torch.Tensor, out: torch.Tensor) -> bool:
-    """Whether out may be written while x is read: x itself, memory of its own, or other columns of x's rows."""
-    if x.data_ptr() == out.data_ptr() and x.stride() == out.stride():
+def _apart(x: torch.Tensor, out: torch.Tensor, x_bytes: int, out_bytes: int) -> bool:
+    """Whether out may be written while x is read: x itself, memory of its own, or other columns of x's rows.  (x_bytes,
+    out_bytes: from their first element to their last.)"""
+    a, b = x.data_ptr(), out.data_ptr()
+    if a + x_bytes <= b or b + out_bytes <= a or (a == b and x.stride() == out.stride()) or x.numel() == 0:
         return True
     size = x.element_size()
-    span = [(t.data_ptr(), t.data_ptr() + size * (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))))
-            for t in (x, out)]
-    if x.numel() == 0 or span[0][1] <= span[1][0] or span[1][1] <= span[0][0]:
-        return True
     if x.stride() != out.stride() or min(x.stride()[:2]) < 1 or max(x.stride()[:2]) % min(x.stride()[:2]) != 0:
         return False
-    step, d = min(x.stride()[:2]), (out.data_ptr() - x.data_ptr()) % (size * min(x.stride()[:2]))
+    step, d = min(x.stride()[:2]), (b - a) % (size * min(x.stride()[:2]))
     return size * x.shape[2] <= d <= size * (step - x.shape[2])
+
+
+def _span_bytes(t: torch.Tensor) -> int:
+    return t.element_size() * (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))
 
 
 def sparse_mla_norm_rope(x: torch.Tensor, positions: Optional[torch.Tensor] = None,
@@ -350,6 +383,24 @@ def sparse_mla_norm_rope(x: torch.Tensor, positions: Optional[torch.Tensor] = No
     """x [T,H,D] (bf16, fp16 or fp32, unit stride along D): RMS norm of each head's vector (norm, with an optional
     weight [D] of x's type or fp32), then rotation of the dims [rope_offset, rope_offset + cos_sin.shape[1]) at
     positions [T] (cos_sin fp32, rope_table; None: no rotation).  out: as x, or x itself."""
+    key = _call_key((x, positions, cos_sin, weight, out, err_word), "norm_rope", bool(norm), rope_offset, bool(interleaved))
+    dims, x_bytes, out_bytes = _CHECKED.get(key) or _remember(
+        key, _norm_rope_dims(x, positions, cos_sin, weight, norm, rope_offset, interleaved, out, err_word))
+    with _on(x.device, stream) as st:
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        elif not _apart(x, out, x_bytes, out_bytes):
+            raise ValueError("out must be x itself or not overlap it")
+        r = _lib().sparse_mla_norm_rope(
+            dims, x.data_ptr(), _ptr(weight), eps, _ptr(cos_sin), positions.data_ptr() if dims.rope_dim else None,
+            out.data_ptr(), _ptr(err_word), st)
+    if r != 0:
+        check("sparse_mla_norm_rope", r)
+    return out
+
+
+def _norm_rope_dims(x, positions, cos_sin, weight, norm, rope_offset, interleaved, out, err_word):
+    """Checked dims, and the bytes that x and out span."""
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
     if not x.is_cuda or x.dtype not in _DTYPE:
@@ -357,7 +408,6 @@ def sparse_mla_norm_rope(x: torch.Tensor, positions: Optional[torch.Tensor] = No
     if x.dim() != 3 or x.shape[1] < 1 or x.shape[2] < 1 or (x.shape[2] > 1 and x.stride(2) != 1):
         raise ValueError("x must be [T,H,D] with unit stride along D")
     T, H, D = x.shape
-    dev = x.device
     if weight is not None:
         if not norm:
             raise ValueError("weight without norm")
@@ -373,23 +423,15 @@ def sparse_mla_norm_rope(x: torch.Tensor, positions: Optional[torch.Tensor] = No
         if positions.shape[0] != T:
             raise ValueError("positions must be [T]")
         max_pos, rope_dim = cos_sin.shape
-    _same_device(dev, weight=weight, cos_sin=cos_sin, positions=positions, out=out)
-    err = _err_word(err_word, dev)
-    with _on(dev, stream) as st:
-        if out is None:
-            out = torch.empty((T, H, D), dtype=x.dtype, device=dev)
-        elif out.shape != x.shape or out.dtype != x.dtype or (D > 1 and out.stride(2) != 1):
-            raise ValueError("out must have x's shape and type and unit stride along D")
-        elif not _apart(x, out):
-            raise ValueError("out must be x itself or not overlap it")
-        dims = SmlaNormRopeDims(T, H, D, rope_dim, rope_offset, _DTYPE[x.dtype],
-                                _DTYPE[weight.dtype if weight is not None else x.dtype], 1 if norm else 0,
-                                1 if interleaved else 0, max_pos, x.stride(0), x.stride(1), out.stride(0),
-                                out.stride(1))
-        check("sparse_mla_norm_rope", _lib().sparse_mla_norm_rope(
-            C.byref(dims), _ptr(x), _ptr(weight), eps, _ptr(cos_sin), _ptr(positions) if rope_dim else None,
-            _ptr(out), err, st))
-    return out
+    _same_device(x.device, weight=weight, cos_sin=cos_sin, positions=positions, out=out)
+    _err_word(err_word, x.device)
+    if out is not None and (out.shape != x.shape or out.dtype != x.dtype or (D > 1 and out.stride(2) != 1)):
+        raise ValueError("out must have x's shape and type and unit stride along D")
+    o_strides = (H * D, D) if out is None else out.stride()
+    dims = SmlaNormRopeDims(T, H, D, rope_dim, rope_offset, _DTYPE[x.dtype],
+                            _DTYPE[weight.dtype if weight is not None else x.dtype], 1 if norm else 0,
+                            1 if interleaved else 0, max_pos, x.stride(0), x.stride(1), o_strides[0], o_strides[1])
+    return dims, _span_bytes(x), 0 if out is None else _span_bytes(out)
 
 
 def sparse_mla_kv_read(kv_cache: torch.Tensor, block_table: torch.Tensor, positions: torch.Tensor,
@@ -398,6 +440,21 @@ def sparse_mla_kv_read(kv_cache: torch.Tensor, block_table: torch.Tensor, positi
                        stream=None) -> torch.Tensor:
     """[T,576]: the records at (requests[i] or i, positions[i]) as [latent * scale | rope] rows of dtype (out's type
     when out is given); zeros for a token out of range."""
+    key = _call_key((kv_cache, block_table, positions, requests, out, err_word), "kv_read", dtype)
+    dims, dtype = _CHECKED.get(key) or _remember(key, _read_dims(kv_cache, block_table, positions, requests, out, dtype,
+                                                                 err_word))
+    with _on(kv_cache.device, stream) as st:
+        if out is None:
+            out = torch.empty((positions.shape[0], D_QK), dtype=dtype, device=kv_cache.device)
+        r = _lib().sparse_mla_kv_read(dims, kv_cache.data_ptr(), block_table.data_ptr(), _ptr(requests),
+                                      positions.data_ptr(), out.data_ptr(), _DTYPE[dtype], _ptr(err_word), st)
+    if r != 0:
+        check("sparse_mla_kv_read", r)
+    return out
+
+
+def _read_dims(kv_cache, block_table, positions, requests, out, dtype, err_word):
+    """Checked dims and the output's type."""
     T = positions.shape[0] if isinstance(positions, torch.Tensor) and positions.dim() == 1 else -1
     _need_paged(kv_cache, block_table, positions, requests, T)
     dev = kv_cache.device
@@ -408,16 +465,9 @@ def sparse_mla_kv_read(kv_cache: torch.Tensor, block_table: torch.Tensor, positi
             raise ValueError(f"out must be [T,576] on {dev}")
     if dtype not in _DTYPE:
         raise TypeError("out must be bfloat16, float16 or float32")
-    err = _err_word(err_word, dev)
-    dims = SmlaAppendDims(T, block_table.shape[0], PAGE_SIZE, block_table.shape[1], D_LATENT, D_ROPE,
-                          kv_cache.shape[0])
-    with _on(dev, stream) as st:
-        if out is None:
-            out = torch.empty((T, D_QK), dtype=dtype, device=dev)
-        check("sparse_mla_kv_read", _lib().sparse_mla_kv_read(
-            C.byref(dims), _ptr(kv_cache), _ptr(block_table), _ptr(requests), _ptr(positions), _ptr(out),
-            _DTYPE[dtype], err, st))
-    return out
+    _err_word(err_word, dev)
+    return SmlaAppendDims(T, block_table.shape[0], PAGE_SIZE, block_table.shape[1], D_LATENT, D_ROPE,
+                          kv_cache.shape[0]), dtype
 
 
 def make_dense_dims(B: int, H: int, max_pages_per_seq: int, num_pages: int, queries_per_request: int = 1,

@@ -87,8 +87,8 @@ constexpr int kNormAppendBlocksPerSm = 6;   // resident at once (80 registers; 5
 // dims 8 l .. 8 l + 7 of each 128-dim block, so every access of the warp is contiguous and a block's amax is a
 // reduction over the 16 lanes; the four reductions share their exchanges (each lane ends with one block's amax and
 // forms that block's scale and reciprocal).  What bounds it: HBM bytes (1152 read, 256 of cos and sin mostly from L2, 656
-// written per token of a 16-bit type) and, behind them, issue.  Measured, 65521 bf16 tokens: 26.5 us (4.5 TB/s of these
-// bytes without the table); a warp per token, which repeats the addresses, divisions and reductions, 30.4 us; with the
+// written per token of a 16-bit type) and, behind them, issue.  Measured, 65521 bf16 tokens: 27.5 us (4.3 TB/s of these
+// bytes without the table); a warp per token, which repeats the addresses, divisions and reductions, 31 us; with the
 // next token's loads in flight as well (half the warps) 34 us.
 template <typename T, bool kWide>
 __global__ void __launch_bounds__(32 * kNormAppendWarps, kNormAppendBlocksPerSm)
