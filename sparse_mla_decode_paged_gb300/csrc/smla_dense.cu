@@ -845,7 +845,8 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
     }
     swap_red();
     const uint32_t moved = __ballot_sync(0xffffffffu, f != 1.f);
-    if (moved) {                                        // (the ballot orders the factors' stores before the loads)
+    if (moved) {
+      __syncwarp();                                     // the factors are written
 #pragma unroll
       for (int i = 0; i < HC / 2; i += 2) {
         const ulonglong2 c = ptx::lds128_pairs(row_f + i * 8);
