@@ -33,14 +33,15 @@
 // an SM.  Of the 6700 cycles that a tile of 64 rows takes (3.2 us; an SM's share of the HBM rate is a tile per 1.9 us)
 // shared memory feeds the tensor core for 3300 (M = 128 positions or dims, N = 64: 6 KB of operands per MMA of 32 dims or
 // positions) and takes in and gives out another 100 KB; the rest is the latency from scores to weights to the PV, whose
-// K slots come free one by one for the next tile's blocks.  Measured, 32 requests x 32768 positions: 64 heads 224 us
-// (3.1 TB/s), 32 heads 140 us (4.9 TB/s), 16 heads 122 us (5.7 TB/s); 1 x 8192 positions of 64 heads 18.5 us, 1 x 77 of
-// 16 heads 11 us.
+// K slots come free one by one for the next tile's blocks.  Measured, 32 requests x 32768 positions: 64 heads 226 us
+// (3.0 TB/s), 32 heads 138 us (5.0 TB/s), 16 heads 122 us (5.6 TB/s); 1 x 8192 positions of 64 heads 17.9 us, 1 x 77 of
+// 16 heads 10.3 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
 #include <atomic>
+#include <cstddef>
 
 #include "smla_device.cuh"
 #include "smla_internal.h"
@@ -108,6 +109,9 @@ struct DC {
   static_assert(kTmemCols == 512 || kTmemCols == 256, "TMEM allocations are powers of two");
 };
 
+// Limits below this are meant to run out: nothing is issued and the call reports a timeout.
+constexpr uint64_t kLeastWaitNs = 1000;
+
 struct Bars {
   uint64_t kfull[9], kempty[9], rfull[2], rempty[2], sfull[4], sempty[4], scfull[3], scempty[3];
   uint64_t pfull[4], pempty[4], qfull, drain[2];
@@ -120,6 +124,27 @@ struct Bars {
   long long total, last_begin, last_end;  // tiles of the batch, global tile range of the last item
 };
 static_assert(sizeof(Bars) <= 640, "barrier area");
+
+// The barriers, one per lane: those that the softmax warps arrive on count these warps.
+template <int kSoftWarps>
+__device__ __forceinline__ void init_bars(Bars* bars, const DenseParams& p, int lane, const CUtensorMap* map,
+                                          const CUtensorMap* smap) {
+  constexpr int kBars = offsetof(Bars, tmem) / 8;
+  constexpr uint64_t kBySoftmax = (15ull << offsetof(Bars, sempty) / 8) | (7ull << offsetof(Bars, scempty) / 8) |
+                                  (15ull << offsetof(Bars, pfull) / 8) | (1ull << offsetof(Bars, qfull) / 8);
+  static_assert(kBars <= 64, "one bit per barrier");
+  for (int i = lane; i < kBars; i += 32)
+    ptx::mbar_init(reinterpret_cast<uint64_t*>(bars) + i, kBySoftmax >> i & 1 ? kSoftWarps : 1);
+  if (lane < 9) bars->armed_k[lane] = 0;
+  if (lane < 2) bars->armed_r[lane] = 0;
+  if (lane < 3) bars->armed_sc[lane] = 0;
+  if (lane == 0) {
+    bars->abort = p.wait_ns < kLeastWaitNs;
+    ptx::prefetch_tensormap(map);
+    ptx::prefetch_tensormap(smap);
+  }
+  ptx::fence_mbar_init();
+}
 
 // One (request, row group): rows row0 .. row0 + nrows - 1 of the request's s_q H rows.
 struct Rows {
@@ -161,7 +186,10 @@ __device__ __forceinline__ Lens lens_of(const DenseParams& p, const Rows& r) {
 }
 
 // First tile of CTA c's run when T tiles are shared out over n CTAs.
-__device__ __forceinline__ long long run_start(long long T, int n, int c) { return T * c / n; }
+__device__ __forceinline__ long long run_start(long long T, int n, int c) {
+  const unsigned long long x = (unsigned long long)T * c;
+  return x >> 32 ? x / n : (uint32_t)x / (uint32_t)n;
+}
 
 // What the kernel leaves for the merge: the item that begins in a CTA's run and ends in a later one's, if any, and
 // the number of runs that it crosses (0: nothing to join).
@@ -193,9 +221,6 @@ struct Walk {
     }
   }
 };
-
-// Limits below this are meant to run out: nothing is issued and the call reports a timeout.
-constexpr uint64_t kLeastWaitNs = 1000;
 
 // A ring position: slot and the parity of its current use.
 template <int N>
@@ -944,10 +969,64 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
 
 // ----------------------------------------------------------------------------- kernel
 
-// This CTA's run of tiles: every CTA adds up the tiles of all items (a run of items per thread, then a scan of
-// the threads' sums).
+// This CTA's run of tiles: every CTA adds up the tiles of all items.  The tiles [a, e) of T, and in the items i0 .. i1 - 1,
+// whose tiles begin at `at` and number `mine`, those in which the run begins and ends.
+__device__ __forceinline__ void run_bounds(const DenseParams& p, long long T, Bars* bars, bool write, long long& a, long long& e) {
+  const int active = (int)min((long long)p.ctas, T), c = blockIdx.x;      // CTAs with at least one tile
+  a = c < active ? run_start(T, active, c) : T;
+  e = c < active ? run_start(T, active, c + 1) : T;
+  if (write) {
+    bars->total = T;
+    bars->my_tiles = (int)(e - a);
+    bars->active = active;
+  }
+}
+
+__device__ __forceinline__ void find_ends(const DenseParams& p, Bars* bars, int i0, int i1, long long at, long long mine,
+                                          long long a, long long e) {
+  if (a >= e || a >= at + mine || e <= at) return;
+  long long x = at;
+#pragma unroll 1
+  for (int i = i0; i < i1 && x < e; ++i) {
+    const int tiles = lens_of(p, rows_of(p, i)).tiles;
+    if (a >= x && a < x + tiles) {
+      bars->first_item = i;
+      bars->first_tile = (int)(a - x);
+    }
+    if (e - 1 >= x && e - 1 < x + tiles) {
+      bars->last_item = i;
+      bars->last_begin = x;
+      bars->last_end = x + tiles;
+    }
+    x += tiles;
+  }
+}
+
+// Few items: one warp, up to four items per lane (the general search's code and barriers take 0.7 us more of a
+// call: 1 x 77 positions 11.0 us instead of 10.3).
+// Else a run of items per thread, then a scan of the threads' sums.
 template <int kThreads>
 __device__ __forceinline__ void find_run(const DenseParams& p, unsigned char* scratch, Bars* bars) {
+  if (p.requests * p.groups <= 128) {
+    if (threadIdx.x < 32) {
+      const int n = p.requests * p.groups, per = (n + 31) >> 5, lane = threadIdx.x;
+      const int i0 = min(n, lane * per), i1 = min(n, i0 + per);
+      long long mine = 0;
+#pragma unroll 1
+      for (int i = i0; i < i1; ++i) mine += lens_of(p, rows_of(p, i)).tiles;
+      long long upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long up = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += up;
+      }
+      long long a, e;
+      run_bounds(p, __shfl_sync(0xffffffffu, upto, 31), bars, lane == 0, a, e);
+      find_ends(p, bars, i0, i1, upto - mine, mine, a, e);
+    }
+    __syncthreads();
+    return;
+  }
   constexpr int kPer = kThreads / 32;
   long long* sums = reinterpret_cast<long long*>(scratch);
   const int n = p.requests * p.groups, per = (n + kThreads - 1) / kThreads;
@@ -976,44 +1055,9 @@ __device__ __forceinline__ void find_run(const DenseParams& p, unsigned char* sc
     for (int j = 0; j < kPer; ++j) sums[kPer * threadIdx.x + j] = before + v[j];
   }
   __syncthreads();
-  const long long T = bars->total;
-  const int active = (int)min((long long)p.ctas, T);     // CTAs with at least one tile
-  const int c = blockIdx.x;
-  const long long a = c < active ? run_start(T, active, c) : T, e = c < active ? run_start(T, active, c + 1) : T;
-  if (threadIdx.x == 0) {
-    bars->my_tiles = (int)(e - a);
-    bars->active = active;
-  }
-  const long long at = sums[threadIdx.x];
-  if (a < e && mine > 0) {
-    if (a >= at && a < at + mine) {                      // the run begins in this thread's items
-      long long x = at;
-#pragma unroll 1
-      for (int i = i0; i < i1; ++i) {
-        const int tiles = lens_of(p, rows_of(p, i)).tiles;
-        if (a < x + tiles) {
-          bars->first_item = i;
-          bars->first_tile = (int)(a - x);
-          break;
-        }
-        x += tiles;
-      }
-    }
-    if (e - 1 >= at && e - 1 < at + mine) {              // and ends in these
-      long long x = at;
-#pragma unroll 1
-      for (int i = i0; i < i1; ++i) {
-        const int tiles = lens_of(p, rows_of(p, i)).tiles;
-        if (e - 1 < x + tiles) {
-          bars->last_item = i;
-          bars->last_begin = x;
-          bars->last_end = x + tiles;
-          break;
-        }
-        x += tiles;
-      }
-    }
-  }
+  long long a, e;
+  run_bounds(p, bars->total, bars, threadIdx.x == 0, a, e);
+  find_ends(p, bars, i0, i1, sums[threadIdx.x], mine, a, e);
   __syncthreads();
 }
 
@@ -1037,36 +1081,8 @@ __global__ void __launch_bounds__(DC<NR>::kThreads, 1)
   Bars* bars = reinterpret_cast<Bars*>(sm + C::kBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) ptx::griddep_launch_dependents();   // the merge, which waits for this grid's results
-  if (threadIdx.x == 0) {
-    ptx::prefetch_tensormap(&map);
-    ptx::prefetch_tensormap(&smap);
-    for (int i = 0; i < C::kRing; ++i) {
-      ptx::mbar_init(&bars->kfull[i], 1);
-      ptx::mbar_init(&bars->kempty[i], 1);
-      bars->armed_k[i] = 0;
-    }
-    for (int i = 0; i < 4; ++i) {
-      ptx::mbar_init(&bars->sfull[i], 1);
-      ptx::mbar_init(&bars->sempty[i], C::kSoftWarps);
-      ptx::mbar_init(&bars->pfull[i], C::kSoftWarps);
-      ptx::mbar_init(&bars->pempty[i], 1);
-    }
-    for (int i = 0; i < C::kScaleSlots; ++i) {
-      ptx::mbar_init(&bars->scfull[i], 1);
-      ptx::mbar_init(&bars->scempty[i], C::kSoftWarps);
-      bars->armed_sc[i] = 0;
-    }
-    for (int i = 0; i < 2; ++i) ptx::mbar_init(&bars->drain[i], 1);
-    for (int i = 0; i < C::kRopeSlots; ++i) {
-      ptx::mbar_init(&bars->rfull[i], 1);
-      ptx::mbar_init(&bars->rempty[i], 1);
-      bars->armed_r[i] = 0;
-    }
-    ptx::mbar_init(&bars->qfull, C::kSoftWarps);
-    bars->abort = p.wait_ns < kLeastWaitNs;
-    ptx::fence_mbar_init();
-  }
   const int role = warp - C::kSoftWarps;                 // of the warps behind the softmax warps
+  if (role == kCopyRole) init_bars<C::kSoftWarps>(bars, p, lane, &map, &smap);
   if (role == kQkRole) {
     ptx::tmem_alloc(&bars->tmem, C::kTmemCols);
     ptx::tmem_relinquish();
