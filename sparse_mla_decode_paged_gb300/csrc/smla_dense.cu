@@ -54,7 +54,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kTopWeight = 7.75f;       // a row's largest weight is at most 2^7.75: times m_b < 2 within E4M3's 448
-constexpr float kWindow = 3.f;            // a row's reference moves when a tile's largest weight would lie further below that
+constexpr float kWindow = 3.f;            // a reference moves when a tile's largest weight would lie further below that
 constexpr float kLowest = 30.f;           // how far below its highest value a reference may go
 constexpr int kMostTiles16 = 4, kMostTiles32 = 24;   // tiles of a CTA up to which row groups are of 16 and of 32
 
@@ -392,7 +392,7 @@ __device__ void qk_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars
           const uint64_t dk = ptx::sw128_desc(base + C::kRope + rope.slot * kSlot, 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) ptx::mma_f16_ss(d, dk + 2 * kk, dr + 2 * kk, kIdescRope, kk > 0);
-          ptx::mma_commit(&bars->rempty[rope.slot]);                // the codes stay for the PV
+          ptx::mma_commit(&bars->rempty[rope.slot]);     // (the codes stay for the PV)
         } else {
           const uint64_t dk = ptx::sw128_desc(base + C::kK + ks * kSlot, 16, 1024);
           const uint64_t dqb = dq + (uint64_t)((cu * C::kQ8Chunk) >> 4);
@@ -400,7 +400,8 @@ __device__ void qk_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars
           for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
             for (int pass = 0; pass < C::kPasses; ++pass)
-              ptx::mma_f8_ss(d, dk + 2 * kk, dqb + 2 * kk + (uint64_t)((pass * NR * 128) >> 4), kIdescCodes, kk > 0 || pass > 0);
+              ptx::mma_f8_ss(d, dk + 2 * kk, dqb + 2 * kk + (uint64_t)((pass * NR * 128) >> 4), kIdescCodes,
+                             kk > 0 || pass > 0);
         }
         ptx::mma_commit(&bars->sfull[s.slot]);
       }
@@ -484,7 +485,8 @@ __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint3
 // Rows of one item into the Q operands: hi and lo E4M3 codes of the latent part scaled by 2^-x, the rope as it is;
 // each row's factor 2^x sm_scale log2 e and length go to buffer `buf`.
 template <int NR>
-__device__ __forceinline__ void load_q(const DenseParams& p, int item, unsigned char* sm, uint32_t base, int buf, int warp, int lane) {
+__device__ __forceinline__ void load_q(const DenseParams& p, int item, unsigned char* sm, uint32_t base, int buf,
+                                       int warp, int lane) {
   using C = DC<NR>;
   constexpr int kRows = NR / C::kSoftWarps;             // rows warp, warp + kSoftWarps, ... of this warp
   const Rows it = rows_of(p, item);
@@ -629,8 +631,9 @@ __device__ __forceinline__ void write_block(const uint64_t (&x)[HC / 2], uint32_
       const float got = __shfl_xor_sync(0xffffffffu, second ? v.x : v.y, 1);
       const float d0 = second ? got : v.x, d1 = second ? v.y : got;
       if (2 * (i + j) < left) {
-        if constexpr (kBf16) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(to) + 2 * (i + j) * kDLatent) = f32x2_to_bf16x2(d0, d1);
-        else *reinterpret_cast<float2*>(static_cast<float*>(to) + 2 * (i + j) * kDLatent) = make_float2(d0, d1);
+        const int at = 2 * (i + j) * kDLatent;
+        if constexpr (kBf16) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(to) + at) = f32x2_to_bf16x2(d0, d1);
+        else *reinterpret_cast<float2*>(static_cast<float*>(to) + at) = make_float2(d0, d1);
       }
     }
   }
@@ -652,7 +655,9 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
   Ring<C::kScaleSlots> sc;
   Ring<C::kPBufs> pb;
   int kslot = 0;
-  uint32_t red = base + C::kRed + col0 * 4, red_other = red + 4 * NR * 4;   // values of a part's rows meet here: [quad][row]
+  // values of a part's rows meet here, [quad][row]: two buffers in turn, so that a warp may write its next ones while
+  // another still reads (the part's barrier in between holds it from going further)
+  uint32_t red = base + C::kRed + col0 * 4, red_other = red + 4 * NR * 4;
   uint32_t last_par = 0;                                // of the last tile's last PV
   uint32_t ok = p.wait_ns >= kLeastWaitNs;
   bool first = true, begins = w.t == 0;
@@ -690,7 +695,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
     if (!more) done = item;
     if (first && done >= 0) {
       const Rows it = rows_of(p, done);
-      // row sums over the tile's 128 positions
+      // row sums over the 128 positions of the tiles
       float ls[HC];
 #pragma unroll
       for (int i = 0; i < HC / 2; ++i) {
@@ -705,7 +710,8 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
       const size_t slot = 2 * (size_t)blockIdx.x + (begins ? 1 : 0);
       if (lane < HC) {
         const uint32_t at = red + lane * 4;
-        const float z = ptx::lds32f(at) + ptx::lds32f(at + NR * 4) + ptx::lds32f(at + 2 * NR * 4) + ptx::lds32f(at + 3 * NR * 4);
+        const float z = (ptx::lds32f(at) + ptx::lds32f(at + NR * 4)) +
+                        (ptx::lds32f(at + 2 * NR * 4) + ptx::lds32f(at + 3 * NR * 4));
         const float inv = z > 0.f ? 1.f / z : (z == 0.f ? 0.f : CUDART_NAN_F);
         const float lse = z == 0.f ? -CUDART_INF_F : (log2f(z) + ref) * kLn2;
         if (quad == 0 && ok && col0 + lane < it.nrows) {
@@ -751,7 +757,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
     }
     if (!more) break;
     if (first) {
-      ptx::named_bar_sync(1 + C::kParts, C::kSoftWarps * 32);          // red is free, the rows' factors and lengths are written
+      ptx::named_bar_sync(1 + C::kParts, C::kSoftWarps * 32);   // the rows' factors and lengths are written
 #pragma unroll
       for (int i = 0; i < HC / 2; ++i) l[i] = 0;
       ref = CUDART_NAN_F;
@@ -969,9 +975,9 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
 
 // ----------------------------------------------------------------------------- kernel
 
-// This CTA's run of tiles: every CTA adds up the tiles of all items.  The tiles [a, e) of T, and in the items i0 .. i1 - 1,
-// whose tiles begin at `at` and number `mine`, those in which the run begins and ends.
-__device__ __forceinline__ void run_bounds(const DenseParams& p, long long T, Bars* bars, bool write, long long& a, long long& e) {
+// This CTA's run: the tiles [a, e) of T.
+__device__ __forceinline__ void run_bounds(const DenseParams& p, long long T, Bars* bars, bool write, long long& a,
+                                           long long& e) {
   const int active = (int)min((long long)p.ctas, T), c = blockIdx.x;      // CTAs with at least one tile
   a = c < active ? run_start(T, active, c) : T;
   e = c < active ? run_start(T, active, c + 1) : T;
@@ -982,6 +988,7 @@ __device__ __forceinline__ void run_bounds(const DenseParams& p, long long T, Ba
   }
 }
 
+// The items in which the run begins and ends, if they are among i0 .. i1 - 1, whose `mine` tiles begin at `at`.
 __device__ __forceinline__ void find_ends(const DenseParams& p, Bars* bars, int i0, int i1, long long at, long long mine,
                                           long long a, long long e) {
   if (a >= e || a >= at + mine || e <= at) return;
@@ -1002,7 +1009,7 @@ __device__ __forceinline__ void find_ends(const DenseParams& p, Bars* bars, int 
   }
 }
 
-// Few items: one warp, up to four items per lane (the general search's code and barriers take 0.7 us more of a
+// Every CTA adds up the tiles of all items.  Few items: one warp, up to four items per lane (the general search's code and barriers take 0.7 us more of a
 // call: 1 x 77 positions 11.0 us instead of 10.3).
 // Else a run of items per thread, then a scan of the threads' sums.
 template <int kThreads>
@@ -1064,7 +1071,8 @@ __device__ __forceinline__ void find_run(const DenseParams& p, unsigned char* sc
 __device__ __forceinline__ RunDesc describe_run(const Bars* bars) {
   const int c = blockIdx.x, active = bars->active;
   const long long T = bars->total, end = bars->last_end;
-  if (bars->my_tiles == 0 || bars->last_begin < run_start(T, active, c) || end <= run_start(T, active, c + 1)) return RunDesc{0, 0};
+  if (bars->my_tiles == 0 || bars->last_begin < run_start(T, active, c) || end <= run_start(T, active, c + 1))
+    return RunDesc{0, 0};
   int c1 = (int)((end * active + T - 1) / T);            // first CTA past the item, give or take one
   while (c1 > c && run_start(T, active, c1) >= end) --c1;
   while (c1 + 1 < active && run_start(T, active, c1 + 1) < end) ++c1;
@@ -1141,7 +1149,8 @@ __device__ __forceinline__ void add_part(float4& acc, float w, const float4& v) 
   acc.w = fmaf(w, v.w, acc.w);
 }
 
-__device__ __forceinline__ void store_joined(const DenseParams& p, size_t row, int block, int lane, const float4& v, float lse) {
+__device__ __forceinline__ void store_joined(const DenseParams& p, size_t row, int block, int lane, const float4& v,
+                                             float lse) {
   reinterpret_cast<uint2*>(p.out + row * kDLatent + 128 * block)[lane] =
       make_uint2(f32x2_to_bf16x2(v.x, v.y), f32x2_to_bf16x2(v.z, v.w));
   if (lane == 0 && block == 0) p.lse[row] = lse;

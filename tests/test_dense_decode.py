@@ -84,6 +84,13 @@ def test_ragged_batch_with_empty_requests():
     _check(*make_dense(lens, 16, seed=6))
 
 
+@pytest.mark.parametrize("R", [31, 32, 33, 127, 128, 129, 200])
+def test_request_counts(R):
+    g = np.random.default_rng(R)
+    lens = [0 if i % 9 == 4 else int(x) for i, x in enumerate(np.exp(g.uniform(0, np.log(700), R)))]
+    _check(*make_dense(lens, 16, seed=R))
+
+
 def test_many_short_requests():
     lens = [i % 4 for i in range(3000)]
     _check(*make_dense(lens, 2, seed=7))
