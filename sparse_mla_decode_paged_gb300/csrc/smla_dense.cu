@@ -1009,9 +1009,9 @@ __device__ __forceinline__ void find_ends(const DenseParams& p, Bars* bars, int 
   }
 }
 
-// Every CTA adds up the tiles of all items.  Few items: one warp, up to four items per lane (the general search's code and barriers take 0.7 us more of a
-// call: 1 x 77 positions 11.0 us instead of 10.3).
-// Else a run of items per thread, then a scan of the threads' sums.
+// Every CTA adds up the tiles of all items.  Few items: one warp, up to four items per lane (the general search's code
+// and barriers take 0.7 us more of a call: 1 x 77 positions 11.0 us instead of 10.3).  Else a run of items per thread,
+// then a scan of the threads' sums.
 template <int kThreads>
 __device__ __forceinline__ void find_run(const DenseParams& p, unsigned char* scratch, Bars* bars) {
   if (p.requests * p.groups <= 128) {
