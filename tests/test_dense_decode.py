@@ -91,6 +91,26 @@ def test_request_counts(R):
     _check(*make_dense(lens, 16, seed=R))
 
 
+def test_largest_batch():
+    # 65535 queries of one position each: the output is that position's value, lse its score
+    B, g = 65535, torch.Generator().manual_seed(40)
+    cache = wl.fill_kv_cache(64, g, "cpu").to(DEV)
+    bt = torch.randint(0, 64, (B, 1), generator=g).to(torch.int32).to(DEV)
+    q = torch.randn((B, 1, 576), generator=g).to(torch.bfloat16).to(DEV)
+    lens = torch.ones(B, dtype=torch.int32, device=DEV)
+    ws = api.alloc_dense_workspace(api.dense_dims_of(q, cache, bt), DEV)
+    out, lse = api.sparse_mla_dense_decode(q, cache, bt, lens, SCALE, workspace=ws)
+    k = api.sparse_mla_kv_read(cache, bt, torch.zeros(B, dtype=torch.int32, device=DEV), dtype=torch.float32).double()
+    score = SCALE * (q[:, 0].double() * k).sum(-1)
+    size = SCALE * (q[:, 0].double() * k).abs().sum(-1)
+    # q's terms are exact but for 2^-17 of the largest element, the rest are float32 sums
+    err = 2.0 ** -17 * SCALE * q[:, 0].abs().amax(-1).double() * k.abs().sum(-1) + 2.0 ** -18 * size + 2.0 ** -20
+    assert bool(((lse[:, 0].double() - score).abs() <= err).all())
+    # a weight's two terms: 2^-8 of the value with its own rounding, and one of the output
+    assert bool(((out[:, 0].double() - k[:, :512]).abs() <= 2.0 ** -7 * k[:, :512].abs() + 1e-30).all())
+    assert api.read_errors(ws) == 0
+
+
 def test_many_short_requests():
     lens = [i % 4 for i in range(3000)]
     _check(*make_dense(lens, 2, seed=7))
