@@ -34,8 +34,8 @@
 // shared memory feeds the tensor core for 3300 (M = 128 positions or dims, N = 64: 6 KB of operands per MMA of 32 dims or
 // positions) and takes in and gives out another 100 KB; the rest is the latency from scores to weights to the PV, whose
 // K slots come free one by one for the next tile's blocks.  Measured, 32 requests x 32768 positions: 64 heads 226 us
-// (3.0 TB/s), 32 heads 138 us (5.0 TB/s), 16 heads 122 us (5.6 TB/s); 1 x 8192 positions of 64 heads 17.9 us, 1 x 77 of
-// 16 heads 10.3 us.
+// (3.0 TB/s), 32 heads 138 us (5.0 TB/s), 16 heads 122 us (5.6 TB/s); 1 x 8192 positions of 64 heads 18 us, 1 x 77 of 16
+// heads 9.2 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -1024,11 +1024,31 @@ __device__ __forceinline__ void find_ends(const DenseParams& p, Bars* bars, int 
   }
 }
 
+// A table of at most two pages gives every item one tile: no lengths to add up, nothing to merge (1 x 77 positions 9.2 us
+// instead of 10.2).
+__host__ __device__ __forceinline__ bool one_tile(const DenseParams& p) { return p.max_pages <= 2; }
+
 // Every CTA adds up the tiles of all items.  Few items: one warp, up to four items per lane (the general search's code
 // and barriers take 0.7 us more of a call: 1 x 77 positions 11.0 us instead of 10.3).  Else a run of items per thread,
 // then a scan of the threads' sums.
 template <int kThreads>
 __device__ __forceinline__ void find_run(const DenseParams& p, unsigned char* scratch, Bars* bars) {
+  if (one_tile(p)) {                                     // an item is a tile: nothing to look up
+    if (threadIdx.x == 0) {
+      const int n = p.requests * p.groups, active = min(p.ctas, n), c = min((int)blockIdx.x, active);
+      bars->units = n;
+      bars->active = active;
+      bars->run_begin = run_start(n, active, c);
+      bars->run_end = c < active ? run_start(n, active, c + 1) : n;
+      bars->first_item = (int)bars->run_begin;
+      bars->first_tile = 0;
+      bars->last_item = (int)bars->run_end - 1;
+      bars->last_begin = bars->run_end - 1;
+      bars->last_end = bars->run_end;
+    }
+    __syncthreads();
+    return;
+  }
   if (threadIdx.x == 0) bars->run_begin = bars->run_end = 0;
   if (p.requests * p.groups <= 128) {
     if (threadIdx.x < 32) {
@@ -1364,8 +1384,7 @@ cudaError_t launch_nr(const DenseParams& p, unsigned char* ws, cudaStream_t stre
   float* o_part = reinterpret_cast<float*>(ws + kWorkspaceHeader + kDescBytes + lse_part_bytes(p.ctas, NR));
   dense_kernel<NR><<<p.ctas, DC<NR>::kThreads, DC<NR>::kBytes, stream>>>(p, map, smap, descs, lse_part, o_part);
   e = cudaGetLastError();
-  // a table of at most two pages gives every item one tile: nothing to merge
-  if (e != cudaSuccess || p.max_pages <= 2) return e;
+  if (e != cudaSuccess || one_tile(p)) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(8 * p.ctas);
   cfg.blockDim = dim3(kMergeThreads);
