@@ -33,8 +33,8 @@
 // an SM.  Of the 6700 cycles that a tile of 64 rows takes (3.2 us; an SM's share of the HBM rate is a tile per 1.9 us)
 // shared memory feeds the tensor core for 3300 (M = 128 positions or dims, N = 64: 6 KB of operands per MMA of 32 dims or
 // positions) and takes in and gives out another 100 KB; the rest is the latency from scores to weights to the PV, whose
-// K slots come free one by one for the next tile's blocks.  Measured, 32 requests x 32768 positions: 64 heads 226 us
-// (3.0 TB/s), 32 heads 138 us (5.0 TB/s), 16 heads 122 us (5.6 TB/s); 1 x 8192 positions of 64 heads 18 us, 1 x 77 of 16
+// K slots come free one by one for the next tile's blocks.  Measured, 32 requests x 32768 positions: 64 heads 220 us
+// (3.1 TB/s), 32 heads 137 us (5.0 TB/s), 16 heads 122 us (5.6 TB/s); 1 x 8192 positions of 64 heads 18 us, 1 x 77 of 16
 // heads 9.2 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
