@@ -57,7 +57,7 @@ def score_error_bound(q: np.ndarray, k: np.ndarray, sm_scale: float) -> np.ndarr
     top = ql.max(axis=1, keepdims=True)
     small = (ql < 2.0 ** -8 * top) & (ql > 0)
     err = err + 2.0 ** -17 * (top * small) @ kl.T
-    return sm_scale * err
+    return abs(sm_scale) * err
 
 
 def dense_decode(q, kv_cache, block_table, seq_lens, sm_scale: float):
