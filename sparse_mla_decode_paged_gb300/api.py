@@ -298,6 +298,11 @@ def _need_rows(t, name: str, cols: int):
         raise ValueError(f"{name} must be [T,{cols}] with unit stride in a row and rows that do not overlap")
 
 
+def _need_weight(t, name: str, dtype):
+    """A vector of dtype or float32."""
+    _need(t, name, torch.float32 if isinstance(t, torch.Tensor) and t.dtype == torch.float32 else dtype, 1)
+
+
 def _need_paged(kv_cache, block_table, positions, requests, T: int):
     _need(block_table, "block_table", torch.int32, 2)
     _need(positions, "positions", torch.int32, 1)
@@ -342,7 +347,7 @@ def _norm_append_dims(latent, rope, norm_weight, cos_sin, block_table, positions
     T = latent.shape[0]
     if rope.shape[0] != T or rope.dtype != latent.dtype:
         raise ValueError("latent and rope need the same number of rows and one type")
-    _need(norm_weight, "norm_weight", norm_weight.dtype if norm_weight.dtype == torch.float32 else latent.dtype, 1)
+    _need_weight(norm_weight, "norm_weight", latent.dtype)
     if norm_weight.shape[0] != D_LATENT:
         raise ValueError("norm_weight must be [512]")
     _need(cos_sin, "cos_sin", torch.float32, 2)
@@ -411,7 +416,7 @@ def _norm_rope_dims(x, positions, cos_sin, weight, norm, rope_offset, interleave
     if weight is not None:
         if not norm:
             raise ValueError("weight without norm")
-        _need(weight, "weight", weight.dtype if weight.dtype == torch.float32 else x.dtype, 1)
+        _need_weight(weight, "weight", x.dtype)
         if weight.shape[0] != D:
             raise ValueError("weight must be [D]")
     rope_dim = max_pos = 0

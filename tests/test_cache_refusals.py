@@ -1,0 +1,27 @@
+"""Refusals of the Python entry points that need no GPU: arguments of the wrong kind are named, views of equal layout are
+accepted in place."""
+import pytest
+import torch
+
+from sparse_mla_decode_paged_gb300 import api
+
+
+@pytest.fixture
+def on_cpu(monkeypatch):
+    """Checks that look at the device are answered as if the tensors were on the GPU."""
+    monkeypatch.setattr(api, "_need_rows", lambda t, name, cols: None)
+    monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda t: True))
+
+
+@pytest.mark.parametrize("weight", [None, [1.0] * 512, 1.0])
+def test_a_norm_weight_that_is_no_tensor_is_named(on_cpu, weight):
+    bf = torch.zeros((2, 576), dtype=torch.bfloat16)
+    i32 = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(TypeError, match="norm_weight"):
+        api._norm_append_dims(bf[:, :512], bf[:, 512:], weight, torch.zeros((4, 64)), torch.zeros((2, 1), dtype=torch.int32),
+                              i32, torch.zeros((2, 64, 656), dtype=torch.uint8), None, True, None)
+
+
+def test_a_head_weight_that_is_no_tensor_is_named(on_cpu):
+    with pytest.raises(TypeError, match="weight"):
+        api._norm_rope_dims(torch.zeros((2, 3, 64)), None, None, [1.0] * 64, True, 0, True, None, None)
