@@ -369,11 +369,17 @@ def _apart(x: torch.Tensor, out: torch.Tensor, x_bytes: int, out_bytes: int) -> 
     a, b = x.data_ptr(), out.data_ptr()
     if a + x_bytes <= b or b + out_bytes <= a or (a == b and x.stride() == out.stride()) or x.numel() == 0:
         return True
-    size = x.element_size()
-    if x.stride() != out.stride() or min(x.stride()[:2]) < 1 or max(x.stride()[:2]) % min(x.stride()[:2]) != 0:
+    # a dim of size 1 may have any stride
+    steps = [(s, t) for n, s, t in zip(x.shape[:2], x.stride(), out.stride()) if n > 1]
+    if any(s != t for s, t in steps):
         return False
-    step, d = min(x.stride()[:2]), (b - a) % (size * min(x.stride()[:2]))
-    return size * x.shape[2] <= d <= size * (step - x.shape[2])
+    if a == b:
+        return True
+    strides = [s for s, _ in steps]
+    if not strides or min(strides) < 1 or max(strides) % min(strides) != 0:
+        return False
+    size, step = x.element_size(), min(strides)
+    return size * x.shape[2] <= (b - a) % (size * step) <= size * (step - x.shape[2])
 
 
 def _span_bytes(t: torch.Tensor) -> int:
