@@ -1205,6 +1205,7 @@ __device__ __forceinline__ void store_joined(const DenseParams& p, size_t row, i
 // warps share the parts.  Measured, whole calls with four warps / one warp: 32 x 2048 positions of 64 heads (6 parts) 62 /
 // 50 us, 10 x 8192 of 64 heads (16 parts) 42.3 / 38.5 us, 10 x 8192 of 16 heads 23.1 / 24.8 us; of 64 parts and more one
 // warp would take its loads in eight rounds.
+// This grid is resident while the decode's still writes, so partials are read from L2, not through the read-only path.
 __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const DenseParams p, const RunDesc* descs,
                                                                     const float* lse_part, const float* o_part) {
   __shared__ int parts_s[kDenseMaxCtas], item_s[kDenseMaxCtas];     // of the item that begins in CTA c, 0: none to join
@@ -1246,11 +1247,11 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const DenseP
     if (row >= it.nrows) continue;
     const PartRows rows{c, row, nr};
     const float4* o = reinterpret_cast<const float4*>(o_part) + 32 * block + lane;
-    const float x = lane < parts ? __ldg(lse_part + rows.at(lane)) : -CUDART_INF_F;
+    const float x = lane < parts ? __ldcg(lse_part + rows.at(lane)) : -CUDART_INF_F;
     float4 v[kMergeBatch];
 #pragma unroll
     for (int s = 0; s < kMergeBatch; ++s)
-      if (s < parts) v[s] = __ldg(o + rows.at(s) * (kDLatent / 4));
+      if (s < parts) v[s] = __ldcg(o + rows.at(s) * (kDLatent / 4));
     float m = x;
 #pragma unroll
     for (int h = 16; h; h >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, h));
@@ -1266,7 +1267,7 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const DenseP
       if (s < parts) add_part(acc, __shfl_sync(0xffffffffu, w, s), v[s]);
 #pragma unroll
     for (int s = kMergeBatch; s < kFewParts; ++s)
-      if (s < parts) v[s - kMergeBatch] = __ldg(o + rows.at(s) * (kDLatent / 4));
+      if (s < parts) v[s - kMergeBatch] = __ldcg(o + rows.at(s) * (kDLatent / 4));
 #pragma unroll
     for (int s = kMergeBatch; s < kFewParts; ++s)
       if (s < parts) add_part(acc, __shfl_sync(0xffffffffu, w, s), v[s - kMergeBatch]);
@@ -1283,13 +1284,13 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const DenseP
     float4 v[kMergeBatch];
 #pragma unroll
     for (int s = 0; s < kMergeBatch; ++s)
-      if (warp + 4 * s < parts) v[s] = __ldg(o + rows.at(warp + 4 * s) * (kDLatent / 4));
+      if (warp + 4 * s < parts) v[s] = __ldcg(o + rows.at(warp + 4 * s) * (kDLatent / 4));
     __syncthreads();                                     // w_s and sum_s of the row before have been read
     if (warp == 0) {
       float m = -CUDART_INF_F;
       bool bad = false;
       for (int s = lane; s < parts; s += 32) {
-        const float x = __ldg(lse_part + rows.at(s));
+        const float x = __ldcg(lse_part + rows.at(s));
         bad |= isnan(x);
         m = fmaxf(m, x);
         w_s[s] = x;
@@ -1315,7 +1316,7 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const DenseP
       if (s0 > 0) {
 #pragma unroll
         for (int s = 0; s < kMergeBatch; ++s)
-          if (warp + 4 * (s0 + s) < parts) v[s] = __ldg(o + rows.at(warp + 4 * (s0 + s)) * (kDLatent / 4));
+          if (warp + 4 * (s0 + s) < parts) v[s] = __ldcg(o + rows.at(warp + 4 * (s0 + s)) * (kDLatent / 4));
       }
 #pragma unroll
       for (int s = 0; s < kMergeBatch; ++s)
