@@ -95,6 +95,53 @@ def dense_decode(q, kv_cache, block_table, seq_lens, sm_scale: float):
     return out, lse, weighted, floor, score_err
 
 
+def dense_errors(q, kv_cache, block_table, seq_lens, sm_scale: float, weight_bits: float, floor: float):
+    """What rounding may do to dense_decode's result: (out, lse, worst, sigma, score_err), worst and sigma as out.
+
+    A position's operand in a 128-dim block is its softmax weight times the block's scale.  It is off by at most
+    weight_bits of itself or `floor` of the largest operand that the row has in the block's tile of 128 positions,
+    whichever is more; a block whose codes are all zero has no operand.  (A tile more than 2^29 below the row's largest
+    operand in the block has the floor of one 2^29 below.)  The result is rounded to bf16 (2^-8 of itself), and a score
+    off by e changes a weight by at most 2 e of itself.
+    worst: what an element's error cannot exceed when the errors u_t of the positions are unrelated: a sum of a_t u_t
+           with |u_t| <= 1 exceeds 7 sqrt(sum a_t^2) with probability 2 exp(-49 / 2) < 5e-11, and never sum a_t.
+           Equal weights may share one error: weight_bits of the result.
+    sigma: the root of the sum of the squares of the same terms, each at its most.
+    """
+    qf = as_f64_q(q)
+    cache = np.asarray(kv_cache, dtype=np.uint8)
+    flat = cache.reshape(-1, RECORD_BYTES)
+    bt = np.asarray(block_table, dtype=np.int64)
+    B, H, _ = qf.shape
+    s_q = B // bt.shape[0]
+    out, lse, _, _, score_err = dense_decode(q, kv_cache, block_table, seq_lens, sm_scale)
+    worst, sigma = np.zeros_like(out), np.zeros_like(out)
+    for b in range(B):
+        rows, pos = positions_rows(bt[b // s_q], int(seq_lens[b]), cache.shape[0])
+        if rows.size == 0:
+            continue
+        k = dequantize_record(flat[rows])
+        p = np.exp(sm_scale * (qf[b] @ k.T) - lse[b][:, None])
+        v = np.abs(k[:, :D_LATENT])
+        codes, scales, _ = decode_record(flat[rows])
+        codes = np.abs(codes).reshape(-1, 4, D_LATENT // 4)
+        size = np.where(codes.any(axis=2), np.abs(scales), 0.0)                     # [n, 4]
+        operand = p[:, :, None] * size[None]                                        # [H, n, 4]
+        least = np.empty_like(operand)
+        for tile in np.unique(pos // TILE):
+            at = pos // TILE == tile
+            least[:, at] = operand[:, at].max(axis=1, keepdims=True)
+        least = np.maximum(least, 2.0 ** -29 * operand.max(axis=1, keepdims=True)) * floor
+        small = [np.einsum("hnb,nbd->hbd", least ** n, codes ** n).reshape(H, D_LATENT) for n in (1, 2)]
+        weighted = p @ v
+        spread = np.sqrt(weight_bits ** 2 * (p ** 2 @ v ** 2) + small[1])
+        common = (2.0 ** -8 + weight_bits) * np.abs(out[b])
+        score = (2 * score_err[b][:, None] + 2.0 ** -18) * weighted
+        worst[b] = common + score + np.minimum(7 * spread, weight_bits * weighted + small[0])
+        sigma[b] = np.sqrt((2.0 ** -8 * out[b]) ** 2 + score ** 2 + spread ** 2)
+    return out, lse, worst, sigma, score_err
+
+
 def read_records(kv_cache, block_table, positions, requests=None) -> np.ndarray:
     """float64 [T, 576]: the dequantised records; zeros for a token out of range."""
     cache = np.asarray(kv_cache, dtype=np.uint8)
