@@ -18,24 +18,31 @@
 // form s = 2^x sum_b (S_hi + S_lo) scale_b in fp32.  The rope part is a bf16 product.
 // Weights and values.  The codes are the values, too: O^T[512 x NR] += codes^T (P scale), with the same tile read
 // MN-major, accumulated in TMEM over the run's tiles of an item.  A position's scales are split as scale_b = m_b 2^e, e
-// the exponent of the largest of the four, and the weight takes the power of two: w = 2^(s + e - R), with R an integer
-// per row.  Block b's operand is w m_b as two E4M3 terms, hi + lo: 8 significant bits (off by 2^-9 at most) down to
-// 2^-6 and steps of 2^-9 below.  w and m_b are fp16 before (their product once more: 3 roundings of 2^-11).
-//   R follows the tiles' maxima: it moves when a tile's largest weight of the row would lie above 2^7.75 (w m_b < 448)
-// or at or below 2^3.75, and the row's accumulators and sum are then scaled by a power of two, which is exact.  So every
-// weight is off by at most 2^-8 of itself or 2^-13.75 of its tile's largest, and a long tail beside one dominating
-// position keeps its bits.  Moves cost: with a range of 3 powers of two 32 x 32768 positions of 64 heads (random
-// queries and records) take 224 us, with 2 228 us, with 4 218 us, without moves 214 us.  (R does not go further than 30
-// below its highest: what lies there is below 2^-30 of the row's largest weight, and the sums stay finite.)
-//   l = sum w 2^-e in fp32, out = O / l, lse = ln 2 (R + log2 l).
+// the exponent of the largest, and its weight is w = 2^(s + e - A), A an integer per row.  Block b's operand is
+// w m_b 2^(A - R_b), R_b an integer per row and block, as two E4M3 terms: hi + lo, 8 significant bits, off by 2^-9 at
+// most.  (w, m_b and the products are fp16 before: four roundings of 2^-11.)  Operands below 2^-6 are multiples of 2^-9,
+// for 16 and 32 rows, whose lo has accumulators of its own and is held times 16, of 2^-13; there every position adds an
+// offset of its own, spread evenly over +- half a step, before the rounding, so that many small weights keep their sum
+// instead of all becoming 0 (0 stays 0).
+//   R_b follows the largest operands that the tiles have in the block.  It puts them between 2^3.75 and 2^4.75 (2^6.75 and
+// 2^7.75 where they rise), and moves when a tile's would lie above 2^8.75 or at or below 2^-0.25; the row's accumulators of
+// the block are then scaled by a power of two, which is exact.  One R per block, because blocks differ: with one per row a
+// block whose scales are 2^-9 of its neighbour's, or whose neighbour has a position of large weight, loses its bits to it.
+// A block whose codes are all zero has no operand and counts for neither e nor R (the appends write a scale of 1 for it, far
+// above ordinary ones); it has scores of 0 in every row, so its codes are looked at where the first two rows' are.  Moves
+// cost: with a range of 4 instead of 8 powers of two 32 x 32768 positions of 64 heads (random queries and records) take
+// 282 us instead of 235; one reference per row and one exponent per position, 220 us.  (R does not go further than 30 below
+// its highest: what lies there is below 2^-30 of the row's largest operand in the block, and the sums stay finite.)
+//   l = sum w 2^-e in fp32, out_b = O_b 2^(R_b - A) / l, lse = ln 2 (A + log2 l).
 //
-// What bounds it: HBM bytes (656 per position) for 16 rows and nearly so for 32; for 64 rows the steps of a tile inside
-// an SM.  Of the 6700 cycles that a tile of 64 rows takes (3.2 us; an SM's share of the HBM rate is a tile per 1.9 us)
-// shared memory feeds the tensor core for 3300 (M = 128 positions or dims, N = 64: 6 KB of operands per MMA of 32 dims or
-// positions) and takes in and gives out another 100 KB; the rest is the latency from scores to weights to the PV, whose
-// K slots come free one by one for the next tile's blocks.  Measured, 32 requests x 32768 positions: 64 heads 220 us
-// (3.1 TB/s), 32 heads 137 us (5.0 TB/s), 16 heads 122 us (5.6 TB/s); 1 x 8192 positions of 64 heads 18 us, 1 x 77 of 16
-// heads 9.2 us.
+// What bounds it: HBM bytes (656 per position) for 16 rows; for more the steps of a tile inside an SM.  A tile of 64 rows
+// takes 8000 cycles (4.2 us; an SM's share of the HBM rate is a tile per 1.9 us): shared memory feeds the tensor core for
+// 3300 (M = 128 positions or dims, N = 64: 6 KB of operands per MMA of 32 dims or positions), and the softmax warps' steps
+// follow one another: scores 1600 (with the waits for them), scales and rope 550, maxima 1200 (an SM reduces a value over a
+// warp in 0.8 cycles: 1024 of them are 820), exchange 700, weights 350, operands 1400, their stores 900 (and 600 of waits
+// for the PV, whose K slots come free one by one for the next tile's blocks).  Measured, 32 requests x 32768 positions: 64
+// heads 235 us (2.9 TB/s), 32 heads 155 us (4.4 TB/s), 16 heads 124 us (5.5 TB/s); 1 x 8192 positions of 64 heads 19 us, 1
+// x 77 of 16 heads 9.7 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -53,9 +60,12 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kTopWeight = 7.75f;       // a row's largest weight is at most 2^7.75: times m_b < 2 within E4M3's 448
-constexpr float kWindow = 3.f;            // a reference moves when a tile's largest weight would lie further below that
+constexpr float kTopOperand = 8.75f;      // a (row, block)'s largest operand is at most 2^8.75, within E4M3's 448
+constexpr float kWindow = 8.f;            // a reference moves when a tile's largest operand would lie further below that
 constexpr float kLowest = 30.f;           // how far below its highest value a reference may go
+constexpr float kSlack = 4.f;             // A lies at most so far above the highest R
+constexpr int kMantissaUp = 6;            // m_b is held times 2^6: products with the weights up to 2^14.75, within fp16
+constexpr int kLeastExponent = -60;       // of the scale that a position counts with
 constexpr int kMostTiles16 = 4, kMostTiles32 = 24;   // tiles of a CTA up to which row groups are of 16 and of 32
 
 // Warps: the softmax warps (warp w: TMEM lanes of quadrant w % 4, row part w / 4), then one warp each for the
@@ -72,13 +82,17 @@ template <int NR>
 struct DC {
   static constexpr int kRing = NR == 64 ? 6 : NR == 32 ? 8 : 9;     // slots of code blocks
   static constexpr int kRopeSlots = NR == 16 ? 2 : 1;              // the rope's slot is free once its scores are done
-  static constexpr int kScaleSlots = NR == 64 ? 2 : 3;
+  static constexpr int kScaleSlots = NR == 64 ? 1 : 3;
   static constexpr int kPBufs = NR == 64 ? 2 : 4;                   // weights of so many blocks
   static constexpr int kSBufs = 4;                                  // score accumulators
+  // the maxima of a tile and of the next have places of their own where a warp may be a tile ahead of another: with the
+  // weights of two blocks at a time the later ones wait for the PV of the first, so for every warp's
+  static constexpr int kReds = kPBufs < 4 ? 1 : 2;
   // hi and lo terms (of q, and of the weights) meet in one accumulator for 64 rows, where TMEM is full; for fewer rows
   // they are one MMA of twice the columns and meet in the registers
   static constexpr int kPasses = NR == 64 ? 2 : 1;
   static constexpr int kOCols = NR == 64 ? NR : 2 * NR;             // columns of a block's O^T of one tile, or scores
+  static constexpr float kLoUp = kPasses == 1 ? 16.f : 1.f;         // lo is stored times this
   // Row parts: 8 softmax warps.  (16, with half the rows per thread, take as long for 64 rows and longer for 32: 32 x
   // 32768 positions of 64 heads 231 us instead of 228.)
   static constexpr int kParts = 2;
@@ -98,9 +112,10 @@ struct DC {
   static constexpr uint32_t kScale = kP + kPBufs * kPBuf;
   static constexpr uint32_t kF = kScale + kScaleSlots * 2048;     // [2][NR] float
   static constexpr uint32_t kLen = kF + 2 * NR * 4;               // [2][NR] int
-  static constexpr uint32_t kRed = kLen + 2 * NR * 4;             // [2][4][NR] float
-  static constexpr uint32_t kRow = kRed + 8 * NR * 4;             // per softmax warp [HC] minus R, [HC] factor
-  static constexpr uint32_t kBar = kRow + kSoftWarps * 2 * HC * 4;
+  static constexpr uint32_t kRed = kLen + 2 * NR * 4;             // [4 quadrants][NR][4 blocks] float
+  static constexpr uint32_t kRow = kRed + kReds * 16 * NR * 4;  // per softmax warp [4 blocks][HC] 2^(A - R) fp16, [HC] -A
+  static constexpr uint32_t kRowWarp = 4 * HC * 2 + HC * 4;
+  static constexpr uint32_t kBar = kRow + kSoftWarps * kRowWarp;
   static constexpr uint32_t kBytes = kBar + 640;
   // TMEM: O^T of block b at kOCols b, score buffer i at kSCol + kOCols i
   static constexpr uint32_t kSCol = 4 * kOCols;
@@ -575,7 +590,7 @@ __device__ __forceinline__ void tmem_ld(uint32_t a, uint32_t (&r)[NR]) {
 // The exponent e that a position's weights take from its scales.
 __device__ __forceinline__ int scale_exponent(const float4& s) {
   const float top = fmaxf(fmaxf(fabsf(s.x), fabsf(s.y)), fmaxf(fabsf(s.z), fabsf(s.w)));
-  return min(max((int)(__float_as_uint(top) >> 23) - 127, -60), 100);
+  return min(max((int)(__float_as_uint(top) >> 23) - 127, kLeastExponent), 126);
 }
 
 // Two fp16 pairs -> four E4M3 codes in one word (round to nearest even, saturating), and back.
@@ -618,6 +633,45 @@ __device__ __noinline__ void clean_codes(uint32_t base, int slot, int tok, int p
   }
 }
 
+// Which of the blocks in `maybe` hold codes of zero alone at position tok.  (Another row part may be cleaning the codes of
+// a position at the same time: of one that no row sees, whose weights are 0, or NaN codes, whose scores are never 0.)
+template <int NR>
+__device__ __noinline__ uint32_t zero_blocks(uint32_t base, int slot, int tok, uint32_t maybe) {
+  using C = DC<NR>;
+#pragma unroll 1
+  for (int b = 0; b < 4; ++b) {
+    if (maybe >> b & 1) {
+      const uint32_t at = base + C::kK + slot * kSlot;
+      uint32_t any = 0;
+#pragma unroll 1
+      for (int u = 0; u < 8; ++u) {
+        const uint4 v = ptx::lds128(at + swz128(tok, u));
+        any |= v.x | v.y | v.z | v.w;
+      }
+      if (any & 0x7f7f7f7fu) maybe &= ~(1u << b);
+    }
+    if (++slot == C::kRing) slot = 0;
+  }
+  return maybe;
+}
+
+// A scale as the values' operands take it: 0 for a block without values, or a NaN or infinite one (whose rows are NaN
+// by their scores).
+__device__ __forceinline__ float value_scale(float s, bool zero) { return !zero && fabsf(s) < CUDART_INF_F ? s : 0.f; }
+
+// v[lane % N], of values that are the same in every lane: N - 1 selects.
+template <int N>
+__device__ __forceinline__ float pick(const float (&v)[N], int lane) {
+  if constexpr (N == 1) {
+    return v[0];
+  } else {
+    float h[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) h[i] = lane & (N / 2) ? v[i + N / 2] : v[i];
+    return pick<N / 2>(h, lane);
+  }
+}
+
 // One dim of a block for HC rows (pairs), times the rows' factors, out to global memory: lanes 2j, 2j + 1 hold dims
 // d, d + 1 of two rows; the first ends with both dims of the first row, the other (`second`) with both of the second,
 // and stores them at `to` (rows 2 apart; `left` of them from this thread's first on), as bf16 or fp32.
@@ -650,34 +704,33 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
   const int tok = 32 * quad + lane;
   const uint32_t lane_base = tmem + ((uint32_t)(32 * quad) << 16);
   const float kf = p.sm_scale * kLog2e;
-  const uint32_t row_nr = base + C::kRow + warp * 2 * HC * 4, row_f = row_nr + HC * 4;
+  const uint32_t row_c = base + C::kRow + warp * C::kRowWarp, row_na = row_c + 4 * HC * 2;
   Walk w(bars);
   Ring<C::kSBufs> s;
   Ring<C::kScaleSlots> sc;
   Ring<C::kPBufs> pb;
   int kslot = 0;
-  // values of a part's rows meet here, [quad][row]: two buffers in turn, so that a warp may write its next ones while
-  // another still reads (the part's barrier in between holds it from going further)
-  uint32_t red = base + C::kRed + col0 * 4, red_other = red + 4 * NR * 4;
+  uint32_t red = base + C::kRed + col0 * 16;            // values of a part's rows meet here, [quad][row][block]
+  const uint32_t fac = red;                             // and their factors, [block][row], in the first quadrant's place
   uint32_t last_par = 0;                                // of the last tile's last PV
   uint32_t ok = p.wait_ns >= kLeastWaitNs;
   bool first = true, begins = w.t == 0;
   int buf = 0;
   uint64_t l[HC / 2];                                   // row sums over this thread's positions, pairs of rows
-  float ref = CUDART_NAN_F;                             // R of row col0 + lane; NaN: the row has met no position
-  float top = 0.f;                                      // its highest value
+  // Lane l keeps references of row col0 + l % HC: R of blocks kRefs (l / HC) + j (NaN while no value of the block was
+  // met), their highest values, and A (NaN while the row has met no position).  Every warp of the part keeps the same.
+  constexpr int kRefs = HC / 8;
+  const int row = lane % HC, block0 = lane / HC * kRefs;
+  float ref[kRefs], top[kRefs], level = CUDART_NAN_F;
+#pragma unroll
+  for (int j = 0; j < kRefs; ++j) ref[j] = CUDART_NAN_F, top[j] = 0.f;
+  bool live = false;                                    // the part has rows
 
   // every PV of the tiles before is done: their accumulators (dims 128 b + tok) can be read and scaled
   auto wait_pv = [&]() {
     SMLA_WAIT(&bars->pempty[3 % C::kPBufs], last_par);
     ptx::tc_fence_after();
   };
-  auto swap_red = [&]() {
-    const uint32_t r = red;
-    red = red_other;
-    red_other = r;
-  };
-
   int item = -1, done = -1;                             // items whose rows are loaded, whose segment has ended
   bool whole = false;                                   // the segment is its whole item
 #pragma unroll 1
@@ -688,6 +741,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
       done = item;
       item = w.i;
       buf ^= 1;
+      live = col0 < rows_of(p, item).nrows;
       load_q<NR>(p, item, sm, base, buf, warp, lane);
       ptx::fence_proxy_async_smem();
       __syncwarp();
@@ -705,24 +759,35 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
         ls[2 * i + 1] = x.y;
       }
       const float sum = reduce_scatter<HC>(ls, lane, [](float a, float b) { return a + b; });
-      if (lane < HC) ptx::sts32f(red + (quad * NR + lane) * 4, sum);
+      if (lane < HC) ptx::sts32f(red + (quad * NR + lane) * 16, sum);
       ptx::named_bar_sync(1 + part, 128);
       // a run's first segment that continues an item goes to slot 0 of the CTA, its last segment to slot 1
       const size_t slot = 2 * (size_t)blockIdx.x + (begins ? 1 : 0);
-      if (lane < HC) {
-        const uint32_t at = red + lane * 4;
-        const float z = (ptx::lds32f(at) + ptx::lds32f(at + NR * 4)) +
-                        (ptx::lds32f(at + 2 * NR * 4) + ptx::lds32f(at + 3 * NR * 4));
-        const float inv = z > 0.f ? 1.f / z : (z == 0.f ? 0.f : CUDART_NAN_F);
-        const float lse = z == 0.f ? -CUDART_INF_F : (log2f(z) + ref) * kLn2;
-        if (quad == 0 && ok && col0 + lane < it.nrows) {
+      float factor = 0.f;                                 // of block `quad`
+      {
+        const uint32_t at = red + row * 16;
+        const float z = (ptx::lds32f(at) + ptx::lds32f(at + NR * 16)) +
+                        (ptx::lds32f(at + 2 * NR * 16) + ptx::lds32f(at + 3 * NR * 16));
+        const bool none = z == 0.f && !(level == level);   // (a sum of 0 beside positions is refused as a NaN)
+        const float lse = none ? -CUDART_INF_F : z == 0.f ? CUDART_NAN_F : (log2f(z) + level) * kLn2;
+        if (quad == 0 && lane < HC && ok && col0 + lane < it.nrows) {
           if (whole) p.lse[(size_t)it.req * p.q_per_req * p.H + it.row0 + col0 + lane] = lse;
           else lse_part[slot * NR + col0 + lane] = lse;
         }
-        ptx::sts32f(row_f + lane * 4, inv);               // the rows' factors 1 / l, read back as pairs
+        // 2^(R - A) / l, by which a block's accumulators become outputs
+        int ez;
+        const float m = frexpf(z, &ez);
+#pragma unroll
+        for (int j = 0; j < kRefs; ++j) {
+          if (block0 + j != quad) continue;
+          float inv = none ? 0.f : CUDART_NAN_F;
+          if (z > 0.f) inv = ref[j] == ref[j] ? ldexpf(1.f / m, (int)fminf(fmaxf(ref[j] - level, -400.f), 400.f) - ez) : 0.f;
+          factor = inv;
+        }
       }
-      swap_red();
-      __syncwarp();
+      ptx::named_bar_sync(1 + part, 128);
+      if (block0 <= quad && quad < block0 + kRefs) ptx::sts32f(fac + (quad * HC + row) * 4, factor);
+      ptx::named_bar_sync(1 + part, 128);
       // lanes 2j, 2j + 1 hold dims d, d + 1 of two rows: the first ends with both dims of the first row, the other
       // with both of the second, and writes them there
       const bool second = lane & 1;
@@ -746,11 +811,13 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
 #pragma unroll
           for (int i = 0; i < kChunk / 2; ++i) {
             x[i] = ptx::pack2(hi[b][2 * i], hi[b][2 * i + 1]);
-            if constexpr (C::kPasses == 1) x[i] = ptx::add2(x[i], ptx::pack2(lo[b][2 * i], lo[b][2 * i + 1]));
+            if constexpr (C::kPasses == 1)
+              x[i] = ptx::fma2(ptx::pack2(lo[b][2 * i], lo[b][2 * i + 1]), ptx::pack2(1.f / C::kLoUp, 1.f / C::kLoUp), x[i]);
           }
           const size_t to = at + 128 * b + (size_t)i0 * kDLatent;
-          if (whole) write_block<kChunk, true>(x, row_f + i0 * 4, rows_left - i0, second, p.out + to);
-          else write_block<kChunk, false>(x, row_f + i0 * 4, rows_left - i0, second, o_part + to);
+          const uint32_t by = fac + (b * HC + i0) * 4;
+          if (whole) write_block<kChunk, true>(x, by, rows_left - i0, second, p.out + to);
+          else write_block<kChunk, false>(x, by, rows_left - i0, second, o_part + to);
         }
       }
       ptx::tc_fence_before();
@@ -761,7 +828,9 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
       ptx::named_bar_sync(1 + C::kParts, C::kSoftWarps * 32);   // the rows' factors and lengths are written
 #pragma unroll
       for (int i = 0; i < HC / 2; ++i) l[i] = 0;
-      ref = CUDART_NAN_F;
+#pragma unroll
+      for (int j = 0; j < kRefs; ++j) ref[j] = CUDART_NAN_F;
+      level = CUDART_NAN_F;
     }
     // scores of this thread's position for its HC rows, in units of log2
     SMLA_WAIT(&bars->scfull[sc.slot], sc.parity);
@@ -770,8 +839,8 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
     __syncwarp();
     if (ok && lane == 0) ptx::mbar_arrive(&bars->scempty[sc.slot]);
     sc.next();
-    const int e = scale_exponent(s4);
     uint64_t acc[HC / 2];                               // pairs of rows
+    uint32_t zero = 0;                                  // bit b: the position may have no value in block b
     {
       float4 rot = s4;
 #pragma unroll
@@ -796,6 +865,8 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
         tmem_ld<HC>(a1, x1);
         if constexpr (C::kPasses == 1) tmem_ld<HC>(a1 + NR, y1);
         ptx::tmem_wait_ld();
+        if (((x0[0] | x0[1]) & 0x7fffffffu) == 0) zero |= 1u << b;
+        if (((x1[0] | x1[1]) & 0x7fffffffu) == 0) zero |= 2u << b;
 #pragma unroll
         for (int i = 0; i < HC; i += 2) {
           uint64_t x = ptx::pack2(x0[i], x0[i + 1]), y = ptx::pack2(x1[i], x1[i + 1]);
@@ -813,7 +884,21 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
         }
       }
     }
-    // s + e, as 2^x (latent part) + (rope part sm_scale log2 e + e)
+    // the scales that the position's values have: a block without values has none
+    if (__builtin_expect(zero != 0, 0)) zero = live ? zero_blocks<NR>(base, kslot, tok, zero) : 0u;
+    const float4 v4 = make_float4(value_scale(s4.x, zero & 1), value_scale(s4.y, zero & 2), value_scale(s4.z, zero & 4),
+                                  value_scale(s4.w, zero & 8));
+    const int e = scale_exponent(v4);
+    float4 lg;                                          // log2(scale_b 2^-e)
+    {
+      const float d = exp2_int(-e);
+      lg = make_float4(ptx::lg2_approx(fabsf(v4.x * d)), ptx::lg2_approx(fabsf(v4.y * d)), ptx::lg2_approx(fabsf(v4.z * d)),
+                       ptx::lg2_approx(fabsf(v4.w * d)));
+      // (a position with next to no value counts all the same, so that its weight is a float)
+      if (e == kLeastExponent) lg.x = fmaxf(lg.x, 0.f);
+    }
+    __syncwarp();
+    // s + e in powers of two: 2^x sm_scale log2 e (latent part) + (rope part sm_scale log2 e + e)
     SMLA_WAIT(&bars->sfull[s.slot], s.parity);
     ptx::tc_fence_after();
     {
@@ -850,100 +935,170 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
       if (!here || t >= w.n.min_len) clean_codes<NR>(base, kslot, tok, part, here && t < w.n.max_len);
     }
     kslot = kslot + 4 >= C::kRing ? kslot + 4 - C::kRing : kslot + 4;
-    // R of each row: every warp ends with its rows' maxima over the 128 positions, lane -> row
-#pragma unroll
-    for (int i = 0; i < HC / 2; i += 2) {
-      const float2 a = ptx::unpack2(acc[i]), b = ptx::unpack2(acc[i + 1]);
-      const float m0 = ptx::warp_max(a.x), m1 = ptx::warp_max(a.y), m2 = ptx::warp_max(b.x), m3 = ptx::warp_max(b.y);
-      if (lane == 0) ptx::sts128f(red + (quad * NR + 2 * i) * 4, m0, m1, m2, m3);
-    }
-    ptx::named_bar_sync(1 + part, 128);
-    float f = 1.f;                                      // what a reference that moves takes from the sums so far
-    if (lane < HC) {
-      const uint32_t at = red + lane * 4;
-      const float m = fmaxf(fmaxf(ptx::lds32f(at), ptx::lds32f(at + NR * 4)),
-                            fmaxf(ptx::lds32f(at + 2 * NR * 4), ptx::lds32f(at + 3 * NR * 4)));
-      // (a row without positions here, or of NaNs alone, keeps its reference)
-      const float r = ceilf(m - kTopWeight);
-      if (m > -CUDART_INF_F && !(r <= ref && r >= ref - kWindow)) {
-        const bool set = ref == ref;
-        const float to = set ? fmaxf(r + 1.f, top - kLowest) : r + 1.f;
-        if (set) f = exp2_int((int)fminf(fmaxf(ref - to, -126.f), 126.f));
-        top = set ? fmaxf(top, to) : to;
-        ref = to;
-      }
-      ptx::sts32f(row_nr + lane * 4, ref == ref ? -ref : 0.f);
-      ptx::sts32f(row_f + lane * 4, f);
-    }
-    swap_red();
-    const uint32_t moved = __ballot_sync(0xffffffffu, f != 1.f);
-    if (moved) {
-      __syncwarp();                                     // the factors are written
-#pragma unroll
-      for (int i = 0; i < HC / 2; i += 2) {
-        const ulonglong2 c = ptx::lds128_pairs(row_f + i * 8);
-        l[i] = ptx::mul2(l[i], c.x);
-        l[i + 1] = ptx::mul2(l[i + 1], c.y);
-      }
-      wait_pv();
-#pragma unroll 1
-      for (int i0 = 0; i0 < HC; i0 += kChunk) {
-        if (!(moved >> i0 & 0xffu)) continue;
-        const float4 f0 = ptx::lds128f(row_f + i0 * 4), f1 = ptx::lds128f(row_f + i0 * 4 + 16);
-        const float c[kChunk] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
-#pragma unroll
-        for (int j = 0; j < (C::kPasses == 1 ? 2 : 1); ++j) {
-          uint32_t x[4][kChunk];
-#pragma unroll
-          for (int b = 0; b < 4; ++b) tmem_ld<kChunk>(lane_base + C::kOCols * b + NR * j + col0 + i0, x[b]);
-          ptx::tmem_wait_ld();
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-#pragma unroll
-            for (int i = 0; i < kChunk; ++i) x[b][i] = __float_as_uint(__uint_as_float(x[b][i]) * c[i]);
-            tmem_st<kChunk>(lane_base + C::kOCols * b + NR * j + col0 + i0, x[b]);
-          }
-        }
-      }
-      ptx::tmem_wait_st();
-      ptx::tc_fence_before();
-    }
-    __syncwarp();
-    // weights
-    uint32_t w16[HC / 2];
+    // the largest operand of each row and block over the 128 positions: every warp's 32 first
     {
-      const float d = exp2_int(-e);
-      const uint64_t down = ptx::pack2(d, d);
-#pragma unroll
-      for (int i = 0; i < HC / 2; i += 2) {
-        const ulonglong2 nr = ptx::lds128_pairs(row_nr + i * 8);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float2 x = ptx::unpack2(ptx::add2(acc[i + j], j ? nr.y : nr.x));
-          const float a = ptx::ex2_approx(x.x), b = ptx::ex2_approx(x.y);
-          l[i + j] = ptx::fma2(ptx::pack2(a, b), down, l[i + j]);
-          const __half2 h = __floats2half2_rn(a, b);
-          w16[i + j] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-      }
-    }
-    // block b's operand: w m_b as hi + lo
-    {
-      const float d = exp2_int(-e);
-      float4 rot = s4;
+      float4 g = lg, top4 = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
       for (int b = 0; b < 4; ++b) {
-        // (a NaN or infinite scale: its rows are NaN by their scores)
-        const __half2 m = __float2half2_rn(fminf(fmaxf(rot.x * d, -2.f), 2.f));
+        const uint64_t g2 = ptx::pack2(g.x, g.x);
+        g = make_float4(g.y, g.z, g.w, g.x);
+        float m[HC];
+#pragma unroll
+        for (int i = 0; i < HC / 2; ++i) {
+          const float2 x = ptx::unpack2(ptx::add2(acc[i], g2));
+          m[2 * i] = ptx::warp_max(x.x);
+          m[2 * i + 1] = ptx::warp_max(x.y);
+        }
+        top4 = make_float4(top4.y, top4.z, top4.w, pick<HC>(m, lane));
+      }
+      if (lane < HC) ptx::sts128f(red + (quad * NR + lane) * 16, top4.x, top4.y, top4.z, top4.w);
+    }
+    ptx::named_bar_sync(1 + part, 128);
+    float m[kRefs];                                     // this lane's blocks' largest operands
+    bool stays = true;                                  // within the references' windows
+    {
+      float x[4][kRefs];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) ptx::lds_floats(red + (k * NR + row) * 16 + block0 * 4, x[k]);
+#pragma unroll
+      for (int j = 0; j < kRefs; ++j) {
+        m[j] = fmaxf(fmaxf(x[0][j], x[1][j]), fmaxf(x[2][j], x[3][j]));
+        const float d = m[j] - ref[j];
+        stays = stays && (m[j] == -CUDART_INF_F || (d <= kTopOperand && d > kTopOperand - 1.f - kWindow));
+      }
+    }
+    if constexpr (C::kReds == 2) red = red == fac ? fac + 16 * NR * 4 : fac;
+    if (first || __any_sync(0xffffffffu, !stays)) {     // (the same in the part's four warps)
+      // R of each block, A, and the factors by which the sums so far change when they move
+      float f[kRefs], fa = 1.f, high = CUDART_NAN_F;
+#pragma unroll
+      for (int j = 0; j < kRefs; ++j) {
+        const float r = ceilf(m[j] - kTopOperand);
+        f[j] = 1.f;
+        // (a row without positions here, or of NaNs alone, keeps what it has)
+        const bool moves = m[j] > -CUDART_INF_F && !(r <= ref[j] && r >= ref[j] - kWindow);
+        if (__any_sync(0xffffffffu, moves)) {
+          const bool set = ref[j] == ref[j];
+          const float to = !set ? r + kWindow / 2 : fmaxf(r > ref[j] ? r + 1.f : r + kWindow / 2, top[j] - kLowest);
+          if (moves) {
+            if (set) f[j] = exp2_int((int)fminf(fmaxf(ref[j] - to, -126.f), 126.f));
+            top[j] = set ? fmaxf(top[j], to) : to;
+            ref[j] = to;
+          }
+        }
+        high = fmaxf(high, ref[j]);
+      }
+#pragma unroll
+      for (int o = HC; o < 32; o <<= 1) high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
+      if (!(level >= high && level <= high + kSlack)) {
+        const float to = high + kSlack / 2;
+        if (level == level) fa = exp2_int((int)fminf(fmaxf(level - to, -126.f), 126.f));
+        level = to;
+      }
+      bool moves = false;
+#pragma unroll
+      for (int j = 0; j < kRefs; ++j) moves |= f[j] != 1.f;
+      const bool moved = __any_sync(0xffffffffu, moves);
+      if (__any_sync(0xffffffffu, fa != 1.f)) {
+        if (lane < HC) ptx::sts32f(row_na + lane * 4, fa);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < HC / 2; i += 2) {
+          const ulonglong2 by = ptx::lds128_pairs(row_na + i * 8);
+          l[i] = ptx::mul2(l[i], by.x);
+          l[i + 1] = ptx::mul2(l[i + 1], by.y);
+        }
+        __syncwarp();
+      }
+      if (moved) {
+        wait_pv();
+#pragma unroll 1
+        for (int b = 0; b < 4; ++b) {
+          float fb = f[0];                                // of block b, in the lanes that keep its reference
+#pragma unroll
+          for (int j = 1; j < kRefs; ++j) fb = block0 + j == b ? f[j] : fb;
+          const bool mine = block0 <= b && b < block0 + kRefs;
+          uint32_t rows = __ballot_sync(0xffffffffu, mine && fb != 1.f);
+          if (rows == 0) continue;
+          if constexpr (HC < 32) rows = rows >> (b / kRefs * HC) & ((1u << HC) - 1u);
+          if (mine) ptx::sts32f(row_na + row * 4, fb);
+          __syncwarp();
+          const uint32_t at = lane_base + C::kOCols * b + col0;
+#pragma unroll 1
+          for (int i0 = 0; i0 < HC; i0 += kChunk) {
+            if (!(rows >> i0 & 0xffu)) continue;
+            const float4 f0 = ptx::lds128f(row_na + i0 * 4), f1 = ptx::lds128f(row_na + i0 * 4 + 16);
+            const float by[kChunk] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+            uint32_t x[C::kPasses == 1 ? 2 : 1][kChunk];
+            tmem_ld<kChunk>(at + i0, x[0]);
+            if constexpr (C::kPasses == 1) tmem_ld<kChunk>(at + NR + i0, x[1]);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) {
+              x[0][i] = __float_as_uint(__uint_as_float(x[0][i]) * by[i]);
+              if constexpr (C::kPasses == 1) x[1][i] = __float_as_uint(__uint_as_float(x[1][i]) * by[i]);
+            }
+            tmem_st<kChunk>(at + i0, x[0]);
+            if constexpr (C::kPasses == 1) tmem_st<kChunk>(at + NR + i0, x[1]);
+          }
+          __syncwarp();
+        }
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+      }
+      if (lane < HC) ptx::sts32f(row_na + lane * 4, level == level ? -level : 0.f);
+#pragma unroll
+      for (int j = 0; j < kRefs; ++j) {
+        const int k = (int)fminf(fmaxf(level - ref[j] - kMantissaUp, -14.f), 15.f);
+        ptx::sts16(row_c + ((block0 + j) * HC + row) * 2, ref[j] == ref[j] ? (uint16_t)((15 + k) << 10) : 0);   // 2^k
+      }
+      __syncwarp();
+    }
+    // weights
+    const float down = exp2_int(-e);
+    uint32_t w16[HC / 2];
+    {
+      const uint64_t down2 = ptx::pack2(down, down);
+#pragma unroll
+      for (int i = 0; i < HC / 2; i += 2) {
+        const ulonglong2 na = ptx::lds128_pairs(row_na + i * 8);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float2 x = ptx::unpack2(ptx::add2(acc[i + j], j ? na.y : na.x));
+          const float a = ptx::ex2_approx(x.x), b = ptx::ex2_approx(x.y);
+          l[i + j] = ptx::fma2(ptx::pack2(a, b), down2, l[i + j]);
+          w16[i + j] = as_u32(__floats2half2_rn(a, b));
+        }
+      }
+    }
+    // block b's operand: w m_b 2^(A - R_b) as hi + lo.  The offset: odd multiples of 2^-7 half steps, one per position
+    {
+      float4 rot = v4;
+      const __half2 up = __float2half2_rn(C::kLoUp);
+      const __half2 dither = __float2half2_rn((float)(2 * (int)(__brev(tok) >> 25) - 127) * (0x1p-17f / C::kLoUp));
+#pragma unroll 1
+      for (int b = 0; b < 4; ++b) {
+        const __half2 m = __float2half2_rn(rot.x * (down * (float)(1 << kMantissaUp)));
         rot = make_float4(rot.y, rot.z, rot.w, rot.x);
         uint32_t hi[HC / 4], lo[HC / 4];
 #pragma unroll
-        for (int i = 0; i < HC / 4; ++i) {
-          const __half2 x = __hmul2(as_half2(w16[2 * i]), m), y = __hmul2(as_half2(w16[2 * i + 1]), m);
-          hi[i] = f16x4_to_e4m3x4(as_u32(x), as_u32(y));
-          uint32_t bx, by;
-          e4m3x4_to_f16x4(hi[i], bx, by);
-          lo[i] = f16x4_to_e4m3x4(as_u32(__hsub2(x, as_half2(bx))), as_u32(__hsub2(y, as_half2(by))));
+        for (int i = 0; i < HC / 4; i += 2) {
+          const uint4 c8 = ptx::lds128(row_c + (b * HC + 4 * i) * 2);
+          const uint32_t cs[4] = {c8.x, c8.y, c8.z, c8.w};
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const __half2 x = __hfma2(__hmul2(as_half2(w16[2 * (i + j)]), m), as_half2(cs[2 * j]), dither);
+            const __half2 y = __hfma2(__hmul2(as_half2(w16[2 * (i + j) + 1]), m), as_half2(cs[2 * j + 1]), dither);
+            hi[i + j] = f16x4_to_e4m3x4(as_u32(x), as_u32(y));
+            uint32_t bx, by;
+            e4m3x4_to_f16x4(hi[i + j], bx, by);
+            __half2 dx = __hsub2(x, as_half2(bx)), dy = __hsub2(y, as_half2(by));
+            if constexpr (C::kPasses == 1) {
+              dx = __hmul2(dx, up);
+              dy = __hmul2(dy, up);
+            }
+            lo[i + j] = f16x4_to_e4m3x4(as_u32(dx), as_u32(dy));
+          }
         }
         SMLA_WAIT(&bars->pempty[pb.slot], pb.parity ^ 1);
         const uint32_t dst = base + C::kP + pb.slot * C::kPBuf;
@@ -1425,10 +1580,10 @@ extern "C" int sparse_mla_dense_plan_for(const smla_dense_dims* d, int32_t sm_co
   const int64_t rows = (int64_t)sq * d->num_heads;
   plan->ctas = d->ctas > 0 ? d->ctas : (sm_count < kDenseMaxCtas ? sm_count : kDenseMaxCtas);
   plan->reserved = 0;
-  // Rows that a CTA takes through a tile together.  Few rows: a tile is done sooner (1.9, 2.5 and 3.9 us for 16, 32
+  // Rows that a CTA takes through a tile together.  Few rows: a tile is done sooner (1.9, 2.8 and 4.2 us for 16, 32
   // and 64 rows), and so are the steps around the tiles (a CTA's rows read and its results written), but each row
-  // group reads the tile again.  Measured at 64 heads, 16 / 32 / 64 rows: 1 request x 8192 positions 19.0 / 20.1 / 25.0
-  // us, 4 x 8192 30.1 / 27.9 / 32.1, 32 x 4096 69 / 58 / 67, 32 x 8192 130 / 99 / 101, 32 x 16384 237 / 166 / 154.  So:
+  // group reads the tile again.  Measured at 64 heads, 16 / 32 / 64 rows: 1 request x 8192 positions 19.2 / 19.4 / 23.8
+  // us, 4 x 8192 28.5 / 26.9 / 31.5, 32 x 4096 80.0 / 60.7 / 60.9, 32 x 8192 133 / 94 / 86, 32 x 16384 235 / 157 / 136.  So:
   // the fewest rows with which a CTA has at most a few tiles if every request is as long as its table.
   const int64_t tiles = d->batch / sq * ((d->max_pages_per_seq + (int64_t)1) / 2);
   auto groups = [&](int nr) { return (rows + nr - 1) / nr; };

@@ -444,8 +444,19 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
+// log2 x, hardware approximation (absolute error about 2^-22), subnormal x taken as zero; -inf for zero.
+__device__ __forceinline__ float lg2_approx(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ void sts32f(uint32_t saddr, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(saddr), "f"(v) : "memory");
+}
+
+__device__ __forceinline__ void sts16(uint32_t saddr, uint16_t v) {
+  asm volatile("st.shared.b16 [%0], %1;" ::"r"(saddr), "h"(v) : "memory");
 }
 
 __device__ __forceinline__ float lds32f(uint32_t saddr) {
@@ -456,6 +467,19 @@ __device__ __forceinline__ float lds32f(uint32_t saddr) {
 
 __device__ __forceinline__ void sts128f(uint32_t saddr, float a, float b, float c, float d) {
   asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(saddr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
+}
+
+// 1, 2 or 4 consecutive floats.
+template <int N>
+__device__ __forceinline__ void lds_floats(uint32_t saddr, float (&v)[N]) {
+  static_assert(N == 1 || N == 2 || N == 4, "one load");
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(saddr)
+                 : "memory");
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "r"(saddr) : "memory");
+  else
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[0]) : "r"(saddr) : "memory");
 }
 
 __device__ __forceinline__ float4 lds128f(uint32_t saddr) {
