@@ -404,10 +404,10 @@ int sparse_mla_dense_plan(const smla_dense_dims* dims, int32_t device, smla_dens
  * follows the 128-position tiles: off by 2^-8 of itself, or by a rounding to steps of 2^-9 (row groups of 64 rows) or
  * 2^-13 (of 16 and 32) where the tile's largest lies between 2^-0.25 and 2^8.75, whichever is more.  That rounding is
  * offset evenly over the positions, so that sums of many small weights are kept.  Blocks of one record keep their bits
- * whatever the other blocks' scales are (down to 2^-17 of the largest in the row's weights, fewer bits below), and a
- * position or block whose codes are all zero takes none from the others, whatever its scale.  Scales count as they are
- * between 2^-60 and 2^100 (smaller ones lose bits, beyond 2^126 the row may be NaN).  A row that sees a NaN (in q, a code,
- * a scale or the rope) is NaN.
+ * whatever the other blocks' scales are (off by up to 2^-23 of the row's largest product of weight and scale in any
+ * block), and a position or block whose codes are all zero takes none from the others, whatever its scale (while its
+ * weight is below 2^50 times theirs).  Scales count as they are between 2^-60 and 2^100 (smaller ones lose bits, beyond
+ * 2^126 the row may be NaN).  A row that sees a NaN (in q, a code, a scale or the rope) is NaN.
  * Statuses as sparse_mla_decode. */
 int sparse_mla_dense_decode(const smla_dense_dims* dims, const void* q, const void* kv_cache,
                             const int32_t* block_table, const int32_t* seq_lens, float sm_scale, void* out,

@@ -95,13 +95,15 @@ def dense_decode(q, kv_cache, block_table, seq_lens, sm_scale: float):
     return out, lse, weighted, floor, score_err
 
 
-def dense_errors(q, kv_cache, block_table, seq_lens, sm_scale: float, weight_bits: float, floor: float):
+def dense_errors(q, kv_cache, block_table, seq_lens, sm_scale: float, weight_bits: float, floor: float,
+                 least: float):
     """What rounding may do to dense_decode's result: (out, lse, worst, sigma, score_err), worst and sigma as out.
 
     A position's operand in a 128-dim block is its softmax weight times the block's scale.  It is off by at most
     weight_bits of itself or `floor` of the largest operand that the row has in the block's tile of 128 positions,
-    whichever is more; a block whose codes are all zero has no operand.  (A tile more than 2^29 below the row's largest
-    operand in the block has the floor of one 2^29 below.)  The result is rounded to bf16 (2^-8 of itself), and a score
+    whichever is more, or `least` of the row's largest operand in any block; a block whose codes are all zero has no
+    operand.  (A tile more than 2^29 below the row's largest operand in the block has the floor of one 2^29 below.)  The
+    result is rounded to bf16 (2^-8 of itself), and a score
     off by e changes a weight by at most 2 e of itself.
     worst: what an element's error cannot exceed when the errors u_t of the positions are unrelated: a sum of a_t u_t
            with |u_t| <= 1 exceeds 7 sqrt(sum a_t^2) with probability 2 exp(-49 / 2) < 5e-11, and never sum a_t.
@@ -127,12 +129,13 @@ def dense_errors(q, kv_cache, block_table, seq_lens, sm_scale: float, weight_bit
         codes = np.abs(codes).reshape(-1, 4, D_LATENT // 4)
         size = np.where(codes.any(axis=2), np.abs(scales), 0.0)                     # [n, 4]
         operand = p[:, :, None] * size[None]                                        # [H, n, 4]
-        least = np.empty_like(operand)
+        off = np.empty_like(operand)
         for tile in np.unique(pos // TILE):
             at = pos // TILE == tile
-            least[:, at] = operand[:, at].max(axis=1, keepdims=True)
-        least = np.maximum(least, 2.0 ** -29 * operand.max(axis=1, keepdims=True)) * floor
-        small = [np.einsum("hnb,nbd->hbd", least ** n, codes ** n).reshape(H, D_LATENT) for n in (1, 2)]
+            off[:, at] = operand[:, at].max(axis=1, keepdims=True)
+        off = floor * np.maximum(off, 2.0 ** -29 * operand.max(axis=1, keepdims=True))
+        off += least * operand.max(axis=(1, 2), keepdims=True)
+        small = [np.einsum("hnb,nbd->hbd", off ** n, codes ** n).reshape(H, D_LATENT) for n in (1, 2)]
         weighted = p @ v
         spread = np.sqrt(weight_bits ** 2 * (p ** 2 @ v ** 2) + small[1])
         common = (2.0 ** -8 + weight_bits) * np.abs(out[b])

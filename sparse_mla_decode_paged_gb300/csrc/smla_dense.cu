@@ -31,8 +31,9 @@
 // A block whose codes are all zero has no operand and counts for neither e nor R (the appends write a scale of 1 for it, far
 // above ordinary ones); it has scores of 0 in every row, so its codes are looked at where the first two rows' are.  Moves
 // cost: with a range of 4 instead of 8 powers of two 32 x 32768 positions of 64 heads (random queries and records) take
-// 282 us instead of 235; one reference per row and one exponent per position, 220 us.  (R does not go further than 30 below
-// its highest: what lies there is below 2^-30 of the row's largest operand in the block, and the sums stay finite.)
+// 282 us instead of 240; one reference per row and one exponent per position, 220 us.  (R does not go further than 30 below
+// its highest, nor 15 below A: what lies there is below 2^-30 of the row's largest operand in the block, or 2^-17 of
+// its largest in any block, and the sums and factors stay finite.)
 //   l = sum w 2^-e in fp32, out_b = O_b 2^(R_b - A) / l, lse = ln 2 (A + log2 l).
 //
 // What bounds it: HBM bytes (656 per position) for 16 rows; for more the steps of a tile inside an SM.  A tile of 64 rows
@@ -41,7 +42,7 @@
 // follow one another: scores 1600 (with the waits for them), scales and rope 550, maxima 1200 (an SM reduces a value over a
 // warp in 0.8 cycles: 1024 of them are 820), exchange 700, weights 350, operands 1400, their stores 900 (and 600 of waits
 // for the PV, whose K slots come free one by one for the next tile's blocks).  Measured, 32 requests x 32768 positions: 64
-// heads 235 us (2.9 TB/s), 32 heads 155 us (4.4 TB/s), 16 heads 124 us (5.5 TB/s); 1 x 8192 positions of 64 heads 19 us, 1
+// heads 240 us (2.9 TB/s), 32 heads 155 us (4.4 TB/s), 16 heads 124 us (5.5 TB/s); 1 x 8192 positions of 64 heads 19 us, 1
 // x 77 of 16 heads 9.7 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -63,8 +64,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kTopOperand = 8.75f;      // a (row, block)'s largest operand is at most 2^8.75, within E4M3's 448
 constexpr float kWindow = 8.f;            // a reference moves when a tile's largest operand would lie further below that
 constexpr float kLowest = 30.f;           // how far below its highest value a reference may go
-constexpr float kSlack = 4.f;             // A lies at most so far above the highest R
-constexpr int kMantissaUp = 6;            // m_b is held times 2^6: products with the weights up to 2^14.75, within fp16
+constexpr float kAbove = 6.f;             // A is at most so far below the highest R: weights times m_b stay below 2^14.75, in fp16
+constexpr float kSlack = 4.f;             // and moves when it is less far by more than this
+constexpr float kFactor = 15.f;           // no R is further below A than this: 2^(A - R) stays in fp16
 constexpr int kLeastExponent = -60;       // of the scale that a position counts with
 constexpr int kMostTiles16 = 4, kMostTiles32 = 24;   // tiles of a CTA up to which row groups are of 16 and of 32
 
@@ -722,8 +724,9 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
   constexpr int kRefs = HC / 8;
   const int row = lane % HC, block0 = lane / HC * kRefs;
   float ref[kRefs], top[kRefs], level = CUDART_NAN_F;
+  float upper[kRefs], lower[kRefs];                     // a reference stays for a largest operand up to, and above, these
 #pragma unroll
-  for (int j = 0; j < kRefs; ++j) ref[j] = CUDART_NAN_F, top[j] = 0.f;
+  for (int j = 0; j < kRefs; ++j) ref[j] = CUDART_NAN_F, top[j] = 0.f, upper[j] = lower[j] = -CUDART_INF_F;
   bool live = false;                                    // the part has rows
 
   // every PV of the tiles before is done: their accumulators (dims 128 b + tok) can be read and scaled
@@ -769,19 +772,19 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
         const float z = (ptx::lds32f(at) + ptx::lds32f(at + NR * 16)) +
                         (ptx::lds32f(at + 2 * NR * 16) + ptx::lds32f(at + 3 * NR * 16));
         const bool none = z == 0.f && !(level == level);   // (a sum of 0 beside positions is refused as a NaN)
-        const float lse = none ? -CUDART_INF_F : z == 0.f ? CUDART_NAN_F : (log2f(z) + level) * kLn2;
+        int ez;
+        const float mz = frexpf(z, &ez);                  // (the exponents meet as whole numbers)
+        const float lse = none ? -CUDART_INF_F : z == 0.f ? CUDART_NAN_F : (log2f(mz) + ((float)ez + level)) * kLn2;
         if (quad == 0 && lane < HC && ok && col0 + lane < it.nrows) {
           if (whole) p.lse[(size_t)it.req * p.q_per_req * p.H + it.row0 + col0 + lane] = lse;
           else lse_part[slot * NR + col0 + lane] = lse;
         }
         // 2^(R - A) / l, by which a block's accumulators become outputs
-        int ez;
-        const float m = frexpf(z, &ez);
 #pragma unroll
         for (int j = 0; j < kRefs; ++j) {
           if (block0 + j != quad) continue;
           float inv = none ? 0.f : CUDART_NAN_F;
-          if (z > 0.f) inv = ref[j] == ref[j] ? ldexpf(1.f / m, (int)fminf(fmaxf(ref[j] - level, -400.f), 400.f) - ez) : 0.f;
+          if (z > 0.f) inv = ref[j] == ref[j] ? ldexpf(1.f / mz, (int)fminf(fmaxf(ref[j] - level, -400.f), 400.f) - ez) : 0.f;
           factor = inv;
         }
       }
@@ -829,7 +832,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
 #pragma unroll
       for (int i = 0; i < HC / 2; ++i) l[i] = 0;
 #pragma unroll
-      for (int j = 0; j < kRefs; ++j) ref[j] = CUDART_NAN_F;
+      for (int j = 0; j < kRefs; ++j) ref[j] = CUDART_NAN_F, upper[j] = lower[j] = -CUDART_INF_F;
       level = CUDART_NAN_F;
     }
     // scores of this thread's position for its HC rows, in units of log2
@@ -963,41 +966,43 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
 #pragma unroll
       for (int j = 0; j < kRefs; ++j) {
         m[j] = fmaxf(fmaxf(x[0][j], x[1][j]), fmaxf(x[2][j], x[3][j]));
-        const float d = m[j] - ref[j];
-        stays = stays && (m[j] == -CUDART_INF_F || (d <= kTopOperand && d > kTopOperand - 1.f - kWindow));
+        stays = stays && m[j] <= upper[j] && (m[j] > lower[j] || m[j] == -CUDART_INF_F);
       }
     }
     if constexpr (C::kReds == 2) red = red == fac ? fac + 16 * NR * 4 : fac;
     if (first || __any_sync(0xffffffffu, !stays)) {     // (the same in the part's four warps)
       // R of each block, A, and the factors by which the sums so far change when they move
-      float f[kRefs], fa = 1.f, high = CUDART_NAN_F;
+      float f[kRefs], fa = 1.f, high = CUDART_NAN_F, to[kRefs];
 #pragma unroll
       for (int j = 0; j < kRefs; ++j) {
         const float r = ceilf(m[j] - kTopOperand);
-        f[j] = 1.f;
         // (a row without positions here, or of NaNs alone, keeps what it has)
-        const bool moves = m[j] > -CUDART_INF_F && !(r <= ref[j] && r >= ref[j] - kWindow);
-        if (__any_sync(0xffffffffu, moves)) {
-          const bool set = ref[j] == ref[j];
-          const float to = !set ? r + kWindow / 2 : fmaxf(r > ref[j] ? r + 1.f : r + kWindow / 2, top[j] - kLowest);
-          if (moves) {
-            if (set) f[j] = exp2_int((int)fminf(fmaxf(ref[j] - to, -126.f), 126.f));
-            top[j] = set ? fmaxf(top[j], to) : to;
-            ref[j] = to;
-          }
-        }
-        high = fmaxf(high, ref[j]);
+        const bool moves = m[j] > -CUDART_INF_F && !(r <= ref[j] && r >= ref[j] - kWindow), set = ref[j] == ref[j];
+        const float next = set ? fmaxf(r > ref[j] ? r + 1.f : r + kWindow / 2, top[j] - kLowest) : r + kWindow / 2;
+        to[j] = moves ? next : ref[j];
+        high = fmaxf(high, to[j]);
       }
 #pragma unroll
       for (int o = HC; o < 32; o <<= 1) high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
-      if (!(level >= high && level <= high + kSlack)) {
-        const float to = high + kSlack / 2;
-        if (level == level) fa = exp2_int((int)fminf(fmaxf(level - to, -126.f), 126.f));
-        level = to;
+      if (!(level >= high - kAbove && level <= high - kAbove + kSlack)) {
+        const float next = high - kAbove + kSlack / 2;
+        if (level == level) fa = exp2_int((int)fminf(fmaxf(level - next, -126.f), 126.f));
+        level = next;
       }
       bool moves = false;
 #pragma unroll
-      for (int j = 0; j < kRefs; ++j) moves |= f[j] != 1.f;
+      for (int j = 0; j < kRefs; ++j) {
+        f[j] = 1.f;
+        if (to[j] == to[j]) {
+          const float next = fmaxf(to[j], level - kFactor);
+          if (ref[j] == ref[j]) f[j] = exp2_int((int)fminf(fmaxf(ref[j] - next, -126.f), 126.f));
+          top[j] = ref[j] == ref[j] ? fmaxf(top[j], next) : next;
+          ref[j] = next;
+          upper[j] = next + kTopOperand;                // (one that is as low as it may be stays below its window)
+          lower[j] = next <= fmaxf(top[j] - kLowest, level - kFactor) ? -CUDART_INF_F : upper[j] - 1.f - kWindow;
+        }
+        moves |= f[j] != 1.f;
+      }
       const bool moved = __any_sync(0xffffffffu, moves);
       if (__any_sync(0xffffffffu, fa != 1.f)) {
         if (lane < HC) ptx::sts32f(row_na + lane * 4, fa);
@@ -1049,7 +1054,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
       if (lane < HC) ptx::sts32f(row_na + lane * 4, level == level ? -level : 0.f);
 #pragma unroll
       for (int j = 0; j < kRefs; ++j) {
-        const int k = (int)fminf(fmaxf(level - ref[j] - kMantissaUp, -14.f), 15.f);
+        const int k = (int)fminf(fmaxf(level - ref[j], -14.f), kFactor);
         ptx::sts16(row_c + ((block0 + j) * HC + row) * 2, ref[j] == ref[j] ? (uint16_t)((15 + k) << 10) : 0);   // 2^k
       }
       __syncwarp();
@@ -1078,7 +1083,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
       const __half2 dither = __float2half2_rn((float)(2 * (int)(__brev(tok) >> 25) - 127) * (0x1p-17f / C::kLoUp));
 #pragma unroll 1
       for (int b = 0; b < 4; ++b) {
-        const __half2 m = __float2half2_rn(rot.x * (down * (float)(1 << kMantissaUp)));
+        const __half2 m = __float2half2_rn(rot.x * down);
         rot = make_float4(rot.y, rot.z, rot.w, rot.x);
         uint32_t hi[HC / 4], lo[HC / 4];
 #pragma unroll

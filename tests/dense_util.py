@@ -6,6 +6,11 @@ from oracle import dense_oracle
 
 # A weight times its block's scale: two E4M3 terms of 4 bits each (2^-9 of it), after four roundings to fp16 (2^-11 each).
 WEIGHT = 2.0 ** -8
+# fp16's least step, 2^-24, where the row's largest product of weight and scale is at least 2^1.75 (the window's lower end
+# less 2^4 for A): half of it, for a weight (times a mantissa below 2), a mantissa (for weights below the largest product)
+# and their product: 2^-25.75 + 2^-25 + 2^-26.75.  A reference is at most 2^-16.75 of the largest operand, with steps of
+# 2^-9 and as much for the offset: 2^-25.75.  Together below 2^-23.5.
+LEAST = 2.0 ** -23.5
 
 
 def floor_of(rows: int) -> float:
@@ -17,7 +22,7 @@ def floor_of(rows: int) -> float:
 def check_weights(out, lse, q, cache, bt, lens, sm_scale, rows):
     """Element by element, and by the root mean square over each block's 128 dims."""
     ref, rl, worst, sigma, e = dense_oracle.dense_errors(bits(q).reshape(q.shape), cache.cpu().numpy(), bt.cpu().numpy(),
-                                                         lens.cpu().numpy(), sm_scale, WEIGHT, floor_of(rows))
+                                                         lens.cpu().numpy(), sm_scale, WEIGHT, floor_of(rows), LEAST)
     got, gl = out.float().cpu().double().numpy(), lse.cpu().double().numpy()
     full = np.isfinite(rl)
     assert np.array_equal(np.isneginf(gl), ~full) and np.all(got[~full] == 0.0)

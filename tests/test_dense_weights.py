@@ -179,3 +179,41 @@ def test_negative_scales():
     sc[:, ::3, 1:3] *= -1
     _put_scales(cache, sc)
     _check(q, cache, bt, lens)
+
+
+@pytest.mark.parametrize("n", [1, 2, 90])
+@pytest.mark.parametrize("power", [18, 20, 22])
+def test_blocks_of_very_small_scale(power, n):
+    # beyond what a factor between two blocks' references can hold: fewer bits, but the right size.  (Off by at most
+    # 2^-23.5 of the row's largest operand; scales of ordinary records differ by less than 2^4 among themselves.)
+    q, cache, bt, lens = make_dense([n], 64, seed=power, poison=False)
+    sc = _scales(cache)
+    sc[..., 1] *= 2.0 ** -power
+    sc[..., 2] *= 2.0 ** (6 - power)
+    _put_scales(cache, sc)
+    _check(q, cache, bt, lens, worst_block=2.0 ** (power - 19.5) if power < 19 else None)
+
+
+def test_block_scales_that_spread_over_time():
+    # block 0 grows by 2^26 over the tiles while the others stay: their references have to follow its weights
+    n = 128 * 14
+    q, cache, bt, lens = make_dense([n], 64, seed=3, poison=False)
+    _rope_scores(q, cache, bt, [0.0] * n)
+    sc = _scales(cache)
+    for i in range(bt.shape[1]):
+        sc[int(bt[0, i]), :, 0] *= 2.0 ** (i - 10)
+    _put_scales(cache, sc)
+    for rows, wide in _every_row_group(q, cache, bt).items():
+        out, lse, err = _run(q, cache, wide, lens, 1.0)
+        check_weights(out, lse, q, cache, bt, lens, 1.0, rows)
+
+
+def test_a_context_of_zero_latents_alone():
+    q, cache, bt, lens = make_dense([200, 3], 64, seed=4, poison=False)
+    cache[..., :512] = 0
+    _put_scales(cache, torch.ones_like(_scales(cache)))
+    ref = dense_oracle.dense_decode(bits(q).reshape(q.shape), cache.numpy(), bt.numpy(), lens.numpy(), SCALE)
+    for wide in _every_row_group(q, cache, bt).values():
+        out, lse, err = _run(q, cache, wide, lens)
+        # (such positions' scores are rounded beside an exponent of 60: 2^-19 in units of log2)
+        assert err == 0 and not out.any() and np.abs(lse.cpu().numpy() - ref[1]).max() <= ref[4].max() + 2.0 ** -18
