@@ -265,6 +265,8 @@ typedef struct smla_norm_append_dims {
  * latent, rotation of the rope part, FP8 quantisation and the record write in
  * one pass.  For token i at position t = positions[i] of request r:
  *   n_d    = latent_d / sqrt(mean_d latent_d^2 + eps) * norm_weight_d     (fp32)
+ *            (a row whose squares sum past fp32, beyond 1e19, has n = 0; with
+ *            eps = 0 a row below 1e-19 has no norm in fp32)
  *   scale_j = fp32(amax_j / 448) of n as in sparse_mla_kv_append,
  *   code_d  = E4M3(n_d / scale_{d / 128}), round to nearest even, saturating
  *            (n is not rounded to 16 bits before it is quantised);
@@ -313,7 +315,8 @@ typedef struct smla_norm_rope_dims {
  *   out = n with the dims [rope_offset, rope_offset + rope_dim) rotated in
  *         pairs (a, b) -> (a c - b s, a s + b c), c = cos_sin[p][j],
  *         s = cos_sin[p][rope_dim / 2 + j] for pair j and p = positions[t].
- * All in fp32, rounded once to dtype.
+ * All in fp32, rounded once to dtype (rows whose squares leave fp32 as in
+ * sparse_mla_kv_norm_append).
  *   x, out   dtype, element aligned, strides in elements (non-negative); out
  *            may be x with equal strides (in place), else must not overlap it,
  *            and the rows of out must not overlap one another

@@ -42,8 +42,8 @@
 // follow one another: scores 1600 (with the waits for them), scales and rope 550, maxima 1200 (an SM reduces a value over a
 // warp in 0.8 cycles: 1024 of them are 820), exchange 700, weights 350, operands 1400, their stores 900 (and 600 of waits
 // for the PV, whose K slots come free one by one for the next tile's blocks).  Measured, 32 requests x 32768 positions: 64
-// heads 240 us (2.9 TB/s), 32 heads 155 us (4.4 TB/s), 16 heads 124 us (5.5 TB/s); 1 x 8192 positions of 64 heads 19 us, 1
-// x 77 of 16 heads 9.7 us.
+// heads 241 us (2.9 TB/s), 32 heads 153 us (4.5 TB/s), 16 heads 126 us (5.5 TB/s); 1 x 8192 positions of 64 heads 19 us, 1
+// x 77 of 16 heads 9.8 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -64,7 +64,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kTopOperand = 8.75f;      // a (row, block)'s largest operand is at most 2^8.75, within E4M3's 448
 constexpr float kWindow = 8.f;            // a reference moves when a tile's largest operand would lie further below that
 constexpr float kLowest = 30.f;           // how far below its highest value a reference may go
-constexpr float kAbove = 6.f;             // A is at most so far below the highest R: weights times m_b stay below 2^14.75, in fp16
+constexpr float kAbove = 6.f;             // A is at most so far below the highest R: w m_b stay below 2^14.75, in fp16
 constexpr float kSlack = 4.f;             // and moves when it is less far by more than this
 constexpr float kFactor = 15.f;           // no R is further below A than this: 2^(A - R) stays in fp16
 constexpr int kLeastExponent = -60;       // of the scale that a position counts with
@@ -1138,9 +1138,10 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
 
 // The line that is shared out: each item is kStart units and then its tiles.  A CTA that goes on to a further item spends
 // about two tiles' time on it (the item's rows read, the last one's results written, the pipeline filled again), so its
-// run is shorter by as much; while not every CTA has a tile, nothing is set aside.  Measured with tiles alone / with
-// starts of 1 / 2 / 3 tiles: 18 requests x 8192 positions of 64 heads 64.1 / 60.2 / 57.2 / 57.4 us, 96 ragged requests of
-// 16 heads 80.5 / 77.0 / 73.8 / 73.7, 40 x 8192 of 32 heads 63.0 / 60.8 / 59.3 / 59.5.
+// run is shorter by as much; while not every CTA has a tile, nothing is set aside.  Measured, when tiles took less (1.9, 2.5
+// and 3.6 us for 16, 32 and 64 rows), with tiles alone / with starts of 1 / 2 / 3 tiles: 18 requests x 8192 positions of 64
+// heads 64.1 / 60.2 / 57.2 / 57.4 us, 96 ragged requests of 16 heads 80.5 / 77.0 / 73.8 / 73.7, 40 x 8192 of 32 heads 63.0 /
+// 60.8 / 59.3 / 59.5.
 constexpr int kStart = 2;
 
 // This CTA's run: the units [a, e) of the line, for T tiles and n items.
@@ -1362,9 +1363,9 @@ __device__ __forceinline__ void store_joined(const DenseParams& p, size_t row, i
 // c + 1 .. c1.  Every CTA lists those items from the run descriptors, in the same order, and takes its share of their
 // (row, 128 dims).  Bound by the latency of the partials (in L2): an item of few parts, of which a batch has many,
 // takes one warp, all its loads in flight at once and no barrier; in one of many parts (a single long request) four
-// warps share the parts.  Measured, whole calls with four warps / one warp: 32 x 2048 positions of 64 heads (6 parts) 62 /
-// 50 us, 10 x 8192 of 64 heads (16 parts) 42.3 / 38.5 us, 10 x 8192 of 16 heads 23.1 / 24.8 us; of 64 parts and more one
-// warp would take its loads in eight rounds.
+// warps share the parts.  Measured, whole calls with four warps / one warp (the decode itself took less then): 32 x 2048
+// positions of 64 heads (6 parts) 62 / 50 us, 10 x 8192 of 64 heads (16 parts) 42.3 / 38.5 us, 10 x 8192 of 16 heads 23.1 /
+// 24.8 us; of 64 parts and more one warp would take its loads in eight rounds.
 // This grid is resident while the decode's still writes, so partials are read from L2, not through the read-only path.
 __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const DenseParams p, const RunDesc* descs,
                                                                     const float* lse_part, const float* o_part) {

@@ -81,7 +81,9 @@ __device__ __forceinline__ void load_weights(const void* w, int at, int weight_d
 }
 
 constexpr int kNormAppendWarps = 4;
-constexpr int kNormAppendBlocksPerSm = 6;   // resident at once (80 registers; 5: 27.7 us, 7: 26.6)
+// Resident at once.  65521 tokens / 32 tokens with 6 (80 registers) 27.7 / 2.79 us, with 7 (72) 26.6 / 2.95: the small call, a
+// step's, weighs more; with 5 the large one takes 6 % longer.
+constexpr int kNormAppendBlocksPerSm = 6;
 
 // Half a warp per token (two tokens per warp).  Lane l of a half takes
 // dims 8 l .. 8 l + 7 of each 128-dim block, so every access of the warp is contiguous and a block's amax is a
