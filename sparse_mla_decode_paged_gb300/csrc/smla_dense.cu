@@ -646,11 +646,11 @@ __device__ __noinline__ uint32_t zero_blocks(uint32_t base, int slot, int tok, u
       const uint32_t at = base + C::kK + slot * kSlot;
       uint32_t any = 0;
 #pragma unroll 1
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < 8 && any == 0; ++u) {
         const uint4 v = ptx::lds128(at + swz128(tok, u));
-        any |= v.x | v.y | v.z | v.w;
+        any = (v.x | v.y | v.z | v.w) & 0x7f7f7f7fu;
       }
-      if (any & 0x7f7f7f7fu) maybe &= ~(1u << b);
+      if (any) maybe &= ~(1u << b);
     }
     if (++slot == C::kRing) slot = 0;
   }
