@@ -416,6 +416,88 @@ int sparse_mla_dense_decode(const smla_dense_dims* dims, const void* q, const vo
                             const int32_t* block_table, const int32_t* seq_lens, float sm_scale, void* out,
                             float* lse, void* workspace, size_t workspace_bytes, smla_stream_t stream);
 
+/* Shapes of one attention-weight call. */
+typedef struct smla_weights_dims {
+  int32_t batch;              /* B decode queries, 0 .. 65535                            */
+  int32_t num_heads;          /* H, 1 .. 128                                             */
+  int32_t page_size;          /* tokens per page; must be 64                             */
+  int32_t max_pages_per_seq;  /* row length of block_table, >= 1                         */
+  int32_t d_latent;           /* must be 512                                             */
+  int32_t d_rope;             /* must be 64                                              */
+  int64_t num_pages;          /* pages in kv_cache, 1 .. 2^31 - 1                        */
+  int32_t queries_per_request;/* as in smla_dense_dims                                   */
+  int32_t num_cols;           /* positions per row of weights, 0 .. 2^30                 */
+  int64_t weights_stride;     /* elements between rows of weights, >= num_cols           */
+} smla_weights_dims;
+
+/* Attention weights accumulated per cached position, from the lse that a
+ * decode of the same queries returned:
+ *   weights[r][t] = decay * weights[r][t]
+ *                   + sum_{b, h} exp(sm_scale * q[b][h].k_t - lse[b][h])
+ * over the queries b of request r and their heads with t < seq_lens[b], for
+ * every t below the longest of the request's lengths; later entries are left
+ * as they are.  decay 0 overwrites (nothing is read).  The sums have a fixed
+ * order: the result does not depend on timing.
+ *   q, kv_cache, block_table, seq_lens  as in sparse_mla_dense_decode
+ *   lse       float32 [B][H]; weights float32 [B / s_q][weights_stride] (written)
+ *   err_word  device uint32 (may be NULL): lengths above num_cols or the block
+ *             table are clamped and set SMLA_DEVERR_LEN_RANGE; positions whose page
+ *             is outside the cache add nothing and set SMLA_DEVERR_PAGE_RANGE.
+ * Scores as in sparse_mla_dense_decode; weights and sums in fp32.
+ * SMLA_ERR_INVALID_ARG for null or misaligned pointers, bad shapes or a decay
+ * that is negative or not finite, SMLA_ERR_UNSUPPORTED for shapes outside the stated
+ * ranges, SMLA_ERR_CUDA if the launch fails.  Asynchronous on `stream`. */
+int sparse_mla_attention_weights(const smla_weights_dims* dims, const void* q, const void* kv_cache,
+                                 const int32_t* block_table, const int32_t* seq_lens, const float* lse, float sm_scale,
+                                 float decay, float* weights, uint32_t* err_word, smla_stream_t stream);
+
+/* Shapes and rules of one eviction call. */
+typedef struct smla_evict_dims {
+  int32_t num_requests;       /* R, 0 .. 65535                                           */
+  int32_t num_cols;           /* slots per row of weights and positions, 1 .. 2^30       */
+  int32_t page_size;          /* tokens per page; must be 64                             */
+  int32_t max_pages_per_seq;  /* row length of block_table, >= 1                         */
+  int32_t d_latent;           /* must be 512                                             */
+  int32_t d_rope;             /* must be 64                                              */
+  int64_t num_pages;          /* pages in kv_cache, 1 .. 2^31 - 1                        */
+  int64_t weights_stride, positions_stride;  /* elements between rows, >= num_cols       */
+  int32_t keep;               /* records a request keeps, >= 0 (without a keep array)    */
+  int32_t sinks, recent;      /* held positions, >= 0: see below                         */
+} smla_evict_dims;
+
+/* Bytes of workspace that sparse_mla_kv_evict needs (host only). */
+size_t sparse_mla_kv_evict_workspace_size(const smla_evict_dims* dims);
+
+/* Eviction from the paged cache, in place.  Request r has n = seq_lens[r]
+ * records in slots 0 .. n - 1 of its block-table row, slot t holding the token
+ * of position positions[r][t] (any order).  Held are the slots with
+ * positions[r][t] < sinks or >= next_positions[r] - recent.  It keeps
+ *   m = min(n, max(keep, held slots))
+ * records: the held ones, then those of largest weights[r][t], ranked by IEEE
+ * 754 totalOrder, equal patterns by the lower slot.  Kept records in slots >=
+ * m move, in increasing order, to the free slots below m, in increasing
+ * order, with their weights and positions; weights of the slots m .. n - 1
+ * become 0, everything else stays as it is, and new_lens[r] = m (the length that
+ * the next calls take).
+ *   weights   float32, positions int32 [R][stride] (both written)
+ *   next_positions, seq_lens int32 [R]; keep int32 [R] or NULL (negative
+ *             entries count as 0); new_lens int32 [R] (written; may be
+ *             seq_lens itself)
+ *   kv_cache, block_table  as in sparse_mla_decode; a request's pages must
+ *             be its own (a page in two rows would be written by both)
+ *   workspace sparse_mla_kv_evict_workspace_size bytes, 256-byte aligned; not
+ *             shared by concurrent calls
+ *   err_word  device uint32 (may be NULL): lengths above num_cols or the block
+ *             table are clamped and set SMLA_DEVERR_LEN_RANGE; a move from or to a page
+ *             outside the cache leaves the record and sets SMLA_DEVERR_PAGE_RANGE.
+ * SMLA_ERR_INVALID_ARG for null or misaligned pointers and bad shapes,
+ * SMLA_ERR_UNSUPPORTED for shapes outside the stated ranges,
+ * SMLA_ERR_WORKSPACE, SMLA_ERR_CUDA.  Asynchronous on `stream`. */
+int sparse_mla_kv_evict(const smla_evict_dims* dims, float* weights, int32_t* positions, const int32_t* next_positions,
+                        const int32_t* seq_lens, const int32_t* keep, void* kv_cache, const int32_t* block_table,
+                        int32_t* new_lens, void* workspace, size_t workspace_bytes, uint32_t* err_word,
+                        smla_stream_t stream);
+
 /* Shapes of one top-k selection call. */
 typedef struct smla_topk_dims {
   int32_t batch;          /* queries (rows of scores), >= 0                               */

@@ -48,6 +48,20 @@ class SmlaDensePlan(C.Structure):
                 ("reserved", C.c_int32), ("workspace_bytes", C.c_size_t)]
 
 
+class SmlaWeightsDims(C.Structure):
+    _fields_ = [("batch", C.c_int32), ("num_heads", C.c_int32), ("page_size", C.c_int32),
+                ("max_pages_per_seq", C.c_int32), ("d_latent", C.c_int32), ("d_rope", C.c_int32),
+                ("num_pages", C.c_int64), ("queries_per_request", C.c_int32), ("num_cols", C.c_int32),
+                ("weights_stride", C.c_int64)]
+
+
+class SmlaEvictDims(C.Structure):
+    _fields_ = [("num_requests", C.c_int32), ("num_cols", C.c_int32), ("page_size", C.c_int32),
+                ("max_pages_per_seq", C.c_int32), ("d_latent", C.c_int32), ("d_rope", C.c_int32),
+                ("num_pages", C.c_int64), ("weights_stride", C.c_int64), ("positions_stride", C.c_int64),
+                ("keep", C.c_int32), ("sinks", C.c_int32), ("recent", C.c_int32)]
+
+
 class SmlaTopkDims(C.Structure):
     _fields_ = [("batch", C.c_int32), ("num_cols", C.c_int32), ("row_stride", C.c_int64), ("k", C.c_int32),
                 ("cluster_ctas", C.c_int32)]
@@ -74,6 +88,10 @@ _SIGS = {
     "sparse_mla_dense_plan": (C.c_int, [C.POINTER(SmlaDenseDims), C.c_int32, C.POINTER(SmlaDensePlan)]),
     "sparse_mla_dense_decode": (C.c_int, [C.POINTER(SmlaDenseDims), _P, _P, _P, _P, C.c_float, _P, _P, _P,
                                           C.c_size_t, _P]),
+    "sparse_mla_attention_weights": (C.c_int, [C.POINTER(SmlaWeightsDims), _P, _P, _P, _P, _P, C.c_float, C.c_float, _P,
+                                               _P, _P]),
+    "sparse_mla_kv_evict_workspace_size": (C.c_size_t, [C.POINTER(SmlaEvictDims)]),
+    "sparse_mla_kv_evict": (C.c_int, [C.POINTER(SmlaEvictDims), _P, _P, _P, _P, _P, _P, _P, _P, _P, C.c_size_t, _P, _P]),
     "sparse_mla_topk_select": (C.c_int, [C.POINTER(SmlaTopkDims), _P, _P, _P, _P, _P]),
     "sparse_mla_topk_plan_for": (C.c_int, [C.POINTER(SmlaTopkDims), C.c_int32, C.POINTER(C.c_int32),
                                          C.POINTER(C.c_int32)]),

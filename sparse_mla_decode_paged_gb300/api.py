@@ -11,8 +11,8 @@ from typing import Optional, Tuple
 import torch
 
 from . import _native
-from ._native import (SmlaAppendDims, SmlaDenseDims, SmlaDensePlan, SmlaDims, SmlaNormAppendDims, SmlaNormRopeDims,
-                      SmlaPlan, SmlaTopkDims, check)
+from ._native import (SmlaAppendDims, SmlaDenseDims, SmlaDensePlan, SmlaDims, SmlaEvictDims, SmlaNormAppendDims,
+                      SmlaNormRopeDims, SmlaPlan, SmlaTopkDims, SmlaWeightsDims, check)
 
 PAGE_SIZE, D_LATENT, D_ROPE, D_QK = 64, 512, 64, 576
 
@@ -568,6 +568,145 @@ def sparse_mla_dense_decode(q: torch.Tensor, kv_cache: torch.Tensor, block_table
     if r != 0:
         check("sparse_mla_dense_decode", r)
     return out, lse
+
+
+def _need_slots(t, name: str, dtype, rows: int):
+    """[rows, n] of dtype with unit stride in a row and rows that do not overlap."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or t.dtype != dtype:
+        raise TypeError(f"{name} must be a {dtype} CUDA tensor")
+    if t.dim() != 2 or t.shape[0] != rows or (t.shape[1] > 1 and t.stride(1) != 1) or \
+            (rows > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name} must be [{rows},n] with unit stride in a row and rows that do not overlap")
+
+
+def sparse_mla_attention_weights(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.Tensor,
+                                 seq_lens: torch.Tensor, lse: torch.Tensor, sm_scale: float, weights: torch.Tensor,
+                                 decay: float = 1.0, err_word: Optional[torch.Tensor] = None,
+                                 stream=None) -> torch.Tensor:
+    """weights[r, t] = decay * weights[r, t] + the softmax weights that request r's queries and heads give position t, for
+    t below the longest of its lengths; returns weights (fp32 [R, n], rows may be strided, written in place).
+
+    q [B,H,576], kv_cache, block_table [R, pages], seq_lens [B] as in sparse_mla_dense_decode, lse fp32 [B,H] what that
+    call returned.  decay 0 overwrites."""
+    key = _call_key((q, kv_cache, block_table, seq_lens, lse, weights, err_word), "attention_weights")
+    dims = _CHECKED.get(key) or _remember(key, _weights_dims(q, kv_cache, block_table, seq_lens, lse, weights, err_word))
+    with _on(q.device, stream) as st:
+        r = _lib().sparse_mla_attention_weights(dims, q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(),
+                                                seq_lens.data_ptr(), lse.data_ptr(), sm_scale, decay, weights.data_ptr(),
+                                                _ptr(err_word), st)
+    if r != 0:
+        check("sparse_mla_attention_weights", r)
+    return weights
+
+
+def _need_queries(q, kv_cache, block_table, seq_lens) -> int:
+    """Checks of what every call over whole contexts takes; the queries per request."""
+    _need(q, "q", torch.bfloat16, 3)
+    _need(kv_cache, "kv_cache", torch.uint8, 3)
+    _need(block_table, "block_table", torch.int32, 2)
+    _need(seq_lens, "seq_lens", torch.int32, 1)
+    B, R = q.shape[0], block_table.shape[0]
+    if q.shape[2] != D_QK or kv_cache.shape[1] != PAGE_SIZE or kv_cache.shape[2] != 656:
+        raise ValueError("q must be [B,H,576] and kv_cache [pages,64,656]")
+    if R < 1 or B % R != 0 or seq_lens.shape[0] != B:
+        raise ValueError("q and seq_lens need one row per query, block_table one row per request (a divisor of "
+                         "the query count)")
+    return B // R
+
+
+def _weights_dims(q, kv_cache, block_table, seq_lens, lse, weights, err_word) -> SmlaWeightsDims:
+    s_q = _need_queries(q, kv_cache, block_table, seq_lens)
+    _need(lse, "lse", torch.float32, 2)
+    if lse.shape != q.shape[:2]:
+        raise ValueError("lse must be [B,H]")
+    R = block_table.shape[0]
+    _need_slots(weights, "weights", torch.float32, R)
+    _same_device(q.device, kv_cache=kv_cache, block_table=block_table, seq_lens=seq_lens, lse=lse, weights=weights)
+    _err_word(err_word, q.device)
+    n = weights.shape[1]
+    return SmlaWeightsDims(q.shape[0], q.shape[1], PAGE_SIZE, block_table.shape[1], D_LATENT, D_ROPE, kv_cache.shape[0],
+                           s_q, n, weights.stride(0) if R > 1 else n)
+
+
+def alloc_evict_workspace(weights: torch.Tensor) -> torch.Tensor:
+    """Caller-owned workspace of sparse_mla_kv_evict for weights of this shape."""
+    d = SmlaEvictDims(num_requests=weights.shape[0], num_cols=weights.shape[1])
+    return torch.empty(int(_lib().sparse_mla_kv_evict_workspace_size(d)), dtype=torch.uint8, device=weights.device)
+
+
+def sparse_mla_kv_evict(weights: torch.Tensor, positions: torch.Tensor, next_positions: torch.Tensor,
+                        seq_lens: torch.Tensor, keep, kv_cache: torch.Tensor, block_table: torch.Tensor, sinks: int = 0,
+                        recent: int = 0, new_lens: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, err_word: Optional[torch.Tensor] = None,
+                        stream=None) -> torch.Tensor:
+    """Cuts every request's cache to `keep` records (an int, or int32 [R]) in place and returns the new lengths int32 [R]
+    (new_lens, which may be seq_lens itself).
+
+    weights fp32 and positions int32 [R, n] (rows may be strided) hold each slot's accumulated weight and its token's
+    position, in any order.  Positions below `sinks` and the `recent` ones before next_positions [R] stay, then the
+    largest weights (IEEE totalOrder, ties to the lower slot).  Records kept in slots past the new length move to the
+    free slots before it, with their weights and positions; the weights behind it become 0.  A request's pages must be
+    its own.  Calls in flight at once need a workspace each (alloc_evict_workspace)."""
+    key = _call_key((weights, positions, next_positions, seq_lens, kv_cache, block_table, new_lens, err_word,
+                     keep if isinstance(keep, torch.Tensor) else None), "kv_evict", sinks, recent,
+                    None if isinstance(keep, torch.Tensor) else keep)
+    dims = _CHECKED.get(key) or _remember(key, _evict_dims(weights, positions, next_positions, seq_lens, keep, kv_cache,
+                                                           block_table, sinks, recent, new_lens, err_word))
+    with _on(weights.device, stream) as st:
+        if new_lens is None:
+            new_lens = torch.empty(seq_lens.shape, dtype=torch.int32, device=weights.device)
+        if workspace is None:
+            workspace = alloc_evict_workspace(weights)
+        else:
+            _need(workspace, "workspace", torch.uint8, 1)
+            _same_device(weights.device, workspace=workspace)
+        r = _lib().sparse_mla_kv_evict(
+            dims, weights.data_ptr(), positions.data_ptr(), next_positions.data_ptr(), seq_lens.data_ptr(),
+            keep.data_ptr() if isinstance(keep, torch.Tensor) else None, kv_cache.data_ptr(), block_table.data_ptr(),
+            new_lens.data_ptr(), workspace.data_ptr(), workspace.numel(), _ptr(err_word), st)
+    if r != 0:
+        check("sparse_mla_kv_evict", r)
+    return new_lens
+
+
+def _whole(value, name: str) -> int:
+    """A whole number of at most 2^31 - 1, 0 or more."""
+    if isinstance(value, bool) or not isinstance(value, int):
+        raise TypeError(f"{name} must be an int")
+    if not 0 <= value < 1 << 31:
+        raise ValueError(f"{name} must be in [0, 2^31)")
+    return value
+
+
+def _evict_dims(weights, positions, next_positions, seq_lens, keep, kv_cache, block_table, sinks, recent, new_lens,
+                err_word) -> SmlaEvictDims:
+    _need(block_table, "block_table", torch.int32, 2)
+    _need(kv_cache, "kv_cache", torch.uint8, 3)
+    if kv_cache.shape[1] != PAGE_SIZE or kv_cache.shape[2] != 656:
+        raise ValueError("kv_cache must be [pages,64,656]")
+    R = block_table.shape[0]
+    _need_slots(weights, "weights", torch.float32, R)
+    _need_slots(positions, "positions", torch.int32, R)
+    if weights.shape != positions.shape or weights.shape[1] < 1:
+        raise ValueError("weights and positions must have one shape [R,n]")
+    per_request = {"next_positions": next_positions, "seq_lens": seq_lens}
+    if isinstance(keep, torch.Tensor):
+        per_request["keep"] = keep
+    if new_lens is not None:
+        per_request["new_lens"] = new_lens
+    for name, t in per_request.items():
+        _need(t, name, torch.int32, 1)
+        if t.shape[0] != R:
+            raise ValueError(f"{name} must be [R]")
+    _same_device(weights.device, kv_cache=kv_cache, block_table=block_table, positions=positions, **per_request)
+    _err_word(err_word, weights.device)
+    n = weights.shape[1]
+    return SmlaEvictDims(R, n, PAGE_SIZE, block_table.shape[1], D_LATENT, D_ROPE, kv_cache.shape[0],
+                         weights.stride(0) if R > 1 else n, positions.stride(0) if R > 1 else n,
+                         0 if isinstance(keep, torch.Tensor) else _whole(keep, "keep"), _whole(sinks, "sinks"),
+                         _whole(recent, "recent"))
 
 
 def sparse_mla_topk_select(scores: torch.Tensor, seq_lens: torch.Tensor, k: int, cluster_ctas: int = 0,

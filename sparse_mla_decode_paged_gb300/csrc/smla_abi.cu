@@ -532,3 +532,109 @@ extern "C" const char* sparse_mla_status_string(int status) {
     default: return "unknown status";
   }
 }
+
+extern "C" int sparse_mla_attention_weights(const smla_weights_dims* d, const void* q, const void* kv_cache,
+                                            const int32_t* block_table, const int32_t* seq_lens, const float* lse,
+                                            float sm_scale, float decay, float* weights, uint32_t* err_word,
+                                            smla_stream_t stream) {
+  if (!d) return SMLA_ERR_INVALID_ARG;
+  const int sq = d->queries_per_request > 1 ? d->queries_per_request : 1;
+  if (d->batch < 0 || d->num_heads < 1 || d->max_pages_per_seq < 1 || d->num_pages < 1 || d->queries_per_request < 0 ||
+      d->batch % sq != 0 || d->num_cols < 0 || !(decay >= 0.f && decay <= 3.0e38f))
+    return SMLA_ERR_INVALID_ARG;
+  const int requests = d->batch / sq;
+  if (requests > 1 && d->weights_stride < d->num_cols) return SMLA_ERR_INVALID_ARG;
+  if (d->page_size != kPageSize || d->d_latent != kDLatent || d->d_rope != kDRope) return SMLA_ERR_UNSUPPORTED;
+  // a CTA counts its tiles, and a request its positions, in 32 bits
+  if (d->batch > kMaxBatch || d->num_heads > kDenseMaxHeads || d->num_pages > 0x7fffffff || d->num_cols > kMaxCols)
+    return SMLA_ERR_UNSUPPORTED;
+  if (d->batch > 0 && d->num_cols > 0) {
+    const int st = check_inputs(q, kv_cache, block_table, seq_lens, seq_lens);
+    if (st != SMLA_OK) return st;
+    if (!lse || !weights || !aligned(lse, 4) || !aligned(weights, 4)) return SMLA_ERR_INVALID_ARG;
+  }
+  if (err_word && !aligned(err_word, 4)) return SMLA_ERR_INVALID_ARG;
+  if (d->batch == 0 || d->num_cols == 0) return SMLA_OK;
+  int sms = 0;
+  const int st = sm_count_of_current_device(&sms);
+  if (st != SMLA_OK) return st;
+  if ((int64_t)requests * ((d->num_cols + kDenseTile - 1) / kDenseTile) / sms >= 0x7fffffff) return SMLA_ERR_UNSUPPORTED;
+  WeightsParams p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.kv = static_cast<const uint8_t*>(kv_cache);
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.lse = lse;
+  p.weights = weights;
+  p.sm_scale = sm_scale;
+  p.decay = decay;
+  p.H = d->num_heads;
+  p.q_per_req = sq;
+  p.requests = requests;
+  p.max_pages = d->max_pages_per_seq;
+  p.cols = d->num_cols;
+  p.num_pages = d->num_pages;
+  p.weights_stride = d->weights_stride;
+  p.err = err_word;
+  p.wait_ns = split_wait_limit_ns();
+  return launch_weights(p, sms, (cudaStream_t)stream) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+}
+
+namespace {
+// Records of a request that can move at most (half of its slots), and the workspace's parts.
+int evict_list_len(const smla_evict_dims* d) { return d->num_cols / 2 + 1; }
+size_t evict_moved_bytes(const smla_evict_dims* d) { return ((size_t)d->num_requests * 4 + 255) / 256 * 256; }
+}  // namespace
+
+extern "C" size_t sparse_mla_kv_evict_workspace_size(const smla_evict_dims* d) {
+  if (!d || d->num_requests < 0 || d->num_cols < 0) return 0;
+  return evict_moved_bytes(d) + (size_t)d->num_requests * 2 * evict_list_len(d) * 4;
+}
+
+extern "C" int sparse_mla_kv_evict(const smla_evict_dims* d, float* weights, int32_t* positions,
+                                   const int32_t* next_positions, const int32_t* seq_lens, const int32_t* keep,
+                                   void* kv_cache, const int32_t* block_table, int32_t* new_lens, void* workspace,
+                                   size_t workspace_bytes, uint32_t* err_word, smla_stream_t stream) {
+  if (!d) return SMLA_ERR_INVALID_ARG;
+  if (d->num_requests < 0 || d->num_cols < 1 || d->max_pages_per_seq < 1 || d->num_pages < 1 || d->sinks < 0 ||
+      d->recent < 0 || (!keep && d->keep < 0))
+    return SMLA_ERR_INVALID_ARG;
+  if (d->num_requests > 1 && (d->weights_stride < d->num_cols || d->positions_stride < d->num_cols))
+    return SMLA_ERR_INVALID_ARG;
+  if (d->page_size != kPageSize || d->d_latent != kDLatent || d->d_rope != kDRope) return SMLA_ERR_UNSUPPORTED;
+  if (d->num_requests > kMaxBatch || d->num_cols > kMaxCols || d->num_pages > 0x7fffffff) return SMLA_ERR_UNSUPPORTED;
+  if (err_word && !aligned(err_word, 4)) return SMLA_ERR_INVALID_ARG;
+  if (d->num_requests == 0) return SMLA_OK;
+  if (!weights || !positions || !next_positions || !seq_lens || !kv_cache || !block_table || !new_lens ||
+      !aligned(weights, 4) || !aligned(positions, 4) || !aligned(next_positions, 4) || !aligned(seq_lens, 4) ||
+      !aligned(kv_cache, 16) || !aligned(block_table, 4) || !aligned(new_lens, 4) || (keep && !aligned(keep, 4)))
+    return SMLA_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < sparse_mla_kv_evict_workspace_size(d))
+    return SMLA_ERR_WORKSPACE;
+  int sms = 0;
+  const int st = sm_count_of_current_device(&sms);
+  if (st != SMLA_OK) return st;
+  EvictParams p{};
+  p.weights = weights;
+  p.positions = positions;
+  p.next_positions = next_positions;
+  p.seq_lens = seq_lens;
+  p.keep = keep;
+  p.kv = static_cast<uint8_t*>(kv_cache);
+  p.block_table = block_table;
+  p.new_lens = new_lens;
+  p.num_pages = d->num_pages;
+  p.weights_stride = d->weights_stride;
+  p.positions_stride = d->positions_stride;
+  p.requests = d->num_requests;
+  p.cols = d->num_cols;
+  p.max_pages = d->max_pages_per_seq;
+  p.keep_all = d->keep;
+  p.sinks = d->sinks;
+  p.recent = d->recent;
+  p.list_len = evict_list_len(d);
+  p.moved = static_cast<int32_t*>(workspace);
+  p.lists = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + evict_moved_bytes(d));
+  p.err = err_word;
+  return launch_evict(p, sms, (cudaStream_t)stream) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+}

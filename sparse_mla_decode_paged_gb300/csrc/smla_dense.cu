@@ -51,6 +51,7 @@
 #include <atomic>
 #include <cstddef>
 
+#include "smla_dense_parts.cuh"
 #include "smla_device.cuh"
 #include "smla_internal.h"
 #include "smla_ptx.cuh"
@@ -59,8 +60,6 @@
 namespace smla {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kTopOperand = 8.75f;      // a (row, block)'s largest operand is at most 2^8.75, within E4M3's 448
 constexpr float kWindow = 8.f;            // a reference moves when a tile's largest operand would lie further below that
 constexpr float kLowest = 30.f;           // how far below its highest value a reference may go
@@ -240,33 +239,6 @@ struct Walk {
   }
 };
 
-// A ring position: slot and the parity of its current use.
-template <int N>
-struct Ring {
-  int slot = 0;
-  uint32_t parity = 0;
-  __device__ __forceinline__ void next() {
-    if (++slot == N) {
-      slot = 0;
-      parity ^= 1;
-    }
-  }
-};
-
-// A wait for a slot to be freed (the other parity) passes at once on the ring's first round: an mbarrier that has
-// completed no phase yet reports the phase before its first as complete.
-// A wait of a whole warp, bounded by p.wait_ns.  The common case is one try; once a wait has given up (ok 0) a
-// role runs its loop to the end without arriving or issuing, so that the named barriers of the softmax warps stay
-// matched.  (`ok` passes through an empty asm: otherwise the compiler makes a copy of the rest of the role for
-// each wait that may give up.)
-#define SMLA_WAIT(bar, par)                                                                               \
-  do {                                                                                                    \
-    if (__builtin_expect(__any_sync(0xffffffffu, !ptx::mbar_try_wait((bar), (par))), 0)) {                \
-      if (ok) ok = ptx::mbar_wait_rest((bar), (par), &bars->abort, p.wait_ns);                            \
-      asm volatile("" : "+r"(ok));                                                                        \
-    }                                                                                                     \
-  } while (0)
-
 // ----------------------------------------------------------------------------- copies
 
 __device__ __forceinline__ int page_entry(const DenseParams& p, int req, int max_len, int lp) {
@@ -368,14 +340,6 @@ __device__ void copy_role(const DenseParams& p, const CUtensorMap* map, const CU
     }
     w.next();
   }
-}
-
-// After a wait that gave up: every copy that was armed has to land before the CTA leaves.  Nothing arms a slot
-// again by then, so the slot's last phase is waited for.
-__device__ void drain_copies(uint64_t* bar, const int* armed, int n, int lane) {
-  int never = 0;
-  for (int s = 0; s < n; ++s)
-    if (armed[s] > 0) ptx::mbar_wait_warp(&bar[s], (uint32_t)(armed[s] - 1) & 1u, &never, lane, 100000000ull);
 }
 
 // ----------------------------------------------------------------------------- MMA issue
@@ -498,8 +462,6 @@ __device__ __forceinline__ float reduce_scatter(float (&v)[N], int lane, Op op) 
   return r;
 }
 
-__device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
-
 // Rows of one item into the Q operands: hi and lo E4M3 codes of the latent part scaled by 2^-x, the rope as it is;
 // each row's factor 2^x sm_scale log2 e and length go to buffer `buf`.
 template <int NR>
@@ -545,31 +507,8 @@ __device__ __forceinline__ void load_q(const DenseParams& p, int item, unsigned 
     const int r = warp + C::kSoftWarps * k;
     const uint32_t wds[8] = {raw[k][0].x, raw[k][0].y, raw[k][0].z, raw[k][0].w,
                              raw[k][1].x, raw[k][1].y, raw[k][1].z, raw[k][1].w};
-    float amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(wds[i] << 16)), fabsf(__uint_as_float(wds[i] & 0xffff0000u))));
-#pragma unroll
-    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    // x = floor(log2 amax) - 7, kept where 2^x and 2^-x are normal floats
-    const int x = amax > 0.f ? min(max((int)(__float_as_uint(amax) >> 23) - 127 - 7, -120), 120) : 0;
-    const float down = exp2_int(-x);
     uint32_t hi[4], lo[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint16_t h2[2], l2[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float a = __uint_as_float(wds[2 * i + j] << 16) * down, c = __uint_as_float(wds[2 * i + j] & 0xffff0000u) * down;
-        a = isinf(a) ? CUDART_NAN_F : a;                 // an infinite q makes the row NaN
-        c = isinf(c) ? CUDART_NAN_F : c;
-        h2[j] = f32x2_to_e4m3x2(a, c);
-        const float2 back = f16x2_to_f32x2(e4m3x2_to_f16x2(h2[j]));
-        l2[j] = f32x2_to_e4m3x2(a - back.x, c - back.y);
-      }
-      hi[i] = (uint32_t)h2[0] | ((uint32_t)h2[1] << 16);
-      lo[i] = (uint32_t)l2[0] | ((uint32_t)l2[1] << 16);
-    }
+    const int x = split_q(wds, hi, lo);
     const uint32_t q8 = base + C::kQ8 + b * C::kQ8Chunk;
     ptx::sts128(q8 + swz128(r, u), make_uint4(hi[0], hi[1], hi[2], hi[3]));
     ptx::sts128(q8 + swz128(NR + r, u), make_uint4(lo[0], lo[1], lo[2], lo[3]));
@@ -1499,37 +1438,11 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const DenseP
 constexpr size_t kDescBytes = (kDenseMaxCtas * sizeof(RunDesc) + 255) / 256 * 256;
 size_t lse_part_bytes(int ctas, int nr) { return ((size_t)2 * ctas * nr * sizeof(float) + 255) / 256 * 256; }
 
-typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encoder() {
-  static const EncodeTiled fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<EncodeTiled>(f);
-  }();
-  return fn;
-}
-
-// The cache as [page][record][byte], in boxes of 64 records of one page, `bytes` wide.
-bool encode_map(CUtensorMap* map, const DenseParams& p, uint32_t bytes, CUtensorMapSwizzle swizzle) {
-  const cuuint64_t dims[3] = {kRecordBytes, kPageSize, (cuuint64_t)p.num_pages};
-  const cuuint64_t strides[2] = {kRecordBytes, (cuuint64_t)kRecordBytes * kPageSize};
-  const cuuint32_t box[3] = {bytes, kPageSize, 1}, step[3] = {1, 1, 1};
-  return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(p.kv), dims, strides, box, step,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int NR>
 cudaError_t launch_nr(const DenseParams& p, unsigned char* ws, cudaStream_t stream) {
   CUtensorMap map, smap;
-  if (!encoder() || !encode_map(&map, p, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_map(&smap, p, 16, CU_TENSOR_MAP_SWIZZLE_NONE))
+  if (!encoder() || !encode_map(&map, p.kv, p.num_pages, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_map(&smap, p.kv, p.num_pages, 16, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorNotSupported;
   // the shared-memory attribute belongs to the device's copy of the kernel: set once per device
   static std::atomic<bool> set[64];

@@ -141,6 +141,7 @@ struct ReadParams {
 constexpr int kDenseTile = 128;        // positions per tile (two pages)
 constexpr int kDenseMaxCtas = 1024;
 constexpr int kDenseMaxHeads = 128;
+constexpr int kMaxCols = 1 << 30;      // slots of a request in per-slot arrays
 struct DenseParams {
   const uint16_t* q;          // bf16 [B][H][576]
   const uint8_t* kv;          // [num_pages][64][656]
@@ -159,6 +160,40 @@ struct DenseParams {
   uint64_t wait_ns;           // time limit of each pipeline wait inside the kernel
 };
 
+// Everything the attention-weight kernel needs for one launch.
+struct WeightsParams {
+  const uint16_t* q;          // bf16 [B][H][576]
+  const uint8_t* kv;          // [num_pages][64][656]
+  const int32_t* block_table; // [requests][max_pages]
+  const int32_t* seq_lens;    // [B]
+  const float* lse;           // [B][H]
+  float* weights;             // [requests][cols], rows weights_stride elements apart
+  float sm_scale, decay;
+  int H, q_per_req, requests, max_pages, cols;
+  int64_t num_pages, weights_stride;
+  int groups;                 // row groups per request (set by launch_weights)
+  uint32_t* err;              // device error word (may be null)
+  uint64_t wait_ns;           // time limit of each pipeline wait inside the kernel
+};
+
+// Eviction from the cache: see smla_evict.cu.
+struct EvictParams {
+  float* weights;             // [requests][cols], rows weights_stride elements apart
+  int32_t* positions;         // [requests][cols], rows positions_stride elements apart
+  const int32_t* next_positions;   // [requests]
+  const int32_t* seq_lens;    // [requests]
+  const int32_t* keep;        // [requests], or null: keep_all
+  uint8_t* kv;                // [num_pages][64][656]
+  const int32_t* block_table; // [requests][max_pages]
+  int32_t* new_lens;          // [requests] (may be seq_lens)
+  int64_t num_pages, weights_stride, positions_stride;
+  int requests, cols, max_pages, keep_all, sinks, recent;
+  int32_t* moved;             // workspace: records to move per request
+  int32_t* lists;             // workspace: [requests][2][list_len] free slots, survivors
+  int list_len;
+  uint32_t* err;              // device error word (may be null)
+};
+
 // Kernel launchers (return the launch error).
 cudaError_t launch_split(const SplitParams& p, cudaStream_t stream);
 size_t workspace_bytes_for(int B, int H, int nsplit);
@@ -169,6 +204,8 @@ cudaError_t launch_kv_norm_append(const NormAppendParams& p, cudaStream_t stream
 cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t stream);
 cudaError_t launch_kv_read(const ReadParams& p, cudaStream_t stream);
 cudaError_t launch_dense(const DenseParams& p, cudaStream_t stream);
+cudaError_t launch_weights(const WeightsParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_evict(const EvictParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_gather_rows(const int32_t* bt, const int32_t* topk, const int32_t* seq_lens,
                                int B, int topk_n, int max_pages, int64_t num_pages, int q_per_req,
                                int64_t* rows, cudaStream_t stream);
