@@ -416,6 +416,29 @@ int sparse_mla_dense_decode(const smla_dense_dims* dims, const void* q, const vo
                             const int32_t* block_table, const int32_t* seq_lens, float sm_scale, void* out,
                             float* lse, void* workspace, size_t workspace_bytes, smla_stream_t stream);
 
+/* sparse_mla_dense_decode with scores of another form and positions hidden:
+ *   s_t = sm_scale * q[b][h].k_t
+ *   s_t = softcap * tanh(s_t / softcap)             if softcap > 0
+ *   s_t = s_t + slopes[h] * (t - (seq_lens[b] - 1)) if slopes is not NULL
+ * over the positions t < seq_lens[b] with t >= starts[b] or t <
+ * prefix_lens[b] (all, if starts is NULL): a window with the first tokens kept,
+ * the last of several documents behind a common prefix.  The
+ * query's own position is seq_lens[b] - 1.
+ *   softcap     0 (none) or in [2^-20, 2^20]
+ *   slopes      float32 [H] or NULL
+ *   starts      int32 [B] or NULL; prefix_lens int32 [B] or NULL (only with
+ *               starts); values below 0 or past the length count as those
+ * 128-position tiles that no row of a CTA sees are neither read nor computed,
+ * pages that no query sees may be -1 in the block table.  A capped score is
+ * off by 2^-20 of itself.  Everything else, dims, plan and workspace among it,
+ * as in sparse_mla_dense_decode; with nothing given the results are the same.
+ * SMLA_ERR_INVALID_ARG for a softcap outside its range, prefix_lens without
+ * starts and misaligned pointers. */
+int sparse_mla_masked_decode(const smla_dense_dims* dims, const void* q, const void* kv_cache,
+                             const int32_t* block_table, const int32_t* seq_lens, float sm_scale, float softcap,
+                             const float* slopes, const int32_t* starts, const int32_t* prefix_lens, void* out, float* lse,
+                             void* workspace, size_t workspace_bytes, smla_stream_t stream);
+
 /* Shapes of one attention-weight call. */
 typedef struct smla_weights_dims {
   int32_t batch;              /* B decode queries, 0 .. 65535                            */

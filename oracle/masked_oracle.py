@@ -1,0 +1,103 @@
+"""Oracle for the decode with capped, biased and masked scores, and for the decode behind shared prefixes.
+
+TEST INFRASTRUCTURE ONLY.  Nothing in the product path imports this module: only the tests may call it.  It shares no
+code with the CUDA library.
+
+Results are those of dense_oracle.dense_decode: (out, lse, weighted, floor, score_err), the last three being sizes that
+bounds on rounding errors need.
+"""
+from __future__ import annotations
+
+import numpy as np
+
+from .dense_oracle import TILE, positions_rows, score_error_bound
+from .sparse_mla_oracle import D_LATENT, RECORD_BYTES, as_f64_q, decode_record, dequantize_record
+
+
+def visible(pos, length, start, prefix):
+    """Which positions a query of this length sees."""
+    seen = pos < length
+    if start is not None:
+        seen &= (pos >= start) | (pos < (prefix if prefix is not None else 0))
+    return seen
+
+
+def attend(q, k, codes, scales, s, err, tile):
+    """One query's heads over records k with scores s [H, n], off by err at most, in tiles of these numbers."""
+    H = q.shape[0]
+    m = s.max(axis=1, keepdims=True)
+    e = np.exp(s - m)
+    z = e.sum(axis=1, keepdims=True)
+    p = e / z
+    floor = np.zeros((H, D_LATENT))
+    top = np.abs(scales).max(axis=1)
+    size = p * np.exp2(np.floor(np.log2(np.where(top > 0, top, 1.0))))
+    for t in np.unique(tile):
+        at = tile == t
+        floor += size[:, at].max(axis=1)[:, None] * np.abs(codes[at]).sum(axis=0)
+    # a position without weight to speak of adds less than its weight, whatever its score's error
+    score_err = np.where(p > 2.0 ** -40, err, 0.0).max(axis=1)
+    return p @ k[:, :D_LATENT], (m + np.log(z))[:, 0], p @ np.abs(k[:, :D_LATENT]), floor, score_err
+
+
+def _empty(B, H):
+    return (np.zeros((B, H, D_LATENT)), np.full((B, H), -np.inf), np.zeros((B, H, D_LATENT)), np.zeros((B, H, D_LATENT)),
+            np.zeros((B, H)))
+
+
+def masked_decode(q, kv_cache, block_table, seq_lens, sm_scale, softcap=0.0, slopes=None, starts=None, prefix_lens=None):
+    """A capped score is off by the score's error, 2^-20 of itself and the roundings of its factors; a biased one by
+    2^-23 of the bias and of the sum more."""
+    qf = as_f64_q(q)
+    cache = np.asarray(kv_cache, dtype=np.uint8)
+    flat = cache.reshape(-1, RECORD_BYTES)
+    bt = np.asarray(block_table, dtype=np.int64)
+    B, H, _ = qf.shape
+    s_q = B // bt.shape[0]
+    res = _empty(B, H)
+    for b in range(B):
+        n = max(0, int(seq_lens[b]))
+        rows, pos = positions_rows(bt[b // s_q], n, cache.shape[0])
+        seen = visible(pos, n, None if starts is None else int(starts[b]), None if prefix_lens is None else int(prefix_lens[b]))
+        rows, pos = rows[seen], pos[seen]
+        if rows.size == 0:
+            continue
+        k = dequantize_record(flat[rows])
+        codes, scales, _ = decode_record(flat[rows])
+        s = sm_scale * (qf[b] @ k.T)
+        err = score_error_bound(qf[b], k, sm_scale)
+        if softcap > 0:
+            s = softcap * np.tanh(s / softcap)
+            err = err + 2.0 ** -20 * np.abs(s)
+        if slopes is not None:
+            bias = np.asarray(slopes, dtype=np.float64)[:, None] * (pos - (n - 1))[None]
+            s = s + bias
+            err = err + 2.0 ** -22 * (np.abs(bias) + np.abs(s))
+        for to, got in zip(res, attend(qf[b], k, codes, scales, s, err, pos // TILE)):
+            to[b] = got
+    return res
+
+
+def shared_decode(q, kv_cache, prefix_table, prefix_lens, block_table, seq_lens, sm_scale):
+    """Requests r attend over the positions of their group's prefix, then over their own."""
+    qf = as_f64_q(q)
+    cache = np.asarray(kv_cache, dtype=np.uint8)
+    flat = cache.reshape(-1, RECORD_BYTES)
+    pt, bt = np.asarray(prefix_table, dtype=np.int64), np.asarray(block_table, dtype=np.int64)
+    B, H, _ = qf.shape
+    s_q, each = B // bt.shape[0], bt.shape[0] // pt.shape[0]
+    res = _empty(B, H)
+    for b in range(B):
+        r = b // s_q
+        a, pa = positions_rows(pt[r // each], int(prefix_lens[r // each]), cache.shape[0])
+        c, pc = positions_rows(bt[r], int(seq_lens[b]), cache.shape[0])
+        rows = np.concatenate([a, c])
+        if rows.size == 0:
+            continue
+        k = dequantize_record(flat[rows])
+        codes, scales, _ = decode_record(flat[rows])
+        s = sm_scale * (qf[b] @ k.T)
+        tile = np.concatenate([pa // TILE, 10 ** 7 + pc // TILE])
+        for to, got in zip(res, attend(qf[b], k, codes, scales, s, score_error_bound(qf[b], k, sm_scale), tile)):
+            to[b] = got
+    return res

@@ -88,6 +88,8 @@ _SIGS = {
     "sparse_mla_dense_plan": (C.c_int, [C.POINTER(SmlaDenseDims), C.c_int32, C.POINTER(SmlaDensePlan)]),
     "sparse_mla_dense_decode": (C.c_int, [C.POINTER(SmlaDenseDims), _P, _P, _P, _P, C.c_float, _P, _P, _P,
                                           C.c_size_t, _P]),
+    "sparse_mla_masked_decode": (C.c_int, [C.POINTER(SmlaDenseDims), _P, _P, _P, _P, C.c_float, C.c_float, _P, _P, _P, _P,
+                                           _P, _P, C.c_size_t, _P]),
     "sparse_mla_attention_weights": (C.c_int, [C.POINTER(SmlaWeightsDims), _P, _P, _P, _P, _P, C.c_float, C.c_float, _P,
                                                _P, _P]),
     "sparse_mla_kv_evict_workspace_size": (C.c_size_t, [C.POINTER(SmlaEvictDims)]),

@@ -570,6 +570,85 @@ def sparse_mla_dense_decode(q: torch.Tensor, kv_cache: torch.Tensor, block_table
     return out, lse
 
 
+def _need_queries(q, kv_cache, block_table, seq_lens) -> int:
+    """Checks of what every call over whole contexts takes; the queries per request."""
+    _need(q, "q", torch.bfloat16, 3)
+    _need(kv_cache, "kv_cache", torch.uint8, 3)
+    _need(block_table, "block_table", torch.int32, 2)
+    _need(seq_lens, "seq_lens", torch.int32, 1)
+    B, R = q.shape[0], block_table.shape[0]
+    if q.shape[2] != D_QK or kv_cache.shape[1] != PAGE_SIZE or kv_cache.shape[2] != 656:
+        raise ValueError("q must be [B,H,576] and kv_cache [pages,64,656]")
+    if R < 1 or B % R != 0 or seq_lens.shape[0] != B:
+        raise ValueError("q and seq_lens need one row per query, block_table one row per request (a divisor of "
+                         "the query count)")
+    return B // R
+
+
+def sparse_mla_masked_decode(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.Tensor,
+                             seq_lens: torch.Tensor, sm_scale: float, softcap: float = 0.0,
+                             slopes: Optional[torch.Tensor] = None, starts: Optional[torch.Tensor] = None,
+                             prefix_lens: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                             lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None,
+                             ctas: int = 0) -> Tuple[torch.Tensor, torch.Tensor]:
+    """sparse_mla_dense_decode whose scores are capped by a tanh (softcap > 0), biased by slopes [H] fp32 times the distance
+    t - (seq_lens[b] - 1), and hidden below starts [B] but for the first prefix_lens [B] positions (int32).
+
+    Workspaces are alloc_dense_workspace's.  Tiles that no row sees are not read: a window costs its own length."""
+    key = _call_key((q, kv_cache, block_table, seq_lens, slopes, starts, prefix_lens, out, lse, workspace), "masked_decode",
+                    ctas)
+    dims = _CHECKED.get(key) or _remember(key, _masked_dims(q, kv_cache, block_table, seq_lens, slopes, starts,
+                                                            prefix_lens, out, lse, workspace, ctas))
+    dev = q.device
+    with _on(dev, stream) as st:
+        if out is None:
+            out = torch.empty((q.shape[0], q.shape[1], D_LATENT), dtype=torch.bfloat16, device=dev)
+        if lse is None:
+            lse = torch.empty((q.shape[0], q.shape[1]), dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = alloc_dense_workspace(dims, dev)
+        r = _lib().sparse_mla_masked_decode(
+            dims, q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), sm_scale, softcap,
+            _ptr(slopes), _ptr(starts), _ptr(prefix_lens), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+            workspace.numel(), st)
+    if r != 0:
+        check("sparse_mla_masked_decode", r)
+    return out, lse
+
+
+def _need_outputs(q, out, lse, workspace):
+    if out is not None:
+        _need(out, "out", torch.bfloat16, 3)
+        if out.shape[:2] != q.shape[:2] or out.shape[2] != D_LATENT:
+            raise ValueError("out must be [B,H,512]")
+    if lse is not None:
+        _need(lse, "lse", torch.float32, 2)
+        if lse.shape != q.shape[:2]:
+            raise ValueError("lse must be [B,H]")
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8, 1)
+
+
+def _masked_dims(q, kv_cache, block_table, seq_lens, slopes, starts, prefix_lens, out, lse, workspace,
+                 ctas) -> SmlaDenseDims:
+    _need_queries(q, kv_cache, block_table, seq_lens)
+    if slopes is not None:
+        _need(slopes, "slopes", torch.float32, 1)
+        if slopes.shape[0] != q.shape[1]:
+            raise ValueError("slopes must be [H]")
+    if prefix_lens is not None and starts is None:
+        raise ValueError("prefix_lens without starts")
+    for name, t in (("starts", starts), ("prefix_lens", prefix_lens)):
+        if t is not None:
+            _need(t, name, torch.int32, 1)
+            if t.shape[0] != q.shape[0]:
+                raise ValueError(f"{name} must be [B]")
+    _need_outputs(q, out, lse, workspace)
+    _same_device(q.device, kv_cache=kv_cache, block_table=block_table, seq_lens=seq_lens, slopes=slopes, starts=starts,
+                 prefix_lens=prefix_lens, out=out, lse=lse, workspace=workspace)
+    return dense_dims_of(q, kv_cache, block_table, ctas)
+
+
 def _need_slots(t, name: str, dtype, rows: int):
     """[rows, n] of dtype with unit stride in a row and rows that do not overlap."""
     if not isinstance(t, torch.Tensor):
@@ -599,21 +678,6 @@ def sparse_mla_attention_weights(q: torch.Tensor, kv_cache: torch.Tensor, block_
     if r != 0:
         check("sparse_mla_attention_weights", r)
     return weights
-
-
-def _need_queries(q, kv_cache, block_table, seq_lens) -> int:
-    """Checks of what every call over whole contexts takes; the queries per request."""
-    _need(q, "q", torch.bfloat16, 3)
-    _need(kv_cache, "kv_cache", torch.uint8, 3)
-    _need(block_table, "block_table", torch.int32, 2)
-    _need(seq_lens, "seq_lens", torch.int32, 1)
-    B, R = q.shape[0], block_table.shape[0]
-    if q.shape[2] != D_QK or kv_cache.shape[1] != PAGE_SIZE or kv_cache.shape[2] != 656:
-        raise ValueError("q must be [B,H,576] and kv_cache [pages,64,656]")
-    if R < 1 or B % R != 0 or seq_lens.shape[0] != B:
-        raise ValueError("q and seq_lens need one row per query, block_table one row per request (a divisor of "
-                         "the query count)")
-    return B // R
 
 
 def _weights_dims(q, kv_cache, block_table, seq_lens, lse, weights, err_word) -> SmlaWeightsDims:

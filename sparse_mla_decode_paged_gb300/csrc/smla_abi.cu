@@ -399,9 +399,18 @@ extern "C" int sparse_mla_dense_plan(const smla_dense_dims* dims, int32_t device
   return sparse_mla_dense_plan_for(dims, sms, plan);
 }
 
-extern "C" int sparse_mla_dense_decode(const smla_dense_dims* d, const void* q, const void* kv_cache,
-                                       const int32_t* block_table, const int32_t* seq_lens, float sm_scale, void* out,
-                                       float* lse, void* workspace, size_t workspace_bytes, smla_stream_t stream) {
+namespace {
+// What a masked decode adds to a dense one.
+struct ScoreForm {
+  float softcap = 0.f;
+  const float* slopes = nullptr;
+  const int32_t* starts = nullptr;
+  const int32_t* prefix_lens = nullptr;
+};
+
+int dense_decode(const smla_dense_dims* d, const ScoreForm& form, const void* q, const void* kv_cache,
+                 const int32_t* block_table, const int32_t* seq_lens, float sm_scale, void* out, float* lse, void* workspace,
+                 size_t workspace_bytes, smla_stream_t stream) {
   // the checks that need no device come first; the workspace's size and what a CTA can count depend on its SMs
   smla_dense_plan plan;
   int st = sparse_mla_dense_plan_for(d, kDenseMaxCtas, &plan);
@@ -434,8 +443,37 @@ extern "C" int sparse_mla_dense_decode(const smla_dense_dims* d, const void* q, 
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
   p.err = static_cast<uint32_t*>(workspace);
+  p.softcap = form.softcap;
+  p.slopes = form.slopes;
+  p.starts = form.starts;
+  p.prefix_lens = form.prefix_lens;
   p.wait_ns = split_wait_limit_ns();
   return launch_dense(p, (cudaStream_t)stream) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+}
+}  // namespace
+
+extern "C" int sparse_mla_dense_decode(const smla_dense_dims* d, const void* q, const void* kv_cache,
+                                       const int32_t* block_table, const int32_t* seq_lens, float sm_scale, void* out,
+                                       float* lse, void* workspace, size_t workspace_bytes, smla_stream_t stream) {
+  return dense_decode(d, ScoreForm{}, q, kv_cache, block_table, seq_lens, sm_scale, out, lse, workspace, workspace_bytes,
+                      stream);
+}
+
+extern "C" int sparse_mla_masked_decode(const smla_dense_dims* d, const void* q, const void* kv_cache,
+                                        const int32_t* block_table, const int32_t* seq_lens, float sm_scale, float softcap,
+                                        const float* slopes, const int32_t* starts, const int32_t* prefix_lens, void* out,
+                                        float* lse, void* workspace, size_t workspace_bytes, smla_stream_t stream) {
+  // (a cap outside this range would leave the exponent's factor 2 / cap without bits; false for a NaN)
+  if (!(softcap == 0.f || (softcap >= 0x1p-20f && softcap <= 0x1p20f))) return SMLA_ERR_INVALID_ARG;
+  if ((prefix_lens && !starts) || (slopes && !aligned(slopes, 4)) || (starts && !aligned(starts, 4)) ||
+      (prefix_lens && !aligned(prefix_lens, 4)))
+    return SMLA_ERR_INVALID_ARG;
+  ScoreForm form;
+  form.softcap = softcap;
+  form.slopes = slopes;
+  form.starts = starts;
+  form.prefix_lens = prefix_lens;
+  return dense_decode(d, form, q, kv_cache, block_table, seq_lens, sm_scale, out, lse, workspace, workspace_bytes, stream);
 }
 
 extern "C" int sparse_mla_topk_select(const smla_topk_dims* d, const float* scores, const int32_t* seq_lens,

@@ -67,6 +67,8 @@ constexpr float kAbove = 6.f;             // A is at most so far below the highe
 constexpr float kSlack = 4.f;             // and moves when it is less far by more than this
 constexpr float kFactor = 15.f;           // no R is further below A than this: 2^(A - R) stays in fp16
 constexpr int kLeastExponent = -60;       // of the scale that a position counts with
+// tanh(x) / x - 1 as a polynomial in x^2, |x| < 1/2
+constexpr float kTanh1 = -0.333331436f, kTanh2 = 0.13325879f, kTanh3 = -0.0530454926f, kTanh4 = 0.017241491f;
 constexpr int kMostTiles16 = 4, kMostTiles32 = 24;   // tiles of a CTA up to which row groups are of 16 and of 32
 
 // Warps: the softmax warps (warp w: TMEM lanes of quadrant w % 4, row part w / 4), then one warp each for the
@@ -118,10 +120,12 @@ struct DC {
   static constexpr uint32_t kRowWarp = 4 * HC * 2 + HC * 4;
   static constexpr uint32_t kBar = kRow + kSoftWarps * kRowWarp;
   static constexpr uint32_t kBytes = kBar + 640;
+  static constexpr uint32_t kSlope = kBytes;                      // [NR] float, of calls with slopes
+  static constexpr uint32_t kBytesMasked = kSlope + NR * 4;
   // TMEM: O^T of block b at kOCols b, score buffer i at kSCol + kOCols i
   static constexpr uint32_t kSCol = 4 * kOCols;
   static constexpr uint32_t kTmemCols = kSCol + kSBufs * kOCols;
-  static_assert(kBytes <= 232448, "shared memory");
+  static_assert(kBytesMasked <= 232448, "shared memory");
   static_assert(kTmemCols == 512 || kTmemCols == 256, "TMEM allocations are powers of two");
 };
 
@@ -182,23 +186,91 @@ __device__ __forceinline__ int clamped_len(const DenseParams& p, int b) {
   return (int)min(n, table);
 }
 
-// Lengths of an item's queries (clamped to [0, table]) and its tiles: at least 1, so that a group without
-// positions has one empty tile.
-struct Lens {
-  int max_len, min_len, tiles;
+// What a query sees: positions below pre and from start up to len (start 0, pre 0: all below len).
+struct Sight {
+  int len, start, pre;
 };
 
-__device__ __forceinline__ Lens lens_of(const DenseParams& p, const Rows& r) {
-  Lens n{0, 0x7fffffff, 0};
+template <bool kMasked>
+__device__ __forceinline__ Sight sight_of(const DenseParams& p, int b) {
+  Sight s{clamped_len(p, b), 0, 0};
+  if constexpr (kMasked) {
+    if (p.starts) {
+      s.start = min(max(__ldg(p.starts + b), 0), s.len);
+      if (p.prefix_lens) s.pre = min(max(__ldg(p.prefix_lens + b), 0), s.len);
+      if (s.start <= s.pre) s.start = s.pre = 0;
+    }
+  }
+  return s;
+}
+
+// Lengths of an item's queries (clamped to [0, table]) and its tiles: at least 1, so that a group without
+// positions has one empty tile.
+template <bool kMasked>
+struct Lens {
+  int max_len, min_len, tiles;
+  __device__ __forceinline__ int at(int t) const { return t; }                  // the tile's place in the request
+  __device__ __forceinline__ bool sees_page(int lp) const { return (long long)lp * kPageSize < max_len; }
+  __device__ __forceinline__ bool all_see(int tile) const { return (long long)(tile + 1) * kDenseTile <= min_len; }
+  __device__ __forceinline__ bool seen(long long t) const { return t < max_len; }        // by some row, at most
+  __device__ __forceinline__ bool seen_by_all(long long t) const { return t < min_len; }
+};
+
+// With a mask: the tiles that hold positions below max_pre, then those from the first that holds a position at or past
+// min_start (of the queries that have one) on.
+template <>
+struct Lens<true> {
+  int max_len, min_len, tiles;
+  int max_pre, min_pre, min_start, max_start, pre_tiles, skip;
+  __device__ __forceinline__ int at(int t) const { return t < pre_tiles ? t : t + skip; }
+  __device__ __forceinline__ bool sees_page(int lp) const {
+    const long long t = (long long)lp * kPageSize;
+    return t < max_pre || (t + kPageSize > min_start && t < max_len);
+  }
+  __device__ __forceinline__ bool all_see(int tile) const {
+    const long long a = (long long)tile * kDenseTile, e = a + kDenseTile;
+    return e <= min_len && (a >= max_start || e <= min_pre);
+  }
+  __device__ __forceinline__ bool seen(long long t) const { return t < max_pre || (t >= min_start && t < max_len); }
+  __device__ __forceinline__ bool seen_by_all(long long t) const { return t < min_len && (t >= max_start || t < min_pre); }
+};
+
+template <bool kMasked>
+__device__ __forceinline__ Lens<kMasked> lens_of(const DenseParams& p, const Rows& r) {
+  Lens<kMasked> n;
+  n.max_len = 0;
+  n.min_len = 0x7fffffff;
+  if constexpr (kMasked) {
+    n.max_pre = n.max_start = 0;
+    n.min_pre = n.min_start = 0x7fffffff;
+  }
   int b = r.req * p.q_per_req + r.row0 / p.H;
   const int last = r.req * p.q_per_req + (r.row0 + r.nrows - 1) / p.H;
 #pragma unroll 1
   for (; b <= last; ++b) {
-    const int len = clamped_len(p, b);
-    n.max_len = max(n.max_len, len);
-    n.min_len = min(n.min_len, len);
+    const Sight s = sight_of<kMasked>(p, b);
+    n.min_len = min(n.min_len, s.len);
+    if constexpr (kMasked) {
+      n.max_pre = max(n.max_pre, s.pre);
+      n.min_pre = min(n.min_pre, s.pre);
+      n.max_start = max(n.max_start, s.start);
+      if (s.start < s.len) {                               // max_len: of the queries that see more than a prefix
+        n.min_start = min(n.min_start, s.start);
+        n.max_len = max(n.max_len, s.len);
+      }
+    } else {
+      n.max_len = max(n.max_len, s.len);
+    }
   }
-  n.tiles = max(1, (int)(((long long)n.max_len + kDenseTile - 1) / kDenseTile));
+  const int end = (int)(((long long)n.max_len + kDenseTile - 1) / kDenseTile);
+  if constexpr (kMasked) {
+    n.pre_tiles = (int)(((long long)n.max_pre + kDenseTile - 1) / kDenseTile);
+    const int from = end > 0 ? max(n.min_start / kDenseTile, n.pre_tiles) : 0;
+    n.skip = max(from - n.pre_tiles, 0);
+    n.tiles = max(1, n.pre_tiles + max(end - from, 0));
+  } else {
+    n.tiles = max(1, end);
+  }
   return n;
 }
 
@@ -215,15 +287,16 @@ struct RunDesc {
 };
 
 // Walks the (item, tile) pairs of a run; every role has its own:  while (w.here(p)) { ...; w.next(); }
+template <bool kMasked>
 struct Walk {
   int i, t, left;
   bool entered = false;
-  Lens n;
+  Lens<kMasked> n;
   __device__ __forceinline__ explicit Walk(const Bars* bars)
       : i(bars->first_item), t(bars->first_tile), left((int)(bars->run_end - bars->run_begin)) {}
   __device__ __forceinline__ bool here(const DenseParams& p) {
     if (left > 0 && !entered) {
-      n = lens_of(p, rows_of(p, i));
+      n = lens_of<kMasked>(p, rows_of(p, i));
       entered = true;
     }
     return left > 0;
@@ -241,17 +314,18 @@ struct Walk {
 
 // ----------------------------------------------------------------------------- copies
 
-__device__ __forceinline__ int page_entry(const DenseParams& p, int req, int max_len, int lp) {
-  return lp < p.max_pages && (long long)lp * kPageSize < max_len
+template <bool kMasked>
+__device__ __forceinline__ int page_entry(const DenseParams& p, int req, const Lens<kMasked>& n, int lp) {
+  return lp < p.max_pages && n.sees_page(lp)
              ? __ldg(p.block_table + (size_t)req * p.max_pages + lp)
              : -1;
 }
 
-template <int NR>
+template <int NR, bool kMasked>
 __device__ void copy_role(const DenseParams& p, const CUtensorMap* map, const CUtensorMap* smap, uint32_t base,
                           Bars* bars, int lane) {
   using C = DC<NR>;
-  Walk w(bars);
+  Walk<kMasked> w(bars);
   int req = 0;
   Ring<C::kRing> k;
   Ring<C::kScaleSlots> sc;
@@ -261,14 +335,14 @@ __device__ void copy_role(const DenseParams& p, const CUtensorMap* map, const CU
   int cur = 0, nxt = 0, base_lp = 0, item = -1;
 #pragma unroll 1
   while (w.here(p)) {
-    const int lp = 2 * w.t;
+    const int lp = 2 * w.n.at(w.t);
     const bool enters = item != w.i;
     if (enters) {
       item = w.i;
       const Rows r = rows_of(p, item);
       req = r.req;
       base_lp = lp;
-      nxt = page_entry(p, req, w.n.max_len, lp + lane);
+      nxt = page_entry(p, req, w.n, lp + lane);
       if (lane == 0) {
         const int last = req * p.q_per_req + (r.row0 + r.nrows - 1) / p.H;
 #pragma unroll 1
@@ -276,16 +350,19 @@ __device__ void copy_role(const DenseParams& p, const CUtensorMap* map, const CU
           if (__ldg(p.seq_lens + b) > (long long)p.max_pages * kPageSize) atomicOr(p.err, SMLA_DEVERR_PAGE_RANGE);
       }
     }
-    if (enters || lp == base_lp + 32) {
+    bool jumps = false;                                    // over tiles that no row sees
+    if constexpr (kMasked) jumps = !enters && w.n.skip > 0 && w.t == w.n.pre_tiles;
+    if (jumps) nxt = page_entry(p, req, w.n, lp + lane);
+    if (enters || jumps || lp == base_lp + 32) {
       base_lp = lp;
       cur = nxt;
-      nxt = page_entry(p, req, w.n.max_len, lp + 32 + lane);
+      nxt = page_entry(p, req, w.n, lp + 32 + lane);
     }
     const int pg[2] = {__shfl_sync(0xffffffffu, cur, lp - base_lp), __shfl_sync(0xffffffffu, cur, lp - base_lp + 1)};
     int good = 0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const bool used = (long long)(lp + h) * kPageSize < w.n.max_len;
+      const bool used = w.n.sees_page(lp + h);
       const bool in_cache = pg[h] >= 0 && (int64_t)pg[h] < p.num_pages;
       if (used && in_cache) good |= 1 << h;
       if (used && !in_cache && lane == 0) atomicOr(p.err, SMLA_DEVERR_PAGE_RANGE);
@@ -296,6 +373,7 @@ __device__ void copy_role(const DenseParams& p, const CUtensorMap* map, const CU
     const int ahead = lp - base_lp + 2 * kAhead + (lane & 1);
     const int page_cur = __shfl_sync(0xffffffffu, cur, ahead & 31), page_nxt = __shfl_sync(0xffffffffu, nxt, ahead & 31);
     const int page = ahead < 32 ? page_cur : page_nxt;
+    // (past a jump it prefetches pages that no row sees: table entries of -1, so nothing)
     if (w.left > kAhead && lane < 2 && page >= 0 && (int64_t)page < p.num_pages)
       ptx::prefetch_l2_bulk(p.kv + (size_t)page * kPageSize * kRecordBytes, kPageSize * kRecordBytes);
     SMLA_WAIT(&bars->scempty[sc.slot], sc.parity ^ 1);
@@ -344,11 +422,11 @@ __device__ void copy_role(const DenseParams& p, const CUtensorMap* map, const CU
 
 // ----------------------------------------------------------------------------- MMA issue
 
-template <int NR>
+template <int NR, bool kMasked>
 __device__ void qk_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars* bars, int lane) {
   using C = DC<NR>;
   constexpr uint32_t kIdescCodes = ptx::idesc_e4m3(128, C::kOCols), kIdescRope = ptx::idesc_bf16(128, NR);
-  Walk w(bars);
+  Walk<kMasked> w(bars);
   Ring<C::kRing> k;
   Ring<C::kSBufs> s;
   Ring<C::kRopeSlots> rope;
@@ -398,12 +476,12 @@ __device__ void qk_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars
   __syncwarp();
 }
 
-template <int NR>
+template <int NR, bool kMasked>
 __device__ void pv_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars* bars, int lane) {
   using C = DC<NR>;
   constexpr int N = C::kOCols;
   constexpr uint32_t kIdesc = ptx::idesc_e4m3(128, N) | (1u << 15) | (1u << 16);     // A and B MN-major
-  Walk w(bars);
+  Walk<kMasked> w(bars);
   Ring<C::kRing> k;
   Ring<C::kPBufs> pb;
   uint32_t ok = p.wait_ns >= kLeastWaitNs;
@@ -635,7 +713,71 @@ __device__ __forceinline__ void write_block(const uint64_t (&x)[HC / 2], uint32_
   }
 }
 
-template <int NR>
+// Scores in units of log2 -> cap log2 e tanh(score / cap).  tanh x is x times a polynomial in x^2 below 1/2 (the least
+// largest relative error over [0, 1/2], 1.5e-8) and 1 - 2 / (e^2x + 1) from there on, where that form loses no digits.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <int HC>
+__device__ __forceinline__ void cap_scores(uint64_t (&acc)[HC / 2], float cap) {
+  const float up = 2.f / cap, c2 = cap * kLog2e, per = kLn2 / cap;
+  const uint64_t per2 = ptx::pack2(per, per), one = ptx::pack2(1.f, 1.f);
+#pragma unroll
+  for (int i = 0; i < HC / 2; ++i) {
+    const uint64_t x = ptx::mul2(acc[i], per2), z = ptx::mul2(x, x);
+    uint64_t y = ptx::fma2(z, ptx::pack2(kTanh4, kTanh4), ptx::pack2(kTanh3, kTanh3));
+    y = ptx::fma2(y, z, ptx::pack2(kTanh2, kTanh2));
+    y = ptx::fma2(y, z, ptx::pack2(kTanh1, kTanh1));
+    y = ptx::mul2(ptx::fma2(y, z, one), acc[i]);
+    const float2 s = ptx::unpack2(acc[i]), a = ptx::unpack2(x);
+    float2 r = ptx::unpack2(y);
+    if (!(fabsf(a.x) < 0.5f)) r.x = fmaf(-2.f * c2, rcp_approx(ptx::ex2_approx(s.x * up) + 1.f), c2);
+    if (!(fabsf(a.y) < 0.5f)) r.y = fmaf(-2.f * c2, rcp_approx(ptx::ex2_approx(s.y * up) + 1.f), c2);
+    acc[i] = ptx::pack2(r.x, r.y);
+  }
+}
+
+// Adds slope log2 e (t - (len - 1)) of each row (t and the lengths may be past 2^24: the distance is formed in whole
+// numbers).
+template <int HC>
+__device__ __forceinline__ void add_bias(uint64_t (&acc)[HC / 2], uint32_t slopes, uint32_t lens, int t) {
+#pragma unroll
+  for (int i = 0; i < HC; i += 4) {
+    const ulonglong2 f = ptx::lds128_pairs(slopes + i * 4);
+    const uint4 n = ptx::lds128(lens + i * 4);
+    acc[i / 2] = ptx::fma2(f.x, ptx::pack2((float)(t + 1 - (int)n.x), (float)(t + 1 - (int)n.y)), acc[i / 2]);
+    acc[i / 2 + 1] = ptx::fma2(f.y, ptx::pack2((float)(t + 1 - (int)n.z), (float)(t + 1 - (int)n.w)), acc[i / 2 + 1]);
+  }
+}
+
+// Position t for the rows whose query sees neither its prefix nor its window there.  (A part's rows are mostly of one
+// query.)
+template <int HC>
+__device__ __forceinline__ void hide_between(uint64_t (&acc)[HC / 2], const DenseParams& p, const Rows& it, int col0,
+                                             long long t) {
+  int b = -1;
+  bool hidden = false;
+#pragma unroll
+  for (int i = 0; i < HC; ++i) {
+    const int r = col0 + i;
+    if (r < it.nrows) {
+      const int at = it.req * p.q_per_req + (it.row0 + r) / p.H;
+      if (at != b) {
+        b = at;
+        const Sight s = sight_of<true>(p, b);
+        hidden = t >= s.pre && t < s.start;
+      }
+    }
+    float2 d = ptx::unpack2(acc[i / 2]);
+    if (hidden) (i & 1 ? d.y : d.x) = -CUDART_INF_F;
+    acc[i / 2] = ptx::pack2(d.x, d.y);
+  }
+}
+
+template <int NR, bool kMasked>
 __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t base, uint32_t tmem, Bars* bars, int warp,
                              int lane, float* o_part, float* lse_part) {
   using C = DC<NR>;
@@ -646,7 +788,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
   const uint32_t lane_base = tmem + ((uint32_t)(32 * quad) << 16);
   const float kf = p.sm_scale * kLog2e;
   const uint32_t row_c = base + C::kRow + warp * C::kRowWarp, row_na = row_c + 4 * HC * 2;
-  Walk w(bars);
+  Walk<kMasked> w(bars);
   Ring<C::kSBufs> s;
   Ring<C::kScaleSlots> sc;
   Ring<C::kPBufs> pb;
@@ -773,6 +915,15 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
 #pragma unroll
       for (int j = 0; j < kRefs; ++j) ref[j] = CUDART_NAN_F, upper[j] = lower[j] = -CUDART_INF_F;
       level = CUDART_NAN_F;
+      if constexpr (kMasked) {
+        if (p.slopes) {                                     // every warp is past the last item's tiles
+          const int r = rows_of(p, item).row0 + col0 + lane;
+          if (quad == 0 && lane < HC)
+            ptx::sts32f(base + C::kSlope + (col0 + lane) * 4,
+                        r < p.q_per_req * p.H ? __ldg(p.slopes + r % p.H) * kLog2e : 0.f);
+          ptx::named_bar_sync(1 + part, 128);
+        }
+      }
     }
     // scores of this thread's position for its HC rows, in units of log2
     SMLA_WAIT(&bars->scfull[sc.slot], sc.parity);
@@ -845,7 +996,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
     ptx::tc_fence_after();
     {
       const uint32_t a = lane_base + C::kSCol + C::kOCols * s.slot + col0;
-      const uint64_t kf2 = ptx::pack2(kf, kf), e2 = ptx::pack2((float)e, (float)e);
+      const uint64_t kf2 = ptx::pack2(kf, kf), e2 = kMasked ? 0 : ptx::pack2((float)e, (float)e);
       const uint32_t fa = base + C::kF + (buf * NR + col0) * 4;
       uint32_t r[HC];
       tmem_ld<HC>(a, r);
@@ -862,9 +1013,18 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
     __syncwarp();
     if (ok && lane == 0) ptx::mbar_arrive(&bars->sempty[s.slot]);
     s.next();
+    const int tile = w.n.at(w.t);
+    if constexpr (kMasked) {
+      if (p.softcap > 0.f) cap_scores<HC>(acc, p.softcap);
+      if (p.slopes)
+        add_bias<HC>(acc, base + C::kSlope + col0 * 4, base + C::kLen + (buf * NR + col0) * 4, tile * kDenseTile + tok);
+      const uint64_t e2 = ptx::pack2((float)e, (float)e);
+#pragma unroll
+      for (int i = 0; i < HC / 2; ++i) acc[i] = ptx::add2(acc[i], e2);
+    }
     // positions that a row may not see
-    if (__builtin_expect((long long)(w.t + 1) * kDenseTile > w.n.min_len || pages != 3, 0)) {
-      const long long t = (long long)w.t * kDenseTile + tok;
+    if (__builtin_expect(!w.n.all_see(tile) || pages != 3, 0)) {
+      const long long t = (long long)tile * kDenseTile + tok;
       const int* lens = reinterpret_cast<const int*>(sm + C::kLen) + buf * NR + col0;
       const bool here = pages >> (tok >> 6) & 1;
 #pragma unroll
@@ -874,7 +1034,10 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
         if (!here || t >= lens[i + 1]) d.y = -CUDART_INF_F;
         acc[i / 2] = ptx::pack2(d.x, d.y);
       }
-      if (!here || t >= w.n.min_len) clean_codes<NR>(base, kslot, tok, part, here && t < w.n.max_len);
+      if constexpr (kMasked) {
+        if (p.starts) hide_between<HC>(acc, p, rows_of(p, item), col0, t);
+      }
+      if (!here || !w.n.seen_by_all(t)) clean_codes<NR>(base, kslot, tok, part, here && w.n.seen(t));
     }
     kslot = kslot + 4 >= C::kRing ? kslot + 4 - C::kRing : kslot + 4;
     // the largest operand of each row and block over the 128 positions: every warp's 32 first
@@ -1098,13 +1261,14 @@ __device__ __forceinline__ void run_bounds(const DenseParams& p, long long T, in
 }
 
 // The items in which the run begins and ends, if they are among i0 .. i1 - 1, whose `mine` tiles begin at tile `at`.
+template <bool kMasked>
 __device__ __forceinline__ void find_ends(const DenseParams& p, Bars* bars, int i0, int i1, long long at, long long mine,
                                           int start, long long a, long long e) {
   if (a >= e || a >= at + mine + (long long)start * i1 || e <= at + (long long)start * i0) return;
   long long x = at;
 #pragma unroll 1
   for (int i = i0; i < i1; ++i) {
-    const int tiles = lens_of(p, rows_of(p, i)).tiles;
+    const int tiles = lens_of<kMasked>(p, rows_of(p, i)).tiles;
     const long long begin = x + (long long)start * (i + 1), end = begin + tiles;       // the item's tiles on the line
     const long long from = max(a, begin), to = min(e, end);
     if (from < to) {
@@ -1131,7 +1295,7 @@ __host__ __device__ __forceinline__ bool one_tile(const DenseParams& p) { return
 // Every CTA adds up the tiles of all items.  Few items: one warp, up to four items per lane (the general search's code
 // and barriers take 0.7 us more of a call: 1 x 77 positions 11.0 us instead of 10.3).  Else a run of items per thread,
 // then a scan of the threads' sums.
-template <int kThreads>
+template <int kThreads, bool kMasked>
 __device__ __forceinline__ void find_run(const DenseParams& p, unsigned char* scratch, Bars* bars) {
   if (one_tile(p)) {                                     // an item is a tile: nothing to look up
     if (threadIdx.x == 0) {
@@ -1156,7 +1320,7 @@ __device__ __forceinline__ void find_run(const DenseParams& p, unsigned char* sc
       const int i0 = min(n, lane * per), i1 = min(n, i0 + per);
       long long mine = 0;
 #pragma unroll 1
-      for (int i = i0; i < i1; ++i) mine += lens_of(p, rows_of(p, i)).tiles;
+      for (int i = i0; i < i1; ++i) mine += lens_of<kMasked>(p, rows_of(p, i)).tiles;
       __syncwarp();                                      // the empty run is written
       long long upto = mine;
 #pragma unroll
@@ -1167,7 +1331,7 @@ __device__ __forceinline__ void find_run(const DenseParams& p, unsigned char* sc
       long long a, e;
       int start;
       run_bounds(p, __shfl_sync(0xffffffffu, upto, 31), n, bars, lane == 0, start, a, e);
-      find_ends(p, bars, i0, i1, upto - mine, mine, start, a, e);
+      find_ends<kMasked>(p, bars, i0, i1, upto - mine, mine, start, a, e);
     }
     __syncthreads();
     return;
@@ -1178,7 +1342,7 @@ __device__ __forceinline__ void find_run(const DenseParams& p, unsigned char* sc
   const int i0 = min(n, (int)threadIdx.x * per), i1 = min(n, i0 + per);
   long long mine = 0;
 #pragma unroll 1
-  for (int i = i0; i < i1; ++i) mine += lens_of(p, rows_of(p, i)).tiles;
+  for (int i = i0; i < i1; ++i) mine += lens_of<kMasked>(p, rows_of(p, i)).tiles;
   sums[threadIdx.x] = mine;
   __syncthreads();
   if (threadIdx.x < 32) {                                // exclusive prefix over kPer sums per lane
@@ -1205,7 +1369,7 @@ __device__ __forceinline__ void find_run(const DenseParams& p, unsigned char* sc
   const long long T = bars->units;
   __syncthreads();
   run_bounds(p, T, n, bars, threadIdx.x == 0, start, a, e);
-  find_ends(p, bars, i0, i1, sums[threadIdx.x], mine, start, a, e);
+  find_ends<kMasked>(p, bars, i0, i1, sums[threadIdx.x], mine, start, a, e);
   __syncthreads();
 }
 
@@ -1220,7 +1384,7 @@ __device__ __forceinline__ RunDesc describe_run(const Bars* bars) {
   return RunDesc{bars->last_item, c1 - c + 1};
 }
 
-template <int NR>
+template <int NR, bool kMasked>
 __global__ void __launch_bounds__(DC<NR>::kThreads, 1)
     dense_kernel(const DenseParams p, const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap smap,
                  RunDesc* descs, float* lse_part, float* o_part) {
@@ -1236,7 +1400,7 @@ __global__ void __launch_bounds__(DC<NR>::kThreads, 1)
     ptx::tmem_alloc(&bars->tmem, C::kTmemCols);
     ptx::tmem_relinquish();
   }
-  find_run<C::kThreads>(p, sm, bars);            // the scratch is overwritten by the pipeline afterwards
+  find_run<C::kThreads, kMasked>(p, sm, bars);            // the scratch is overwritten by the pipeline afterwards
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -1244,12 +1408,12 @@ __global__ void __launch_bounds__(DC<NR>::kThreads, 1)
 
   if (role < 0) {
     ptx::setmaxnreg_inc<C::kSoftRegs>();
-    softmax_role<NR>(p, sm, base, tmem, bars, warp, lane, o_part, lse_part);
+    softmax_role<NR, kMasked>(p, sm, base, tmem, bars, warp, lane, o_part, lse_part);
   } else {
     ptx::setmaxnreg_dec<C::kMiscRegs>();
-    if (role == kCopyRole) copy_role<NR>(p, &map, &smap, base, bars, lane);
-    else if (role == kQkRole) qk_role<NR>(p, base, tmem, bars, lane);
-    else if (role == kPvRole) pv_role<NR>(p, base, tmem, bars, lane);
+    if (role == kCopyRole) copy_role<NR, kMasked>(p, &map, &smap, base, bars, lane);
+    else if (role == kQkRole) qk_role<NR, kMasked>(p, base, tmem, bars, lane);
+    else if (role == kPvRole) pv_role<NR, kMasked>(p, base, tmem, bars, lane);
     else if (lane == 0) descs[blockIdx.x] = describe_run(bars);
   }
 
@@ -1438,8 +1602,9 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const DenseP
 constexpr size_t kDescBytes = (kDenseMaxCtas * sizeof(RunDesc) + 255) / 256 * 256;
 size_t lse_part_bytes(int ctas, int nr) { return ((size_t)2 * ctas * nr * sizeof(float) + 255) / 256 * 256; }
 
-template <int NR>
+template <int NR, bool kMasked>
 cudaError_t launch_nr(const DenseParams& p, unsigned char* ws, cudaStream_t stream) {
+  constexpr uint32_t kBytes = kMasked ? DC<NR>::kBytesMasked : DC<NR>::kBytes;
   CUtensorMap map, smap;
   if (!encoder() || !encode_map(&map, p.kv, p.num_pages, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_map(&smap, p.kv, p.num_pages, 16, CU_TENSOR_MAP_SWIZZLE_NONE))
@@ -1450,14 +1615,14 @@ cudaError_t launch_nr(const DenseParams& p, unsigned char* ws, cudaStream_t stre
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !set[dev].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(dense_kernel<NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, DC<NR>::kBytes);
+    e = cudaFuncSetAttribute(dense_kernel<NR, kMasked>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return e;
     if (dev < 64) set[dev].store(true, std::memory_order_relaxed);
   }
   RunDesc* descs = reinterpret_cast<RunDesc*>(ws + kWorkspaceHeader);
   float* lse_part = reinterpret_cast<float*>(ws + kWorkspaceHeader + kDescBytes);
   float* o_part = reinterpret_cast<float*>(ws + kWorkspaceHeader + kDescBytes + lse_part_bytes(p.ctas, NR));
-  dense_kernel<NR><<<p.ctas, DC<NR>::kThreads, DC<NR>::kBytes, stream>>>(p, map, smap, descs, lse_part, o_part);
+  dense_kernel<NR, kMasked><<<p.ctas, DC<NR>::kThreads, kBytes, stream>>>(p, map, smap, descs, lse_part, o_part);
   e = cudaGetLastError();
   if (e != cudaSuccess || one_tile(p)) return e;
   cudaLaunchConfig_t cfg = {};
@@ -1477,9 +1642,14 @@ cudaError_t launch_nr(const DenseParams& p, unsigned char* ws, cudaStream_t stre
 
 cudaError_t launch_dense(const DenseParams& p, cudaStream_t stream) {
   unsigned char* ws = reinterpret_cast<unsigned char*>(p.err);    // the workspace begins with the error word
-  if (p.nr == 16) return launch_nr<16>(p, ws, stream);
-  if (p.nr == 32) return launch_nr<32>(p, ws, stream);
-  return launch_nr<64>(p, ws, stream);
+  if (p.softcap > 0.f || p.slopes || p.starts) {
+    if (p.nr == 16) return launch_nr<16, true>(p, ws, stream);
+    if (p.nr == 32) return launch_nr<32, true>(p, ws, stream);
+    return launch_nr<64, true>(p, ws, stream);
+  }
+  if (p.nr == 16) return launch_nr<16, false>(p, ws, stream);
+  if (p.nr == 32) return launch_nr<32, false>(p, ws, stream);
+  return launch_nr<64, false>(p, ws, stream);
 }
 
 }  // namespace smla

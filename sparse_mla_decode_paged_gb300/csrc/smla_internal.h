@@ -154,6 +154,10 @@ struct DenseParams {
   int nr;                     // rows per CTA (16, 32 or 64)
   int groups;                 // row groups per request
   int ctas;
+  float softcap;              // > 0: scores become softcap tanh(score / softcap)
+  const float* slopes;        // [H] or null: slope (t - (len - 1)) is added to them
+  const int32_t* starts;      // [B] or null: positions below starts[b] are seen below prefix_lens[b] alone
+  const int32_t* prefix_lens; // [B] or null (with starts)
   uint16_t* out;              // bf16 [B][H][512]
   float* lse;                 // [B][H]
   uint32_t* err;              // device error word
