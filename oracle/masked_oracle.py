@@ -22,8 +22,10 @@ def visible(pos, length, start, prefix):
     return seen
 
 
-def attend(q, k, codes, scales, s, err, tile):
-    """One query's heads over records k with scores s [H, n], off by err at most, in tiles of these numbers."""
+def attend(q, k, codes, scales, s, err, tile, steep=None):
+    """One query's heads over records k with scores s [H, n], off by err at most, in tiles of these numbers.  The rows
+    `steep` keep the reference of their largest weight, so the steps of their small weights follow that one instead of
+    the tile's largest."""
     H = q.shape[0]
     m = s.max(axis=1, keepdims=True)
     e = np.exp(s - m)
@@ -34,7 +36,10 @@ def attend(q, k, codes, scales, s, err, tile):
     size = p * np.exp2(np.floor(np.log2(np.where(top > 0, top, 1.0))))
     for t in np.unique(tile):
         at = tile == t
-        floor += size[:, at].max(axis=1)[:, None] * np.abs(codes[at]).sum(axis=0)
+        most = size[:, at].max(axis=1)
+        if steep is not None:
+            most = np.where(steep, size.max(axis=1), most)
+        floor += most[:, None] * np.abs(codes[at]).sum(axis=0)
     # a position without weight to speak of adds less than its weight, whatever its score's error
     score_err = np.where(p > 2.0 ** -40, err, 0.0).max(axis=1)
     return p @ k[:, :D_LATENT], (m + np.log(z))[:, 0], p @ np.abs(k[:, :D_LATENT]), floor, score_err
@@ -65,7 +70,7 @@ def masked_decode(q, kv_cache, block_table, seq_lens, sm_scale, softcap=0.0, slo
         k = dequantize_record(flat[rows])
         codes, scales, _ = decode_record(flat[rows])
         s = sm_scale * (qf[b] @ k.T)
-        err = score_error_bound(qf[b], k, sm_scale)
+        err, steep = score_error_bound(qf[b], k, sm_scale), None
         if softcap > 0:
             s = softcap * np.tanh(s / softcap)
             err = err + 2.0 ** -20 * np.abs(s)
@@ -73,7 +78,8 @@ def masked_decode(q, kv_cache, block_table, seq_lens, sm_scale, softcap=0.0, slo
             bias = np.asarray(slopes, dtype=np.float64)[:, None] * (pos - (n - 1))[None]
             s = s + bias
             err = err + 2.0 ** -22 * (np.abs(bias) + np.abs(s))
-        for to, got in zip(res, attend(qf[b], k, codes, scales, s, err, pos // TILE)):
+            steep = np.asarray(slopes, dtype=np.float32) * np.log2(np.e) * TILE >= 0.25 - 1e-6
+        for to, got in zip(res, attend(qf[b], k, codes, scales, s, err, pos // TILE, steep)):
             to[b] = got
     return res
 

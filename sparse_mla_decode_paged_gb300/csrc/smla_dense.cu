@@ -66,6 +66,11 @@ constexpr float kLowest = 30.f;           // how far below its highest value a r
 constexpr float kAbove = 6.f;             // A is at most so far below the highest R: w m_b stay below 2^14.75, in fp16
 constexpr float kSlack = 4.f;             // and moves when it is less far by more than this
 constexpr float kFactor = 15.f;           // no R is further below A than this: 2^(A - R) stays in fp16
+// Rows whose bias falls by so many powers of two per tile keep their references when a tile lies below the window (the last
+// tile comes first).  Operands below 2^-6 then keep steps of 2^-9, evenly spread: from 2^0 down to 2^-9 a row takes at
+// most 36 such tiles, whose 4608 roundings of 2^-10.8 each (root mean square) add up to 2^-4.7, 2^-8.5 of the largest
+// operand alone.  (32 x 32768 positions of 64 heads, slopes 2^(-8 h / 64): 349 us with references that follow, 266 without.)
+constexpr float kSteep = 0.25f;
 constexpr int kLeastExponent = -60;       // of the scale that a position counts with
 // tanh(x) / x - 1 as a polynomial in x^2, |x| < 1/2
 constexpr float kTanh1 = -0.333331436f, kTanh2 = 0.13325879f, kTanh3 = -0.0530454926f, kTanh4 = 0.017241491f;
@@ -222,7 +227,11 @@ template <>
 struct Lens<true> {
   int max_len, min_len, tiles;
   int max_pre, min_pre, min_start, max_start, pre_tiles, skip;
-  __device__ __forceinline__ int at(int t) const { return t < pre_tiles ? t : t + skip; }
+  bool back;                                               // the last tile first
+  __device__ __forceinline__ int at(int t) const {
+    if (back) t = tiles - 1 - t;
+    return t < pre_tiles ? t : t + skip;
+  }
   __device__ __forceinline__ bool sees_page(int lp) const {
     const long long t = (long long)lp * kPageSize;
     return t < max_pre || (t + kPageSize > min_start && t < max_len);
@@ -268,6 +277,7 @@ __device__ __forceinline__ Lens<kMasked> lens_of(const DenseParams& p, const Row
     const int from = end > 0 ? max(n.min_start / kDenseTile, n.pre_tiles) : 0;
     n.skip = max(from - n.pre_tiles, 0);
     n.tiles = max(1, n.pre_tiles + max(end - from, 0));
+    n.back = p.slopes != nullptr;
   } else {
     n.tiles = max(1, end);
   }
@@ -314,11 +324,12 @@ struct Walk {
 
 // ----------------------------------------------------------------------------- copies
 
+// Entry `lane` of 16 tiles from the item's t-th on, two pages each.
 template <bool kMasked>
-__device__ __forceinline__ int page_entry(const DenseParams& p, int req, const Lens<kMasked>& n, int lp) {
-  return lp < p.max_pages && n.sees_page(lp)
-             ? __ldg(p.block_table + (size_t)req * p.max_pages + lp)
-             : -1;
+__device__ __forceinline__ int page_entry(const DenseParams& p, int req, const Lens<kMasked>& n, int t, int lane) {
+  t += lane >> 1;
+  const int lp = t < n.tiles ? 2 * n.at(t) + (lane & 1) : p.max_pages;
+  return lp < p.max_pages && n.sees_page(lp) ? __ldg(p.block_table + (size_t)req * p.max_pages + lp) : -1;
 }
 
 template <int NR, bool kMasked>
@@ -332,7 +343,7 @@ __device__ void copy_role(const DenseParams& p, const CUtensorMap* map, const CU
   Ring<C::kRopeSlots> rope;
   uint32_t ok = p.wait_ns >= kLeastWaitNs;
   // block-table entries of 16 tiles per load, one lane each, the next 16 tiles' already in flight
-  int cur = 0, nxt = 0, base_lp = 0, item = -1;
+  int cur = 0, nxt = 0, base_t = 0, item = -1;
 #pragma unroll 1
   while (w.here(p)) {
     const int lp = 2 * w.n.at(w.t);
@@ -341,8 +352,7 @@ __device__ void copy_role(const DenseParams& p, const CUtensorMap* map, const CU
       item = w.i;
       const Rows r = rows_of(p, item);
       req = r.req;
-      base_lp = lp;
-      nxt = page_entry(p, req, w.n, lp + lane);
+      nxt = page_entry(p, req, w.n, w.t, lane);
       if (lane == 0) {
         const int last = req * p.q_per_req + (r.row0 + r.nrows - 1) / p.H;
 #pragma unroll 1
@@ -350,15 +360,13 @@ __device__ void copy_role(const DenseParams& p, const CUtensorMap* map, const CU
           if (__ldg(p.seq_lens + b) > (long long)p.max_pages * kPageSize) atomicOr(p.err, SMLA_DEVERR_PAGE_RANGE);
       }
     }
-    bool jumps = false;                                    // over tiles that no row sees
-    if constexpr (kMasked) jumps = !enters && w.n.skip > 0 && w.t == w.n.pre_tiles;
-    if (jumps) nxt = page_entry(p, req, w.n, lp + lane);
-    if (enters || jumps || lp == base_lp + 32) {
-      base_lp = lp;
+    if (enters || w.t == base_t + 16) {
+      base_t = w.t;
       cur = nxt;
-      nxt = page_entry(p, req, w.n, lp + 32 + lane);
+      nxt = page_entry(p, req, w.n, w.t + 16, lane);
     }
-    const int pg[2] = {__shfl_sync(0xffffffffu, cur, lp - base_lp), __shfl_sync(0xffffffffu, cur, lp - base_lp + 1)};
+    const int at = 2 * (w.t - base_t);
+    const int pg[2] = {__shfl_sync(0xffffffffu, cur, at), __shfl_sync(0xffffffffu, cur, at + 1)};
     int good = 0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -370,10 +378,9 @@ __device__ void copy_role(const DenseParams& p, const CUtensorMap* map, const CU
     const uint32_t n_good = (good & 1) + (good >> 1);
     // a later tile of the item into L2: K slots come free one by one behind the PV, and their loads would bring the
     // latency of HBM into every tile
-    const int ahead = lp - base_lp + 2 * kAhead + (lane & 1);
+    const int ahead = at + 2 * kAhead + (lane & 1);
     const int page_cur = __shfl_sync(0xffffffffu, cur, ahead & 31), page_nxt = __shfl_sync(0xffffffffu, nxt, ahead & 31);
     const int page = ahead < 32 ? page_cur : page_nxt;
-    // (past a jump it prefetches pages that no row sees: table entries of -1, so nothing)
     if (w.left > kAhead && lane < 2 && page >= 0 && (int64_t)page < p.num_pages)
       ptx::prefetch_l2_bulk(p.kv + (size_t)page * kPageSize * kRecordBytes, kPageSize * kRecordBytes);
     SMLA_WAIT(&bars->scempty[sc.slot], sc.parity ^ 1);
@@ -721,21 +728,35 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
+__device__ __forceinline__ uint64_t small_cap(uint64_t s, uint64_t per2, uint64_t one) {
+  const uint64_t x = ptx::mul2(s, per2), z = ptx::mul2(x, x);
+  uint64_t y = ptx::fma2(z, ptx::pack2(kTanh4, kTanh4), ptx::pack2(kTanh3, kTanh3));
+  y = ptx::fma2(y, z, ptx::pack2(kTanh2, kTanh2));
+  y = ptx::fma2(y, z, ptx::pack2(kTanh1, kTanh1));
+  return ptx::mul2(ptx::fma2(y, z, one), s);
+}
+
 template <int HC>
 __device__ __forceinline__ void cap_scores(uint64_t (&acc)[HC / 2], float cap) {
-  const float up = 2.f / cap, c2 = cap * kLog2e, per = kLn2 / cap;
+  const float up = 2.f / cap, c2 = cap * kLog2e, per = kLn2 / cap, half = 0.5f / per;
   const uint64_t per2 = ptx::pack2(per, per), one = ptx::pack2(1.f, 1.f);
+  float most = 0.f;                                        // (a NaN stays one in either form)
 #pragma unroll
   for (int i = 0; i < HC / 2; ++i) {
-    const uint64_t x = ptx::mul2(acc[i], per2), z = ptx::mul2(x, x);
-    uint64_t y = ptx::fma2(z, ptx::pack2(kTanh4, kTanh4), ptx::pack2(kTanh3, kTanh3));
-    y = ptx::fma2(y, z, ptx::pack2(kTanh2, kTanh2));
-    y = ptx::fma2(y, z, ptx::pack2(kTanh1, kTanh1));
-    y = ptx::mul2(ptx::fma2(y, z, one), acc[i]);
-    const float2 s = ptx::unpack2(acc[i]), a = ptx::unpack2(x);
-    float2 r = ptx::unpack2(y);
-    if (!(fabsf(a.x) < 0.5f)) r.x = fmaf(-2.f * c2, rcp_approx(ptx::ex2_approx(s.x * up) + 1.f), c2);
-    if (!(fabsf(a.y) < 0.5f)) r.y = fmaf(-2.f * c2, rcp_approx(ptx::ex2_approx(s.y * up) + 1.f), c2);
+    const float2 s = ptx::unpack2(acc[i]);
+    most = fmaxf(most, fmaxf(fabsf(s.x), fabsf(s.y)));
+  }
+  if (!__any_sync(0xffffffffu, most >= half)) {
+#pragma unroll
+    for (int i = 0; i < HC / 2; ++i) acc[i] = small_cap(acc[i], per2, one);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < HC / 2; ++i) {
+    const float2 s = ptx::unpack2(acc[i]);
+    float2 r = ptx::unpack2(small_cap(acc[i], per2, one));
+    if (!(fabsf(s.x) < half)) r.x = fmaf(-2.f * c2, rcp_approx(ptx::ex2_approx(s.x * up) + 1.f), c2);
+    if (!(fabsf(s.y) < half)) r.y = fmaf(-2.f * c2, rcp_approx(ptx::ex2_approx(s.y * up) + 1.f), c2);
     acc[i] = ptx::pack2(r.x, r.y);
   }
 }
@@ -753,28 +774,20 @@ __device__ __forceinline__ void add_bias(uint64_t (&acc)[HC / 2], uint32_t slope
   }
 }
 
-// Position t for the rows whose query sees neither its prefix nor its window there.  (A part's rows are mostly of one
-// query.)
+// Bit i: row col0 + i of the group has a query that sees position t neither in its prefix nor from its start on.
 template <int HC>
-__device__ __forceinline__ void hide_between(uint64_t (&acc)[HC / 2], const DenseParams& p, const Rows& it, int col0,
-                                             long long t) {
-  int b = -1;
-  bool hidden = false;
-#pragma unroll
-  for (int i = 0; i < HC; ++i) {
-    const int r = col0 + i;
-    if (r < it.nrows) {
-      const int at = it.req * p.q_per_req + (it.row0 + r) / p.H;
-      if (at != b) {
-        b = at;
-        const Sight s = sight_of<true>(p, b);
-        hidden = t >= s.pre && t < s.start;
-      }
-    }
-    float2 d = ptx::unpack2(acc[i / 2]);
-    if (hidden) (i & 1 ? d.y : d.x) = -CUDART_INF_F;
-    acc[i / 2] = ptx::pack2(d.x, d.y);
+__device__ __noinline__ uint32_t hidden_rows(const int32_t* starts, const int32_t* prefix_lens, int b, int head, int H, int rows,
+                                             int t) {
+  uint32_t hidden = 0;
+#pragma unroll 1
+  for (int i = 0; i < min(rows, HC);) {                     // a query's rows at a time
+    const int n = min(H - head, HC - i), pre = prefix_lens ? __ldg(prefix_lens + b) : 0;
+    if (t >= pre && t < __ldg(starts + b)) hidden |= (n < 32 ? (1u << n) - 1u : ~0u) << i;
+    i += n;
+    head = 0;
+    ++b;
   }
+  return hidden;
 }
 
 template <int NR, bool kMasked>
@@ -809,6 +822,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
 #pragma unroll
   for (int j = 0; j < kRefs; ++j) ref[j] = CUDART_NAN_F, top[j] = 0.f, upper[j] = lower[j] = -CUDART_INF_F;
   bool live = false;                                    // the part has rows
+  bool steep = false;                                   // this lane's row keeps its references in tiles far below
 
   // every PV of the tiles before is done: their accumulators (dims 128 b + tok) can be read and scaled
   auto wait_pv = [&]() {
@@ -922,6 +936,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
             ptx::sts32f(base + C::kSlope + (col0 + lane) * 4,
                         r < p.q_per_req * p.H ? __ldg(p.slopes + r % p.H) * kLog2e : 0.f);
           ptx::named_bar_sync(1 + part, 128);
+          steep = ptx::lds32f(base + C::kSlope + (col0 + row) * 4) * kDenseTile >= kSteep;
         }
       }
     }
@@ -1035,7 +1050,19 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
         acc[i / 2] = ptx::pack2(d.x, d.y);
       }
       if constexpr (kMasked) {
-        if (p.starts) hide_between<HC>(acc, p, rows_of(p, item), col0, t);
+        const Rows it = rows_of(p, item);
+        const int b = (it.row0 + col0) / p.H, head = it.row0 + col0 - b * p.H;
+        const uint32_t hidden = p.starts && live ? hidden_rows<HC>(p.starts, p.prefix_lens, it.req * p.q_per_req + b, head,
+                                                                  p.H, it.nrows - col0, (int)t) : 0u;
+        if (hidden) {
+#pragma unroll
+          for (int i = 0; i < HC; i += 2) {
+            float2 d = ptx::unpack2(acc[i / 2]);
+            if (hidden >> i & 1) d.x = -CUDART_INF_F;
+            if (hidden >> (i + 1) & 1) d.y = -CUDART_INF_F;
+            acc[i / 2] = ptx::pack2(d.x, d.y);
+          }
+        }
       }
       if (!here || !w.n.seen_by_all(t)) clean_codes<NR>(base, kslot, tok, part, here && w.n.seen(t));
     }
@@ -1079,7 +1106,8 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
       for (int j = 0; j < kRefs; ++j) {
         const float r = ceilf(m[j] - kTopOperand);
         // (a row without positions here, or of NaNs alone, keeps what it has)
-        const bool moves = m[j] > -CUDART_INF_F && !(r <= ref[j] && r >= ref[j] - kWindow), set = ref[j] == ref[j];
+        const bool set = ref[j] == ref[j];
+        const bool moves = m[j] > -CUDART_INF_F && !(r <= ref[j] && (r >= ref[j] - kWindow || (kMasked && steep)));
         const float next = set ? fmaxf(r > ref[j] ? r + 1.f : r + kWindow / 2, top[j] - kLowest) : r + kWindow / 2;
         to[j] = moves ? next : ref[j];
         high = fmaxf(high, to[j]);
@@ -1101,7 +1129,8 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
           top[j] = ref[j] == ref[j] ? fmaxf(top[j], next) : next;
           ref[j] = next;
           upper[j] = next + kTopOperand;                // (one that is as low as it may be stays below its window)
-          lower[j] = next <= fmaxf(top[j] - kLowest, level - kFactor) ? -CUDART_INF_F : upper[j] - 1.f - kWindow;
+          lower[j] = next <= fmaxf(top[j] - kLowest, level - kFactor) || (kMasked && steep) ? -CUDART_INF_F
+                                                                                            : upper[j] - 1.f - kWindow;
         }
         moves |= f[j] != 1.f;
       }
