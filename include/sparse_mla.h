@@ -439,6 +439,40 @@ int sparse_mla_masked_decode(const smla_dense_dims* dims, const void* q, const v
                              const float* slopes, const int32_t* starts, const int32_t* prefix_lens, void* out, float* lse,
                              void* workspace, size_t workspace_bytes, smla_stream_t stream);
 
+/* Shapes of one decode behind shared prefixes. */
+typedef struct smla_shared_dims {
+  int32_t batch;              /* B decode queries, 1 .. 65535                            */
+  int32_t num_heads;          /* H, 1 .. 128                                             */
+  int32_t page_size;          /* tokens per page; must be 64                             */
+  int32_t max_pages_per_seq;  /* row length of block_table, >= 1                         */
+  int32_t d_latent;           /* must be 512                                             */
+  int32_t d_rope;             /* must be 64                                              */
+  int64_t num_pages;          /* pages in kv_cache, 1 .. 2^31 - 1                        */
+  int32_t queries_per_request;/* as in smla_dense_dims                                   */
+  int32_t num_prefixes;       /* G >= 1, a divisor of the number of requests             */
+  int32_t prefix_pages;       /* row length of prefix_table, >= 1                        */
+} smla_shared_dims;
+
+/* Bytes of workspace that sparse_mla_shared_decode needs on a device with
+ * sm_count SMs (host only).  Statuses as sparse_mla_dense_plan_for. */
+int sparse_mla_shared_workspace_size(const smla_shared_dims* dims, int32_t sm_count, size_t* bytes);
+
+/* sparse_mla_dense_decode of requests that share prefixes: R requests in G
+ * groups of R / G; query b of request r attends over the first
+ * prefix_lens[r / (R / G)] positions of its group's row of prefix_table, then
+ * over the first seq_lens[b] of its own row of block_table.  The records of a
+ * prefix are read once for all rows that share it.
+ *   prefix_table int32 [G][prefix_pages], prefix_lens int32 [G]
+ *   seq_lens     int32 [B]: lengths without the prefix (0 is fine)
+ *   workspace    sparse_mla_shared_workspace_size bytes, 256-byte aligned; its first 4
+ *                bytes are the device error word.  Concurrent calls must not share it.
+ * Everything else, errors and numerics among it, as in
+ * sparse_mla_dense_decode; SMLA_ERR_INVALID_ARG also where G does not divide R. */
+int sparse_mla_shared_decode(const smla_shared_dims* dims, const void* q, const void* kv_cache,
+                             const int32_t* prefix_table, const int32_t* prefix_lens, const int32_t* block_table,
+                             const int32_t* seq_lens, float sm_scale, void* out, float* lse, void* workspace,
+                             size_t workspace_bytes, smla_stream_t stream);
+
 /* Shapes of one attention-weight call. */
 typedef struct smla_weights_dims {
   int32_t batch;              /* B decode queries, 0 .. 65535                            */

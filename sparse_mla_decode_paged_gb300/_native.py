@@ -48,6 +48,13 @@ class SmlaDensePlan(C.Structure):
                 ("reserved", C.c_int32), ("workspace_bytes", C.c_size_t)]
 
 
+class SmlaSharedDims(C.Structure):
+    _fields_ = [("batch", C.c_int32), ("num_heads", C.c_int32), ("page_size", C.c_int32),
+                ("max_pages_per_seq", C.c_int32), ("d_latent", C.c_int32), ("d_rope", C.c_int32),
+                ("num_pages", C.c_int64), ("queries_per_request", C.c_int32), ("num_prefixes", C.c_int32),
+                ("prefix_pages", C.c_int32)]
+
+
 class SmlaWeightsDims(C.Structure):
     _fields_ = [("batch", C.c_int32), ("num_heads", C.c_int32), ("page_size", C.c_int32),
                 ("max_pages_per_seq", C.c_int32), ("d_latent", C.c_int32), ("d_rope", C.c_int32),
@@ -90,6 +97,9 @@ _SIGS = {
                                           C.c_size_t, _P]),
     "sparse_mla_masked_decode": (C.c_int, [C.POINTER(SmlaDenseDims), _P, _P, _P, _P, C.c_float, C.c_float, _P, _P, _P, _P,
                                            _P, _P, C.c_size_t, _P]),
+    "sparse_mla_shared_workspace_size": (C.c_int, [C.POINTER(SmlaSharedDims), C.c_int32, C.POINTER(C.c_size_t)]),
+    "sparse_mla_shared_decode": (C.c_int, [C.POINTER(SmlaSharedDims), _P, _P, _P, _P, _P, _P, C.c_float, _P, _P, _P,
+                                           C.c_size_t, _P]),
     "sparse_mla_attention_weights": (C.c_int, [C.POINTER(SmlaWeightsDims), _P, _P, _P, _P, _P, C.c_float, C.c_float, _P,
                                                _P, _P]),
     "sparse_mla_kv_evict_workspace_size": (C.c_size_t, [C.POINTER(SmlaEvictDims)]),

@@ -12,7 +12,7 @@ import torch
 
 from . import _native
 from ._native import (SmlaAppendDims, SmlaDenseDims, SmlaDensePlan, SmlaDims, SmlaEvictDims, SmlaNormAppendDims,
-                      SmlaNormRopeDims, SmlaPlan, SmlaTopkDims, SmlaWeightsDims, check)
+                      SmlaNormRopeDims, SmlaPlan, SmlaSharedDims, SmlaTopkDims, SmlaWeightsDims, check)
 
 PAGE_SIZE, D_LATENT, D_ROPE, D_QK = 64, 512, 64, 576
 
@@ -647,6 +647,70 @@ def _masked_dims(q, kv_cache, block_table, seq_lens, slopes, starts, prefix_lens
     _same_device(q.device, kv_cache=kv_cache, block_table=block_table, seq_lens=seq_lens, slopes=slopes, starts=starts,
                  prefix_lens=prefix_lens, out=out, lse=lse, workspace=workspace)
     return dense_dims_of(q, kv_cache, block_table, ctas)
+
+
+def shared_dims_of(q, kv_cache, prefix_table, block_table) -> SmlaSharedDims:
+    """Shapes of a decode behind shared prefixes; several queries per request when q has a multiple of block_table's
+    rows."""
+    return SmlaSharedDims(q.shape[0], q.shape[1], PAGE_SIZE, block_table.shape[1], D_LATENT, D_ROPE, kv_cache.shape[0],
+                          q.shape[0] // block_table.shape[0], prefix_table.shape[0], prefix_table.shape[1])
+
+
+def alloc_shared_workspace(q, kv_cache, prefix_table, block_table) -> torch.Tensor:
+    """Caller-owned workspace of sparse_mla_shared_decode with a clear error word."""
+    return _shared_workspace(shared_dims_of(q, kv_cache, prefix_table, block_table), q.device)
+
+
+def _shared_workspace(dims: SmlaSharedDims, dev) -> torch.Tensor:
+    n = C.c_size_t(0)
+    sms = torch.cuda.get_device_properties(dev).multi_processor_count
+    check("sparse_mla_shared_workspace_size", _lib().sparse_mla_shared_workspace_size(dims, sms, C.byref(n)))
+    ws = torch.empty(n.value, dtype=torch.uint8, device=dev)
+    ws[:256].zero_()
+    return ws
+
+
+def sparse_mla_shared_decode(q: torch.Tensor, kv_cache: torch.Tensor, prefix_table: torch.Tensor,
+                             prefix_lens: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                             sm_scale: float, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                             workspace: Optional[torch.Tensor] = None,
+                             stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """sparse_mla_dense_decode of R requests in G groups of R / G that share a prefix each: prefix_table int32 [G, pages],
+    prefix_lens int32 [G]; block_table [R, pages] and seq_lens [B] are the requests' own positions behind it.
+
+    Calls in flight at once need a workspace each (alloc_shared_workspace); without one a call allocates its own, and
+    its error word is lost."""
+    key = _call_key((q, kv_cache, prefix_table, prefix_lens, block_table, seq_lens, out, lse, workspace), "shared_decode")
+    dims = _CHECKED.get(key) or _remember(key, _shared_dims(q, kv_cache, prefix_table, prefix_lens, block_table, seq_lens,
+                                                            out, lse, workspace))
+    dev = q.device
+    with _on(dev, stream) as st:
+        if out is None:
+            out = torch.empty((q.shape[0], q.shape[1], D_LATENT), dtype=torch.bfloat16, device=dev)
+        if lse is None:
+            lse = torch.empty((q.shape[0], q.shape[1]), dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = _shared_workspace(dims, dev)
+        r = _lib().sparse_mla_shared_decode(
+            dims, q.data_ptr(), kv_cache.data_ptr(), prefix_table.data_ptr(), prefix_lens.data_ptr(),
+            block_table.data_ptr(), seq_lens.data_ptr(), sm_scale, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+            workspace.numel(), st)
+    if r != 0:
+        check("sparse_mla_shared_decode", r)
+    return out, lse
+
+
+def _shared_dims(q, kv_cache, prefix_table, prefix_lens, block_table, seq_lens, out, lse, workspace) -> SmlaSharedDims:
+    _need_queries(q, kv_cache, block_table, seq_lens)
+    _need(prefix_table, "prefix_table", torch.int32, 2)
+    _need(prefix_lens, "prefix_lens", torch.int32, 1)
+    G = prefix_table.shape[0]
+    if G < 1 or block_table.shape[0] % G != 0 or prefix_lens.shape[0] != G:
+        raise ValueError("prefix_table and prefix_lens need one row per group, a divisor of the number of requests")
+    _need_outputs(q, out, lse, workspace)
+    _same_device(q.device, kv_cache=kv_cache, prefix_table=prefix_table, prefix_lens=prefix_lens, block_table=block_table,
+                 seq_lens=seq_lens, out=out, lse=lse, workspace=workspace)
+    return shared_dims_of(q, kv_cache, prefix_table, block_table)
 
 
 def _need_slots(t, name: str, dtype, rows: int):

@@ -676,3 +676,95 @@ extern "C" int sparse_mla_kv_evict(const smla_evict_dims* d, float* weights, int
   p.err = err_word;
   return launch_evict(p, sms, (cudaStream_t)stream) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
 }
+
+namespace {
+
+// How a shared decode runs on a device with `sms` SMs.
+struct SharedPlan {
+  int nr, own_groups, prefix_groups;
+  size_t results_at, lse_at, bytes;        // parts of the workspace behind the dense decode's
+};
+
+int shared_plan(const smla_shared_dims* d, int sms, SharedPlan* plan) {
+  if (!d || sms < 1) return SMLA_ERR_INVALID_ARG;
+  const int sq = d->queries_per_request > 1 ? d->queries_per_request : 1;
+  if (d->batch < 1 || d->num_heads < 1 || d->max_pages_per_seq < 1 || d->prefix_pages < 1 || d->num_prefixes < 1 ||
+      d->num_pages < 1 || d->queries_per_request < 0 || d->batch % sq != 0 || d->batch / sq % d->num_prefixes != 0)
+    return SMLA_ERR_INVALID_ARG;
+  if (d->page_size != kPageSize || d->d_latent != kDLatent || d->d_rope != kDRope) return SMLA_ERR_UNSUPPORTED;
+  if (d->batch > kMaxBatch || d->num_heads > kDenseMaxHeads || d->num_pages > 0x7fffffff) return SMLA_ERR_UNSUPPORTED;
+  const int ctas = sms < kDenseMaxCtas ? sms : kDenseMaxCtas;
+  const int64_t requests = d->batch / sq, rows = (int64_t)sq * d->num_heads, all = (int64_t)d->batch * d->num_heads;
+  const int64_t prefix_rows = all / d->num_prefixes;
+  auto tiles = [&](int nr) {
+    return requests * ((rows + nr - 1) / nr) * ((d->max_pages_per_seq + (int64_t)1) / 2) +
+           d->num_prefixes * ((prefix_rows + nr - 1) / nr) * ((d->prefix_pages + (int64_t)1) / 2);
+  };
+  plan->nr = dense_rows_per_cta(prefix_rows, ctas, tiles);
+  if (tiles(plan->nr) / ctas >= 0x7fffffff) return SMLA_ERR_UNSUPPORTED;     // a CTA counts its tiles in 32 bits
+  plan->own_groups = (int)((rows + plan->nr - 1) / plan->nr);
+  plan->prefix_groups = (int)((prefix_rows + plan->nr - 1) / plan->nr);
+  plan->results_at = dense_workspace_bytes(ctas, plan->nr);
+  plan->lse_at = plan->results_at + (size_t)2 * all * kDLatent * sizeof(float);
+  plan->bytes = plan->lse_at + (size_t)2 * all * sizeof(float);
+  return SMLA_OK;
+}
+
+}  // namespace
+
+extern "C" int sparse_mla_shared_workspace_size(const smla_shared_dims* d, int32_t sm_count, size_t* bytes) {
+  SharedPlan plan;
+  if (!bytes) return SMLA_ERR_INVALID_ARG;
+  const int st = shared_plan(d, sm_count, &plan);
+  if (st == SMLA_OK) *bytes = plan.bytes;
+  return st;
+}
+
+extern "C" int sparse_mla_shared_decode(const smla_shared_dims* d, const void* q, const void* kv_cache,
+                                        const int32_t* prefix_table, const int32_t* prefix_lens, const int32_t* block_table,
+                                        const int32_t* seq_lens, float sm_scale, void* out, float* lse, void* workspace,
+                                        size_t workspace_bytes, smla_stream_t stream) {
+  SharedPlan plan;
+  int st = shared_plan(d, kDenseMaxCtas, &plan);
+  if (st != SMLA_OK) return st;
+  st = check_inputs(q, kv_cache, block_table, seq_lens, seq_lens);
+  if (st != SMLA_OK) return st;
+  if (!prefix_table || !prefix_lens || !aligned(prefix_table, 4) || !aligned(prefix_lens, 4)) return SMLA_ERR_INVALID_ARG;
+  if (!out || !lse || !aligned(out, 16) || !aligned(lse, 4)) return SMLA_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < kWorkspaceHeader || !aligned(workspace, 256)) return SMLA_ERR_WORKSPACE;
+  int sms = 0;
+  st = sm_count_of_current_device(&sms);
+  if (st != SMLA_OK) return st;
+  st = shared_plan(d, sms, &plan);
+  if (st != SMLA_OK) return st;
+  if (workspace_bytes < plan.bytes) return SMLA_ERR_WORKSPACE;
+  SharedParams s{};
+  DenseParams& p = s.dense;
+  p.q = static_cast<const uint16_t*>(q);
+  p.kv = static_cast<const uint8_t*>(kv_cache);
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.sm_scale = sm_scale;
+  p.B = d->batch;
+  p.H = d->num_heads;
+  p.q_per_req = d->queries_per_request > 1 ? d->queries_per_request : 1;
+  p.max_pages = d->max_pages_per_seq;
+  p.num_pages = d->num_pages;
+  p.requests = p.B / p.q_per_req;
+  p.nr = plan.nr;
+  p.groups = plan.own_groups;
+  p.ctas = sms < kDenseMaxCtas ? sms : kDenseMaxCtas;
+  p.shared_table = prefix_table;
+  p.shared_lens = prefix_lens;
+  p.prefixes = d->num_prefixes;
+  p.shared_pages = d->prefix_pages;
+  p.prefix_rows = p.B / d->num_prefixes * p.H;
+  p.prefix_groups = plan.prefix_groups;
+  p.out32 = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.results_at);
+  p.lse32 = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.lse_at);
+  p.err = static_cast<uint32_t*>(workspace);
+  p.wait_ns = split_wait_limit_ns();
+  s.out = static_cast<uint16_t*>(out);
+  s.lse = lse;
+  return launch_shared(s, (cudaStream_t)stream) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+}

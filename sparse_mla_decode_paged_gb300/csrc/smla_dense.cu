@@ -50,6 +50,7 @@
 
 #include <atomic>
 #include <cstddef>
+#include <functional>
 
 #include "smla_dense_parts.cuh"
 #include "smla_device.cuh"
@@ -75,6 +76,10 @@ constexpr int kLeastExponent = -60;       // of the scale that a position counts
 // tanh(x) / x - 1 as a polynomial in x^2, |x| < 1/2
 constexpr float kTanh1 = -0.333331436f, kTanh2 = 0.13325879f, kTanh3 = -0.0530454926f, kTanh4 = 0.017241491f;
 constexpr int kMostTiles16 = 4, kMostTiles32 = 24;   // tiles of a CTA up to which row groups are of 16 and of 32
+
+// Forms of the kernel: the plain decode; scores capped, biased and masked; requests and the prefixes that groups of them
+// share, whose items all lie on the one line of tiles, with results in fp32 for the join.
+enum { kPlain, kMasked, kShared };
 
 // Warps: the softmax warps (warp w: TMEM lanes of quadrant w % 4, row part w / 4), then one warp each for the
 // copies, the QK and the PV, and one that describes the run for the merge.
@@ -172,16 +177,23 @@ __device__ __forceinline__ void init_bars(Bars* bars, const DenseParams& p, int 
   ptx::fence_mbar_init();
 }
 
-// One (request, row group): rows row0 .. row0 + nrows - 1 of the request's s_q H rows.
+// One (request, row group): rows row0 .. row0 + nrows - 1 of the request's s_q H rows, or of the rows of the requests that
+// share a prefix (form kShared); `first` is row 0 of them among all rows.
 struct Rows {
-  int req, row0, nrows;
+  int req, row0, nrows, first;
+  bool prefix;
 };
 
+template <int kForm>
 __device__ __forceinline__ Rows rows_of(const DenseParams& p, int i) {
   Rows r;
-  r.req = i / p.groups;
-  r.row0 = (i - r.req * p.groups) * p.nr;
-  r.nrows = min(p.nr, p.q_per_req * p.H - r.row0);
+  r.prefix = kForm == kShared && i >= p.requests * p.groups;
+  const int groups = r.prefix ? p.prefix_groups : p.groups, rows = r.prefix ? p.prefix_rows : p.q_per_req * p.H;
+  if (r.prefix) i -= p.requests * p.groups;
+  r.req = i / groups;
+  r.row0 = (i - r.req * groups) * p.nr;
+  r.nrows = min(p.nr, rows - r.row0);
+  r.first = r.req * rows + r.row0;
   return r;
 }
 
@@ -191,15 +203,19 @@ __device__ __forceinline__ int clamped_len(const DenseParams& p, int b) {
   return (int)min(n, table);
 }
 
+__device__ __forceinline__ int clamped_prefix(const DenseParams& p, int group) {
+  return (int)min((long long)max(__ldg(p.shared_lens + group), 0), (long long)p.shared_pages * kPageSize);
+}
+
 // What a query sees: positions below pre and from start up to len (start 0, pre 0: all below len).
 struct Sight {
   int len, start, pre;
 };
 
-template <bool kMasked>
+template <int kForm>
 __device__ __forceinline__ Sight sight_of(const DenseParams& p, int b) {
   Sight s{clamped_len(p, b), 0, 0};
-  if constexpr (kMasked) {
+  if constexpr (kForm == kMasked) {
     if (p.starts) {
       s.start = min(max(__ldg(p.starts + b), 0), s.len);
       if (p.prefix_lens) s.pre = min(max(__ldg(p.prefix_lens + b), 0), s.len);
@@ -211,7 +227,7 @@ __device__ __forceinline__ Sight sight_of(const DenseParams& p, int b) {
 
 // Lengths of an item's queries (clamped to [0, table]) and its tiles: at least 1, so that a group without
 // positions has one empty tile.
-template <bool kMasked>
+template <int kForm>
 struct Lens {
   int max_len, min_len, tiles;
   __device__ __forceinline__ int at(int t) const { return t; }                  // the tile's place in the request
@@ -224,7 +240,7 @@ struct Lens {
 // With a mask: the tiles that hold positions below max_pre, then those from the first that holds a position at or past
 // min_start (of the queries that have one) on.
 template <>
-struct Lens<true> {
+struct Lens<kMasked> {
   int max_len, min_len, tiles;
   int max_pre, min_pre, min_start, max_start, pre_tiles, skip;
   bool back;                                               // the last tile first
@@ -244,22 +260,28 @@ struct Lens<true> {
   __device__ __forceinline__ bool seen_by_all(long long t) const { return t < min_len && (t >= max_start || t < min_pre); }
 };
 
-template <bool kMasked>
-__device__ __forceinline__ Lens<kMasked> lens_of(const DenseParams& p, const Rows& r) {
-  Lens<kMasked> n;
+template <int kForm>
+__device__ __forceinline__ Lens<kForm> lens_of(const DenseParams& p, const Rows& r) {
+  Lens<kForm> n;
   n.max_len = 0;
   n.min_len = 0x7fffffff;
-  if constexpr (kMasked) {
+  if constexpr (kForm == kMasked) {
     n.max_pre = n.max_start = 0;
     n.min_pre = n.min_start = 0x7fffffff;
   }
   int b = r.req * p.q_per_req + r.row0 / p.H;
-  const int last = r.req * p.q_per_req + (r.row0 + r.nrows - 1) / p.H;
+  int last = r.req * p.q_per_req + (r.row0 + r.nrows - 1) / p.H;
+  if constexpr (kForm == kShared) {
+    if (r.prefix) {
+      n.max_len = n.min_len = clamped_prefix(p, r.req);
+      last = b - 1;
+    }
+  }
 #pragma unroll 1
   for (; b <= last; ++b) {
-    const Sight s = sight_of<kMasked>(p, b);
+    const Sight s = sight_of<kForm>(p, b);
     n.min_len = min(n.min_len, s.len);
-    if constexpr (kMasked) {
+    if constexpr (kForm == kMasked) {
       n.max_pre = max(n.max_pre, s.pre);
       n.min_pre = min(n.min_pre, s.pre);
       n.max_start = max(n.max_start, s.start);
@@ -272,7 +294,7 @@ __device__ __forceinline__ Lens<kMasked> lens_of(const DenseParams& p, const Row
     }
   }
   const int end = (int)(((long long)n.max_len + kDenseTile - 1) / kDenseTile);
-  if constexpr (kMasked) {
+  if constexpr (kForm == kMasked) {
     n.pre_tiles = (int)(((long long)n.max_pre + kDenseTile - 1) / kDenseTile);
     const int from = end > 0 ? max(n.min_start / kDenseTile, n.pre_tiles) : 0;
     n.skip = max(from - n.pre_tiles, 0);
@@ -297,16 +319,16 @@ struct RunDesc {
 };
 
 // Walks the (item, tile) pairs of a run; every role has its own:  while (w.here(p)) { ...; w.next(); }
-template <bool kMasked>
+template <int kForm>
 struct Walk {
   int i, t, left;
   bool entered = false;
-  Lens<kMasked> n;
+  Lens<kForm> n;
   __device__ __forceinline__ explicit Walk(const Bars* bars)
       : i(bars->first_item), t(bars->first_tile), left((int)(bars->run_end - bars->run_begin)) {}
   __device__ __forceinline__ bool here(const DenseParams& p) {
     if (left > 0 && !entered) {
-      n = lens_of<kMasked>(p, rows_of(p, i));
+      n = lens_of<kForm>(p, rows_of<kForm>(p, i));
       entered = true;
     }
     return left > 0;
@@ -325,19 +347,21 @@ struct Walk {
 // ----------------------------------------------------------------------------- copies
 
 // Entry `lane` of 16 tiles from the item's t-th on, two pages each.
-template <bool kMasked>
-__device__ __forceinline__ int page_entry(const DenseParams& p, int req, const Lens<kMasked>& n, int t, int lane) {
+template <int kForm>
+__device__ __forceinline__ int page_entry(const DenseParams& p, const Rows& r, const Lens<kForm>& n, int t, int lane) {
   t += lane >> 1;
-  const int lp = t < n.tiles ? 2 * n.at(t) + (lane & 1) : p.max_pages;
-  return lp < p.max_pages && n.sees_page(lp) ? __ldg(p.block_table + (size_t)req * p.max_pages + lp) : -1;
+  const int pages = kForm == kShared && r.prefix ? p.shared_pages : p.max_pages;
+  const int32_t* table = kForm == kShared && r.prefix ? p.shared_table : p.block_table;
+  const int lp = t < n.tiles ? 2 * n.at(t) + (lane & 1) : pages;
+  return lp < pages && n.sees_page(lp) ? __ldg(table + (size_t)r.req * pages + lp) : -1;
 }
 
-template <int NR, bool kMasked>
+template <int NR, int kForm>
 __device__ void copy_role(const DenseParams& p, const CUtensorMap* map, const CUtensorMap* smap, uint32_t base,
                           Bars* bars, int lane) {
   using C = DC<NR>;
-  Walk<kMasked> w(bars);
-  int req = 0;
+  Walk<kForm> w(bars);
+  Rows r{};
   Ring<C::kRing> k;
   Ring<C::kScaleSlots> sc;
   Ring<C::kRopeSlots> rope;
@@ -350,20 +374,22 @@ __device__ void copy_role(const DenseParams& p, const CUtensorMap* map, const CU
     const bool enters = item != w.i;
     if (enters) {
       item = w.i;
-      const Rows r = rows_of(p, item);
-      req = r.req;
-      nxt = page_entry(p, req, w.n, w.t, lane);
-      if (lane == 0) {
-        const int last = req * p.q_per_req + (r.row0 + r.nrows - 1) / p.H;
+      r = rows_of<kForm>(p, item);
+      nxt = page_entry(p, r, w.n, w.t, lane);
+      if (kForm == kShared && r.prefix) {
+        if (lane == 0 && __ldg(p.shared_lens + r.req) > (long long)p.shared_pages * kPageSize)
+          atomicOr(p.err, SMLA_DEVERR_PAGE_RANGE);
+      } else if (lane == 0) {
+        const int last = r.req * p.q_per_req + (r.row0 + r.nrows - 1) / p.H;
 #pragma unroll 1
-        for (int b = req * p.q_per_req + r.row0 / p.H; b <= last; ++b)
+        for (int b = r.req * p.q_per_req + r.row0 / p.H; b <= last; ++b)
           if (__ldg(p.seq_lens + b) > (long long)p.max_pages * kPageSize) atomicOr(p.err, SMLA_DEVERR_PAGE_RANGE);
       }
     }
     if (enters || w.t == base_t + 16) {
       base_t = w.t;
       cur = nxt;
-      nxt = page_entry(p, req, w.n, w.t + 16, lane);
+      nxt = page_entry(p, r, w.n, w.t + 16, lane);
     }
     const int at = 2 * (w.t - base_t);
     const int pg[2] = {__shfl_sync(0xffffffffu, cur, at), __shfl_sync(0xffffffffu, cur, at + 1)};
@@ -429,11 +455,11 @@ __device__ void copy_role(const DenseParams& p, const CUtensorMap* map, const CU
 
 // ----------------------------------------------------------------------------- MMA issue
 
-template <int NR, bool kMasked>
+template <int NR, int kForm>
 __device__ void qk_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars* bars, int lane) {
   using C = DC<NR>;
   constexpr uint32_t kIdescCodes = ptx::idesc_e4m3(128, C::kOCols), kIdescRope = ptx::idesc_bf16(128, NR);
-  Walk<kMasked> w(bars);
+  Walk<kForm> w(bars);
   Ring<C::kRing> k;
   Ring<C::kSBufs> s;
   Ring<C::kRopeSlots> rope;
@@ -483,12 +509,12 @@ __device__ void qk_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars
   __syncwarp();
 }
 
-template <int NR, bool kMasked>
+template <int NR, int kForm>
 __device__ void pv_role(const DenseParams& p, uint32_t base, uint32_t tmem, Bars* bars, int lane) {
   using C = DC<NR>;
   constexpr int N = C::kOCols;
   constexpr uint32_t kIdesc = ptx::idesc_e4m3(128, N) | (1u << 15) | (1u << 16);     // A and B MN-major
-  Walk<kMasked> w(bars);
+  Walk<kForm> w(bars);
   Ring<C::kRing> k;
   Ring<C::kPBufs> pb;
   uint32_t ok = p.wait_ns >= kLeastWaitNs;
@@ -549,16 +575,16 @@ __device__ __forceinline__ float reduce_scatter(float (&v)[N], int lane, Op op) 
 
 // Rows of one item into the Q operands: hi and lo E4M3 codes of the latent part scaled by 2^-x, the rope as it is;
 // each row's factor 2^x sm_scale log2 e and length go to buffer `buf`.
-template <int NR>
+template <int NR, int kForm>
 __device__ __forceinline__ void load_q(const DenseParams& p, int item, unsigned char* sm, uint32_t base, int buf,
                                        int warp, int lane) {
   using C = DC<NR>;
   constexpr int kRows = NR / C::kSoftWarps;             // rows warp, warp + kSoftWarps, ... of this warp
-  const Rows it = rows_of(p, item);
+  const Rows it = rows_of<kForm>(p, item);
   float* f = reinterpret_cast<float*>(sm + C::kF) + buf * NR;
   int* lens = reinterpret_cast<int*>(sm + C::kLen) + buf * NR;
   const float kf = p.sm_scale * kLog2e;
-  const uint16_t* q0 = p.q + ((size_t)it.req * p.q_per_req * p.H + it.row0) * kDQK;
+  const uint16_t* q0 = p.q + (size_t)it.first * kDQK;
   const int b = lane >> 3, u = lane & 7;
   uint4 raw[kRows][2], rope[(kRows + 3) / 4];
 #pragma unroll
@@ -580,7 +606,8 @@ __device__ __forceinline__ void load_q(const DenseParams& p, int item, unsigned 
   }
   if (lane < kRows) {
     const int r = warp + C::kSoftWarps * lane;
-    lens[r] = r < it.nrows ? clamped_len(p, it.req * p.q_per_req + (it.row0 + r) / p.H) : 0x7fffffff;
+    if (kForm == kShared && it.prefix) lens[r] = r < it.nrows ? clamped_prefix(p, it.req) : 0x7fffffff;
+    else lens[r] = r < it.nrows ? clamped_len(p, it.req * p.q_per_req + (it.row0 + r) / p.H) : 0x7fffffff;
   }
 #pragma unroll
   for (int i = 0; i < (kRows + 3) / 4; ++i) {
@@ -790,7 +817,16 @@ __device__ __noinline__ uint32_t hidden_rows(const int32_t* starts, const int32_
   return hidden;
 }
 
-template <int NR, bool kMasked>
+// Where results go: rows' lse (of `it`), and in form kShared the fp32 rows of requests and, behind them, of prefixes.
+template <int kForm>
+__device__ __forceinline__ float* lse_of(const DenseParams& p, const Rows& it) {
+  return (kForm == kShared ? p.lse32 + (it.prefix ? (size_t)p.B * p.H : 0) : p.lse) + it.first;
+}
+__device__ __forceinline__ float* out32_of(const DenseParams& p, const Rows& it) {
+  return p.out32 + (it.prefix ? (size_t)p.B * p.H * kDLatent : 0);
+}
+
+template <int NR, int kForm>
 __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t base, uint32_t tmem, Bars* bars, int warp,
                              int lane, float* o_part, float* lse_part) {
   using C = DC<NR>;
@@ -801,7 +837,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
   const uint32_t lane_base = tmem + ((uint32_t)(32 * quad) << 16);
   const float kf = p.sm_scale * kLog2e;
   const uint32_t row_c = base + C::kRow + warp * C::kRowWarp, row_na = row_c + 4 * HC * 2;
-  Walk<kMasked> w(bars);
+  Walk<kForm> w(bars);
   Ring<C::kSBufs> s;
   Ring<C::kScaleSlots> sc;
   Ring<C::kPBufs> pb;
@@ -822,6 +858,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
 #pragma unroll
   for (int j = 0; j < kRefs; ++j) ref[j] = CUDART_NAN_F, top[j] = 0.f, upper[j] = lower[j] = -CUDART_INF_F;
   bool live = false;                                    // the part has rows
+  const bool changed = kForm == kMasked && (p.softcap > 0.f || p.slopes);    // scores are more than products
   bool steep = false;                                   // this lane's row keeps its references in tiles far below
 
   // every PV of the tiles before is done: their accumulators (dims 128 b + tok) can be read and scaled
@@ -839,15 +876,15 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
       done = item;
       item = w.i;
       buf ^= 1;
-      live = col0 < rows_of(p, item).nrows;
-      load_q<NR>(p, item, sm, base, buf, warp, lane);
+      live = col0 < rows_of<kForm>(p, item).nrows;
+      load_q<NR, kForm>(p, item, sm, base, buf, warp, lane);
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (ok && lane == 0) ptx::mbar_arrive(&bars->qfull);
     }
     if (!more) done = item;
     if (first && done >= 0) {
-      const Rows it = rows_of(p, done);
+      const Rows it = rows_of<kForm>(p, done);
       // row sums over the 128 positions of the tiles
       float ls[HC];
 #pragma unroll
@@ -871,7 +908,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
         const float mz = frexpf(z, &ez);                  // (the exponents meet as whole numbers)
         const float lse = none ? -CUDART_INF_F : z == 0.f ? CUDART_NAN_F : (log2f(mz) + ((float)ez + level)) * kLn2;
         if (quad == 0 && lane < HC && ok && col0 + lane < it.nrows) {
-          if (whole) p.lse[(size_t)it.req * p.q_per_req * p.H + it.row0 + col0 + lane] = lse;
+          if (whole) lse_of<kForm>(p, it)[col0 + lane] = lse;
           else lse_part[slot * NR + col0 + lane] = lse;
         }
         // 2^(R - A) / l, by which a block's accumulators become outputs
@@ -890,7 +927,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
       // with both of the second, and writes them there
       const bool second = lane & 1;
       const int c0 = col0 + (second ? 1 : 0);             // this thread's rows: c0, c0 + 2, ...
-      const size_t row0 = whole ? (size_t)it.req * p.q_per_req * p.H + it.row0 : slot * NR;
+      const size_t row0 = whole ? (size_t)it.first : slot * NR;
       const size_t at = (row0 + c0) * kDLatent + (tok & ~1);
       const int rows_left = ok ? it.nrows - c0 : 0;
       wait_pv();
@@ -914,7 +951,8 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
           }
           const size_t to = at + 128 * b + (size_t)i0 * kDLatent;
           const uint32_t by = fac + (b * HC + i0) * 4;
-          if (whole) write_block<kChunk, true>(x, by, rows_left - i0, second, p.out + to);
+          if (kForm == kShared && whole) write_block<kChunk, false>(x, by, rows_left - i0, second, out32_of(p, it) + to);
+          else if (whole) write_block<kChunk, true>(x, by, rows_left - i0, second, p.out + to);
           else write_block<kChunk, false>(x, by, rows_left - i0, second, o_part + to);
         }
       }
@@ -929,9 +967,9 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
 #pragma unroll
       for (int j = 0; j < kRefs; ++j) ref[j] = CUDART_NAN_F, upper[j] = lower[j] = -CUDART_INF_F;
       level = CUDART_NAN_F;
-      if constexpr (kMasked) {
+      if constexpr (kForm == kMasked) {
         if (p.slopes) {                                     // every warp is past the last item's tiles
-          const int r = rows_of(p, item).row0 + col0 + lane;
+          const int r = rows_of<kForm>(p, item).row0 + col0 + lane;
           if (quad == 0 && lane < HC)
             ptx::sts32f(base + C::kSlope + (col0 + lane) * 4,
                         r < p.q_per_req * p.H ? __ldg(p.slopes + r % p.H) * kLog2e : 0.f);
@@ -1011,7 +1049,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
     ptx::tc_fence_after();
     {
       const uint32_t a = lane_base + C::kSCol + C::kOCols * s.slot + col0;
-      const uint64_t kf2 = ptx::pack2(kf, kf), e2 = kMasked ? 0 : ptx::pack2((float)e, (float)e);
+      const uint64_t kf2 = ptx::pack2(kf, kf), e2 = changed ? 0 : ptx::pack2((float)e, (float)e);
       const uint32_t fa = base + C::kF + (buf * NR + col0) * 4;
       uint32_t r[HC];
       tmem_ld<HC>(a, r);
@@ -1029,13 +1067,15 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
     if (ok && lane == 0) ptx::mbar_arrive(&bars->sempty[s.slot]);
     s.next();
     const int tile = w.n.at(w.t);
-    if constexpr (kMasked) {
+    if constexpr (kForm == kMasked) {
       if (p.softcap > 0.f) cap_scores<HC>(acc, p.softcap);
       if (p.slopes)
         add_bias<HC>(acc, base + C::kSlope + col0 * 4, base + C::kLen + (buf * NR + col0) * 4, tile * kDenseTile + tok);
-      const uint64_t e2 = ptx::pack2((float)e, (float)e);
+      if (changed) {
+        const uint64_t e2 = ptx::pack2((float)e, (float)e);
 #pragma unroll
-      for (int i = 0; i < HC / 2; ++i) acc[i] = ptx::add2(acc[i], e2);
+        for (int i = 0; i < HC / 2; ++i) acc[i] = ptx::add2(acc[i], e2);
+      }
     }
     // positions that a row may not see
     if (__builtin_expect(!w.n.all_see(tile) || pages != 3, 0)) {
@@ -1049,8 +1089,8 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
         if (!here || t >= lens[i + 1]) d.y = -CUDART_INF_F;
         acc[i / 2] = ptx::pack2(d.x, d.y);
       }
-      if constexpr (kMasked) {
-        const Rows it = rows_of(p, item);
+      if constexpr (kForm == kMasked) {
+        const Rows it = rows_of<kForm>(p, item);
         const int b = (it.row0 + col0) / p.H, head = it.row0 + col0 - b * p.H;
         const uint32_t hidden = p.starts && live ? hidden_rows<HC>(p.starts, p.prefix_lens, it.req * p.q_per_req + b, head,
                                                                   p.H, it.nrows - col0, (int)t) : 0u;
@@ -1107,7 +1147,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
         const float r = ceilf(m[j] - kTopOperand);
         // (a row without positions here, or of NaNs alone, keeps what it has)
         const bool set = ref[j] == ref[j];
-        const bool moves = m[j] > -CUDART_INF_F && !(r <= ref[j] && (r >= ref[j] - kWindow || (kMasked && steep)));
+        const bool moves = m[j] > -CUDART_INF_F && !(r <= ref[j] && (r >= ref[j] - kWindow || (kForm == kMasked && steep)));
         const float next = set ? fmaxf(r > ref[j] ? r + 1.f : r + kWindow / 2, top[j] - kLowest) : r + kWindow / 2;
         to[j] = moves ? next : ref[j];
         high = fmaxf(high, to[j]);
@@ -1129,7 +1169,7 @@ __device__ void softmax_role(const DenseParams& p, unsigned char* sm, uint32_t b
           top[j] = ref[j] == ref[j] ? fmaxf(top[j], next) : next;
           ref[j] = next;
           upper[j] = next + kTopOperand;                // (one that is as low as it may be stays below its window)
-          lower[j] = next <= fmaxf(top[j] - kLowest, level - kFactor) || (kMasked && steep) ? -CUDART_INF_F
+          lower[j] = next <= fmaxf(top[j] - kLowest, level - kFactor) || (kForm == kMasked && steep) ? -CUDART_INF_F
                                                                                             : upper[j] - 1.f - kWindow;
         }
         moves |= f[j] != 1.f;
@@ -1290,14 +1330,14 @@ __device__ __forceinline__ void run_bounds(const DenseParams& p, long long T, in
 }
 
 // The items in which the run begins and ends, if they are among i0 .. i1 - 1, whose `mine` tiles begin at tile `at`.
-template <bool kMasked>
+template <int kForm>
 __device__ __forceinline__ void find_ends(const DenseParams& p, Bars* bars, int i0, int i1, long long at, long long mine,
                                           int start, long long a, long long e) {
   if (a >= e || a >= at + mine + (long long)start * i1 || e <= at + (long long)start * i0) return;
   long long x = at;
 #pragma unroll 1
   for (int i = i0; i < i1; ++i) {
-    const int tiles = lens_of<kMasked>(p, rows_of(p, i)).tiles;
+    const int tiles = lens_of<kForm>(p, rows_of<kForm>(p, i)).tiles;
     const long long begin = x + (long long)start * (i + 1), end = begin + tiles;       // the item's tiles on the line
     const long long from = max(a, begin), to = min(e, end);
     if (from < to) {
@@ -1319,16 +1359,21 @@ __device__ __forceinline__ void find_ends(const DenseParams& p, Bars* bars, int 
 
 // A table of at most two pages gives every item one tile: no lengths to add up, nothing to merge (1 x 77 positions 9.2 us
 // instead of 10.2).
-__host__ __device__ __forceinline__ bool one_tile(const DenseParams& p) { return p.max_pages <= 2; }
+__host__ __device__ __forceinline__ bool one_tile(const DenseParams& p) { return p.max_pages <= 2 && p.shared_pages <= 2; }
 
 // Every CTA adds up the tiles of all items.  Few items: one warp, up to four items per lane (the general search's code
 // and barriers take 0.7 us more of a call: 1 x 77 positions 11.0 us instead of 10.3).  Else a run of items per thread,
 // then a scan of the threads' sums.
-template <int kThreads, bool kMasked>
+template <int kForm>
+__device__ __forceinline__ int items_of(const DenseParams& p) {
+  return p.requests * p.groups + (kForm == kShared ? p.prefixes * p.prefix_groups : 0);
+}
+
+template <int kThreads, int kForm>
 __device__ __forceinline__ void find_run(const DenseParams& p, unsigned char* scratch, Bars* bars) {
   if (one_tile(p)) {                                     // an item is a tile: nothing to look up
     if (threadIdx.x == 0) {
-      const int n = p.requests * p.groups, active = min(p.ctas, n), c = min((int)blockIdx.x, active);
+      const int n = items_of<kForm>(p), active = min(p.ctas, n), c = min((int)blockIdx.x, active);
       bars->units = n;
       bars->active = active;
       bars->run_begin = run_start(n, active, c);
@@ -1343,13 +1388,13 @@ __device__ __forceinline__ void find_run(const DenseParams& p, unsigned char* sc
     return;
   }
   if (threadIdx.x == 0) bars->run_begin = bars->run_end = 0;
-  if (p.requests * p.groups <= 128) {
+  if (items_of<kForm>(p) <= 128) {
     if (threadIdx.x < 32) {
-      const int n = p.requests * p.groups, per = (n + 31) >> 5, lane = threadIdx.x;
+      const int n = items_of<kForm>(p), per = (n + 31) >> 5, lane = threadIdx.x;
       const int i0 = min(n, lane * per), i1 = min(n, i0 + per);
       long long mine = 0;
 #pragma unroll 1
-      for (int i = i0; i < i1; ++i) mine += lens_of<kMasked>(p, rows_of(p, i)).tiles;
+      for (int i = i0; i < i1; ++i) mine += lens_of<kForm>(p, rows_of<kForm>(p, i)).tiles;
       __syncwarp();                                      // the empty run is written
       long long upto = mine;
 #pragma unroll
@@ -1360,18 +1405,18 @@ __device__ __forceinline__ void find_run(const DenseParams& p, unsigned char* sc
       long long a, e;
       int start;
       run_bounds(p, __shfl_sync(0xffffffffu, upto, 31), n, bars, lane == 0, start, a, e);
-      find_ends<kMasked>(p, bars, i0, i1, upto - mine, mine, start, a, e);
+      find_ends<kForm>(p, bars, i0, i1, upto - mine, mine, start, a, e);
     }
     __syncthreads();
     return;
   }
   constexpr int kPer = kThreads / 32;
   long long* sums = reinterpret_cast<long long*>(scratch);
-  const int n = p.requests * p.groups, per = (n + kThreads - 1) / kThreads;
+  const int n = items_of<kForm>(p), per = (n + kThreads - 1) / kThreads;
   const int i0 = min(n, (int)threadIdx.x * per), i1 = min(n, i0 + per);
   long long mine = 0;
 #pragma unroll 1
-  for (int i = i0; i < i1; ++i) mine += lens_of<kMasked>(p, rows_of(p, i)).tiles;
+  for (int i = i0; i < i1; ++i) mine += lens_of<kForm>(p, rows_of<kForm>(p, i)).tiles;
   sums[threadIdx.x] = mine;
   __syncthreads();
   if (threadIdx.x < 32) {                                // exclusive prefix over kPer sums per lane
@@ -1398,7 +1443,7 @@ __device__ __forceinline__ void find_run(const DenseParams& p, unsigned char* sc
   const long long T = bars->units;
   __syncthreads();
   run_bounds(p, T, n, bars, threadIdx.x == 0, start, a, e);
-  find_ends<kMasked>(p, bars, i0, i1, sums[threadIdx.x], mine, start, a, e);
+  find_ends<kForm>(p, bars, i0, i1, sums[threadIdx.x], mine, start, a, e);
   __syncthreads();
 }
 
@@ -1413,7 +1458,7 @@ __device__ __forceinline__ RunDesc describe_run(const Bars* bars) {
   return RunDesc{bars->last_item, c1 - c + 1};
 }
 
-template <int NR, bool kMasked>
+template <int NR, int kForm>
 __global__ void __launch_bounds__(DC<NR>::kThreads, 1)
     dense_kernel(const DenseParams p, const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap smap,
                  RunDesc* descs, float* lse_part, float* o_part) {
@@ -1429,7 +1474,7 @@ __global__ void __launch_bounds__(DC<NR>::kThreads, 1)
     ptx::tmem_alloc(&bars->tmem, C::kTmemCols);
     ptx::tmem_relinquish();
   }
-  find_run<C::kThreads, kMasked>(p, sm, bars);            // the scratch is overwritten by the pipeline afterwards
+  find_run<C::kThreads, kForm>(p, sm, bars);            // the scratch is overwritten by the pipeline afterwards
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -1437,12 +1482,12 @@ __global__ void __launch_bounds__(DC<NR>::kThreads, 1)
 
   if (role < 0) {
     ptx::setmaxnreg_inc<C::kSoftRegs>();
-    softmax_role<NR, kMasked>(p, sm, base, tmem, bars, warp, lane, o_part, lse_part);
+    softmax_role<NR, kForm>(p, sm, base, tmem, bars, warp, lane, o_part, lse_part);
   } else {
     ptx::setmaxnreg_dec<C::kMiscRegs>();
-    if (role == kCopyRole) copy_role<NR, kMasked>(p, &map, &smap, base, bars, lane);
-    else if (role == kQkRole) qk_role<NR, kMasked>(p, base, tmem, bars, lane);
-    else if (role == kPvRole) pv_role<NR, kMasked>(p, base, tmem, bars, lane);
+    if (role == kCopyRole) copy_role<NR, kForm>(p, &map, &smap, base, bars, lane);
+    else if (role == kQkRole) qk_role<NR, kForm>(p, base, tmem, bars, lane);
+    else if (role == kPvRole) pv_role<NR, kForm>(p, base, tmem, bars, lane);
     else if (lane == 0) descs[blockIdx.x] = describe_run(bars);
   }
 
@@ -1483,11 +1528,13 @@ __device__ __forceinline__ void add_part(float4& acc, float w, const float4& v) 
   acc.w = fmaf(w, v.w, acc.w);
 }
 
-__device__ __forceinline__ void store_joined(const DenseParams& p, size_t row, int block, int lane, const float4& v,
+template <int kForm>
+__device__ __forceinline__ void store_joined(const DenseParams& p, const Rows& it, int row, int block, int lane, const float4& v,
                                              float lse) {
-  reinterpret_cast<uint2*>(p.out + row * kDLatent + 128 * block)[lane] =
-      make_uint2(f32x2_to_bf16x2(v.x, v.y), f32x2_to_bf16x2(v.z, v.w));
-  if (lane == 0 && block == 0) p.lse[row] = lse;
+  const size_t to = ((size_t)it.first + row) * kDLatent + 128 * block;
+  if constexpr (kForm == kShared) reinterpret_cast<float4*>(out32_of(p, it) + to)[lane] = v;
+  else reinterpret_cast<uint2*>(p.out + to)[lane] = make_uint2(f32x2_to_bf16x2(v.x, v.y), f32x2_to_bf16x2(v.z, v.w));
+  if (lane == 0 && block == 0) lse_of<kForm>(p, it)[row] = lse;
 }
 
 // Joins the partials of the items that cross CTA runs: lse = ln sum_s exp(lse_s), out = sum_s exp(lse_s - lse)
@@ -1499,6 +1546,7 @@ __device__ __forceinline__ void store_joined(const DenseParams& p, size_t row, i
 // positions of 64 heads (6 parts) 62 / 50 us, 10 x 8192 of 64 heads (16 parts) 42.3 / 38.5 us, 10 x 8192 of 16 heads 23.1 /
 // 24.8 us; of 64 parts and more one warp would take its loads in eight rounds.
 // This grid is resident while the decode's still writes, so partials are read from L2, not through the read-only path.
+template <int kForm>
 __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const DenseParams p, const RunDesc* descs,
                                                                     const float* lse_part, const float* o_part) {
   __shared__ int parts_s[kDenseMaxCtas], item_s[kDenseMaxCtas];     // of the item that begins in CTA c, 0: none to join
@@ -1508,6 +1556,7 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const DenseP
   __shared__ float lse_s;
   __shared__ float4 sum_s[4][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (kForm == kShared && tid == 0) ptx::griddep_launch_dependents();    // the join
   ptx::griddep_wait();
   for (int c = tid; c < p.ctas; c += kMergeThreads) {
     const RunDesc d = descs[c];
@@ -1536,7 +1585,7 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const DenseP
   const int nr = p.nr;
   for (int idx = blockIdx.x * (kMergeThreads / 32) + warp; idx < few_s * nr * 4; idx += gridDim.x * (kMergeThreads / 32)) {
     const int c = order_s[idx / (4 * nr)], row = (idx >> 2) % nr, block = idx & 3, parts = parts_s[c];
-    const Rows it = rows_of(p, item_s[c]);
+    const Rows it = rows_of<kForm>(p, item_s[c]);
     if (row >= it.nrows) continue;
     const PartRows rows{c, row, nr};
     const float4* o = reinterpret_cast<const float4*>(o_part) + 32 * block + lane;
@@ -1564,12 +1613,12 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const DenseP
 #pragma unroll
     for (int s = kMergeBatch; s < kFewParts; ++s)
       if (s < parts) add_part(acc, __shfl_sync(0xffffffffu, w, s), v[s - kMergeBatch]);
-    store_joined(p, (size_t)it.req * p.q_per_req * p.H + it.row0 + row, block, lane, acc,
-                 z == 0.f ? -CUDART_INF_F : m + logf(z));
+    store_joined<kForm>(p, it, row, block, lane, acc,
+                        z == 0.f ? -CUDART_INF_F : m + logf(z));
   }
   for (int idx = blockIdx.x; idx < many_s * nr * 4; idx += gridDim.x) {
     const int c = order_s[kDenseMaxCtas - 1 - idx / (4 * nr)], row = (idx >> 2) % nr, block = idx & 3, parts = parts_s[c];
-    const Rows it = rows_of(p, item_s[c]);
+    const Rows it = rows_of<kForm>(p, item_s[c]);
     if (row >= it.nrows) continue;                       // uniform over the CTA
     // warp w takes parts w, w + 4, ...: their rows in flight before the weights are known
     const PartRows rows{c, row, nr};
@@ -1620,7 +1669,7 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const DenseP
     if (warp == 0) {
 #pragma unroll
       for (int s = 1; s < 4; ++s) add_part(acc, 1.f, sum_s[s][lane]);
-      store_joined(p, (size_t)it.req * p.q_per_req * p.H + it.row0 + row, block, lane, acc, lse_s);
+      store_joined<kForm>(p, it, row, block, lane, acc, lse_s);
     }
   }
 }
@@ -1631,9 +1680,9 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const DenseP
 constexpr size_t kDescBytes = (kDenseMaxCtas * sizeof(RunDesc) + 255) / 256 * 256;
 size_t lse_part_bytes(int ctas, int nr) { return ((size_t)2 * ctas * nr * sizeof(float) + 255) / 256 * 256; }
 
-template <int NR, bool kMasked>
+template <int NR, int kForm>
 cudaError_t launch_nr(const DenseParams& p, unsigned char* ws, cudaStream_t stream) {
-  constexpr uint32_t kBytes = kMasked ? DC<NR>::kBytesMasked : DC<NR>::kBytes;
+  constexpr uint32_t kBytes = kForm == kMasked ? DC<NR>::kBytesMasked : DC<NR>::kBytes;
   CUtensorMap map, smap;
   if (!encoder() || !encode_map(&map, p.kv, p.num_pages, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_map(&smap, p.kv, p.num_pages, 16, CU_TENSOR_MAP_SWIZZLE_NONE))
@@ -1644,14 +1693,14 @@ cudaError_t launch_nr(const DenseParams& p, unsigned char* ws, cudaStream_t stre
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !set[dev].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(dense_kernel<NR, kMasked>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    e = cudaFuncSetAttribute(dense_kernel<NR, kForm>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return e;
     if (dev < 64) set[dev].store(true, std::memory_order_relaxed);
   }
   RunDesc* descs = reinterpret_cast<RunDesc*>(ws + kWorkspaceHeader);
   float* lse_part = reinterpret_cast<float*>(ws + kWorkspaceHeader + kDescBytes);
   float* o_part = reinterpret_cast<float*>(ws + kWorkspaceHeader + kDescBytes + lse_part_bytes(p.ctas, NR));
-  dense_kernel<NR, kMasked><<<p.ctas, DC<NR>::kThreads, kBytes, stream>>>(p, map, smap, descs, lse_part, o_part);
+  dense_kernel<NR, kForm><<<p.ctas, DC<NR>::kThreads, kBytes, stream>>>(p, map, smap, descs, lse_part, o_part);
   e = cudaGetLastError();
   if (e != cudaSuccess || one_tile(p)) return e;
   cudaLaunchConfig_t cfg = {};
@@ -1663,22 +1712,35 @@ cudaError_t launch_nr(const DenseParams& p, unsigned char* ws, cudaStream_t stre
   a[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = a;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, dense_merge_kernel, p, (const RunDesc*)descs, (const float*)lse_part,
+  return cudaLaunchKernelEx(&cfg, dense_merge_kernel<kForm == kShared ? kShared : kPlain>, p, (const RunDesc*)descs, (const float*)lse_part,
                             (const float*)o_part);
+}
+
+template <int kForm>
+cudaError_t launch_form(const DenseParams& p, unsigned char* ws, cudaStream_t stream) {
+  if (p.nr == 16) return launch_nr<16, kForm>(p, ws, stream);
+  if (p.nr == 32) return launch_nr<32, kForm>(p, ws, stream);
+  return launch_nr<64, kForm>(p, ws, stream);
 }
 
 }  // namespace
 
+size_t dense_workspace_bytes(int ctas, int nr) {
+  return kWorkspaceHeader + kDescBytes + lse_part_bytes(ctas, nr) + (size_t)2 * ctas * nr * kDLatent * sizeof(float);
+}
+
+// The fewest rows per CTA with which it has at most a few tiles: `tiles` with groups of a given size.
+int dense_rows_per_cta(long long rows, int ctas, const std::function<long long(int)>& tiles) {
+  if (rows <= 16 || tiles(16) <= kMostTiles16 * (long long)ctas) return 16;
+  if (rows <= 32 || tiles(32) <= kMostTiles32 * (long long)ctas) return 32;
+  return 64;
+}
+
 cudaError_t launch_dense(const DenseParams& p, cudaStream_t stream) {
   unsigned char* ws = reinterpret_cast<unsigned char*>(p.err);    // the workspace begins with the error word
-  if (p.softcap > 0.f || p.slopes || p.starts) {
-    if (p.nr == 16) return launch_nr<16, true>(p, ws, stream);
-    if (p.nr == 32) return launch_nr<32, true>(p, ws, stream);
-    return launch_nr<64, true>(p, ws, stream);
-  }
-  if (p.nr == 16) return launch_nr<16, false>(p, ws, stream);
-  if (p.nr == 32) return launch_nr<32, false>(p, ws, stream);
-  return launch_nr<64, false>(p, ws, stream);
+  if (p.shared_table) return launch_form<kShared>(p, ws, stream);
+  if (p.softcap > 0.f || p.slopes || p.starts) return launch_form<kMasked>(p, ws, stream);
+  return launch_form<kPlain>(p, ws, stream);
 }
 
 }  // namespace smla
@@ -1705,14 +1767,11 @@ extern "C" int sparse_mla_dense_plan_for(const smla_dense_dims* d, int32_t sm_co
   // the fewest rows with which a CTA has at most a few tiles if every request is as long as its table.
   const int64_t tiles = d->batch / sq * ((d->max_pages_per_seq + (int64_t)1) / 2);
   auto groups = [&](int nr) { return (rows + nr - 1) / nr; };
-  if (rows <= 16 || tiles * groups(16) <= kMostTiles16 * (int64_t)plan->ctas) plan->rows_per_cta = 16;
-  else if (rows <= 32 || tiles * groups(32) <= kMostTiles32 * (int64_t)plan->ctas) plan->rows_per_cta = 32;
-  else plan->rows_per_cta = 64;
+  plan->rows_per_cta = dense_rows_per_cta(rows, plan->ctas, [&](int nr) { return tiles * groups(nr); });
   plan->row_groups = (int32_t)groups(plan->rows_per_cta);
   // a CTA counts its tiles in 32 bits
   const int64_t most = tiles * plan->row_groups;
   if (most / plan->ctas >= 0x7fffffff) return SMLA_ERR_UNSUPPORTED;
-  plan->workspace_bytes = kWorkspaceHeader + kDescBytes + lse_part_bytes(plan->ctas, plan->rows_per_cta) +
-                          (size_t)2 * plan->ctas * plan->rows_per_cta * kDLatent * sizeof(float);
+  plan->workspace_bytes = dense_workspace_bytes(plan->ctas, plan->rows_per_cta);
   return SMLA_OK;
 }

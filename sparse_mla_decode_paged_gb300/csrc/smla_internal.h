@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <functional>
+
 #include "sparse_mla.h"
 
 namespace smla {
@@ -158,10 +160,24 @@ struct DenseParams {
   const float* slopes;        // [H] or null: slope (t - (len - 1)) is added to them
   const int32_t* starts;      // [B] or null: positions below starts[b] are seen below prefix_lens[b] alone
   const int32_t* prefix_lens; // [B] or null (with starts)
+  const int32_t* shared_table;// [prefixes][shared_pages] or null: prefixes that groups of requests share
+  const int32_t* shared_lens; // [prefixes]
+  int prefixes, shared_pages;
+  int prefix_rows;            // rows of a prefix's requests
+  int prefix_groups;          // row groups per prefix
+  float* out32;               // with prefixes: [2][B][H][512] results of the requests' own positions and of the prefixes
+  float* lse32;               // [2][B][H]
   uint16_t* out;              // bf16 [B][H][512]
   float* lse;                 // [B][H]
   uint32_t* err;              // device error word
   uint64_t wait_ns;           // time limit of each pipeline wait inside the kernel
+};
+
+// Decode behind shared prefixes: the dense decode's items of requests and prefixes, then their join.
+struct SharedParams {
+  DenseParams dense;          // form kShared: out32 and lse32 set
+  uint16_t* out;              // bf16 [B][H][512]
+  float* lse;                 // [B][H]
 };
 
 // Everything the attention-weight kernel needs for one launch.
@@ -208,6 +224,9 @@ cudaError_t launch_kv_norm_append(const NormAppendParams& p, cudaStream_t stream
 cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t stream);
 cudaError_t launch_kv_read(const ReadParams& p, cudaStream_t stream);
 cudaError_t launch_dense(const DenseParams& p, cudaStream_t stream);
+size_t dense_workspace_bytes(int ctas, int nr);
+int dense_rows_per_cta(long long rows, int ctas, const std::function<long long(int)>& tiles);
+cudaError_t launch_shared(const SharedParams& p, cudaStream_t stream);
 cudaError_t launch_weights(const WeightsParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_evict(const EvictParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_gather_rows(const int32_t* bt, const int32_t* topk, const int32_t* seq_lens,
