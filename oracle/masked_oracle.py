@@ -84,15 +84,21 @@ def masked_decode(q, kv_cache, block_table, seq_lens, sm_scale, softcap=0.0, slo
     return res
 
 
-def shared_decode(q, kv_cache, prefix_table, prefix_lens, block_table, seq_lens, sm_scale):
-    """Requests r attend over the positions of their group's prefix, then over their own."""
+def shared_decode(q, kv_cache, prefix_table, prefix_lens, block_table, seq_lens, sm_scale, half_keys=False):
+    """Requests r attend over the positions of their group's prefix, then over their own.
+
+    With half_keys the keys are rounded to fp16 (2^-11 of each element, or of 2^-28 of the largest of its group of
+    32 positions): a score's error is a sum of 576 unrelated roundings a_i u_i, |u_i| <= 1, which exceeds 7 sqrt(sum
+    a_i^2) with probability 2 exp(-49 / 2) < 5e-11 and never sum |a_i|; lse's is their mean under the weights, bounded
+    alike (to first order; the second adds less than the square of the largest).  Then a sixth size is returned, lse's
+    error."""
     qf = as_f64_q(q)
     cache = np.asarray(kv_cache, dtype=np.uint8)
     flat = cache.reshape(-1, RECORD_BYTES)
     pt, bt = np.asarray(prefix_table, dtype=np.int64), np.asarray(block_table, dtype=np.int64)
     B, H, _ = qf.shape
     s_q, each = B // bt.shape[0], bt.shape[0] // pt.shape[0]
-    res = _empty(B, H)
+    res = _empty(B, H) + ((np.zeros((B, H)),) if half_keys else ())
     for b in range(B):
         r = b // s_q
         a, pa = positions_rows(pt[r // each], int(prefix_lens[r // each]), cache.shape[0])
@@ -104,6 +110,21 @@ def shared_decode(q, kv_cache, prefix_table, prefix_lens, block_table, seq_lens,
         codes, scales, _ = decode_record(flat[rows])
         s = sm_scale * (qf[b] @ k.T)
         tile = np.concatenate([pa // TILE, 10 ** 7 + pc // TILE])
-        for to, got in zip(res, attend(qf[b], k, codes, scales, s, score_error_bound(qf[b], k, sm_scale), tile)):
-            to[b] = got
+        err = score_error_bound(qf[b], k, sm_scale)
+        sigma = np.zeros_like(err)
+        if half_keys:
+            size = np.abs(k)
+            page = np.concatenate([pa // 32, 10 ** 7 + pc // 32])
+            each_page, at = np.unique(page, return_inverse=True)
+            most = np.array([size[page == t].max() for t in each_page])[at]
+            off = abs(sm_scale) * 2.0 ** -11 * np.maximum(size, 2.0 ** -27 * most[:, None])
+            sigma = np.sqrt(qf[b] ** 2 @ (off ** 2).T)
+            err = err + np.minimum(7 * sigma, np.abs(qf[b]) @ off.T)
+        got = attend(qf[b], k, codes, scales, s, err, tile)
+        for to, x in zip(res, got):
+            to[b] = x
+        if half_keys:
+            p = np.exp(s - got[1][:, None])
+            res[5][b] = 7 * np.sqrt((p ** 2 * sigma ** 2).sum(1)) + got[4] ** 2 + \
+                (p * score_error_bound(qf[b], k, sm_scale)).sum(1)
     return res

@@ -679,10 +679,16 @@ extern "C" int sparse_mla_kv_evict(const smla_evict_dims* d, float* weights, int
 
 namespace {
 
+// The prefix kernel takes prefixes of at least so many rows, with tables of at least so many pages.
+constexpr int64_t kPairsLeastRows = 128, kPairsLeastPages = 16;
+
 // How a shared decode runs on a device with `sms` SMs.
 struct SharedPlan {
   int nr, own_groups, prefix_groups;
-  size_t results_at, lse_at, bytes;        // parts of the workspace behind the dense decode's
+  bool pairs;                              // the prefix kernel takes the prefixes
+  bool own;                                // and the requests' own positions
+  int row_blocks, tiles_per_prefix, own_blocks, tiles_per_own;
+  size_t results_at, lse_at, slots_at, slots_lse_at, info_at, begins_at, expanded_at, bytes;  // behind the dense decode's
 };
 
 int shared_plan(const smla_shared_dims* d, int sms, SharedPlan* plan) {
@@ -696,17 +702,37 @@ int shared_plan(const smla_shared_dims* d, int sms, SharedPlan* plan) {
   const int ctas = sms < kDenseMaxCtas ? sms : kDenseMaxCtas;
   const int64_t requests = d->batch / sq, rows = (int64_t)sq * d->num_heads, all = (int64_t)d->batch * d->num_heads;
   const int64_t prefix_rows = all / d->num_prefixes;
+  plan->tiles_per_prefix = (int)((d->prefix_pages + (int64_t)1) / 2);
+  plan->tiles_per_own = (int)((d->max_pages_per_seq + (int64_t)1) / 2);
+  plan->pairs = prefix_rows >= kPairsLeastRows && d->prefix_pages >= kPairsLeastPages && sms >= 2;
   auto tiles = [&](int nr) {
     return requests * ((rows + nr - 1) / nr) * ((d->max_pages_per_seq + (int64_t)1) / 2) +
-           d->num_prefixes * ((prefix_rows + nr - 1) / nr) * ((d->prefix_pages + (int64_t)1) / 2);
+           (plan->pairs ? 0 : d->num_prefixes * ((prefix_rows + nr - 1) / nr) * plan->tiles_per_prefix);
   };
-  plan->nr = dense_rows_per_cta(prefix_rows, ctas, tiles);
+  plan->nr = dense_rows_per_cta(plan->pairs ? rows : prefix_rows, ctas, tiles);
   if (tiles(plan->nr) / ctas >= 0x7fffffff) return SMLA_ERR_UNSUPPORTED;     // a CTA counts its tiles in 32 bits
   plan->own_groups = (int)((rows + plan->nr - 1) / plan->nr);
   plan->prefix_groups = (int)((prefix_rows + plan->nr - 1) / plan->nr);
   plan->results_at = dense_workspace_bytes(ctas, plan->nr);
   plan->lse_at = plan->results_at + (size_t)2 * all * kDLatent * sizeof(float);
   plan->bytes = plan->lse_at + (size_t)2 * all * sizeof(float);
+  plan->own = false;
+  if (plan->pairs) {
+    auto after = [](size_t at) { return (at + 255) / 256 * 256; };
+    const int64_t pairs = ctas / 2, all_tiles = (int64_t)d->num_prefixes * plan->tiles_per_prefix;
+    plan->row_blocks = (int)((prefix_rows + 127) / 128);
+    plan->own_blocks = (int)((rows + 127) / 128);
+    const int64_t work = all_tiles * plan->row_blocks, own_tiles = requests * plan->tiles_per_own;
+    if (4 * (all_tiles + own_tiles) >= 0x7fffffff || work / pairs >= 0x7fffffff) return SMLA_ERR_UNSUPPORTED;
+    plan->own = own_tiles * plan->own_blocks <= (work / 4 > 2 * pairs ? work / 4 : 2 * pairs);
+    const size_t pages = 2 * (size_t)(all_tiles + (plan->own ? own_tiles : 0));
+    plan->slots_at = after(plan->bytes);
+    plan->slots_lse_at = plan->slots_at + 2 * pairs * 128 * kDLatent * sizeof(float);
+    plan->begins_at = after(plan->slots_lse_at + 2 * pairs * 128 * sizeof(float));
+    plan->info_at = after(plan->begins_at + (size_t)(d->num_prefixes + requests + 2) * sizeof(long long));
+    plan->expanded_at = after(plan->info_at + 2 * pages * sizeof(int4));
+    plan->bytes = plan->expanded_at + pages * 9 * 8192;
+  }
   return SMLA_OK;
 }
 
@@ -764,6 +790,42 @@ extern "C" int sparse_mla_shared_decode(const smla_shared_dims* d, const void* q
   p.lse32 = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.lse_at);
   p.err = static_cast<uint32_t*>(workspace);
   p.wait_ns = split_wait_limit_ns();
+  PrefixParams& x = s.prefix;                                  // (what the join needs in any case first)
+  x.prefixes = d->num_prefixes;
+  x.rows = p.prefix_rows;
+  x.q_per_req = p.q_per_req;
+  x.H = p.H;
+  x.all_rows = (size_t)p.B * p.H;
+  x.out32 = p.out32;
+  x.lse32 = p.lse32;
+  if (plan.pairs) {
+    char* ws = static_cast<char*>(workspace);
+    x.q = p.q;
+    x.kv = p.kv;
+    x.table = prefix_table;
+    x.lens = prefix_lens;
+    x.num_pages = p.num_pages;
+    x.sm_scale = sm_scale;
+    x.pages = d->prefix_pages;
+    x.row_blocks = plan.row_blocks;
+    x.tiles_per_prefix = plan.tiles_per_prefix;
+    x.own = plan.own;
+    x.own_table = block_table;
+    x.own_lens = seq_lens;
+    x.requests = p.requests;
+    x.own_pages = p.max_pages;
+    x.own_blocks = plan.own_blocks;
+    x.tiles_per_own = plan.tiles_per_own;
+    x.pairs = p.ctas / 2;
+    x.expanded = reinterpret_cast<unsigned char*>(ws + plan.expanded_at);
+    x.info = reinterpret_cast<int4*>(ws + plan.info_at);
+    x.begins = reinterpret_cast<long long*>(ws + plan.begins_at);
+    x.slots = reinterpret_cast<float*>(ws + plan.slots_at);
+    x.slots_lse = reinterpret_cast<float*>(ws + plan.slots_lse_at);
+    x.err = p.err;
+    x.wait_ns = p.wait_ns;
+    p.prefixes = p.prefix_groups = p.shared_pages = 0;       // the dense kernel has the requests' own positions at most
+  }
   s.out = static_cast<uint16_t*>(out);
   s.lse = lse;
   return launch_shared(s, (cudaStream_t)stream) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;

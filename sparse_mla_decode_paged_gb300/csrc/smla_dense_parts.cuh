@@ -27,6 +27,13 @@ struct Ring {
       parity ^= 1;
     }
   }
+  __device__ __forceinline__ void skip(int n) {
+    slot += n;
+    if (slot >= N) {
+      slot -= N;
+      parity ^= 1;
+    }
+  }
 };
 
 // A wait for a slot to be freed (the other parity) passes at once on the ring's first round: an mbarrier that has

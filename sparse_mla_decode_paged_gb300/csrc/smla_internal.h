@@ -173,9 +173,41 @@ struct DenseParams {
   uint64_t wait_ns;           // time limit of each pipeline wait inside the kernel
 };
 
+// Attention of many rows over shared prefixes: see smla_prefix.cu.  Segments 0 .. prefixes - 1 are the prefixes, each seen by
+// `rows` rows; behind them, if `own` is set, come the requests' own positions, seen by the request's rows.
+struct PrefixParams {
+  const uint16_t* q;          // bf16 [all rows][576]: the rows of a prefix's requests lie together
+  const uint8_t* kv;          // [num_pages][64][656]
+  const int32_t* table;       // [prefixes][pages]
+  const int32_t* lens;        // [prefixes]
+  int64_t num_pages;
+  float sm_scale;
+  int prefixes, pages;
+  int rows;                   // rows per prefix
+  int row_blocks;             // of 128 rows
+  int tiles_per_prefix;       // room for tiles of 128 positions
+  int own;                    // whether the requests' own positions are segments, too
+  const int32_t* own_table;   // [requests][own_pages]
+  const int32_t* own_lens;    // [requests x q_per_req]
+  int requests, own_pages, q_per_req, H;
+  int own_blocks, tiles_per_own;
+  int pairs;                  // pairs of CTAs
+  unsigned char* expanded;    // the segments' pages in fp16
+  int4* info;                 // per half page: exponent, whether it is in the cache, a bit per position that is no number
+  long long* begins;          // [segments + 2]: where each segment begins on the line, its end, the units of an item's start
+  float* slots;               // [2 pairs][128][512] results of blocks that cross runs
+  float* slots_lse;           // [2 pairs][128]
+  float* out32;               // [2][all rows][512] results of the others: requests' own positions, prefixes
+  float* lse32;               // [2][all rows]
+  size_t all_rows;
+  uint32_t* err;              // device error word
+  uint64_t wait_ns;           // time limit of each pipeline wait inside the kernel
+};
+
 // Decode behind shared prefixes: the dense decode's items of requests and prefixes, then their join.
 struct SharedParams {
-  DenseParams dense;          // form kShared: out32 and lse32 set
+  DenseParams dense;          // form kShared: out32 and lse32 set; without prefixes where `prefix` takes them
+  PrefixParams prefix;        // prefixes 0: the dense kernel takes them
   uint16_t* out;              // bf16 [B][H][512]
   float* lse;                 // [B][H]
 };
@@ -226,6 +258,7 @@ cudaError_t launch_kv_read(const ReadParams& p, cudaStream_t stream);
 cudaError_t launch_dense(const DenseParams& p, cudaStream_t stream);
 size_t dense_workspace_bytes(int ctas, int nr);
 int dense_rows_per_cta(long long rows, int ctas, const std::function<long long(int)>& tiles);
+cudaError_t launch_prefix(const PrefixParams& p, cudaStream_t stream);
 cudaError_t launch_shared(const SharedParams& p, cudaStream_t stream);
 cudaError_t launch_weights(const WeightsParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_evict(const EvictParams& p, int sms, cudaStream_t stream);

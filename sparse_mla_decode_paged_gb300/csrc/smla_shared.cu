@@ -1,64 +1,172 @@
 // Decode of requests behind shared prefixes: every request attends over the positions of its group's prefix, then over its
 // own, and the records of a prefix are read for all of the group's rows at once.
 //
-// The dense decode's kernel takes both kinds of items on one line of tiles (a prefix's rows are those of all its requests)
-// and leaves two results per row in fp32; the join here makes one of them:
-//   lse = ln(exp(lse_own) + exp(lse_prefix)), out = exp(lse_own - lse) out_own + exp(lse_prefix - lse) out_prefix.
+// Short prefixes and few rows: the dense decode's kernel takes both kinds of items on one line of tiles (a prefix's rows
+// are those of all its requests).  Else the prefix kernel takes the prefixes and, where they are short, the requests' own
+// positions, too; long ones stay with the dense kernel.  Either way results per row are left in fp32, and the join here makes one of them:
+//   lse = ln sum_i exp(lse_i), out = sum_i exp(lse_i - lse) out_i.
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
 #include "smla_device.cuh"
 #include "smla_internal.h"
+#include "smla_prefix_parts.cuh"
 #include "smla_ptx.cuh"
 
 namespace smla {
 namespace {
 
-constexpr int kJoinThreads = 128;
+constexpr int kJoinDims = 128;             // threads that share a row's 512 dims
+constexpr int kJoinGroups = 4;            // groups of them that share its parts
+constexpr int kJoinBatch = 4;             // parts in flight per thread
+constexpr int kMostParts = 1024 + 2;
 
-// One warp per row, 16 dims per lane.  (This grid is resident while results are still written, so they are read from L2.)
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const float* o, const float* lse, uint16_t* out, float* lse_out,
-                                                            int rows) {
-  const int row = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  ptx::griddep_wait();
-  if (row >= rows) return;
-  const float4 *a = reinterpret_cast<const float4*>(o + (size_t)row * kDLatent),
-               *b = reinterpret_cast<const float4*>(o + ((size_t)rows + row) * kDLatent);
-  float4 x[4], y[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[i] = __ldcg(a + 32 * i + lane);
-    y[i] = __ldcg(b + 32 * i + lane);
+// Where a row's results lie: `parts` of them, the s-th at place(s) of the arrays.
+struct Parts {
+  const float *o, *lse;
+  int parts, pair, at;
+  __device__ __forceinline__ size_t place(int s) const {
+    return parts == 1 ? (size_t)at : (size_t)(2 * (pair + s) + (s == 0 ? 1 : 0)) * kPrefixRows + at;
   }
-  const float la = __ldcg(lse + row), lb = __ldcg(lse + rows + row);
-  float m = fmaxf(la, lb);
-  if (isnan(la) || isnan(lb)) m = CUDART_NAN_F;
-  const float ea = m == -CUDART_INF_F ? 0.f : expf(la - m), eb = m == -CUDART_INF_F ? 0.f : expf(lb - m), z = ea + eb;
-  const float wa = z == 0.f ? 0.f : ea / z, wb = z == 0.f ? 0.f : eb / z;
-  uint2* to = reinterpret_cast<uint2*>(out + (size_t)row * kDLatent);
+};
+
+// The prefix kernel's results of row r of segment g: a whole one lies with the rows, the first of several in slot 1 of its
+// pair, the others in slot 0 of theirs.
+__device__ __forceinline__ Parts segment_parts(const PrefixParams& p, int g, int row) {
+  const Segment seg = segment_of(p, g);
+  const int r = row - seg.first_row, block = r / kPrefixRows;
+  Parts x{p.slots, p.slots_lse, 0, 0, r - block * kPrefixRows};
+  const long long* ends = p.begins + segments_of(p);
+  const long long total = __ldcg(ends), start = __ldcg(ends + 1), begin = __ldcg(p.begins + g);
+  const long long units = (__ldcg(p.begins + g + 1) - begin) / seg.blocks;       // of an item
+  if (units == 0) return x;
+  const long long a = begin + block * units + start, e = begin + (block + 1) * units;
+  const int active = active_pairs(total, p.pairs);
+  int c = (int)min((long long)active - 1, a * active / total);         // the pair whose run holds tile a, give or take one
+  while (c > 0 && pair_start(total, active, c) > a) --c;
+  while (c + 1 < active && pair_start(total, active, c + 1) <= a) ++c;
+  int c1 = min(active - 1, max(c, (int)(e * active / total)));
+  while (c1 > c && pair_start(total, active, c1) >= e) --c1;
+  while (c1 + 1 < active && pair_start(total, active, c1 + 1) < e) ++c1;
+  x.parts = c1 - c + 1;
+  x.pair = c;
+  if (x.parts == 1) {
+    x.o = p.out32 + (seg.own ? 0 : p.all_rows) * kDLatent;
+    x.lse = p.lse32 + (seg.own ? 0 : p.all_rows);
+    x.at = row;
+  }
+  return x;
+}
+
+// One CTA per row; a group of 128 threads takes 4 dims each of every kGroups-th part.  (This grid is resident while results
+// are still written, so they are read from L2.)
+template <int kGroups>
+__global__ void __launch_bounds__(kJoinDims * kGroups) join_kernel(const PrefixParams p, uint16_t* out, float* lse_out) {
+  __shared__ Parts own_s, prefix_s;
+  __shared__ float w_s[kMostParts], z_s;
+  __shared__ float4 sum_s[kGroups][kJoinDims];
+  const int row = blockIdx.x, lane = threadIdx.x & 31, dim = threadIdx.x % kJoinDims, group = threadIdx.x / kJoinDims;
+  ptx::griddep_wait();
+  if (threadIdx.x == 0) {
+    if (p.own) own_s = segment_parts(p, p.prefixes + row / (p.q_per_req * p.H), row);
+    else own_s = Parts{p.out32, p.lse32, 1, 0, row};
+  }
+  if (threadIdx.x == 32) {
+    if (p.pairs > 0) prefix_s = segment_parts(p, row / p.rows, row);
+    else prefix_s = Parts{p.out32 + p.all_rows * kDLatent, p.lse32 + p.all_rows, 1, 0, row};
+  }
+  __syncthreads();
+  const Parts a = own_s, b = prefix_s;
+  const int parts = a.parts + b.parts;
+  auto row_of = [&](int s) {
+    return reinterpret_cast<const float4*>(s < a.parts ? a.o + a.place(s) * kDLatent : b.o + b.place(s - a.parts) * kDLatent) + dim;
+  };
+  float4 v[kJoinBatch];                                    // in flight before the weights are known
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    to[32 * i + lane] = make_uint2(f32x2_to_bf16x2(fmaf(wa, x[i].x, wb * y[i].x), fmaf(wa, x[i].y, wb * y[i].y)),
-                                   f32x2_to_bf16x2(fmaf(wa, x[i].z, wb * y[i].z), fmaf(wa, x[i].w, wb * y[i].w)));
-  if (lane == 0) lse_out[row] = z == 0.f ? -CUDART_INF_F : m + logf(z);
+  for (int j = 0; j < kJoinBatch; ++j)
+    if (group + kGroups * j < parts) v[j] = __ldcg(row_of(group + kGroups * j));
+  if (threadIdx.x < 32) {
+    float m = -CUDART_INF_F;
+    bool bad = false;
+    for (int s = lane; s < parts; s += 32) {
+      const float x = __ldcg(s < a.parts ? a.lse + a.place(s) : b.lse + b.place(s - a.parts));
+      w_s[s] = x;
+      bad |= isnan(x);
+      m = fmaxf(m, x);
+    }
+#pragma unroll
+    for (int h = 16; h; h >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, h));
+    if (__any_sync(0xffffffffu, bad)) m = CUDART_NAN_F;
+    float z = 0.f;
+    for (int s = lane; s < parts; s += 32) {
+      const float e = m == -CUDART_INF_F ? 0.f : expf(w_s[s] - m);
+      w_s[s] = e;
+      z += e;
+    }
+#pragma unroll
+    for (int h = 16; h; h >>= 1) z += __shfl_xor_sync(0xffffffffu, z, h);
+    if (lane == 0) {
+      z_s = z;
+      lse_out[row] = z == 0.f ? -CUDART_INF_F : m + logf(z);
+    }
+  }
+  __syncthreads();
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = group; s0 < parts; s0 += kGroups * kJoinBatch) {
+    if (s0 > group) {
+#pragma unroll
+      for (int j = 0; j < kJoinBatch; ++j)
+        if (s0 + kGroups * j < parts) v[j] = __ldcg(row_of(s0 + kGroups * j));
+    }
+#pragma unroll
+    for (int j = 0; j < kJoinBatch; ++j) {
+      if (s0 + kGroups * j >= parts) continue;
+      const float w = w_s[s0 + kGroups * j];
+      acc.x = fmaf(w, v[j].x, acc.x);
+      acc.y = fmaf(w, v[j].y, acc.y);
+      acc.z = fmaf(w, v[j].z, acc.z);
+      acc.w = fmaf(w, v[j].w, acc.w);
+    }
+  }
+  if constexpr (kGroups > 1) {
+    sum_s[group][dim] = acc;
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int i = 1; i < kGroups; ++i) {
+      const float4 x = sum_s[i][dim];
+      acc.x += x.x;
+      acc.y += x.y;
+      acc.z += x.z;
+      acc.w += x.w;
+    }
+  }
+  const float inv = z_s == 0.f ? 0.f : 1.f / z_s;
+  reinterpret_cast<uint2*>(out + (size_t)row * kDLatent)[dim] =
+      make_uint2(f32x2_to_bf16x2(acc.x * inv, acc.y * inv), f32x2_to_bf16x2(acc.z * inv, acc.w * inv));
 }
 
 }  // namespace
 
 cudaError_t launch_shared(const SharedParams& p, cudaStream_t stream) {
-  cudaError_t e = launch_dense(p.dense, stream);
+  const PrefixParams& x = p.prefix;
+  cudaError_t e = x.pairs > 0 ? launch_prefix(x, stream) : cudaSuccess;
   if (e != cudaSuccess) return e;
-  const int rows = p.dense.B * p.dense.H;
+  if (!x.own) e = launch_dense(p.dense, stream);
+  if (e != cudaSuccess) return e;
+  // parts of a prefix's block of rows, about
+  const long long blocks = (long long)x.prefixes * x.row_blocks, parts = x.pairs > 0 ? x.pairs / blocks : 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
-  cfg.blockDim = dim3(kJoinThreads);
+  cfg.gridDim = dim3((unsigned)x.all_rows);
+  cfg.blockDim = dim3(parts > kJoinBatch ? kJoinDims * kJoinGroups : kJoinDims);
   cfg.stream = stream;
   cudaLaunchAttribute a[1];
   a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   a[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = a;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel, (const float*)p.dense.out32, (const float*)p.dense.lse32, p.out, p.lse, rows);
+  return parts > kJoinBatch ? cudaLaunchKernelEx(&cfg, join_kernel<kJoinGroups>, x, p.out, p.lse)
+                            : cudaLaunchKernelEx(&cfg, join_kernel<1>, x, p.out, p.lse);
 }
 
 }  // namespace smla

@@ -55,17 +55,114 @@ def _run(case, ws=None, **kw):
     return out, lse, api.read_errors(ws)
 
 
+# Prefixes of so many rows and pages are taken by pairs of CTAs, with keys rounded to fp16.
+PAIR_ROWS, PAIR_PAGES = 128, 16
+
+
 def _want(case):
     q, cache, pt, pl, bt, ln = case
+    pairs = q.shape[0] * q.shape[1] // pt.shape[0] >= PAIR_ROWS and pt.shape[1] >= PAIR_PAGES
     return masked_oracle.shared_decode(bits(q).reshape(q.shape), cache.numpy(), pt.numpy(), pl.numpy(), bt.numpy(),
-                                       ln.numpy(), SCALE)
+                                       ln.numpy(), SCALE, half_keys=pairs)
 
 
-def _check(*args, flags=0, **kw):
+def _widened(case):
+    """The same prefixes in a table of as many pages as pairs of CTAs take."""
+    pt = torch.full((case[2].shape[0], max(PAIR_PAGES, case[2].shape[1])), -1, dtype=torch.int32)
+    pt[:, :case[2].shape[1]] = case[2]
+    return (*case[:2], pt, *case[3:])
+
+
+def _check(*args, flags=0, wide=False, **kw):
     case = make(*args, **kw)
+    if wide:
+        case = _widened(case)
     out, lse, err = _run(case)
     assert err == flags
     check_decode(out, lse, _want(case))
+
+
+@pytest.mark.parametrize("n", [1, 63, 64, 65, 127, 128, 129, 300, 1000, 1024, 2500])
+def test_pairs_of_ctas_lengths(n):
+    _check([n], [100, 0], 64, seed=n, wide=True)
+
+
+@pytest.mark.parametrize("H,R", [(64, 3), (128, 1), (128, 2), (100, 2), (16, 9), (5, 40), (1, 130)])
+def test_pairs_of_ctas_rows(H, R):
+    _check([1100], [(i * 37) % 90 for i in range(R)], H, seed=H, wide=True)
+
+
+@pytest.mark.parametrize("G,each", [(2, 2), (3, 2), (9, 2), (200, 2)])
+def test_pairs_of_ctas_groups(G, each):
+    """More blocks than pairs, empty prefixes among them."""
+    _check([0 if i % 4 == 1 else (i * 331 + 500) % 1300 for i in range(G)], [(i * 97) % 70 for i in range(G * each)], 64 if G < 20 else 66,
+           seed=G, wide=True)
+
+
+def test_pairs_of_ctas_nothing_to_see():
+    _check([0, 0], [0, 3, 0, 0], 64, seed=1, wide=True)
+
+
+@pytest.mark.parametrize("q_scale", [0.01, 8.0, 60.0])
+def test_pairs_of_ctas_scores_far_apart(q_scale):
+    _check([2000], [100, 5], 64, seed=2, q_scale=q_scale, wide=True)
+
+
+def test_pairs_of_ctas_long():
+    _check([20000], [10, 300], 64, seed=3, wide=True)
+
+
+def test_pairs_of_ctas_bad_pages():
+    case = _widened(make([1500], [300, 200], 64, seed=3))
+    case[2][0, 2], case[2][0, 7], case[4][1, 0] = -1, 10 ** 6, 10 ** 6
+    out, lse, err = _run(case)
+    assert err == _native.DEVERR_PAGE_RANGE
+    check_decode(out, lse, _want(case))
+
+
+def test_pairs_of_ctas_scales_far_apart():
+    """Tiles whose scales differ by powers of two, rising and falling: the references and the sums follow."""
+    q, cache, pt, pl, bt, ln = make([1500], [64, 64], 64, seed=9)
+    for i, pg in enumerate(pt[0].tolist()):
+        sc = cache[pg, :, 512:528].contiguous().view(torch.float32) * 2.0 ** ((i * 7) % 23 - 16)
+        cache[pg, :, 512:528] = sc.view(torch.uint8)
+    case = _widened((q, cache, pt, pl, bt, ln))
+    out, lse, err = _run(case)
+    check_decode(out, lse, _want(case))
+
+
+def test_pairs_of_ctas_runs_are_equal():
+    case = _widened(make([9000], [100, 200, 3], 64, seed=10))
+    a = _run(case)
+    for _ in range(5):
+        b = _run(case)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_pairs_of_ctas_a_nan_that_one_query_sees():
+    """The last query of a request sees a position that is no number, the one before does not; nor do other requests."""
+    case = _widened(make([1200], [39, 40, 64, 64], 64, s_q=2, seed=12))
+    case[1][int(case[4][0, 0]), 39, 7] = 0x7F
+    out, lse, err = _run(case)
+    assert torch.isnan(lse[1]).all() and torch.isnan(out[1]).all()
+    keep = [0, 2, 3]
+    case[1][int(case[4][0, 0]), 39] = 0
+    want = _want(case)
+    check_decode(out[keep], lse[keep], tuple(x[keep] for x in want))
+
+
+@pytest.mark.parametrize("own", [1, 64, 200, 700, 2000])
+def test_pairs_of_ctas_own_positions(own):
+    """Few own positions go with the prefixes, many to the dense kernel."""
+    _check([1100, 900], [own, 0, 3, own // 2], 64, seed=own, wide=True)
+    _check([1100], [max(0, own - 2), own - 1, own, 0, 1, 2], 64, s_q=3, seed=own + 1, wide=True)
+
+
+def test_pairs_of_ctas_nan():
+    case = _widened(make([1200], [10, 20], 64, seed=11))
+    case[1][int(case[2][0, 3]), 5, 100] = 0x7F
+    out, lse, err = _run(case)
+    assert torch.isnan(lse).all() and torch.isnan(out).all()
 
 
 @pytest.mark.parametrize("n", [0, 1, 63, 64, 65, 128, 129, 500, 1000, 3000])
