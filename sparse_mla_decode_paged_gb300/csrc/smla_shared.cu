@@ -17,8 +17,9 @@ namespace smla {
 namespace {
 
 constexpr int kJoinDims = 128;             // threads that share a row's 512 dims
-constexpr int kJoinGroups = 4;            // groups of them that share its parts
-constexpr int kJoinBatch = 4;             // parts in flight per thread
+constexpr int kJoinGroups = 4;            // groups of them that share its parts, where they are many
+constexpr int kJoinBatch = 8;             // parts in flight per thread
+constexpr int kManyParts = 24;
 constexpr int kMostParts = 1024 + 2;
 
 // Where a row's results lie: `parts` of them, the s-th at place(s) of the arrays.
@@ -42,10 +43,15 @@ __device__ __forceinline__ Parts segment_parts(const PrefixParams& p, int g, int
   if (units == 0) return x;
   const long long a = begin + block * units + start, e = begin + (block + 1) * units;
   const int active = active_pairs(total, p.pairs);
-  int c = (int)min((long long)active - 1, a * active / total);         // the pair whose run holds tile a, give or take one
+  auto about = [&](long long u) {                          // the pair whose run holds unit u, give or take one
+    const unsigned long long x = (unsigned long long)u * active;
+    return (int)min((unsigned long long)active - 1,
+                    (x | (unsigned long long)total) >> 32 ? x / total : (uint32_t)x / (uint32_t)total);
+  };
+  int c = about(a);
   while (c > 0 && pair_start(total, active, c) > a) --c;
   while (c + 1 < active && pair_start(total, active, c + 1) <= a) ++c;
-  int c1 = min(active - 1, max(c, (int)(e * active / total)));
+  int c1 = max(c, about(e));
   while (c1 > c && pair_start(total, active, c1) >= e) --c1;
   while (c1 + 1 < active && pair_start(total, active, c1 + 1) < e) ++c1;
   x.parts = c1 - c + 1;
@@ -158,14 +164,14 @@ cudaError_t launch_shared(const SharedParams& p, cudaStream_t stream) {
   const long long blocks = (long long)x.prefixes * x.row_blocks, parts = x.pairs > 0 ? x.pairs / blocks : 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)x.all_rows);
-  cfg.blockDim = dim3(parts > kJoinBatch ? kJoinDims * kJoinGroups : kJoinDims);
+  cfg.blockDim = dim3(parts > kManyParts ? kJoinDims * kJoinGroups : kJoinDims);
   cfg.stream = stream;
   cudaLaunchAttribute a[1];
   a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   a[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = a;
   cfg.numAttrs = 1;
-  return parts > kJoinBatch ? cudaLaunchKernelEx(&cfg, join_kernel<kJoinGroups>, x, p.out, p.lse)
+  return parts > kManyParts ? cudaLaunchKernelEx(&cfg, join_kernel<kJoinGroups>, x, p.out, p.lse)
                             : cudaLaunchKernelEx(&cfg, join_kernel<1>, x, p.out, p.lse);
 }
 
