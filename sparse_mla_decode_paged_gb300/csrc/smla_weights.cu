@@ -32,14 +32,18 @@ constexpr int kSoftWarps = 8;             // warp w: TMEM lanes of quadrant w % 
 constexpr int kThreads = 32 * (kSoftWarps + 2);
 constexpr int kCopyWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
 constexpr int kSub = 8;
+// Tiles between a tile's prefetch into L2 and its copy (32 x 32768 positions of 16, 32, 64 heads: 111, 115, 134 us, none 121,
+// 122, 133, two 118 and 141 for 16 and 64).
+constexpr int kAhead = 1;
 constexpr uint64_t kLeastWaitNs = 1000;   // limits below this are meant to run out: nothing is issued
 
 template <int NR>
 struct WC {
-  // hi and lo terms of q: one MMA of twice the columns up to 32 rows, which meet in registers, else two MMAs
-  static constexpr int kPasses = NR >= 64 ? 2 : 1;
-  static constexpr int kCols = NR >= 64 ? NR : 2 * NR;               // columns of a score accumulator
-  static constexpr int kSBufs = NR == 128 ? 4 : 5;
+  // hi and lo terms of q: one MMA of twice the columns up to 64 rows, which meet in registers, else two MMAs (64 rows: 124 us
+  // for 32 x 32768 positions, 134 with two MMAs, which read the codes twice)
+  static constexpr int kPasses = NR >= 128 ? 2 : 1;
+  static constexpr int kCols = NR >= 128 ? NR : 2 * NR;               // columns of a score accumulator
+  static constexpr int kSBufs = NR >= 64 ? 4 : 5;
   static constexpr uint32_t kTmemCols = NR >= 64 ? 512 : NR == 32 ? 512 : 256;
   static constexpr int kRing = NR == 128 ? 4 : NR == 64 ? 8 : 10;    // slots of code blocks and ropes
   static constexpr int kScaleSlots = 3;
@@ -164,6 +168,12 @@ __device__ void copy_role(const WeightsParams& p, const CUtensorMap* map, const 
       if (used && !in_cache && lane == 0 && p.err) atomicOr(p.err, SMLA_DEVERR_PAGE_RANGE);
     }
     const uint32_t n_good = (good & 1) + (good >> 1);
+    // a later tile of the run into L2, in whole pages
+    const int ahead = lp - base_lp + 2 * kAhead + (lane & 1);
+    const int page_cur = __shfl_sync(0xffffffffu, cur, ahead & 31), page_nxt = __shfl_sync(0xffffffffu, nxt, ahead & 31);
+    const int page = ahead < 32 ? page_cur : page_nxt;
+    if (w.group == 0 && w.t + kAhead < w.to && lane < 2 && page >= 0 && (int64_t)page < p.num_pages)
+      ptx::prefetch_l2_bulk(p.kv + (size_t)page * kPageSize * kRecordBytes, kPageSize * kRecordBytes);
     SMLA_WAIT(&bars->scempty[sc.slot], sc.parity ^ 1);
     if (ok && ptx::elect_one()) {
       bars->pages_ok[sc.slot] = good;
@@ -211,33 +221,44 @@ __device__ void mma_role(const WeightsParams& p, uint32_t base, uint32_t tmem, B
       SMLA_WAIT(&bars->qfull, qpar);
       qpar ^= 1;
     }
+    // (no branch where MMAs are issued: with operands in uniform registers an MMA of N = 64 takes 48 cycles, else 75)
 #pragma unroll 1
-    for (int c = 0; c < kChunks; ++c) {
+    for (uint32_t c = 0; c < 4; ++c) {
       SMLA_WAIT(&bars->sempty[s.slot], s.parity ^ 1);
       SMLA_WAIT(&bars->kfull[k.slot], k.parity);
       ptx::tc_fence_after();
-      const uint32_t ks = k.slot, d = tmem + C::kCols * s.slot, cu = c;
+      const uint32_t ks = k.slot, ss = s.slot;
       if (ok && ptx::elect_one()) {
+        const uint32_t d = tmem + C::kCols * ss;
         const uint64_t dk = ptx::sw128_desc(base + C::kK + ks * kSlot, 16, 1024);
-        if (c == 4) {
+        const uint64_t dqb = dq + (uint64_t)((c * C::kQ8Chunk) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) ptx::mma_f16_ss(d, dk + 2 * kk, dr + 2 * kk, kIdescRope, kk > 0);
-        } else {
-          const uint64_t dqb = dq + (uint64_t)((cu * C::kQ8Chunk) >> 4);
+        for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-            for (int pass = 0; pass < C::kPasses; ++pass)
-              ptx::mma_f8_ss(d, dk + 2 * kk, dqb + 2 * kk + (uint64_t)((pass * NR * 128) >> 4), kIdescCodes,
-                             kk > 0 || pass > 0);
-        }
-        ptx::mma_commit(&bars->kempty[k.slot]);
-        ptx::mma_commit(&bars->sfull[s.slot]);
+          for (int pass = 0; pass < C::kPasses; ++pass)
+            ptx::mma_f8_ss(d, dk + 2 * kk, dqb + 2 * kk + (uint64_t)((pass * NR * 128) >> 4), kIdescCodes, kk > 0 || pass > 0);
+        ptx::mma_commit(&bars->kempty[ks]);
+        ptx::mma_commit(&bars->sfull[ss]);
       }
       __syncwarp();
       k.next();
       s.next();
     }
+    SMLA_WAIT(&bars->sempty[s.slot], s.parity ^ 1);
+    SMLA_WAIT(&bars->kfull[k.slot], k.parity);
+    ptx::tc_fence_after();
+    const uint32_t ks = k.slot, ss = s.slot;
+    if (ok && ptx::elect_one()) {
+      const uint32_t d = tmem + C::kCols * ss;
+      const uint64_t dk = ptx::sw128_desc(base + C::kK + ks * kSlot, 16, 1024);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) ptx::mma_f16_ss(d, dk + 2 * kk, dr + 2 * kk, kIdescRope, kk > 0);
+      ptx::mma_commit(&bars->kempty[ks]);
+      ptx::mma_commit(&bars->sfull[ss]);
+    }
+    __syncwarp();
+    k.next();
+    s.next();
     w.next(p);
   }
   if (ptx::elect_one()) ptx::mma_commit(&bars->drain);
