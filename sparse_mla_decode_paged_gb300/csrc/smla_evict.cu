@@ -27,8 +27,10 @@ constexpr int kWarps = 32;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMostCluster = 8;
 constexpr int kBins = 2048;
+constexpr int kBatch = 4;                 // steps of 32 slots that a warp loads at once
 constexpr int kKeySlots = 40960;          // slots of a CTA whose keys fit into shared memory
-constexpr int kSlotsPerCta = 4096;        // a request takes another CTA per so many slots
+// A request takes another CTA per so many slots.  (1 x 32768 slots: 4 CTAs 23.5 us, 8 CTAs 30, whole calls.)
+constexpr int kSlotsPerCta = 8192;
 constexpr uint32_t kDynBytes = kKeySlots * 4 + kKeySlots / 8;
 
 struct Shared {
@@ -85,38 +87,64 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
     if (csize > 1) ptx::cluster_sync_all();
     else __syncthreads();
   };
-  // key of slot t, and whether it is held
-  auto load = [&](int t, bool& held) -> uint32_t {
+  // keys of kBatch steps of 32 slots from b on, one per lane, and their held slots (a bit each): all loads first
+  struct Keys {
+    uint32_t key[kBatch], held[kBatch];
+  };
+  auto load = [&](int b) {
+    Keys k;
     if (cached) {
-      held = heldbits[(t - first) >> 5] >> (t - first & 31) & 1;
-      return keys[t - first];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int at = b + 32 * j - first;
+        k.key[j] = b + 32 * j + lane < t1 ? keys[at + lane] : 0u;
+        k.held[j] = b + 32 * j < t1 ? heldbits[at >> 5] : 0u;
+      }
+    } else {
+      float v[kBatch];
+      int at[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int t = b + 32 * j + lane;
+        v[j] = t < t1 ? __ldcg(w + t) : 0.f;
+        at[j] = t < t1 ? __ldg(pos + t) : 0;
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const bool in = b + 32 * j + lane < t1;
+        k.key[j] = order_key(v[j]);
+        k.held[j] = __ballot_sync(0xffffffffu, in && (at[j] < p.sinks || at[j] >= recent_from));
+      }
     }
-    const int at = __ldg(pos + t);
-    held = at < p.sinks || at >= recent_from;
-    return order_key(w[t]);
+    return k;
   };
 
   for (int i = threadIdx.x; i < 3 * kBins; i += kThreads) (&s.hist[0][0])[i] = 0;
   if (threadIdx.x == 0) s.held = 0;
   __syncthreads();
   uint32_t mine = 0;
-#pragma unroll 4
-  for (int b = t0; b < t1; b += 32) {
-    const int t = b + lane;
-    const bool in = t < t1;
-    uint32_t key = 0;
-    bool held = false;
-    if (in) {
-      const int at = __ldg(pos + t);
-      key = order_key(w[t]);
-      held = at < p.sinks || at >= recent_from;
-      if (!held) atomicAdd(&s.hist[0][key >> 21], 1u);
+#pragma unroll 1
+  for (int b0 = t0; b0 < t1; b0 += 32 * kBatch) {
+    float v[kBatch];
+    int at[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int t = b0 + 32 * j + lane;
+      v[j] = t < t1 ? __ldcg(w + t) : 0.f;
+      at[j] = t < t1 ? __ldg(pos + t) : 0;
     }
-    const uint32_t bits = __ballot_sync(0xffffffffu, held);
-    mine += __popc(bits);
-    if (cached) {
-      if (in) keys[t - first] = key;
-      if (lane == 0) heldbits[(b - first) >> 5] = bits;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int b = b0 + 32 * j, t = b + lane;
+      if (b >= t1) break;
+      const bool in = t < t1, held = in && (at[j] < p.sinks || at[j] >= recent_from);
+      const uint32_t key = order_key(v[j]), bits = __ballot_sync(0xffffffffu, held);
+      if (in && !held) atomicAdd(&s.hist[0][key >> 21], 1u);
+      mine += __popc(bits);
+      if (cached) {
+        if (in) keys[t - first] = key;
+        if (lane == 0) heldbits[(b - first) >> 5] = bits;
+      }
     }
   }
   if (lane == 0 && mine) atomicAdd(&s.held, mine);
@@ -141,13 +169,13 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
     for (int d = 0; d < 3; ++d) {
       const int shift = d == 0 ? 21 : d == 1 ? 10 : 0, bins = d == 2 ? 1024 : kBins;
       if (d > 0) {
-#pragma unroll 4
-        for (int b = t0; b < t1; b += 32) {
-          const int t = b + lane;
-          if (t >= t1) continue;
-          bool held;
-          const uint32_t key = load(t, held);
-          if (!held && key >> (shift + (d == 2 ? 10 : 11)) == limit) atomicAdd(&s.hist[d][key >> shift & (bins - 1)], 1u);
+#pragma unroll 1
+        for (int b = t0; b < t1; b += 32 * kBatch) {
+          const Keys k = load(b);
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j)
+            if (b + 32 * j + lane < t1 && !(k.held[j] >> lane & 1) && k.key[j] >> (shift + (d == 2 ? 10 : 11)) == limit)
+              atomicAdd(&s.hist[d][k.key[j] >> shift & (bins - 1)], 1u);
         }
         sync();
       }
@@ -189,10 +217,12 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
   uint32_t tie = 0;
   if (some && need < ties) {
     uint32_t m = 0;
-    for (int b = t0; b < t1; b += 32) {
-      bool held = true;
-      const uint32_t key = b + lane < t1 ? load(b + lane, held) : 0u;
-      m += __popc(__ballot_sync(0xffffffffu, !held && key == limit));
+#pragma unroll 1
+    for (int b = t0; b < t1; b += 32 * kBatch) {
+      const Keys k = load(b);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        m += __popc(__ballot_sync(0xffffffffu, b + 32 * j + lane < t1 && k.key[j] == limit) & ~k.held[j]);
     }
     if (lane == 0) s.ties[warp] = m;
     sync();
@@ -203,23 +233,28 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
   }
   // which of a step's 32 slots stay
   uint32_t seen = tie;
-  auto stays = [&](int b) -> uint32_t {
-    bool held = true;
+  auto stays = [&](int b, uint32_t key, uint32_t held) -> uint32_t {
     const bool in = b + lane < t1;
-    const uint32_t key = in ? load(b + lane, held) : 0u;
-    const uint32_t same = __ballot_sync(0xffffffffu, some && !held && key == limit);
+    const uint32_t same = some ? __ballot_sync(0xffffffffu, in && key == limit) & ~held : 0u;
     const bool first_ones = seen + __popc(same & ((1u << lane) - 1u)) < need;
     seen += __popc(same);
-    return __ballot_sync(0xffffffffu, in && (held || (some && (key > limit || (key == limit && first_ones)))));
+    return held | __ballot_sync(0xffffffffu, in && some && (key > limit || (key == limit && first_ones)));
   };
   // slots of a step that are free below k, and that survive at or past it
   auto below_k = [&](int b) -> uint32_t { return b + 32 <= k ? ~0u : b >= k ? 0u : (1u << (k - b)) - 1u; };
   auto inside = [&](int b) -> uint32_t { return b + 32 <= t1 ? ~0u : (1u << (t1 - b)) - 1u; };
   uint2 m = make_uint2(0u, 0u);
-  for (int b = t0; b < t1; b += 32) {
-    const uint32_t kept = stays(b);
-    m.x += __popc(~kept & below_k(b) & inside(b));
-    m.y += __popc(kept & ~below_k(b));
+#pragma unroll 1
+  for (int b0 = t0; b0 < t1; b0 += 32 * kBatch) {
+    const Keys ks = load(b0);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int b = b0 + 32 * j;
+      if (b >= t1) break;
+      const uint32_t kept = stays(b, ks.key[j], ks.held[j]);
+      m.x += __popc(~kept & below_k(b) & inside(b));
+      m.y += __popc(kept & ~below_k(b));
+    }
   }
   if (lane == 0) s.moves[warp] = m;
   sync();
@@ -234,14 +269,21 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
   all = warp_sum(all);
   seen = tie;
   const uint32_t lower = (1u << lane) - 1u;
-  for (int b = t0; b < t1; b += 32) {
-    const uint32_t kept = stays(b), low = below_k(b), free = ~kept & low & inside(b), moves = kept & ~low;
-    const int t = b + lane;
-    if (free >> lane & 1) lists[x + __popc(free & lower)] = t;
-    if (moves >> lane & 1) lists[p.list_len + y + __popc(moves & lower)] = t;
-    if (t < t1 && !(low >> lane & 1) && !(kept >> lane & 1)) w[t] = 0.f;
-    x += __popc(free);
-    y += __popc(moves);
+#pragma unroll 1
+  for (int b0 = t0; b0 < t1; b0 += 32 * kBatch) {
+    const Keys ks = load(b0);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int b = b0 + 32 * j, t = b + lane;
+      if (b >= t1) break;
+      const uint32_t kept = stays(b, ks.key[j], ks.held[j]), low = below_k(b), free = ~kept & low & inside(b),
+                     moves = kept & ~low;
+      if (free >> lane & 1) lists[x + __popc(free & lower)] = t;
+      if (moves >> lane & 1) lists[p.list_len + y + __popc(moves & lower)] = t;
+      if (t < t1 && !(low >> lane & 1) && !(kept >> lane & 1)) w[t] = 0.f;
+      x += __popc(free);
+      y += __popc(moves);
+    }
   }
   if (threadIdx.x == 0 && rank == 0) {
     p.moved[r] = (int32_t)all;
@@ -254,16 +296,27 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
 
 constexpr int kMoveThreads = 256;
 constexpr int kUnits = kRecordBytes / 16;               // 41
-constexpr int kPairs = 2;                               // records in flight per warp
+constexpr int kPairs = 4;                               // records in flight per warp
 
-__device__ __forceinline__ unsigned char* record(const EvictParams& p, int r, int t) {
-  const int page = __ldg(p.block_table + (size_t)r * p.max_pages + (t >> 6));
-  return page >= 0 && (int64_t)page < p.num_pages
-             ? p.kv + ((int64_t)page * kPageSize + (t & (kPageSize - 1))) * kRecordBytes
-             : nullptr;
+// Slot of a list's entry `lane` (lanes 0 .. 3: free slots, 4 .. 7: survivors) and its record's row in the cache: -1 where its
+// page is not in it.
+struct Place {
+  int slot;
+  int64_t row;
+};
+
+__device__ __forceinline__ Place place_of(const EvictParams& p, const int32_t* lists, int r, int i, int moved, int lane) {
+  Place x{0, -1};
+  const int at = i + (lane & (kPairs - 1));
+  if (lane >= 2 * kPairs || at >= moved) return x;
+  x.slot = __ldcg(lists + (lane < kPairs ? at : p.list_len + at));
+  const int page = __ldg(p.block_table + (size_t)r * p.max_pages + (x.slot >> 6));
+  if (page >= 0 && (int64_t)page < p.num_pages) x.row = (int64_t)page * kPageSize + (x.slot & (kPageSize - 1));
+  return x;
 }
 
-// (This grid is resident while the selection still writes, so the lists are read from L2.)
+// A warp moves kPairs records at a time, their places looked up while the ones before are under way.  (This grid is resident
+// while the selection still writes, so the lists are read from L2.)
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p) {
   const int lane = threadIdx.x & 31, r = blockIdx.y;
   ptx::griddep_wait();
@@ -271,40 +324,41 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
   const int32_t* lists = p.lists + (size_t)r * 2 * p.list_len;
   float* w = p.weights + (size_t)r * p.weights_stride;
   int32_t* pos = p.positions + (size_t)r * p.positions_stride;
-  for (int i = (blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5)) * kPairs; i < moved; i += step) {
-    unsigned char *from[kPairs], *to[kPairs];
-    int src[kPairs], dst[kPairs];
+  int i = (blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5)) * kPairs;
+  Place next = place_of(p, lists, r, i, moved, lane);
+#pragma unroll 1
+  for (; i < moved; i += step) {
+    const Place here = next;
     uint4 a[kPairs], b[kPairs];
+    const unsigned char* from[kPairs];
 #pragma unroll
     for (int j = 0; j < kPairs; ++j) {
-      from[j] = to[j] = nullptr;
-      src[j] = dst[j] = 0;
-      if (i + j >= moved) continue;
-      dst[j] = __ldcg(lists + i + j);
-      src[j] = __ldcg(lists + p.list_len + i + j);
-      from[j] = record(p, r, src[j]);
-      to[j] = record(p, r, dst[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < kPairs; ++j) {
-      if (!from[j] || !to[j]) continue;
+      const int64_t dst = __shfl_sync(0xffffffffu, here.row, j), src = __shfl_sync(0xffffffffu, here.row, kPairs + j);
+      from[j] = dst >= 0 && src >= 0 ? p.kv + src * kRecordBytes : nullptr;
+      if (!from[j]) continue;
       a[j] = __ldcg(reinterpret_cast<const uint4*>(from[j]) + lane);
       if (lane < kUnits - 32) b[j] = __ldcg(reinterpret_cast<const uint4*>(from[j]) + 32 + lane);
     }
+    // weights and positions: lane j for pair j
+    const int src = __shfl_down_sync(0xffffffffu, here.slot, kPairs);
+    if (lane < kPairs && i + lane < moved) {
+      const float wv = __ldcg(w + src);
+      const int32_t pv = __ldcg(pos + src);
+      w[here.slot] = wv;
+      w[src] = 0.f;
+      pos[here.slot] = pv;
+    }
+    next = place_of(p, lists, r, i + step, moved, lane);
 #pragma unroll
     for (int j = 0; j < kPairs; ++j) {
-      if (i + j >= moved) continue;
-      if (lane == 0) {
-        w[dst[j]] = __ldcg(w + src[j]);
-        w[src[j]] = 0.f;
-        pos[dst[j]] = __ldcg(pos + src[j]);
-      }
-      if (!from[j] || !to[j]) {
-        if (lane == 0 && p.err) atomicOr(p.err, SMLA_DEVERR_PAGE_RANGE);
+      const int64_t dst = __shfl_sync(0xffffffffu, here.row, j);
+      if (!from[j]) {
+        if (lane == 0 && i + j < moved && p.err) atomicOr(p.err, SMLA_DEVERR_PAGE_RANGE);
         continue;
       }
-      reinterpret_cast<uint4*>(to[j])[lane] = a[j];
-      if (lane < kUnits - 32) reinterpret_cast<uint4*>(to[j])[32 + lane] = b[j];
+      unsigned char* to = p.kv + dst * kRecordBytes;
+      reinterpret_cast<uint4*>(to)[lane] = a[j];
+      if (lane < kUnits - 32) reinterpret_cast<uint4*>(to)[32 + lane] = b[j];
     }
   }
 }
