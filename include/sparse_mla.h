@@ -454,7 +454,10 @@ typedef struct smla_shared_dims {
 } smla_shared_dims;
 
 /* Bytes of workspace that sparse_mla_shared_decode needs on a device with
- * sm_count SMs (host only).  Statuses as sparse_mla_dense_plan_for. */
+ * sm_count SMs (host only).  With many rows per prefix the tables' records are
+ * expanded to fp16 in it (1152 bytes per position of prefix_table, and of
+ * block_table where that is short; up to about 5 GiB).  Statuses as
+ * sparse_mla_dense_plan_for. */
 int sparse_mla_shared_workspace_size(const smla_shared_dims* dims, int32_t sm_count, size_t* bytes);
 
 /* sparse_mla_dense_decode of requests that share prefixes: R requests in G
@@ -466,8 +469,15 @@ int sparse_mla_shared_workspace_size(const smla_shared_dims* dims, int32_t sm_co
  *   seq_lens     int32 [B]: lengths without the prefix (0 is fine)
  *   workspace    sparse_mla_shared_workspace_size bytes, 256-byte aligned; its first 4
  *                bytes are the device error word.  Concurrent calls must not share it.
- * Everything else, errors and numerics among it, as in
- * sparse_mla_dense_decode; SMLA_ERR_INVALID_ARG also where G does not divide R. */
+ * Numerics: as in sparse_mla_dense_decode where a prefix is seen by fewer than
+ * 128 rows or its table has fewer than 16 pages.  Else keys and values of the
+ * prefixes, and of short tables of the requests' own, are rounded to fp16 (2^-11 of
+ * each element, or of 2^-27 of the largest of its 32 positions), and so are the
+ * weights; sums are fp32.  A score is then off by about 1e-4 of |q||k| / sqrt(576), lse
+ * by their weighted mean.  A position that is no number, or beyond 2^114, makes
+ * the rows that see it NaN.
+ * Everything else, errors among it, as in sparse_mla_dense_decode;
+ * SMLA_ERR_INVALID_ARG also where G does not divide R. */
 int sparse_mla_shared_decode(const smla_shared_dims* dims, const void* q, const void* kv_cache,
                              const int32_t* prefix_table, const int32_t* prefix_lens, const int32_t* block_table,
                              const int32_t* seq_lens, float sm_scale, void* out, float* lse, void* workspace,

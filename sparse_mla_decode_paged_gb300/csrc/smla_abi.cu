@@ -679,8 +679,11 @@ extern "C" int sparse_mla_kv_evict(const smla_evict_dims* d, float* weights, int
 
 namespace {
 
-// The prefix kernel takes prefixes of at least so many rows, with tables of at least so many pages.
-constexpr int64_t kPairsLeastRows = 128, kPairsLeastPages = 16;
+// The prefix kernel takes prefixes of at least so many rows, with tables of at least so many pages, in all not more than 4 GiB
+// of expanded records (a call's workspace).  Measured, the dense kernel / the prefix kernel, whole calls: 64 rows x 1000 /
+// 4096 / 65536 positions 21.1 / 18.7, 21.2 / 23.5, 40.9 / 56.7 us; 128 rows 21.1 / 18.7, 23.8 / 23.8, 57.9 / 57.4; 256 rows
+// 22.2 / 19.2, 29.6 / 24.9, 87 / 65; 1024 rows 34 / 28, 45 / 35, 260 / 145.  (Shorter ones keep the dense kernel's exact keys.)
+constexpr int64_t kPairsLeastRows = 128, kPairsLeastPages = 16, kPairsMostTiles = ((int64_t)4 << 30) / (9 * 16384);
 
 // How a shared decode runs on a device with `sms` SMs.
 struct SharedPlan {
@@ -704,12 +707,13 @@ int shared_plan(const smla_shared_dims* d, int sms, SharedPlan* plan) {
   const int64_t prefix_rows = all / d->num_prefixes;
   plan->tiles_per_prefix = (int)((d->prefix_pages + (int64_t)1) / 2);
   plan->tiles_per_own = (int)((d->max_pages_per_seq + (int64_t)1) / 2);
-  plan->pairs = prefix_rows >= kPairsLeastRows && d->prefix_pages >= kPairsLeastPages && sms >= 2;
+  plan->pairs = prefix_rows >= kPairsLeastRows && d->prefix_pages >= kPairsLeastPages && sms >= 2 &&
+                (int64_t)d->num_prefixes * plan->tiles_per_prefix <= kPairsMostTiles;
   auto tiles = [&](int nr) {
     return requests * ((rows + nr - 1) / nr) * ((d->max_pages_per_seq + (int64_t)1) / 2) +
            (plan->pairs ? 0 : d->num_prefixes * ((prefix_rows + nr - 1) / nr) * plan->tiles_per_prefix);
   };
-  plan->nr = dense_rows_per_cta(plan->pairs ? rows : prefix_rows, ctas, tiles);
+  plan->nr = dense_rows_per_cta(plan->pairs ? rows : prefix_rows, ctas, tiles(16), tiles(32));
   if (tiles(plan->nr) / ctas >= 0x7fffffff) return SMLA_ERR_UNSUPPORTED;     // a CTA counts its tiles in 32 bits
   plan->own_groups = (int)((rows + plan->nr - 1) / plan->nr);
   plan->prefix_groups = (int)((prefix_rows + plan->nr - 1) / plan->nr);

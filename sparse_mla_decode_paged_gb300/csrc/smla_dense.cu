@@ -50,7 +50,6 @@
 
 #include <atomic>
 #include <cstddef>
-#include <functional>
 
 #include "smla_dense_parts.cuh"
 #include "smla_device.cuh"
@@ -1729,10 +1728,10 @@ size_t dense_workspace_bytes(int ctas, int nr) {
   return kWorkspaceHeader + kDescBytes + lse_part_bytes(ctas, nr) + (size_t)2 * ctas * nr * kDLatent * sizeof(float);
 }
 
-// The fewest rows per CTA with which it has at most a few tiles: `tiles` with groups of a given size.
-int dense_rows_per_cta(long long rows, int ctas, const std::function<long long(int)>& tiles) {
-  if (rows <= 16 || tiles(16) <= kMostTiles16 * (long long)ctas) return 16;
-  if (rows <= 32 || tiles(32) <= kMostTiles32 * (long long)ctas) return 32;
+// The fewest rows per CTA with which it has at most a few tiles: tiles16 with groups of 16 rows, tiles32 with groups of 32.
+int dense_rows_per_cta(long long rows, int ctas, long long tiles16, long long tiles32) {
+  if (rows <= 16 || tiles16 <= kMostTiles16 * (long long)ctas) return 16;
+  if (rows <= 32 || tiles32 <= kMostTiles32 * (long long)ctas) return 32;
   return 64;
 }
 
@@ -1767,7 +1766,7 @@ extern "C" int sparse_mla_dense_plan_for(const smla_dense_dims* d, int32_t sm_co
   // the fewest rows with which a CTA has at most a few tiles if every request is as long as its table.
   const int64_t tiles = d->batch / sq * ((d->max_pages_per_seq + (int64_t)1) / 2);
   auto groups = [&](int nr) { return (rows + nr - 1) / nr; };
-  plan->rows_per_cta = dense_rows_per_cta(rows, plan->ctas, [&](int nr) { return tiles * groups(nr); });
+  plan->rows_per_cta = dense_rows_per_cta(rows, plan->ctas, tiles * groups(16), tiles * groups(32));
   plan->row_groups = (int32_t)groups(plan->rows_per_cta);
   // a CTA counts its tiles in 32 bits
   const int64_t most = tiles * plan->row_groups;

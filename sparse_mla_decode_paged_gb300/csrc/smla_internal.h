@@ -4,8 +4,6 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <functional>
-
 #include "sparse_mla.h"
 
 namespace smla {
@@ -257,7 +255,7 @@ cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t stream);
 cudaError_t launch_kv_read(const ReadParams& p, cudaStream_t stream);
 cudaError_t launch_dense(const DenseParams& p, cudaStream_t stream);
 size_t dense_workspace_bytes(int ctas, int nr);
-int dense_rows_per_cta(long long rows, int ctas, const std::function<long long(int)>& tiles);
+int dense_rows_per_cta(long long rows, int ctas, long long tiles16, long long tiles32);
 cudaError_t launch_prefix(const PrefixParams& p, cudaStream_t stream);
 cudaError_t launch_shared(const SharedParams& p, cudaStream_t stream);
 cudaError_t launch_weights(const WeightsParams& p, int sms, cudaStream_t stream);

@@ -1,24 +1,30 @@
-// Attention of many rows over shared prefixes: the part of the shared decode that is bound by the tensor core.
+// Attention of many rows over shared prefixes: the part of the shared decode that is bound by the SM, not by HBM.
 //
-//   s_t = sm_scale q.k_t,  out = sum_t softmax_t(s) v_t,  lse = ln sum_t exp(s_t)   over the positions of a prefix.
+//   s_t = sm_scale q.k_t,  out = sum_t softmax_t(s) v_t,  lse = ln sum_t exp(s_t)
 //
-// Expand.  The records of every prefix are written once as fp16, K' = [code scale | rope] 2^-e, e one exponent per 32
-// positions that puts their largest value into [2^13, 2^14): one rounding of 2^-11 of the value (2^-38 of the
-// largest for the smallest).  The rows serve all row blocks, so the conversion is not in the loop that feeds
-// the tensor core.  A page is 9 chunks of 64 dims, 64 rows of 128 bytes each, 128B-swizzled as in shared memory.
+// over the positions of a prefix, for the rows of all requests that share it; short positions of the requests' own go along as
+// further segments, each seen by its request's rows.
 //
-// Attention.  A pair of CTAs (a cluster of two, cta_group::2) takes 128 rows, 64 each, through the tiles: 64 rows are what
-// a CTA's tensor memory holds of O (64 x 512 fp32, half of it) beside two score buffers, and what shared memory holds of q
-// (72 KB) beside the ring of operands.  Scores: M = 128 rows, N = 128 positions; each CTA loads the 9 chunks of its 64
-// positions.  Values: M = 128, N = 256 dims twice; each CTA loads its 4 chunks of 64 dims of all 128 positions.  So of the 147 KB
-// of a tile a CTA loads 136 KB for 64 rows, where alone it would load 278 KB.  TMEM lane l holds row l % 64, the scores
-// of positions 64 (l / 64) .. and, of each half of the dims, dims 128 (l / 64) ...
-//   Weights p = 2^(s + e - R) as fp16, R a power-of-two reference per row that puts the first tile's largest at 2^6 and moves when
-// a weight would pass 2^15 (the accumulators are then scaled back); l = sum p 2^-e in fp32.
-// q is exact in fp16 but for elements below 2^-20 of their row's largest.
+// Expand.  The records are written once as fp16, K' = [code scale | rope] 2^-e, e one exponent per 32 positions that puts
+// their largest value into [2^13, 2^14): one rounding of 2^-11 of the value (2^-38 of the largest for the smallest).  They
+// serve all row blocks, so the conversion is not in the loop that feeds the tensor core.  A page is 9 chunks of 64
+// dims, 64 rows of 128 bytes each, 128B-swizzled as in shared memory.
 //
-// Tiles of all (prefix, block of 128 rows), laid end to end, are shared out over the pairs in equal runs; a block that crosses
-// runs leaves fp32 partials for the join.
+// Attention.  A pair of CTAs (a cluster of two, cta_group::2) takes 128 rows, 64 each, through the tiles of 128 positions: 64
+// rows are what a CTA's tensor memory holds of O (64 x 512 fp32, half of it) beside two score buffers, and what its shared
+// memory holds of q (72 KB) beside the ring of operands.  Scores: M = 128 rows, N = 128 positions; each CTA loads the 9
+// chunks of its page.  Values: M = 128, N = 256 dims twice; each CTA loads its 4 chunks of both pages: 136 KB per tile,
+// where a CTA alone would need 278 KB for its 64 rows.  TMEM lane l holds row l % 64: the scores of page l / 64, and dims
+// 128 (l / 64) .. of each half of the dims.
+//   Weights are p = 2^(s + e - R) in fp16, R a power-of-two reference per row that puts the first tile's largest at 2^6 and
+// moves when a weight would pass 2^15 (the accumulators are then scaled back); l = sum p 2^-e in fp32.  q is exact in fp16
+// but for elements below 2^-20 of their row's largest.
+//   The tiles of all (segment, block of 128 rows) items, laid end to end with a few units for each item's start, are
+// shared out over the pairs in equal runs; an item that crosses runs leaves fp32 partials for the join.
+//
+// What bounds it: shared memory.  A tile's operands and copies are 392 KB per CTA (q 72, keys 72, weights 48, values 64, copies
+// 136), 3060 cycles at 128 bytes each; measured 3080 (the products alone 2180).  Measured, whole calls: 2048 rows x 32768
+// positions 126 us (146 GFLOP), of them 11 the expansion and 9 the join.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -51,35 +57,15 @@ __device__ __forceinline__ float largest_code(const uint4& v) {
   return f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)m)).x;
 }
 
-// Half a page per CTA, 4 positions per warp, 16 latent dims and 2 rope dims per lane.  (32768 positions, with the launch: a
-// tile per CTA with one exponent 17.7 us, a page 12.8, half a page TBD.)  Positions that are no numbers are written as zeros
+// Half a page at a time, 4 positions per warp, 16 latent dims and 2 rope dims per lane.  (32768 positions, with the
+// launch: a page per CTA 12.8 us, half a page 13.7, with a lane's 32 bytes stored at once instead of in halves of two sectors
+// 10.7: 59 MB, 5.5 TB/s.)  Positions that are no numbers are written as zeros
 // and marked, because a weight of 0 would make a NaN of them for the rows that do not see them.
-__global__ void __launch_bounds__(32 * kExpandWarps) expand_kernel(const PrefixParams p) {
-  __shared__ float top_s[kExpandWarps];
-  __shared__ uint32_t marks_s[kExpandWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0) ptx::griddep_launch_dependents();
-  // CTAs: the prefixes' half pages, then the requests'
-  const int per_prefix = 4 * p.tiles_per_prefix, per_own = 4 * p.tiles_per_own, in_prefixes = p.prefixes * per_prefix;
-  const bool own = (int)blockIdx.x >= in_prefixes;
-  const int x = own ? blockIdx.x - in_prefixes : blockIdx.x, per = own ? per_own : per_prefix;
-  const int r = x / per, part = x - r * per, lp = part >> 1, g = own ? p.prefixes + r : r;
-  const int len = segment_len(p, g), pages = own ? p.own_pages : p.pages;
-  if (part == 0 && threadIdx.x == 0) {
-    bool over = false;
-    if (own) {
-      for (int b = r * p.q_per_req; b < (r + 1) * p.q_per_req; ++b)
-        over |= __ldg(p.own_lens + b) > (long long)p.own_pages * kPageSize;
-    } else {
-      over = __ldg(p.lens + r) > (long long)p.pages * kPageSize;
-    }
-    if (over) atomicOr(p.err, SMLA_DEVERR_PAGE_RANGE);
-  }
-  const int t0 = part * kExpandPart;
-  // (the rest of the last tile is written where no position lies in it, too: zeros, which its weights of 0 meet)
-  if (t0 >= tiles_of(len) * kDenseTile) return;
+__device__ __forceinline__ void expand_part(const PrefixParams& p, int g, bool own, int part, int len, const int32_t* table,
+                                            float* top_s, uint32_t* marks_s, int warp, int lane) {
+  const int t0 = part * kExpandPart, lp = part >> 1;
   const bool used = lp * kPageSize < len;
-  const int page = used ? __ldg((own ? p.own_table : p.table) + (size_t)r * pages + lp) : -1;
+  const int page = used ? __ldg(table + lp) : -1;
   const bool good = page >= 0 && (int64_t)page < p.num_pages;
   if (!good && used && threadIdx.x == 0) atomicOr(p.err, SMLA_DEVERR_PAGE_RANGE);
   uint4 code[kExpandTokens];
@@ -151,6 +137,34 @@ __global__ void __launch_bounds__(32 * kExpandWarps) expand_kernel(const PrefixP
     marks = __reduce_or_sync((1u << kExpandWarps) - 1u, marks_s[threadIdx.x] << threadIdx.x * kExpandTokens);
     if (threadIdx.x == 0) p.info[2 * at + (part & 1)] = make_int4(e, good, (int)marks, 0);
   }
+  __syncthreads();                                         // (the shared values have been read)
+}
+
+__global__ void __launch_bounds__(32 * kExpandWarps) expand_kernel(const PrefixParams p, int per_prefix, int per_own) {
+  __shared__ float top_s[kExpandWarps];
+  __shared__ uint32_t marks_s[kExpandWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) ptx::griddep_launch_dependents();
+  // CTAs: per_prefix for each prefix, then per_own for each request
+  const bool own = (int)blockIdx.x >= p.prefixes * per_prefix;
+  const int x = own ? blockIdx.x - p.prefixes * per_prefix : blockIdx.x, per = own ? per_own : per_prefix;
+  const int r = x / per, g = own ? p.prefixes + r : r;
+  const int len = segment_len(p, g), pages = own ? p.own_pages : p.pages;
+  if (x == r * per && threadIdx.x == 0) {
+    bool over = false;
+    if (own) {
+      for (int b = r * p.q_per_req; b < (r + 1) * p.q_per_req; ++b)
+        over |= __ldg(p.own_lens + b) > (long long)p.own_pages * kPageSize;
+    } else {
+      over = __ldg(p.lens + r) > (long long)p.pages * kPageSize;
+    }
+    if (over) atomicOr(p.err, SMLA_DEVERR_PAGE_RANGE);
+  }
+  // (the rest of the last tile is written where no position lies in it, too: zeros, which its weights of 0 meet)
+  const int parts = tiles_of(len) * (kDenseTile / kExpandPart);
+#pragma unroll 1
+  for (int part = x - r * per; part < parts; part += per)
+    expand_part(p, g, own, part, len, (own ? p.own_table : p.table) + (size_t)r * pages, top_s, marks_s, warp, lane);
 }
 
 // ----------------------------------------------------------------------------- attention
@@ -343,9 +357,8 @@ __device__ void relay_role(const PrefixParams& p, uint32_t base, Bars* bars) {
   if (follows) pass(4);
 }
 
-// Scores and values are issued by a warp each: a warp that has waited for a slot leaves the tensor core idle for the wait's
-// 100 cycles, 14 times per tile, where the other's products do not fill them (one warp for both: 145 us for 2048 rows x
-// 32768 positions instead of TBD).  Both follow the ring in the order of the copies and pass over each other's slots.
+// Scores and values are issued by a warp each, so that what one waits for hides behind the other's products.  Both follow
+// the ring in the order of the copies and pass over each other's slots.
 __device__ void qk_role(const PrefixParams& p, uint32_t base, uint32_t tmem, Bars* bars) {
   constexpr uint32_t kIdesc = ptx::idesc_f16(128, 128, 0, 0);
   Walk w(bars);
@@ -457,7 +470,7 @@ __device__ void pv_role(const PrefixParams& p, uint32_t base, uint32_t tmem, Bar
 
 // 64 rows of q as fp16 times 2^-x, x per row such that its largest element lies in [2^3, 2^4); the rows' factors
 // 2^x sm_scale log2 e.  A row with an infinity becomes NaN.  One row at a time, the next two's loads in flight: straight code for
-// a warp's eight rows took 11000 cycles instead of TBD, most of them for its instructions.
+// a warp's eight rows took 11000 cycles instead of 5300, most of them for its instructions.
 __device__ __forceinline__ void load_q(const PrefixParams& p, int first, int rows, unsigned char* sm, uint32_t base, int warp,
                                        int lane) {
   constexpr int kRows = kRowsPerCta / kSoftWarps;
@@ -551,7 +564,7 @@ __device__ void softmax_role(const PrefixParams& p, unsigned char* sm, uint32_t 
       const float lse = none ? -CUDART_INF_F : (ref + log2f(z)) * kLn2, inv = none ? 0.f : 1.f / z;
       if (row < to_rows && part == 0) (whole ? p.lse32 : p.slots_lse)[to_row + row] = lse;
       // 32 rows x 32 dims at a time through the P buffers, which nobody writes before the next item's rows are there:
-      // whole lines to global memory (rows of 16 bytes per lane took 12800 cycles instead of TBD)
+      // whole lines to global memory (16 bytes of a row per lane: 12800 cycles instead of 7400)
       float* o_to = (whole ? p.out32 : p.slots) + (to_row + row - lane) * kDLatent + 256 * half + 128 * side;
       const uint32_t stage = base + kP + warp * 4096;
       const int most = to_rows - 32 * (quad & 1);          // of these 32 rows
@@ -842,8 +855,14 @@ cudaError_t launch_prefix(const PrefixParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev < 64) set[dev].store(true, std::memory_order_relaxed);
   }
-  const long long pages = 2 * ((long long)p.prefixes * p.tiles_per_prefix + (p.own ? (long long)p.requests * p.tiles_per_own : 0));
-  expand_kernel<<<(unsigned)(2 * pages), 32 * kExpandWarps, 0, stream>>>(p);
+  // a CTA per half page, up to about eight per SM (tables are often far wider than what is in them)
+  auto ctas = [&](int segments, int tiles) {
+    const long long room = (16ll * p.pairs + segments - 1) / segments, parts = 4ll * tiles;
+    return (int)(parts < room ? parts : room);
+  };
+  const int per_prefix = ctas(p.prefixes, p.tiles_per_prefix), per_own = p.own ? ctas(p.requests, p.tiles_per_own) : 0;
+  expand_kernel<<<p.prefixes * per_prefix + (p.own ? p.requests * per_own : 0), 32 * kExpandWarps, 0, stream>>>(p, per_prefix,
+                                                                                                              per_own);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};

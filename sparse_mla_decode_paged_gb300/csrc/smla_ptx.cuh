@@ -162,8 +162,8 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, v
 }
 
 // Arrive on an mbarrier of any CTA of the cluster (address from mapa).  Orders what the tensor core and the copies do, which
-// need no more (a release over the cluster waits for every store of the SM: 11000 cycles per tile of the prefix kernel
-// instead of 3300); data that another CTA's threads are to read needs a cluster barrier.
+// need no more (a release over the cluster waits for every store of the SM: 304 us instead of 145 for 2048 rows x 32768
+// positions of the prefix kernel); data that another CTA's threads are to read needs a cluster barrier.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t caddr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
 }
