@@ -797,6 +797,7 @@ extern "C" int sparse_mla_shared_decode(const smla_shared_dims* d, const void* q
   PrefixParams& x = s.prefix;                                  // (what the join needs in any case first)
   x.prefixes = d->num_prefixes;
   x.rows = p.prefix_rows;
+  x.requests = p.requests;
   x.q_per_req = p.q_per_req;
   x.H = p.H;
   x.all_rows = (size_t)p.B * p.H;
@@ -816,7 +817,6 @@ extern "C" int sparse_mla_shared_decode(const smla_shared_dims* d, const void* q
     x.own = plan.own;
     x.own_table = block_table;
     x.own_lens = seq_lens;
-    x.requests = p.requests;
     x.own_pages = p.max_pages;
     x.own_blocks = plan.own_blocks;
     x.tiles_per_own = plan.tiles_per_own;

@@ -1527,13 +1527,11 @@ __device__ __forceinline__ void add_part(float4& acc, float w, const float4& v) 
   acc.w = fmaf(w, v.w, acc.w);
 }
 
-template <int kForm>
-__device__ __forceinline__ void store_joined(const DenseParams& p, const Rows& it, int row, int block, int lane, const float4& v,
+__device__ __forceinline__ void store_joined(const DenseParams& p, size_t row, int block, int lane, const float4& v,
                                              float lse) {
-  const size_t to = ((size_t)it.first + row) * kDLatent + 128 * block;
-  if constexpr (kForm == kShared) reinterpret_cast<float4*>(out32_of(p, it) + to)[lane] = v;
-  else reinterpret_cast<uint2*>(p.out + to)[lane] = make_uint2(f32x2_to_bf16x2(v.x, v.y), f32x2_to_bf16x2(v.z, v.w));
-  if (lane == 0 && block == 0) lse_of<kForm>(p, it)[row] = lse;
+  reinterpret_cast<uint2*>(p.out + row * kDLatent + 128 * block)[lane] =
+      make_uint2(f32x2_to_bf16x2(v.x, v.y), f32x2_to_bf16x2(v.z, v.w));
+  if (lane == 0 && block == 0) p.lse[row] = lse;
 }
 
 // Joins the partials of the items that cross CTA runs: lse = ln sum_s exp(lse_s), out = sum_s exp(lse_s - lse)
@@ -1545,7 +1543,6 @@ __device__ __forceinline__ void store_joined(const DenseParams& p, const Rows& i
 // positions of 64 heads (6 parts) 62 / 50 us, 10 x 8192 of 64 heads (16 parts) 42.3 / 38.5 us, 10 x 8192 of 16 heads 23.1 /
 // 24.8 us; of 64 parts and more one warp would take its loads in eight rounds.
 // This grid is resident while the decode's still writes, so partials are read from L2, not through the read-only path.
-template <int kForm>
 __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const DenseParams p, const RunDesc* descs,
                                                                     const float* lse_part, const float* o_part) {
   __shared__ int parts_s[kDenseMaxCtas], item_s[kDenseMaxCtas];     // of the item that begins in CTA c, 0: none to join
@@ -1555,7 +1552,6 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const DenseP
   __shared__ float lse_s;
   __shared__ float4 sum_s[4][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (kForm == kShared && tid == 0) ptx::griddep_launch_dependents();    // the join
   ptx::griddep_wait();
   for (int c = tid; c < p.ctas; c += kMergeThreads) {
     const RunDesc d = descs[c];
@@ -1584,7 +1580,7 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const DenseP
   const int nr = p.nr;
   for (int idx = blockIdx.x * (kMergeThreads / 32) + warp; idx < few_s * nr * 4; idx += gridDim.x * (kMergeThreads / 32)) {
     const int c = order_s[idx / (4 * nr)], row = (idx >> 2) % nr, block = idx & 3, parts = parts_s[c];
-    const Rows it = rows_of<kForm>(p, item_s[c]);
+    const Rows it = rows_of<kPlain>(p, item_s[c]);
     if (row >= it.nrows) continue;
     const PartRows rows{c, row, nr};
     const float4* o = reinterpret_cast<const float4*>(o_part) + 32 * block + lane;
@@ -1612,12 +1608,12 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const DenseP
 #pragma unroll
     for (int s = kMergeBatch; s < kFewParts; ++s)
       if (s < parts) add_part(acc, __shfl_sync(0xffffffffu, w, s), v[s - kMergeBatch]);
-    store_joined<kForm>(p, it, row, block, lane, acc,
-                        z == 0.f ? -CUDART_INF_F : m + logf(z));
+    store_joined(p, (size_t)it.first + row, block, lane, acc,
+                 z == 0.f ? -CUDART_INF_F : m + logf(z));
   }
   for (int idx = blockIdx.x; idx < many_s * nr * 4; idx += gridDim.x) {
     const int c = order_s[kDenseMaxCtas - 1 - idx / (4 * nr)], row = (idx >> 2) % nr, block = idx & 3, parts = parts_s[c];
-    const Rows it = rows_of<kForm>(p, item_s[c]);
+    const Rows it = rows_of<kPlain>(p, item_s[c]);
     if (row >= it.nrows) continue;                       // uniform over the CTA
     // warp w takes parts w, w + 4, ...: their rows in flight before the weights are known
     const PartRows rows{c, row, nr};
@@ -1668,7 +1664,7 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const DenseP
     if (warp == 0) {
 #pragma unroll
       for (int s = 1; s < 4; ++s) add_part(acc, 1.f, sum_s[s][lane]);
-      store_joined<kForm>(p, it, row, block, lane, acc, lse_s);
+      store_joined(p, (size_t)it.first + row, block, lane, acc, lse_s);
     }
   }
 }
@@ -1701,7 +1697,7 @@ cudaError_t launch_nr(const DenseParams& p, unsigned char* ws, cudaStream_t stre
   float* o_part = reinterpret_cast<float*>(ws + kWorkspaceHeader + kDescBytes + lse_part_bytes(p.ctas, NR));
   dense_kernel<NR, kForm><<<p.ctas, DC<NR>::kThreads, kBytes, stream>>>(p, map, smap, descs, lse_part, o_part);
   e = cudaGetLastError();
-  if (e != cudaSuccess || one_tile(p)) return e;
+  if (e != cudaSuccess || one_tile(p) || kForm == kShared) return e;     // (the join reads the parts itself)
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(8 * p.ctas);
   cfg.blockDim = dim3(kMergeThreads);
@@ -1711,7 +1707,7 @@ cudaError_t launch_nr(const DenseParams& p, unsigned char* ws, cudaStream_t stre
   a[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = a;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, dense_merge_kernel<kForm == kShared ? kShared : kPlain>, p, (const RunDesc*)descs, (const float*)lse_part,
+  return cudaLaunchKernelEx(&cfg, dense_merge_kernel, p, (const RunDesc*)descs, (const float*)lse_part,
                             (const float*)o_part);
 }
 
@@ -1726,6 +1722,16 @@ cudaError_t launch_form(const DenseParams& p, unsigned char* ws, cudaStream_t st
 
 size_t dense_workspace_bytes(int ctas, int nr) {
   return kWorkspaceHeader + kDescBytes + lse_part_bytes(ctas, nr) + (size_t)2 * ctas * nr * kDLatent * sizeof(float);
+}
+
+DenseSlots dense_slots(const DenseParams& p) {
+  const unsigned char* ws = reinterpret_cast<const unsigned char*>(p.err) + kWorkspaceHeader;
+  static_assert(sizeof(RunDesc) == sizeof(int2) && offsetof(RunDesc, item) == 0, "a pair of whole numbers");
+  DenseSlots s;
+  s.descs = reinterpret_cast<const int2*>(ws);
+  s.lse = reinterpret_cast<const float*>(ws + kDescBytes);
+  s.o = reinterpret_cast<const float*>(ws + kDescBytes + lse_part_bytes(p.ctas, p.nr));
+  return s;
 }
 
 // The fewest rows per CTA with which it has at most a few tiles: tiles16 with groups of 16 rows, tiles32 with groups of 32.

@@ -255,6 +255,13 @@ cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t stream);
 cudaError_t launch_kv_read(const ReadParams& p, cudaStream_t stream);
 cudaError_t launch_dense(const DenseParams& p, cudaStream_t stream);
 size_t dense_workspace_bytes(int ctas, int nr);
+// Where a call with prefixes leaves the results of items that cross CTA runs: {item, parts} of the one that begins in each CTA, and
+// slots of nr rows, part 0 in slot 1 of that CTA, part s in slot 0 of the s-th after it.
+struct DenseSlots {
+  const int2* descs;          // [ctas]
+  const float *o, *lse;       // [2 ctas][nr][512], [2 ctas][nr]
+};
+DenseSlots dense_slots(const DenseParams& p);
 int dense_rows_per_cta(long long rows, int ctas, long long tiles16, long long tiles32);
 cudaError_t launch_prefix(const PrefixParams& p, cudaStream_t stream);
 cudaError_t launch_shared(const SharedParams& p, cudaStream_t stream);

@@ -20,15 +20,21 @@ constexpr int kJoinDims = 128;             // threads that share a row's 512 dim
 constexpr int kJoinGroups = 4;            // groups of them that share its parts, where they are many
 constexpr int kJoinBatch = 8;             // parts in flight per thread
 constexpr int kManyParts = 24;
-constexpr int kMostParts = 1024 + 2;
+constexpr int kMostParts = 2 * kDenseMaxCtas;
 
 // Where a row's results lie: `parts` of them, the s-th at place(s) of the arrays.
 struct Parts {
   const float *o, *lse;
-  int parts, pair, at;
+  int parts, pair, at, rows;              // one result at row `at`, or parts in slots of `rows` rows from that pair (or CTA) on
   __device__ __forceinline__ size_t place(int s) const {
-    return parts == 1 ? (size_t)at : (size_t)(2 * (pair + s) + (s == 0 ? 1 : 0)) * kPrefixRows + at;
+    return parts == 1 ? (size_t)at : (size_t)(2 * (pair + s) + (s == 0 ? 1 : 0)) * rows + at;
   }
+};
+
+// The dense kernel's side of a call.
+struct DenseItems {
+  DenseSlots slots;
+  int ctas, nr, groups, prefix_groups;    // rows per slot, row groups per request and per prefix
 };
 
 // The prefix kernel's results of row r of segment g: a whole one lies with the rows, the first of several in slot 1 of its
@@ -36,7 +42,7 @@ struct Parts {
 __device__ __forceinline__ Parts segment_parts(const PrefixParams& p, int g, int row) {
   const Segment seg = segment_of(p, g);
   const int r = row - seg.first_row, block = r / kPrefixRows;
-  Parts x{p.slots, p.slots_lse, 0, 0, r - block * kPrefixRows};
+  Parts x{p.slots, p.slots_lse, 0, 0, r - block * kPrefixRows, kPrefixRows};
   const long long* ends = p.begins + segments_of(p);
   const long long total = __ldcg(ends), start = __ldcg(ends + 1), begin = __ldcg(p.begins + g);
   const long long units = (__ldcg(p.begins + g + 1) - begin) / seg.blocks;       // of an item
@@ -67,19 +73,34 @@ __device__ __forceinline__ Parts segment_parts(const PrefixParams& p, int g, int
 // One CTA per row; a group of 128 threads takes 4 dims each of every kGroups-th part.  (This grid is resident while results
 // are still written, so they are read from L2.)
 template <int kGroups>
-__global__ void __launch_bounds__(kJoinDims * kGroups) join_kernel(const PrefixParams p, uint16_t* out, float* lse_out) {
+__global__ void __launch_bounds__(kJoinDims * kGroups) join_kernel(const PrefixParams p, const DenseItems d, uint16_t* out,
+                                                                   float* lse_out) {
   __shared__ Parts own_s, prefix_s;
   __shared__ float w_s[kMostParts], z_s;
   __shared__ float4 sum_s[kGroups][kJoinDims];
   const int row = blockIdx.x, lane = threadIdx.x & 31, dim = threadIdx.x % kJoinDims, group = threadIdx.x / kJoinDims;
+  const int own_rows = p.q_per_req * p.H, req = row / own_rows, prefix = row / p.rows;
+  const bool own_dense = !p.own, prefix_dense = p.pairs == 0;
+  // the dense kernel's items of this row, and its row in them
+  const int own_group = own_dense ? (row - req * own_rows) / d.nr : 0;
+  const int prefix_group = prefix_dense ? (row - prefix * p.rows) / d.nr : 0;
+  if (threadIdx.x == 0 && own_dense) own_s = Parts{p.out32, p.lse32, 1, 0, row, 0};
+  if (threadIdx.x == 0 && prefix_dense)
+    prefix_s = Parts{p.out32 + p.all_rows * kDLatent, p.lse32 + p.all_rows, 1, 0, row, 0};
+  __syncthreads();
   ptx::griddep_wait();
-  if (threadIdx.x == 0) {
-    if (p.own) own_s = segment_parts(p, p.prefixes + row / (p.q_per_req * p.H), row);
-    else own_s = Parts{p.out32, p.lse32, 1, 0, row};
-  }
-  if (threadIdx.x == 32) {
-    if (p.pairs > 0) prefix_s = segment_parts(p, row / p.rows, row);
-    else prefix_s = Parts{p.out32 + p.all_rows * kDLatent, p.lse32 + p.all_rows, 1, 0, row};
+  if (threadIdx.x == 0 && !own_dense) own_s = segment_parts(p, p.prefixes + req, row);
+  if (threadIdx.x == 32 && !prefix_dense) prefix_s = segment_parts(p, prefix, row);
+  if (own_dense) {
+    const int own_item = req * d.groups + own_group;
+    const int prefix_item = prefix_dense ? p.requests * d.groups + prefix * d.prefix_groups + prefix_group : -1;
+    for (int c = threadIdx.x; c < d.ctas; c += kJoinDims * kGroups) {
+      const int2 x = __ldcg(d.slots.descs + c);            // {item, parts}; an item is found at most once
+      if (x.y > 0 && x.x == own_item)
+        own_s = Parts{d.slots.o, d.slots.lse, x.y, c, row - req * own_rows - own_group * d.nr, d.nr};
+      if (x.y > 0 && x.x == prefix_item)
+        prefix_s = Parts{d.slots.o, d.slots.lse, x.y, c, row - prefix * p.rows - prefix_group * d.nr, d.nr};
+    }
   }
   __syncthreads();
   const Parts a = own_s, b = prefix_s;
@@ -160,8 +181,17 @@ cudaError_t launch_shared(const SharedParams& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if (!x.own) e = launch_dense(p.dense, stream);
   if (e != cudaSuccess) return e;
+  DenseItems d{};
+  if (!x.own) {
+    d.slots = dense_slots(p.dense);
+    d.ctas = p.dense.ctas;
+    d.nr = p.dense.nr;
+    d.groups = p.dense.groups;
+    d.prefix_groups = p.dense.prefix_groups;
+  }
   // parts of a prefix's block of rows, about
-  const long long blocks = (long long)x.prefixes * x.row_blocks, parts = x.pairs > 0 ? x.pairs / blocks : 1;
+  const long long parts = x.pairs > 0 ? x.pairs / ((long long)x.prefixes * x.row_blocks)
+                                      : p.dense.ctas / ((long long)x.prefixes * p.dense.prefix_groups);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)x.all_rows);
   cfg.blockDim = dim3(parts > kManyParts ? kJoinDims * kJoinGroups : kJoinDims);
@@ -171,8 +201,8 @@ cudaError_t launch_shared(const SharedParams& p, cudaStream_t stream) {
   a[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = a;
   cfg.numAttrs = 1;
-  return parts > kManyParts ? cudaLaunchKernelEx(&cfg, join_kernel<kJoinGroups>, x, p.out, p.lse)
-                            : cudaLaunchKernelEx(&cfg, join_kernel<1>, x, p.out, p.lse);
+  return parts > kManyParts ? cudaLaunchKernelEx(&cfg, join_kernel<kJoinGroups>, x, d, p.out, p.lse)
+                            : cudaLaunchKernelEx(&cfg, join_kernel<1>, x, d, p.out, p.lse);
 }
 
 }  // namespace smla
