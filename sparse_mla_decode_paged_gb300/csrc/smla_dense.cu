@@ -1698,6 +1698,7 @@ cudaError_t launch_nr(const DenseParams& p, unsigned char* ws, cudaStream_t stre
   dense_kernel<NR, kForm><<<p.ctas, DC<NR>::kThreads, kBytes, stream>>>(p, map, smap, descs, lse_part, o_part);
   e = cudaGetLastError();
   if (e != cudaSuccess || one_tile(p) || kForm == kShared) return e;     // (the join reads the parts itself)
+  if (kForm == kMasked) return launch_row_merge(p, stream);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(8 * p.ctas);
   cfg.blockDim = dim3(kMergeThreads);

@@ -265,6 +265,7 @@ DenseSlots dense_slots(const DenseParams& p);
 int dense_rows_per_cta(long long rows, int ctas, long long tiles16, long long tiles32);
 cudaError_t launch_prefix(const PrefixParams& p, cudaStream_t stream);
 cudaError_t launch_shared(const SharedParams& p, cudaStream_t stream);
+cudaError_t launch_row_merge(const DenseParams& p, cudaStream_t stream);
 cudaError_t launch_weights(const WeightsParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_evict(const EvictParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_gather_rows(const int32_t* bt, const int32_t* topk, const int32_t* seq_lens,

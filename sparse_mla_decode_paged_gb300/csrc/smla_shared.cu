@@ -70,40 +70,12 @@ __device__ __forceinline__ Parts segment_parts(const PrefixParams& p, int g, int
   return x;
 }
 
-// One CTA per row; a group of 128 threads takes 4 dims each of every kGroups-th part.  (This grid is resident while results
-// are still written, so they are read from L2.)
+// Joins a row's parts, those of a before those of b.  A group of 128 threads takes 4 dims each of every kGroups-th part.
 template <int kGroups>
-__global__ void __launch_bounds__(kJoinDims * kGroups) join_kernel(const PrefixParams p, const DenseItems d, uint16_t* out,
-                                                                   float* lse_out) {
-  __shared__ Parts own_s, prefix_s;
+__device__ __forceinline__ void join_row(const Parts& a, const Parts& b, uint16_t* out, float* lse_out, int row) {
   __shared__ float w_s[kMostParts], z_s;
   __shared__ float4 sum_s[kGroups][kJoinDims];
-  const int row = blockIdx.x, lane = threadIdx.x & 31, dim = threadIdx.x % kJoinDims, group = threadIdx.x / kJoinDims;
-  const int own_rows = p.q_per_req * p.H, req = row / own_rows, prefix = row / p.rows;
-  const bool own_dense = !p.own, prefix_dense = p.pairs == 0;
-  // the dense kernel's items of this row, and its row in them
-  const int own_group = own_dense ? (row - req * own_rows) / d.nr : 0;
-  const int prefix_group = prefix_dense ? (row - prefix * p.rows) / d.nr : 0;
-  if (threadIdx.x == 0 && own_dense) own_s = Parts{p.out32, p.lse32, 1, 0, row, 0};
-  if (threadIdx.x == 0 && prefix_dense)
-    prefix_s = Parts{p.out32 + p.all_rows * kDLatent, p.lse32 + p.all_rows, 1, 0, row, 0};
-  __syncthreads();
-  ptx::griddep_wait();
-  if (threadIdx.x == 0 && !own_dense) own_s = segment_parts(p, p.prefixes + req, row);
-  if (threadIdx.x == 32 && !prefix_dense) prefix_s = segment_parts(p, prefix, row);
-  if (own_dense) {
-    const int own_item = req * d.groups + own_group;
-    const int prefix_item = prefix_dense ? p.requests * d.groups + prefix * d.prefix_groups + prefix_group : -1;
-    for (int c = threadIdx.x; c < d.ctas; c += kJoinDims * kGroups) {
-      const int2 x = __ldcg(d.slots.descs + c);            // {item, parts}; an item is found at most once
-      if (x.y > 0 && x.x == own_item)
-        own_s = Parts{d.slots.o, d.slots.lse, x.y, c, row - req * own_rows - own_group * d.nr, d.nr};
-      if (x.y > 0 && x.x == prefix_item)
-        prefix_s = Parts{d.slots.o, d.slots.lse, x.y, c, row - prefix * p.rows - prefix_group * d.nr, d.nr};
-    }
-  }
-  __syncthreads();
-  const Parts a = own_s, b = prefix_s;
+  const int lane = threadIdx.x & 31, dim = threadIdx.x % kJoinDims, group = threadIdx.x / kJoinDims;
   const int parts = a.parts + b.parts;
   auto row_of = [&](int s) {
     return reinterpret_cast<const float4*>(s < a.parts ? a.o + a.place(s) * kDLatent : b.o + b.place(s - a.parts) * kDLatent) + dim;
@@ -173,7 +145,89 @@ __global__ void __launch_bounds__(kJoinDims * kGroups) join_kernel(const PrefixP
       make_uint2(f32x2_to_bf16x2(acc.x * inv, acc.y * inv), f32x2_to_bf16x2(acc.z * inv, acc.w * inv));
 }
 
+// One CTA per row.  (This grid is resident while results are still written, so they are read from L2.)
+template <int kGroups>
+__global__ void __launch_bounds__(kJoinDims * kGroups) join_kernel(const PrefixParams p, const DenseItems d, uint16_t* out,
+                                                                   float* lse_out) {
+  __shared__ Parts own_s, prefix_s;
+  const int row = blockIdx.x;
+  const int own_rows = p.q_per_req * p.H, req = row / own_rows, prefix = row / p.rows;
+  const bool own_dense = !p.own, prefix_dense = p.pairs == 0;
+  // the dense kernel's items of this row, and its row in them
+  const int own_group = own_dense ? (row - req * own_rows) / d.nr : 0;
+  const int prefix_group = prefix_dense ? (row - prefix * p.rows) / d.nr : 0;
+  if (threadIdx.x == 0 && own_dense) own_s = Parts{p.out32, p.lse32, 1, 0, row, 0};
+  if (threadIdx.x == 0 && prefix_dense)
+    prefix_s = Parts{p.out32 + p.all_rows * kDLatent, p.lse32 + p.all_rows, 1, 0, row, 0};
+  __syncthreads();
+  ptx::griddep_wait();
+  if (threadIdx.x == 0 && !own_dense) own_s = segment_parts(p, p.prefixes + req, row);
+  if (threadIdx.x == 32 && !prefix_dense) prefix_s = segment_parts(p, prefix, row);
+  if (own_dense) {
+    const int own_item = req * d.groups + own_group;
+    const int prefix_item = prefix_dense ? p.requests * d.groups + prefix * d.prefix_groups + prefix_group : -1;
+    for (int c = threadIdx.x; c < d.ctas; c += kJoinDims * kGroups) {
+      const int2 x = __ldcg(d.slots.descs + c);            // {item, parts}; an item is found at most once
+      if (x.y > 0 && x.x == own_item)
+        own_s = Parts{d.slots.o, d.slots.lse, x.y, c, row - req * own_rows - own_group * d.nr, d.nr};
+      if (x.y > 0 && x.x == prefix_item)
+        prefix_s = Parts{d.slots.o, d.slots.lse, x.y, c, row - prefix * p.rows - prefix_group * d.nr, d.nr};
+    }
+  }
+  __syncthreads();
+  join_row<kGroups>(own_s, prefix_s, out, lse_out, row);
+}
+
+// The same for a call without prefixes: rows of items that cross runs alone, the others are written.
+template <int kGroups>
+__global__ void __launch_bounds__(kJoinDims * kGroups) row_merge_kernel(const DenseItems d, int item_rows, uint16_t* out,
+                                                                        float* lse_out) {
+  __shared__ Parts found_s;
+  const int row = blockIdx.x, req = row / item_rows, in = row - req * item_rows, item = req * d.groups + in / d.nr;
+  if (threadIdx.x == 0) found_s.parts = 0;
+  __syncthreads();
+  ptx::griddep_wait();
+  for (int c = threadIdx.x; c < d.ctas; c += kJoinDims * kGroups) {
+    const int2 x = __ldcg(d.slots.descs + c);              // {item, parts}; an item is found at most once
+    if (x.y > 0 && x.x == item) found_s = Parts{d.slots.o, d.slots.lse, x.y, c, in % d.nr, d.nr};
+  }
+  __syncthreads();
+  if (found_s.parts > 0) join_row<kGroups>(found_s, Parts{}, out, lse_out, row);
+}
+
 }  // namespace
+
+namespace {
+DenseItems items_of(const DenseParams& p) {
+  DenseItems d{};
+  d.slots = dense_slots(p);
+  d.ctas = p.ctas;
+  d.nr = p.nr;
+  d.groups = p.groups;
+  d.prefix_groups = p.prefix_groups;
+  return d;
+}
+
+cudaLaunchConfig_t dependent(unsigned grid, unsigned block, cudaStream_t stream, cudaLaunchAttribute* a) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.stream = stream;
+  a->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a->val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+}  // namespace
+
+cudaError_t launch_row_merge(const DenseParams& p, cudaStream_t stream) {
+  const bool many = p.ctas / ((long long)p.requests * p.groups) > kManyParts;
+  cudaLaunchAttribute a;
+  const cudaLaunchConfig_t cfg = dependent((unsigned)(p.B * p.H), many ? kJoinDims * kJoinGroups : kJoinDims, stream, &a);
+  return many ? cudaLaunchKernelEx(&cfg, row_merge_kernel<kJoinGroups>, items_of(p), p.q_per_req * p.H, p.out, p.lse)
+              : cudaLaunchKernelEx(&cfg, row_merge_kernel<1>, items_of(p), p.q_per_req * p.H, p.out, p.lse);
+}
 
 cudaError_t launch_shared(const SharedParams& p, cudaStream_t stream) {
   const PrefixParams& x = p.prefix;
@@ -181,26 +235,13 @@ cudaError_t launch_shared(const SharedParams& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if (!x.own) e = launch_dense(p.dense, stream);
   if (e != cudaSuccess) return e;
-  DenseItems d{};
-  if (!x.own) {
-    d.slots = dense_slots(p.dense);
-    d.ctas = p.dense.ctas;
-    d.nr = p.dense.nr;
-    d.groups = p.dense.groups;
-    d.prefix_groups = p.dense.prefix_groups;
-  }
+  const DenseItems d = x.own ? DenseItems{} : items_of(p.dense);
   // parts of a prefix's block of rows, about
   const long long parts = x.pairs > 0 ? x.pairs / ((long long)x.prefixes * x.row_blocks)
                                       : p.dense.ctas / ((long long)x.prefixes * p.dense.prefix_groups);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)x.all_rows);
-  cfg.blockDim = dim3(parts > kManyParts ? kJoinDims * kJoinGroups : kJoinDims);
-  cfg.stream = stream;
-  cudaLaunchAttribute a[1];
-  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  a[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = a;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute a;
+  const cudaLaunchConfig_t cfg =
+      dependent((unsigned)x.all_rows, parts > kManyParts ? kJoinDims * kJoinGroups : kJoinDims, stream, &a);
   return parts > kManyParts ? cudaLaunchKernelEx(&cfg, join_kernel<kJoinGroups>, x, d, p.out, p.lse)
                             : cudaLaunchKernelEx(&cfg, join_kernel<1>, x, d, p.out, p.lse);
 }
