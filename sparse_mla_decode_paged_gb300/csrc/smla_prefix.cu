@@ -281,6 +281,7 @@ __device__ int copy_role(const PrefixParams& p, uint32_t base, Bars* bars, uint3
   Ring<1> rope;
   uint32_t ok = p.wait_ns >= kLeastWaitNs;
   int filled = 0;
+  ptx::griddep_wait();                                     // the expanded pages
   // the values of a tile are loaded behind the keys of the next, in the order of their use
   const unsigned char* before = nullptr;
   auto load = [&](const unsigned char* from) {
@@ -594,7 +595,10 @@ __device__ void softmax_role(const PrefixParams& p, unsigned char* sm, uint32_t 
     if (!more) break;
     // this thread's 32 positions, read a tile ahead
     const int4* infos = p.info + 2 * (w.page() + side) + half;
-    if (first) next_info = __ldcg(infos);
+    if (first) {
+      ptx::griddep_wait();                                 // (done for a run's later segments)
+      next_info = __ldcg(infos);
+    }
     const int4 info = next_info;
     if (!w.last_of_segment()) next_info = __ldcg(infos + 4);
     if (first) {
@@ -722,11 +726,13 @@ __device__ __forceinline__ void find_run(const PrefixParams& p, Bars* bars) {
   const int n = segments_of(p), per = (n + kThreads - 1) / kThreads, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g0 = min(n, (int)threadIdx.x * per), g1 = min(n, g0 + per);
   long long tiles = 0, items = 0;
+  int last = 0;                                            // tiles of this thread's last segment, mostly its only one
 #pragma unroll 1
   for (int g = g0; g < g1; ++g) {
-    const int x = tiles_of(segment_len(p, g)), blocks = segment_of(p, g).blocks;
-    tiles += (long long)x * blocks;
-    if (x > 0) items += blocks;
+    const int blocks = segment_of(p, g).blocks;
+    last = tiles_of(segment_len(p, g));
+    tiles += (long long)last * blocks;
+    if (last > 0) items += blocks;
   }
   long long all_tiles = tiles;
 #pragma unroll
@@ -762,7 +768,7 @@ __device__ __forceinline__ void find_run(const PrefixParams& p, Bars* bars) {
   if (starts || blockIdx.x == 0) {
 #pragma unroll 1
     for (int g = g0; g < g1; ++g) {
-      const int x = tiles_of(segment_len(p, g));
+      const int x = g == g1 - 1 ? last : tiles_of(segment_len(p, g));
       const long long all = x > 0 ? (long long)(start + x) * segment_of(p, g).blocks : 0;
       if (starts && a >= before && a < before + all) {
         const int block = (int)((a - before) / (start + x));
@@ -812,7 +818,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefix_
   ptx::tc_fence_before();
   ptx::cluster_sync_all();                                 // both CTAs' barriers are set up
   ptx::tc_fence_after();
-  ptx::griddep_wait();                                     // the expanded prefixes
   const uint32_t tmem = bars->tmem;
 
   int filled = 0, ropes = 0;
