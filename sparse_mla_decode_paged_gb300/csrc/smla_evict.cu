@@ -7,7 +7,7 @@
 // slots would move nearly every record behind the first free slot; scores do not depend on it, the rotation being in
 // the records.)  Weights and positions move along; the weights of slots k .. n - 1 become 0.
 //
-// Select: a cluster of 1 .. 8 CTAs per request, each warp with a contiguous part of the slots.  The k-th largest key by
+// Select: a cluster of 1 .. 16 CTAs per request, each warp with a contiguous part of the slots.  The k-th largest key by
 // histograms of 11, 11 and 10 bits, summed over the cluster through distributed shared memory; then every warp counts
 // its ties, free slots and survivors, and writes its part of the two lists behind those of the warps before it.  Keys
 // stay in shared memory.  Move: one warp per record, two in flight.
@@ -25,7 +25,7 @@ namespace {
 
 constexpr int kWarps = 32;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kMostCluster = 8;
+constexpr int kPortableCluster = 8, kMostCluster = 16;
 constexpr int kBins = 2048;
 constexpr int kBatch = 4;                 // steps of 32 slots that a warp loads at once
 constexpr int kKeySlots = 40960;          // slots of a CTA whose keys fit into shared memory
@@ -211,6 +211,10 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
       need -= s.above;
       ties = s.ties[0];
       __syncthreads();
+      if (need == ties) {                                  // all keys from here on stay, whatever their lower bits
+        limit <<= shift;
+        break;
+      }
     }
   }
   // the first `need` slots whose key is the limit stay: ties of the warps before this one
@@ -373,13 +377,18 @@ cudaError_t launch_evict(const EvictParams& p, int sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !set[dev].load(std::memory_order_relaxed)) {
     e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDynBytes);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     if (dev < 64) set[dev].store(true, std::memory_order_relaxed);
   }
   // one CTA per kSlotsPerCta slots, while the requests leave SMs for them
   int csize = 1;
-  while (csize < kMostCluster && (long long)p.requests * csize * 2 <= sms && p.cols > (long long)csize * kSlotsPerCta)
+  while (csize < kPortableCluster && (long long)p.requests * csize * 2 <= sms && p.cols > (long long)csize * kSlotsPerCta)
     csize *= 2;
+  // and the largest cluster where the keys do not fit otherwise (1 x 500000 slots: 153 us with 8 CTAs that read them anew for
+  // each pass)
+  if (csize == kPortableCluster && (long long)p.requests * kMostCluster <= sms && p.cols > (long long)csize * kKeySlots)
+    csize = kMostCluster;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.requests * csize);
   cfg.blockDim = dim3(kThreads);
