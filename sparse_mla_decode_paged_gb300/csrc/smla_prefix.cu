@@ -106,15 +106,14 @@ __device__ __forceinline__ void expand_part(const PrefixParams& p, int g, bool o
     const int t = first + i;
     const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
     uint32_t o[8], most = 0;
+    const float by = scale[i] * down;                      // (exact where the products are above fp16's least)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 a = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)(w[j] & 0xffffu)));
-      const float2 b = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)(w[j] >> 16)));
-      const __half2 x = __floats2half2_rn(a.x * scale[i] * down, a.y * scale[i] * down);
-      const __half2 y = __floats2half2_rn(b.x * scale[i] * down, b.y * scale[i] * down);
-      o[2 * j] = *reinterpret_cast<const uint32_t*>(&x);
-      o[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&y);
-      most = __vmaxu2(most, __vmaxu2(o[2 * j] & 0x7fff7fffu, o[2 * j + 1] & 0x7fff7fffu));
+    for (int j = 0; j < 8; ++j) {
+      const float2 a = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)(w[j >> 1] >> (16 * (j & 1)))));
+      const float2 b = ptx::unpack2(ptx::mul2(ptx::pack2(a.x, a.y), ptx::pack2(by, by)));
+      const __half2 x = __floats2half2_rn(b.x, b.y);
+      o[j] = *reinterpret_cast<const uint32_t*>(&x);
+      most = __vmaxu2(most, o[j] & 0x7fff7fffu);
     }
     const __half2 rv = __floats2half2_rn(__uint_as_float(rope[i] << 16) * down, __uint_as_float(rope[i] & 0xffff0000u) * down);
     uint32_t ro = *reinterpret_cast<const uint32_t*>(&rv);
