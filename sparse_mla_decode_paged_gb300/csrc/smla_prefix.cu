@@ -24,7 +24,7 @@
 //
 // What bounds it: shared memory.  A tile's operands and copies are 392 KB per CTA (q 72, keys 72, weights 48, values 64, copies
 // 136), 3060 cycles at 128 bytes each; measured 3080 (the products alone 2180).  Measured, whole calls: 2048 rows x 32768
-// positions 126 us (146 GFLOP), of them 11 the expansion and 9 the join.
+// positions 127 us (146 GFLOP), of them 11 the expansion and 9 the join.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
