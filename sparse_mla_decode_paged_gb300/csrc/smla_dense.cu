@@ -351,7 +351,7 @@ __device__ __forceinline__ int page_entry(const DenseParams& p, const Rows& r, c
   t += lane >> 1;
   const int pages = kForm == kShared && r.prefix ? p.shared_pages : p.max_pages;
   const int32_t* table = kForm == kShared && r.prefix ? p.shared_table : p.block_table;
-  const int lp = t < n.tiles ? 2 * n.at(t) + (lane & 1) : pages;
+  const int lp = kForm != kMasked || t < n.tiles ? 2 * n.at(t) + (lane & 1) : pages;
   return lp < pages && n.sees_page(lp) ? __ldg(table + (size_t)r.req * pages + lp) : -1;
 }
 
@@ -366,7 +366,7 @@ __device__ void copy_role(const DenseParams& p, const CUtensorMap* map, const CU
   Ring<C::kRopeSlots> rope;
   uint32_t ok = p.wait_ns >= kLeastWaitNs;
   // block-table entries of 16 tiles per load, one lane each, the next 16 tiles' already in flight
-  int cur = 0, nxt = 0, base_t = 0, item = -1;
+  int cur = 0, nxt = 0, at = 0, item = -1;
 #pragma unroll 1
   while (w.here(p)) {
     const int lp = 2 * w.n.at(w.t);
@@ -385,12 +385,11 @@ __device__ void copy_role(const DenseParams& p, const CUtensorMap* map, const CU
           if (__ldg(p.seq_lens + b) > (long long)p.max_pages * kPageSize) atomicOr(p.err, SMLA_DEVERR_PAGE_RANGE);
       }
     }
-    if (enters || w.t == base_t + 16) {
-      base_t = w.t;
+    if (enters || at == 32) {
+      at = 0;
       cur = nxt;
       nxt = page_entry(p, r, w.n, w.t + 16, lane);
     }
-    const int at = 2 * (w.t - base_t);
     const int pg[2] = {__shfl_sync(0xffffffffu, cur, at), __shfl_sync(0xffffffffu, cur, at + 1)};
     int good = 0;
 #pragma unroll
@@ -448,6 +447,7 @@ __device__ void copy_role(const DenseParams& p, const CUtensorMap* map, const CU
       __syncwarp();
       k.next();
     }
+    at += 2;
     w.next();
   }
 }
