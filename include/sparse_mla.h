@@ -430,8 +430,10 @@ int sparse_mla_dense_decode(const smla_dense_dims* dims, const void* q, const vo
  *               starts); values below 0 or past the length count as those
  * 128-position tiles that no row of a CTA sees are neither read nor computed,
  * pages that no query sees may be -1 in the block table.  A capped score is
- * off by 2^-20 of itself.  Everything else, dims, plan and workspace among it,
- * as in sparse_mla_dense_decode; with nothing given the results are the same.
+ * off by 2^-20 of itself.  Rows whose bias falls by a quarter of a power of two and more
+ * per 128 positions keep the reference of their largest operand: smaller ones are
+ * rounded to steps of at most 2^-12.75 of that one.  Everything else, dims, plan
+ * and workspace among it, as in sparse_mla_dense_decode; with nothing given the results are the same.
  * SMLA_ERR_INVALID_ARG for a softcap outside its range, prefix_lens without
  * starts and misaligned pointers. */
 int sparse_mla_masked_decode(const smla_dense_dims* dims, const void* q, const void* kv_cache,
@@ -456,7 +458,7 @@ typedef struct smla_shared_dims {
 /* Bytes of workspace that sparse_mla_shared_decode needs on a device with
  * sm_count SMs (host only).  With many rows per prefix the tables' records are
  * expanded to fp16 in it (1152 bytes per position of prefix_table, and of
- * block_table where that is short; up to about 5 GiB).  Statuses as
+ * block_table where that is short; 5 GiB at most).  Statuses as
  * sparse_mla_dense_plan_for. */
 int sparse_mla_shared_workspace_size(const smla_shared_dims* dims, int32_t sm_count, size_t* bytes);
 

@@ -684,6 +684,8 @@ namespace {
 // 4096 / 65536 positions 21.1 / 18.7, 21.2 / 23.5, 40.9 / 56.7 us; 128 rows 21.1 / 18.7, 23.8 / 23.8, 57.9 / 57.4; 256 rows
 // 22.2 / 19.2, 29.6 / 24.9, 87 / 65; 1024 rows 34 / 28, 45 / 35, 260 / 145.  (Shorter ones keep the dense kernel's exact keys.)
 constexpr int64_t kPairsLeastRows = 128, kPairsLeastPages = 16, kPairsMostTiles = ((int64_t)4 << 30) / (9 * 16384);
+// The requests' own tables go along while all that is expanded stays within 5 GiB.
+constexpr int64_t kPairsMostAll = ((int64_t)5 << 30) / (9 * 16384);
 
 // How a shared decode runs on a device with `sms` SMs.
 struct SharedPlan {
@@ -727,8 +729,9 @@ int shared_plan(const smla_shared_dims* d, int sms, SharedPlan* plan) {
     plan->row_blocks = (int)((prefix_rows + 127) / 128);
     plan->own_blocks = (int)((rows + 127) / 128);
     const int64_t work = all_tiles * plan->row_blocks, own_tiles = requests * plan->tiles_per_own;
-    if (4 * (all_tiles + own_tiles) >= 0x7fffffff || work / pairs >= 0x7fffffff) return SMLA_ERR_UNSUPPORTED;
-    plan->own = own_tiles * plan->own_blocks <= (work / 4 > 2 * pairs ? work / 4 : 2 * pairs);
+    if (work / pairs >= 0x7fffffff) return SMLA_ERR_UNSUPPORTED;
+    plan->own = own_tiles * plan->own_blocks <= (work / 4 > 2 * pairs ? work / 4 : 2 * pairs) &&
+                all_tiles + own_tiles <= kPairsMostAll;
     const size_t pages = 2 * (size_t)(all_tiles + (plan->own ? own_tiles : 0));
     plan->slots_at = after(plan->bytes);
     plan->slots_lse_at = plan->slots_at + 2 * pairs * 128 * kDLatent * sizeof(float);
