@@ -10,7 +10,7 @@
 // Select: a cluster of 1 .. 16 CTAs per request, each warp with a contiguous part of the slots.  The k-th largest key by
 // histograms of 11, 11 and 10 bits, summed over the cluster through distributed shared memory; then every warp counts
 // its ties, free slots and survivors, and writes its part of the two lists behind those of the warps before it.  Keys
-// stay in shared memory.  Move: one warp per record, two in flight.
+// stay in shared memory.  Move: a warp has four records in flight.
 // What bounds it: the selection is a chain of cluster barriers and passes over shared memory, the moves HBM bytes.
 #include <cuda_runtime.h>
 
