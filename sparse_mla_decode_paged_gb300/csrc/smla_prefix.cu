@@ -185,8 +185,8 @@ constexpr uint32_t kRingAt = kP + 2 * kSlot;
 constexpr uint32_t kRope = kRingAt + kRing * kSlot;        // one half chunk
 constexpr uint32_t kRed = kRope + kHalfChunk;              // [64 rows][4] float
 constexpr uint32_t kSum = kRed + kRowsPerCta * 16;         // [64 rows][4] float
-constexpr uint32_t kFactor = kSum + kRowsPerCta * 16;      // [64 rows] float
-constexpr uint32_t kBar = kFactor + kRowsPerCta * 4;
+constexpr uint32_t kFactor = kSum + kRowsPerCta * 16;      // [2][64 rows] float
+constexpr uint32_t kBar = kFactor + 2 * kRowsPerCta * 4;
 constexpr uint32_t kBytes = kBar + 512;
 static_assert(kBytes <= 232448, "shared memory");
 
@@ -471,12 +471,13 @@ __device__ void pv_role(const PrefixParams& p, uint32_t base, uint32_t tmem, Bar
 }
 
 // 64 rows of q as fp16 times 2^-x, x per row such that its largest element lies in [2^3, 2^4); the rows' factors
-// 2^x sm_scale log2 e.  A row with an infinity becomes NaN.  One row at a time, the next two's loads in flight: straight code for
+// 2^x sm_scale log2 e to buffer `buf`: the warps of the other 32 rows may not have read the item's before, as nothing but an
+// item's start joins the two.  A row with an infinity becomes NaN.  One row at a time, the next two's loads in flight: straight code for
 // a warp's eight rows took 11000 cycles instead of 5300, most of them for its instructions.
-__device__ __forceinline__ void load_q(const PrefixParams& p, int first, int rows, unsigned char* sm, uint32_t base, int warp,
-                                       int lane) {
+__device__ __forceinline__ void load_q(const PrefixParams& p, int first, int rows, unsigned char* sm, uint32_t base, int buf,
+                                       int warp, int lane) {
   constexpr int kRows = kRowsPerCta / kSoftWarps;
-  float* f = reinterpret_cast<float*>(sm + kFactor);
+  float* f = reinterpret_cast<float*>(sm + kFactor) + buf * kRowsPerCta;
   const uint4* src = reinterpret_cast<const uint4*>(p.q + (size_t)(first + warp * kRows) * kDQK) + lane;
   const int here = rows - warp * kRows;                    // of this warp's rows
   auto read = [&](int i, uint4 (&to)[3]) {
@@ -538,6 +539,7 @@ __device__ void softmax_role(const PrefixParams& p, unsigned char* sm, uint32_t 
   int row_len = 0;                                         // positions that this thread's row sees
   float f = 0.f, ref = -CUDART_INF_F, l = 0.f;
   bool first = true, begins = false;
+  int buf = 0;                                             // of the item's factors
   Ring<2> last;                                            // the P buffer of the tile before
   int4 next_info = make_int4(0, 0, 0, 0);
   // results of the segment before, written beside the next one's first scores: their place, its rows
@@ -551,7 +553,8 @@ __device__ void softmax_role(const PrefixParams& p, unsigned char* sm, uint32_t 
     const int rows = min(kRowsPerCta, w.seg.rows - row0);  // (none, or fewer than none, in a block of at most 64)
     if (more && first) {
       // (every score of the last segment was computed, so no product reads its rows)
-      load_q(p, w.seg.first_row + row0, rows, sm, base, warp, lane);
+      buf ^= 1;
+      load_q(p, w.seg.first_row + row0, rows, sm, base, buf, warp, lane);
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (ok && lane == 0) ptx::mbar_arrive_cluster(to_q);
@@ -604,7 +607,7 @@ __device__ void softmax_role(const PrefixParams& p, unsigned char* sm, uint32_t 
     if (!w.last_of_segment()) next_info = __ldcg(infos + 4);
     if (first) {
       ptx::named_bar_sync(3, kSoftWarps * 32);             // the rows' factors are written, the results before have left
-      f = ptx::lds32f(base + kFactor + row * 4);
+      f = ptx::lds32f(base + kFactor + (buf * kRowsPerCta + row) * 4);
       row_len = w.len;
       if (w.seg.own && row < rows)
         row_len = clamped_to(__ldg(p.own_lens + (w.g - p.prefixes) * p.q_per_req + (row0 + row) / p.H), p.own_pages);
