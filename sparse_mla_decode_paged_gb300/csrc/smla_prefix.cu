@@ -49,6 +49,11 @@ constexpr uint32_t kHalfChunk = kKChunk / 2;               // 64 positions (or r
 // ----------------------------------------------------------------------------- expand
 
 constexpr int kExpandPart = 32;           // positions with one exponent
+// The exponent of positions without values, whose scores are 0.  Any would be right, but the rows' references follow the
+// largest s + e: a higher one takes bits from the weights of the others, a lower one leaves too little between a zero's
+// weight and the least float where those have large values.  This one leaves all bits beside largest values from 2^-57 to
+// 2^49.  (With e = 0 prefixes of values of 2^-42 came out as zeros.)
+constexpr int kNoValues = -50;
 constexpr int kExpandWarps = 8, kExpandTokens = kExpandPart / kExpandWarps;
 
 // The largest |E4M3| among 16 codes (NaNs count as the largest number).
@@ -98,7 +103,7 @@ __device__ __forceinline__ void expand_part(const PrefixParams& p, int g, bool o
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kExpandWarps; ++w) top = fmaxf(top, top_s[w]);
-  const int e = top > 0.f ? min(max((int)(__float_as_uint(top) >> 23) - 127 - 13, -100), 100) : 0;
+  const int e = top > 0.f ? min(max((int)(__float_as_uint(top) >> 23) - 127 - 13, -100), 100) : kNoValues;
   const float down = exp2_int(-e);
   const size_t at = segment_of(p, g).page + lp;
   unsigned char* to = p.expanded + at * kExpandedPage;
