@@ -506,8 +506,9 @@ typedef struct smla_weights_dims {
  *                   + sum_{b, h} exp(sm_scale * q[b][h].k_t - lse[b][h])
  * over the queries b of request r and their heads with t < seq_lens[b], for
  * every t below the longest of the request's lengths; later entries are left
- * as they are.  decay 0 overwrites (nothing is read).  The sums have a fixed
- * order: the result does not depend on timing.
+ * as they are.  decay 0 overwrites (nothing is read).  Rows with an lse of
+ * -inf saw no position and add nothing.  The sums have a fixed order: the
+ * result does not depend on timing.
  *   q, kv_cache, block_table, seq_lens  as in sparse_mla_dense_decode
  *   lse       float32 [B][H]; weights float32 [B / s_q][weights_stride] (written)
  *   err_word  device uint32 (may be NULL): lengths above num_cols or the block

@@ -2,8 +2,9 @@
 //
 //   w[r][t] = decay w[r][t] + sum over the request's queries b and heads h of exp(sm_scale q[b][h].k_t - lse[b][h]),
 //
-// t below seq_lens[b].  The codes go to the tensor core as they are, q as two E4M3 terms that are exact but for elements
-// below 2^-9 of the row's largest, the scales and the sums stay in fp32 (as the dense decode's scores; no values are read).
+// t below seq_lens[b]; rows with an lse of -inf saw nothing and add nothing.  The codes go to the tensor core as they are, q as
+// two E4M3 terms that are exact but for elements below 2^-9 of the row's largest, the scales and the sums stay in fp32 (as the
+// dense decode's scores; no values are read).
 // S^T of a tile: M = 128 positions, N = the rows, one accumulator per 128-dim scale block and one for the rope, so a thread
 // has one position and half of the rows: it forms their scores and adds up the weights in registers; no maximum is needed, lse
 // is given.  The two halves of a position meet in shared memory, always in the same order.
@@ -13,6 +14,7 @@
 // What bounds it: HBM bytes (656 per position) for up to 128 rows.
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <math_constants.h>
 
 #include <atomic>
 #include <cstddef>
@@ -298,7 +300,7 @@ __device__ __forceinline__ void load_q(const WeightsParams& p, int req, int grou
     if (lane < 8) ptx::sts128(base + C::kQr + swz128(r, lane), rope);
     if (lane == 0) {
       f[r] = exp2_int(x) * (p.sm_scale * kLog2e);
-      f[NR + r] = -lse * kLog2e;
+      f[NR + r] = lse == -CUDART_INF_F ? lse : -lse * kLog2e;      // a row that saw nothing adds nothing
       reinterpret_cast<int*>(f)[2 * NR + r] = len;
     }
   }
