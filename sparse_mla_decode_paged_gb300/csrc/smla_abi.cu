@@ -592,7 +592,11 @@ extern "C" int sparse_mla_attention_weights(const smla_weights_dims* d, const vo
     if (!lse || !weights || !aligned(lse, 4) || !aligned(weights, 4)) return SMLA_ERR_INVALID_ARG;
   }
   if (err_word && !aligned(err_word, 4)) return SMLA_ERR_INVALID_ARG;
-  if (d->batch == 0 || d->num_cols == 0) return SMLA_OK;
+  if (d->batch == 0) return SMLA_OK;
+  if (d->num_cols == 0) {                                   // lengths are checked all the same, for the error word
+    if (!err_word || !seq_lens) return SMLA_OK;
+    if (!aligned(seq_lens, 4)) return SMLA_ERR_INVALID_ARG;
+  }
   int sms = 0;
   const int st = sm_count_of_current_device(&sms);
   if (st != SMLA_OK) return st;

@@ -527,6 +527,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0 && bars->abort && p.err) atomicOr(p.err, SMLA_DEVERR_TIMEOUT);
 }
 
+// Without columns there are no tiles: the lengths alone are looked at.
+__global__ void __launch_bounds__(kThreads) lengths_kernel(const WeightsParams p) {
+  bool over = false;
+  for (int b = threadIdx.x; b < p.requests * p.q_per_req; b += kThreads) over |= __ldg(p.seq_lens + b) > clamped_len(p, b);
+  if (over) atomicOr(p.err, SMLA_DEVERR_LEN_RANGE);
+}
+
 template <int NR>
 cudaError_t launch_nr(const WeightsParams& p, int ctas, cudaStream_t stream) {
   CUtensorMap map, smap;
@@ -550,6 +557,10 @@ cudaError_t launch_nr(const WeightsParams& p, int ctas, cudaStream_t stream) {
 
 cudaError_t launch_weights(const WeightsParams& q, int sms, cudaStream_t stream) {
   if (q.requests == 0) return cudaSuccess;
+  if (q.cols == 0) {
+    if (q.err && q.seq_lens) lengths_kernel<<<1, kThreads, 0, stream>>>(q);
+    return cudaGetLastError();
+  }
   WeightsParams p = q;
   const long long rows = (long long)p.q_per_req * p.H;
   const int nr = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
@@ -557,7 +568,6 @@ cudaError_t launch_weights(const WeightsParams& q, int sms, cudaStream_t stream)
   const long long slots = (long long)p.max_pages * kPageSize < p.cols ? (long long)p.max_pages * kPageSize : p.cols;
   const long long most = p.requests * ((slots + kDenseTile - 1) / kDenseTile);
   const int ctas = (int)(most < sms ? most : sms);
-  if (ctas == 0) return cudaSuccess;
   if (nr == 16) return launch_nr<16>(p, ctas, stream);
   if (nr == 32) return launch_nr<32>(p, ctas, stream);
   if (nr == 64) return launch_nr<64>(p, ctas, stream);
