@@ -17,6 +17,7 @@
 #include <atomic>
 
 #include "smla_device.cuh"
+#include "smla_evict_plan.h"
 #include "smla_internal.h"
 #include "smla_ptx.cuh"
 
@@ -25,12 +26,9 @@ namespace {
 
 constexpr int kWarps = 32;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kPortableCluster = 8, kMostCluster = 16;
 constexpr int kBins = 2048;
 constexpr int kBatch = 4;                 // steps of 32 slots that a warp loads at once
-constexpr int kKeySlots = 40960;          // slots of a CTA whose keys fit into shared memory
-// A request takes another CTA per so many slots.  (1 x 32768 slots: 4 CTAs 23.5 us, 8 CTAs 30, whole calls.)
-constexpr int kSlotsPerCta = 8192;
+constexpr int kKeySlots = kEvictKeySlots;
 constexpr uint32_t kDynBytes = kKeySlots * 4 + kKeySlots / 8;
 
 struct Shared {
@@ -367,39 +365,52 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
   }
 }
 
+cudaLaunchConfig_t select_config(int requests, int csize, cudaStream_t stream, cudaLaunchAttribute* a) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)requests * csize);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kDynBytes;
+  cfg.stream = stream;
+  a->id = cudaLaunchAttributeClusterDimension;
+  a->val.clusterDim.x = csize;
+  a->val.clusterDim.y = a->val.clusterDim.z = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+// Sets the selection up on the current device; the largest cluster of it that the device can hold.
+cudaError_t largest_cluster(int* most) {
+  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDynBytes);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  for (*most = kEvictMostCluster; *most > 1; *most /= 2) {
+    cudaLaunchAttribute a;
+    const cudaLaunchConfig_t cfg = select_config(1, *most, nullptr, &a);
+    int clusters = 0;
+    if (cudaOccupancyMaxActiveClusters(&clusters, evict_select_kernel, &cfg) == cudaSuccess && clusters > 0) break;
+    (void)cudaGetLastError();                          // (an answer, not an error of the call)
+  }
+  return cudaSuccess;
+}
+
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams& p, int sms, cudaStream_t stream) {
   if (p.requests == 0) return cudaSuccess;
-  static std::atomic<bool> set[64];
+  static std::atomic<int> most_of[64];                 // the devices' largest clusters, 0: not looked up yet
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev >= 64 || !set[dev].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDynBytes);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  int most = dev < 64 ? most_of[dev].load(std::memory_order_relaxed) : 0;
+  if (most == 0) {
+    e = largest_cluster(&most);
     if (e != cudaSuccess) return e;
-    if (dev < 64) set[dev].store(true, std::memory_order_relaxed);
+    if (dev < 64) most_of[dev].store(most, std::memory_order_relaxed);
   }
-  // one CTA per kSlotsPerCta slots, while the requests leave SMs for them
-  int csize = 1;
-  while (csize < kPortableCluster && (long long)p.requests * csize * 2 <= sms && p.cols > (long long)csize * kSlotsPerCta)
-    csize *= 2;
-  // and the largest cluster where the keys do not fit otherwise (1 x 500000 slots: 153 us with 8 CTAs that read them anew for
-  // each pass)
-  if (csize == kPortableCluster && (long long)p.requests * kMostCluster <= sms && p.cols > (long long)csize * kKeySlots)
-    csize = kMostCluster;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.requests * csize);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kDynBytes;
-  cfg.stream = stream;
-  cudaLaunchAttribute a[1];
-  a[0].id = cudaLaunchAttributeClusterDimension;
-  a[0].val.clusterDim.x = csize;
-  a[0].val.clusterDim.y = a[0].val.clusterDim.z = 1;
-  cfg.attrs = a;
-  cfg.numAttrs = 1;
+  const int csize = evict_cluster(p.requests, p.cols, sms, most);
+  cudaLaunchAttribute a;
+  const cudaLaunchConfig_t cfg = select_config(p.requests, csize, stream, &a);
   e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p, csize);
   if (e != cudaSuccess) return e;
   const int warps = kMoveThreads / 32;
