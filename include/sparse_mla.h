@@ -424,6 +424,9 @@ int sparse_mla_dense_decode(const smla_dense_dims* dims, const void* q, const vo
  * prefix_lens[b] (all, if starts is NULL): a window with the first tokens kept,
  * the last of several documents behind a common prefix.  The
  * query's own position is seq_lens[b] - 1.
+ *   t is the slot in the block table.  After sparse_mla_kv_evict slots do not
+ * follow the tokens' positions, and this call has no array of them: slopes,
+ * starts and prefix_lens then mean slots, not distances (softcap alone is right).
  *   softcap     0 (none) or in [2^-20, 2^20]
  *   slopes      float32 [H] or NULL
  *   starts      int32 [B] or NULL; prefix_lens int32 [B] or NULL (only with
@@ -472,11 +475,16 @@ int sparse_mla_shared_workspace_size(const smla_shared_dims* dims, int32_t sm_co
  *   workspace    sparse_mla_shared_workspace_size bytes, 256-byte aligned; its first 4
  *                bytes are the device error word.  Concurrent calls must not share it.
  * Numerics: as in sparse_mla_dense_decode where a prefix is seen by fewer than
- * 128 rows or its table has fewer than 16 pages.  Else keys and values of the
+ * 128 rows, its table has fewer than 16 pages or all of them have more than 4 GiB
+ * of expanded records: widths of tables and numbers of rows choose, not lengths.
+ * Else keys and values of the
  * prefixes, and of short tables of the requests' own, are rounded to fp16 (2^-11 of
  * each element, or of 2^-27 of the largest of its 32 positions), and so are the
- * weights; sums are fp32.  A score is then off by about 1e-4 of |q||k| / sqrt(576), lse
- * by their weighted mean (rms 8e-6 behind 9000 positions, less behind more).
+ * weights; sums are fp32.  A score is then off by about 2e-4 of
+ * sm_scale |q||k| / sqrt(576) (root mean square), lse by their mean under the
+ * row's weights: measured with unit records, rms 2e-5 behind 1000 and 2000 positions,
+ * 8e-6 .. 1.2e-5 behind 9000, 5e-6 .. 1.5e-5 behind 32768, and 5e-4 in the worst of
+ * 2048 rows, where one position has a fifth of the weight.
  * A position that is no number, or beyond 2^114, makes
  * the rows that see it NaN.
  * Everything else, errors among it, as in sparse_mla_dense_decode;
@@ -500,8 +508,8 @@ typedef struct smla_weights_dims {
   int64_t weights_stride;     /* elements between rows of weights, >= num_cols           */
 } smla_weights_dims;
 
-/* Attention weights accumulated per cached position, from the lse that a
- * decode of the same queries returned:
+/* Attention weights accumulated per cached position, from the lse that
+ * sparse_mla_dense_decode of the same queries returned:
  *   weights[r][t] = decay * weights[r][t]
  *                   + sum_{b, h} exp(sm_scale * q[b][h].k_t - lse[b][h])
  * over the queries b of request r and their heads with t < seq_lens[b], for
@@ -509,6 +517,11 @@ typedef struct smla_weights_dims {
  * as they are.  decay 0 overwrites (nothing is read).  Rows with an lse of
  * -inf saw no position and add nothing.  The sums have a fixed order: the
  * result does not depend on timing.
+ *   Another decode's lse is not checked.  That of sparse_mla_shared_decode gives
+ * the requests' own positions their weights in the whole softmax (and, called
+ * with each request's prefix as its row of the block table, the prefix's).  That of
+ * sparse_mla_masked_decode does not: scores are neither capped nor biased
+ * here, and positions that its mask hid are given terms that are no weights.
  *   q, kv_cache, block_table, seq_lens  as in sparse_mla_dense_decode
  *   lse       float32 [B][H]; weights float32 [B / s_q][weights_stride] (written)
  *   err_word  device uint32 (may be NULL): lengths above num_cols or the block
@@ -561,6 +574,12 @@ size_t sparse_mla_kv_evict_workspace_size(const smla_evict_dims* dims);
  *   err_word  device uint32 (may be NULL): lengths above num_cols or the block
  *             table are clamped and set SMLA_DEVERR_LEN_RANGE; a move from or to a page
  *             outside the cache leaves the record and sets SMLA_DEVERR_PAGE_RANGE.
+ *             Weight, position and length change all the same: that slot's
+ *             record is then not its position's token, and the request is not to
+ *             be read again.
+ * Afterwards a request's next slot (new_lens[r]) is not its next position, so
+ * sparse_mla_kv_norm_append, which takes one number for both, cannot append to it:
+ * sparse_mla_norm_rope at the position, then sparse_mla_kv_append at the slot.
  * SMLA_ERR_INVALID_ARG for null or misaligned pointers and bad shapes,
  * SMLA_ERR_UNSUPPORTED for shapes outside the stated ranges,
  * SMLA_ERR_WORKSPACE, SMLA_ERR_CUDA.  Asynchronous on `stream`. */

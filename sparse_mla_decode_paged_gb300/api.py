@@ -594,7 +594,8 @@ def sparse_mla_masked_decode(q: torch.Tensor, kv_cache: torch.Tensor, block_tabl
     """sparse_mla_dense_decode whose scores are capped by a tanh (softcap > 0), biased by slopes [H] fp32 times the distance
     t - (seq_lens[b] - 1), and hidden below starts [B] but for the first prefix_lens [B] positions (int32).
 
-    Workspaces are alloc_dense_workspace's.  Tiles that no row sees are not read: a window costs its own length."""
+    Workspaces are alloc_dense_workspace's.  Tiles that no row sees are not read: a window costs its own length.  t is the
+    slot: after sparse_mla_kv_evict slopes, starts and prefix_lens no longer follow the tokens' positions."""
     key = _call_key((q, kv_cache, block_table, seq_lens, slopes, starts, prefix_lens, out, lse, workspace), "masked_decode",
                     ctas)
     dims = _CHECKED.get(key) or _remember(key, _masked_dims(q, kv_cache, block_table, seq_lens, slopes, starts,
@@ -678,8 +679,9 @@ def sparse_mla_shared_decode(q: torch.Tensor, kv_cache: torch.Tensor, prefix_tab
     """sparse_mla_dense_decode of R requests in G groups of R / G that share a prefix each: prefix_table int32 [G, pages],
     prefix_lens int32 [G]; block_table [R, pages] and seq_lens [B] are the requests' own positions behind it.
 
-    Calls in flight at once need a workspace each (alloc_shared_workspace); without one a call allocates its own, and
-    its error word is lost."""
+    Many rows behind long tables are computed with keys and values rounded to fp16 (include/sparse_mla.h says when and how
+    far lse is off).  Calls in flight at once need a workspace each (alloc_shared_workspace); without one a call allocates
+    its own, of up to 5 GiB by the tables' widths, and its error word is lost."""
     key = _call_key((q, kv_cache, prefix_table, prefix_lens, block_table, seq_lens, out, lse, workspace), "shared_decode")
     dims = _CHECKED.get(key) or _remember(key, _shared_dims(q, kv_cache, prefix_table, prefix_lens, block_table, seq_lens,
                                                             out, lse, workspace))
@@ -732,7 +734,8 @@ def sparse_mla_attention_weights(q: torch.Tensor, kv_cache: torch.Tensor, block_
     t below the longest of its lengths; returns weights (fp32 [R, n], rows may be strided, written in place).
 
     q [B,H,576], kv_cache, block_table [R, pages], seq_lens [B] as in sparse_mla_dense_decode, lse fp32 [B,H] what that
-    call returned.  decay 0 overwrites."""
+    call returned (of a shared decode: the own positions' weights in the whole softmax; a masked decode's does not fit,
+    as scores are neither capped nor biased here and hidden positions count).  decay 0 overwrites."""
     key = _call_key((q, kv_cache, block_table, seq_lens, lse, weights, err_word), "attention_weights")
     dims = _CHECKED.get(key) or _remember(key, _weights_dims(q, kv_cache, block_table, seq_lens, lse, weights, err_word))
     with _on(q.device, stream) as st:
@@ -776,7 +779,8 @@ def sparse_mla_kv_evict(weights: torch.Tensor, positions: torch.Tensor, next_pos
     position, in any order.  Positions below `sinks` and the `recent` ones before next_positions [R] stay, then the
     largest weights (IEEE totalOrder, ties to the lower slot).  Records kept in slots past the new length move to the
     free slots before it, with their weights and positions; the weights behind it become 0.  A request's pages must be
-    its own.  Calls in flight at once need a workspace each (alloc_evict_workspace)."""
+    its own.  From then on a token's slot is not its position: append with sparse_mla_norm_rope (at the position) and
+    sparse_mla_kv_append (at the slot).  Calls in flight at once need a workspace each (alloc_evict_workspace)."""
     key = _call_key((weights, positions, next_positions, seq_lens, kv_cache, block_table, new_lens, err_word,
                      keep if isinstance(keep, torch.Tensor) else None), "kv_evict", sinks, recent,
                     None if isinstance(keep, torch.Tensor) else keep)

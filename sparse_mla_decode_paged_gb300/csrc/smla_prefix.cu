@@ -7,7 +7,8 @@
 //
 // Expand.  The records are written once as fp16, K' = [code scale | rope] 2^-e, e one exponent per 32 positions that puts
 // their largest value into [2^13, 2^14): one rounding of 2^-11 of the value (2^-38 of the largest for the smallest).  It makes up
-// nearly all of lse's error (rms 8e-6 behind 9001 positions, 1e-6 without it), and buys one product per tile instead of one
+// nearly all of lse's error (unit records: rms 2e-5 behind 1000 and 2000 positions, 8e-6 .. 1.2e-5 behind 9001, 1e-6 without it;
+// the worst of 2048 rows 5e-4, where one position has a fifth of the weight), and buys one product per tile instead of one
 // per scale block, whose accumulators do not fit beside O.  The expanded
 // pages serve all row blocks, so the conversion is not in the loop that feeds the tensor core.  A page is 9 chunks of 64
 // dims, 64 rows of 128 bytes each, 128B-swizzled as in shared memory.
@@ -26,7 +27,7 @@
 //
 // What bounds it: shared memory.  A tile's operands and copies are 392 KB per CTA (q 72, keys 72, weights 48, values 64, copies
 // 136), 3060 cycles at 128 bytes each; measured 3080 (the products alone 2180).  Measured, whole calls: 2048 rows x 32768
-// positions 127 us (146 GFLOP), of them 11 the expansion and 9 the join.
+// positions with 64 own per request 125 us (146 GFLOP), with 16 .. 1024 own 129 us; of them 13 and 16 the expansion, 9 the join.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -477,8 +478,8 @@ __device__ void pv_role(const PrefixParams& p, uint32_t base, uint32_t tmem, Bar
 
 // 64 rows of q as fp16 times 2^-x, x per row such that its largest element lies in [2^3, 2^4); the rows' factors
 // 2^x sm_scale log2 e to buffer `buf`: the warps of the other 32 rows may not have read the item's before, as nothing but an
-// item's start joins the two.  A row with an infinity becomes NaN.  One row at a time, the next two's loads in flight: straight code for
-// a warp's eight rows took 11000 cycles instead of 5300, most of them for its instructions.
+// item's start joins the two.  A row with an infinity becomes NaN.  One row at a time, the next two's loads in flight: straight
+// code for a warp's eight rows took 11000 cycles instead of 5300, most of them for its instructions.
 __device__ __forceinline__ void load_q(const PrefixParams& p, int first, int rows, unsigned char* sm, uint32_t base, int buf,
                                        int warp, int lane) {
   constexpr int kRows = kRowsPerCta / kSoftWarps;
