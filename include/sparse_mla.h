@@ -475,18 +475,18 @@ int sparse_mla_shared_workspace_size(const smla_shared_dims* dims, int32_t sm_co
  *   workspace    sparse_mla_shared_workspace_size bytes, 256-byte aligned; its first 4
  *                bytes are the device error word.  Concurrent calls must not share it.
  * Numerics: as in sparse_mla_dense_decode where a prefix is seen by fewer than
- * 128 rows, its table has fewer than 16 pages or all of them have more than 4 GiB
- * of expanded records: widths of tables and numbers of rows choose, not lengths.
- * Else keys and values of the
- * prefixes, and of short tables of the requests' own, are rounded to fp16 (2^-11 of
- * each element, or of 2^-27 of the largest of its 32 positions), and so are the
- * weights; sums are fp32.  A score is then off by about 2e-4 of
- * sm_scale |q||k| / sqrt(576) (root mean square), lse by their mean under the
- * row's weights: measured with unit records, rms 2e-5 behind 1000 and 2000 positions,
- * 8e-6 .. 1.2e-5 behind 9000, 5e-6 .. 1.5e-5 behind 32768, and 5e-4 in the worst of
- * 2048 rows, where one position has a fifth of the weight.
- * A position that is no number, or beyond 2^114, makes
- * the rows that see it NaN.
+ * 128 rows, its table has fewer than 16 pages or all of them have more than 4
+ * GiB of expanded records: widths of tables and numbers of rows choose, not
+ * lengths.  Else keys and values of the prefixes, and of short tables of the
+ * requests' own, are rounded to fp16 (2^-11 of each element, or of 2^-27 of the
+ * largest of its 32 positions), and so are the weights (times that largest:
+ * 2^-11 of each product, or 2^-30 of the row's largest); sums are fp32.  A score
+ * is then off by about 2e-4 of sm_scale |q||k| / sqrt(576) (root mean square),
+ * lse by their mean under the row's weights: measured with unit records, rms
+ * 2e-5 behind 1000 and 2000 positions, 8e-6 .. 1.2e-5 behind 9000, 5e-6 ..
+ * 1.5e-5 behind 32768, and 5e-4 in the worst of 2048 rows, where one position
+ * has a fifth of the weight.  A position that is no number, or beyond 2^114,
+ * makes the rows that see it NaN.
  * Everything else, errors among it, as in sparse_mla_dense_decode;
  * SMLA_ERR_INVALID_ARG also where G does not divide R. */
 int sparse_mla_shared_decode(const smla_shared_dims* dims, const void* q, const void* kv_cache,
